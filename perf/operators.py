@@ -252,7 +252,7 @@ def run(s):
     if s["op"] == "q4":
         if own:
             import gated_deltanet_linear_gb300 as gdn
-            gdn.gdn_linear_q4(s["x"], s["qw"], s["scales"], s["y"])
+            gdn.gdn_quant_linear(s["x"], s["qw"], s["scales"], s["y"])
         else:
             _plain_q4(s)
         return s["y"]
