@@ -29,7 +29,9 @@ __all__ = [
     "gdn_prefill_timeouts", "gdn_layer_prologue_m", "gdn_layer_workspace",
     "gdn_layer_step_m", "gdn_layer_hist_rollback",
     "gdn_layer_step_m_noalloc", "GDN_NOALLOC_SCRATCH_BYTES",
-    "gdn_gated_rmsnorm_m",
+    "gdn_gated_rmsnorm_m", "gdn_linattn_step", "gdn_linattn_step_m",
+    "gdn_linattn_prefill_workspace", "gdn_linattn_prefill",
+    "gdn_quant_linear",
 ]
 
 GDN_OK, GDN_EINVAL, GDN_ESHAPE, GDN_EALIGN = 0, -1, -2, -3
@@ -38,6 +40,10 @@ GDN_ESCRATCH = -8
 GDN_PREC_FP32, GDN_PREC_BF16X3, GDN_PREC_BF16 = 0, 1, 2
 GDN_MAX_TOKENS = 1 << 20
 GDN_NOALLOC_SCRATCH_BYTES = 16 << 20
+GDN_F32, GDN_BF16 = 0, 1
+GDN_DECAY_TOKEN, GDN_DECAY_HEAD = 0, 1
+GDN_QUANT_MAX_DIM = 1 << 20
+_DTYPES = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16}
 
 # Every symbol include/gdn.h declares.
 EXPORTS = ("gdn_step", "gdn_step_m", "gdn_mark", "gdn_rollback",
@@ -45,7 +51,10 @@ EXPORTS = ("gdn_step", "gdn_step_m", "gdn_mark", "gdn_rollback",
            "gdn_prefill_timeouts", "gdn_wait_timeouts", "gdn_layer_prologue_m",
            "gdn_layer_workspace", "gdn_layer_step_m",
            "gdn_layer_hist_rollback", "gdn_gated_rmsnorm_m",
-           "gdn_layer_step_m_noalloc", "gdn_strerror", "gdn_version")
+           "gdn_layer_step_m_noalloc", "gdn_linattn_step",
+           "gdn_linattn_step_m", "gdn_linattn_prefill_workspace",
+           "gdn_linattn_prefill", "gdn_quant_linear", "gdn_strerror",
+           "gdn_version")
 
 
 class GDNError(RuntimeError):
@@ -106,6 +115,17 @@ def load():
     lib.gdn_layer_step_m_noalloc.restype = ctypes.c_int
     lib.gdn_layer_hist_rollback.argtypes = [cp, ip, ip] + [vp] * 6
     lib.gdn_layer_hist_rollback.restype = ctypes.c_int
+    fp, sz = ctypes.c_float, ctypes.c_size_t
+    lib.gdn_linattn_step.argtypes = [cp, ip, ip, fp] + [vp] * 7
+    lib.gdn_linattn_step.restype = ctypes.c_int
+    lib.gdn_linattn_step_m.argtypes = [cp, ip, ip, ip, fp] + [vp] * 9
+    lib.gdn_linattn_step_m.restype = ctypes.c_int
+    lib.gdn_linattn_prefill_workspace.argtypes = [cp, ip, ip]
+    lib.gdn_linattn_prefill_workspace.restype = sz
+    lib.gdn_linattn_prefill.argtypes = [cp, ip, ip, ip, fp] + [vp] * 9 + [sz, vp]
+    lib.gdn_linattn_prefill.restype = ctypes.c_int
+    lib.gdn_quant_linear.argtypes = [ip] * 5 + [vp] * 5
+    lib.gdn_quant_linear.restype = ctypes.c_int
     lib.gdn_prefill_timeouts.argtypes = [ctypes.POINTER(ctypes.c_uint)]
     lib.gdn_prefill_timeouts.restype = ctypes.c_int
     lib.gdn_wait_timeouts.argtypes = [ctypes.POINTER(ctypes.c_uint)]
@@ -405,3 +425,122 @@ def gdn_layer_hist_rollback(hist, M, m_dev, hist_snap, x, kh, kd=128, vd=128,
         _t(x, "x", B * int(M) * conv_dim), _t(hist, "hist", hist.numel()),
         None if err_dev is None else err_dev.data_ptr(), _stream(stream)),
         "gdn_layer_hist_rollback")
+
+
+def _tok(x, name, shape, dtype):
+    """Pointer of a contiguous CUDA tensor of this shape and type."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.dtype != dtype or not x.is_cuda or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor")
+    if x.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {shape}")
+    return x.data_ptr()
+
+
+def _linattn(S, q, k, v, g, o, M):
+    """Shape, element type, decay mode and pointers (q, k, v, g, o) of a
+    linear-attention call; M None: one token without a token dimension."""
+    if not isinstance(S, torch.Tensor) or S.dim() != 4:
+        raise ValueError("S must be [B][vh][kd][vd]")
+    B, vh, kd, vd = S.shape
+    dtype = q.dtype
+    if dtype not in _DTYPES:
+        raise ValueError("q, k, v, o must be float32 or bfloat16")
+    if q.dim() < 2:
+        raise ValueError("q must be [B][T][kh][kd]")
+    kh = q.shape[-2]
+    qk, vo, gs = (B, M, kh, kd), (B, M, vh, vd), (B, M, vh)
+    if M is None:
+        lead = tuple(q.shape[:-2])
+        if lead not in ((B,), (B, 1)):
+            raise ValueError(f"q has shape {tuple(q.shape)}: one token for each "
+                             f"of {B} sequences expected")
+        qk, vo, gs = lead + (kh, kd), lead + (vh, vd), lead + (vh,)
+    head = g.dim() == 1
+    ptrs = (_tok(q, "q", qk, dtype), _tok(k, "k", qk, dtype),
+            _tok(v, "v", vo, dtype),
+            _tok(g, "g", (vh,) if head else gs, torch.float32),
+            _tok(o, "o", vo, dtype))
+    return (Shape(B, kh, vh, kd, vd), _DTYPES[dtype],
+            GDN_DECAY_HEAD if head else GDN_DECAY_TOKEN, ptrs)
+
+
+def gdn_linattn_step(S, q, k, v, g, o, scale=1.0, stream=None):
+    """One token of linear attention with a decay for each head: S = exp(g) S
+    + k v^T in place, o = scale S^T q.  q, k [B][kh][kd] (or [B][1][kh][kd]),
+    v, o likewise with vh, all float32 or all bfloat16; g per token [B][vh]
+    (or [B][1][vh]) or per head [vh]."""
+    sh, dtype, decay, ptrs = _linattn(S, q, k, v, g, o, None)
+    _check(load().gdn_linattn_step(
+        ctypes.byref(sh), dtype, decay, float(scale),
+        _tok(S, "S", S.shape, torch.float32), *ptrs, _stream(stream)),
+        "gdn_linattn_step")
+
+
+def gdn_linattn_step_m(S_in, S_out, ckpt, q, k, v, g, o, scale=1.0,
+                       stream=None):
+    """M = q.shape[1] tokens of gdn_linattn_step in one launch; S_out may be
+    S_in; ckpt [M][B][vh][kd][vd] or None receives the state after each
+    token."""
+    if q.dim() != 4:
+        raise ValueError("q must be [B][M][kh][kd]")
+    M = int(q.shape[1])
+    sh, dtype, decay, ptrs = _linattn(S_in, q, k, v, g, o, M)
+    f32 = torch.float32
+    _check(load().gdn_linattn_step_m(
+        ctypes.byref(sh), M, dtype, decay, float(scale),
+        _tok(S_in, "S_in", S_in.shape, f32), _tok(S_out, "S_out", S_in.shape, f32),
+        None if ckpt is None else _tok(ckpt, "ckpt", (M,) + tuple(S_in.shape), f32),
+        *ptrs, _stream(stream)), "gdn_linattn_step_m")
+
+
+def gdn_linattn_prefill_workspace(B, kh, vh, T, dtype=torch.float32, kd=128,
+                                  vd=128):
+    """Bytes of workspace gdn_linattn_prefill needs for this shape."""
+    sh = Shape(B, kh, vh, kd, vd)
+    return int(load().gdn_linattn_prefill_workspace(ctypes.byref(sh), int(T),
+                                                    _DTYPES[dtype]))
+
+
+def gdn_linattn_prefill(S, q, k, v, g, o, scale=1.0, lens=None, err_dev=None,
+                        workspace=None, stream=None):
+    """Prompts of T = q.shape[1] tokens, S updated in place.  lens (int32 CUDA
+    tensor [B]): the first lens[b] rows of sequence b count; its other rows
+    of o keep what they held.  A length outside 0..T leaves the sequence as it
+    was and sets err_dev (int32 CUDA tensor of one element)."""
+    if q.dim() != 4:
+        raise ValueError("q must be [B][T][kh][kd]")
+    T = int(q.shape[1])
+    sh, dtype, decay, ptrs = _linattn(S, q, k, v, g, o, T)
+    lens_ptr = None if lens is None else _tok(lens, "lens", (sh.B,), torch.int32)
+    err_ptr = None if err_dev is None else _tok(err_dev, "err_dev", (1,), torch.int32)
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        ws_ptr = workspace.data_ptr()
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _check(load().gdn_linattn_prefill(
+        ctypes.byref(sh), T, dtype, decay, float(scale),
+        _tok(S, "S", S.shape, torch.float32), *ptrs, lens_ptr, err_ptr, ws_ptr,
+        ws_bytes, _stream(stream)), "gdn_linattn_prefill")
+
+
+def gdn_quant_linear(x, qw, scales, y, stream=None):
+    """y = x W^T with 4-bit weights: x [rows][K] and y [rows][N] float32 or
+    bfloat16, qw uint8 [N][K/2] (element 2j in the low half of byte j, two's
+    complement), scales float16 [N][K/group], group 32, 64 or 128."""
+    if x.dim() != 2 or qw.dim() != 2 or scales.dim() != 2:
+        raise ValueError("x, qw and scales must have two dimensions")
+    rows, K = x.shape
+    N, groups = scales.shape
+    if x.dtype not in _DTYPES:
+        raise ValueError("x and y must be float32 or bfloat16")
+    if groups < 1 or K % groups:
+        raise ValueError(f"{groups} scales for a row of {K} elements")
+    _check(load().gdn_quant_linear(
+        rows, N, K, K // groups, _DTYPES[x.dtype],
+        _tok(x, "x", (rows, K), x.dtype), _tok(qw, "qw", (N, K // 2), torch.uint8),
+        _tok(scales, "scales", (N, groups), torch.float16),
+        _tok(y, "y", (rows, N), x.dtype), _stream(stream)), "gdn_quant_linear")

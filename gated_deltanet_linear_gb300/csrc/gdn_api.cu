@@ -518,6 +518,155 @@ int gdn_gated_rmsnorm_m(const gdn_shape *s, int M, float eps, const float *o,
                                          (cudaStream_t)stream));
 }
 
+}  // extern "C"
+
+// ------------------------------------------------------ linear attention
+
+namespace {
+
+int element_size(int dtype) {
+  return dtype == GDN_F32 ? 4 : dtype == GDN_BF16 ? 2 : 0;
+}
+
+// The checks shared by the linear-attention calls, in order: shape, counts,
+// values, then (for B > 0) the buffers and their overlaps.  S_out may equal
+// S_in.  Fills *P on success.
+int linattn_args(const gdn_shape *s, int M, int dtype, int decay, float scale,
+                 const float *S_in, float *S_out, float *ckpt, const void *q,
+                 const void *k, const void *v, const float *g, void *o,
+                 gdn::LinattnArgs *P) {
+  int r = check_shape(s);
+  if (r) return r;
+  if (M < 1 || M > GDN_MAX_TOKENS) return GDN_ERANGE;
+  const int e = element_size(dtype);
+  if (!e || (decay != GDN_DECAY_TOKEN && decay != GDN_DECAY_HEAD)) return GDN_EINVAL;
+  if (!(scale >= -3.0e38f && scale <= 3.0e38f)) return GDN_EINVAL;
+  if (s->B == 0) return GDN_OK;
+  const size_t sb = state_floats(s) * 4;
+  const size_t qkb = (size_t)s->B * M * s->kh * s->kd * e;
+  const size_t vb = (size_t)s->B * M * s->vh * s->vd * e;
+  const size_t gb = (decay == GDN_DECAY_HEAD ? 1 : (size_t)s->B * M) * s->vh * 4;
+  Buf in[] = {{S_in, sb}, {q, qkb}, {k, qkb}, {v, vb}, {g, gb}};
+  Buf out[] = {{S_out, sb}, {o, vb}, {ckpt, sb * (size_t)M}};
+  const int nout = ckpt ? 3 : 2;
+  Buf all[] = {in[0], in[1], in[2], in[3], in[4], out[0], out[1], out[2]};
+  r = check_bufs(all, 5 + nout);
+  if (r) return r;
+  for (int i = 0; i < nout; ++i) {
+    for (int j = 0; j < 5; ++j) {
+      if (i == 0 && j == 0 && S_out == S_in) continue;
+      if (overlaps(out[i], in[j])) return GDN_EALIAS;
+    }
+    for (int j = i + 1; j < nout; ++j)
+      if (overlaps(out[i], out[j])) return GDN_EALIAS;
+  }
+  *P = gdn::LinattnArgs{S_in, S_out, ckpt, q, k, v, g, o, nullptr, nullptr,
+                        scale, decay == GDN_DECAY_HEAD, s->B, s->kh, s->vh,
+                        s->vh / s->kh, M};
+  return GDN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gdn_linattn_step_m(const gdn_shape *s, int M, int dtype, int decay,
+                       float scale, const float *S_in, float *S_out,
+                       float *ckpt, const void *q, const void *k,
+                       const void *v, const float *g, void *o,
+                       gdn_stream_t stream) {
+  gdn::LinattnArgs P;
+  const int r = linattn_args(s, M, dtype, decay, scale, S_in, S_out, ckpt, q, k,
+                             v, g, o, &P);
+  if (r || s->B == 0) return r;
+  cudaGetLastError();
+  return status_of(gdn::launch_linattn_steps(P, dtype == GDN_BF16,
+                                             (cudaStream_t)stream));
+}
+
+int gdn_linattn_step(const gdn_shape *s, int dtype, int decay, float scale,
+                     float *S, const void *q, const void *k, const void *v,
+                     const float *g, void *o, gdn_stream_t stream) {
+  return gdn_linattn_step_m(s, 1, dtype, decay, scale, S, S, nullptr, q, k, v, g,
+                            o, stream);
+}
+
+size_t gdn_linattn_prefill_workspace(const gdn_shape *s, int T, int dtype) {
+  if (check_shape(s) || T < 1 || T > GDN_MAX_TOKENS || !element_size(dtype)) return 0;
+  return gdn::linattn_prefill_workspace_bytes(s->B, s->vh, T, dtype == GDN_BF16);
+}
+
+int gdn_linattn_prefill(const gdn_shape *s, int T, int dtype, int decay,
+                        float scale, float *S, const void *q, const void *k,
+                        const void *v, const float *g, void *o,
+                        const int *lens, int *err_dev, void *workspace,
+                        size_t ws_bytes, gdn_stream_t stream) {
+  gdn::LinattnArgs P;
+  int r = linattn_args(s, T, dtype, decay, scale, S, S, nullptr, q, k, v, g, o, &P);
+  if (r) return r;
+  // the copy engine addresses a sequence's rows with strides below 2^40 bytes
+  if ((unsigned long long)T * (unsigned long long)s->vh >= (1ull << 31)) return GDN_ERANGE;
+  if (s->B == 0) return GDN_OK;
+  const size_t need = gdn_linattn_prefill_workspace(s, T, dtype);
+  if (need && (!workspace || ws_bytes < need)) return workspace ? GDN_ERANGE : GDN_EINVAL;
+  const Buf out[] = {{S, state_floats(s) * 4},
+                     {o, (size_t)s->B * T * s->vh * s->vd * element_size(dtype)}};
+  if (need) {
+    const size_t e = element_size(dtype);
+    const Buf ws{workspace, need};
+    r = check_bufs(&ws, 1);
+    if (r) return r;
+    const size_t qkb = (size_t)s->B * T * s->kh * s->kd * e;
+    const Buf in[] = {{q, qkb}, {k, qkb}, {v, out[1].bytes},
+                      {g, (decay == GDN_DECAY_HEAD ? 1 : (size_t)s->B * T) * s->vh * 4},
+                      {lens, lens ? (size_t)s->B * 4 : 0}, out[0], out[1]};
+    for (const Buf &x : in)
+      if (overlaps(ws, x)) return GDN_EALIAS;
+  }
+  const void *ints[] = {lens, err_dev};
+  for (const void *p : ints) {
+    if (!p) continue;
+    if (((uintptr_t)p & 3u) != 0) return GDN_EALIGN;
+    r = check_device_ptr(p);
+    if (r) return r;
+    for (const Buf &x : out)
+      if (overlaps(x, Buf{p, p == lens ? (size_t)s->B * 4 : 4})) return GDN_EALIAS;
+  }
+  P.lens = lens;
+  P.err = err_dev;
+  cudaGetLastError();
+  return status_of(gdn::launch_linattn_prefill(P, dtype == GDN_BF16, workspace,
+                                               (cudaStream_t)stream));
+}
+
+int gdn_quant_linear(int rows, int N, int K, int group, int dtype,
+                     const void *x, const unsigned char *qw,
+                     const void *scales, void *y, gdn_stream_t stream) {
+  if (group != 32 && group != 64 && group != 128) return GDN_ESHAPE;
+  if (rows < 0 || N < 0 || K < group || K % group) return GDN_ESHAPE;
+  if (rows > GDN_MAX_TOKENS || N > GDN_QUANT_MAX_DIM || K > GDN_QUANT_MAX_DIM)
+    return GDN_ERANGE;
+  const int e = element_size(dtype);
+  if (!e) return GDN_EINVAL;
+  if (rows == 0 || N == 0) return GDN_OK;
+  const Buf b[] = {{x, (size_t)rows * K * e},
+                   {qw, (size_t)N * (K / 2)},
+                   {scales, (size_t)N * (K / group) * 2},
+                   {y, (size_t)rows * N * e}};
+  const int r = check_bufs(b, 4);
+  if (r) return r;
+  for (int j = 0; j < 3; ++j)
+    if (overlaps(b[3], b[j])) return GDN_EALIAS;
+  cudaGetLastError();
+  return status_of(gdn::launch_quant_linear(x, qw, scales, y, rows, N, K, group,
+                                            dtype == GDN_BF16,
+                                            (cudaStream_t)stream));
+}
+
+}  // extern "C"
+
+extern "C" {
+
 const char *gdn_strerror(int status) {
   switch (status) {
     case GDN_OK: return "success";

@@ -70,6 +70,36 @@ cudaError_t launch_rollback_seq(float *S, const float *snap, const float *ckpt,
                                 const int *m_dev, int *err_dev, int B, int vh,
                                 int M, cudaStream_t stream);
 
+// Linear attention with a decay for each head (gdn_linattn_step_m): token
+// rows q, k, v, o in fp32 or bf16, states and g in fp32.  S_out may equal
+// S_in, ckpt may be null.  lens (device, or null): sequence b has its first
+// lens[b] of the M tokens; a value outside 0..M leaves the sequence alone
+// and raises *err (may be null).
+struct LinattnArgs {
+  const float *S_in;
+  float *S_out, *ckpt;
+  const void *q, *k, *v;
+  const float *g;
+  void *o;
+  const int *lens;
+  int *err;
+  float scale;
+  int g_head;  // g is [vh] rather than [B][M][vh]
+  int B, kh, vh, rep, M;
+};
+cudaError_t launch_linattn_steps(const LinattnArgs &P, bool bf16,
+                                 cudaStream_t stream);
+// The same over whole prompts (gdn_linattn_prefill), in place.
+size_t linattn_prefill_workspace_bytes(int B, int vh, int T, bool bf16);
+cudaError_t launch_linattn_prefill(const LinattnArgs &P, bool bf16,
+                                   void *workspace, cudaStream_t stream);
+
+// y = x W^T, W in 4 bits with fp16 group scales (gdn_quant_linear).
+cudaError_t launch_quant_linear(const void *x, const unsigned char *qw,
+                                const void *scales, void *y, int rows, int N,
+                                int K, int group, bool bf16,
+                                cudaStream_t stream);
+
 // Chunked tensor-core prefill (defined in gdn_prefill.cu).
 size_t prefill_workspace_bytes(int B, int kh, int vh, int T, int chunk,
                                int precision);

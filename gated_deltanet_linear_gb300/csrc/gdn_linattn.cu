@@ -1,0 +1,231 @@
+// Token-serial linear attention with a decay for each head, for sm_103a
+// (decode, M-token verify).
+//
+// What it computes (per sequence b, value head vi, key head hh = vi / rep,
+// token m):
+//     S = exp(g) S + k v^T;   o = scale S^T q.
+// The delta rule of gdn_decode.cu without its correction: nothing of the
+// state has to be reduced before it is updated, so a token is one pass of
+// multiply-adds over registers and the only reduction is o's.
+//
+// Work split.  A CTA of 4 warps takes a 32-column group of a head (16 KB of
+// the 64 KB state), so that one sequence of 48 heads still gives every SM
+// work.  Warp w has key rows 32w .. 32w+31; lane = 8 rg + cl has rows
+// 32w + 8 rg .. + 7 and columns 4 cl .. 4 cl + 3 of the group: one warp
+// request covers four whole 128-byte row segments, and a lane's q and k are
+// 8 consecutive elements.  The 8 x 4 block stays in registers for all M
+// tokens: the state is read once and written once per launch.  The partial
+// sums of o meet in shared memory, one barrier for every 8 tokens.
+//
+// Determinism.  Every product and sum is an explicit round-to-nearest
+// intrinsic in a fixed tree (a lane's rows in order, the row groups
+// (0 + 1) + (2 + 3), the warps (0 + 2) + (1 + 3)), so M tokens in one launch
+// give the bits of M launches.
+//
+// Bound by HBM: 128 KB of state per head against three FP32 lane operations
+// per state element and token.
+
+#include <cuda_bf16.h>
+
+#include "gdn_internal.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kBlk = 8;  // tokens between barriers
+
+__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
+  const float4 b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
+  const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ void load4(const float *p, float (&x)[4]) {
+  const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+}
+
+__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&x)[4]) {
+  const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
+  x[0] = __uint_as_float(u.x << 16);
+  x[1] = __uint_as_float(u.x & 0xffff0000u);
+  x[2] = __uint_as_float(u.y << 16);
+  x[3] = __uint_as_float(u.y & 0xffff0000u);
+}
+
+__device__ __forceinline__ void store4(float *p, const float (&x)[4]) {
+  *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float (&x)[4]) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]);
+  const __nv_bfloat162 b = __floats2bfloat162_rn(x[2], x[3]);
+  uint2 u;
+  u.x = *reinterpret_cast<const uint32_t *>(&a);
+  u.y = *reinterpret_cast<const uint32_t *>(&b);
+  *reinterpret_cast<uint2 *>(p) = u;
+}
+
+__device__ __forceinline__ float4 ld_state(const float *p) {
+  float4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ void st_state(float *p, const float4 &v) {
+  asm volatile("st.global.L1::no_allocate.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p),
+               "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
+}
+
+template <typename T>
+struct Token {
+  float k[8], q[8], v[4], a;
+  // token m of the head's rows; g: this head's log decay of the token
+  __device__ __forceinline__ void load(const T *qp, const T *kp, const T *vp,
+                                       const float *gp) {
+    load8(qp, q);
+    load8(kp, k);
+    load4(vp, v);
+    a = __ldg(gp);
+  }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(128)
+    linattn_steps_kernel(const LinattnArgs P) {
+  __shared__ float part[2][kBlk][4][32];
+  // behind the kernel before it: nothing is read or written before that
+  // kernel has ended
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int head = blockIdx.x >> 2, cg = blockIdx.x & 3;
+  const int b = head / P.vh, vi = head % P.vh, hh = vi / P.rep;
+  int n = P.M;
+  if (P.lens) {
+    n = __ldg(P.lens + b);
+    if (n < 0 || n > P.M) {
+      if (tid == 0 && P.err) *P.err = 1;
+      return;
+    }
+  }
+  const int row = 32 * warp + 8 * (lane >> 3);
+  const int col = 32 * cg + 4 * (lane & 7);
+  const size_t blk = (size_t)row * kDim + col;  // of the state
+
+  const size_t tok0 = (size_t)b * P.M;
+  const T *qp = static_cast<const T *>(P.q) + (tok0 * P.kh + hh) * kDim + row;
+  const T *kp = static_cast<const T *>(P.k) + (tok0 * P.kh + hh) * kDim + row;
+  const T *vp = static_cast<const T *>(P.v) + (tok0 * P.vh + vi) * kDim + col;
+  T *op = static_cast<T *>(P.o) + (tok0 * P.vh + vi) * kDim + 32 * cg;
+  const float *gp = P.g + (P.g_head ? (size_t)vi : tok0 * P.vh + vi);
+  const size_t qk_step = (size_t)P.kh * kDim, v_step = (size_t)P.vh * kDim;
+  const size_t g_step = P.g_head ? 0 : P.vh;
+
+  float4 s[8];
+  {
+    const float *Sp = P.S_in + (size_t)head * kDim * kDim + blk;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = ld_state(Sp + i * kDim);
+  }
+  Token<T> t;
+  if (n > 0) t.load(qp, kp, vp, gp);
+  int buf = 0;
+  for (int m0 = 0; m0 < n; m0 += kBlk) {
+    const int nb = min(kBlk, n - m0);
+    for (int j = 0; j < nb; ++j) {
+      const int m = m0 + j;
+      Token<T> u = t;
+      if (m + 1 < n)
+        t.load(qp + (m + 1) * qk_step, kp + (m + 1) * qk_step,
+               vp + (m + 1) * v_step, gp + (m + 1) * g_step);
+      const float a = expf(u.a);
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        s[i].x = __fmaf_rn(a, s[i].x, __fmul_rn(u.k[i], u.v[0]));
+        s[i].y = __fmaf_rn(a, s[i].y, __fmul_rn(u.k[i], u.v[1]));
+        s[i].z = __fmaf_rn(a, s[i].z, __fmul_rn(u.k[i], u.v[2]));
+        s[i].w = __fmaf_rn(a, s[i].w, __fmul_rn(u.k[i], u.v[3]));
+        acc[0] = __fmaf_rn(s[i].x, u.q[i], acc[0]);
+        acc[1] = __fmaf_rn(s[i].y, u.q[i], acc[1]);
+        acc[2] = __fmaf_rn(s[i].z, u.q[i], acc[2]);
+        acc[3] = __fmaf_rn(s[i].w, u.q[i], acc[3]);
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        acc[c] = __fadd_rn(acc[c], __shfl_xor_sync(kFull, acc[c], 8));
+        acc[c] = __fadd_rn(acc[c], __shfl_xor_sync(kFull, acc[c], 16));
+      }
+      if (lane < 8)
+        *reinterpret_cast<float4 *>(&part[buf][j][warp][4 * lane]) =
+            make_float4(acc[0], acc[1], acc[2], acc[3]);
+      if (P.ckpt) {
+        float *cp = P.ckpt + (((size_t)m * P.B * P.vh) + head) * kDim * kDim + blk;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) st_state(cp + i * kDim, s[i]);
+      }
+    }
+    __syncthreads();
+    // (the other buffer is written next; this one again only after the
+    // next barrier, which follows these reads)
+    if (tid < 8 * nb) {
+      const int j = tid >> 3, c = 4 * (tid & 7);
+      float y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        y[e] = __fmul_rn(P.scale,
+                         __fadd_rn(__fadd_rn(part[buf][j][0][c + e], part[buf][j][2][c + e]),
+                                   __fadd_rn(part[buf][j][1][c + e], part[buf][j][3][c + e])));
+      store4(op + (m0 + j) * v_step + c, y);
+    }
+    buf ^= 1;
+  }
+  float *So = P.S_out + (size_t)head * kDim * kDim + blk;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) st_state(So + i * kDim, s[i]);
+}
+
+}  // namespace
+
+cudaError_t launch_linattn_steps(const LinattnArgs &P, bool bf16,
+                                 cudaStream_t stream) {
+  const size_t blocks = (size_t)P.B * P.vh * 4;
+  if (blocks == 0) return cudaSuccess;
+  if (blocks > 0x7fffffffull) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return bf16 ? cudaLaunchKernelEx(&cfg, linattn_steps_kernel<__nv_bfloat16>, P)
+              : cudaLaunchKernelEx(&cfg, linattn_steps_kernel<float>, P);
+}
+
+size_t linattn_prefill_workspace_bytes(int, int, int, bool) { return 0; }
+
+cudaError_t launch_linattn_prefill(const LinattnArgs &P, bool bf16, void *,
+                                   cudaStream_t stream) {
+  return launch_linattn_steps(P, bf16, stream);
+}
+
+}  // namespace gdn

@@ -386,6 +386,104 @@ int gdn_layer_step_m_noalloc(const gdn_shape *shape, int M, int ck, float eps,
                              const float *A_log, const float *dt_bias,
                              float *o, gdn_stream_t stream);
 
+/* Element types of the token tensors of the calls below. */
+enum { GDN_F32 = 0, GDN_BF16 = 1 };
+
+/* Where the log decay g of the linear-attention calls comes from. */
+enum {
+    GDN_DECAY_TOKEN = 0, /* g [B][T][vh]: one per token and value head       */
+    GDN_DECAY_HEAD = 1   /* g [vh]: one per value head, the same every token */
+};
+
+/*
+ * gdn_linattn_step - one token of linear attention with a decay for each
+ * head, for all B * vh heads, state updated in place:
+ *     S = exp(g) S + k v^T;   o = scale * S^T q      (with the updated S).
+ * The recurrence of gdn_step without its correction (no beta), on the same
+ * states and head layout, so gdn_mark, gdn_rollback and gdn_rollback_seq
+ * serve these states too, and gdn_gated_rmsnorm_m takes its fp32 o.
+ *   dtype  GDN_F32 or GDN_BF16: the type of q, k, v and o (GDN_EINVAL
+ *          otherwise).  S and g are fp32; every product and sum is fp32, and
+ *          a bf16 o is rounded once.
+ *   decay  GDN_DECAY_TOKEN: g [B][vh];  GDN_DECAY_HEAD: g [vh].
+ *   scale  finite factor on o (GDN_EINVAL otherwise)
+ *   S      [B][vh][kd][vd]  in/out;   q, k [B][kh][kd];   v, o [B][vh][vd]
+ * Any g is taken, -inf among them (the state is emptied; a state that holds
+ * infinities or NaN gives NaN then, as 0 * inf does).
+ * Token tensors are device memory (no mapped host memory).
+ */
+int gdn_linattn_step(const gdn_shape *shape, int dtype, int decay, float scale,
+                     float *S, const void *q, const void *k, const void *v,
+                     const float *g, void *o, gdn_stream_t stream);
+
+/*
+ * gdn_linattn_step_m - M tokens in one launch, the state read once and
+ * written once.  Arguments as in gdn_step_m and gdn_linattn_step:
+ *   S_in, S_out [B][vh][kd][vd] (S_out may equal S_in exactly);
+ *   ckpt [M][B][vh][kd][vd] or NULL: ckpt[m] = state after token m;
+ *   q, k [B][M][kh][kd];  v, o [B][M][vh][vd];  g [B][M][vh] or [vh].
+ * 1 <= M <= GDN_MAX_TOKENS (GDN_ERANGE otherwise).  Output m and ckpt[m] are
+ * bit-identical to the m-th of M gdn_linattn_step calls.  The launch is a
+ * programmatic dependent of the kernel before it on the stream and touches
+ * no memory before that kernel has completed.
+ */
+int gdn_linattn_step_m(const gdn_shape *shape, int M, int dtype, int decay,
+                       float scale, const float *S_in, float *S_out,
+                       float *ckpt, const void *q, const void *k,
+                       const void *v, const float *g, void *o,
+                       gdn_stream_t stream);
+
+/*
+ * gdn_linattn_prefill_workspace - bytes of device workspace that
+ * gdn_linattn_prefill needs (0 if none, and on invalid arguments).
+ */
+size_t gdn_linattn_prefill_workspace(const gdn_shape *shape, int T, int dtype);
+
+/*
+ * gdn_linattn_prefill - a prompt of T tokens for every sequence, state in
+ * place (in: S_0, out: the state after the sequence's last token).
+ *   q, k [B][T][kh][kd];  v, o [B][T][vh][vd];  g [B][T][vh] or [vh].
+ *   lens   device int [B], or NULL (every sequence has T tokens): sequence b
+ *          has its first lens[b] rows; its other rows of o keep what they
+ *          held and its other rows of q, k, v, g are not used, whatever they
+ *          hold.  0 is a length.  A value outside 0..T leaves the sequence's
+ *          S and o as they were and sets *err_dev (device int, may be NULL)
+ *          to 1.
+ *   workspace  at least gdn_linattn_prefill_workspace() bytes (GDN_ERANGE if
+ *          smaller, GDN_EINVAL if NULL where bytes are needed); calls that
+ *          may overlap on the GPU need one each.
+ * 1 <= T <= GDN_MAX_TOKENS and T * vh < 2^31 (GDN_ERANGE otherwise).
+ */
+int gdn_linattn_prefill(const gdn_shape *shape, int T, int dtype, int decay,
+                        float scale, float *S, const void *q, const void *k,
+                        const void *v, const float *g, void *o,
+                        const int *lens, int *err_dev, void *workspace,
+                        size_t ws_bytes, gdn_stream_t stream);
+
+/* Largest N and K of gdn_quant_linear. */
+#define GDN_QUANT_MAX_DIM (1 << 20)
+
+/*
+ * gdn_quant_linear - a projection with 4-bit weights,
+ *     y[r][n] = sum_k x[r][k] * code[n][k] * scale[n][k / group],
+ * for the rows (tokens) of a decode or verify step: steps 1 and 7 of figure
+ * 1 of "24 · GDN linear attention to GPU" (the projections in front of and
+ * behind the layer core), with M rows as in "34 · batched M rows", section
+ * 3.3, and the weight format of article 24's q4 path (two's complement codes,
+ * fp16 scales).
+ *   x       [rows][K], y [rows][N]: GDN_F32 or GDN_BF16 (dtype)
+ *   qw      [N][K/2] bytes: element 2j of a row in the low half of byte j,
+ *           element 2j + 1 in the high half, each -8..7 in two's complement
+ *   scales  [N][K/group] fp16
+ *   group   32, 64 or 128; K a positive multiple of it (GDN_ESHAPE otherwise)
+ * N, K <= GDN_QUANT_MAX_DIM, rows <= GDN_MAX_TOKENS (GDN_ERANGE otherwise);
+ * rows == 0 or N == 0 is a no-op.  Sums are fp32; results are the same bits
+ * on every call.
+ */
+int gdn_quant_linear(int rows, int N, int K, int group, int dtype,
+                     const void *x, const unsigned char *qw,
+                     const void *scales, void *y, gdn_stream_t stream);
+
 /* Static description of a status code (never NULL).  The codes are the
  * refusals of "24 · GDN linear attention to GPU", section 8 (a request the
  * library cannot serve as asked is refused with an error, never served by a

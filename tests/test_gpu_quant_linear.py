@@ -1,0 +1,179 @@
+"""Projections with 4-bit weights against a plain 64-bit product.
+
+Tolerance, against the magnitude sum |x||w|: an element of x enters as a sum
+of two 11-bit parts (2^-22; exact for bf16 within 2^-25 of the row's
+largest element's binade), code * scale is exact in fp32, and the fp32 sums run over
+at most K / 16 + 64 steps of 2^-23 (a tensor product may truncate).  bf16
+results add their own rounding, and bf16 rows in the form for many rows take
+the weights rounded to fp16 (2^-11).
+"""
+
+import pytest
+import torch
+
+import gated_deltanet_linear_gb300 as gdn
+from linattn_ref import (assert_within, half_step, linattn, make_linattn, make_quant,
+                         quant_linear, weights)
+
+pytestmark = pytest.mark.gpu
+TYPES = {"fp32": torch.float32, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__
+    __graft_entry__.build()
+    torch.cuda.set_device(0)
+
+
+def tol(K, dtype, ref, mag):
+    t = (K / 16 + 64) * 2.0 ** -23 + (2.0 ** -11 if dtype == torch.bfloat16 else 0.0)
+    return t * mag + half_step(dtype) * (ref.abs() + t * mag)
+
+
+def check(x, qw, sc):
+    y = torch.full((x.shape[0] + 1, qw.shape[0]), -3.0, device="cuda", dtype=x.dtype)
+    gdn.gdn_quant_linear(x, qw, sc, y[:-1])
+    ref, mag = quant_linear(x, qw, sc)
+    assert_within(y[:-1], ref, tol(x.shape[1], x.dtype, ref, mag), "y")
+    assert (y[-1] == -3.0).all()
+    return y[:-1]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("rows,N,groups", [
+    (1, 1, 1), (1, 48, 40), (1, 1000, 3), (2, 17, 5), (3, 129, 7), (4, 16, 64), (5, 300, 9),
+    (7, 33, 2), (8, 2056, 20), (9, 64, 33), (13, 15, 3), (16, 500, 8), (17, 130, 11),
+    (33, 257, 4), (64, 700, 21), (65, 40, 6), (130, 129, 3), (300, 20, 2)])
+def test_product(dtype, group, rows, N, groups):
+    check(*make_quant(rows * N + group, rows, N, groups * group, group, TYPES[dtype]))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", [1, 6, 40])
+def test_codes_and_order(dtype, rows):
+    """Every code at every position: x picks single elements, scales are
+    powers of two, so results are exact."""
+    K, N, group = 256, 64, 32
+    qw = torch.arange(N * K // 2, device="cuda").mul(37).remainder(256).to(torch.uint8).view(N, K // 2)
+    sc = torch.exp2((torch.arange(N * K // group, device="cuda") % 9 - 4).float()).half().view(N, -1)
+    w = weights(qw, sc)
+    for k0 in range(0, K, rows):
+        k = torch.arange(k0, min(K, k0 + rows), device="cuda")
+        x = torch.zeros(len(k), K, device="cuda", dtype=TYPES[dtype])
+        x[torch.arange(len(k)), k] = 1.0
+        y = torch.empty(len(k), N, device="cuda", dtype=TYPES[dtype])
+        gdn.gdn_quant_linear(x, qw, sc, y)
+        assert torch.equal(y.double(), w[:, k].t())
+
+
+@pytest.mark.parametrize("rows", [1, 5, 40])
+def test_ranges(rows):
+    """Rows of very different size beside each other, elements far below
+    their row's largest, scales down to fp16's subnormals."""
+    x, qw, sc = make_quant(3, rows, 200, 512, 64)
+    x *= torch.logspace(-20, 20, rows, device="cuda")[:, None]
+    x[:, ::3] *= 2.0 ** -20
+    x[:, 1::5] = 0.0
+    sc = sc * 0 + torch.logspace(-7, 4, sc.numel(), device="cuda").view_as(sc).half()
+    check(x, qw, sc)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", [1, 5, 40])
+def test_non_finite_rows_stay_apart(dtype, rows):
+    x, qw, sc = make_quant(4, rows + 2, 100, 256, 64, TYPES[dtype])
+    y0 = check(x, qw, sc)
+    x[0, 5], x[-1, 7] = float("nan"), float("inf")
+    y = torch.empty_like(y0)
+    gdn.gdn_quant_linear(x, qw, sc, y)
+    assert not torch.isfinite(y[0]).any() and torch.isnan(y[0]).all()
+    code = weights(qw, sc)[:, 7] != 0
+    assert not torch.isfinite(y[-1][code]).any()
+    assert torch.equal(y[1:-1], y0[1:-1])
+    x[0] = 0
+    gdn.gdn_quant_linear(x, qw, sc, y)
+    assert (y[0] == 0).all()
+
+
+def test_same_bits_and_graph():
+    for rows in (1, 8, 50):
+        x, qw, sc = make_quant(6, rows, 777, 1024, 128)
+        y, y2 = (torch.empty(rows, 777, device="cuda") for _ in range(2))
+        gdn.gdn_quant_linear(x, qw, sc, y)
+        stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(graph, stream=stream):
+            gdn.gdn_quant_linear(x, qw, sc, y2)
+        y2.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, y2)
+
+
+def test_weights_beyond_32_bits():
+    """More than 2^32 weights: the last rows against their own product."""
+    N, K, group = 300000, 16384, 128
+    x, qw, sc = make_quant(8, 2, 1000, K, group)
+    big, bs = qw.repeat(N // 1000, 1), sc.repeat(N // 1000, 1)
+    y = torch.empty(2, N, device="cuda")
+    gdn.gdn_quant_linear(x, big, bs, y)
+    ref, mag = quant_linear(x, qw, sc)
+    t = tol(K, x.dtype, ref, mag)
+    for a in (0, N // 2, N - 1000):
+        assert_within(y[:, a:a + 1000], ref, t, f"rows from {a}")
+
+
+@pytest.mark.parametrize("rows", [1, 4])
+def test_layer_run(rows):
+    """In-projection, linear-attention steps, gated norm, out-projection: one
+    layer step from hidden state to hidden state, against the same in fp64."""
+    B, kh, vh, hidden = rows, 2, 4, 512
+    conv = 2 * kh * 128 + vh * 128
+    x, w_in, s_in = make_quant(1, B, conv, hidden, 64)
+    z, w_out, s_out = make_quant(2, B, hidden, vh * 128, 64)
+    d = make_linattn(3, B, 1, kh, vh, decay="head")
+    w = torch.ones(128, device="cuda")
+    proj = torch.empty(B, conv, device="cuda")
+    gdn.gdn_quant_linear(x, w_in, s_in, proj)
+    q, k, v = (t.contiguous() for t in proj.split([kh * 128, kh * 128, vh * 128], 1))
+    S, o = d["S"].clone(), torch.empty(B, vh, 128, device="cuda")
+    gdn.gdn_linattn_step(S, q.view(B, kh, 128), k.view(B, kh, 128), v.view(B, vh, 128), d["g"], o)
+    y = torch.empty(B, 1, vh, 128, device="cuda")
+    gdn.gdn_gated_rmsnorm_m(o.view(B, 1, vh, 128), z.view(B, 1, vh, 128), w, y)
+    out = torch.empty(B, hidden, device="cuda")
+    gdn.gdn_quant_linear(y.view(B, vh * 128), w_out, s_out, out)
+    # fp64
+    p, _ = quant_linear(x, w_in, s_in)
+    q, k, v = p.split([kh * 128, kh * 128, vh * 128], 1)
+    ref = linattn(d["S"], q.view(B, 1, kh, 128), k.view(B, 1, kh, 128), v.view(B, 1, vh, 128), d["g"])
+    r = ref["o"] / (ref["o"].square().mean(-1, keepdim=True) + 1e-6).sqrt()
+    zz = z.double().view(B, 1, vh, 128)
+    r = (r * zz * torch.sigmoid(zz)).view(B, vh * 128)
+    want, _ = quant_linear(r, w_out, s_out)
+    # each stage is off by at most some 2^-17 of its magnitudes; the sums here
+    # cancel by less than 2^5
+    assert (out - want).norm() <= 2.0 ** -12 * want.norm()
+    assert (S - ref["S"]).norm() <= 2.0 ** -12 * ref["S"].norm()
+
+
+def test_refusals():
+    x, qw, sc = make_quant(1, 2, 10, 128, 64)
+    y = torch.empty(2, 10, device="cuda")
+    with pytest.raises(ValueError):
+        gdn.gdn_quant_linear(x.half(), qw, sc, y)
+    with pytest.raises(ValueError):
+        gdn.gdn_quant_linear(x, qw, sc.float(), y)
+    with pytest.raises(ValueError):
+        gdn.gdn_quant_linear(x, qw[:, :-1].contiguous(), sc, y)
+    with pytest.raises(ValueError):
+        gdn.gdn_quant_linear(x, qw, sc, y.t())
+    with pytest.raises(gdn.GDNError) as e:
+        gdn.gdn_quant_linear(x, qw, sc.repeat(1, 4)[:, :8].contiguous(), y)  # groups of 16
+    assert e.value.status == gdn.GDN_ESHAPE
+    big = torch.empty(64, 64, device="cuda")
+    with pytest.raises(gdn.GDNError) as e:  # y over x
+        gdn.gdn_quant_linear(big, torch.zeros(64, 32, device="cuda", dtype=torch.uint8),
+                             torch.ones(64, 1, device="cuda").half(), big)
+    assert e.value.status == gdn.GDN_EALIAS
