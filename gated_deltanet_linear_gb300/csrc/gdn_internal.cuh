@@ -93,6 +93,8 @@ cudaError_t launch_linattn_steps(const LinattnArgs &P, bool bf16,
 size_t linattn_prefill_workspace_bytes(int B, int vh, int T, bool bf16);
 cudaError_t launch_linattn_prefill(const LinattnArgs &P, bool bf16,
                                    void *workspace, cudaStream_t stream);
+// CTAs of it that gave up a wait.
+cudaError_t linattn_timeouts(unsigned int *count);
 
 // y = x W^T, W in 4 bits with fp16 group scales (gdn_quant_linear).
 cudaError_t launch_quant_linear(const void *x, const unsigned char *qw,

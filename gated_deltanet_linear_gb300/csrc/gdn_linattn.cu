@@ -221,11 +221,4 @@ cudaError_t launch_linattn_steps(const LinattnArgs &P, bool bf16,
               : cudaLaunchKernelEx(&cfg, linattn_steps_kernel<float>, P);
 }
 
-size_t linattn_prefill_workspace_bytes(int, int, int, bool) { return 0; }
-
-cudaError_t launch_linattn_prefill(const LinattnArgs &P, bool bf16, void *,
-                                   cudaStream_t stream) {
-  return launch_linattn_steps(P, bf16, stream);
-}
-
 }  // namespace gdn
