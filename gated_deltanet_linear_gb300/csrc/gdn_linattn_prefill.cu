@@ -25,8 +25,8 @@
 // 2^-17 of it keep all their bits.  The scores of row t are scaled by the
 // largest k row up to t.  The state is kept in fp32 registers: a chunk's KV
 // product is read out, unscaled and added, so scales may differ from chunk to
-// chunk.  Gamma is summed in fp64 and its differences are split into two
-// floats, so strong decays keep the small differences between near tokens.
+// chunk.  Gamma is summed as two floats (48 bits), so strong decays
+// keep the small differences between near tokens.
 //
 // Roles (20 warps, one CTA per SM, persistent over (sequence, head, segment)
 // units): 8 warps A hold the state and make its operand and the two V
@@ -66,8 +66,11 @@ constexpr int kSms = 152;
 constexpr uint32_t kWaitLimit = 1u << 24;
 
 // Shared memory (bytes from a 1024-aligned base).  The q, k regions hold a
-// chunk's staged rows (K then Q), converted in place to the [K; Q] operand:
-// 128 rows x 128 fp16, 128-byte swizzle, the hi tile then the lo tile.
+// chunk's staged rows (K then Q), converted in place to the [K; Q] operand of
+// 128 rows x 128 fp16: the rows of a group of 8 stay in the bytes that they
+// were staged in, as 128-byte-swizzled blocks of 8 rows x 64 columns (hi
+// columns 0-63, hi 64-127, then the same of lo), so a warp converts a group by
+// itself.
 constexpr uint32_t OFF_KQ = 0, kKQ = 65536;   // by chunk parity
 constexpr uint32_t OFF_V = 131072;            // staged v rows [64][128]
 constexpr uint32_t OFF_O = 163840;            // o tile [64][128]
@@ -106,49 +109,51 @@ struct Args {
   const int *lens;
   int *err;
   float scale;
-  int g_head, vh, rep, T, nseg, nchunks, units;
+  int g_head, vh, rep, T, nseg, per_seg, units;  // per_seg: chunks of a segment
 };
 
 // ------------------------------------------------------------- sequencing
 
 // The chunks this CTA works on, in order; every role walks the same list.
+// (next() is written once per role: the code of all roles together should
+// stay within the instruction cache.)
 template <bool kLocal>
 struct Walk {
   const Args *p;
   int u, c, c_hi, it;   // unit, chunk, end of its chunks, running index
   int head, b, vi, seg, n;
   bool ok, first;
-  __device__ Walk(const Args &P) : p(&P), u((int)blockIdx.x - (int)gridDim.x), it(0) {
-    unit();
-  }
+  __device__ Walk(const Args &P)
+      : p(&P), u((int)blockIdx.x - (int)gridDim.x), c(0), c_hi(0), it(-1), ok(false) {}
   // Decodes unit u; false if its sequence has no valid length.
-  __device__ bool decode() {
-    const int per = kLocal ? p->nseg - 1 : p->nseg;
-    head = u / per;
+  __device__ __forceinline__ bool decode() {
+    const unsigned per = kLocal ? p->nseg - 1 : p->nseg;
+    head = (unsigned)u / per;
     seg = u - head * per;
-    b = head / p->vh;
+    b = (unsigned)head / (unsigned)p->vh;
     vi = head - b * p->vh;
-    n = p->lens ? __ldg(p->lens + b) : p->T;
+    n = p->T;
+    if (p->lens) n = __shfl_sync(0xffffffffu, __ldg(p->lens + b), 0);
     const bool good = n >= 0 && n <= p->T;
     if (!good) n = 0;
-    c = (int)((long long)seg * p->nchunks / p->nseg);
-    c_hi = min((int)((long long)(seg + 1) * p->nchunks / p->nseg), (n + kC - 1) / kC);
+    c = seg * p->per_seg;
+    c_hi = min(c + p->per_seg, (n + kC - 1) / kC);
     return good;
   }
-  __device__ void unit() {
-    first = true;
-    for (;;) {
-      u += gridDim.x;
-      ok = u < p->units;
-      if (!ok) return;
-      decode();
-      if (c < c_hi) return;
-    }
-  }
-  __device__ void next() {
+  // The next chunk; false (and !ok) behind the last one.
+  __device__ __forceinline__ bool next() {
     ++it;
     first = false;
-    if (++c >= c_hi) unit();
+    ok = true;
+    if (++c < c_hi) return true;
+    first = true;
+#pragma unroll 1
+    do {
+      u += gridDim.x;
+      if (u >= p->units) return ok = false;
+      decode();
+    } while (c >= c_hi);
+    return true;
   }
   __device__ bool last() const { return c + 1 >= c_hi; }
   __device__ int valid() const { return min(kC, n - c * kC); }  // tokens
@@ -165,9 +170,36 @@ __device__ __forceinline__ int scale_exp(float m) {
   return min(141 - (__float_as_int(m) >> 23), 126);
 }
 
-// max |x| that keeps NaN (as a bit pattern above infinity's)
+// max(|m|, |x|) and max(|m|, |x|, |y|), NaN if any is
 __device__ __forceinline__ float amax(float m, float x) {
-  return __int_as_float(max(__float_as_int(m), __float_as_int(x) & 0x7fffffff));
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(m)), "f"(fabsf(x)));
+  return r;
+}
+__device__ __forceinline__ float amax(float m, float x, float y) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(x), "f"(y));
+  return r;
+}
+
+// Unevaluated sum of two floats (about 48 bits): the cumulative log decays.
+struct Two {
+  float h, l;
+};
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  const float s = a.h + b.h, v = s - a.h;
+  const float e = (a.h - (s - v)) + (b.h - v) + (a.l + b.l);
+  const float h = s + e;
+  return Two{h, e - (h - s)};
+}
+__device__ __forceinline__ Two neg2(Two a) { return Two{-a.h, -a.l}; }
+// 2^x: exp2 of the high part times 1 + ln 2 of the low one
+__device__ __forceinline__ float ex2(Two x) {
+  const float e = exp2f(x.h);
+  return fmaf(e, x.l * 0.69314718f, e);
+}
+__device__ __forceinline__ Two shfl_up2(Two x, int d) {
+  return Two{__shfl_up_sync(0xffffffffu, x.h, d), __shfl_up_sync(0xffffffffu, x.l, d)};
 }
 
 __device__ __forceinline__ uint32_t h2_bits(__half2 v) {
@@ -184,18 +216,14 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t 
   }
 }
 
-// Columns c0 .. c0+7 of row r of an R x C tile (hi; lo behind it), times s.
+// Eight elements times s: hi parts to the 16 bytes at p, lo parts `lo_off` on.
 template <bool kLo>
-__device__ __forceinline__ void put8(unsigned char *gb, uint32_t off, int R, int C,
-                                     int r, int c0, const float *x, float s) {
+__device__ __forceinline__ void put8(unsigned char *p, uint32_t lo_off, const float *x, float s) {
   uint32_t hi[4], lo[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) split2<kLo>(x[2 * i] * s, x[2 * i + 1] * s, hi[i], lo[i]);
-  const uint32_t o = off + sw128_off(R, r, c0, 2);
-  *reinterpret_cast<uint4 *>(gb + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-  if (kLo)
-    *reinterpret_cast<uint4 *>(gb + o + (uint32_t)(R * C * 2)) =
-        make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  *reinterpret_cast<uint4 *>(p) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  if (kLo) *reinterpret_cast<uint4 *>(p + lo_off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }
 
 // Elements c0 .. c0+15 of this lane of an A operand in TMEM, times s.
@@ -247,17 +275,39 @@ __device__ __forceinline__ void mbar_expect(uint32_t mbar, uint32_t bytes) {
 // soon as another role of the CTA has (the flag): every role then runs on to
 // the end, through the same barriers, without waiting again.
 __device__ __forceinline__ void wait_bar(uint32_t bar, uint32_t parity, volatile int *fail) {
-  for (uint32_t i = 0; i < kWaitLimit; i += 256) {
-    if (mbar_wait(bar, parity, 256)) return;
-    if (*fail) return;
+#pragma unroll 1
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return;
+    if ((i & 255) == 255 && *fail) return;
   }
   *fail = 1;
 }
 
+// A warp's part of "operands ready" (one arrival per warp; 256 arrivals on one
+// barrier took longer than the work they announced): its TMEM accesses
+// ordered, and with kSmem its shared-memory writes made visible to the tensor
+// cores.
+template <bool kSmem>
 __device__ __forceinline__ void signal_ready(uint32_t mbar) {
-  fence_proxy_async();
+  if (kSmem) fence_proxy_async();
   fence_before_sync();
-  mbar_arrive(mbar);
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(mbar);
+}
+
+// Where every role ends: after it nothing of the CTA is in flight.
+__device__ __forceinline__ void cta_end() {
+  fence_before_sync();
+  asm volatile("bar.sync 0, %0;" ::"n"(kThreads) : "memory");
+  fence_after_sync();
 }
 
 __device__ __forceinline__ void bar_pair(int quad) {  // warps w and w + 4 of A
@@ -289,17 +339,57 @@ __device__ __forceinline__ void tma_store(const CUtensorMap *map, int h, int t0,
 
 // ---------------------------------------------------------------- products
 
-// Shared-memory operand tile of R rows, C columns: descriptor of K step ks of
-// the hi (part 0) or lo tile.  K-major: rows are M or N.  MN-major: rows are K.
-__device__ __forceinline__ uint64_t kdesc(uint32_t base, int R, int ks) {
-  return desc_kstep(base, R, ks);
+// Descriptors: the high word holds the stride between 8-row groups, the low
+// word the address (and, MN-major, the distance of 64-column blocks), so the
+// steps of a product are additions to the low word.
+__device__ __forceinline__ uint32_t desc_hi(uint32_t stride) {
+  return (uint32_t)(desc_sw128(0) >> 32) & ~0x3FFFu | (stride >> 4);
+}
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead) {
+  return ((addr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16);
+}
+__device__ __forceinline__ uint64_t desc64(uint32_t hi, uint32_t lo) {
+  return ((uint64_t)hi << 32) | lo;
+}
+// Bytes of K step ks (16 elements) from a K-major operand's start.
+__host__ __device__ constexpr uint32_t kstep(int ks) {
+  return (uint32_t)((ks >> 2) * 1024 + (ks & 3) * 32);
 }
 
-__device__ __forceinline__ uint64_t mndesc(uint32_t base, int R, int ks) {
-  uint64_t d = desc_sw128(base + (uint32_t)ks * 2048u);
-  d &= ~((uint64_t)0x3FFF << 16);
-  d |= (uint64_t)(((uint32_t)R * 128u) >> 4) << 16;
-  return d;
+// The products are issued by a converged warp, one elected lane executing:
+// the operand addresses stay in uniform registers.  (Issued by lane 0 of a
+// diverged warp, each instruction took about 90 cycles.)
+__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint64_t a, uint64_t b,
+                                       uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc), "r"(one));
+}
+__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a, uint64_t b,
+                                       uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc), "r"(one));
+}
+__device__ __forceinline__ void commit_one(uint32_t one, uint32_t mbar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::
+          "r"(mbar),
+      "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r));
+  return r;
 }
 
 // ------------------------------------------------------------------ kernel
@@ -313,6 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                          const __grid_constant__ Args P) {
   constexpr bool kLo = !kBf16;                 // second parts of q, k, v, P, S
   constexpr uint32_t kRow = kBf16 ? 256 : 512; // bytes of a token row
+  constexpr uint32_t kGrp = 8 * kRow;          // of 8 rows, staged or converted
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw_s = (uint32_t)__cvta_generic_to_shared(smem_raw);
   const uint32_t sb = (raw_s + 1023u) & ~1023u;
@@ -342,9 +433,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kIssuer) tmem_alloc(sb + OFF_BAR + 160, 512);
   if (tid == 0) {
-    const int count[20] = {1, 1, 1, 1, kGroup, kGroup, 1, 8, kGroup, kGroup,
-                           kGroup, 1, 1, 1, kGroup, 1, 1, 1, 1, 1};
-    for (int i = 0; i < 20; ++i) mbar_init(bar(i), count[i]);
+    // one arrival each, or one from each warp of a group
+    constexpr uint32_t kByWarps = 1u << 4 | 1u << 5 | 1u << 7 | 1u << 8 | 1u << 9 | 1u << 10 | 1u << 14;
+#pragma unroll 1
+    for (int i = 0; i < 20; ++i) mbar_init(bar(i), (kByWarps >> i & 1) ? kGroup / 32 : 1);
     *fail = 0;
   }
   fence_before_sync();
@@ -353,7 +445,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *slot;
   const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
 
+  // Registers: launched with 640 x 96 = 61,440; 256 x 120 + 256 x 88 + 128 x 56
+  // = 60,416 after the split.  No code follows the roles' branches: it would
+  // have to fit the smallest count.
   if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
     // ============================================ group A: state, V operands
     float s[kC];  // state rows dk = 64 half .. + 63 of column dv = myrow
     float *ps = reinterpret_cast<float *>(gb + OFF_PS);
@@ -362,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto state_operand = [&](int it) {
       float m = 0.f;
 #pragma unroll
-      for (int j = 0; j < kC; ++j) m = amax(m, s[j]);
+      for (int j = 0; j < kC; j += 2) m = amax(m, s[j], s[j + 1]);
       ps[128 * half + myrow] = m;
       bar_pair(quad);
       const int e = scale_exp(amax(m, ps[128 * (half ^ 1) + myrow]));
@@ -372,11 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         put16<kLo>(tl + T_SOP, tl + T_SOP + 64, 64 * half + c0, s + c0, f);
       if (half == 0) lanef(it)[myrow] = pow2(-e);
       tmem_wait_st();
-      signal_ready(rdy_s);
-    };
-    auto store_state = [&](float *dst) {
-#pragma unroll
-      for (int j = 0; j < kC; ++j) dst[(size_t)(kC * half + j) * kD + myrow] = s[j];
+      signal_ready<false>(rdy_s);
     };
     // units without a chunk of their own: their states, and bad lengths
     if (P.lens || kLocal || P.nseg > 1) {
@@ -398,7 +490,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    for (Walk<kLocal> w(P); w.ok;) {
+    Walk<kLocal> w(P);
+    while (w.next()) {
       const int it = w.it;
       if (w.first) {
         const size_t at = ((size_t)w.head * P.nseg + w.seg) * kD * kD;
@@ -406,38 +499,53 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < kC; ++j)
           s[j] = kLocal ? 0.f : src[(size_t)(kC * half + j) * kD + myrow];
-        if (!kLocal) state_operand(it);
       }
+      if (!kLocal) state_operand(it);
       // ---- V^T and (V f)^T operands, lane dv, K = t = 32 half .. + 31
       wait_bar(vstaged, it & 1, fail);
       wait_bar(vecs + 8 * (it & 3), (it >> 2) & 1, fail);
       const float *vc = vec(it);
-      const int nv = w.valid() - 32 * half;  // of this thread's 32 tokens
+      // this thread's 32 values: column myrow of rows 32 half ..
+      unsigned char *vp = gb + OFF_V + 32 * half * kRow + myrow * (kRow / kD);
       auto vload = [&](int j) -> float {
-        const int t = 32 * half + j;
-        if (kBf16) {
-          const uint32_t h = *reinterpret_cast<const unsigned short *>(
-              gb + OFF_V + t * 256 + 2 * myrow);
-          return __uint_as_float(h << 16);
-        }
-        return *reinterpret_cast<const float *>(gb + OFF_V + t * 512 + 4 * myrow);
+        if (kBf16)
+          return __uint_as_float(
+              (uint32_t) * reinterpret_cast<const unsigned short *>(vp + j * kRow) << 16);
+        return *reinterpret_cast<const float *>(vp + j * kRow);
       };
+      const int nv = w.valid() - 32 * half;
+      if (nv < 32) {  // rows behind the end, whatever they hold, are zeros
+#pragma unroll 1
+        for (int j = max(nv, 0); j < 32; ++j) {
+          if (kBf16)
+            *reinterpret_cast<unsigned short *>(vp + j * kRow) = 0;
+          else
+            *reinterpret_cast<float *>(vp + j * kRow) = 0.f;
+        }
+        fence_proxy_async();  // the copy engine writes these bytes next
+      }
+      const float *vf = vc + VF + 32 * half;
       float ma = 0.f, mb = 0.f;
+#pragma unroll 1
+      for (int j0 = 0; j0 < 32; j0 += 8) {
+        float x[8];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const float x = j < nv ? vload(j) : 0.f;
-        ma = amax(ma, x);
-        mb = amax(mb, x * vc[VF + 32 * half + j]);
+        for (int j = 0; j < 8; ++j) x[j] = vload(j0 + j);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          ma = amax(ma, x[j], x[j + 1]);
+          mb = amax(mb, x[j] * vf[j0 + j], x[j + 1] * vf[j0 + j + 1]);
+        }
       }
       // A value that is not finite must not reach the rows before it (its
       // weight there is 0, but 0 * inf is NaN): PV takes 0 for it, and the
       // output becomes NaN from its token on.
       int bad = kC;
-      if (!kLocal && __float_as_int(ma) >= 0x7f800000) {
+      if (!kLocal && !isfinite(ma)) {
         ma = 0.f;
 #pragma unroll 1
         for (int j = 31; j >= 0; --j) {
-          const float x = j < nv ? vload(j) : 0.f;
+          const float x = vload(j);
           if (!isfinite(x))
             bad = 32 * half + j;
           else
@@ -456,29 +564,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_after_sync();
         if (half == 0) lanef(it)[128 + myrow] = pow2(-ea);
       }
-#pragma unroll
+#pragma unroll 1
       for (int c0 = 0; c0 < 32; c0 += 16) {
         float x[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = c0 + j < nv ? vload(c0 + j) : 0.f;
         const int t0 = 32 * half + c0;
-        if (!kLocal) {
-          float y[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) y[j] = x[j];
+        for (int j = 0; j < 16; ++j) x[j] = vload(c0 + j) * vf[c0 + j];
+        put16<true>(tl + T_WOP, tl + T_WOP + 32, t0, x, fb);
+        if (!kLocal) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) x[j] = vload(c0 + j);
           if (bad < kC)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) y[j] = isfinite(x[j]) ? x[j] : 0.f;
-          put16<kLo>(tl + T_VOP, tl + T_VOP + 32, t0, y, fa);
+            for (int j = 0; j < 16; ++j) x[j] = isfinite(x[j]) ? x[j] : 0.f;
+          put16<kLo>(tl + T_VOP, tl + T_VOP + 32, t0, x, fa);
         }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] *= vc[VF + t0 + j];
-        put16<true>(tl + T_WOP, tl + T_WOP + 32, t0, x, fb);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(v_free);
       tmem_wait_st();
-      signal_ready(rdy_v);
+      signal_ready<false>(rdy_v);
       // ---- the state after the chunk
       const float gC = vc[VM], inv = pow2(-eb);
       wait_bar(done_kv, it & 1, fail);
@@ -492,151 +597,199 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < 32; ++j)
           s[c0 + j] = fmaf(gC, s[c0 + j], __uint_as_float(d[j]) * inv);
       }
-      if (w.last()) {
-        const size_t hd = (size_t)w.head * kD * kD;
-        if (kLocal)
-          store_state(P.ws_state + ((size_t)w.head * P.nseg + w.seg) * kD * kD);
-        else if (w.seg == P.nseg - 1)
-          store_state(P.S + hd);
-        if (kLocal) signal_ready(rdy_s);
-      } else if (kLocal) {
-        signal_ready(rdy_s);  // the KV columns are read
-      } else {
-        state_operand(it + 1);
+      if (kLocal) signal_ready<false>(rdy_s);  // the KV columns are read
+      if (w.last() && (kLocal || w.seg == P.nseg - 1)) {
+        float *dst = kLocal ? P.ws_state + ((size_t)w.head * P.nseg + w.seg) * kD * kD
+                            : P.S + (size_t)w.head * kD * kD;
+#pragma unroll
+        for (int j = 0; j < kC; ++j) dst[(size_t)(kC * half + j) * kD + myrow] = s[j];
       }
-      w.next();
+    }
+    cta_end();
+    if (*fail) {
+      // a wait ran out: everything this CTA was to write becomes NaN, so the
+      // failure shows in the results as well as in the counter
+      if (tid == 0) atomicAdd(&g_linattn_timeouts, 1u);
+      const float nan = __int_as_float(0x7fffffff);
+      Walk<kLocal> f(P);
+#pragma unroll 1
+      for (f.u = blockIdx.x; f.u < P.units; f.u += gridDim.x) {
+        f.decode();
+        float *dst = kLocal ? P.ws_state + ((size_t)f.head * P.nseg + f.seg) * kD * kD
+                            : P.S + (size_t)f.head * kD * kD;
+#pragma unroll 1
+        for (int e = tid; e < kD * kD; e += kGroup) dst[e] = nan;
+        const int t_end = kLocal ? 0 : min(f.n, f.c_hi * kC);
+#pragma unroll 1
+        for (int t = f.c * kC; t < t_end; ++t) {
+          const size_t row = (((size_t)f.b * P.T + t) * P.vh + f.vi) * kRow;
+          if (tid < (int)kRow / 4)
+            *reinterpret_cast<uint32_t *>(static_cast<unsigned char *>(P.o) + row + 4 * tid) =
+                0x7fffffffu;
+        }
+      }
     }
   } else if (warp < 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     // ======================================= group B: q, k rows, P, output
     const int bt = tid - kGroup;
-    // [K; Q] operand of a chunk, in place: rows (bt >> 4) + 16 i, columns
-    // 8 (bt & 15) .. + 7; rows 0-63 K, 64-127 Q
+    // [K; Q] operand of a chunk, in place: this warp's two groups of 8 rows
+    // (K rows only in the state pass: one group).  Lane l has rows
+    // 2 i + (l >> 4) and of each, with m = l & 15, columns 4 m .. + 3 and
+    // 64 + 4 m .. + 3 (fp32) or 8 m .. + 7 (bf16), so that every access of
+    // a quarter warp covers whole banks.
     auto convert = [&](const Walk<kLocal> &w) {
-      const uint32_t reg = OFF_KQ + (w.it & 1) * kKQ;
+      const int m16 = lane & 15, r1 = lane >> 4, nv = w.valid();
       wait_bar(staged + 8 * (w.it & 1), (w.it >> 1) & 1, fail);
-      constexpr int kRows = kLocal ? 4 : 8;
-      const int swap = (bt >> 2) & 1, c0 = (bt & 15) * 8, nv = w.valid();
-      float x[kRows][8];
-      float sc[kRows];
+      int *ex = rowexp(w.it);
+#pragma unroll 1
+      for (int grp = warp - 8; grp < (kLocal ? 8 : 16); grp += 8) {
+        unsigned char *g8 = gb + OFF_KQ + (w.it & 1) * kKQ + grp * kGrp;
+        float x[4][8], sc[4];
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const int row = (bt >> 4) + 16 * i;
-        if (kBf16) {
-          const uint4 u = *reinterpret_cast<const uint4 *>(gb + reg + row * 256 + c0 * 2);
-          const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+        for (int i = 0; i < 4; ++i) {
+          const unsigned char *st = g8 + (2 * i + r1) * kRow + m16 * 16;
+          const uint4 u = *reinterpret_cast<const uint4 *>(st);
+          if (kBf16) {
+            const uint32_t q[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            x[i][2 * j] = __uint_as_float(q[j] << 16);
-            x[i][2 * j + 1] = __uint_as_float(q[j] & 0xffff0000u);
+            for (int j = 0; j < 4; ++j) {
+              x[i][2 * j] = __uint_as_float(q[j] << 16);
+              x[i][2 * j + 1] = __uint_as_float(q[j] & 0xffff0000u);
+            }
+          } else {
+            const uint4 v = *reinterpret_cast<const uint4 *>(st + 256);
+            const uint32_t q[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[i][j] = __uint_as_float(q[j]);
           }
-        } else {
-          const float *st = reinterpret_cast<const float *>(gb + reg) + row * 128 + c0;
-          const float4 ya = *reinterpret_cast<const float4 *>(st + 4 * swap);
-          const float4 yb = *reinterpret_cast<const float4 *>(st + 4 - 4 * swap);
-          const float4 x0 = swap ? yb : ya, x1 = swap ? ya : yb;
-          x[i][0] = x0.x; x[i][1] = x0.y; x[i][2] = x0.z; x[i][3] = x0.w;
-          x[i][4] = x1.x; x[i][5] = x1.y; x[i][6] = x1.z; x[i][7] = x1.w;
         }
-        if ((row & 63) >= nv)
+        if (8 * (grp & 7) + 8 > nv) {  // rows behind the end are zeros
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
-        float m = 0.f;
+          for (int i = 0; i < 4; ++i)
+            if (8 * (grp & 7) + 2 * i + r1 >= nv)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = amax(m, x[i][j]);
+              for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
+        }
 #pragma unroll
-        for (int d = 8; d; d >>= 1) m = amax(m, __shfl_xor_sync(0xffffffffu, m, d));
-        const int e = scale_exp(m);
-        sc[i] = pow2(e);
-        if ((bt & 15) == 0) rowexp(w.it)[row] = e;
+        for (int i = 0; i < 4; ++i) {
+          float m = amax(x[i][0], x[i][1], x[i][2]);
+          m = amax(m, x[i][3], x[i][4]);
+          m = amax(m, x[i][5], x[i][6]);
+          sc[i] = amax(m, x[i][7]);
+        }
+#pragma unroll
+        for (int d = 8; d; d >>= 1)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            sc[i] = amax(sc[i], __shfl_xor_sync(0xffffffffu, sc[i], d));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = scale_exp(sc[i]);
+          if (m16 == 0) ex[8 * grp + 2 * i + r1] = e;
+          sc[i] = pow2(e);
+        }
+        __syncwarp();  // every row of the group is read
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 2 * i + r1;
+          if (kBf16) {
+            put8<kLo>(g8 + (m16 >> 3) * 1024 + r * 128 + (((m16 & 7) ^ r) << 4), 2048, x[i], sc[i]);
+          } else {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              split2<true>(x[i][2 * j] * sc[i], x[i][2 * j + 1] * sc[i], hi[j], lo[j]);
+            unsigned char *p = g8 + r * 128 + (((m16 >> 1) ^ r) << 4) + (m16 & 1) * 8;
+            *reinterpret_cast<uint2 *>(p) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2 *>(p + 1024) = make_uint2(hi[2], hi[3]);
+            *reinterpret_cast<uint2 *>(p + 2048) = make_uint2(lo[0], lo[1]);
+            *reinterpret_cast<uint2 *>(p + 3072) = make_uint2(lo[2], lo[3]);
+          }
+        }
       }
-      if (!kLocal && bt == 0)  // the o tile's last store has read it
-        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-      bar_b();
-#pragma unroll
-      for (int i = 0; i < kRows; ++i)
-        put8<kLo>(gb, reg, 128, 128, (bt >> 4) + 16 * i, c0, x[i], sc[i]);
-      signal_ready(rdy_kq + 8 * (w.it & 1));
+      signal_ready<true>(rdy_kq + 8 * (w.it & 1));
     };
-    Walk<kLocal> w(P);
-    if (w.ok) convert(w);
-    while (w.ok) {
-      Walk<kLocal> nx = w;
+    Walk<kLocal> w(P), nx(P);  // the chunk at hand (none at first), the next
+    for (;;) {
+      w = nx;
       nx.next();
-      if (kLocal) {
-        if (nx.ok) convert(nx);
-        w = nx;
-        continue;
-      }
       const int it = w.it;
       const float *vc = vec(it);
+      if (!kLocal && w.ok) {
       // ---- P[t][s] = G e^{Gamma_t - Gamma_s}, s <= t (lanes 64-127: q rows)
       wait_bar(vecs + 8 * (it & 3), (it >> 2) & 1, fail);
       wait_bar(done_qk, it & 1, fail);
       fence_after_sync();
       if (quad >= 2) {
-        const int t = myrow - kC, s0 = 32 * half;
-        if (s0 <= 32 * (quad - 2)) {
-          uint32_t r[32];
-          tmem_ld32_async(tl + T_G + s0, r);
-          tmem_wait_ld(r);
-          const float at = vc[VA + t];
-          float x[32];
-          if (vc[VM + 1] != 0.f) {
+        const int t = myrow - kC;
+        const float at = vc[VA + t], gh = vc[VGH + t], gl = vc[VGL + t];
+        const bool fac = vc[VM + 1] != 0.f;
+        unsigned char *pr = gb + OFF_P + t * 128;
+#pragma unroll 1
+        for (int s0 = 32 * half; s0 < 32 * half + 32; s0 += 16) {
+          float x[16];
+          if (s0 < 32 * (quad - 1)) {  // some s <= t in this warp
+            tmem_ld16(tl + T_G + s0, x);
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              x[j] = s0 + j <= t ? __uint_as_float(r[j]) * (at * vc[VB + s0 + j]) : 0.f;
+            for (int j = 0; j < 16; ++j) x[j] *= at * vc[VB + s0 + j];
+            if (!fac)
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                x[j] *= exp2f((gh - vc[VGH + s0 + j]) + (gl - vc[VGL + s0 + j]));
+            if (s0 + 15 > 32 * (quad - 2))
+#pragma unroll
+              for (int j = 0; j < 16; ++j) x[j] = s0 + j <= t ? x[j] : 0.f;
           } else {
-            const float gh = vc[VGH + t], gl = vc[VGL + t];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float d = (gh - vc[VGH + s0 + j]) + (gl - vc[VGL + s0 + j]);
-              x[j] = s0 + j <= t
-                         ? __uint_as_float(r[j]) * (at * vc[VB + s0 + j]) * exp2f(d)
-                         : 0.f;
-            }
+            for (int j = 0; j < 16; ++j) x[j] = 0.f;
           }
 #pragma unroll
-          for (int c0 = 0; c0 < 32; c0 += 8)
-            put8<kLo>(gb, OFF_P, kC, kC, t, s0 + c0, x + c0, 1.f);
-        } else {
-          const float z[8] = {};
-#pragma unroll
-          for (int c0 = 0; c0 < 32; c0 += 8) put8<kLo>(gb, OFF_P, kC, kC, t, s0 + c0, z, 1.f);
+          for (int c0 = 0; c0 < 16; c0 += 8)
+            put8<kLo>(pr + ((((s0 + c0) >> 3) ^ (t & 7)) << 4), 8192, x + c0, 1.f);
         }
       }
-      signal_ready(rdy_p);
-      // ---- the next chunk's rows, under this one's products
-      if (nx.ok) {
-        convert(nx);
-      } else {
-        if (bt == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        bar_b();
+      signal_ready<true>(rdy_p);
       }
+      // ---- the next chunk's rows, under this one's products
+      if (nx.ok) convert(nx);
+      if (kLocal || !w.ok) {
+        if (!nx.ok) break;
+        continue;
+      }
+      // the o tile's last store has read it
+      if (bt == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      bar_b();
       // ---- o^T = cA QS + cB PV, lane dv, columns t = 32 half .. + 31
       wait_bar(done_o, it & 1, fail);
       fence_after_sync();
       {
-        uint32_t qs[32], pvr[32];
-        tmem_ld32_async(tl + T_QS + 32 * half, qs);
-        tmem_ld32_async(tl + T_G + 32 * half, pvr);
         const float fs = lanef(it)[myrow], fv = lanef(it)[128 + myrow];
-        tmem_wait_ld(qs);
-        tmem_wait_ld(pvr);
-        fence_before_sync();
-        mbar_arrive(acc_free);
-        unsigned char *ot = gb + OFF_O + 32 * half * kRow;
         const int bad = min((int)badtok(it)[myrow], (int)badtok(it)[128 + myrow]);
-        const bool finite = bad >= kC;
+        uint32_t qs[32], pv[32];
+        tmem_ld32_async(tl + T_QS + 32 * half, qs);
+        tmem_ld32_async(tl + T_G + 32 * half, pv);
+        tmem_wait_ld(qs);
+        tmem_wait_ld(pv);
+        signal_ready<false>(acc_free);
+        const float *ca = vc + VCA + 32 * half, *cb = vc + VCB + 32 * half;
+        unsigned char *ot = gb + OFF_O + 32 * half * kRow + myrow * (kRow / kD);
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          const int t = 32 * half + j;
-          float y = fmaf(__uint_as_float(qs[j]) * fs, vc[VCA + t],
-                         __uint_as_float(pvr[j]) * fv * vc[VCB + t]);
-          if (!finite && t >= bad) y = __int_as_float(0x7fffffff);
+          const float y = fmaf(__uint_as_float(qs[j]) * fs, ca[j],
+                               __uint_as_float(pv[j]) * fv * cb[j]);
           if (kBf16)
-            *reinterpret_cast<__nv_bfloat16 *>(ot + j * 256 + 2 * myrow) = __float2bfloat16_rn(y);
+            *reinterpret_cast<__nv_bfloat16 *>(ot + j * kRow) = __float2bfloat16_rn(y);
           else
-            *reinterpret_cast<float *>(ot + j * 512 + 4 * myrow) = y;
+            *reinterpret_cast<float *>(ot + j * kRow) = y;
+        }
+        // (the same thread's stores, so in order)
+#pragma unroll 1
+        for (int j = max(bad - 32 * half, 0); j < 32; ++j) {
+          if (kBf16)
+            *reinterpret_cast<unsigned short *>(ot + j * kRow) = 0x7fff;
+          else
+            *reinterpret_cast<uint32_t *>(ot + j * kRow) = 0x7fffffffu;
         }
       }
       fence_proxy_async();
@@ -654,41 +807,50 @@ __global__ void __launch_bounds__(kThreads, 1)
               *reinterpret_cast<const uint4 *>(gb + OFF_O + r * kRow + x * 16);
         }
       }
-      w = nx;
+      if (!nx.ok) break;
     }
     if (!kLocal && bt == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-  } else if (warp == kIssuer) {
-    // =================================================== the issuing thread
-    if (lane == 0) {
-      for (Walk<kLocal> w(P); w.ok; w.next()) {
+    cta_end();
+  } else {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  if (warp == kIssuer) {
+    // ===================================================== the issuing warp
+    {
+      const uint32_t one = elect();
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      constexpr uint32_t idn = idesc16(128, kC, 0), idk = idesc16(128, kD, 1);
+      const uint32_t hi = desc_hi(kGrp), hi_p = desc_hi(1024);
+      const uint32_t lo_p = desc_lo(sb + OFF_P, 16);
+      for (Walk<kLocal> w(P); w.next();) {
         const int it = w.it;
-        const uint32_t kq = sb + OFF_KQ + (it & 1) * kKQ, ql = 32768u;
+        const uint32_t kq = sb + OFF_KQ + (it & 1) * kKQ;
         wait_bar(rdy_kq + 8 * (it & 1), (it >> 1) & 1, fail);
         if (!kLocal) {
           if (it > 0) wait_bar(acc_free, (it - 1) & 1, fail);
           fence_after_sync();
-          constexpr uint32_t id = idesc16(128, kC, 0);
+          const uint32_t lo_k = desc_lo(kq, 16), lo_q = lo_k + (8 * kGrp >> 4);
 #pragma unroll
           for (int ks = 0; ks < kD / 16; ++ks) {
-            const uint64_t h = kdesc(kq, 128, ks), l = kdesc(kq + ql, 128, ks);
-            mma_bf16(tmem + T_G, h, h, id, ks > 0);
+            const uint64_t h = desc64(hi, lo_k + (kstep(ks) >> 4));
+            const uint64_t l = desc64(hi, lo_k + ((kstep(ks) + 2048) >> 4));
+            mma_ss(one, tm + T_G, h, h, idn, ks > 0);
             if (kLo) {
-              mma_bf16(tmem + T_G, h, l, id, 1u);
-              mma_bf16(tmem + T_G, l, h, id, 1u);
+              mma_ss(one, tm + T_G, h, l, idn, 1u);
+              mma_ss(one, tm + T_G, l, h, idn, 1u);
             }
           }
-          commit(done_qk);
+          commit_one(one, done_qk);
           wait_bar(rdy_s, it & 1, fail);
           fence_after_sync();
 #pragma unroll
           for (int ks = 0; ks < kD / 16; ++ks) {
-            // Q: rows 64-127 of the operand
-            const uint64_t h = kdesc(kq + 8192u, 128, ks), l = kdesc(kq + ql + 8192u, 128, ks);
-            const uint32_t a = tmem + T_SOP + 8u * ks;
-            mma_bf16_ta(tmem + T_QS, a, h, id, ks > 0);
+            const uint64_t h = desc64(hi, lo_q + (kstep(ks) >> 4));
+            const uint64_t l = desc64(hi, lo_q + ((kstep(ks) + 2048) >> 4));
+            const uint32_t a = tm + T_SOP + 8u * ks;
+            mma_ts(one, tm + T_QS, a, h, idn, ks > 0);
             if (kLo) {
-              mma_bf16_ta(tmem + T_QS, a, l, id, 1u);
-              mma_bf16_ta(tmem + T_QS, a + 64u, h, id, 1u);
+              mma_ts(one, tm + T_QS, a, l, idn, 1u);
+              mma_ts(one, tm + T_QS, a + 64u, h, idn, 1u);
             }
           }
         } else {
@@ -698,180 +860,190 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_bar(rdy_v, it & 1, fail);
         fence_after_sync();
         {
-          constexpr uint32_t id = idesc16(128, kD, 1);
+          const uint32_t lo_k = desc_lo(kq, 1024);  // rows are K: two groups a step
 #pragma unroll
           for (int ks = 0; ks < kC / 16; ++ks) {
-            const uint64_t h = mndesc(kq, 128, ks), l = mndesc(kq + ql, 128, ks);
-            const uint32_t a = tmem + T_WOP + 8u * ks;
-            mma_bf16_ta(tmem + T_D, a, h, id, ks > 0);
-            mma_bf16_ta(tmem + T_D, a + 32u, h, id, 1u);
-            if (kLo) mma_bf16_ta(tmem + T_D, a, l, id, 1u);
+            const uint64_t h = desc64(hi, lo_k + (ks * 2 * kGrp >> 4));
+            const uint64_t l = desc64(hi, lo_k + ((ks * 2 * kGrp + 2048) >> 4));
+            const uint32_t a = tm + T_WOP + 8u * ks;
+            mma_ts(one, tm + T_D, a, h, idk, ks > 0);
+            mma_ts(one, tm + T_D, a + 32u, h, idk, 1u);
+            if (kLo) mma_ts(one, tm + T_D, a, l, idk, 1u);
           }
         }
-        commit(done_kv);
-        commit(kq_free + 8 * (it & 1));
+        commit_one(one, done_kv);
+        commit_one(one, kq_free + 8 * (it & 1));
         if (!kLocal) {
           wait_bar(rdy_p, it & 1, fail);
           fence_after_sync();
-          constexpr uint32_t id = idesc16(128, kC, 0);
-          const uint32_t p = sb + OFF_P;
 #pragma unroll
           for (int ks = 0; ks < kC / 16; ++ks) {
-            const uint64_t h = kdesc(p, kC, ks), l = kdesc(p + 8192u, kC, ks);
-            const uint32_t a = tmem + T_VOP + 8u * ks;
-            mma_bf16_ta(tmem + T_G, a, h, id, ks > 0);
+            const uint64_t h = desc64(hi_p, lo_p + (kstep(ks) >> 4));
+            const uint64_t l = desc64(hi_p, lo_p + ((kstep(ks) + 8192) >> 4));
+            const uint32_t a = tm + T_VOP + 8u * ks;
+            mma_ts(one, tm + T_G, a, h, idn, ks > 0);
             if (kLo) {
-              mma_bf16_ta(tmem + T_G, a, l, id, 1u);
-              mma_bf16_ta(tmem + T_G, a + 32u, h, id, 1u);
+              mma_ts(one, tm + T_G, a, l, idn, 1u);
+              mma_ts(one, tm + T_G, a + 32u, h, idn, 1u);
             }
           }
-          commit(done_o);
+          commit_one(one, done_o);
         }
       }
-      commit(drain);  // arrives once every product issued above is done
+      commit_one(one, drain);  // arrives once every product issued above is done
+      mbar_wait(drain, 0, kWaitLimit);
     }
     __syncwarp();
+    cta_end();
+    tmem_dealloc(tmem, 512);
   } else if (warp == kLoader) {
     // ===================================================== the copying warp
-    if (lane == 0) {
-      int it = 0;
-      for (Walk<kLocal> w(P); w.ok; w.next()) {
-        it = w.it;
-        const uint32_t reg = sb + OFF_KQ + (it & 1) * kKQ, st = staged + 8 * (it & 1);
-        if (it >= 2) wait_bar(kq_free + 8 * (it & 1), ((it - 2) >> 1) & 1, fail);
+    int it = -1;
+    for (Walk<kLocal> w(P); w.next();) {
+      it = w.it;
+      const uint32_t reg = sb + OFF_KQ + (it & 1) * kKQ, st = staged + 8 * (it & 1);
+      if (it >= 2) wait_bar(kq_free + 8 * (it & 1), ((it - 2) >> 1) & 1, fail);
+      if (lane == 0) {
         mbar_expect(st, (kLocal ? 1u : 2u) * kC * kRow);
         tma_load(reg, &tm_k, w.vi / P.rep, w.c * kC, w.b, st);
         if (!kLocal) tma_load(reg + kC * kRow, &tm_q, w.vi / P.rep, w.c * kC, w.b, st);
-        if (it >= 1) wait_bar(v_free, (it - 1) & 1, fail);
+      }
+      __syncwarp();
+      if (it >= 1) wait_bar(v_free, (it - 1) & 1, fail);
+      if (lane == 0) {
         mbar_expect(vstaged, kC * kRow);
         tma_load(sb + OFF_V, &tm_v, w.vi, w.c * kC, w.b, vstaged);
-        ++it;
       }
-      // nothing may still be copying into shared memory when the CTA ends
-      // (the last chunk of either parity, and the last V rows)
-      for (int j = it - 2; j < it; ++j)
-        if (j >= 0) mbar_wait(staged + 8 * (j & 1), (j >> 1) & 1, kWaitLimit);
-      if (it > 0) mbar_wait(vstaged, (it - 1) & 1, kWaitLimit);
+      __syncwarp();
     }
+    // nothing may still be copying into shared memory when the CTA ends
+    // (the last chunk of either parity, and the last V rows)
+    for (int j = max(it - 1, 0); j <= it; ++j)
+      mbar_wait(staged + 8 * (j & 1), (j >> 1) & 1, kWaitLimit);
+    if (it >= 0) mbar_wait(vstaged, it & 1, kWaitLimit);
     __syncwarp();
+    cta_end();
   } else if (warp == kGates) {
     // ====================================================== decay vectors
-    // Lane l has tokens l and l + 32.  exp2 of a double difference: its float
-    // part, times 1 + ln 2 of the rest.
-    auto ex2 = [](double x) {
-      const float h = (float)x;
-      const float l = (float)(x - (double)h);
-      const float e = exp2f(h);
-      return fmaf(e, l * 0.69314718f, e);
-    };
+    // Lane l has tokens 2 l and 2 l + 1; log decays to base 2.
     double total = 0.0;
-    for (Walk<kLocal> w(P); w.ok; w.next()) {
+    for (Walk<kLocal> w(P); w.next();) {
       const int it = w.it, nv = w.valid();
       if (w.first) total = 0.0;
       const size_t base = P.g_head ? (size_t)w.vi
                                    : ((size_t)w.b * P.T + (size_t)w.c * kC) * P.vh + w.vi;
       const size_t step = P.g_head ? 0 : (size_t)P.vh;
-      float ga = lane < nv ? __ldg(P.g + base + lane * step) : 0.f;
-      float gc = lane + 32 < nv ? __ldg(P.g + base + (lane + 32) * step) : 0.f;
-      // -inf as a decay that no float survives; NaN stays
-      if (ga < -1e4f) ga = -1e4f;
-      if (gc < -1e4f) gc = -1e4f;
-      double da = (double)ga * 1.4426950408889634, dc = (double)gc * 1.4426950408889634;
+      Two G[2];  // cumulative
+      bool up = false;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int t = 2 * lane + i;
+        float x = t < nv ? __ldg(P.g + base + t * step) : 0.f;
+        if (x < -1e4f) x = -1e4f;  // -inf: a decay that no float survives; NaN stays
+        up |= x > 0.f;
+        const float h = x * 1.44269502f;  // log2 e = 1.44269502 + 1.925963e-8
+        G[i] = Two{h, fmaf(x, 1.44269502f, -h) + x * 1.925963033e-8f};
+      }
+      G[1] = add2(G[0], G[1]);
+      Two run = G[1];
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
-        const double ya = __shfl_up_sync(0xffffffffu, da, off);
-        const double yc = __shfl_up_sync(0xffffffffu, dc, off);
-        if (lane >= off) {
-          da += ya;
-          dc += yc;
-        }
+        const Two y = shfl_up2(run, off);
+        if (lane >= off) run = add2(run, y);
       }
-      dc += __shfl_sync(0xffffffffu, da, 31);
-      const double end = __shfl_sync(0xffffffffu, dc, 31);
-      total += end;
+      const Two end{__shfl_sync(0xffffffffu, run.h, 31), __shfl_sync(0xffffffffu, run.l, 31)};
+      const Two before = shfl_up2(run, 1);
+      if (lane > 0) {
+        G[0] = add2(G[0], before);
+        G[1] = add2(G[1], before);
+      }
+      total += (double)end.h + (double)end.l;
       float *vc = vec(it);
-      const float wa = ex2(end - da), wc = ex2(end - dc);
-      if (kLocal) {
-        wait_bar(rdy_kq + 8 * (it & 1), (it >> 1) & 1, fail);
-        const int *ex = rowexp(it);
-        vc[VF + lane] = wa * pow2(-ex[lane]);
-        vc[VF + lane + 32] = wc * pow2(-ex[lane + 32]);
-        if (lane == 0) vc[VM] = ex2(end);
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(vecs + 8 * (it & 3));
-          if (w.last()) P.ws_decay[(size_t)w.head * P.nseg + w.seg] = total;
-        }
-        continue;
-      }
-      // growth: the largest Gamma_t - Gamma_s, s <= t (0 for decays)
-      const float fa = (float)da, fc = (float)dc;
-      float na = fa, nc = fc;
+      // the decay from each token to the chunk's end
+      float wt[2], at[2], bs[2], gm[2];
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const float ya = __shfl_up_sync(0xffffffffu, na, off);
-        const float yc = __shfl_up_sync(0xffffffffu, nc, off);
-        if (lane >= off) {
-          na = fminf(na, ya);
-          nc = fminf(nc, yc);
+      for (int i = 0; i < 2; ++i) wt[i] = ex2(add2(end, neg2(G[i])));
+      int ew = 22;
+      bool fac = true;
+      if (!kLocal) {
+        if (__any_sync(0xffffffffu, up)) {
+          // growth: the largest Gamma_t - Gamma_s, s <= t (0 for decays)
+          float lo = fminf(G[0].h, G[1].h), run_lo = lo;
+#pragma unroll
+          for (int off = 1; off < 32; off <<= 1) {
+            const float y = __shfl_up_sync(0xffffffffu, run_lo, off);
+            if (lane >= off) run_lo = fminf(run_lo, y);
+          }
+          float grow = fmaxf(fmaxf(G[0].h, G[1].h) - run_lo, 0.f);
+#pragma unroll
+          for (int off = 16; off; off >>= 1)
+            grow = fmaxf(grow, __shfl_xor_sync(0xffffffffu, grow, off));
+          ew += (int)ceilf(fminf(grow, 80.f));
+        }
+        float top = fmaxf(G[0].h, G[1].h), low = fminf(G[0].h, G[1].h);
+#pragma unroll
+        for (int off = 16; off; off >>= 1) {
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+          low = fminf(low, __shfl_xor_sync(0xffffffffu, low, off));
+        }
+        // one factor per row and column while their product cannot leave the
+        // normal floats; otherwise an exponential per element
+        fac = top - low <= 115.f;
+        const Two mid{-0.5f * (top + low), 0.f};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const Two d = add2(G[i], mid);
+          at[i] = fac ? ex2(d) : 1.f;
+          bs[i] = fac ? ex2(neg2(d)) : 1.f;
+          gm[i] = P.scale * ex2(G[i]);
         }
       }
-      nc = fminf(nc, __shfl_sync(0xffffffffu, na, 31));
-      float grow = fmaxf(fa - na, fc - nc), top = fmaxf(fa, fc), low = fminf(fa, fc);
-#pragma unroll
-      for (int off = 16; off; off >>= 1) {
-        grow = fmaxf(grow, __shfl_xor_sync(0xffffffffu, grow, off));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        low = fminf(low, __shfl_xor_sync(0xffffffffu, low, off));
-      }
-      const int ew = 22 + (int)ceilf(fminf(grow, 80.f));
-      // one factor per row and column while their product cannot leave the
-      // normal floats; otherwise an exponential per element
-      const bool fac = top - low <= 115.f;
-      const double mid = 0.5 * ((double)top + (double)low);
-      const float ra = fac ? ex2(da - mid) : 1.f, rc = fac ? ex2(dc - mid) : 1.f;
-      const float ca = fac ? ex2(mid - da) : 1.f, cc = fac ? ex2(mid - dc) : 1.f;
-      const float Ga = ex2(da), Gc = ex2(dc);
+      const float gend = ex2(end);
       wait_bar(rdy_kq + 8 * (it & 1), (it >> 1) & 1, fail);
       const int *ex = rowexp(it);
-      const int ka = ex[lane], kc = ex[lane + 32], qa = ex[64 + lane], qc = ex[96 + lane];
-      int pa = ka, pc = kc;  // the smallest exponent (largest k row) up to t
+      const int2 k2 = *reinterpret_cast<const int2 *>(ex + 2 * lane);
+      const int kx[2] = {k2.x, k2.y};
+      if (!kLocal) {
+        const int2 q2 = *reinterpret_cast<const int2 *>(ex + 64 + 2 * lane);
+        const int qx[2] = {q2.x, q2.y};
+        // the smallest exponent (the largest k row) up to t
+        int run_k = min(k2.x, k2.y);
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int ya = __shfl_up_sync(0xffffffffu, pa, off);
-        const int yc = __shfl_up_sync(0xffffffffu, pc, off);
-        if (lane >= off) {
-          pa = min(pa, ya);
-          pc = min(pc, yc);
+        for (int off = 1; off < 32; off <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, run_k, off);
+          if (lane >= off) run_k = min(run_k, y);
+        }
+        const int before_k = __shfl_up_sync(0xffffffffu, run_k, 1);
+        const int pk[2] = {lane > 0 ? min(before_k, k2.x) : k2.x, run_k};
+        // where the two factors split: the smallest exponent of a finite row
+        int ref = min(k2.x > -114 ? k2.x : 126, k2.y > -114 ? k2.y : 126);
+#pragma unroll
+        for (int off = 16; off; off >>= 1)
+          ref = min(ref, __shfl_xor_sync(0xffffffffu, ref, off));
+        // (exactly; 0 below the normal floats)
+        auto p2 = [](int e) { return e < -126 ? 0.f : pow2(min(e, 127)); };
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int t = 2 * lane + i;
+          vc[VA + t] = at[i] * p2(pk[i] - ref - ew);
+          vc[VB + t] = bs[i] * p2(ref - kx[i]);
+          vc[VCA + t] = gm[i] * p2(-qx[i]);
+          vc[VCB + t] = P.scale * p2(ew - qx[i] - pk[i]);
+          vc[VGH + t] = G[i].h;
+          vc[VGL + t] = G[i].l;
         }
       }
-      pc = min(pc, __shfl_sync(0xffffffffu, pa, 31));
-      // where the two factors split: the smallest exponent of a finite row
-      int ref = min(ka > -114 ? ka : 126, kc > -114 ? kc : 126);
 #pragma unroll
-      for (int off = 16; off; off >>= 1) ref = min(ref, __shfl_xor_sync(0xffffffffu, ref, off));
-      // (exactly; 0 below the normal floats)
-      auto p2 = [](int e) { return e < -126 ? 0.f : pow2(min(e, 127)); };
-      vc[VA + lane] = ra * p2(pa - ref - ew);
-      vc[VA + lane + 32] = rc * p2(pc - ref - ew);
-      vc[VB + lane] = ca * p2(ref - ka);
-      vc[VB + lane + 32] = cc * p2(ref - kc);
-      vc[VF + lane] = wa * p2(-ka);
-      vc[VF + lane + 32] = wc * p2(-kc);
-      vc[VCA + lane] = P.scale * Ga * p2(-qa);
-      vc[VCA + lane + 32] = P.scale * Gc * p2(-qc);
-      vc[VCB + lane] = P.scale * p2(ew - qa - pa);
-      vc[VCB + lane + 32] = P.scale * p2(ew - qc - pc);
-      vc[VGH + lane] = fa;
-      vc[VGH + lane + 32] = fc;
-      vc[VGL + lane] = (float)(da - (double)fa);
-      vc[VGL + lane + 32] = (float)(dc - (double)fc);
+      for (int i = 0; i < 2; ++i) vc[VF + 2 * lane + i] = wt[i] * pow2(-kx[i]);
       if (lane == 0) {
-        vc[VM] = ex2(end);
+        vc[VM] = gend;
         vc[VM + 1] = fac ? 1.f : 0.f;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(vecs + 8 * (it & 3));
+      if (lane == 0) {
+        mbar_arrive(vecs + 8 * (it & 3));
+        if (kLocal && w.last()) P.ws_decay[(size_t)w.head * P.nseg + w.seg] = total;
+      }
     }
     if (kLocal) {  // segments without a chunk: no decay
       Walk<kLocal> w(P);
@@ -881,36 +1053,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (w.c >= w.c_hi && lane == 0) P.ws_decay[(size_t)w.head * P.nseg + w.seg] = 0.0;
       }
     }
+    cta_end();
+  } else {
+    cta_end();
   }
-
-  if (warp == kIssuer) {
-    if (lane == 0) mbar_wait(drain, 0, kWaitLimit);
-    __syncwarp();
-  }
-  fence_before_sync();
-  __syncthreads();
-  fence_after_sync();
-  if (warp == kIssuer) tmem_dealloc(tmem, 512);
-  if (*fail) {
-    // a wait ran out: everything this CTA was to write becomes NaN, so the
-    // failure shows in the results as well as in the counter
-    if (tid == 0) atomicAdd(&g_linattn_timeouts, 1u);
-    const float nan = __int_as_float(0x7fffffff);
-    Walk<kLocal> w(P);
-    for (int u = blockIdx.x; u < P.units; u += gridDim.x) {
-      w.u = u;
-      w.decode();
-      const size_t at = ((size_t)w.head * P.nseg + w.seg) * kD * kD;
-      float *dst = kLocal ? P.ws_state + at : P.S + (size_t)w.head * kD * kD;
-      for (int e = tid; e < kD * kD; e += kThreads) dst[e] = nan;
-      const int t_end = kLocal ? 0 : min(w.n, w.c_hi * kC);
-      for (int t = w.c * kC; t < t_end; ++t) {
-        const size_t row = (((size_t)w.b * P.T + t) * P.vh + w.vi) * kRow;
-        if (tid < (int)kRow / 4)
-          *reinterpret_cast<uint32_t *>(static_cast<unsigned char *>(P.o) + row + 4 * tid) =
-              0x7fffffffu;
-      }
-    }
   }
 }
 
@@ -1034,7 +1180,7 @@ cudaError_t launch_linattn_prefill(const LinattnArgs &L, bool bf16, void *worksp
   a.rep = L.rep;
   a.T = L.M;
   a.nseg = nseg;
-  a.nchunks = (L.M + kC - 1) / kC;
+  a.per_seg = ((L.M + kC - 1) / kC + nseg - 1) / nseg;
   CUtensorMap m[4];
   cudaError_t e;
   if ((e = rows_map(&m[0], L.q, bf16, L.kh, L.M, L.B)) != cudaSuccess) return e;
