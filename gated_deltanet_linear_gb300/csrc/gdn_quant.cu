@@ -1,65 +1,671 @@
 // Projections with 4-bit weights: y[r][n] = sum_k x[r][k] w[n][k],
-// w[n][k] = code[n][k] * scale[n][k / group].
+// w[n][k] = code[n][k] * scale[n][k / group], for few rows of x.
 //
-// One warp per weight row: lanes read the packed codes 8 at a time and
-// carry up to 8 rows of x.
+// Bound by reading the weights (half a byte each); the arithmetic runs on
+// mma.sync m16n8k16 so that it stays below that: A is 16 weight rows (codes as
+// 16-bit floats, exact), B the rows of x, and the fp32 products of one group
+// are multiplied by the group's scale and added up in fp32.
+// (A tcgen05 product would put the codes through shared memory or tensor
+// memory first, and its 128-row tiles leave too few of them to split over the
+// SMs; a handful of columns does not pay for that.)
+//
+//   fp32 x   two columns per row: x 2^e = hi + lo in fp16 (22 bits; e by row
+//            and block of 128, so that the largest element is in [2^14, 2^15))
+//   bf16 x   one column per row, as it is; the codes as bf16, left at 136 + c:
+//            a group's product starts at -136 times the sum of its x (fp32)
+//            instead of 0, which costs 5 of the 24 bits of sums that are
+//            rounded to 8 at the end
+//
+// Order of k.  A lane of a fragment row reads 16 bytes, 32 consecutive codes;
+// the four lanes of a row read 128 (a block).  The sum over k may run in any
+// order, so the codes are used as they unpack (elements 0 and 4 of a word are
+// one register, 1 and 5 the next, ...) and x is put into shared memory in that
+// order.  Every m16n8k16 step has to stay inside one group: with groups of 64 or
+// 32 the four lanes exchange words first (xor 2, xor 1), so that step i of a
+// block covers the 32 codes of quarter i.
+//
+// Work split.  One CTA of 16 (many columns: 8) warps per SM; a CTA, or a cluster of up to 8 that
+// cut K between them (few tiles, or much x to convert), takes a range of 32-row
+// tiles.  Inside a CTA the (tile, block) pairs are one list, cut evenly over the
+// warps whatever the sizes; a warp keeps several blocks in flight in registers.
+// At the end of a tile, or of its share, it stores its partial sums in a slot of
+// its own in the CTA that adds up the tile; slots are added in a fixed order, so
+// results are the same bits on every call.
 
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <array>
+#include <map>
+#include <mutex>
+
 #include "gdn_internal.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace gdn {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kRows = 8;
+// Warps of a CTA: 16, or 8 where the sums of 32 columns need the registers.
+__host__ __device__ constexpr int warps_of(int n8) { return n8 > 2 ? 8 : 16; }
+constexpr int kBlock = 128;   // k elements of a block
+constexpr int kTile = 32;     // weight rows of a tile
+constexpr int kSmemMax = 220 * 1024;
+// Costs of make_plan(), relative to a block of 32 weight rows.
+constexpr double kXCost = 0.1, kClusterCost = 12.0;
 
-__device__ __forceinline__ float ld1(const float *p) { return __ldg(p); }
-__device__ __forceinline__ float ld1(const __nv_bfloat16 *p) {
-  return __bfloat162float(*p);
-}
-__device__ __forceinline__ void st1(float *p, float x) { *p = x; }
-__device__ __forceinline__ void st1(__nv_bfloat16 *p, float x) {
-  *p = __float2bfloat16_rn(x);
+struct QuantArgs {
+  const void *x;
+  const uint8_t *qw;
+  const __half *sc;
+  void *y;
+  int rows, N, K;
+  int tiles, blocks;      // 32-row tiles, 128-element blocks of a row
+  int round_tiles;        // tiles of a cluster in one round
+  int round_blocks;       // blocks of a CTA's slice in one round
+  int csize, slots;       // CTAs of a cluster, slots of partial sums
+};
+
+// Blocks of CTA `rank`'s slice of a round: an even share where one round takes
+// all of K, else round_blocks in every round (behind the end of K they are
+// zeros), so that a warp's share of tiles is the same in all rounds.
+__device__ __forceinline__ void slice(const QuantArgs &P, int csize, int rank, int &lo, int &n) {
+  if (P.blocks <= csize * P.round_blocks) {
+    lo = (unsigned)(P.blocks * rank) / (unsigned)csize;
+    n = (unsigned)(P.blocks * (rank + 1)) / (unsigned)csize - lo;
+  } else {
+    lo = rank * P.round_blocks;
+    n = P.round_blocks;
+  }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(128)
-    quant_linear_kernel(const T *__restrict__ x, const uint8_t *__restrict__ qw,
-                        const __half *__restrict__ sc, T *__restrict__ y,
-                        int rows, int N, int K, int group) {
-  const int lane = threadIdx.x & 31;
-  const size_t n = (size_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (n >= (size_t)N) return;
-  const uint32_t *wp = reinterpret_cast<const uint32_t *>(qw + n * (K / 2));
-  const __half *sp = sc + n * (K / group);
-  for (int r0 = 0; r0 < rows; r0 += kRows) {
-    const int nr = min(kRows, rows - r0);
-    float acc[kRows];
+// The most warps that share a tile, of nt tiles and at most `blocks` blocks.
+__host__ __device__ inline int most_warps(int warps, int nt, int blocks) {
+  int m = (warps + nt - 1) / nt + 1;
+  if (m > blocks) m = blocks;
+  return m < warps ? m : warps;
+}
+
+// Warp w's share [share(w), share(w + 1)) of a list of `total` pairs.
+template <int kWarps>
+__device__ __forceinline__ int share(unsigned total, int w) {
+  return (int)((unsigned long long)total * w / kWarps);
+}
+
+// 8 codes of a word as four registers of two 16-bit floats: elements (0, 4),
+// (1, 5), (2, 6), (3, 7).  A code c is stored as c + 16 (c < 0); flipping its
+// bit 3 gives c + 8, which as the low mantissa bits of 1024 (fp16) or 128
+// (bf16) is 1032 + c or 136 + c.
+template <bool kBf16>
+__device__ __forceinline__ void codes(uint32_t u, uint32_t (&r)[4]) {
+  if (kBf16) {
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) acc[r] = 0.f;
-    for (int k = 8 * lane; k < K; k += 256) {
-      const uint32_t u = __ldg(wp + (k >> 3));
-      const float s = __half2float(sp[k / group]);
-      float w[8];
+    for (int i = 0; i < 4; ++i) r[i] = ((u >> (4 * i)) & 0x000f000fu) ^ 0x43084308u;
+  } else {
+    const __half2 m = __floats2half2_rn(-1032.f, -1032.f);
+    const __half2 s = __floats2half2_rn(0.0625f, 0.0625f), m16 = __floats2half2_rn(-72.f, -72.f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = s * (float)((int)(u << (28 - 4 * i)) >> 28);
-#pragma unroll
-      for (int r = 0; r < kRows; ++r)
-        if (r < nr) {
-          const T *xp = x + (size_t)(r0 + r) * K + k;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) acc[r] = fmaf(ld1(xp + i), w[i], acc[r]);
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-#pragma unroll
-      for (int d = 16; d; d >>= 1) acc[r] += __shfl_xor_sync(kFull, acc[r], d);
-      if (r < nr && lane == 0) st1(y + (size_t)(r0 + r) * N + n, acc[r]);
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t v = u >> (8 * i);
+      const uint32_t a = (v & 0x000f000fu) ^ 0x64086408u;   // 1032 + c
+      const uint32_t b = (v & 0x00f000f0u) ^ 0x64806480u;   // 1024 + 16 (8 + c)
+      const __half2 da = __hadd2(*reinterpret_cast<const __half2 *>(&a), m);
+      const __half2 db = __hfma2(*reinterpret_cast<const __half2 *>(&b), s, m16);
+      r[2 * i] = *reinterpret_cast<const uint32_t *>(&da);
+      r[2 * i + 1] = *reinterpret_cast<const uint32_t *>(&db);
     }
   }
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1,
+                                    const float (&c)[4]) {
+  if (kBf16)
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
+          "f"(c[2]), "f"(c[3]));
+  else
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
+          "f"(c[2]), "f"(c[3]));
+}
+
+// Where the 8-element part p (0..15) of a block sits in shared memory: at
+// 4 * step + lane of the order in which the lanes use them.
+template <int kGroup>
+__device__ __forceinline__ int place(int p) {
+  if (kGroup == 128) return 4 * (p & 3) + (p >> 2);
+  if (kGroup == 64) {
+    // group p >> 3; lane t has part 4 (t & 1) + 2 j + (t >> 1) in step j
+    const int q = p & 7, t = (q >> 2) | ((q & 1) << 1), j = (q >> 1) & 1;
+    return 4 * (2 * (p >> 3) + j) + t;
+  }
+  // group p >> 2; lane t has part 2 (t & 1) + (t >> 1)
+  const int q = p & 3, t = (q >> 1) | ((q & 1) << 1);
+  return 4 * (p >> 2) + t;
+}
+
+// After the exchange, word i of every lane belongs to step i (see place()).
+template <int kGroup>
+__device__ __forceinline__ void exchange(uint32_t (&w)[4], int t) {
+  if (kGroup == 128) return;
+  const bool up = t >= 2;
+  // keep w0, w2 (low lanes) or w1, w3 (high lanes), swap the others
+  uint32_t s0 = up ? w[0] : w[1], s1 = up ? w[2] : w[3];
+  const uint32_t k0 = up ? w[1] : w[0], k1 = up ? w[3] : w[2];
+  s0 = __shfl_xor_sync(kFull, s0, 2);
+  s1 = __shfl_xor_sync(kFull, s1, 2);
+  // first 64 elements: own words of the low lanes, received ones of the high
+  uint32_t a0 = up ? s0 : k0, a1 = up ? s1 : k1, b0 = up ? k0 : s0, b1 = up ? k1 : s1;
+  if (kGroup == 32) {
+    const bool odd = t & 1;
+    uint32_t sa = odd ? a0 : a1, sb = odd ? b0 : b1;
+    const uint32_t ka = odd ? a1 : a0, kb = odd ? b1 : b0;
+    sa = __shfl_xor_sync(kFull, sa, 1);
+    sb = __shfl_xor_sync(kFull, sb, 1);
+    a0 = odd ? sa : ka;
+    a1 = odd ? ka : sa;
+    b0 = odd ? sb : kb;
+    b1 = odd ? kb : sb;
+  }
+  w[0] = a0;
+  w[1] = a1;
+  w[2] = b0;
+  w[3] = b1;
+}
+
+// x elements 8 p .. + 7 of a row, as fp32.
+__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
+  const float4 b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+
+template <bool kBf16, int kNT, int kGroup>
+__global__ void __launch_bounds__(32 * warps_of(kNT), 1)
+    quant_linear_kernel(const QuantArgs P) {
+  constexpr int kWarps = warps_of(kNT), kThreads = 32 * kWarps;
+  constexpr int kCols = 8 * kNT;
+  constexpr int kRowsX = kBf16 ? kCols : kCols / 2;  // rows of x of a pass
+  constexpr int kSc = kBlock / kGroup;               // scales of a block
+  constexpr int kDepth = 3;                          // blocks in flight a warp
+  constexpr int kSums = kBf16 ? 4 : 2;               // of a lane and m16n8 tile
+  extern __shared__ __align__(16) unsigned char smem[];
+  const cg::cluster_group cl = cg::this_cluster();
+  const int csize = P.csize, crank = csize > 1 ? (int)cl.block_rank() : 0;
+  const int cluster = (unsigned)blockIdx.x / (unsigned)csize;
+  const int clusters = (unsigned)gridDim.x / (unsigned)csize;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(kFull, tid >> 5, 0);
+  const int gr = lane >> 2, t = lane & 3;
+
+  // shared memory: partial sums, x (a column is round_blocks * 256 + 64 bytes),
+  // then by block: 2^-e of each row (fp32) or -136 sums of each group (bf16),
+  // then by slice and tile: the first warp in it and the number of warps
+  const uint32_t xstride = (uint32_t)P.round_blocks * 256 + 64;
+  float *slots = reinterpret_cast<float *>(smem);
+  unsigned char *xs = smem + (size_t)P.slots * kTile * kRowsX * 4;
+  float *side = reinterpret_cast<float *>(xs + (size_t)kCols * xstride);
+  unsigned char *tab = reinterpret_cast<unsigned char *>(
+      side + P.round_blocks * (kBf16 ? kSc * kCols : kRowsX));
+  const unsigned char *xl = xs + gr * xstride + t * 16;  // of this lane's column
+
+  // behind the kernel before it: nothing is read or written before it has ended
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (csize > 1) cl.sync();  // every CTA's shared memory is there
+
+  const uint32_t wrow = (uint32_t)P.K / 2;
+  const int groups = P.K / kGroup;
+
+  for (int r0 = 0; r0 < P.rows; r0 += kRowsX) {
+    const int nr = min(kRowsX, P.rows - r0);
+    for (int t0 = cluster * P.round_tiles; t0 < P.tiles; t0 += clusters * P.round_tiles) {
+      const int nt = min(P.round_tiles, P.tiles - t0);
+      const int own = (unsigned)(nt + csize - 1) / (unsigned)csize;  // tiles a CTA adds up
+      const int most = most_warps(kWarps, nt, P.round_blocks);
+      for (int kr = 0; kr < P.blocks; kr += csize * P.round_blocks) {
+        int b_lo, nb;
+        slice(P, csize, crank, b_lo, nb);
+        b_lo += kr;
+        const unsigned total = nt * nb;
+        int pos = share<kWarps>(total, warp);
+        const int end = share<kWarps>(total, warp + 1);
+
+        // ---- weights: a ring of blocks in registers, loads ahead of use.
+        // Rows gr + 8 i of a tile; rows behind the last one read it again (and
+        // nothing stores them).  Lanes behind the end of K read nothing.
+        uint4 wv[kDepth][4];
+        __half sv[kDepth][4][kSc];
+        const uint8_t *wp = nullptr;  // of the tile, and the lane's row offsets
+        const __half *sp = nullptr;
+        uint32_t wo[4], so[4];
+        int lpos = pos, lb = 0, lt = 0;  // the next load
+        auto aim = [&]() {
+          const int n0 = (t0 + lt) * kTile;
+          wp = P.qw + (size_t)n0 * wrow;
+          sp = P.sc + (size_t)n0 * groups;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int n = min(gr + 8 * i, P.N - 1 - n0), b = b_lo + lb;
+            wo[i] = n * wrow + b * (kBlock / 2) + 16 * t;
+            so[i] = n * groups + b * kSc;
+          }
+        };
+        if (pos < end) {
+          lt = (unsigned)pos / (unsigned)nb;
+          lb = pos - lt * nb;
+          aim();
+        }
+        auto fetch = [&](int d) {
+          if (lpos < end) {
+            const int b = b_lo + lb;
+            if (b * kBlock + kBlock <= P.K) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                wv[d][i] = __ldg(reinterpret_cast<const uint4 *>(wp + wo[i]));
+#pragma unroll
+                for (int j = 0; j < kSc; ++j) sv[d][i][j] = __ldg(sp + (so[i] + j));
+              }
+            } else {  // the end of K
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                wv[d][i] = make_uint4(0, 0, 0, 0);
+                if (b * kBlock + 32 * t < P.K)
+                  wv[d][i] = __ldg(reinterpret_cast<const uint4 *>(wp + wo[i]));
+#pragma unroll
+                for (int j = 0; j < kSc; ++j)
+                  sv[d][i][j] = b * kSc + j < groups ? __ldg(sp + (so[i] + j)) : __half(0.f);
+              }
+            }
+            ++lpos;
+            if (++lb == nb) {
+              lb = 0;
+              ++lt;
+              aim();
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                wo[i] += kBlock / 2;
+                so[i] += kSc;
+              }
+            }
+          }
+        };
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) fetch(d);
+
+        // ---- x: this slice of the rows in the order of use; half a warp to a
+        // block of a row
+        if (kr || t0 != cluster * P.round_tiles || r0) __syncthreads();  // readers are done
+        {
+          const int p = lane & 15;
+          int b = 2 * warp + (lane >> 4), r = 0;
+          while (b >= nb && r < kRowsX) {
+            b -= nb;
+            ++r;
+          }
+          // (both halves run the same number of turns: shuffles inside)
+          const int turns = (kRowsX * nb + 2 * kWarps - 1) / (2 * kWarps);
+#pragma unroll 2
+          for (int turn = 0; turn < turns; ++turn) {
+            const int k = (b_lo + b) * kBlock + 8 * p;
+            const bool on = r < nr && k < P.K;
+            const size_t at = (size_t)(r0 + r) * P.K + k;
+            unsigned char *dst = xs + b * 256 + place<kGroup>(p) * 16;
+            if (kBf16) {
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (on)
+                v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(P.x) + at));
+              const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+              float sum = 0.f;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                sum += __uint_as_float(q[j] << 16) + __uint_as_float(q[j] & 0xffff0000u);
+#pragma unroll
+              for (int d = kGroup / 16; d; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
+              if (r < kRowsX) {
+                // elements (0, 4), (1, 5), (2, 6), (3, 7)
+                uint4 o;
+                o.x = __byte_perm(v.x, v.z, 0x5410);
+                o.y = __byte_perm(v.x, v.z, 0x7632);
+                o.z = __byte_perm(v.y, v.w, 0x5410);
+                o.w = __byte_perm(v.y, v.w, 0x7632);
+                *reinterpret_cast<uint4 *>(dst + r * xstride) = o;
+                if ((p & (kGroup / 8 - 1)) == 0)
+                  side[(b * kSc + p / (kGroup / 8)) * kCols + r] = -136.f * sum;
+              }
+            } else {
+              float v[8] = {};
+              if (on) load8(static_cast<const float *>(P.x) + at, v);
+              int m = 0;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) m = max(m, __float_as_int(v[i]) & 0x7fffffff);
+#pragma unroll
+              for (int d = 8; d; d >>= 1) m = max(m, __shfl_xor_sync(kFull, m, d));
+              // 2^e: the block's largest element into [2^14, 2^15)
+              const int ex = min(141 - (m >> 23), 126);
+              const float f = __int_as_float((ex + 127) << 23);
+              uint32_t hi[4], lo[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float x0 = v[i] * f, x1 = v[i + 4] * f;
+                const __half2 h = __floats2half2_rn(x0, x1);
+                const float2 g = __half22float2(h);
+                const __half2 l = __floats2half2_rn(x0 - g.x, x1 - g.y);
+                hi[i] = *reinterpret_cast<const uint32_t *>(&h);
+                lo[i] = *reinterpret_cast<const uint32_t *>(&l);
+              }
+              if (r < kRowsX) {
+                dst += 2 * r * xstride;
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(dst + xstride) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                if (p == 0) side[b * kRowsX + r] = __int_as_float((127 - ex) << 23);
+              }
+            }
+            b += 2 * kWarps;
+            while (b >= nb && r < kRowsX) {
+              b -= nb;
+              ++r;
+            }
+          }
+        }
+        // the warps in each tile of each slice: share(w) <= i exactly for
+        // w <= (kWarps (i + 1) - 1) / total (lists shorter than the warps: one
+        // pair each, numbered by block)
+        if (!kr)
+          for (int e = tid; e < csize * nt; e += kThreads) {
+            const int q = (unsigned)e / (unsigned)nt, tile = e - q * nt;
+            int q_lo, qb;
+            slice(P, csize, q, q_lo, qb);
+            const unsigned all = nt * qb;
+            int w_lo = 0, n = qb;
+            if (all >= kWarps) {
+              w_lo = (kWarps * (tile * qb + 1) - 1) / all;
+              n = (kWarps * (tile + 1) * qb - 1) / all - w_lo + 1;
+            }
+            tab[2 * e] = (unsigned char)w_lo;
+            tab[2 * e + 1] = (unsigned char)n;
+          }
+        __syncthreads();
+
+        // ---- products
+        float acc[2][kNT][kSums];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < kNT; ++j)
+#pragma unroll
+            for (int i = 0; i < kSums; ++i) acc[h][j][i] = 0.f;
+        int tile = 0, blk = 0;
+        if (pos < end) {
+          tile = (unsigned)pos / (unsigned)nb;
+          blk = pos - tile * nb;
+        }
+        while (pos < end) {
+#pragma unroll
+          for (int d = 0; d < kDepth; ++d) {
+            if (pos >= end) break;
+            uint32_t w[4][4];
+            float f[4][kSc];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              w[i][0] = wv[d][i].x;
+              w[i][1] = wv[d][i].y;
+              w[i][2] = wv[d][i].z;
+              w[i][3] = wv[d][i].w;
+              exchange<kGroup>(w[i], t);
+#pragma unroll
+              for (int j = 0; j < kSc; ++j) f[i][j] = __half2float(sv[d][i][j]);
+            }
+            float part[2][kNT][4], un[kNT];
+            if (!kBf16)
+#pragma unroll
+              for (int j = 0; j < kNT; ++j) un[j] = side[blk * kRowsX + 4 * j + t];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              constexpr int kSteps = kGroup / 32;
+              const int g = i / kSteps;
+              if (i % kSteps == 0) {
+#pragma unroll
+                for (int j = 0; j < kNT; ++j) {
+                  float2 c = make_float2(0.f, 0.f);
+                  if (kBf16)
+                    c = *reinterpret_cast<const float2 *>(side + (blk * kSc + g) * kCols +
+                                                          8 * j + 2 * t);
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    part[h][j][0] = part[h][j][2] = c.x;
+                    part[h][j][1] = part[h][j][3] = c.y;
+                  }
+                }
+              }
+              uint32_t c[4][4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) codes<kBf16>(w[q][i], c[q]);
+#pragma unroll
+              for (int j = 0; j < kNT; ++j) {
+                const uint4 x4 =
+                    *reinterpret_cast<const uint4 *>(xl + 8 * j * xstride + blk * 256 + i * 64);
+                const uint32_t v[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  mma<kBf16>(part[h][j], c[2 * h][0], c[2 * h + 1][0], c[2 * h][1],
+                             c[2 * h + 1][1], v[0], v[1], part[h][j]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  mma<kBf16>(part[h][j], c[2 * h][2], c[2 * h + 1][2], c[2 * h][3],
+                             c[2 * h + 1][3], v[2], v[3], part[h][j]);
+              }
+              if ((i + 1) % kSteps == 0) {
+#pragma unroll
+                for (int j = 0; j < kNT; ++j)
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    if (kBf16) {
+                      acc[h][j][0] = fmaf(f[2 * h][g], part[h][j][0], acc[h][j][0]);
+                      acc[h][j][1] = fmaf(f[2 * h][g], part[h][j][1], acc[h][j][1]);
+                      acc[h][j][2 % kSums] = fmaf(f[2 * h + 1][g], part[h][j][2], acc[h][j][2 % kSums]);
+                      acc[h][j][3 % kSums] = fmaf(f[2 * h + 1][g], part[h][j][3], acc[h][j][3 % kSums]);
+                    } else {  // the hi and lo columns of one row
+                      acc[h][j][0] = fmaf(f[2 * h][g] * un[j], part[h][j][0] + part[h][j][1],
+                                          acc[h][j][0]);
+                      acc[h][j][1] = fmaf(f[2 * h + 1][g] * un[j], part[h][j][2] + part[h][j][3],
+                                          acc[h][j][1]);
+                    }
+                  }
+              }
+            }
+            fetch(d);
+            ++pos;
+            ++blk;
+            if (blk == nb || pos == end) {
+              // partial sums of the tile, to their slot in the CTA that adds it
+              // up: [slice][tile][warp in the tile]
+              const int at = (unsigned)tile / (unsigned)csize, to = tile - at * csize;
+              const int nth = total < kWarps ? blk - 1 : warp - tab[2 * (crank * nt + tile)];
+              float *sl = slots + (size_t)((crank * own + at) * most + nth) * kTile * kRowsX +
+                          gr * kRowsX;
+              if (csize > 1) sl = cl.map_shared_rank(sl, to);
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < kNT; ++j)
+#pragma unroll
+                  for (int i = 0; i < kSums; ++i) {
+                    // bf16: rows gr, gr + 8 and columns 2 t, 2 t + 1; fp32: the
+                    // two rows of x row t
+                    const int row = 16 * h + 8 * (kBf16 ? i >> 1 : i);
+                    const int col = kBf16 ? 8 * j + 2 * t + (i & 1) : 4 * j + t;
+                    float v = acc[h][j][i];
+                    if (kr) v += sl[row * kRowsX + col];
+                    sl[row * kRowsX + col] = v;
+                    acc[h][j][i] = 0.f;
+                  }
+              blk = 0;
+              ++tile;
+            }
+          }
+        }
+      }
+
+      // ---- the sum over slices and warps, tiles crank, crank + csize, ...
+      if (csize > 1)
+        cl.sync();
+      else
+        __syncthreads();
+      for (int e = tid; e < own * kTile * nr; e += kThreads) {
+        const int c = (unsigned)e / (unsigned)nr, r = e - c * nr;  // weight row, row of x
+        const int at = c / kTile, tile = at * csize + crank, n = (t0 + tile) * kTile + c % kTile;
+        if (tile >= nt || n >= P.N) continue;
+        float sum = 0.f;
+        for (int q = 0; q < csize; ++q) {
+          const float *sl = slots + ((size_t)((q * own + at) * most) * kTile + c % kTile) * kRowsX + r;
+          const int cnt = tab[2 * (q * nt + tile) + 1];
+          for (int w = 0; w < cnt; ++w, sl += kTile * kRowsX) sum += *sl;
+        }
+        const size_t out = (size_t)(r0 + r) * P.N + n;
+        if (kBf16)
+          static_cast<__nv_bfloat16 *>(P.y)[out] = __float2bfloat16_rn(sum);
+        else
+          static_cast<float *>(P.y)[out] = sum;
+      }
+      // the slots are read
+      if (csize > 1 && (r0 + kRowsX < P.rows || t0 + clusters * P.round_tiles < P.tiles)) cl.sync();
+    }
+  }
+}
+
+struct Plan {
+  int nt, csize, clusters, round_tiles, round_blocks, slots;
+  size_t smem;
+};
+
+// Cluster size and rounds for the shape.  The cost of a CTA, in blocks of 32
+// weight rows: its list, its share of x, and for a cluster its two barriers.
+// `most`: clusters of 1, 2, 4, 8 CTAs that the GPU runs at once.
+Plan make_plan(int rows, int N, int K, int group, bool bf16, const int (&most)[4]) {
+  Plan p = {};
+  const int cols = bf16 ? rows : 2 * rows;
+  p.nt = cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
+  const int rows_x = bf16 ? 8 * p.nt : 4 * p.nt;
+  const int tiles = (N + kTile - 1) / kTile, blocks = (K + kBlock - 1) / kBlock;
+  // shared memory of cluster size c, rt tiles and rb blocks a round
+  auto bytes = [&](int c, int rt, int rb) {
+    const int last = tiles % rt;  // tiles of the last round, if fewer
+    const auto slots = [&](int n) { return n ? c * ((n + c - 1) / c) * most_warps(warps_of(p.nt), n, rb) : 0; };
+    p.slots = slots(rt) > slots(last) ? slots(rt) : slots(last);
+    return (size_t)p.slots * kTile * rows_x * 4 + (size_t)8 * p.nt * ((size_t)rb * 256 + 64) +
+           (size_t)rb * 4 * (bf16 ? (kBlock / group) * 8 * p.nt : rows_x) + (size_t)2 * c * rt;
+  };
+  double best = 1e300;
+  for (int i = 0; i < 4; ++i) {
+    const int c = 1 << i, clusters = most[i] < tiles ? most[i] : tiles;
+    const int rt = (tiles + clusters - 1) / clusters, rb = (blocks + c - 1) / c;
+    double cost = (double)rt * rb + kXCost * rows_x * rb + (c > 1 ? kClusterCost : 0.0);
+    if (bytes(c, rt, rb) > kSmemMax) cost += 1e100;  // in rounds: the largest cluster
+    if (cost < best || (cost >= 1e100 && best >= 1e100)) {
+      best = cost;
+      p.csize = c;
+      p.clusters = clusters;
+      p.round_tiles = rt;
+      p.round_blocks = rb;
+    }
+  }
+  // Rounds where shared memory does not hold a CTA's share: at least 8 tiles
+  // at a time, then as many blocks as fit (one block of 8 tiles always does).
+  while (p.round_tiles > 8 && bytes(p.csize, p.round_tiles, p.round_blocks) > kSmemMax)
+    p.round_tiles = (p.round_tiles + 1) / 2;
+  while (p.round_blocks > 1 && bytes(p.csize, p.round_tiles, p.round_blocks) > kSmemMax)
+    p.round_blocks = (p.round_blocks + 1) / 2;
+  p.smem = bytes(p.csize, p.round_tiles, p.round_blocks);
+  return p;
+}
+
+template <bool kBf16, int kNT, int kGroup>
+cudaError_t launch(const QuantArgs &a, const Plan &p, cudaStream_t stream) {
+  const auto kernel = quant_linear_kernel<kBf16, kNT, kGroup>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.clusters * p.csize));
+  cfg.blockDim = dim3(32 * warps_of(kNT));
+  cfg.dynamicSmemBytes = p.smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.csize;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (p.csize == 1) {
+    cfg.attrs = attr + 1;
+    cfg.numAttrs = 1;
+  }
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+// How many clusters of 1, 2, 4, 8 such CTAs (one per SM) the current device runs
+// at once: GPCs differ in their SMs, so clusters of 8 leave some of them idle
+// (15 of the 19 that 152 SMs would hold on a GB300).  Asked once per device.
+cudaError_t cluster_counts(int (&most)[4]) {
+  static std::mutex lock;
+  static std::map<int, std::array<int, 4>> known;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> hold(lock);
+  auto it = known.find(dev);
+  if (it == known.end()) {
+    const auto kernel = quant_linear_kernel<true, 1, 128>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    if (e != cudaSuccess) return e;
+    std::array<int, 4> n;
+    for (int i = 0; i < 4; ++i) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(8);
+      cfg.blockDim = dim3(32 * warps_of(1));
+      cfg.dynamicSmemBytes = kSmemMax;
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = 1u << i;
+      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&n[i], kernel, &cfg);
+      if (e != cudaSuccess) return e;
+      if (n[i] < 1) n[i] = 1;
+    }
+    it = known.emplace(dev, n).first;
+  }
+  for (int i = 0; i < 4; ++i) most[i] = it->second[i];
+  return cudaSuccess;
+}
+
+template <bool kBf16, int kNT>
+cudaError_t by_group(int group, const QuantArgs &a, const Plan &p, cudaStream_t stream) {
+  return group == 128  ? launch<kBf16, kNT, 128>(a, p, stream)
+         : group == 64 ? launch<kBf16, kNT, 64>(a, p, stream)
+                       : launch<kBf16, kNT, 32>(a, p, stream);
+}
+
+template <bool kBf16>
+cudaError_t by_columns(int group, const QuantArgs &a, const Plan &p, cudaStream_t stream) {
+  return p.nt == 1   ? by_group<kBf16, 1>(group, a, p, stream)
+         : p.nt == 2 ? by_group<kBf16, 2>(group, a, p, stream)
+                     : by_group<kBf16, 4>(group, a, p, stream);
 }
 
 }  // namespace
@@ -69,17 +675,14 @@ cudaError_t launch_quant_linear(const void *x, const unsigned char *qw,
                                 int K, int group, bool bf16,
                                 cudaStream_t stream) {
   if (rows == 0 || N == 0) return cudaSuccess;
-  const unsigned blocks = (unsigned)(((size_t)N + 3) / 4);
-  const __half *sc = static_cast<const __half *>(scales);
-  if (bf16)
-    quant_linear_kernel<<<blocks, 128, 0, stream>>>(
-        static_cast<const __nv_bfloat16 *>(x), qw, sc,
-        static_cast<__nv_bfloat16 *>(y), rows, N, K, group);
-  else
-    quant_linear_kernel<<<blocks, 128, 0, stream>>>(
-        static_cast<const float *>(x), qw, sc, static_cast<float *>(y), rows, N,
-        K, group);
-  return cudaGetLastError();
+  int most[4];
+  const cudaError_t e = cluster_counts(most);
+  if (e != cudaSuccess) return e;
+  const Plan p = make_plan(rows, N, K, group, bf16, most);
+  const QuantArgs a{x, qw, static_cast<const __half *>(scales), y, rows, N, K,
+                    (N + kTile - 1) / kTile, (K + kBlock - 1) / kBlock, p.round_tiles, p.round_blocks,
+                    p.csize, p.slots};
+  return bf16 ? by_columns<true>(group, a, p, stream) : by_columns<false>(group, a, p, stream);
 }
 
 }  // namespace gdn
