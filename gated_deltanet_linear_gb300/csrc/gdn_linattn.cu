@@ -14,8 +14,10 @@
 // 32w + 8 rg .. + 7 and columns 4 cl .. 4 cl + 3 of the group: one warp
 // request covers four whole 128-byte row segments, and a lane's q and k are
 // 8 consecutive elements.  The 8 x 4 block stays in registers for all M
-// tokens: the state is read once and written once per launch.  The partial
-// sums of o meet in shared memory, one barrier for every 8 tokens.
+// tokens: the state is read once and written once per launch.  A lane keeps
+// one of its 4 sums of o in the reduction over the row groups (3 shuffles
+// instead of 8); the warps' sums meet in shared memory, one barrier for every
+// 8 tokens.
 //
 // Determinism.  Every product and sum is an explicit round-to-nearest
 // intrinsic in a fixed tree (a lane's rows in order, the row groups
@@ -92,23 +94,20 @@ __device__ __forceinline__ void st_state(float *p, const float4 &v) {
                : "memory");
 }
 
-template <typename T>
-struct Token {
-  float k[8], q[8], v[4], a;
-  // token m of the head's rows; g: this head's log decay of the token
-  __device__ __forceinline__ void load(const T *qp, const T *kp, const T *vp,
-                                       const float *gp) {
-    load8(qp, q);
-    load8(kp, k);
-    load4(vp, v);
-    a = __ldg(gp);
-  }
+// Token inputs of a block of tokens in shared memory, as fp32 (several tokens:
+// converted once for the CTA's four warps, and read again without the latency
+// of a cache miss).
+struct Staged {
+  float k[kBlk][kDim], q[kBlk][kDim], v[kBlk][32], a[kBlk];
 };
 
-template <typename T>
-__global__ void __launch_bounds__(128)
+// kMulti: more than one token: token inputs are staged 8 at a time.  One token: each lane reads its own, beside the state's
+// loads.
+template <typename T, bool kMulti>
+__global__ void __launch_bounds__(128, kMulti ? 8 : 5)
     linattn_steps_kernel(const LinattnArgs P) {
   __shared__ float part[2][kBlk][4][32];
+  __shared__ __align__(16) Staged st[1];
   // behind the kernel before it: nothing is read or written before that
   // kernel has ended
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -116,22 +115,15 @@ __global__ void __launch_bounds__(128)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int head = blockIdx.x >> 2, cg = blockIdx.x & 3;
   const int b = head / P.vh, vi = head % P.vh, hh = vi / P.rep;
-  int n = P.M;
-  if (P.lens) {
-    n = __ldg(P.lens + b);
-    if (n < 0 || n > P.M) {
-      if (tid == 0 && P.err) *P.err = 1;
-      return;
-    }
-  }
+  const int n = P.M;
   const int row = 32 * warp + 8 * (lane >> 3);
-  const int col = 32 * cg + 4 * (lane & 7);
+  const int cl = 4 * (lane & 7), col = 32 * cg + cl;
   const size_t blk = (size_t)row * kDim + col;  // of the state
 
   const size_t tok0 = (size_t)b * P.M;
-  const T *qp = static_cast<const T *>(P.q) + (tok0 * P.kh + hh) * kDim + row;
-  const T *kp = static_cast<const T *>(P.k) + (tok0 * P.kh + hh) * kDim + row;
-  const T *vp = static_cast<const T *>(P.v) + (tok0 * P.vh + vi) * kDim + col;
+  const T *qp = static_cast<const T *>(P.q) + (tok0 * P.kh + hh) * kDim;
+  const T *kp = static_cast<const T *>(P.k) + (tok0 * P.kh + hh) * kDim;
+  const T *vp = static_cast<const T *>(P.v) + (tok0 * P.vh + vi) * kDim + 32 * cg;
   T *op = static_cast<T *>(P.o) + (tok0 * P.vh + vi) * kDim + 32 * cg;
   const float *gp = P.g + (P.g_head ? (size_t)vi : tok0 * P.vh + vi);
   const size_t qk_step = (size_t)P.kh * kDim, v_step = (size_t)P.vh * kDim;
@@ -143,62 +135,98 @@ __global__ void __launch_bounds__(128)
 #pragma unroll
     for (int i = 0; i < 8; ++i) s[i] = ld_state(Sp + i * kDim);
   }
-  Token<T> t;
-  if (n > 0) t.load(qp, kp, vp, gp);
-  int buf = 0;
-  for (int m0 = 0; m0 < n; m0 += kBlk) {
-    const int nb = min(kBlk, n - m0);
-    for (int j = 0; j < nb; ++j) {
-      const int m = m0 + j;
-      Token<T> u = t;
-      if (m + 1 < n)
-        t.load(qp + (m + 1) * qk_step, kp + (m + 1) * qk_step,
-               vp + (m + 1) * v_step, gp + (m + 1) * g_step);
-      const float a = expf(u.a);
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  // One token: S = a S + k v^T, and this lane's share of S^T q into part[j].
+  const bool up8 = lane & 8, up16 = lane & 16;
+  // the column of the group whose sum this lane ends up with
+  const int mine = cl + 2 * (up8 ? 1 : 0) + (up16 ? 1 : 0);
+  auto token = [&](const float (&k)[8], const float (&q)[8], const float (&v)[4], float a,
+                   float (&sums)[4][32]) {
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        s[i].x = __fmaf_rn(a, s[i].x, __fmul_rn(u.k[i], u.v[0]));
-        s[i].y = __fmaf_rn(a, s[i].y, __fmul_rn(u.k[i], u.v[1]));
-        s[i].z = __fmaf_rn(a, s[i].z, __fmul_rn(u.k[i], u.v[2]));
-        s[i].w = __fmaf_rn(a, s[i].w, __fmul_rn(u.k[i], u.v[3]));
-        acc[0] = __fmaf_rn(s[i].x, u.q[i], acc[0]);
-        acc[1] = __fmaf_rn(s[i].y, u.q[i], acc[1]);
-        acc[2] = __fmaf_rn(s[i].z, u.q[i], acc[2]);
-        acc[3] = __fmaf_rn(s[i].w, u.q[i], acc[3]);
-      }
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        acc[c] = __fadd_rn(acc[c], __shfl_xor_sync(kFull, acc[c], 8));
-        acc[c] = __fadd_rn(acc[c], __shfl_xor_sync(kFull, acc[c], 16));
-      }
-      if (lane < 8)
-        *reinterpret_cast<float4 *>(&part[buf][j][warp][4 * lane]) =
-            make_float4(acc[0], acc[1], acc[2], acc[3]);
-      if (P.ckpt) {
-        float *cp = P.ckpt + (((size_t)m * P.B * P.vh) + head) * kDim * kDim + blk;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) st_state(cp + i * kDim, s[i]);
-      }
+    for (int i = 0; i < 8; ++i) {
+      s[i].x = __fmaf_rn(a, s[i].x, __fmul_rn(k[i], v[0]));
+      s[i].y = __fmaf_rn(a, s[i].y, __fmul_rn(k[i], v[1]));
+      s[i].z = __fmaf_rn(a, s[i].z, __fmul_rn(k[i], v[2]));
+      s[i].w = __fmaf_rn(a, s[i].w, __fmul_rn(k[i], v[3]));
+      acc[0] = __fmaf_rn(s[i].x, q[i], acc[0]);
+      acc[1] = __fmaf_rn(s[i].y, q[i], acc[1]);
+      acc[2] = __fmaf_rn(s[i].z, q[i], acc[2]);
+      acc[3] = __fmaf_rn(s[i].w, q[i], acc[3]);
     }
-    __syncthreads();
-    // (the other buffer is written next; this one again only after the
-    // next barrier, which follows these reads)
+    float k0 = up8 ? acc[2] : acc[0], k1 = up8 ? acc[3] : acc[1];
+    k0 = __fadd_rn(k0, __shfl_xor_sync(kFull, up8 ? acc[0] : acc[2], 8));
+    k1 = __fadd_rn(k1, __shfl_xor_sync(kFull, up8 ? acc[1] : acc[3], 8));
+    sums[warp][mine] = __fadd_rn(up16 ? k1 : k0, __shfl_xor_sync(kFull, up16 ? k0 : k1, 16));
+  };
+  auto state_to = [&](float *p) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) st_state(p + blk + i * kDim, s[i]);
+  };
+  // The sums of nb tokens from m0 on, from the four warps' parts.
+  auto output = [&](int m0, int nb, float (&p)[kBlk][4][32]) {
     if (tid < 8 * nb) {
       const int j = tid >> 3, c = 4 * (tid & 7);
       float y[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        y[e] = __fmul_rn(P.scale,
-                         __fadd_rn(__fadd_rn(part[buf][j][0][c + e], part[buf][j][2][c + e]),
-                                   __fadd_rn(part[buf][j][1][c + e], part[buf][j][3][c + e])));
+        y[e] = __fmul_rn(P.scale, __fadd_rn(__fadd_rn(p[j][0][c + e], p[j][2][c + e]),
+                                            __fadd_rn(p[j][1][c + e], p[j][3][c + e])));
       store4(op + (m0 + j) * v_step + c, y);
     }
-    buf ^= 1;
-  }
-  float *So = P.S_out + (size_t)head * kDim * kDim + blk;
+  };
+  if (!kMulti) {
+    float k[8], q[8], v[4];
+    load8(kp + row, k);
+    load8(qp + row, q);
+    load4(vp + cl, v);
+    token(k, q, v, expf(__ldg(gp)), part[0][0]);
+    if (P.ckpt) state_to(P.ckpt + (size_t)head * kDim * kDim);
+    __syncthreads();
+    output(0, 1, part[0]);
+  } else {
+    int buf = 0;
+    for (int m0 = 0; m0 < n; m0 += kBlk, buf ^= 1) {
+      const int nb = min(kBlk, n - m0);
+      // (the last block's inputs are read: every warp has passed the barrier
+      // behind its tokens)
+      for (int e = tid; e < nb * 36; e += 128) {  // 8 elements each: 16 k, 16 q, 4 v
+        const int j = e / 36, x = e - 36 * j;
+        float f[8];
+        if (x < 16)
+          load8(kp + (m0 + j) * qk_step + 8 * x, f);
+        else if (x < 32)
+          load8(qp + (m0 + j) * qk_step + 8 * (x - 16), f);
+        else
+          load8(vp + (m0 + j) * v_step + 8 * (x - 32), f);
+        float *d = x < 16 ? &st->k[j][8 * x] : x < 32 ? &st->q[j][8 * (x - 16)]
+                                                      : &st->v[j][8 * (x - 32)];
+        *reinterpret_cast<float4 *>(d) = make_float4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<float4 *>(d + 4) = make_float4(f[4], f[5], f[6], f[7]);
+      }
+      if (tid < nb) st->a[tid] = expf(__ldg(gp + (m0 + tid) * g_step));
+      __syncthreads();
+      for (int j = 0; j < nb; ++j) {
+        float k[8], q[8], v[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) st_state(So + i * kDim, s[i]);
+        for (int i = 0; i < 8; i += 4) {
+          const float4 x = *reinterpret_cast<const float4 *>(&st->k[j][row + i]);
+          const float4 y = *reinterpret_cast<const float4 *>(&st->q[j][row + i]);
+          k[i] = x.x; k[i + 1] = x.y; k[i + 2] = x.z; k[i + 3] = x.w;
+          q[i] = y.x; q[i + 1] = y.y; q[i + 2] = y.z; q[i + 3] = y.w;
+        }
+        const float4 z = *reinterpret_cast<const float4 *>(&st->v[j][cl]);
+        v[0] = z.x; v[1] = z.y; v[2] = z.z; v[3] = z.w;
+        token(k, q, v, st->a[j], part[buf][j]);
+        if (P.ckpt)
+          state_to(P.ckpt + (((size_t)(m0 + j) * P.B * P.vh) + head) * kDim * kDim);
+      }
+      __syncthreads();
+      // (the other buffer is written next; this one again only after the
+      // barriers of the next block, which follow these reads)
+      output(m0, nb, part[buf]);
+    }
+  }
+  state_to(P.S_out + (size_t)head * kDim * kDim);
 }
 
 }  // namespace
@@ -217,8 +245,11 @@ cudaError_t launch_linattn_steps(const LinattnArgs &P, bool bf16,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return bf16 ? cudaLaunchKernelEx(&cfg, linattn_steps_kernel<__nv_bfloat16>, P)
-              : cudaLaunchKernelEx(&cfg, linattn_steps_kernel<float>, P);
+  if (P.M == 1)
+    return bf16 ? cudaLaunchKernelEx(&cfg, linattn_steps_kernel<__nv_bfloat16, false>, P)
+                : cudaLaunchKernelEx(&cfg, linattn_steps_kernel<float, false>, P);
+  return bf16 ? cudaLaunchKernelEx(&cfg, linattn_steps_kernel<__nv_bfloat16, true>, P)
+              : cudaLaunchKernelEx(&cfg, linattn_steps_kernel<float, true>, P);
 }
 
 }  // namespace gdn
