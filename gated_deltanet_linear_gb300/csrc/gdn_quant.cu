@@ -16,21 +16,24 @@
 //            instead of 0, which costs 5 of the 24 bits of sums that are
 //            rounded to 8 at the end
 //
-// Order of k.  A lane of a fragment row reads 16 bytes, 32 consecutive codes;
-// the four lanes of a row read 128 (a block).  The sum over k may run in any
-// order, so the codes are used as they unpack (elements 0 and 4 of a word are
-// one register, 1 and 5 the next, ...) and x is put into shared memory in that
-// order.  Every m16n8k16 step has to stay inside one group: with groups of 64 or
-// 32 the four lanes exchange words first (xor 2, xor 1), so that step i of a
-// block covers the 32 codes of quarter i.
+// Weights.  A warp takes blocks of 16 rows x 256 codes (128 bytes of each row)
+// through a ring of its own in shared memory: asynchronous 16-byte copies, 8
+// lanes to a row, so that a request is four whole lines (fragment-shaped loads,
+// 64 bytes of 8 rows, spent more cycles on cache tags than the arithmetic
+// takes), chunks XOR-ed by the row.  ldmatrix hands lane (row g, t) word t of a
+// row's 16-byte chunk, 8 codes; chunk i is k 32 i .. 32 i + 31, so every product
+// step stays inside one group whatever the group size.  The sum over k may run
+// in any order: the codes are used as they unpack (elements 0 and 4 of a word
+// are one register, 1 and 5 the next, ...), and x is put into shared memory in
+// that order.
 //
-// Work split.  One CTA of 16 (many columns: 8) warps per SM; a CTA, or a cluster of up to 8 that
-// cut K between them (few tiles, or much x to convert), takes a range of 32-row
-// tiles.  Inside a CTA the (tile, block) pairs are one list, cut evenly over the
-// warps whatever the sizes; a warp keeps several blocks in flight in registers.
-// At the end of a tile, or of its share, it stores its partial sums in a slot of
-// its own in the CTA that adds up the tile; slots are added in a fixed order, so
-// results are the same bits on every call.
+// Work split.  One CTA of 16 (many columns: 8) warps per SM; a CTA, or a cluster
+// of up to 8 that cut K between them (few tiles, or much x to convert), takes a
+// range of 16-row tiles.  Inside a CTA the (tile, block) pairs are one list, cut
+// evenly over the warps whatever the sizes.  At the end of a tile, or of its
+// share, a warp stores its partial sums in a slot of its own in the CTA that
+// adds up the tile; slots are added in a fixed order, so results are the same
+// bits on every call.
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -39,6 +42,7 @@
 #include <array>
 #include <map>
 #include <mutex>
+#include <type_traits>
 
 #include "gdn_internal.cuh"
 
@@ -50,10 +54,14 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 // Warps of a CTA: 16, or 8 where the sums of 32 columns need the registers.
 __host__ __device__ constexpr int warps_of(int n8) { return n8 > 2 ? 8 : 16; }
-constexpr int kBlock = 128;   // k elements of a block
-constexpr int kTile = 32;     // weight rows of a tile
+constexpr int kBlock = 256;   // k elements of a block
+constexpr int kTile = 16;     // weight rows of a tile
+constexpr int kBlockBytes = kTile * kBlock / 2;
+constexpr int kXBlock = kBlock * 2;  // bytes of a block of a column of x
+// Blocks of a warp's ring.
+__host__ __device__ constexpr int depth_of(int n8) { return n8 > 2 ? 4 : 3; }
 constexpr int kSmemMax = 220 * 1024;
-// Costs of make_plan(), relative to a block of 32 weight rows.
+// Costs of make_plan(), relative to a block.
 constexpr double kXCost = 0.1, kClusterCost = 12.0;
 
 struct QuantArgs {
@@ -62,10 +70,12 @@ struct QuantArgs {
   const __half *sc;
   void *y;
   int rows, N, K;
-  int tiles, blocks;      // 32-row tiles, 128-element blocks of a row
+  int tiles, blocks;      // 16-row tiles, 256-element blocks of a row
   int round_tiles;        // tiles of a cluster in one round
   int round_blocks;       // blocks of a CTA's slice in one round
   int csize, slots;       // CTAs of a cluster, slots of partial sums
+  int columns;            // of x in shared memory (those beyond are not used)
+  int sc_shared;          // the round's scales are copied to shared memory
 };
 
 // Blocks of CTA `rank`'s slice of a round: an even share where one round takes
@@ -139,48 +149,25 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
           "f"(c[2]), "f"(c[3]));
 }
 
-// Where the 8-element part p (0..15) of a block sits in shared memory: at
-// 4 * step + lane of the order in which the lanes use them.
-template <int kGroup>
-__device__ __forceinline__ int place(int p) {
-  if (kGroup == 128) return 4 * (p & 3) + (p >> 2);
-  if (kGroup == 64) {
-    // group p >> 3; lane t has part 4 (t & 1) + 2 j + (t >> 1) in step j
-    const int q = p & 7, t = (q >> 2) | ((q & 1) << 1), j = (q >> 1) & 1;
-    return 4 * (2 * (p >> 3) + j) + t;
-  }
-  // group p >> 2; lane t has part 2 (t & 1) + (t >> 1)
-  const int q = p & 3, t = (q >> 1) | ((q & 1) << 1);
-  return 4 * (p >> 2) + t;
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
+  // (bytes < 16: the rest is filled with zeros and not read)
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
 }
-
-// After the exchange, word i of every lane belongs to step i (see place()).
-template <int kGroup>
-__device__ __forceinline__ void exchange(uint32_t (&w)[4], int t) {
-  if (kGroup == 128) return;
-  const bool up = t >= 2;
-  // keep w0, w2 (low lanes) or w1, w3 (high lanes), swap the others
-  uint32_t s0 = up ? w[0] : w[1], s1 = up ? w[2] : w[3];
-  const uint32_t k0 = up ? w[1] : w[0], k1 = up ? w[3] : w[2];
-  s0 = __shfl_xor_sync(kFull, s0, 2);
-  s1 = __shfl_xor_sync(kFull, s1, 2);
-  // first 64 elements: own words of the low lanes, received ones of the high
-  uint32_t a0 = up ? s0 : k0, a1 = up ? s1 : k1, b0 = up ? k0 : s0, b1 = up ? k1 : s1;
-  if (kGroup == 32) {
-    const bool odd = t & 1;
-    uint32_t sa = odd ? a0 : a1, sb = odd ? b0 : b1;
-    const uint32_t ka = odd ? a1 : a0, kb = odd ? b1 : b0;
-    sa = __shfl_xor_sync(kFull, sa, 1);
-    sb = __shfl_xor_sync(kFull, sb, 1);
-    a0 = odd ? sa : ka;
-    a1 = odd ? ka : sa;
-    b0 = odd ? sb : kb;
-    b1 = odd ? kb : sb;
-  }
-  w[0] = a0;
-  w[1] = a1;
-  w[2] = b0;
-  w[3] = b1;
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Four 8 x 16-byte matrices; lane l gives the address of row l & 7 of matrix
+// l >> 3 and receives word l & 3 of row l >> 2 of each.
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
 }
 
 // x elements 8 p .. + 7 of a row, as fp32.
@@ -191,14 +178,25 @@ __device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
   x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
 
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
+  const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
 template <bool kBf16, int kNT, int kGroup>
 __global__ void __launch_bounds__(32 * warps_of(kNT), 1)
     quant_linear_kernel(const QuantArgs P) {
+  using T = typename std::conditional<kBf16, __nv_bfloat16, float>::type;
   constexpr int kWarps = warps_of(kNT), kThreads = 32 * kWarps;
   constexpr int kCols = 8 * kNT;
   constexpr int kRowsX = kBf16 ? kCols : kCols / 2;  // rows of x of a pass
   constexpr int kSc = kBlock / kGroup;               // scales of a block
-  constexpr int kDepth = 3;                          // blocks in flight a warp
+  constexpr int kDepth = depth_of(kNT);
   constexpr int kSums = kBf16 ? 4 : 2;               // of a lane and m16n8 tile
   extern __shared__ __align__(16) unsigned char smem[];
   const cg::cluster_group cl = cg::this_cluster();
@@ -209,23 +207,33 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1)
   const int warp = __shfl_sync(kFull, tid >> 5, 0);
   const int gr = lane >> 2, t = lane & 3;
 
-  // shared memory: partial sums, x (a column is round_blocks * 256 + 64 bytes),
-  // then by block: 2^-e of each row (fp32) or -136 sums of each group (bf16),
-  // then by slice and tile: the first warp in it and the number of warps
-  const uint32_t xstride = (uint32_t)P.round_blocks * 256 + 64;
-  float *slots = reinterpret_cast<float *>(smem);
-  unsigned char *xs = smem + (size_t)P.slots * kTile * kRowsX * 4;
-  float *side = reinterpret_cast<float *>(xs + (size_t)kCols * xstride);
+  // shared memory: the warps' rings, partial sums, x (a column is round_blocks *
+  // 512 + 64 bytes), then by block: 2^-e of each row (fp32) or -136 sums of each
+  // group (bf16), then by slice and tile: the first warp in it and the number
+  // of warps, then the scales of the round's rows
+  const uint32_t xstride = (uint32_t)P.round_blocks * kXBlock + 64;
+  const uint32_t ring =
+      (uint32_t)__cvta_generic_to_shared(smem) + warp * kDepth * kBlockBytes;
+  float *slots = reinterpret_cast<float *>(smem + kWarps * kDepth * kBlockBytes);
+  unsigned char *xs =
+      reinterpret_cast<unsigned char *>(slots) + (size_t)P.slots * kTile * kRowsX * 4;
+  float *side = reinterpret_cast<float *>(xs + (size_t)P.columns * xstride);
   unsigned char *tab = reinterpret_cast<unsigned char *>(
       side + P.round_blocks * (kBf16 ? kSc * kCols : kRowsX));
-  const unsigned char *xl = xs + gr * xstride + t * 16;  // of this lane's column
+  __half *scs = reinterpret_cast<__half *>(
+      smem + (((size_t)(tab - smem) + 2 * csize * P.round_tiles + 15) & ~(size_t)15));
+  // this lane's column of x in each n8 tile (columns that are not there: any)
+  const unsigned char *xl[kNT];
+#pragma unroll
+  for (int j = 0; j < kNT; ++j)
+    xl[j] = xs + (8 * j + gr < P.columns ? 8 * j + gr : 0) * xstride + t * 16;
 
   // behind the kernel before it: nothing is read or written before it has ended
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (csize > 1) cl.sync();  // every CTA's shared memory is there
 
-  const uint32_t wrow = (uint32_t)P.K / 2;
+  const size_t wrow = (size_t)P.K / 2;
   const int groups = P.K / kGroup;
 
   for (int r0 = 0; r0 < P.rows; r0 += kRowsX) {
@@ -242,141 +250,134 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1)
         int pos = share<kWarps>(total, warp);
         const int end = share<kWarps>(total, warp + 1);
 
-        // ---- weights: a ring of blocks in registers, loads ahead of use.
-        // Rows gr + 8 i of a tile; rows behind the last one read it again (and
-        // nothing stores them).  Lanes behind the end of K read nothing.
-        uint4 wv[kDepth][4];
-        __half sv[kDepth][4][kSc];
-        const uint8_t *wp = nullptr;  // of the tile, and the lane's row offsets
-        const __half *sp = nullptr;
-        uint32_t wo[4], so[4];
-        int lpos = pos, lb = 0, lt = 0;  // the next load
+        // ---- weights: the next block of this warp's list into its ring.  Lane
+        // l copies 16-byte chunk l & 7 of rows (l >> 3) + 4 i; rows and chunks
+        // behind the end are zeros.
+        const int crow = lane >> 3, chunk = lane & 7;
+        int lpos = pos, lb = 0, lt = 0, ld = 0;
+        const uint8_t *wp = nullptr;
+        int left = 0;  // rows from crow on
         auto aim = [&]() {
-          const int n0 = (t0 + lt) * kTile;
-          wp = P.qw + (size_t)n0 * wrow;
-          sp = P.sc + (size_t)n0 * groups;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int n = min(gr + 8 * i, P.N - 1 - n0), b = b_lo + lb;
-            wo[i] = n * wrow + b * (kBlock / 2) + 16 * t;
-            so[i] = n * groups + b * kSc;
-          }
+          const int n0 = (t0 + lt) * kTile + crow;
+          left = P.N - n0;
+          wp = P.qw + (size_t)min(n0, P.N - 1) * wrow + (size_t)(b_lo + lb) * (kBlock / 2) +
+               16 * chunk;
         };
         if (pos < end) {
           lt = (unsigned)pos / (unsigned)nb;
           lb = pos - lt * nb;
           aim();
         }
-        auto fetch = [&](int d) {
+        auto fetch = [&]() {
           if (lpos < end) {
-            const int b = b_lo + lb;
-            if (b * kBlock + kBlock <= P.K) {
+            const int in = (b_lo + lb) * kBlock + 32 * chunk < P.K ? 16 : 0;
+            const uint32_t dst = ring + ld * kBlockBytes;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                wv[d][i] = __ldg(reinterpret_cast<const uint4 *>(wp + wo[i]));
-#pragma unroll
-                for (int j = 0; j < kSc; ++j) sv[d][i][j] = __ldg(sp + (so[i] + j));
-              }
-            } else {  // the end of K
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                wv[d][i] = make_uint4(0, 0, 0, 0);
-                if (b * kBlock + 32 * t < P.K)
-                  wv[d][i] = __ldg(reinterpret_cast<const uint4 *>(wp + wo[i]));
-#pragma unroll
-                for (int j = 0; j < kSc; ++j)
-                  sv[d][i][j] = b * kSc + j < groups ? __ldg(sp + (so[i] + j)) : __half(0.f);
-              }
+            for (int i = 0; i < 4; ++i) {
+              const int r = crow + 4 * i;
+              cp_async16(dst + r * 128 + ((chunk ^ (r & 7)) << 4),
+                         4 * i < left && in ? wp + (size_t)i * 4 * wrow : P.qw, 4 * i < left ? in : 0);
             }
-            ++lpos;
             if (++lb == nb) {
               lb = 0;
               ++lt;
               aim();
             } else {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                wo[i] += kBlock / 2;
-                so[i] += kSc;
-              }
+              wp += kBlock / 2;
             }
+            ++lpos;
+            ld = ld + 1 == kDepth ? 0 : ld + 1;
           }
+          cp_async_commit();
         };
-#pragma unroll
-        for (int d = 0; d < kDepth; ++d) fetch(d);
+        // ---- the scales of the round's rows (contiguous), once a round
+        if (P.sc_shared && !kr) {
+          const int n0 = t0 * kTile, nrows = min(nt * kTile, P.N - n0);
+          const int bytes = nrows * groups * 2;
+          const unsigned char *src = reinterpret_cast<const unsigned char *>(P.sc + (size_t)n0 * groups);
+          const uint32_t dst = (uint32_t)__cvta_generic_to_shared(scs);
+          for (int e = tid * 16; e < bytes; e += kThreads * 16)
+            cp_async16(dst + e, src + e, min(16, bytes - e));
+        }
+        cp_async_commit();
 
-        // ---- x: this slice of the rows in the order of use; half a warp to a
-        // block of a row
+        // ---- x: this slice of the rows in the order of use; half a warp to
+        // 128 elements of a row.  The first part is read before the weights
+        // are asked for.
         if (kr || t0 != cluster * P.round_tiles || r0) __syncthreads();  // readers are done
         {
-          const int p = lane & 15;
+          const int p = lane & 15, halves = 2 * nb;
           int b = 2 * warp + (lane >> 4), r = 0;
-          while (b >= nb && r < kRowsX) {
-            b -= nb;
-            ++r;
-          }
+          auto wrap = [&]() {
+            while (b >= halves && r < kRowsX) {
+              b -= halves;
+              ++r;
+            }
+          };
+          wrap();
+          struct Part {
+            float v[8];
+          };
+          auto read = [&]() {
+            Part x = {};
+            const int k = b_lo * kBlock + b * 128 + 8 * p;
+            if (r < nr && k < P.K) load8(static_cast<const T *>(P.x) + (size_t)(r0 + r) * P.K + k, x.v);
+            return x;
+          };
           // (both halves run the same number of turns: shuffles inside)
-          const int turns = (kRowsX * nb + 2 * kWarps - 1) / (2 * kWarps);
-#pragma unroll 2
+          const int turns = (nr * halves + 2 * kWarps - 1) / (2 * kWarps);
+          Part x = read();
+#pragma unroll
+          for (int d = 0; d < kDepth - 1; ++d) fetch();
           for (int turn = 0; turn < turns; ++turn) {
-            const int k = (b_lo + b) * kBlock + 8 * p;
-            const bool on = r < nr && k < P.K;
-            const size_t at = (size_t)(r0 + r) * P.K + k;
-            unsigned char *dst = xs + b * 256 + place<kGroup>(p) * 16;
+            const int cb = b, cr = r;
+            const Part c = x;
+            b += 2 * kWarps;
+            wrap();
+            if (turn + 1 < turns) x = read();
+            unsigned char *dst = xs + cb * (kXBlock / 2) + p * 16;
             if (kBf16) {
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (on)
-                v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(P.x) + at));
-              const uint32_t q[4] = {v.x, v.y, v.z, v.w};
               float sum = 0.f;
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                sum += __uint_as_float(q[j] << 16) + __uint_as_float(q[j] & 0xffff0000u);
+              for (int j = 0; j < 8; ++j) sum += c.v[j];
 #pragma unroll
               for (int d = kGroup / 16; d; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
-              if (r < kRowsX) {
+              if (cr < nr) {
                 // elements (0, 4), (1, 5), (2, 6), (3, 7)
-                uint4 o;
-                o.x = __byte_perm(v.x, v.z, 0x5410);
-                o.y = __byte_perm(v.x, v.z, 0x7632);
-                o.z = __byte_perm(v.y, v.w, 0x5410);
-                o.w = __byte_perm(v.y, v.w, 0x7632);
-                *reinterpret_cast<uint4 *>(dst + r * xstride) = o;
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  o[j] = __byte_perm(__float_as_uint(c.v[j]), __float_as_uint(c.v[j + 4]), 0x7632);
+                *reinterpret_cast<uint4 *>(dst + cr * xstride) = make_uint4(o[0], o[1], o[2], o[3]);
                 if ((p & (kGroup / 8 - 1)) == 0)
-                  side[(b * kSc + p / (kGroup / 8)) * kCols + r] = -136.f * sum;
+                  side[(cb * (kSc / 2) + p / (kGroup / 8)) * kCols + cr] = -136.f * sum;
               }
             } else {
-              float v[8] = {};
-              if (on) load8(static_cast<const float *>(P.x) + at, v);
               int m = 0;
 #pragma unroll
-              for (int i = 0; i < 8; ++i) m = max(m, __float_as_int(v[i]) & 0x7fffffff);
+              for (int i = 0; i < 8; ++i) m = max(m, __float_as_int(c.v[i]) & 0x7fffffff);
+              // (the other half warp has the other half of the same block)
 #pragma unroll
-              for (int d = 8; d; d >>= 1) m = max(m, __shfl_xor_sync(kFull, m, d));
+              for (int d = 16; d; d >>= 1) m = max(m, __shfl_xor_sync(kFull, m, d));
               // 2^e: the block's largest element into [2^14, 2^15)
               const int ex = min(141 - (m >> 23), 126);
               const float f = __int_as_float((ex + 127) << 23);
               uint32_t hi[4], lo[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const float x0 = v[i] * f, x1 = v[i + 4] * f;
+                const float x0 = c.v[i] * f, x1 = c.v[i + 4] * f;
                 const __half2 h = __floats2half2_rn(x0, x1);
                 const float2 g = __half22float2(h);
                 const __half2 l = __floats2half2_rn(x0 - g.x, x1 - g.y);
                 hi[i] = *reinterpret_cast<const uint32_t *>(&h);
                 lo[i] = *reinterpret_cast<const uint32_t *>(&l);
               }
-              if (r < kRowsX) {
-                dst += 2 * r * xstride;
+              if (cr < nr) {
+                dst += 2 * cr * xstride;
                 *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 *reinterpret_cast<uint4 *>(dst + xstride) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                if (p == 0) side[b * kRowsX + r] = __int_as_float((127 - ex) << 23);
+                if (lane == 0) side[(cb >> 1) * kRowsX + cr] = __int_as_float((127 - ex) << 23);
               }
-            }
-            b += 2 * kWarps;
-            while (b >= nb && r < kRowsX) {
-              b -= nb;
-              ++r;
             }
           }
         }
@@ -397,126 +398,133 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1)
             tab[2 * e] = (unsigned char)w_lo;
             tab[2 * e + 1] = (unsigned char)n;
           }
+        cp_async_wait<kDepth - 1>();  // (the scales)
         __syncthreads();
 
         // ---- products
-        float acc[2][kNT][kSums];
+        float acc[kNT][kSums];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int j = 0; j < kNT; ++j)
 #pragma unroll
-          for (int j = 0; j < kNT; ++j)
-#pragma unroll
-            for (int i = 0; i < kSums; ++i) acc[h][j][i] = 0.f;
-        int tile = 0, blk = 0;
+          for (int i = 0; i < kSums; ++i) acc[j][i] = 0.f;
+        int tile = 0, blk = 0, rd = 0;
         if (pos < end) {
           tile = (unsigned)pos / (unsigned)nb;
           blk = pos - tile * nb;
         }
-        while (pos < end) {
-#pragma unroll
-          for (int d = 0; d < kDepth; ++d) {
-            if (pos >= end) break;
-            uint32_t w[4][4];
-            float f[4][kSc];
+        // this lane's ldmatrix row: row lane & 7, chunk lane >> 3 (then + 4, and
+        // rows + 8)
+        const uint32_t lrow = (lane & 7) * 128;
+        const uint32_t lc0 = lrow + ((((uint32_t)lane >> 3) ^ (lane & 7)) << 4);
+        const uint32_t lc1 = lrow + (((((uint32_t)lane >> 3) + 4) ^ (lane & 7)) << 4);
+        const __half *s0p = nullptr, *s1p = nullptr;
+        auto scales_of = [&]() {  // (rows behind the last one: its scales)
+          const int n0 = t0 * kTile, last = P.N - 1 - n0;
+          const __half *sc = P.sc_shared ? scs : P.sc + (size_t)n0 * groups;
+          s0p = sc + (size_t)min(tile * kTile + gr, last) * groups;
+          s1p = sc + (size_t)min(tile * kTile + gr + 8, last) * groups;
+        };
+        if (pos < end) scales_of();
+        for (; pos < end; ++pos) {
+          cp_async_wait<kDepth - 2>();
+          __syncwarp();  // every lane's copies of this block have landed
+          const uint32_t st = ring + rd * kBlockBytes;
+          rd = rd + 1 == kDepth ? 0 : rd + 1;
+          uint32_t w0[8], w1[8];  // rows gr, gr + 8: chunks 0..7
+          {
+            uint32_t a[4], b[4], c[4], d[4];
+            ldmatrix4(st + lc0, a);
+            ldmatrix4(st + lc1, b);
+            ldmatrix4(st + 1024 + lc0, c);
+            ldmatrix4(st + 1024 + lc1, d);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              w[i][0] = wv[d][i].x;
-              w[i][1] = wv[d][i].y;
-              w[i][2] = wv[d][i].z;
-              w[i][3] = wv[d][i].w;
-              exchange<kGroup>(w[i], t);
-#pragma unroll
-              for (int j = 0; j < kSc; ++j) f[i][j] = __half2float(sv[d][i][j]);
-            }
-            float part[2][kNT][4], un[kNT];
-            if (!kBf16)
-#pragma unroll
-              for (int j = 0; j < kNT; ++j) un[j] = side[blk * kRowsX + 4 * j + t];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              constexpr int kSteps = kGroup / 32;
-              const int g = i / kSteps;
-              if (i % kSteps == 0) {
-#pragma unroll
-                for (int j = 0; j < kNT; ++j) {
-                  float2 c = make_float2(0.f, 0.f);
-                  if (kBf16)
-                    c = *reinterpret_cast<const float2 *>(side + (blk * kSc + g) * kCols +
-                                                          8 * j + 2 * t);
-#pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    part[h][j][0] = part[h][j][2] = c.x;
-                    part[h][j][1] = part[h][j][3] = c.y;
-                  }
-                }
-              }
-              uint32_t c[4][4];
-#pragma unroll
-              for (int q = 0; q < 4; ++q) codes<kBf16>(w[q][i], c[q]);
-#pragma unroll
-              for (int j = 0; j < kNT; ++j) {
-                const uint4 x4 =
-                    *reinterpret_cast<const uint4 *>(xl + 8 * j * xstride + blk * 256 + i * 64);
-                const uint32_t v[4] = {x4.x, x4.y, x4.z, x4.w};
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                  mma<kBf16>(part[h][j], c[2 * h][0], c[2 * h + 1][0], c[2 * h][1],
-                             c[2 * h + 1][1], v[0], v[1], part[h][j]);
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                  mma<kBf16>(part[h][j], c[2 * h][2], c[2 * h + 1][2], c[2 * h][3],
-                             c[2 * h + 1][3], v[2], v[3], part[h][j]);
-              }
-              if ((i + 1) % kSteps == 0) {
-#pragma unroll
-                for (int j = 0; j < kNT; ++j)
-#pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    if (kBf16) {
-                      acc[h][j][0] = fmaf(f[2 * h][g], part[h][j][0], acc[h][j][0]);
-                      acc[h][j][1] = fmaf(f[2 * h][g], part[h][j][1], acc[h][j][1]);
-                      acc[h][j][2 % kSums] = fmaf(f[2 * h + 1][g], part[h][j][2], acc[h][j][2 % kSums]);
-                      acc[h][j][3 % kSums] = fmaf(f[2 * h + 1][g], part[h][j][3], acc[h][j][3 % kSums]);
-                    } else {  // the hi and lo columns of one row
-                      acc[h][j][0] = fmaf(f[2 * h][g] * un[j], part[h][j][0] + part[h][j][1],
-                                          acc[h][j][0]);
-                      acc[h][j][1] = fmaf(f[2 * h + 1][g] * un[j], part[h][j][2] + part[h][j][3],
-                                          acc[h][j][1]);
-                    }
-                  }
-              }
-            }
-            fetch(d);
-            ++pos;
-            ++blk;
-            if (blk == nb || pos == end) {
-              // partial sums of the tile, to their slot in the CTA that adds it
-              // up: [slice][tile][warp in the tile]
-              const int at = (unsigned)tile / (unsigned)csize, to = tile - at * csize;
-              const int nth = total < kWarps ? blk - 1 : warp - tab[2 * (crank * nt + tile)];
-              float *sl = slots + (size_t)((crank * own + at) * most + nth) * kTile * kRowsX +
-                          gr * kRowsX;
-              if (csize > 1) sl = cl.map_shared_rank(sl, to);
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int j = 0; j < kNT; ++j)
-#pragma unroll
-                  for (int i = 0; i < kSums; ++i) {
-                    // bf16: rows gr, gr + 8 and columns 2 t, 2 t + 1; fp32: the
-                    // two rows of x row t
-                    const int row = 16 * h + 8 * (kBf16 ? i >> 1 : i);
-                    const int col = kBf16 ? 8 * j + 2 * t + (i & 1) : 4 * j + t;
-                    float v = acc[h][j][i];
-                    if (kr) v += sl[row * kRowsX + col];
-                    sl[row * kRowsX + col] = v;
-                    acc[h][j][i] = 0.f;
-                  }
-              blk = 0;
-              ++tile;
+              w0[i] = a[i];
+              w0[i + 4] = b[i];
+              w1[i] = c[i];
+              w1[i + 4] = d[i];
             }
           }
+          // (the slot that is filled now was read a turn ago, and every lane
+          // has passed the barrier above since)
+          fetch();
+          float part[kNT][4], un[kNT];
+          if (!kBf16)
+#pragma unroll
+            for (int j = 0; j < kNT; ++j) un[j] = side[blk * kRowsX + 4 * j + t];
+          const int g0 = (b_lo + blk) * kSc;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            constexpr int kSteps = kGroup / 32;
+            const int g = i / kSteps;
+            if (i % kSteps == 0) {
+#pragma unroll
+              for (int j = 0; j < kNT; ++j) {
+                float2 c = make_float2(0.f, 0.f);
+                if (kBf16)
+                  c = *reinterpret_cast<const float2 *>(side + (blk * kSc + g) * kCols + 8 * j +
+                                                        2 * t);
+                part[j][0] = part[j][2] = c.x;
+                part[j][1] = part[j][3] = c.y;
+              }
+            }
+            uint32_t c0[4], c1[4];
+            codes<kBf16>(w0[i], c0);
+            codes<kBf16>(w1[i], c1);
+#pragma unroll
+            for (int j = 0; j < kNT; ++j) {
+              const uint4 x4 = *reinterpret_cast<const uint4 *>(xl[j] + blk * kXBlock + i * 64);
+              mma<kBf16>(part[j], c0[0], c1[0], c0[1], c1[1], x4.x, x4.y, part[j]);
+              mma<kBf16>(part[j], c0[2], c1[2], c0[3], c1[3], x4.z, x4.w, part[j]);
+            }
+            if ((i + 1) % kSteps == 0) {
+              // (a group behind the last one has zeros of x against any scale)
+              const int gi = min(g0 + g, groups - 1);
+              const float f0 = __half2float(s0p[gi]), f1 = __half2float(s1p[gi]);
+#pragma unroll
+              for (int j = 0; j < kNT; ++j) {
+                if (kBf16) {
+                  acc[j][0] = fmaf(f0, part[j][0], acc[j][0]);
+                  acc[j][1] = fmaf(f0, part[j][1], acc[j][1]);
+                  acc[j][2 % kSums] = fmaf(f1, part[j][2], acc[j][2 % kSums]);
+                  acc[j][3 % kSums] = fmaf(f1, part[j][3], acc[j][3 % kSums]);
+                } else {  // the hi and lo columns of one row
+                  acc[j][0] = fmaf(f0 * un[j], part[j][0] + part[j][1], acc[j][0]);
+                  acc[j][1] = fmaf(f1 * un[j], part[j][2] + part[j][3], acc[j][1]);
+                }
+              }
+            }
+          }
+          ++blk;
+          if (blk == nb || pos + 1 == end) {
+            // partial sums of the tile, to their slot in the CTA that adds it
+            // up: [slice][tile][warp in the tile]
+            const int at = (unsigned)tile / (unsigned)csize, to = tile - at * csize;
+            const int nth = total < kWarps ? blk - 1 : warp - tab[2 * (crank * nt + tile)];
+            float *sl = slots + (size_t)((crank * own + at) * most + nth) * kTile * kRowsX +
+                        gr * kRowsX;
+            if (csize > 1) sl = cl.map_shared_rank(sl, to);
+#pragma unroll
+            for (int j = 0; j < kNT; ++j)
+#pragma unroll
+              for (int i = 0; i < kSums; ++i) {
+                // bf16: rows gr, gr + 8 and columns 2 t, 2 t + 1; fp32: the two
+                // rows of x row t
+                const int row = 8 * (kBf16 ? i >> 1 : i);
+                const int col = kBf16 ? 8 * j + 2 * t + (i & 1) : 4 * j + t;
+                if (col < nr) {
+                  float v = acc[j][i];
+                  if (kr) v += sl[row * kRowsX + col];
+                  sl[row * kRowsX + col] = v;
+                }
+                acc[j][i] = 0.f;
+              }
+            blk = 0;
+            ++tile;
+            if (pos + 1 < end) scales_of();
+          }
         }
+        cp_async_wait<0>();
       }
 
       // ---- the sum over slices and warps, tiles crank, crank + csize, ...
@@ -525,7 +533,7 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1)
       else
         __syncthreads();
       for (int e = tid; e < own * kTile * nr; e += kThreads) {
-        const int c = (unsigned)e / (unsigned)nr, r = e - c * nr;  // weight row, row of x
+        const int r = (unsigned)e / (unsigned)(own * kTile), c = e - r * own * kTile;
         const int at = c / kTile, tile = at * csize + crank, n = (t0 + tile) * kTile + c % kTile;
         if (tile >= nt || n >= P.N) continue;
         float sum = 0.f;
@@ -547,37 +555,49 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1)
 }
 
 struct Plan {
-  int nt, csize, clusters, round_tiles, round_blocks, slots;
+  int nt, csize, clusters, round_tiles, round_blocks, slots, columns, sc_shared;
   size_t smem;
 };
 
-// Cluster size and rounds for the shape.  The cost of a CTA, in blocks of 32
-// weight rows: its list, its share of x, and for a cluster its two barriers.
+// Cluster size and rounds for the shape.  The cost of a CTA, in blocks: its
+// list, its share of x, and for a cluster its two barriers.
 // `most`: clusters of 1, 2, 4, 8 CTAs that the GPU runs at once.
 Plan make_plan(int rows, int N, int K, int group, bool bf16, const int (&most)[4]) {
   Plan p = {};
   const int cols = bf16 ? rows : 2 * rows;
   p.nt = cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
-  const int rows_x = bf16 ? 8 * p.nt : 4 * p.nt;
+  p.columns = cols < 8 * p.nt ? cols : 8 * p.nt;
+  const int rows_x = bf16 ? 8 * p.nt : 4 * p.nt, warps = warps_of(p.nt);
   const int tiles = (N + kTile - 1) / kTile, blocks = (K + kBlock - 1) / kBlock;
-  // shared memory of cluster size c, rt tiles and rb blocks a round
+  const int groups = K / group;
+  // shared memory of cluster size c, rt tiles and rb blocks a round; the
+  // scales where they fit
   auto bytes = [&](int c, int rt, int rb) {
     const int last = tiles % rt;  // tiles of the last round, if fewer
-    const auto slots = [&](int n) { return n ? c * ((n + c - 1) / c) * most_warps(warps_of(p.nt), n, rb) : 0; };
+    const auto slots = [&](int n) {
+      return n ? c * ((n + c - 1) / c) * most_warps(warps, n, rb) : 0;
+    };
     p.slots = slots(rt) > slots(last) ? slots(rt) : slots(last);
-    return (size_t)p.slots * kTile * rows_x * 4 + (size_t)8 * p.nt * ((size_t)rb * 256 + 64) +
-           (size_t)rb * 4 * (bf16 ? (kBlock / group) * 8 * p.nt : rows_x) + (size_t)2 * c * rt;
+    const size_t need = (size_t)warps * depth_of(p.nt) * kBlockBytes +
+                        (size_t)p.slots * kTile * rows_x * 4 +
+                        (size_t)p.columns * ((size_t)rb * kXBlock + 64) +
+                        (size_t)rb * 4 * (bf16 ? (kBlock / group) * 8 * p.nt : rows_x) +
+                        (((size_t)2 * c * rt + 31) & ~(size_t)15);
+    const size_t sc = (((size_t)rt * kTile * groups * 2) + 15) & ~(size_t)15;
+    p.sc_shared = need + sc <= kSmemMax;
+    return need + (p.sc_shared ? sc : 0);
   };
   double best = 1e300;
   for (int i = 0; i < 4; ++i) {
     const int c = 1 << i, clusters = most[i] < tiles ? most[i] : tiles;
     const int rt = (tiles + clusters - 1) / clusters, rb = (blocks + c - 1) / c;
-    double cost = (double)rt * rb + kXCost * rows_x * rb + (c > 1 ? kClusterCost : 0.0);
+    double cost = (double)rt * rb + kXCost * (rows < rows_x ? rows : rows_x) * rb +
+                  (c > 1 ? kClusterCost : 0.0);
     if (bytes(c, rt, rb) > kSmemMax) cost += 1e100;  // in rounds: the largest cluster
     if (cost < best || (cost >= 1e100 && best >= 1e100)) {
       best = cost;
       p.csize = c;
-      p.clusters = clusters;
+      p.clusters = (tiles + rt - 1) / rt;
       p.round_tiles = rt;
       p.round_blocks = rb;
     }
@@ -681,7 +701,7 @@ cudaError_t launch_quant_linear(const void *x, const unsigned char *qw,
   const Plan p = make_plan(rows, N, K, group, bf16, most);
   const QuantArgs a{x, qw, static_cast<const __half *>(scales), y, rows, N, K,
                     (N + kTile - 1) / kTile, (K + kBlock - 1) / kBlock, p.round_tiles, p.round_blocks,
-                    p.csize, p.slots};
+                    p.csize, p.slots, p.columns, p.sc_shared};
   return bf16 ? by_columns<true>(group, a, p, stream) : by_columns<false>(group, a, p, stream);
 }
 
