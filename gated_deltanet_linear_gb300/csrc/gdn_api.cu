@@ -297,14 +297,16 @@ int gdn_prefill_timeouts(unsigned int *count) {
 int gdn_wait_timeouts(unsigned int *count) {
   if (!count) return GDN_EINVAL;
   cudaGetLastError();
-  unsigned int a = 0, b = 0, c = 0;
+  unsigned int a = 0, b = 0, c = 0, d = 0;
   const int r = status_of(gdn::prefill_timeouts(&a));
   if (r) return r;
   const int r2 = status_of(gdn::steps_timeouts(&b));
   if (r2) return r2;
   const int r3 = status_of(gdn::linattn_timeouts(&c));
   if (r3) return r3;
-  *count = a + b + c;
+  const int r4 = status_of(gdn::quant_timeouts(&d));
+  if (r4) return r4;
+  *count = a + b + c + d;
   return GDN_OK;
 }
 

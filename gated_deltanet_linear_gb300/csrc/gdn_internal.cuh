@@ -101,6 +101,12 @@ cudaError_t launch_quant_linear(const void *x, const unsigned char *qw,
                                 const void *scales, void *y, int rows, int N,
                                 int K, int group, bool bf16,
                                 cudaStream_t stream);
+// The form for many rows of x (called by launch_quant_linear).
+cudaError_t launch_quant_linear_wide(const void *x, const unsigned char *qw, const void *scales,
+                                     void *y, int rows, int N, int K, int group, bool bf16,
+                                     cudaStream_t stream);
+// Threads of it that gave up a wait for their products.
+cudaError_t quant_timeouts(unsigned int *count);
 
 // Chunked tensor-core prefill (defined in gdn_prefill.cu).
 size_t prefill_workspace_bytes(int B, int kh, int vh, int T, int chunk,

@@ -1,13 +1,14 @@
 // Projections with 4-bit weights: y[r][n] = sum_k x[r][k] w[n][k],
-// w[n][k] = code[n][k] * scale[n][k / group], for few rows of x.
+// w[n][k] = code[n][k] * scale[n][k / group], for few rows of x
+// (up to 8 of fp32, 16 of bf16; gdn_quant_wide.cu has the form for more).
 //
 // Bound by reading the weights (half a byte each); the arithmetic runs on
 // mma.sync m16n8k16 so that it stays below that: A is 16 weight rows (codes as
 // 16-bit floats, exact), B the rows of x, and the fp32 products of one group
 // are multiplied by the group's scale and added up in fp32.
-// (A tcgen05 product would put the codes through shared memory or tensor
-// memory first, and its 128-row tiles leave too few of them to split over the
-// SMs; a handful of columns does not pay for that.)
+// (A tcgen05 product puts the codes through shared memory first, and its
+// 128-row tiles leave too few of them to split over the SMs; a handful of
+// columns does not pay for that.)
 //
 //   fp32 x   two columns per row: x 2^e = hi + lo in fp16 (22 bits; e by row
 //            and block of 128, so that the largest element is in [2^14, 2^15))
@@ -27,7 +28,7 @@
 // are one register, 1 and 5 the next, ...), and x is put into shared memory in
 // that order.
 //
-// Work split.  One CTA of 16 (many columns: 8) warps per SM; a CTA, or a cluster
+// Work split.  One CTA of 16 warps per SM; a CTA, or a cluster
 // of up to 8 that cut K between them (few tiles, or much x to convert), takes a
 // range of 16-row tiles.  Inside a CTA the (tile, block) pairs are one list, cut
 // evenly over the warps whatever the sizes.  At the end of a tile, or of its
@@ -52,14 +53,12 @@ namespace gdn {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-// Warps of a CTA: 16, or 8 where the sums of 32 columns need the registers.
-__host__ __device__ constexpr int warps_of(int n8) { return n8 > 2 ? 8 : 16; }
+constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kBlock = 256;   // k elements of a block
 constexpr int kTile = 16;     // weight rows of a tile
 constexpr int kBlockBytes = kTile * kBlock / 2;
 constexpr int kXBlock = kBlock * 2;  // bytes of a block of a column of x
-// Blocks of a warp's ring.
-__host__ __device__ constexpr int depth_of(int n8) { return n8 > 2 ? 4 : 3; }
+constexpr int kDepth = 3;  // blocks of a warp's ring
 constexpr int kSmemMax = 220 * 1024;
 // Costs of make_plan(), relative to a block.
 constexpr double kXCost = 0.1, kClusterCost = 12.0;
@@ -92,14 +91,13 @@ __device__ __forceinline__ void slice(const QuantArgs &P, int csize, int rank, i
 }
 
 // The most warps that share a tile, of nt tiles and at most `blocks` blocks.
-__host__ __device__ inline int most_warps(int warps, int nt, int blocks) {
-  int m = (warps + nt - 1) / nt + 1;
+__host__ __device__ inline int most_warps(int nt, int blocks) {
+  int m = (kWarps + nt - 1) / nt + 1;
   if (m > blocks) m = blocks;
-  return m < warps ? m : warps;
+  return m < kWarps ? m : kWarps;
 }
 
 // Warp w's share [share(w), share(w + 1)) of a list of `total` pairs.
-template <int kWarps>
 __device__ __forceinline__ int share(unsigned total, int w) {
   return (int)((unsigned long long)total * w / kWarps);
 }
@@ -189,14 +187,12 @@ __device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
 }
 
 template <bool kBf16, int kNT, int kGroup>
-__global__ void __launch_bounds__(32 * warps_of(kNT), 1)
+__global__ void __launch_bounds__(kThreads, 1)
     quant_linear_kernel(const QuantArgs P) {
   using T = typename std::conditional<kBf16, __nv_bfloat16, float>::type;
-  constexpr int kWarps = warps_of(kNT), kThreads = 32 * kWarps;
   constexpr int kCols = 8 * kNT;
   constexpr int kRowsX = kBf16 ? kCols : kCols / 2;  // rows of x of a pass
   constexpr int kSc = kBlock / kGroup;               // scales of a block
-  constexpr int kDepth = depth_of(kNT);
   constexpr int kSums = kBf16 ? 4 : 2;               // of a lane and m16n8 tile
   extern __shared__ __align__(16) unsigned char smem[];
   const cg::cluster_group cl = cg::this_cluster();
@@ -236,19 +232,19 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1)
   const size_t wrow = (size_t)P.K / 2;
   const int groups = P.K / kGroup;
 
-  for (int r0 = 0; r0 < P.rows; r0 += kRowsX) {
-    const int nr = min(kRowsX, P.rows - r0);
+  const int nr = P.rows;  // at most kRowsX
+  {
     for (int t0 = cluster * P.round_tiles; t0 < P.tiles; t0 += clusters * P.round_tiles) {
       const int nt = min(P.round_tiles, P.tiles - t0);
       const int own = (unsigned)(nt + csize - 1) / (unsigned)csize;  // tiles a CTA adds up
-      const int most = most_warps(kWarps, nt, P.round_blocks);
+      const int most = most_warps(nt, P.round_blocks);
       for (int kr = 0; kr < P.blocks; kr += csize * P.round_blocks) {
         int b_lo, nb;
         slice(P, csize, crank, b_lo, nb);
         b_lo += kr;
         const unsigned total = nt * nb;
-        int pos = share<kWarps>(total, warp);
-        const int end = share<kWarps>(total, warp + 1);
+        int pos = share(total, warp);
+        const int end = share(total, warp + 1);
 
         // ---- weights: the next block of this warp's list into its ring.  Lane
         // l copies 16-byte chunk l & 7 of rows (l >> 3) + 4 i; rows and chunks
@@ -304,7 +300,7 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1)
         // ---- x: this slice of the rows in the order of use; half a warp to
         // 128 elements of a row.  The first part is read before the weights
         // are asked for.
-        if (kr || t0 != cluster * P.round_tiles || r0) __syncthreads();  // readers are done
+        if (kr || t0 != cluster * P.round_tiles) __syncthreads();  // readers are done
         {
           const int p = lane & 15, halves = 2 * nb;
           int b = 2 * warp + (lane >> 4), r = 0;
@@ -321,7 +317,7 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1)
           auto read = [&]() {
             Part x = {};
             const int k = b_lo * kBlock + b * 128 + 8 * p;
-            if (r < nr && k < P.K) load8(static_cast<const T *>(P.x) + (size_t)(r0 + r) * P.K + k, x.v);
+            if (r < nr && k < P.K) load8(static_cast<const T *>(P.x) + (size_t)r * P.K + k, x.v);
             return x;
           };
           // (both halves run the same number of turns: shuffles inside)
@@ -542,14 +538,14 @@ __global__ void __launch_bounds__(32 * warps_of(kNT), 1)
           const int cnt = tab[2 * (q * nt + tile) + 1];
           for (int w = 0; w < cnt; ++w, sl += kTile * kRowsX) sum += *sl;
         }
-        const size_t out = (size_t)(r0 + r) * P.N + n;
+        const size_t out = (size_t)r * P.N + n;
         if (kBf16)
           static_cast<__nv_bfloat16 *>(P.y)[out] = __float2bfloat16_rn(sum);
         else
           static_cast<float *>(P.y)[out] = sum;
       }
       // the slots are read
-      if (csize > 1 && (r0 + kRowsX < P.rows || t0 + clusters * P.round_tiles < P.tiles)) cl.sync();
+      if (csize > 1 && t0 + clusters * P.round_tiles < P.tiles) cl.sync();
     }
   }
 }
@@ -565,9 +561,9 @@ struct Plan {
 Plan make_plan(int rows, int N, int K, int group, bool bf16, const int (&most)[4]) {
   Plan p = {};
   const int cols = bf16 ? rows : 2 * rows;
-  p.nt = cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
-  p.columns = cols < 8 * p.nt ? cols : 8 * p.nt;
-  const int rows_x = bf16 ? 8 * p.nt : 4 * p.nt, warps = warps_of(p.nt);
+  p.nt = cols <= 8 ? 1 : 2;
+  p.columns = cols;
+  const int rows_x = bf16 ? 8 * p.nt : 4 * p.nt;
   const int tiles = (N + kTile - 1) / kTile, blocks = (K + kBlock - 1) / kBlock;
   const int groups = K / group;
   // shared memory of cluster size c, rt tiles and rb blocks a round; the
@@ -575,10 +571,10 @@ Plan make_plan(int rows, int N, int K, int group, bool bf16, const int (&most)[4
   auto bytes = [&](int c, int rt, int rb) {
     const int last = tiles % rt;  // tiles of the last round, if fewer
     const auto slots = [&](int n) {
-      return n ? c * ((n + c - 1) / c) * most_warps(warps, n, rb) : 0;
+      return n ? c * ((n + c - 1) / c) * most_warps(n, rb) : 0;
     };
     p.slots = slots(rt) > slots(last) ? slots(rt) : slots(last);
-    const size_t need = (size_t)warps * depth_of(p.nt) * kBlockBytes +
+    const size_t need = (size_t)kWarps * kDepth * kBlockBytes +
                         (size_t)p.slots * kTile * rows_x * 4 +
                         (size_t)p.columns * ((size_t)rb * kXBlock + 64) +
                         (size_t)rb * 4 * (bf16 ? (kBlock / group) * 8 * p.nt : rows_x) +
@@ -591,7 +587,7 @@ Plan make_plan(int rows, int N, int K, int group, bool bf16, const int (&most)[4
   for (int i = 0; i < 4; ++i) {
     const int c = 1 << i, clusters = most[i] < tiles ? most[i] : tiles;
     const int rt = (tiles + clusters - 1) / clusters, rb = (blocks + c - 1) / c;
-    double cost = (double)rt * rb + kXCost * (rows < rows_x ? rows : rows_x) * rb +
+    double cost = (double)rt * rb + kXCost * rows * rb +
                   (c > 1 ? kClusterCost : 0.0);
     if (bytes(c, rt, rb) > kSmemMax) cost += 1e100;  // in rounds: the largest cluster
     if (cost < best || (cost >= 1e100 && best >= 1e100)) {
@@ -619,7 +615,7 @@ cudaError_t launch(const QuantArgs &a, const Plan &p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.clusters * p.csize));
-  cfg.blockDim = dim3(32 * warps_of(kNT));
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = p.smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -656,7 +652,7 @@ cudaError_t cluster_counts(int (&most)[4]) {
     for (int i = 0; i < 4; ++i) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(8);
-      cfg.blockDim = dim3(32 * warps_of(1));
+      cfg.blockDim = dim3(kThreads);
       cfg.dynamicSmemBytes = kSmemMax;
       cudaLaunchAttribute attr;
       attr.id = cudaLaunchAttributeClusterDimension;
@@ -683,9 +679,8 @@ cudaError_t by_group(int group, const QuantArgs &a, const Plan &p, cudaStream_t 
 
 template <bool kBf16>
 cudaError_t by_columns(int group, const QuantArgs &a, const Plan &p, cudaStream_t stream) {
-  return p.nt == 1   ? by_group<kBf16, 1>(group, a, p, stream)
-         : p.nt == 2 ? by_group<kBf16, 2>(group, a, p, stream)
-                     : by_group<kBf16, 4>(group, a, p, stream);
+  return p.nt == 1 ? by_group<kBf16, 1>(group, a, p, stream)
+                   : by_group<kBf16, 2>(group, a, p, stream);
 }
 
 }  // namespace
@@ -695,6 +690,10 @@ cudaError_t launch_quant_linear(const void *x, const unsigned char *qw,
                                 int K, int group, bool bf16,
                                 cudaStream_t stream) {
   if (rows == 0 || N == 0) return cudaSuccess;
+  // more than 16 columns: on 128-row products (64 rows of 10240 x 5120 took 54
+  // us here with 32 columns at a time, 32 rows 27)
+  if ((bf16 ? rows : 2 * rows) > 16)
+    return launch_quant_linear_wide(x, qw, scales, y, rows, N, K, group, bf16, stream);
   int most[4];
   const cudaError_t e = cluster_counts(most);
   if (e != cudaSuccess) return e;
