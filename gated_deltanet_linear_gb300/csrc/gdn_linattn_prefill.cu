@@ -356,42 +356,6 @@ __host__ __device__ constexpr uint32_t kstep(int ks) {
   return (uint32_t)((ks >> 2) * 1024 + (ks & 3) * 32);
 }
 
-// The products are issued by a converged warp, one elected lane executing:
-// the operand addresses stay in uniform registers.  (Issued by lane 0 of a
-// diverged warp, each instruction took about 90 cycles.)
-__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint64_t a, uint64_t b,
-                                       uint32_t id, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(acc), "r"(one));
-}
-__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a, uint64_t b,
-                                       uint32_t id, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(acc), "r"(one));
-}
-__device__ __forceinline__ void commit_one(uint32_t one, uint32_t mbar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::
-          "r"(mbar),
-      "r"(one)
-      : "memory");
-}
-__device__ __forceinline__ uint32_t elect() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(r));
-  return r;
-}
-
 // ------------------------------------------------------------------ kernel
 
 template <bool kBf16, bool kLocal>

@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_wide_kernel(const WideArgs 
   else
     __syncthreads();
   fence_after_sync();
-  const uint32_t tmem = *slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *slot, 0);
 
   const int s_lo = (int)((long long)P.stages * crank / csize);
   const int ns = (int)((long long)P.stages * (crank + 1) / csize) - s_lo;
@@ -155,132 +155,131 @@ __global__ void __launch_bounds__(kThreads, 1) quant_wide_kernel(const WideArgs 
     float acc[kCols];
 #pragma unroll
     for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
-    uint4 w;
-    float xv[kParts][8];
-    // scales of the stage whose products are collected, of the next one, and of
-    // the one in the registers above
-    __half sc0[kGroups] = {}, sc1[kGroups] = {}, sc2[kGroups] = {};
-    // stage s of this slice into registers
-    auto fetch = [&](int s) {
+    // Two stages of this slice in registers, ahead of use.
+    uint4 w[2];
+    float xv[2][kParts][8];
+    __half sn[2][kGroups];
+    // scales of the two stages whose products are under way
+    __half sc[2][kGroups];
+    auto fetch = [&](int u, int s) {
       const int k0 = (s_lo + s) * kStage;
       // (a group behind the last one has zeros of x against any scale)
 #pragma unroll
       for (int g = 0; g < kGroups; ++g)
-        sc2[g] = __ldg(sp + min((s_lo + s) * kGroups + g, groups - 1));
-      w = make_uint4(0, 0, 0, 0);
-      if (k0 + 32 * piece < P.K) w = __ldg(reinterpret_cast<const uint4 *>(wp + k0 / 2));
+        sn[u][g] = __ldg(sp + min((s_lo + s) * kGroups + g, groups - 1));
+      w[u] = make_uint4(0, 0, 0, 0);
+      if (k0 + 32 * piece < P.K) w[u] = __ldg(reinterpret_cast<const uint4 *>(wp + k0 / 2));
 #pragma unroll
       for (int i = 0; i < kParts; ++i) {
         const int e = tid + i * kThreads, r = e >> 4, k = k0 + 8 * (e & 15);
         const bool on = r < nr && k < P.K;
         const T *p = static_cast<const T *>(P.x) + (on ? (size_t)(r0 + r) * P.K + k : 0);
-        if constexpr (kBf16) {
-          const uint4 u = on ? __ldg(reinterpret_cast<const uint4 *>(p)) : make_uint4(0, 0, 0, 0);
-          xv[i][0] = __uint_as_float(u.x);  // as they are, two to a word
-          xv[i][1] = __uint_as_float(u.y);
-          xv[i][2] = __uint_as_float(u.z);
-          xv[i][3] = __uint_as_float(u.w);
-        } else {
-          const float4 a = on ? __ldg(reinterpret_cast<const float4 *>(p)) : make_float4(0, 0, 0, 0);
-          const float4 b = on ? __ldg(reinterpret_cast<const float4 *>(p) + 1) : make_float4(0, 0, 0, 0);
-          xv[i][0] = a.x; xv[i][1] = a.y; xv[i][2] = a.z; xv[i][3] = a.w;
-          xv[i][4] = b.x; xv[i][5] = b.y; xv[i][6] = b.z; xv[i][7] = b.w;
+        const uint4 z = make_uint4(0, 0, 0, 0);
+        const uint4 a = on ? __ldg(reinterpret_cast<const uint4 *>(p)) : z;
+        const uint32_t q[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) xv[u][i][j] = __uint_as_float(q[j]);  // bf16: two to a word
+        if constexpr (!kBf16) {
+          const uint4 b = on ? __ldg(reinterpret_cast<const uint4 *>(p) + 1) : z;
+          const uint32_t v[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) xv[u][i][4 + j] = __uint_as_float(v[j]);
         }
       }
     };
     // Stage counts run on over the passes (barriers and buffers go by them); a
     // pass starts with both buffers free.
     const uint32_t base = done;
-    if (ns > 0) fetch(0);
-    for (int s = 0; s < ns + 2; ++s) {
-      if (s >= 2) {  // buffers of stage s - 2 are free, its accumulators full
-        const uint32_t before = base + (uint32_t)(s - 2);  // index over all passes
-        failed |= !mbar_wait(bar + 8 * (before & 1), (before >> 1) & 1u, kWaitLimit);
-        fence_after_sync();
+    if (ns > 0) fetch(0, 0);
+    if (ns > 1) fetch(1, 1);
+    for (int s0 = 0; s0 < ns + 2; s0 += 2) {
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          float d[kCols];
-          tmem_ld<kCols>(tmem + ((uint32_t)(32 * quad) << 16) +
-                             (uint32_t)(((before & 1) * kGroups + g) * kNC + part * kCols),
-                         d);
-          const float f = __half2float(sc0[g]);
+      for (int u = 0; u < 2; ++u) {
+        const int s = s0 + u;
+        if (s >= 2 && s < ns + 2) {
+          // stage s - 2: its buffers are free, its accumulators full
+          const uint32_t before = base + (uint32_t)(s - 2);  // index over all passes
+          failed |= !mbar_wait(bar + 8 * (before & 1), (before >> 1) & 1u, kWaitLimit);
+          fence_after_sync();
 #pragma unroll
-          for (int i = 0; i < kCols; ++i) acc[i] = fmaf(f, d[i], acc[i]);
-        }
-      }
+          for (int g = 0; g < kGroups; ++g) {
+            float d[kCols];
+            tmem_ld<kCols>(tmem + ((uint32_t)(32 * quad) << 16) +
+                               (uint32_t)(((before & 1) * kGroups + g) * kNC + part * kCols),
+                           d);
+            const float f = __half2float(sc[u][g]);
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        sc0[g] = sc1[g];
-        sc1[g] = sc2[g];
-      }
-      if (s >= ns) continue;
-      const uint32_t at = base + (uint32_t)s;
-      unsigned char *A = gb + (at & 1) * kStageBytes, *B = A + kATile;
-      const uint4 cw = w;
-      float cx[kParts][8];
-#pragma unroll
-      for (int i = 0; i < kParts; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) cx[i][j] = xv[i][j];
-      if (s + 1 < ns) fetch(s + 1);
-      {
-        const uint32_t word[4] = {cw.x, cw.y, cw.z, cw.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // (two pieces of a row lie in tiles that share banks: other order)
-          const int q = i ^ (piece >> 1);
-          uint32_t r[4];
-          codes(q == 0 ? word[0] : q == 1 ? word[1] : q == 2 ? word[2] : word[3], r);
-          *reinterpret_cast<uint4 *>(A + sw128_off(kRowsW, arow, 32 * piece + 8 * q, 2)) =
-              make_uint4(r[0], r[1], r[2], r[3]);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kParts; ++i) {
-        const int e = tid + i * kThreads;
-        unsigned char *dst = B + sw128_off(kNC, e >> 4, 8 * (e & 15), 2);
-        if constexpr (kBf16) {
-          const uint32_t u[4] = {__float_as_uint(cx[i][0]), __float_as_uint(cx[i][1]),
-                                 __float_as_uint(cx[i][2]), __float_as_uint(cx[i][3])};
-          *reinterpret_cast<uint4 *>(dst) =
-              make_uint4(__byte_perm(u[0], u[2], 0x5410), __byte_perm(u[0], u[2], 0x7632),
-                         __byte_perm(u[1], u[3], 0x5410), __byte_perm(u[1], u[3], 0x7632));
-        } else {
-#pragma unroll
-          for (int term = 0; term < 3; ++term, dst += kBTile) {
-            uint32_t o[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const __nv_bfloat162 h = __floats2bfloat162_rn(cx[i][j], cx[i][j + 4]);
-              const float2 f = __bfloat1622float2(h);
-              cx[i][j] -= f.x;
-              cx[i][j + 4] -= f.y;
-              o[j] = bits(h);
-            }
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+            for (int i = 0; i < kCols; ++i) acc[i] = fmaf(f, d[i], acc[i]);
           }
         }
-      }
-      fence_proxy_async();
-      fence_before_sync();
-      __syncthreads();
-      if (tid == 0) {
-        fence_after_sync();
-        const uint32_t a = sb + (at & 1) * kStageBytes, b = a + kATile;
-        constexpr uint32_t id = idesc(kFmtBF16, kRowsW, kNC);
+        if (s >= ns) continue;
+        const uint32_t at = base + (uint32_t)s;
+        unsigned char *A = gb + (at & 1) * kStageBytes, *B = A + kATile;
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          const uint32_t d = tmem + (uint32_t)(((at & 1) * kGroups + g) * kNC);
+        for (int g = 0; g < kGroups; ++g) sc[u][g] = sn[u][g];
+        {
+          const uint32_t word[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
 #pragma unroll
-          for (int term = 0; term < kTerms; ++term)
-#pragma unroll
-            for (int k = 0; k < kGroup / 16; ++k) {
-              const int ks = g * (kGroup / 16) + k;
-              mma_bf16(d, desc_kstep(a, kRowsW, ks), desc_kstep(b + term * kBTile, kNC, ks), id,
-                       term > 0 || k > 0);
-            }
+          for (int i = 0; i < 4; ++i) {
+            // (two pieces of a row lie in tiles that share banks: other order)
+            const bool odd = piece >> 1;
+            uint32_t r[4];
+            codes(odd ? word[i ^ 1] : word[i], r);
+            *reinterpret_cast<uint4 *>(
+                A + sw128_off(kRowsW, arow, 32 * piece + 8 * (odd ? i ^ 1 : i), 2)) =
+                make_uint4(r[0], r[1], r[2], r[3]);
+          }
         }
-        commit(bar + 8 * (at & 1));
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+          const int e = tid + i * kThreads;
+          unsigned char *dst = B + sw128_off(kNC, e >> 4, 8 * (e & 15), 2);
+          float(&x)[8] = xv[u][i];
+          if constexpr (kBf16) {
+            const uint32_t q[4] = {__float_as_uint(x[0]), __float_as_uint(x[1]),
+                                   __float_as_uint(x[2]), __float_as_uint(x[3])};
+            *reinterpret_cast<uint4 *>(dst) =
+                make_uint4(__byte_perm(q[0], q[2], 0x5410), __byte_perm(q[0], q[2], 0x7632),
+                           __byte_perm(q[1], q[3], 0x5410), __byte_perm(q[1], q[3], 0x7632));
+          } else {
+#pragma unroll
+            for (int term = 0; term < 3; ++term, dst += kBTile) {
+              uint32_t o[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(x[j], x[j + 4]);
+                const float2 f = __bfloat1622float2(h);
+                x[j] -= f.x;
+                x[j + 4] -= f.y;
+                o[j] = bits(h);
+              }
+              *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+          }
+        }
+        if (s + 2 < ns) fetch(u, s + 2);
+        fence_proxy_async();
+        fence_before_sync();
+        __syncthreads();
+        if (warp == 0) {
+          fence_after_sync();
+          const uint32_t one = elect();
+          const uint32_t a = sb + (at & 1) * kStageBytes, b = a + kATile;
+          constexpr uint32_t id = idesc(kFmtBF16, kRowsW, kNC);
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) {
+            const uint32_t d = tmem + (uint32_t)(((at & 1) * kGroups + g) * kNC);
+#pragma unroll
+            for (int term = 0; term < kTerms; ++term)
+#pragma unroll
+              for (int k = 0; k < kGroup / 16; ++k) {
+                const int ks = g * (kGroup / 16) + k;
+                mma_ss(one, d, desc_kstep(a, kRowsW, ks), desc_kstep(b + term * kBTile, kNC, ks),
+                       id, term > 0 || k > 0);
+              }
+          }
+          commit_one(one, bar + 8 * (at & 1));
+        }
       }
     }
     done = base + (uint32_t)ns;
