@@ -61,7 +61,7 @@ constexpr int kXBlock = kBlock * 2;  // bytes of a block of a column of x
 constexpr int kDepth = 3;  // blocks of a warp's ring
 constexpr int kSmemMax = 220 * 1024;
 // Costs of make_plan(), relative to a block.
-constexpr double kXCost = 0.1, kClusterCost = 12.0;
+constexpr double kXCost = 0.1, kClusterCost[4] = {0.0, 5.0, 8.0, 20.0};
 
 struct QuantArgs {
   const void *x;
@@ -250,9 +250,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         // l copies 16-byte chunk l & 7 of rows (l >> 3) + 4 i; rows and chunks
         // behind the end are zeros.
         const int crow = lane >> 3, chunk = lane & 7;
-        int lpos = pos, lb = 0, lt = 0, ld = 0;
+        const uint32_t step = 4 * (uint32_t)wrow;  // four rows
+        // (row & 7 of rows crow + 4 i alternates between two values)
+        const uint32_t d0 = ring + crow * 128 + ((chunk ^ crow) << 4);
+        const uint32_t d1 = ring + (crow + 4) * 128 + ((chunk ^ (crow + 4)) << 4);
+        int lpos = pos, lb = 0, lt = 0;
+        uint32_t ld = 0;
         const uint8_t *wp = nullptr;
-        int left = 0;  // rows from crow on
+        int left = 0;  // rows of the tile from crow on
         auto aim = [&]() {
           const int n0 = (t0 + lt) * kTile + crow;
           left = P.N - n0;
@@ -266,13 +271,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         auto fetch = [&]() {
           if (lpos < end) {
-            const int in = (b_lo + lb) * kBlock + 32 * chunk < P.K ? 16 : 0;
-            const uint32_t dst = ring + ld * kBlockBytes;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = crow + 4 * i;
-              cp_async16(dst + r * 128 + ((chunk ^ (r & 7)) << 4),
-                         4 * i < left && in ? wp + (size_t)i * 4 * wrow : P.qw, 4 * i < left ? in : 0);
+            if ((t0 + lt + 1) * kTile <= P.N && (b_lo + lb + 1) * kBlock <= P.K) {
+              cp_async16(d0 + ld, wp, 16);
+              cp_async16(d1 + ld, wp + step, 16);
+              cp_async16(d0 + ld + 1024, wp + 2 * step, 16);
+              cp_async16(d1 + ld + 1024, wp + 3 * step, 16);
+            } else {
+              const int in = (b_lo + lb) * kBlock + 32 * chunk < P.K ? 16 : 0;
+#pragma unroll 1
+              for (int i = 0; i < 4; ++i) {
+                const int bytes = 4 * i < left ? in : 0;
+                cp_async16((i & 1 ? d1 : d0) + ld + 1024 * (i >> 1), bytes ? wp + i * step : P.qw,
+                           bytes);
+              }
             }
             if (++lb == nb) {
               lb = 0;
@@ -282,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               wp += kBlock / 2;
             }
             ++lpos;
-            ld = ld + 1 == kDepth ? 0 : ld + 1;
+            ld = ld == (kDepth - 1) * kBlockBytes ? 0 : ld + kBlockBytes;
           }
           cp_async_commit();
         };
@@ -323,11 +334,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           // (both halves run the same number of turns: shuffles inside)
           const int turns = (nr * halves + 2 * kWarps - 1) / (2 * kWarps);
           Part x = read();
-#pragma unroll
-          for (int d = 0; d < kDepth - 1; ++d) fetch();
-          for (int turn = 0; turn < turns; ++turn) {
+          for (int turn = 0; turn < turns || turn == 0; ++turn) {
             const int cb = b, cr = r;
             const Part c = x;
+            if (turn == 0) {
+              // The weights are asked for once the first part of x is here: a
+              // burst of weights from every SM would keep it waiting for twice
+              // the time.
+              asm volatile("" ::"f"(c.v[0]) : "memory");
+#pragma unroll
+              for (int d = 0; d < kDepth - 1; ++d) fetch();
+            }
             b += 2 * kWarps;
             wrap();
             if (turn + 1 < turns) x = read();
@@ -403,7 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < kNT; ++j)
 #pragma unroll
           for (int i = 0; i < kSums; ++i) acc[j][i] = 0.f;
-        int tile = 0, blk = 0, rd = 0;
+        int tile = 0, blk = 0;
+        uint32_t rd = 0;
         if (pos < end) {
           tile = (unsigned)pos / (unsigned)nb;
           blk = pos - tile * nb;
@@ -424,8 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (; pos < end; ++pos) {
           cp_async_wait<kDepth - 2>();
           __syncwarp();  // every lane's copies of this block have landed
-          const uint32_t st = ring + rd * kBlockBytes;
-          rd = rd + 1 == kDepth ? 0 : rd + 1;
+          const uint32_t st = ring + rd;
+          rd = rd == (kDepth - 1) * kBlockBytes ? 0 : rd + kBlockBytes;
           uint32_t w0[8], w1[8];  // rows gr, gr + 8: chunks 0..7
           {
             uint32_t a[4], b[4], c[4], d[4];
@@ -587,8 +605,7 @@ Plan make_plan(int rows, int N, int K, int group, bool bf16, const int (&most)[4
   for (int i = 0; i < 4; ++i) {
     const int c = 1 << i, clusters = most[i] < tiles ? most[i] : tiles;
     const int rt = (tiles + clusters - 1) / clusters, rb = (blocks + c - 1) / c;
-    double cost = (double)rt * rb + kXCost * rows * rb +
-                  (c > 1 ? kClusterCost : 0.0);
+    double cost = (double)rt * rb + kXCost * rows * rb + kClusterCost[i];
     if (bytes(c, rt, rb) > kSmemMax) cost += 1e100;  // in rounds: the largest cluster
     if (cost < best || (cost >= 1e100 && best >= 1e100)) {
       best = cost;
@@ -690,8 +707,9 @@ cudaError_t launch_quant_linear(const void *x, const unsigned char *qw,
                                 int K, int group, bool bf16,
                                 cudaStream_t stream) {
   if (rows == 0 || N == 0) return cudaSuccess;
-  // more than 16 columns: on 128-row products (64 rows of 10240 x 5120 took 54
-  // us here with 32 columns at a time, 32 rows 27)
+  // More than 16 columns go to products of 128 weight rows: 64 rows of bf16
+  // against 5120 x 6144 took 54 us here, 32 columns at a time, and take 23.5
+  // there; 16 rows take 14 us here (19 there).
   if ((bf16 ? rows : 2 * rows) > 16)
     return launch_quant_linear_wide(x, qw, scales, y, rows, N, K, group, bf16, stream);
   int most[4];
