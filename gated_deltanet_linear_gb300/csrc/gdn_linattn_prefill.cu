@@ -21,16 +21,18 @@
 // state that enter o are rounded to fp16 (2^-11, below o's own 2^-8), and the
 // decayed values that enter the state stay hi + lo.  The scales: q and k by
 // row, v, the decayed values and the state by column dv (the TMEM lane),
-// chosen so that the largest element lies in [2^14, 2^15); elements down to
-// 2^-17 of it keep all their bits.  The scores of row t are scaled by the
-// largest k row up to t.  The state is kept in fp32 registers: a chunk's KV
+// chosen so that the largest element lies in [2^14, 2^15) (the decayed values'
+// by the values' and a bound of the factors); elements down to 2^-17 of it keep
+// all their bits.  The scores of row t are scaled by a bound of the largest
+// |q_t| |k_s| e^{Gamma_t - Gamma_s}, s <= t, so strong decays and rows of very
+// different sizes leave them their bits.  The state is kept in fp32 registers: a chunk's KV
 // product is read out, unscaled and added, so scales may differ from chunk to
 // chunk.  Gamma is summed as two floats (48 bits), so strong decays
 // keep the small differences between near tokens.
 //
 // Roles (20 warps, one CTA per SM, persistent over (sequence, head, segment)
 // units): 8 warps A hold the state and make its operand and the two V
-// operands; 8 warps B turn the staged q and k rows into operands in place,
+// operands (the next chunk's V maxima under this one's KV product); 8 warps B turn the staged q and k rows into operands in place,
 // make P from G, and the output from QS and PV; one warp issues the products,
 // one copies rows by TMA (a chunk ahead), one computes the decay vectors.
 // All meet through mbarriers; the chunks of successive units form one
@@ -46,6 +48,7 @@
 #include <cudaTypedefs.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "gdn_internal.cuh"
 #include "gdn_tc.cuh"
@@ -72,16 +75,15 @@ constexpr uint32_t kWaitLimit = 1u << 24;
 // columns 0-63, hi 64-127, then the same of lo), so a warp converts a group by
 // itself.
 constexpr uint32_t OFF_KQ = 0, kKQ = 65536;   // by chunk parity
-constexpr uint32_t OFF_V = 131072;            // staged v rows [64][128]
-constexpr uint32_t OFF_O = 163840;            // o tile [64][128]
+constexpr uint32_t OFF_V = 131072, kV = 32768;  // staged v rows, by parity
 constexpr uint32_t OFF_P = 196608;            // P operand 64 x 64, hi, lo
 // decay vectors of a chunk, buffer it & 3, 512 floats:
 constexpr int VA = 0, VB = 64, VF = 128, VCA = 192, VCB = 256, VGH = 320,
               VGL = 384, VM = 448;
 constexpr uint32_t OFF_VEC = 212992;
 constexpr uint32_t OFF_EXP = OFF_VEC + 4 * 2048;    // row exponents [2][128]
-constexpr uint32_t OFF_LANE = OFF_EXP + 2 * 512;    // lane factors [4][2][128]
-constexpr uint32_t OFF_PV = OFF_LANE + 4 * 1024;    // exchange: V maxima
+constexpr uint32_t OFF_LANE = OFF_EXP + 2 * 512;    // column factors [4][2][128]
+constexpr uint32_t OFF_PV = OFF_LANE + 4 * 1024;    // exchange: V maxima [2][2][128]
 constexpr uint32_t OFF_PS = OFF_PV + 2048;          // exchange: state maxima
 constexpr uint32_t OFF_BAD = OFF_PS + 1024;         // first bad token [4][2][128]
 constexpr uint32_t OFF_BAR = OFF_BAD + 1024;
@@ -202,54 +204,61 @@ __device__ __forceinline__ Two shfl_up2(Two x, int d) {
   return Two{__shfl_up_sync(0xffffffffu, x.h, d), __shfl_up_sync(0xffffffffu, x.l, d)};
 }
 
-__device__ __forceinline__ uint32_t h2_bits(__half2 v) {
-  return *reinterpret_cast<uint32_t *>(&v);
+// Two floats in a register pair, and the packed operations on them.
+typedef unsigned long long F2;
+__device__ __forceinline__ F2 pack(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack(F2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 
+// The fp16 parts of two floats: hi = fp16(x) and, with kLo, lo = fp16(x - hi).
 template <bool kLo>
-__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
-  const __half2 h = __floats2half2_rn(a, b);
-  hi = h2_bits(h);
+__device__ __forceinline__ void split2(F2 v, uint32_t &hi, uint32_t &lo) {
+  const float2 x = unpack(v);
+  const __half2 h = __floats2half2_rn(x.x, x.y);
+  hi = *reinterpret_cast<const uint32_t *>(&h);
   if (kLo) {
     const float2 f = __half22float2(h);
-    lo = h2_bits(__floats2half2_rn(a - f.x, b - f.y));
+    const float2 d = unpack(fma2(pack(f.x, f.y), pack(-1.f, -1.f), v));
+    const __half2 l = __floats2half2_rn(d.x, d.y);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
   }
 }
 
-// Eight elements times s: hi parts to the 16 bytes at p, lo parts `lo_off` on.
+// Elements c0 .. c0+15 of this lane of an A operand in TMEM.
 template <bool kLo>
-__device__ __forceinline__ void put8(unsigned char *p, uint32_t lo_off, const float *x, float s) {
-  uint32_t hi[4], lo[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) split2<kLo>(x[2 * i] * s, x[2 * i + 1] * s, hi[i], lo[i]);
-  *reinterpret_cast<uint4 *>(p) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-  if (kLo) *reinterpret_cast<uint4 *>(p + lo_off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-}
-
-// Elements c0 .. c0+15 of this lane of an A operand in TMEM, times s.
-template <bool kLo>
-__device__ __forceinline__ void put16(uint32_t hi, uint32_t lo, int c0,
-                                      const float *x, float s) {
+__device__ __forceinline__ void put16(uint32_t hi, uint32_t lo, int c0, const F2 *x) {
   uint32_t h[8], l[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) split2<kLo>(x[2 * i] * s, x[2 * i + 1] * s, h[i], l[i]);
+  for (int i = 0; i < 8; ++i) split2<kLo>(x[i], h[i], l[i]);
   tmem_st8_async(hi + (uint32_t)(c0 >> 1), h);
   if (kLo) tmem_st8_async(lo + (uint32_t)(c0 >> 1), l);
 }
 
-// 32 TMEM columns of this thread's lane; tmem_wait_ld before use.
-__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&u)[32]) {
+// 16 TMEM columns of this thread's lane, as 8 pairs; tmem_wait_ld before use.
+__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&u)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31}, [%32];"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
       : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]),
         "=r"(u[6]), "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]),
-        "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
-        "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]),
-        "=r"(u[22]), "=r"(u[23]), "=r"(u[24]), "=r"(u[25]), "=r"(u[26]),
-        "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+        "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
       : "r"(taddr));
 }
 
@@ -259,6 +268,10 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&u)[N]) {
   // the loaded registers are defined only from here on
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(u[i]));
+}
+
+__device__ __forceinline__ F2 pair(const uint32_t *u) {
+  return pack(__uint_as_float(u[0]), __uint_as_float(u[1]));
 }
 
 __device__ __forceinline__ void mbar_arrive(uint32_t mbar) {
@@ -314,10 +327,6 @@ __device__ __forceinline__ void bar_pair(int quad) {  // warps w and w + 4 of A
   asm volatile("bar.sync %0, 64;" ::"r"(quad + 1) : "memory");
 }
 
-__device__ __forceinline__ void bar_b() {
-  asm volatile("bar.sync 5, %0;" ::"n"(kGroup) : "memory");
-}
-
 __device__ __forceinline__ void tma_load(uint32_t smem, const CUtensorMap *map, int h,
                                          int t0, int b, uint32_t mbar) {
   asm volatile(
@@ -325,16 +334,6 @@ __device__ __forceinline__ void tma_load(uint32_t smem, const CUtensorMap *map, 
       " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(h), "r"(t0), "r"(b), "r"(mbar)
       : "memory");
-}
-
-__device__ __forceinline__ void tma_store(const CUtensorMap *map, int h, int t0, int b,
-                                          uint32_t smem) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group"
-      " [%0, {%1, %2, %3, %4}], [%5];" ::"l"(reinterpret_cast<uint64_t>(map)),
-      "r"(0), "r"(h), "r"(t0), "r"(b), "r"(smem)
-      : "memory");
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
 // ---------------------------------------------------------------- products
@@ -356,6 +355,92 @@ __host__ __device__ constexpr uint32_t kstep(int ks) {
   return (uint32_t)((ks >> 2) * 1024 + (ks & 3) * 32);
 }
 
+// ------------------------------------------------------------ row operands
+
+// A group of 8 staged rows (8 x 512 bytes fp32, or 256 bf16) on its way to the
+// fp16 operand in the same bytes, by one warp: lane l has rows 2 i + (l >> 4)
+// and of each, with m = l & 15, columns 4 m .. + 3 and 64 + 4 m .. + 3 (fp32) or
+// 8 m .. + 7 (bf16), so that every access of a quarter warp covers whole banks.
+template <bool kBf16>
+struct RowGroup {
+  static constexpr uint32_t kRow = kBf16 ? 256 : 512;
+  F2 x[4][4];
+  float sc[4];
+  __device__ __forceinline__ void read(const unsigned char *g8, int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const unsigned char *st = g8 + (2 * i + (lane >> 4)) * kRow + (lane & 15) * 16;
+      const uint4 u = *reinterpret_cast<const uint4 *>(st);
+      const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+      if (kBf16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          x[i][j] = pack(__uint_as_float(q[j] << 16), __uint_as_float(q[j] & 0xffff0000u));
+      } else {
+        const uint4 v = *reinterpret_cast<const uint4 *>(st + 256);
+        const uint32_t z[4] = {v.x, v.y, v.z, v.w};
+        x[i][0] = pair(q);
+        x[i][1] = pair(q + 2);
+        x[i][2] = pair(z);
+        x[i][3] = pair(z + 2);
+      }
+    }
+  }
+  // Rows r0 + r >= n (behind the sequence's end) are zeros, whatever they hold.
+  __device__ __forceinline__ void clear(int r0, int n, int lane) {
+    if (r0 + 8 <= n) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (r0 + 2 * i + (lane >> 4) >= n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[i][j] = 0ull;
+  }
+  // Scale exponents of the rows (127: nothing but zeros), also to ex[8].
+  __device__ __forceinline__ void scales(int *ex, int lane) {
+    float m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack(x[i][j]);
+        m[i] = amax(m[i], f.x, f.y);
+      }
+    }
+#pragma unroll
+    for (int d = 8; d; d >>= 1)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m[i] = amax(m[i], __shfl_xor_sync(0xffffffffu, m[i], d));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = m[i] == 0.f ? 127 : scale_exp(m[i]);
+      if ((lane & 15) == 0) ex[2 * i + (lane >> 4)] = e;
+      sc[i] = pow2(e);
+    }
+  }
+  __device__ __forceinline__ void write(unsigned char *g8, int lane) {
+    const int m16 = lane & 15;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 2 * i + (lane >> 4);
+      const F2 f = pack(sc[i], sc[i]);
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) split2<!kBf16>(mul2(x[i][j], f), hi[j], lo[j]);
+      if (kBf16) {
+        *reinterpret_cast<uint4 *>(g8 + (m16 >> 3) * 1024 + r * 128 + (((m16 & 7) ^ r) << 4)) =
+            make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      } else {
+        unsigned char *p = g8 + r * 128 + (((m16 >> 1) ^ r) << 4) + (m16 & 1) * 8;
+        *reinterpret_cast<uint2 *>(p) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2 *>(p + 1024) = make_uint2(hi[2], hi[3]);
+        *reinterpret_cast<uint2 *>(p + 2048) = make_uint2(lo[0], lo[1]);
+        *reinterpret_cast<uint2 *>(p + 3072) = make_uint2(lo[2], lo[3]);
+      }
+    }
+  }
+};
+
 // ------------------------------------------------------------------ kernel
 
 template <bool kBf16, bool kLocal>
@@ -363,7 +448,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     linattn_chunk_kernel(const __grid_constant__ CUtensorMap tm_q,
                          const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v,
-                         const __grid_constant__ CUtensorMap tm_o,
                          const __grid_constant__ Args P) {
   constexpr bool kLo = !kBf16;                 // second parts of q, k, v, P, S
   constexpr uint32_t kRow = kBf16 ? 256 : 512; // bytes of a token row
@@ -374,14 +458,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char *gb = smem_raw + (sb - raw_s);
   const uint32_t bar0 = sb + OFF_BAR;
   auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
-  // rows landed / operand region free again / operand made, by chunk parity
+  // rows landed / region free again / operand made, by chunk parity
   const uint32_t staged = bar(0), kq_free = bar(2), rdy_kq = bar(4);
-  const uint32_t vstaged = bar(6), v_free = bar(7);
-  const uint32_t rdy_s = bar(8), rdy_v = bar(9), rdy_p = bar(10);
-  const uint32_t done_qk = bar(11), done_o = bar(12), done_kv = bar(13);
-  const uint32_t acc_free = bar(14), drain = bar(15), vecs = bar(16);  // 16..19
-  volatile uint32_t *slot = reinterpret_cast<volatile uint32_t *>(gb + OFF_BAR + 160);
-  volatile int *fail = reinterpret_cast<volatile int *>(gb + OFF_BAR + 164);
+  const uint32_t vstaged = bar(6), v_free = bar(8);
+  const uint32_t rdy_s = bar(10), rdy_v = bar(11), rdy_p = bar(12);
+  const uint32_t done_qk = bar(13), done_o = bar(14), done_kv = bar(15);
+  const uint32_t acc_free = bar(16), drain = bar(17), vecs = bar(18);  // 18..21
+  volatile uint32_t *slot = reinterpret_cast<volatile uint32_t *>(gb + OFF_BAR + 184);
+  volatile int *fail = reinterpret_cast<volatile int *>(gb + OFF_BAR + 188);
   auto vec = [&](int it) { return reinterpret_cast<float *>(gb + OFF_VEC + (it & 3) * 2048); };
   auto rowexp = [&](int it) { return reinterpret_cast<int *>(gb + OFF_EXP + (it & 1) * 512); };
   auto lanef = [&](int it) { return reinterpret_cast<float *>(gb + OFF_LANE + (it & 3) * 1024); };
@@ -395,12 +479,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int quad = warp & 3, half = (warp >> 2) & 1;
   const int myrow = 32 * quad + lane;          // TMEM lane
 
-  if (warp == kIssuer) tmem_alloc(sb + OFF_BAR + 160, 512);
+  if (warp == kIssuer) tmem_alloc(sb + OFF_BAR + 184, 512);
   if (tid == 0) {
     // one arrival each, or one from each warp of a group
-    constexpr uint32_t kByWarps = 1u << 4 | 1u << 5 | 1u << 7 | 1u << 8 | 1u << 9 | 1u << 10 | 1u << 14;
+    constexpr uint32_t kByWarps = 0x3u << 4 | 0x1fu << 8 | 1u << 16;
 #pragma unroll 1
-    for (int i = 0; i < 20; ++i) mbar_init(bar(i), (kByWarps >> i & 1) ? kGroup / 32 : 1);
+    for (int i = 0; i < 22; ++i) mbar_init(bar(i), (kByWarps >> i & 1) ? kGroup / 32 : 1);
     *fail = 0;
   }
   fence_before_sync();
@@ -415,24 +499,60 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
     // ============================================ group A: state, V operands
-    float s[kC];  // state rows dk = 64 half .. + 63 of column dv = myrow
+    F2 s[kC / 2];  // state rows dk = 64 half .. + 63 of column dv = myrow
     float *ps = reinterpret_cast<float *>(gb + OFF_PS);
-    float2 *pv = reinterpret_cast<float2 *>(gb + OFF_PV);
-    // the state operand of chunk `it`
-    auto state_operand = [&](int it) {
+    auto px = [&](int it) { return reinterpret_cast<float *>(gb + OFF_PV + (it & 1) * 1024); };
+    // this thread's 32 v values of a chunk: column myrow of rows 32 half ..
+    auto vcol = [&](int it) {
+      return gb + OFF_V + (it & 1) * kV + 32 * half * kRow + myrow * (kRow / kD);
+    };
+    auto vload = [&](const unsigned char *vp, int t) -> F2 {  // tokens t and t + 1
+      if (kBf16)
+        return pack(__uint_as_float((uint32_t) * reinterpret_cast<const unsigned short *>(
+                                        vp + t * kRow) << 16),
+                    __uint_as_float((uint32_t) * reinterpret_cast<const unsigned short *>(
+                                        vp + (t + 1) * kRow) << 16));
+      return pack(*reinterpret_cast<const float *>(vp + t * kRow),
+                  *reinterpret_cast<const float *>(vp + (t + 1) * kRow));
+    };
+    // The largest |v| of chunk `it` and what is not finite, to the exchange.
+    auto v_max = [&](int it, int valid) {
+      wait_bar(vstaged + 8 * (it & 1), (it >> 1) & 1, fail);
+      unsigned char *vp = vcol(it);
+      const int nv = valid - 32 * half;
+      if (nv < 32) {  // rows behind the end are zeros, whatever they hold
+#pragma unroll 1
+        for (int t = max(nv, 0); t < 32; ++t) {
+          if (kBf16)
+            *reinterpret_cast<unsigned short *>(vp + t * kRow) = 0;
+          else
+            *reinterpret_cast<float *>(vp + t * kRow) = 0.f;
+        }
+        fence_proxy_async();  // the copy engine writes these bytes next
+      }
       float m = 0.f;
+#pragma unroll 1
+      for (int t0 = 0; t0 < 32; t0 += 16)
 #pragma unroll
-      for (int j = 0; j < kC; j += 2) m = amax(m, s[j], s[j + 1]);
-      ps[128 * half + myrow] = m;
-      bar_pair(quad);
-      const int e = scale_exp(amax(m, ps[128 * (half ^ 1) + myrow]));
-      const float f = pow2(e);
-#pragma unroll
-      for (int c0 = 0; c0 < kC; c0 += 16)
-        put16<kLo>(tl + T_SOP, tl + T_SOP + 64, 64 * half + c0, s + c0, f);
-      if (half == 0) lanef(it)[myrow] = pow2(-e);
-      tmem_wait_st();
-      signal_ready<false>(rdy_s);
+        for (int j = 0; j < 16; j += 2) {
+          const float2 f = unpack(vload(vp, t0 + j));
+          m = amax(m, f.x, f.y);
+        }
+      // A value that is not finite must not reach the rows before it (its
+      // weight there is 0, but 0 * inf is NaN): PV takes 0 for it, and the
+      // output becomes NaN from its token on.
+      int bad = kC;
+      if (!isfinite(m)) {
+        m = 0.f;
+#pragma unroll 1
+        for (int t = 30; t >= 0; t -= 2) {
+          const float2 f = unpack(vload(vp, t));
+          if (isfinite(f.y)) m = amax(m, f.y); else bad = 32 * half + t + 1;
+          if (isfinite(f.x)) m = amax(m, f.x); else bad = 32 * half + t;
+        }
+      }
+      px(it)[128 * half + myrow] = m;
+      badtok(it)[128 * half + myrow] = bad;
     };
     // units without a chunk of their own: their states, and bad lengths
     if (P.lens || kLocal || P.nseg > 1) {
@@ -455,118 +575,109 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     Walk<kLocal> w(P);
-    while (w.next()) {
-      const int it = w.it;
+    if (w.next()) v_max(0, w.valid());
+    while (w.ok) {
+      const int it = w.it, head = w.head, seg = w.seg;
+      const bool last = w.last();
       if (w.first) {
-        const size_t at = ((size_t)w.head * P.nseg + w.seg) * kD * kD;
-        const float *src = P.nseg > 1 ? P.ws_state + at : P.S + at;
+        const size_t at = ((size_t)head * P.nseg + seg) * kD * kD;
+        const float *src = (P.nseg > 1 ? P.ws_state + at : P.S + at) + kC * half * kD + myrow;
 #pragma unroll
-        for (int j = 0; j < kC; ++j)
-          s[j] = kLocal ? 0.f : src[(size_t)(kC * half + j) * kD + myrow];
+        for (int j = 0; j < kC; j += 2)
+          s[j / 2] = kLocal ? 0ull : pack(src[j * kD], src[(j + 1) * kD]);
       }
-      if (!kLocal) state_operand(it);
-      // ---- V^T and (V f)^T operands, lane dv, K = t = 32 half .. + 31
-      wait_bar(vstaged, it & 1, fail);
-      wait_bar(vecs + 8 * (it & 3), (it >> 2) & 1, fail);
-      const float *vc = vec(it);
-      // this thread's 32 values: column myrow of rows 32 half ..
-      unsigned char *vp = gb + OFF_V + 32 * half * kRow + myrow * (kRow / kD);
-      auto vload = [&](int j) -> float {
-        if (kBf16)
-          return __uint_as_float(
-              (uint32_t) * reinterpret_cast<const unsigned short *>(vp + j * kRow) << 16);
-        return *reinterpret_cast<const float *>(vp + j * kRow);
-      };
-      const int nv = w.valid() - 32 * half;
-      if (nv < 32) {  // rows behind the end, whatever they hold, are zeros
-#pragma unroll 1
-        for (int j = max(nv, 0); j < 32; ++j) {
-          if (kBf16)
-            *reinterpret_cast<unsigned short *>(vp + j * kRow) = 0;
-          else
-            *reinterpret_cast<float *>(vp + j * kRow) = 0.f;
-        }
-        fence_proxy_async();  // the copy engine writes these bytes next
-      }
-      const float *vf = vc + VF + 32 * half;
-      float ma = 0.f, mb = 0.f;
-#pragma unroll 1
-      for (int j0 = 0; j0 < 32; j0 += 8) {
-        float x[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = vload(j0 + j);
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          ma = amax(ma, x[j], x[j + 1]);
-          mb = amax(mb, x[j] * vf[j0 + j], x[j + 1] * vf[j0 + j + 1]);
-        }
-      }
-      // A value that is not finite must not reach the rows before it (its
-      // weight there is 0, but 0 * inf is NaN): PV takes 0 for it, and the
-      // output becomes NaN from its token on.
-      int bad = kC;
-      if (!kLocal && !isfinite(ma)) {
-        ma = 0.f;
-#pragma unroll 1
-        for (int j = 31; j >= 0; --j) {
-          const float x = vload(j);
-          if (!isfinite(x))
-            bad = 32 * half + j;
-          else
-            ma = amax(ma, x);
-        }
-      }
-      if (!kLocal) badtok(it)[128 * half + myrow] = bad;
-      pv[128 * half + myrow] = make_float2(ma, mb);
-      bar_pair(quad);
-      const float2 other = pv[128 * (half ^ 1) + myrow];
-      const int ea = scale_exp(amax(ma, other.x)), eb = scale_exp(amax(mb, other.y));
-      const float fa = pow2(ea), fb = pow2(eb);
       if (!kLocal) {
-        // V's columns are free once the previous chunk's PV has read them
-        if (it > 0) wait_bar(done_o, (it - 1) & 1, fail);
-        fence_after_sync();
-        if (half == 0) lanef(it)[128 + myrow] = pow2(-ea);
-      }
-#pragma unroll 1
-      for (int c0 = 0; c0 < 32; c0 += 16) {
-        float x[16];
-        const int t0 = 32 * half + c0;
+        float m = 0.f;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = vload(c0 + j) * vf[c0 + j];
-        put16<true>(tl + T_WOP, tl + T_WOP + 32, t0, x, fb);
-        if (!kLocal) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) x[j] = vload(c0 + j);
-          if (bad < kC)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] = isfinite(x[j]) ? x[j] : 0.f;
-          put16<kLo>(tl + T_VOP, tl + T_VOP + 32, t0, x, fa);
+        for (int j = 0; j < kC / 2; ++j) {
+          const float2 x = unpack(s[j]);
+          m = amax(m, x.x, x.y);
         }
+        ps[128 * half + myrow] = m;
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(v_free);
-      tmem_wait_st();
-      signal_ready<false>(rdy_v);
+      // (one exchange a chunk: both halves' v maxima, made under the last
+      // chunk's KV product, and state maxima)
+      bar_pair(quad);
+      if (!kLocal) {
+        // ---- the state operand
+        const int e = scale_exp(amax(ps[myrow], ps[128 + myrow]));
+        const F2 f = pack(pow2(e), pow2(e));
+#pragma unroll
+        for (int c0 = 0; c0 < kC; c0 += 16) {
+          F2 x[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = mul2(s[c0 / 2 + j], f);
+          put16<kLo>(tl + T_SOP, tl + T_SOP + 64, 64 * half + c0, x);
+        }
+        if (half == 0) lanef(it)[myrow] = pow2(-e);
+        tmem_wait_st();
+        signal_ready<false>(rdy_s);
+      }
+      // ---- V^T and (V f)^T operands, lane dv, K = t = 32 half .. + 31
+      const int ea = scale_exp(amax(px(it)[myrow], px(it)[128 + myrow]));
+      wait_bar(vecs + 8 * (it & 3), (it >> 2) & 1, fail);
+      const float gC = vec(it)[VM], inv = pow2(-ea) * vec(it)[VM + 2];
+      {
+        const F2 fa = pack(pow2(ea), pow2(ea));
+        if (!kLocal) {
+          // V's columns are free once the previous chunk's PV has read them
+          if (it > 0) wait_bar(done_o, (it - 1) & 1, fail);
+          fence_after_sync();
+          if (half == 0) lanef(it)[128 + myrow] = pow2(-ea);
+        }
+        const unsigned char *vp = vcol(it);
+        const bool any_bad =
+            !kLocal && __any_sync(0xffffffffu, badtok(it)[128 * half + myrow] < kC);
+#pragma unroll 1
+        for (int t0 = 0; t0 < 32; t0 += 16) {
+          const F2 *vf = reinterpret_cast<const F2 *>(vec(it) + VF + 32 * half + t0);
+          F2 x[8], y[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            x[j] = mul2(vload(vp, t0 + 2 * j), fa);
+            y[j] = mul2(x[j], vf[j]);
+          }
+          put16<true>(tl + T_WOP, tl + T_WOP + 32, 32 * half + t0, y);
+          if (!kLocal) {
+            if (any_bad)
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const float2 f = unpack(x[j]);
+                x[j] = pack(isfinite(f.x) ? f.x : 0.f, isfinite(f.y) ? f.y : 0.f);
+              }
+            put16<kLo>(tl + T_VOP, tl + T_VOP + 32, 32 * half + t0, x);
+          }
+        }
+        tmem_wait_st();
+        signal_ready<false>(rdy_v);
+        if (lane == 0) mbar_arrive(v_free + 8 * (it & 1));
+      }
+      // ---- the next chunk's v maxima, under this one's product
+      if (w.next()) v_max(w.it, w.valid());
       // ---- the state after the chunk
-      const float gC = vc[VM], inv = pow2(-eb);
       wait_bar(done_kv, it & 1, fail);
       fence_after_sync();
+      const F2 a1 = pack(inv, inv), a2 = pack(gC, gC);
 #pragma unroll
-      for (int c0 = 0; c0 < kC; c0 += 32) {
-        uint32_t d[32];
-        tmem_ld32_async(tl + T_D + 64 * half + c0, d);
+      for (int c0 = 0; c0 < kC; c0 += 16) {
+        uint32_t d[16];
+        tmem_ld16_async(tl + T_D + 64 * half + c0, d);
         tmem_wait_ld(d);
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          s[c0 + j] = fmaf(gC, s[c0 + j], __uint_as_float(d[j]) * inv);
+        for (int j = 0; j < 8; ++j)
+          s[c0 / 2 + j] = fma2(pair(d + 2 * j), a1, mul2(s[c0 / 2 + j], a2));
       }
       if (kLocal) signal_ready<false>(rdy_s);  // the KV columns are read
-      if (w.last() && (kLocal || w.seg == P.nseg - 1)) {
-        float *dst = kLocal ? P.ws_state + ((size_t)w.head * P.nseg + w.seg) * kD * kD
-                            : P.S + (size_t)w.head * kD * kD;
+      if (last && (kLocal || seg == P.nseg - 1)) {
+        float *dst = (kLocal ? P.ws_state + ((size_t)head * P.nseg + seg) * kD * kD
+                             : P.S + (size_t)head * kD * kD) +
+                     kC * half * kD + myrow;
 #pragma unroll
-        for (int j = 0; j < kC; ++j) dst[(size_t)(kC * half + j) * kD + myrow] = s[j];
+        for (int j = 0; j < kC; j += 2) {
+          const float2 x = unpack(s[j / 2]);
+          dst[j * kD] = x.x;
+          dst[(j + 1) * kD] = x.y;
+        }
       }
     }
     cta_end();
@@ -596,88 +707,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     // ======================================= group B: q, k rows, P, output
-    const int bt = tid - kGroup;
-    // [K; Q] operand of a chunk, in place: this warp's two groups of 8 rows
-    // (K rows only in the state pass: one group).  Lane l has rows
-    // 2 i + (l >> 4) and of each, with m = l & 15, columns 4 m .. + 3 and
-    // 64 + 4 m .. + 3 (fp32) or 8 m .. + 7 (bf16), so that every access of
-    // a quarter warp covers whole banks.
-    auto convert = [&](const Walk<kLocal> &w) {
-      const int m16 = lane & 15, r1 = lane >> 4, nv = w.valid();
-      wait_bar(staged + 8 * (w.it & 1), (w.it >> 1) & 1, fail);
-      int *ex = rowexp(w.it);
-#pragma unroll 1
-      for (int grp = warp - 8; grp < (kLocal ? 8 : 16); grp += 8) {
-        unsigned char *g8 = gb + OFF_KQ + (w.it & 1) * kKQ + grp * kGrp;
-        float x[4][8], sc[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const unsigned char *st = g8 + (2 * i + r1) * kRow + m16 * 16;
-          const uint4 u = *reinterpret_cast<const uint4 *>(st);
-          if (kBf16) {
-            const uint32_t q[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              x[i][2 * j] = __uint_as_float(q[j] << 16);
-              x[i][2 * j + 1] = __uint_as_float(q[j] & 0xffff0000u);
-            }
-          } else {
-            const uint4 v = *reinterpret_cast<const uint4 *>(st + 256);
-            const uint32_t q[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[i][j] = __uint_as_float(q[j]);
-          }
-        }
-        if (8 * (grp & 7) + 8 > nv) {  // rows behind the end are zeros
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (8 * (grp & 7) + 2 * i + r1 >= nv)
-#pragma unroll
-              for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float m = amax(x[i][0], x[i][1], x[i][2]);
-          m = amax(m, x[i][3], x[i][4]);
-          m = amax(m, x[i][5], x[i][6]);
-          sc[i] = amax(m, x[i][7]);
-        }
-#pragma unroll
-        for (int d = 8; d; d >>= 1)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            sc[i] = amax(sc[i], __shfl_xor_sync(0xffffffffu, sc[i], d));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int e = scale_exp(sc[i]);
-          if (m16 == 0) ex[8 * grp + 2 * i + r1] = e;
-          sc[i] = pow2(e);
-        }
-        __syncwarp();  // every row of the group is read
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 2 * i + r1;
-          if (kBf16) {
-            put8<kLo>(g8 + (m16 >> 3) * 1024 + r * 128 + (((m16 & 7) ^ r) << 4), 2048, x[i], sc[i]);
-          } else {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              split2<true>(x[i][2 * j] * sc[i], x[i][2 * j + 1] * sc[i], hi[j], lo[j]);
-            unsigned char *p = g8 + r * 128 + (((m16 >> 1) ^ r) << 4) + (m16 & 1) * 8;
-            *reinterpret_cast<uint2 *>(p) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2 *>(p + 1024) = make_uint2(hi[2], hi[3]);
-            *reinterpret_cast<uint2 *>(p + 2048) = make_uint2(lo[0], lo[1]);
-            *reinterpret_cast<uint2 *>(p + 3072) = make_uint2(lo[2], lo[3]);
-          }
-        }
-      }
-      signal_ready<true>(rdy_kq + 8 * (w.it & 1));
-    };
     Walk<kLocal> w(P), nx(P);  // the chunk at hand (none at first), the next
-    for (;;) {
+    for (bool more = true; more;) {
       w = nx;
-      nx.next();
+      more = nx.next();
       const int it = w.it;
       const float *vc = vec(it);
       if (!kLocal && w.ok) {
@@ -687,93 +720,112 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_after_sync();
       if (quad >= 2) {
         const int t = myrow - kC;
-        const float at = vc[VA + t], gh = vc[VGH + t], gl = vc[VGL + t];
+        const float at = vc[VA + t];
         const bool fac = vc[VM + 1] != 0.f;
         unsigned char *pr = gb + OFF_P + t * 128;
+        const F2 at2 = pack(at, at);
 #pragma unroll 1
         for (int s0 = 32 * half; s0 < 32 * half + 32; s0 += 16) {
-          float x[16];
+          F2 x[8];
           if (s0 < 32 * (quad - 1)) {  // some s <= t in this warp
-            tmem_ld16(tl + T_G + s0, x);
+            uint32_t r[16];
+            tmem_ld16_async(tl + T_G + s0, r);
+            tmem_wait_ld(r);
+            const F2 *vb = reinterpret_cast<const F2 *>(vc + VB + s0);
+            if (fac) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] *= at * vc[VB + s0 + j];
-            if (!fac)
+              for (int j = 0; j < 8; ++j) x[j] = mul2(pair(r + 2 * j), mul2(at2, vb[j]));
+            } else {
+              const float *h = vc + VGH + s0, *l = vc + VGL + s0;
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                x[j] *= exp2f((gh - vc[VGH + s0 + j]) + (gl - vc[VGL + s0 + j]));
+              for (int j = 0; j < 8; ++j) {
+                const float2 n = unpack(vb[j]);
+                x[j] = mul2(pair(r + 2 * j),
+                            pack(exp2f(((at - h[2 * j]) - l[2 * j]) + n.x),
+                                 exp2f(((at - h[2 * j + 1]) - l[2 * j + 1]) + n.y)));
+              }
+            }
             if (s0 + 15 > 32 * (quad - 2))
 #pragma unroll
-              for (int j = 0; j < 16; ++j) x[j] = s0 + j <= t ? x[j] : 0.f;
+              for (int j = 0; j < 8; ++j) {
+                const float2 f = unpack(x[j]);
+                x[j] = pack(s0 + 2 * j <= t ? f.x : 0.f, s0 + 2 * j + 1 <= t ? f.y : 0.f);
+              }
           } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] = 0.f;
+            for (int j = 0; j < 8; ++j) x[j] = 0ull;
           }
+          uint32_t hi[8], lo[8];
 #pragma unroll
-          for (int c0 = 0; c0 < 16; c0 += 8)
-            put8<kLo>(pr + ((((s0 + c0) >> 3) ^ (t & 7)) << 4), 8192, x + c0, 1.f);
+          for (int j = 0; j < 8; ++j) split2<kLo>(x[j], hi[j], lo[j]);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            unsigned char *p = pr + ((((s0 >> 3) + c) ^ (t & 7)) << 4);
+            *reinterpret_cast<uint4 *>(p) =
+                make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
+            if (kLo)
+              *reinterpret_cast<uint4 *>(p + 8192) =
+                  make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+          }
         }
       }
       signal_ready<true>(rdy_p);
       }
-      // ---- the next chunk's rows, under this one's products
-      if (nx.ok) convert(nx);
-      if (kLocal || !w.ok) {
-        if (!nx.ok) break;
-        continue;
+      // ---- the next chunk's rows, under this one's products: two groups of 8 a
+      // warp (the state pass takes the k rows alone)
+      if (more) {
+        const int par = nx.it & 1;
+        wait_bar(staged + 8 * par, (nx.it >> 1) & 1, fail);
+#pragma unroll 1
+        for (int grp = warp - 8; grp < (kLocal ? 8 : 16); grp += 8) {
+          unsigned char *g8 = gb + OFF_KQ + par * kKQ + grp * kGrp;
+          RowGroup<kBf16> g;
+          g.read(g8, lane);
+          g.clear(8 * (grp & 7), nx.valid(), lane);
+          g.scales(rowexp(nx.it) + 8 * grp, lane);
+          __syncwarp();  // every row of the group is read
+          g.write(g8, lane);
+        }
+        signal_ready<true>(rdy_kq + 8 * par);
       }
-      // the o tile's last store has read it
-      if (bt == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-      bar_b();
-      // ---- o^T = cA QS + cB PV, lane dv, columns t = 32 half .. + 31
+      if (kLocal || !w.ok) continue;
+      // ---- o^T = cA QS + cB PV, lane dv, columns t = 32 half .. + 31: a warp
+      // stores 32 columns of a row at a time, straight to the output
       wait_bar(done_o, it & 1, fail);
       fence_after_sync();
-      {
-        const float fs = lanef(it)[myrow], fv = lanef(it)[128 + myrow];
-        const int bad = min((int)badtok(it)[myrow], (int)badtok(it)[128 + myrow]);
-        uint32_t qs[32], pv[32];
-        tmem_ld32_async(tl + T_QS + 32 * half, qs);
-        tmem_ld32_async(tl + T_G + 32 * half, pv);
-        tmem_wait_ld(qs);
-        tmem_wait_ld(pv);
-        signal_ready<false>(acc_free);
-        const float *ca = vc + VCA + 32 * half, *cb = vc + VCB + 32 * half;
-        unsigned char *ot = gb + OFF_O + 32 * half * kRow + myrow * (kRow / kD);
+      const float fs = lanef(it)[myrow], fv = lanef(it)[128 + myrow];
+      const int nv = w.valid() - 32 * half;
+      typedef typename std::conditional<kBf16, __nv_bfloat16, float>::type Out;
+      const size_t pitch = (size_t)P.vh * kD;
+      Out *op = static_cast<Out *>(P.o) +
+                ((size_t)w.b * P.T + (size_t)w.c * kC + 32 * half) * pitch + w.vi * kD + myrow;
+      const F2 fs2 = pack(fs, fs), fv2 = pack(fv, fv);
+      const int bad = min((int)badtok(it)[myrow], (int)badtok(it)[128 + myrow]) - 32 * half;
+      uint32_t qs[32], pv[32];
+      tmem_ld16_async(tl + T_QS + 32 * half, reinterpret_cast<uint32_t(&)[16]>(qs[0]));
+      tmem_ld16_async(tl + T_QS + 32 * half + 16, reinterpret_cast<uint32_t(&)[16]>(qs[16]));
+      tmem_ld16_async(tl + T_G + 32 * half, reinterpret_cast<uint32_t(&)[16]>(pv[0]));
+      tmem_ld16_async(tl + T_G + 32 * half + 16, reinterpret_cast<uint32_t(&)[16]>(pv[16]));
+      tmem_wait_ld(qs);
+      tmem_wait_ld(pv);
+      signal_ready<false>(acc_free);
+      const F2 *ca = reinterpret_cast<const F2 *>(vc + VCA + 32 * half);
+      const F2 *cb = reinterpret_cast<const F2 *>(vc + VCB + 32 * half);
+      Out *p = op;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float y = fmaf(__uint_as_float(qs[j]) * fs, ca[j],
-                               __uint_as_float(pv[j]) * fv * cb[j]);
-          if (kBf16)
-            *reinterpret_cast<__nv_bfloat16 *>(ot + j * kRow) = __float2bfloat16_rn(y);
-          else
-            *reinterpret_cast<float *>(ot + j * kRow) = y;
-        }
-        // (the same thread's stores, so in order)
+      for (int j = 0; j < 32; j += 2) {
+        const float2 y = unpack(fma2(mul2(pair(qs + j), fs2), ca[j / 2],
+                                     mul2(mul2(pair(pv + j), fv2), cb[j / 2])));
+        if (j < nv) *p = (Out)y.x;
+        p += pitch;
+        if (j + 1 < nv) *p = (Out)y.y;
+        p += pitch;
+      }
+      // (the same thread's stores, so in order)
 #pragma unroll 1
-        for (int j = max(bad - 32 * half, 0); j < 32; ++j) {
-          if (kBf16)
-            *reinterpret_cast<unsigned short *>(ot + j * kRow) = 0x7fff;
-          else
-            *reinterpret_cast<uint32_t *>(ot + j * kRow) = 0x7fffffffu;
-        }
-      }
-      fence_proxy_async();
-      bar_b();
-      const int nv = w.valid();
-      if (nv == kC) {
-        if (bt == 0) tma_store(&tm_o, w.vi, w.c * kC, w.b, sb + OFF_O);
-      } else {  // a part of a chunk: only its rows
-        constexpr int kVec = kRow / 16;
-        for (int e = bt; e < nv * kVec; e += kGroup) {
-          const int r = e / kVec, x = e % kVec;
-          const size_t tok = (size_t)w.b * P.T + (size_t)w.c * kC + r;
-          *reinterpret_cast<uint4 *>(static_cast<unsigned char *>(P.o) +
-                                     (tok * P.vh + w.vi) * kRow + x * 16) =
-              *reinterpret_cast<const uint4 *>(gb + OFF_O + r * kRow + x * 16);
-        }
-      }
-      if (!nx.ok) break;
+      for (int j = max(bad, 0); j < min(nv, 32); ++j)
+        op[j * pitch] = (Out)__int_as_float(0x7fffffff);
     }
-    if (!kLocal && bt == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     cta_end();
   } else {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -873,18 +925,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!kLocal) tma_load(reg + kC * kRow, &tm_q, w.vi / P.rep, w.c * kC, w.b, st);
       }
       __syncwarp();
-      if (it >= 1) wait_bar(v_free, (it - 1) & 1, fail);
+      if (it >= 2) wait_bar(v_free + 8 * (it & 1), ((it - 2) >> 1) & 1, fail);
       if (lane == 0) {
-        mbar_expect(vstaged, kC * kRow);
-        tma_load(sb + OFF_V, &tm_v, w.vi, w.c * kC, w.b, vstaged);
+        mbar_expect(vstaged + 8 * (it & 1), kC * kRow);
+        tma_load(sb + OFF_V + (it & 1) * kV, &tm_v, w.vi, w.c * kC, w.b, vstaged + 8 * (it & 1));
       }
       __syncwarp();
     }
     // nothing may still be copying into shared memory when the CTA ends
-    // (the last chunk of either parity, and the last V rows)
-    for (int j = max(it - 1, 0); j <= it; ++j)
+    // (the last chunk of either parity)
+    for (int j = max(it - 1, 0); j <= it; ++j) {
       mbar_wait(staged + 8 * (j & 1), (j >> 1) & 1, kWaitLimit);
-    if (it >= 0) mbar_wait(vstaged, it & 1, kWaitLimit);
+      mbar_wait(vstaged + 8 * (j & 1), (j >> 1) & 1, kWaitLimit);
+    }
     __syncwarp();
     cta_end();
   } else if (warp == kGates) {
@@ -924,84 +977,99 @@ __global__ void __launch_bounds__(kThreads, 1)
       total += (double)end.h + (double)end.l;
       float *vc = vec(it);
       // the decay from each token to the chunk's end
-      float wt[2], at[2], bs[2], gm[2];
+      float wt[2], gm[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) wt[i] = ex2(add2(end, neg2(G[i])));
-      int ew = 22;
-      bool fac = true;
-      if (!kLocal) {
-        if (__any_sync(0xffffffffu, up)) {
-          // growth: the largest Gamma_t - Gamma_s, s <= t (0 for decays)
-          float lo = fminf(G[0].h, G[1].h), run_lo = lo;
+      for (int i = 0; i < 2; ++i) {
+        wt[i] = ex2(add2(end, neg2(G[i])));
+        gm[i] = P.scale * ex2(G[i]);
+      }
+      int grow = 0;
+      if (__any_sync(0xffffffffu, up)) {
+        // growth: the largest Gamma_t - Gamma_s, s <= t (0 for decays)
+        float lo = fminf(G[0].h, G[1].h), run_lo = lo;
 #pragma unroll
-          for (int off = 1; off < 32; off <<= 1) {
-            const float y = __shfl_up_sync(0xffffffffu, run_lo, off);
-            if (lane >= off) run_lo = fminf(run_lo, y);
-          }
-          float grow = fmaxf(fmaxf(G[0].h, G[1].h) - run_lo, 0.f);
-#pragma unroll
-          for (int off = 16; off; off >>= 1)
-            grow = fmaxf(grow, __shfl_xor_sync(0xffffffffu, grow, off));
-          ew += (int)ceilf(fminf(grow, 80.f));
+        for (int off = 1; off < 32; off <<= 1) {
+          const float y = __shfl_up_sync(0xffffffffu, run_lo, off);
+          if (lane >= off) run_lo = fminf(run_lo, y);
         }
-        float top = fmaxf(G[0].h, G[1].h), low = fminf(G[0].h, G[1].h);
+        float d = fmaxf(fmaxf(G[0].h, G[1].h) - run_lo, 0.f);
 #pragma unroll
-        for (int off = 16; off; off >>= 1) {
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-          low = fminf(low, __shfl_xor_sync(0xffffffffu, low, off));
-        }
-        // one factor per row and column while their product cannot leave the
-        // normal floats; otherwise an exponential per element
-        fac = top - low <= 115.f;
-        const Two mid{-0.5f * (top + low), 0.f};
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const Two d = add2(G[i], mid);
-          at[i] = fac ? ex2(d) : 1.f;
-          bs[i] = fac ? ex2(neg2(d)) : 1.f;
-          gm[i] = P.scale * ex2(G[i]);
-        }
+        for (int off = 16; off; off >>= 1) d = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, off));
+        grow = (int)ceilf(fminf(d, 80.f));
       }
       const float gend = ex2(end);
       wait_bar(rdy_kq + 8 * (it & 1), (it >> 1) & 1, fail);
       const int *ex = rowexp(it);
       const int2 k2 = *reinterpret_cast<const int2 *>(ex + 2 * lane);
       const int kx[2] = {k2.x, k2.y};
+      // the smallest exponent (the largest k row) of the finite rows
+      const int least = __reduce_min_sync(
+          0xffffffffu, min(k2.x > -114 ? k2.x : 127, k2.y > -114 ? k2.y : 127));
+      // (exactly; 0 below the normal floats)
+      auto p2 = [](int e) { return e < -126 ? 0.f : pow2(min(e, 127)); };
+      // The weight of row s in P[t], by its logarithm: r_s = -Gamma_s - kx_s,
+      // and Gamma_t for every s.  R_t >= the largest r_s, s <= t, so P[t][s] =
+      // G 2^{r_s - R_t - 22} keeps its bits whatever the decays and the rows'
+      // sizes (|G| <= 2^37).
+      float R[2] = {0.f, 0.f};
       if (!kLocal) {
-        const int2 q2 = *reinterpret_cast<const int2 *>(ex + 64 + 2 * lane);
-        const int qx[2] = {q2.x, q2.y};
-        // the smallest exponent (the largest k row) up to t
-        int run_k = min(k2.x, k2.y);
+        const float none = -3e38f;
+        float r[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) r[i] = kx[i] < 127 ? -G[i].h - (float)kx[i] : none;
+        float run_r = fmaxf(r[0], r[1]);
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, run_k, off);
-          if (lane >= off) run_k = min(run_k, y);
+          const float y = __shfl_up_sync(0xffffffffu, run_r, off);
+          if (lane >= off) run_r = fmaxf(run_r, y);
         }
-        const int before_k = __shfl_up_sync(0xffffffffu, run_k, 1);
-        const int pk[2] = {lane > 0 ? min(before_k, k2.x) : k2.x, run_k};
-        // where the two factors split: the smallest exponent of a finite row
-        int ref = min(k2.x > -114 ? k2.x : 126, k2.y > -114 ? k2.y : 126);
-#pragma unroll
-        for (int off = 16; off; off >>= 1)
-          ref = min(ref, __shfl_xor_sync(0xffffffffu, ref, off));
-        // (exactly; 0 below the normal floats)
-        auto p2 = [](int e) { return e < -126 ? 0.f : pow2(min(e, 127)); };
+        const float before_r = __shfl_up_sync(0xffffffffu, run_r, 1);
+        R[0] = ceilf(lane > 0 ? fmaxf(before_r, r[0]) : r[0]);
+        R[1] = ceilf(run_r);
+        // rows with nothing but zeros before them take the first other row's
+        const unsigned some = __ballot_sync(0xffffffffu, R[1] > none);
+        const float lo = some ? __shfl_sync(0xffffffffu, R[0] > none ? R[0] : R[1],
+                                            __ffs(some) - 1)
+                              : 0.f;
+        const float hi = fmaxf(__shfl_sync(0xffffffffu, R[1], 31), lo);
+        // one factor per row and column while their product cannot leave the
+        // normal floats; otherwise an exponential per element
+        const bool fac = hi - lo <= 120.f;
+        const float c = -rintf(0.5f * (hi + lo));
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int t = 2 * lane + i;
-          vc[VA + t] = at[i] * p2(pk[i] - ref - ew);
-          vc[VB + t] = bs[i] * p2(ref - kx[i]);
-          vc[VCA + t] = gm[i] * p2(-qx[i]);
-          vc[VCB + t] = P.scale * p2(ew - qx[i] - pk[i]);
+          R[i] = fmaxf(R[i], lo);
+          const float n = -22.f - (float)kx[i];
+          vc[VA + t] = fac ? exp2f(-R[i] - c) : -R[i];
+          vc[VB + t] = fac ? ex2(add2(neg2(G[i]), Two{c + n, 0.f})) : n;
           vc[VGH + t] = G[i].h;
           vc[VGL + t] = G[i].l;
         }
+        if (lane == 0) vc[VM + 1] = fac ? 1.f : 0.f;
       }
+      // f_t = (decay to the end) / (k row scale), relative to a power of two
+      // that bounds it: the growth's and the largest row's
+      const int fe = min(max(grow - least + 1, -126), 126);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) vc[VF + 2 * lane + i] = wt[i] * pow2(-kx[i]);
+      for (int i = 0; i < 2; ++i)  // (a k row that is not finite: the state is lost)
+        vc[VF + 2 * lane + i] = kx[i] > -114 ? wt[i] * p2(-kx[i] - fe) : __int_as_float(0x7fffffff);
       if (lane == 0) {
         vc[VM] = gend;
-        vc[VM + 1] = fac ? 1.f : 0.f;
+        vc[VM + 2] = pow2(fe);
+      }
+      if (!kLocal) {  // the output's factors
+        const int2 q2 = *reinterpret_cast<const int2 *>(ex + 64 + 2 * lane);
+        const int qx[2] = {q2.x, q2.y};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int t = 2 * lane + i;
+          vc[VCA + t] = gm[i] * p2(-qx[i]);
+          // what P[t] and q_t are scaled by (finite also where P[t] is all zeros)
+          Two u = add2(G[i], Two{R[i] + (float)(22 - qx[i]), 0.f});
+          if (u.h > 126.f) u = Two{126.f, 0.f};
+          vc[VCB + t] = P.scale * ex2(u);
+        }
       }
       __syncwarp();
       if (lane == 0) {
@@ -1086,7 +1154,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
 }
 
 // [B][T][heads][128] rows as a 4-d tensor {128, heads, T, B}; a box is 64
-// token rows of one head.  Rows past T read as zeros and are not written.
+// token rows of one head.  Rows past T read as zeros.
 cudaError_t rows_map(CUtensorMap *map, const void *base, bool bf16, int heads, int T, int B) {
   const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_tiled();
   if (fn == nullptr) return cudaErrorNotSupported;
@@ -1111,7 +1179,7 @@ cudaError_t launch(const CUtensorMap *m, const Args &a, cudaStream_t stream) {
                            cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
   if (e != cudaSuccess) return e;
   linattn_chunk_kernel<kBf16, kLocal>
-      <<<(unsigned)min(a.units, kSms), kThreads, kSmemAlloc, stream>>>(m[0], m[1], m[2], m[3], a);
+      <<<(unsigned)min(a.units, kSms), kThreads, kSmemAlloc, stream>>>(m[0], m[1], m[2], a);
   return cudaGetLastError();
 }
 
@@ -1145,12 +1213,11 @@ cudaError_t launch_linattn_prefill(const LinattnArgs &L, bool bf16, void *worksp
   a.T = L.M;
   a.nseg = nseg;
   a.per_seg = ((L.M + kC - 1) / kC + nseg - 1) / nseg;
-  CUtensorMap m[4];
+  CUtensorMap m[3];
   cudaError_t e;
   if ((e = rows_map(&m[0], L.q, bf16, L.kh, L.M, L.B)) != cudaSuccess) return e;
   if ((e = rows_map(&m[1], L.k, bf16, L.kh, L.M, L.B)) != cudaSuccess) return e;
   if ((e = rows_map(&m[2], L.v, bf16, L.vh, L.M, L.B)) != cudaSuccess) return e;
-  if ((e = rows_map(&m[3], L.o, bf16, L.vh, L.M, L.B)) != cudaSuccess) return e;
   if (nseg > 1) {
     a.units = (int)(heads * (nseg - 1));
     e = bf16 ? launch<true, true>(m, a, stream) : launch<false, true>(m, a, stream);

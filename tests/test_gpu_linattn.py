@@ -154,7 +154,7 @@ def prompt_tol(T, dtype=torch.float32):
     return t, t + (2.0 ** -10 if dtype == torch.bfloat16 else 0.0)
 
 
-def check_prompt(d, S, o, scale=1.0, lens=None, rows=None):
+def check_prompt(d, S, o, scale=1.0, lens=None, floor_S=0.0, floor_o=0.0):
     B, T, vh, _ = d["v"].shape
     clean = d
     if lens is not None:  # the plain form reads the rows behind a length as zeros
@@ -164,8 +164,8 @@ def check_prompt(d, S, o, scale=1.0, lens=None, rows=None):
                  for x, t in d.items()}
     ref = linattn(clean["S"], clean["q"], clean["k"], clean["v"], clean["g"], scale, lens=lens)
     ts, to = prompt_tol(T, d["v"].dtype)
-    assert_within(S, ref["S"], ts * ref["mS"], "S")
-    tol = to * ref["mo"] + half_step(d["v"].dtype) * (ref["o"].abs() + to * ref["mo"])
+    assert_within(S, ref["S"], ts * ref["mS"] + floor_S, "S")
+    tol = floor_o + to * ref["mo"] + half_step(d["v"].dtype) * (ref["o"].abs() + to * ref["mo"])
     if lens is not None:
         o = torch.where(on[..., None, None], o.double(), ref["o"])
     assert_within(o, ref["o"], tol, "o")
@@ -238,6 +238,40 @@ def test_rows_of_very_different_size(dtype):
     S, o = d["S"].clone(), torch.empty_like(d["v"])
     run("prefill", S, d, o)
     check_prompt(d, S, o)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("decay", [0.0, -0.5, -1.1, -5.0])
+@pytest.mark.parametrize("zero", ["q", "k", "v", "all"])
+def test_zero_rows(dtype, decay, zero):
+    """Rows of zeros at a prompt's start and within it (their scales are free),
+    next to decays whose factors across a chunk span the range of a float."""
+    T = 150
+    d = make_linattn(23, 1, T, 1, 2, TYPES[dtype])
+    d["g"].fill_(decay)
+    for x in "qkv" if zero == "all" else zero:
+        d[x][:, :40] = 0
+        d[x][:, 70:75] = 0
+        d[x][:, 128:] = 0
+    S, o = d["S"].clone(), torch.empty_like(d["v"])
+    run("prefill", S, d, o)
+    # What the magnitudes of the terms do not cover:
+    # e^-5 a token takes whole sums below fp32; a factor under the smallest normal
+    # number, 2^-126, may read as 0.  It multiplies |k v| or |q.k v| of at most T
+    # tokens, or |S0 q| summed over 128 rows: each below 16, as q and k are
+    # (rounded) unit rows and |v|, |S0| are below 5.
+    assert max(float(d[x].abs().max()) for x in ("v", "S")) < 5
+    assert max(float(d[x].float().norm(dim=-1).max()) for x in "qk") < 2 ** 0.5
+    under = (T + 128) * 16 * 2.0 ** -126
+    # A score (q_t.k_s) e^{decay} is the sum of two fp16 numbers, the second
+    # off by up to 2^-25 (half the spacing of fp16's smallest numbers), in units
+    # of 2^22 (2^-14 |q_t|) (2^-14 2 w), |.| the largest element and w the row's
+    # largest |k_s| e^{decay} <= |k|: by 2^-30 |q_t| |k|, times |v_s| of 64 tokens.
+    # It shows where the tokens near t have v = 0 and the decays leave only
+    # small weights for the others.
+    top = {x: float(d[x].abs().max()) for x in "qkv"}
+    score = 2.0 ** -30 * top["q"] * top["k"] * 64 * top["v"]
+    check_prompt(d, S, o, floor_S=under, floor_o=under + score)
 
 
 @pytest.mark.parametrize("dtype", TYPES)
