@@ -801,25 +801,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ((size_t)w.b * P.T + (size_t)w.c * kC + 32 * half) * pitch + w.vi * kD + myrow;
       const F2 fs2 = pack(fs, fs), fv2 = pack(fv, fv);
       const int bad = min((int)badtok(it)[myrow], (int)badtok(it)[128 + myrow]) - 32 * half;
-      uint32_t qs[32], pv[32];
-      tmem_ld16_async(tl + T_QS + 32 * half, reinterpret_cast<uint32_t(&)[16]>(qs[0]));
-      tmem_ld16_async(tl + T_QS + 32 * half + 16, reinterpret_cast<uint32_t(&)[16]>(qs[16]));
-      tmem_ld16_async(tl + T_G + 32 * half, reinterpret_cast<uint32_t(&)[16]>(pv[0]));
-      tmem_ld16_async(tl + T_G + 32 * half + 16, reinterpret_cast<uint32_t(&)[16]>(pv[16]));
-      tmem_wait_ld(qs);
-      tmem_wait_ld(pv);
-      signal_ready<false>(acc_free);
-      const F2 *ca = reinterpret_cast<const F2 *>(vc + VCA + 32 * half);
-      const F2 *cb = reinterpret_cast<const F2 *>(vc + VCB + 32 * half);
       Out *p = op;
+#pragma unroll 1
+      for (int t0 = 0; t0 < 32; t0 += 16) {
+        uint32_t qs[16], pv[16];
+        tmem_ld16_async(tl + T_QS + 32 * half + t0, qs);
+        tmem_ld16_async(tl + T_G + 32 * half + t0, pv);
+        tmem_wait_ld(qs);
+        tmem_wait_ld(pv);
+        if (t0 == 16) signal_ready<false>(acc_free);
+        const F2 *ca = reinterpret_cast<const F2 *>(vc + VCA + 32 * half + t0);
+        const F2 *cb = reinterpret_cast<const F2 *>(vc + VCB + 32 * half + t0);
 #pragma unroll
-      for (int j = 0; j < 32; j += 2) {
-        const float2 y = unpack(fma2(mul2(pair(qs + j), fs2), ca[j / 2],
-                                     mul2(mul2(pair(pv + j), fv2), cb[j / 2])));
-        if (j < nv) *p = (Out)y.x;
-        p += pitch;
-        if (j + 1 < nv) *p = (Out)y.y;
-        p += pitch;
+        for (int j = 0; j < 16; j += 2) {
+          const float2 y = unpack(fma2(mul2(pair(qs + j), fs2), ca[j / 2],
+                                       mul2(mul2(pair(pv + j), fv2), cb[j / 2])));
+          if (j < nv - t0) *p = (Out)y.x;
+          p += pitch;
+          if (j + 1 < nv - t0) *p = (Out)y.y;
+          p += pitch;
+        }
       }
       // (the same thread's stores, so in order)
 #pragma unroll 1
@@ -845,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (it > 0) wait_bar(acc_free, (it - 1) & 1, fail);
           fence_after_sync();
           const uint32_t lo_k = desc_lo(kq, 16), lo_q = lo_k + (8 * kGrp >> 4);
-#pragma unroll
+#pragma unroll 1
           for (int ks = 0; ks < kD / 16; ++ks) {
             const uint64_t h = desc64(hi, lo_k + (kstep(ks) >> 4));
             const uint64_t l = desc64(hi, lo_k + ((kstep(ks) + 2048) >> 4));
@@ -858,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           commit_one(one, done_qk);
           wait_bar(rdy_s, it & 1, fail);
           fence_after_sync();
-#pragma unroll
+#pragma unroll 1
           for (int ks = 0; ks < kD / 16; ++ks) {
             const uint64_t h = desc64(hi, lo_q + (kstep(ks) >> 4));
             const uint64_t l = desc64(hi, lo_q + ((kstep(ks) + 2048) >> 4));
@@ -877,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_after_sync();
         {
           const uint32_t lo_k = desc_lo(kq, 1024);  // rows are K: two groups a step
-#pragma unroll
+#pragma unroll 1
           for (int ks = 0; ks < kC / 16; ++ks) {
             const uint64_t h = desc64(hi, lo_k + (ks * 2 * kGrp >> 4));
             const uint64_t l = desc64(hi, lo_k + ((ks * 2 * kGrp + 2048) >> 4));
@@ -892,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!kLocal) {
           wait_bar(rdy_p, it & 1, fail);
           fence_after_sync();
-#pragma unroll
+#pragma unroll 1
           for (int ks = 0; ks < kC / 16; ++ks) {
             const uint64_t h = desc64(hi_p, lo_p + (kstep(ks) >> 4));
             const uint64_t l = desc64(hi_p, lo_p + ((kstep(ks) + 8192) >> 4));
@@ -963,7 +964,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       G[1] = add2(G[0], G[1]);
       Two run = G[1];
-#pragma unroll
+#pragma unroll 1
       for (int off = 1; off < 32; off <<= 1) {
         const Two y = shfl_up2(run, off);
         if (lane >= off) run = add2(run, y);
@@ -987,13 +988,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (__any_sync(0xffffffffu, up)) {
         // growth: the largest Gamma_t - Gamma_s, s <= t (0 for decays)
         float lo = fminf(G[0].h, G[1].h), run_lo = lo;
-#pragma unroll
+#pragma unroll 1
         for (int off = 1; off < 32; off <<= 1) {
           const float y = __shfl_up_sync(0xffffffffu, run_lo, off);
           if (lane >= off) run_lo = fminf(run_lo, y);
         }
         float d = fmaxf(fmaxf(G[0].h, G[1].h) - run_lo, 0.f);
-#pragma unroll
+#pragma unroll 1
         for (int off = 16; off; off >>= 1) d = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, off));
         grow = (int)ceilf(fminf(d, 80.f));
       }
@@ -1018,7 +1019,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) r[i] = kx[i] < 127 ? -G[i].h - (float)kx[i] : none;
         float run_r = fmaxf(r[0], r[1]);
-#pragma unroll
+#pragma unroll 1
         for (int off = 1; off < 32; off <<= 1) {
           const float y = __shfl_up_sync(0xffffffffu, run_r, off);
           if (lane >= off) run_r = fmaxf(run_r, y);
