@@ -227,6 +227,15 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   return r;
 }
 
+// x - h, exactly
+__device__ __forceinline__ float less(float x, __half h) {
+  float r;
+  asm("fma.rn.f32.f16 %0, %1, %2, %3;"
+      : "=f"(r)
+      : "h"(__half_as_ushort(h)), "h"((unsigned short)0xbc00), "f"(x));
+  return r;
+}
+
 // The fp16 parts of two floats: hi = fp16(x) and, with kLo, lo = fp16(x - hi).
 template <bool kLo>
 __device__ __forceinline__ void split2(F2 v, uint32_t &hi, uint32_t &lo) {
@@ -234,9 +243,7 @@ __device__ __forceinline__ void split2(F2 v, uint32_t &hi, uint32_t &lo) {
   const __half2 h = __floats2half2_rn(x.x, x.y);
   hi = *reinterpret_cast<const uint32_t *>(&h);
   if (kLo) {
-    const float2 f = __half22float2(h);
-    const float2 d = unpack(fma2(pack(f.x, f.y), pack(-1.f, -1.f), v));
-    const __half2 l = __floats2half2_rn(d.x, d.y);
+    const __half2 l = __floats2half2_rn(less(x.x, __low2half(h)), less(x.y, __high2half(h)));
     lo = *reinterpret_cast<const uint32_t *>(&l);
   }
 }
@@ -364,74 +371,73 @@ __host__ __device__ constexpr uint32_t kstep(int ks) {
 template <bool kBf16>
 struct RowGroup {
   static constexpr uint32_t kRow = kBf16 ? 256 : 512;
-  F2 x[4][4];
-  float sc[4];
+  static constexpr int kN = kBf16 ? 4 : 8;
+  uint32_t x[4][kN];  // as staged
   __device__ __forceinline__ void read(const unsigned char *g8, int lane) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const unsigned char *st = g8 + (2 * i + (lane >> 4)) * kRow + (lane & 15) * 16;
-      const uint4 u = *reinterpret_cast<const uint4 *>(st);
-      const uint32_t q[4] = {u.x, u.y, u.z, u.w};
-      if (kBf16) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          x[i][j] = pack(__uint_as_float(q[j] << 16), __uint_as_float(q[j] & 0xffff0000u));
-      } else {
-        const uint4 v = *reinterpret_cast<const uint4 *>(st + 256);
-        const uint32_t z[4] = {v.x, v.y, v.z, v.w};
-        x[i][0] = pair(q);
-        x[i][1] = pair(q + 2);
-        x[i][2] = pair(z);
-        x[i][3] = pair(z + 2);
-      }
-    }
-  }
-  // Rows r0 + r >= n (behind the sequence's end) are zeros, whatever they hold.
-  __device__ __forceinline__ void clear(int r0, int n, int lane) {
-    if (r0 + 8 <= n) return;
+    g8 += (lane >> 4) * kRow + (lane & 15) * 16;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (r0 + 2 * i + (lane >> 4) >= n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[i][j] = 0ull;
+      for (int j = 0; j < kN; j += 4) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(g8 + 2 * i * kRow + 64 * j);
+        x[i][j] = u.x;
+        x[i][j + 1] = u.y;
+        x[i][j + 2] = u.z;
+        x[i][j + 3] = u.w;
+      }
   }
-  // Scale exponents of the rows (127: nothing but zeros), also to ex[8].
+  // Scale exponents of the rows to ex[8] (127: nothing but zeros).  The four
+  // rows of a lane are reduced together, half of them sent on at each step.
   __device__ __forceinline__ void scales(int *ex, int lane) {
     float m[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      m[i] = 0.f;
+      if (kBf16) {  // |x| by pairs, as integers: NaN above all
+        uint32_t u = x[i][0] & 0x7fff7fffu;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = unpack(x[i][j]);
-        m[i] = amax(m[i], f.x, f.y);
+        for (int j = 1; j < kN; ++j) u = __vmaxu2(u, x[i][j] & 0x7fff7fffu);
+        m[i] = __uint_as_float(max(u << 16, u & 0xffff0000u));
+      } else {
+        m[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < kN; j += 2)
+          m[i] = amax(m[i], __uint_as_float(x[i][j]), __uint_as_float(x[i][j + 1]));
       }
     }
-#pragma unroll
-    for (int d = 8; d; d >>= 1)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) m[i] = amax(m[i], __shfl_xor_sync(0xffffffffu, m[i], d));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = m[i] == 0.f ? 127 : scale_exp(m[i]);
-      if ((lane & 15) == 0) ex[2 * i + (lane >> 4)] = e;
-      sc[i] = pow2(e);
-    }
+    const bool b3 = lane & 8, b2 = lane & 4;
+    const float s0 = __shfl_xor_sync(0xffffffffu, b3 ? m[0] : m[2], 8);
+    const float s1 = __shfl_xor_sync(0xffffffffu, b3 ? m[1] : m[3], 8);
+    const float m0 = amax(b3 ? m[2] : m[0], s0), m1 = amax(b3 ? m[3] : m[1], s1);
+    float t = amax(b2 ? m1 : m0, __shfl_xor_sync(0xffffffffu, b2 ? m0 : m1, 4));
+    t = amax(t, __shfl_xor_sync(0xffffffffu, t, 2));
+    t = amax(t, __shfl_xor_sync(0xffffffffu, t, 1));
+    if ((lane & 3) == 0)
+      ex[(lane >> 1 & 6) + (lane >> 4)] = t == 0.f ? 127 : scale_exp(t);
   }
-  __device__ __forceinline__ void write(unsigned char *g8, int lane) {
-    const int m16 = lane & 15;
+  // (behind a __syncwarp: every row of the group is read, the exponents written)
+  __device__ __forceinline__ void write(unsigned char *g8, const int *ex, int lane) {
+    const int m16 = lane & 15, r1 = lane >> 4;
+    ex += r1;
+    g8 += r1 * 128;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = 2 * i + (lane >> 4);
-      const F2 f = pack(sc[i], sc[i]);
+      const float sc = pow2(ex[2 * i]);
+      const F2 f = pack(sc, sc);
       uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) split2<!kBf16>(mul2(x[i][j], f), hi[j], lo[j]);
+      for (int j = 0; j < 4; ++j) {
+        const F2 v = kBf16 ? pack(__uint_as_float(x[i][j] << 16),
+                                  __uint_as_float(x[i][j] & 0xffff0000u))
+                           : pair(&x[i][kBf16 ? 0 : 2 * j]);
+        split2<!kBf16>(mul2(v, f), hi[j], lo[j]);
+      }
+      // row r = 2 i + r1: blocks of 16 bytes at their place XOR r
       if (kBf16) {
-        *reinterpret_cast<uint4 *>(g8 + (m16 >> 3) * 1024 + r * 128 + (((m16 & 7) ^ r) << 4)) =
+        *reinterpret_cast<uint4 *>(g8 + (m16 >> 3) * 1024 + i * 256 +
+                                   ((((m16 & 7) ^ r1) << 4) ^ (i << 5))) =
             make_uint4(hi[0], hi[1], hi[2], hi[3]);
       } else {
-        unsigned char *p = g8 + r * 128 + (((m16 >> 1) ^ r) << 4) + (m16 & 1) * 8;
+        unsigned char *p = g8 + i * 256 + ((((m16 >> 1) ^ r1) << 4) ^ (i << 5)) + (m16 & 1) * 8;
         *reinterpret_cast<uint2 *>(p) = make_uint2(hi[0], hi[1]);
         *reinterpret_cast<uint2 *>(p + 1024) = make_uint2(hi[2], hi[3]);
         *reinterpret_cast<uint2 *>(p + 2048) = make_uint2(lo[0], lo[1]);
@@ -779,12 +785,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int grp = warp - 8; grp < (kLocal ? 8 : 16); grp += 8) {
           unsigned char *g8 = gb + OFF_KQ + par * kKQ + grp * kGrp;
+          const int nr = nx.valid() - 8 * (grp & 7);
+          if (nr < 8) {  // rows behind the end are zeros, whatever they hold
+#pragma unroll 1
+            for (uint32_t at = max(nr, 0) * kRow + 16 * lane; at < kGrp; at += 512)
+              *reinterpret_cast<uint4 *>(g8 + at) = make_uint4(0u, 0u, 0u, 0u);
+            __syncwarp();
+          }
+          int *ex = rowexp(nx.it) + 8 * grp;
           RowGroup<kBf16> g;
           g.read(g8, lane);
-          g.clear(8 * (grp & 7), nx.valid(), lane);
-          g.scales(rowexp(nx.it) + 8 * grp, lane);
-          __syncwarp();  // every row of the group is read
-          g.write(g8, lane);
+          g.scales(ex, lane);
+          __syncwarp();
+          g.write(g8, ex, lane);
         }
         signal_ready<true>(rdy_kq + 8 * par);
       }
