@@ -34,7 +34,7 @@
 // units): 8 warps A hold the state and make its operand and the two V
 // operands (the next chunk's V maxima under this one's KV product); 8 warps B turn the staged q and k rows into operands in place,
 // make P from G, and the output from QS and PV; one warp issues the products,
-// one copies rows by TMA (a chunk ahead), one computes the decay vectors.
+// one copies rows by TMA (a chunk ahead), two compute the decay vectors.
 // All meet through mbarriers; the chunks of successive units form one
 // sequence, so a unit's first loads run under the previous one's last chunk.
 //
@@ -92,9 +92,10 @@ constexpr uint32_t kSmemAlloc = kSmemUsed + 1024;   // room to align the base
 static_assert(kSmemAlloc <= 232448, "shared memory");
 
 // TMEM columns (512): the KV product, the state operand (hi, lo), the V and
-// decayed V operands (hi, lo), QS, and G, which PV overwrites once P is made.
+// decayed V operands (hi, lo), QS and G.  PV takes the decayed operand's columns,
+// which KV has read, so that the next QK need not wait for the output.
 constexpr uint32_t T_D = 0, T_SOP = 128, T_VOP = 256, T_WOP = 320, T_QS = 384,
-                   T_G = 448;
+                   T_G = 448, T_PV = T_WOP;
 
 __host__ __device__ constexpr uint32_t idesc16(int M, int N, int b_mn) {
   // fp16 operands (format 0), fp32 accumulator; B MN-major if b_mn
@@ -105,7 +106,7 @@ __host__ __device__ constexpr uint32_t idesc16(int M, int N, int b_mn) {
 struct Args {
   float *S;             // [B][vh][128][128], in/out
   float *ws_state;      // [B vh][nseg][128][128]: own sums, then start states
-  double *ws_decay;     // [B vh][nseg]: log2 of a segment's decay
+  double *ws_decay;     // [B vh][nseg][2]: log2 of a segment's decay, in two parts
   const float *g;
   void *o;
   const int *lens;
@@ -626,8 +627,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       {
         const F2 fa = pack(pow2(ea), pow2(ea));
         if (!kLocal) {
-          // V's columns are free once the previous chunk's PV has read them
-          if (it > 0) wait_bar(done_o, (it - 1) & 1, fail);
+          // V's columns are free once the previous chunk's PV has read them, the
+          // decayed ones once the output has been made of it
+          if (it > 0) wait_bar(acc_free, (it - 1) & 1, fail);
           fence_after_sync();
           if (half == 0) lanef(it)[128 + myrow] = pow2(-ea);
         }
@@ -819,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t0 = 0; t0 < 32; t0 += 16) {
         uint32_t qs[16], pv[16];
         tmem_ld16_async(tl + T_QS + 32 * half + t0, qs);
-        tmem_ld16_async(tl + T_G + 32 * half + t0, pv);
+        tmem_ld16_async(tl + T_PV + 32 * half + t0, pv);
         tmem_wait_ld(qs);
         tmem_wait_ld(pv);
         if (t0 == 16) signal_ready<false>(acc_free);
@@ -856,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t kq = sb + OFF_KQ + (it & 1) * kKQ;
         wait_bar(rdy_kq + 8 * (it & 1), (it >> 1) & 1, fail);
         if (!kLocal) {
-          if (it > 0) wait_bar(acc_free, (it - 1) & 1, fail);
+          // (G is free: P of the last chunk is made)
           fence_after_sync();
           const uint32_t lo_k = desc_lo(kq, 16), lo_q = lo_k + (8 * kGrp >> 4);
 #pragma unroll 1
@@ -871,6 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           commit_one(one, done_qk);
           wait_bar(rdy_s, it & 1, fail);
+          if (it > 0) wait_bar(acc_free, (it - 1) & 1, fail);
           fence_after_sync();
 #pragma unroll 1
           for (int ks = 0; ks < kD / 16; ++ks) {
@@ -905,16 +908,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         commit_one(one, kq_free + 8 * (it & 1));
         if (!kLocal) {
           wait_bar(rdy_p, it & 1, fail);
+          wait_bar(done_kv, it & 1, fail);
           fence_after_sync();
 #pragma unroll 1
           for (int ks = 0; ks < kC / 16; ++ks) {
             const uint64_t h = desc64(hi_p, lo_p + (kstep(ks) >> 4));
             const uint64_t l = desc64(hi_p, lo_p + ((kstep(ks) + 8192) >> 4));
             const uint32_t a = tm + T_VOP + 8u * ks;
-            mma_ts(one, tm + T_G, a, h, idn, ks > 0);
+            mma_ts(one, tm + T_PV, a, h, idn, ks > 0);
             if (kLo) {
-              mma_ts(one, tm + T_G, a, l, idn, 1u);
-              mma_ts(one, tm + T_G, a + 32u, h, idn, 1u);
+              mma_ts(one, tm + T_PV, a, l, idn, 1u);
+              mma_ts(one, tm + T_PV, a + 32u, h, idn, 1u);
             }
           }
           commit_one(one, done_o);
@@ -954,13 +958,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     cta_end();
-  } else if (warp == kGates) {
+  } else {
     // ====================================================== decay vectors
-    // Lane l has tokens 2 l and 2 l + 1; log decays to base 2.
+    // Two warps, chunk about (a chunk's vectors take one warp longer than the
+    // other roles take for the chunk).  Lane l has tokens 2 l and 2 l + 1; log
+    // decays to base 2.
+    const int mine = warp - kGates;
     double total = 0.0;
     for (Walk<kLocal> w(P); w.next();) {
       const int it = w.it, nv = w.valid();
       if (w.first) total = 0.0;
+      const bool store = kLocal && w.last() && lane == 0;
+      double *sum = P.ws_decay + 2 * ((size_t)w.head * P.nseg + w.seg) + mine;
+      if ((it & 1) != mine) {
+        if (store) *sum = total;
+        continue;
+      }
       const size_t base = P.g_head ? (size_t)w.vi
                                    : ((size_t)w.b * P.T + (size_t)w.c * kC) * P.vh + w.vi;
       const size_t step = P.g_head ? 0 : (size_t)P.vh;
@@ -1088,7 +1101,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(vecs + 8 * (it & 3));
-        if (kLocal && w.last()) P.ws_decay[(size_t)w.head * P.nseg + w.seg] = total;
+        if (store) *sum = total;
       }
     }
     if (kLocal) {  // segments without a chunk: no decay
@@ -1096,11 +1109,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int u = blockIdx.x; u < P.units; u += gridDim.x) {
         w.u = u;
         w.decode();
-        if (w.c >= w.c_hi && lane == 0) P.ws_decay[(size_t)w.head * P.nseg + w.seg] = 0.0;
+        if (w.c >= w.c_hi && lane == 0)
+          P.ws_decay[2 * ((size_t)w.head * P.nseg + w.seg) + mine] = 0.0;
       }
     }
-    cta_end();
-  } else {
     cta_end();
   }
   }
@@ -1122,7 +1134,7 @@ __global__ void __launch_bounds__(256)
       break;
     }
     const float4 d = *w;
-    const double l = decay[head * nseg + i];
+    const double *d2 = decay + 2 * (head * nseg + i), l = d2[0] + d2[1];
     const float h = (float)l, a0 = exp2f(h), a = fmaf(a0, (float)(l - (double)h) * 0.69314718f, a0);
     *w = s;
     s.x = fmaf(a, s.x, d.x);
@@ -1202,7 +1214,7 @@ cudaError_t launch(const CUtensorMap *m, const Args &a, cudaStream_t stream) {
 size_t linattn_prefill_workspace_bytes(int B, int vh, int T, bool) {
   const size_t heads = (size_t)B * vh;
   const size_t nseg = (size_t)plan(B, vh, T);
-  const size_t bytes = heads * nseg * (kD * kD * sizeof(float) + sizeof(double));
+  const size_t bytes = heads * nseg * (kD * kD * sizeof(float) + 2 * sizeof(double));
   return nseg == 1 ? 0 : (bytes + 15) & ~(size_t)15;
 }
 
