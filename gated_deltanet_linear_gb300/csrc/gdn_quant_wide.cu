@@ -46,6 +46,7 @@ constexpr int kRowsW = 128;   // weight rows of a CTA
 constexpr int kStage = 128;   // k elements of a stage
 constexpr uint32_t kWaitLimit = 1u << 24;
 constexpr int kATile = kRowsW * kStage * 2;
+constexpr int kScales = 4 * 4 * kRowsW * 4;  // of four stages, up to 4 groups each
 
 template <bool kBf16, int kNC>
 __host__ __device__ constexpr int b_tile() {  // all parts of x
@@ -54,8 +55,8 @@ __host__ __device__ constexpr int b_tile() {  // all parts of x
 template <bool kBf16, int kNC>
 __host__ __device__ constexpr int smem_bytes() {
   // two stages, the sums received from the cluster (up to 8 slices of at most
-  // ceil(kNC / c) rows of y), barriers, room to align
-  return 2 * (kATile + b_tile<kBf16, kNC>()) + (kNC + 8) * kRowsW * 4 + 64 + 1024;
+  // ceil(kNC / c) rows of y), the scales of four stages, barriers, room to align
+  return 2 * (kATile + b_tile<kBf16, kNC>()) + (kNC + 8) * kRowsW * 4 + kScales + 64 + 1024;
 }
 
 struct WideArgs {
@@ -113,7 +114,9 @@ __global__ void __launch_bounds__(kThreads, 1) quant_wide_kernel(const WideArgs 
   unsigned char *gb = smem_raw + (sb - raw);
   constexpr uint32_t kStageBytes = kATile + kTerms * kBTile;
   float *recv = reinterpret_cast<float *>(gb + 2 * kStageBytes);  // [slice][row of y][weight row]
-  const uint32_t bar = sb + 2 * kStageBytes + (kNC + 8) * kRowsW * 4;  // 2 mbarriers
+  // scales [stage & 3][group][weight row]
+  float *scl = recv + (kNC + 8) * kRowsW;
+  const uint32_t bar = sb + 2 * kStageBytes + (kNC + 8) * kRowsW * 4 + kScales;  // 2 mbarriers
   volatile uint32_t *slot = reinterpret_cast<volatile uint32_t *>(gb + (bar - sb) + 16);
 
   const cg::cluster_group cl = cg::this_cluster();
@@ -142,11 +145,14 @@ __global__ void __launch_bounds__(kThreads, 1) quant_wide_kernel(const WideArgs 
   const int ns = (int)((long long)P.stages * (crank + 1) / csize) - s_lo;
   const int groups = P.K / kGroup;
   const size_t wrow = (size_t)P.K / 2;
-  // this thread's piece of a stage: 32 codes of weight row tid >> 2, and the
-  // weight row whose sums it keeps (rows behind the last one: the last one's)
+  // this thread's piece of a stage: 32 codes of weight row tid >> 2 and, of that
+  // row, the scale of group `piece` (rows behind the last one: the last one's).
+  // The scales go through shared memory to the threads that keep a row's sums:
+  // a load of 32 rows' scales by each of them took as long as the conversion
+  // (32 lines a request).
   const int arow = tid >> 2, piece = tid & 3;
   const uint8_t *wp = P.qw + (size_t)min(n0 + arow, P.N - 1) * wrow + 16 * piece;
-  const __half *sp = P.sc + (size_t)min(n0 + 32 * quad + lane, P.N - 1) * groups;
+  const __half *sp = P.sc + (size_t)min(n0 + arow, P.N - 1) * groups;
 
   bool failed = false;
   uint32_t done = 0;  // stages issued so far, over all passes
@@ -158,22 +164,24 @@ __global__ void __launch_bounds__(kThreads, 1) quant_wide_kernel(const WideArgs 
     // Two stages of this slice in registers, ahead of use.
     uint4 w[2];
     float xv[2][kParts][8];
-    __half sn[2][kGroups];
-    // scales of the two stages whose products are under way
-    __half sc[2][kGroups];
+    __half sn[2];
+    const T *xp[kParts];  // this thread's parts of x, nullptr behind the last row
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+      const int e = tid + i * kThreads, r = e >> 4;
+      xp[i] = r < nr ? static_cast<const T *>(P.x) + (size_t)(r0 + r) * P.K + 8 * (e & 15)
+                     : nullptr;
+    }
     auto fetch = [&](int u, int s) {
       const int k0 = (s_lo + s) * kStage;
       // (a group behind the last one has zeros of x against any scale)
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g)
-        sn[u][g] = __ldg(sp + min((s_lo + s) * kGroups + g, groups - 1));
+      if (piece < kGroups) sn[u] = __ldg(sp + min((s_lo + s) * kGroups + piece, groups - 1));
       w[u] = make_uint4(0, 0, 0, 0);
       if (k0 + 32 * piece < P.K) w[u] = __ldg(reinterpret_cast<const uint4 *>(wp + k0 / 2));
 #pragma unroll
       for (int i = 0; i < kParts; ++i) {
-        const int e = tid + i * kThreads, r = e >> 4, k = k0 + 8 * (e & 15);
-        const bool on = r < nr && k < P.K;
-        const T *p = static_cast<const T *>(P.x) + (on ? (size_t)(r0 + r) * P.K + k : 0);
+        const bool on = xp[i] != nullptr && k0 + 8 * (tid & 15) < P.K;
+        const T *p = xp[i] + k0;
         const uint4 z = make_uint4(0, 0, 0, 0);
         const uint4 a = on ? __ldg(reinterpret_cast<const uint4 *>(p)) : z;
         const uint32_t q[4] = {a.x, a.y, a.z, a.w};
@@ -207,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_wide_kernel(const WideArgs 
             tmem_ld<kCols>(tmem + ((uint32_t)(32 * quad) << 16) +
                                (uint32_t)(((before & 1) * kGroups + g) * kNC + part * kCols),
                            d);
-            const float f = __half2float(sc[u][g]);
+            const float f = scl[((before & 3) * 4 + g) * kRowsW + 32 * quad + lane];
 #pragma unroll
             for (int i = 0; i < kCols; ++i) acc[i] = fmaf(f, d[i], acc[i]);
           }
@@ -215,8 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_wide_kernel(const WideArgs 
         if (s >= ns) continue;
         const uint32_t at = base + (uint32_t)s;
         unsigned char *A = gb + (at & 1) * kStageBytes, *B = A + kATile;
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) sc[u][g] = sn[u][g];
+        if (piece < kGroups) scl[((at & 3) * 4 + piece) * kRowsW + arow] = __half2float(sn[u]);
         {
           const uint32_t word[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
 #pragma unroll
