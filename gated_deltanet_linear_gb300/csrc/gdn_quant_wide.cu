@@ -311,20 +311,31 @@ __global__ void __launch_bounds__(kThreads, 1) quant_wide_kernel(const WideArgs 
     } else {
       // rank c adds up rows c * per .. of y
       const int per = (kNC + csize - 1) / csize;
+      int to = (unsigned)(part * kCols) / (unsigned)per, c = part * kCols - to * per;
+      const int at = crank * per * kRowsW + 32 * quad + lane;
+      float *dst = cl.map_shared_rank(recv, to) + at;
 #pragma unroll
       for (int i = 0; i < kCols; ++i) {
-        const int col = part * kCols + i, to = (unsigned)col / (unsigned)per;
-        cl.map_shared_rank(recv, to)[((size_t)crank * per + (col - to * per)) * kRowsW + 32 * quad +
-                                     lane] = acc[i];
+        dst[c * kRowsW] = acc[i];
+        if (++c == per && i + 1 < kCols) {
+          c = 0;
+          dst = cl.map_shared_rank(recv, ++to) + at;
+        }
       }
       cl.sync();
-      for (int e = warp; e < 4 * per; e += kThreads / 32) {
-        // (e & 3 is this warp's quadrant: 16 warps step by whole quadrants)
-        const int c = e >> 2;
-        float v = 0.f;
-        for (int q = 0; q < csize; ++q)
-          v += recv[((size_t)q * per + c) * kRowsW + 32 * quad + lane];
-        if (crank * per + c < kNC) put(crank * per + c, v);
+      // (4 columns a time, one by a group of four warps; 32 rows a warp)
+      const float *src = recv + 32 * quad + lane;
+#pragma unroll 2
+      for (int c = part; c < per; c += 4) {
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (q < csize) v[q] = src[(q * per + c) * kRowsW];
+        float sum = v[0];
+#pragma unroll
+        for (int q = 1; q < 8; ++q)
+          if (q < csize) sum += v[q];
+        if (crank * per + c < kNC) put(crank * per + c, sum);
       }
       if (r0 + kNC < P.rows) cl.sync();  // read before the next pass writes
     }
