@@ -231,9 +231,9 @@ __global__ void __launch_bounds__(kThreads, 1) quant_wide_kernel(const WideArgs 
             // (two pieces of a row lie in tiles that share banks: other order)
             const bool odd = piece >> 1;
             uint32_t r[4];
-            codes(odd ? word[i ^ 1] : word[i], r);
+            codes(odd ? word[i ^ 2] : word[i], r);
             *reinterpret_cast<uint4 *>(
-                A + sw128_off(kRowsW, arow, 32 * piece + 8 * (odd ? i ^ 1 : i), 2)) =
+                A + sw128_off(kRowsW, arow, 32 * piece + 8 * (odd ? i ^ 2 : i), 2)) =
                 make_uint4(r[0], r[1], r[2], r[3]);
           }
         }
