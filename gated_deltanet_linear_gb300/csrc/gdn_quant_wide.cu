@@ -78,10 +78,6 @@ __device__ __forceinline__ void codes(uint32_t u, uint32_t (&r)[4]) {
   }
 }
 
-__device__ __forceinline__ uint32_t bits(__nv_bfloat162 v) {
-  return *reinterpret_cast<uint32_t *>(&v);
-}
-
 template <int kN>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&r)[kN]) {
   if constexpr (kN == 16) {
@@ -254,11 +250,12 @@ __global__ void __launch_bounds__(kThreads, 1) quant_wide_kernel(const WideArgs 
               uint32_t o[4];
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(x[j], x[j + 4]);
-                const float2 f = __bfloat1622float2(h);
-                x[j] -= f.x;
-                x[j + 4] -= f.y;
-                o[j] = bits(h);
+                // (cut off, so no finite element becomes infinite; the third
+                // part is exact: 3 x 8 bits)
+                const uint32_t p = __float_as_uint(x[j]), q = __float_as_uint(x[j + 4]);
+                o[j] = __byte_perm(p, q, 0x7632);
+                x[j] -= __uint_as_float(p & 0xffff0000u);
+                x[j + 4] -= __uint_as_float(q & 0xffff0000u);
               }
               *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
             }

@@ -82,6 +82,18 @@ def test_ranges(rows):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("rows", [1, 5, 40])
+def test_large_elements(dtype, rows):
+    """Elements of 2^112, the largest that every group's sum of code x (before
+    its scale) is promised to stay finite for."""
+    x, qw, sc = make_quant(5, rows, 60, 256, 128, TYPES[dtype])
+    x.copy_(torch.where(x > 0, 2.0 ** 112, -2.0 ** 112))
+    check(x, qw, sc)
+    x.fill_(2.0 ** 112)
+    check(x, qw, sc)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", [1, 5, 40])
 def test_non_finite_rows_stay_apart(dtype, rows):
     x, qw, sc = make_quant(4, rows + 2, 100, 256, 64, TYPES[dtype])
     y0 = check(x, qw, sc)
