@@ -51,8 +51,10 @@
  *   - Precision: fp32 throughout (expf from CUDA's math library, fused
  *     multiply-adds, fixed reduction trees), except the chunked prefill
  *     modes, whose tensor-core products take bf16 operands (see
- *     gdn_prefill).  Results are deterministic: the same inputs and shape
- *     give the same bits on every call.
+ *     gdn_prefill), and gdn_linattn_prefill and gdn_quant_linear, whose
+ *     operands are sums of 16-bit numbers or exact codes (see there).
+ *     Results are deterministic: the same inputs and shape give the same
+ *     bits on every call.
  */
 #ifndef GDN_GB300_H
 #define GDN_GB300_H
@@ -241,11 +243,13 @@ int gdn_prefill_timeouts(unsigned int *count);
  * gdn_wait_timeouts - (an interface addition with no counterpart in the
  * articles) number of bounded waits, since the library was loaded on the
  * current device, that ran out in any kernel: the chunked prefill's
- * tensor-core waits (as gdn_prefill_timeouts) and the multi-token update's
+ * tensor-core waits (as gdn_prefill_timeouts), the multi-token update's
  * waits for its token inputs (gdn_step_m with M > 1 or checkpoints, the
- * fp32 prefill, the layer step; device-resident inputs).  A CTA whose wait
- * runs out writes NaN into every state, checkpoint and o element it had not
- * yet produced, so the failure also shows in the results themselves.
+ * fp32 prefill, the layer step; device-resident inputs), gdn_linattn_prefill
+ * and gdn_quant_linear for many rows.  A CTA whose wait runs out writes NaN
+ * into every state, checkpoint, o and y element it had not yet produced
+ * (gdn_linattn_prefill: into all that it was to produce), so the failure also
+ * shows in the results themselves.
  * Synchronises the current device.  Expected to stay 0.
  */
 int gdn_wait_timeouts(unsigned int *count);
@@ -453,6 +457,18 @@ size_t gdn_linattn_prefill_workspace(const gdn_shape *shape, int T, int dtype);
  *          smaller, GDN_EINVAL if NULL where bytes are needed); calls that
  *          may overlap on the GPU need one each.
  * 1 <= T <= GDN_MAX_TOKENS and T * vh < 2^31 (GDN_ERANGE otherwise).
+ * Numbers: chunks of 64 tokens on tensor cores.  fp32 operands are the sum of
+ * two fp16 numbers (22 bits) scaled by rows or columns, bf16 ones a single
+ * fp16 (the scores and the state that enter o are then rounded to 11 bits;
+ * the state itself is kept in fp32), every sum is fp32: about 1e-6 relative
+ * error of S and of an fp32 o, where a step's is 2e-7.  Weights e^{sum of g}
+ * below 2^-126 may count as 0, and within 64 tokens g may grow by up to a
+ * factor of 2^80.  The same call gives the same bits; another B or T may cut
+ * the sequences elsewhere and differ in the last ones.
+ * What is not finite stays with its heads and never reaches a token before
+ * its own: in q it makes its row of o not finite, in v its column from its
+ * token on, in k or g (other than g = -inf, which empties the state) the
+ * whole head from its token on.
  */
 int gdn_linattn_prefill(const gdn_shape *shape, int T, int dtype, int decay,
                         float scale, float *S, const void *q, const void *k,
@@ -478,7 +494,10 @@ int gdn_linattn_prefill(const gdn_shape *shape, int T, int dtype, int decay,
  *   group   32, 64 or 128; K a positive multiple of it (GDN_ESHAPE otherwise)
  * N, K <= GDN_QUANT_MAX_DIM, rows <= GDN_MAX_TOKENS (GDN_ERANGE otherwise);
  * rows == 0 or N == 0 is a no-op.  Sums are fp32; results are the same bits
- * on every call.
+ * on every call.  A group's sum of x code is made before its scale is applied:
+ * it stays finite for |x| up to 2^112.  A row of x with an element that is not
+ * finite gives results that are not finite (NaN also where the formula has an
+ * infinity), in its own row of y alone.
  */
 int gdn_quant_linear(int rows, int N, int K, int group, int dtype,
                      const void *x, const unsigned char *qw,

@@ -16,6 +16,9 @@ values, mS for the state and mo for an output):
 """
 
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -24,6 +27,7 @@ import gated_deltanet_linear_gb300 as gdn
 from linattn_ref import D, assert_within, half_step, linattn, make_linattn
 
 pytestmark = pytest.mark.gpu
+HERE = os.path.dirname(os.path.abspath(__file__))
 TYPES = {"fp32": torch.float32, "bf16": torch.bfloat16}
 
 
@@ -335,6 +339,72 @@ def test_graph_replay_and_streams(call, T):
         once()
     stream.synchronize()
     assert torch.equal(S, S_ref) and torch.equal(o, o_ref)
+
+
+def test_calls_at_once():
+    """A prompt, tokens and projections on three streams at the same time, with
+    workspaces of their own, against the same calls one after the other."""
+    from linattn_ref import make_quant
+    p = make_linattn(51, 3, 700, 2, 6)
+    n = make_linattn(52, 9, 5, 2, 6, torch.bfloat16)
+    xs = [make_quant(53 + r, r, 900, 1024, 64) for r in (3, 40)]
+    ws = workspace(p)
+
+    def outputs():
+        return ([p["S"].clone(), torch.empty_like(p["v"]), n["S"].clone(), torch.empty_like(n["v"])]
+                + [torch.empty(x.shape[0], 900, device="cuda") for x, _, _ in xs])
+
+    def prompts(r, stream=None):
+        for _ in range(6):
+            gdn.gdn_linattn_prefill(r[0], p["q"], p["k"], p["v"], p["g"], r[1], workspace=ws,
+                                    stream=stream)
+
+    def tokens(r, stream=None):
+        for _ in range(40):
+            gdn.gdn_linattn_step_m(r[2], r[2], None, n["q"], n["k"], n["v"], n["g"], r[3],
+                                   stream=stream)
+
+    def projections(r, stream=None):
+        for _ in range(30):
+            for (x, qw, sc), y in zip(xs, r[4:]):
+                gdn.gdn_quant_linear(x, qw, sc, y, stream=stream)
+
+    ref, got = outputs(), outputs()
+    for f in (prompts, tokens, projections):
+        f(ref)
+    torch.cuda.synchronize()
+    for f in (prompts, tokens, projections):
+        f(got, torch.cuda.Stream())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(ref, got))
+    assert gdn.gdn_wait_timeouts() == 0
+
+
+def test_first_call_captured():
+    """In a new process the first call of each entry is captured and replayed."""
+    code = """
+import sys; sys.path[:0] = [{root!r}, {tests!r}]
+import torch, gated_deltanet_linear_gb300 as gdn
+from linattn_ref import make_linattn, make_quant
+p = make_linattn(1, 1, 600, 1, 2); n = make_linattn(2, 2, 3, 1, 2)
+xs = [make_quant(r, r, 300, 512, 32) for r in (2, 30)]
+ws = torch.empty(gdn.gdn_linattn_prefill_workspace(1, 1, 2, 600), dtype=torch.uint8, device="cuda")
+def outs():
+    return [p["S"].clone(), torch.empty_like(p["v"]), n["S"].clone(), torch.empty_like(n["v"])] + [
+        torch.zeros(x.shape[0], 300, device="cuda") for x, _, _ in xs]
+def calls(r):
+    gdn.gdn_linattn_prefill(r[0], p["q"], p["k"], p["v"], p["g"], r[1], workspace=ws)
+    gdn.gdn_linattn_step_m(r[2], r[2], None, n["q"], n["k"], n["v"], n["g"], r[3])
+    for (x, qw, sc), y in zip(xs, r[4:]): gdn.gdn_quant_linear(x, qw, sc, y)
+a, b = outs(), outs()
+graph = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph): calls(a)
+graph.replay(); calls(b); torch.cuda.synchronize()
+assert all(torch.equal(x, y) for x, y in zip(a, b))
+""".format(root=os.path.dirname(HERE), tests=HERE)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 def test_offsets_beyond_32_bits():
