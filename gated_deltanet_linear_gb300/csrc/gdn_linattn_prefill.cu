@@ -936,6 +936,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (Walk<kLocal> w(P); w.next();) {
       it = w.it;
       const uint32_t reg = sb + OFF_KQ + (it & 1) * kKQ, st = staged + 8 * (it & 1);
+      // a unit's state on its way to L2 while the last chunk of the one before
+      // is worked on
+      if (!kLocal && w.first && lane == 0) {
+        const size_t at = ((size_t)w.head * P.nseg + w.seg) * kD * kD;
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                         (P.nseg > 1 ? P.ws_state : P.S) + at),
+                     "r"((uint32_t)(kD * kD * sizeof(float)))
+                     : "memory");
+      }
       if (it >= 2) wait_bar(kq_free + 8 * (it & 1), ((it - 2) >> 1) & 1, fail);
       if (lane == 0) {
         mbar_expect(st, (kLocal ? 1u : 2u) * kC * kRow);
