@@ -25,7 +25,9 @@
 // give the bits of M launches.
 //
 // Bound by HBM: 128 KB of state per head against three FP32 lane operations
-// per state element and token.
+// per state element and token.  64 sequences x 48 heads: one token 58.4 us
+// (405 MB, 103 % of the copy rate), 4 tokens 75 us, 8 tokens 111 us, where the
+// shared-memory reads of k and q are the bound.
 
 #include <cuda_bf16.h>
 

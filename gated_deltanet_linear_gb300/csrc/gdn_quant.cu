@@ -12,10 +12,7 @@
 //
 //   fp32 x   two columns per row: x 2^e = hi + lo in fp16 (22 bits; e by row
 //            and block of 128, so that the largest element is in [2^14, 2^15))
-//   bf16 x   one column per row, as it is; the codes as bf16, left at 136 + c:
-//            a group's product starts at -136 times the sum of its x (fp32)
-//            instead of 0, which costs 5 of the 24 bits of sums that are
-//            rounded to 8 at the end
+//   bf16 x   one column per row, as it is; the codes as bf16
 //
 // Weights.  A warp takes blocks of 16 rows x 256 codes (128 bytes of each row)
 // through a ring of its own in shared memory: asynchronous 16-byte copies, 8
@@ -35,6 +32,12 @@
 // share, a warp stores its partial sums in a slot of its own in the CTA that
 // adds up the tile; slots are added in a fixed order, so results are the same
 // bits on every call.
+//
+// One row against 10240 x 5120: 11.1 us (27 MB from L2 and HBM; 2.4 TB/s), 8
+// rows of fp32 14.9, of bf16 14.7, 16 rows of bf16 19.0; 48 x 5120 (a layer's
+// gates) 4.6 us.  What is left is a start of 2 us, the x that every CTA converts,
+// the products' issue (the SIMD lanes unpack 8 codes in 14 instructions) and for
+// clusters two barriers.
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -105,12 +108,19 @@ __device__ __forceinline__ int share(unsigned total, int w) {
 // 8 codes of a word as four registers of two 16-bit floats: elements (0, 4),
 // (1, 5), (2, 6), (3, 7).  A code c is stored as c + 16 (c < 0); flipping its
 // bit 3 gives c + 8, which as the low mantissa bits of 1024 (fp16) or 128
-// (bf16) is 1032 + c or 136 + c.
+// (bf16) is 1032 + c or 136 + c.  (The 136 left in, and a group's product started
+// at -136 sum x, was no faster and left rounding errors of a sum of |x| where
+// the codes are zeros.)
 template <bool kBf16>
 __device__ __forceinline__ void codes(uint32_t u, uint32_t (&r)[4]) {
   if (kBf16) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = ((u >> (4 * i)) & 0x000f000fu) ^ 0x43084308u;
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t v = ((u >> (4 * i)) & 0x000f000fu) ^ 0x43084308u;
+      const __nv_bfloat162 d = __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&v),
+                                       __floats2bfloat162_rn(-136.f, -136.f));
+      r[i] = *reinterpret_cast<const uint32_t *>(&d);
+    }
   } else {
     const __half2 m = __floats2half2_rn(-1032.f, -1032.f);
     const __half2 s = __floats2half2_rn(0.0625f, 0.0625f), m16 = __floats2half2_rn(-72.f, -72.f);
@@ -204,8 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int gr = lane >> 2, t = lane & 3;
 
   // shared memory: the warps' rings, partial sums, x (a column is round_blocks *
-  // 512 + 64 bytes), then by block: 2^-e of each row (fp32) or -136 sums of each
-  // group (bf16), then by slice and tile: the first warp in it and the number
+  // 512 + 64 bytes), then by block: 2^-e of each row (fp32), then by slice and tile: the first warp in it and the number
   // of warps, then the scales of the round's rows
   const uint32_t xstride = (uint32_t)P.round_blocks * kXBlock + 64;
   const uint32_t ring =
@@ -215,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       reinterpret_cast<unsigned char *>(slots) + (size_t)P.slots * kTile * kRowsX * 4;
   float *side = reinterpret_cast<float *>(xs + (size_t)P.columns * xstride);
   unsigned char *tab = reinterpret_cast<unsigned char *>(
-      side + P.round_blocks * (kBf16 ? kSc * kCols : kRowsX));
+      side + (kBf16 ? 0 : P.round_blocks * kRowsX));
   __half *scs = reinterpret_cast<__half *>(
       smem + (((size_t)(tab - smem) + 2 * csize * P.round_tiles + 15) & ~(size_t)15));
   // this lane's column of x in each n8 tile (columns that are not there: any)
@@ -350,11 +359,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (turn + 1 < turns) x = read();
             unsigned char *dst = xs + cb * (kXBlock / 2) + p * 16;
             if (kBf16) {
-              float sum = 0.f;
-#pragma unroll
-              for (int j = 0; j < 8; ++j) sum += c.v[j];
-#pragma unroll
-              for (int d = kGroup / 16; d; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
               if (cr < nr) {
                 // elements (0, 4), (1, 5), (2, 6), (3, 7)
                 uint32_t o[4];
@@ -362,8 +366,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < 4; ++j)
                   o[j] = __byte_perm(__float_as_uint(c.v[j]), __float_as_uint(c.v[j + 4]), 0x7632);
                 *reinterpret_cast<uint4 *>(dst + cr * xstride) = make_uint4(o[0], o[1], o[2], o[3]);
-                if ((p & (kGroup / 8 - 1)) == 0)
-                  side[(cb * (kSc / 2) + p / (kGroup / 8)) * kCols + cr] = -136.f * sum;
               }
             } else {
               int m = 0;
@@ -473,14 +475,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int g = i / kSteps;
             if (i % kSteps == 0) {
 #pragma unroll
-              for (int j = 0; j < kNT; ++j) {
-                float2 c = make_float2(0.f, 0.f);
-                if (kBf16)
-                  c = *reinterpret_cast<const float2 *>(side + (blk * kSc + g) * kCols + 8 * j +
-                                                        2 * t);
-                part[j][0] = part[j][2] = c.x;
-                part[j][1] = part[j][3] = c.y;
-              }
+              for (int j = 0; j < kNT; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) part[j][c] = 0.f;
             }
             uint32_t c0[4], c1[4];
             codes<kBf16>(w0[i], c0);
@@ -595,7 +592,7 @@ Plan make_plan(int rows, int N, int K, int group, bool bf16, const int (&most)[4
     const size_t need = (size_t)kWarps * kDepth * kBlockBytes +
                         (size_t)p.slots * kTile * rows_x * 4 +
                         (size_t)p.columns * ((size_t)rb * kXBlock + 64) +
-                        (size_t)rb * 4 * (bf16 ? (kBlock / group) * 8 * p.nt : rows_x) +
+                        (bf16 ? 0 : (size_t)rb * 4 * rows_x) +
                         (((size_t)2 * c * rt + 31) & ~(size_t)15);
     const size_t sc = (((size_t)rt * kTile * groups * 2) + 15) & ~(size_t)15;
     p.sc_shared = need + sc <= kSmemMax;
@@ -708,7 +705,7 @@ cudaError_t launch_quant_linear(const void *x, const unsigned char *qw,
                                 cudaStream_t stream) {
   if (rows == 0 || N == 0) return cudaSuccess;
   // More than 16 columns go to products of 128 weight rows: 64 rows of bf16
-  // against 5120 x 6144 took 54 us here, 32 columns at a time, and take 23.5
+  // against 5120 x 6144 took 54 us here, 32 columns at a time, and take 19.3
   // there; 16 rows take 14 us here (19 there).
   if ((bf16 ? rows : 2 * rows) > 16)
     return launch_quant_linear_wide(x, qw, scales, y, rows, N, K, group, bf16, stream);

@@ -16,8 +16,10 @@
 // memory of the CTA that writes the rows of y, added in slice order: the same
 // bits on every call.
 //
-// Bound by the conversion (1.4 operations a code, half of them on the half-rate
-// integer pipe), then by the latency of the stages.
+// Bound by the latency of a stage (sums, conversion, loads, one barrier: 1700
+// cycles, in which the smem traffic takes 800 and the issue slots 1100), then
+// by start and exchange (6000 cycles a call).  64 rows of 5120 x 6144: bf16
+// 19.3 us, fp32 35 us; mma.sync with 16 rows of x at a time took 54 us.
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>

@@ -1,11 +1,10 @@
 """Projections with 4-bit weights against a plain 64-bit product.
 
-Tolerance, against the magnitude sum |x||w|: an element of x enters as a sum
-of two 11-bit parts (2^-22; exact for bf16 within 2^-25 of the row's
-largest element's binade), code * scale is exact in fp32, and the fp32 sums run over
-at most K / 16 + 64 steps of 2^-23 (a tensor product may truncate).  bf16
-results add their own rounding, and bf16 rows in the form for many rows take
-the weights rounded to fp16 (2^-11).
+Tolerance, against the magnitude sum |x||w|: an element of x enters as it is
+(bf16), as a sum of two 11-bit parts (fp32, few rows: 2^-22) or of three 8-bit
+parts (fp32, many rows: exact), codes are exact, code * scale is exact in fp32,
+and the fp32 sums run over at most K / 16 + 64 steps of 2^-23 (a tensor product
+may truncate).  bf16 results add their own rounding.
 """
 
 import pytest
@@ -27,7 +26,7 @@ def built():
 
 
 def tol(K, dtype, ref, mag):
-    t = (K / 16 + 64) * 2.0 ** -23 + (2.0 ** -11 if dtype == torch.bfloat16 else 0.0)
+    t = (K / 16 + 64) * 2.0 ** -23
     return t * mag + half_step(dtype) * (ref.abs() + t * mag)
 
 
@@ -78,6 +77,21 @@ def test_ranges(rows):
     x[:, 1::5] = 0.0
     sc = sc * 0 + torch.logspace(-7, 4, sc.numel(), device="cuda").view_as(sc).half()
     check(x, qw, sc)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", [1, 5, 40])
+def test_small_codes(dtype, rows):
+    """Rows of zeros give zeros; codes of -1, 0, 1 keep the accuracy that
+    their own magnitude allows."""
+    x, qw, sc = make_quant(8, rows, 90, 512, 64, TYPES[dtype])
+    half = torch.tensor([0, 1, 15], device="cuda", dtype=torch.uint8)
+    pick = torch.randint(0, 3, (2, *qw.shape), device="cuda",
+                         generator=torch.Generator("cuda").manual_seed(1))
+    qw = half[pick[0]] | half[pick[1]] << 4
+    qw[::3] = 0
+    y = check(x, qw, sc)
+    assert (y[:, ::3] == 0).all()
 
 
 @pytest.mark.parametrize("dtype", TYPES)
