@@ -451,9 +451,9 @@ struct RowGroup {
       } else {
         unsigned char *p = g8 + i * 256 + ((((m16 >> 1) ^ r1) << 4) ^ (i << 5)) + (m16 & 1) * 8;
         *reinterpret_cast<uint2 *>(p) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2 *>(p + 1024) = make_uint2(hi[2], hi[3]);
-        *reinterpret_cast<uint2 *>(p + 2048) = make_uint2(lo[0], lo[1]);
-        *reinterpret_cast<uint2 *>(p + 3072) = make_uint2(lo[2], lo[3]);
+        *reinterpret_cast<uint2 *>(p + 1 * 1024) = make_uint2(hi[2], hi[3]);
+        *reinterpret_cast<uint2 *>(p + 2 * 1024) = make_uint2(lo[0], lo[1]);
+        *reinterpret_cast<uint2 *>(p + 3 * 1024) = make_uint2(lo[2], lo[3]);
       }
     }
   }
