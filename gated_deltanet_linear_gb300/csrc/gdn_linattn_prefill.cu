@@ -505,6 +505,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 22; ++i) mbar_init(bar(i), (kByWarps >> i & 1) ? kGroup / 32 : 1);
     *fail = 0;
   }
+  // behind the kernel before it: nothing is read or written before it has ended
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
@@ -1144,6 +1147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 __global__ void __launch_bounds__(256)
     linattn_chain_kernel(const float *__restrict__ S, float *__restrict__ ws,
                          const double *__restrict__ decay, int nseg) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const size_t e = (size_t)blockIdx.x * 256 + threadIdx.x;
   const size_t head = e / (kD * kD / 4), x = e % (kD * kD / 4);
   float4 s = reinterpret_cast<const float4 *>(S)[e];
@@ -1218,15 +1222,24 @@ cudaError_t rows_map(CUtensorMap *map, const void *base, bool bf16, int heads, i
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Launched as a programmatic dependent of the kernel before it on the stream.
 template <bool kBf16, bool kLocal>
 cudaError_t launch(const CUtensorMap *m, const Args &a, cudaStream_t stream) {
+  const auto kernel = linattn_chunk_kernel<kBf16, kLocal>;
   const cudaError_t e =
-      cudaFuncSetAttribute(linattn_chunk_kernel<kBf16, kLocal>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
   if (e != cudaSuccess) return e;
-  linattn_chunk_kernel<kBf16, kLocal>
-      <<<(unsigned)min(a.units, kSms), kThreads, kSmemAlloc, stream>>>(m[0], m[1], m[2], a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)min(a.units, kSms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemAlloc;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], a);
 }
 
 }  // namespace
@@ -1268,6 +1281,8 @@ cudaError_t launch_linattn_prefill(const LinattnArgs &L, bool bf16, void *worksp
     a.units = (int)(heads * (nseg - 1));
     e = bf16 ? launch<true, true>(m, a, stream) : launch<false, true>(m, a, stream);
     if (e != cudaSuccess) return e;
+    // (an ordinary launch: started early, all of it would land on the few SMs
+    // that the pass before leaves free; 183 us for the one long prompt, not 145)
     linattn_chain_kernel<<<(unsigned)(heads * (kD * kD / 4 / 256)), 256, 0, stream>>>(
         a.S, a.ws_state, a.ws_decay, nseg);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
