@@ -705,8 +705,8 @@ cudaError_t launch_quant_linear(const void *x, const unsigned char *qw,
                                 cudaStream_t stream) {
   if (rows == 0 || N == 0) return cudaSuccess;
   // More than 16 columns go to products of 128 weight rows: 64 rows of bf16
-  // against 5120 x 6144 took 54 us here, 32 columns at a time, and take 19.3
-  // there; 16 rows take 14 us here (19 there).
+  // against 5120 x 6144 took 54 us here, 32 columns at a time, and take 18.6
+  // there; 16 rows take 14 us here (17 there).
   if ((bf16 ? rows : 2 * rows) > 16)
     return launch_quant_linear_wide(x, qw, scales, y, rows, N, K, group, bf16, stream);
   int most[4];
