@@ -17,7 +17,8 @@
 // Precision.  Operands are fp16 numbers scaled by powers of two; with fp32
 // rows each operand is hi + lo (22 bits), a product hi hi + hi lo + lo hi,
 // accumulated in fp32, so results are fp32 results (a bf16 split keeps 16
-// bits).  With bf16 rows q, k and v fit one fp16 each; the scores and the
+// bits).  The products with a lo come first: the accumulation truncates, and
+// only the hi hi steps, a third of all, then do so at the size of the sum.  With bf16 rows q, k and v fit one fp16 each; the scores and the
 // state that enter o are rounded to fp16 (2^-11, below o's own 2^-8), and the
 // decayed values that enter the state stay hi + lo.  The scales: q and k by
 // row, v, the decayed values and the state by column dv (the TMEM lane),
@@ -875,31 +876,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           // (G is free: P of the last chunk is made)
           fence_after_sync();
           const uint32_t lo_k = desc_lo(kq, 16), lo_q = lo_k + (8 * kGrp >> 4);
+          if (kLo)
+#pragma unroll 1
+            for (int ks = 0; ks < kD / 16; ++ks) {
+              const uint64_t h = desc64(hi, lo_k + (kstep(ks) >> 4));
+              const uint64_t l = desc64(hi, lo_k + ((kstep(ks) + 2048) >> 4));
+              mma_ss(one, tm + T_G, h, l, idn, ks > 0);
+              mma_ss(one, tm + T_G, l, h, idn, 1u);
+            }
 #pragma unroll 1
           for (int ks = 0; ks < kD / 16; ++ks) {
             const uint64_t h = desc64(hi, lo_k + (kstep(ks) >> 4));
-            const uint64_t l = desc64(hi, lo_k + ((kstep(ks) + 2048) >> 4));
-            mma_ss(one, tm + T_G, h, h, idn, ks > 0);
-            if (kLo) {
-              mma_ss(one, tm + T_G, h, l, idn, 1u);
-              mma_ss(one, tm + T_G, l, h, idn, 1u);
-            }
+            mma_ss(one, tm + T_G, h, h, idn, kLo || ks > 0);
           }
           commit_one(one, done_qk);
           wait_bar(rdy_s, it & 1, fail);
           if (it > 0) wait_bar(acc_free, (it - 1) & 1, fail);
           fence_after_sync();
+          if (kLo)
 #pragma unroll 1
-          for (int ks = 0; ks < kD / 16; ++ks) {
-            const uint64_t h = desc64(hi, lo_q + (kstep(ks) >> 4));
-            const uint64_t l = desc64(hi, lo_q + ((kstep(ks) + 2048) >> 4));
-            const uint32_t a = tm + T_SOP + 8u * ks;
-            mma_ts(one, tm + T_QS, a, h, idn, ks > 0);
-            if (kLo) {
-              mma_ts(one, tm + T_QS, a, l, idn, 1u);
-              mma_ts(one, tm + T_QS, a + 64u, h, idn, 1u);
+            for (int ks = 0; ks < kD / 16; ++ks) {
+              const uint32_t a = tm + T_SOP + 8u * ks;
+              mma_ts(one, tm + T_QS, a, desc64(hi, lo_q + ((kstep(ks) + 2048) >> 4)), idn, ks > 0);
+              mma_ts(one, tm + T_QS, a + 64u, desc64(hi, lo_q + (kstep(ks) >> 4)), idn, 1u);
             }
-          }
+#pragma unroll 1
+          for (int ks = 0; ks < kD / 16; ++ks)
+            mma_ts(one, tm + T_QS, tm + T_SOP + 8u * ks, desc64(hi, lo_q + (kstep(ks) >> 4)), idn,
+                   kLo || ks > 0);
         } else {
           // the KV columns are free once the state has taken the last product
           if (it > 0) wait_bar(rdy_s, (it - 1) & 1, fail);
@@ -913,10 +917,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t h = desc64(hi, lo_k + (ks * 2 * kGrp >> 4));
             const uint64_t l = desc64(hi, lo_k + ((ks * 2 * kGrp + 2048) >> 4));
             const uint32_t a = tm + T_WOP + 8u * ks;
-            mma_ts(one, tm + T_D, a, h, idk, ks > 0);
-            mma_ts(one, tm + T_D, a + 32u, h, idk, 1u);
+            mma_ts(one, tm + T_D, a + 32u, h, idk, ks > 0);
             if (kLo) mma_ts(one, tm + T_D, a, l, idk, 1u);
           }
+#pragma unroll 1
+          for (int ks = 0; ks < kC / 16; ++ks)
+            mma_ts(one, tm + T_D, tm + T_WOP + 8u * ks,
+                   desc64(hi, lo_k + (ks * 2 * kGrp >> 4)), idk, 1u);
         }
         commit_one(one, done_kv);
         commit_one(one, kq_free + 8 * (it & 1));
@@ -924,17 +931,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_bar(rdy_p, it & 1, fail);
           wait_bar(done_kv, it & 1, fail);
           fence_after_sync();
+          if (kLo)
 #pragma unroll 1
-          for (int ks = 0; ks < kC / 16; ++ks) {
-            const uint64_t h = desc64(hi_p, lo_p + (kstep(ks) >> 4));
-            const uint64_t l = desc64(hi_p, lo_p + ((kstep(ks) + 8192) >> 4));
-            const uint32_t a = tm + T_VOP + 8u * ks;
-            mma_ts(one, tm + T_PV, a, h, idn, ks > 0);
-            if (kLo) {
-              mma_ts(one, tm + T_PV, a, l, idn, 1u);
-              mma_ts(one, tm + T_PV, a + 32u, h, idn, 1u);
+            for (int ks = 0; ks < kC / 16; ++ks) {
+              const uint32_t a = tm + T_VOP + 8u * ks;
+              mma_ts(one, tm + T_PV, a, desc64(hi_p, lo_p + ((kstep(ks) + 8192) >> 4)), idn,
+                     ks > 0);
+              mma_ts(one, tm + T_PV, a + 32u, desc64(hi_p, lo_p + (kstep(ks) >> 4)), idn, 1u);
             }
-          }
+#pragma unroll 1
+          for (int ks = 0; ks < kC / 16; ++ks)
+            mma_ts(one, tm + T_PV, tm + T_VOP + 8u * ks,
+                   desc64(hi_p, lo_p + (kstep(ks) >> 4)), idn, kLo || ks > 0);
           commit_one(one, done_o);
         }
       }
