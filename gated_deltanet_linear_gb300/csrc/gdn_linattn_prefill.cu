@@ -45,8 +45,8 @@
 // the main pass runs over all segments at once.
 //
 // Measured (8 prompts of 4096 tokens, 16 / 48 heads): fp32 709 us (2.20 GB,
-// 46 % of the copy rate), bf16 572 us (1.13 GB, 29 %); 33 prompts of up to 111
-// tokens, fp32, 95 us; one of 32701 tokens, 2 / 8 heads, bf16, 146 us.  Bound by
+// 46 % of the copy rate), bf16 574 us (1.13 GB, 29 %); 33 prompts of up to 111
+// tokens, fp32, 93 us; one of 32701 tokens, 2 / 8 heads, bf16, 135 us.  Bound by
 // the latency of each chunk's chain (rows - decay vectors - V operands - KV -
 // state, and scores - P - PV - output) on 4 to 5 warps a scheduler: they issue
 // in 54 % of the cycles, the tensor cores are busy in 33 %, DRAM 38 %.  The

@@ -11,7 +11,7 @@
 //                  three bf16 parts (3 x 8 bits, nothing to scale) into operand
 //                  tiles
 //   one thread     the products of the stage, one accumulator for each group of
-//                  the stage (W x1, then x2 and x3 onto it)
+//                  the stage (W x3, then x2 and x1 onto it)
 //   16 warps       two stages later: accumulator times the group's scale, added
 //                  to fp32 sums in registers (lane = weight row)
 // The products of a stage run under the conversion of the next one.  The sums of
@@ -311,12 +311,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int g = 0; g < kGroups; ++g) {
             const uint32_t d = tmem + (uint32_t)(((at % kLag) * kGroups + g) * kNC);
 #pragma unroll
-            for (int term = 0; term < kTerms; ++term)
+            for (int term = kTerms - 1; term >= 0; --term)  // (small ones first)
 #pragma unroll
               for (int k = 0; k < kGroup / 16; ++k) {
                 const int ks = g * (kGroup / 16) + k;
                 mma_ts(one, d, a + 8u * ks, desc_kstep(b + term * kBTile, kNC, ks), id,
-                       term > 0 || k > 0);
+                       term < kTerms - 1 || k > 0);
               }
           }
           commit_one(one, bar + 8 * (at & 1));
