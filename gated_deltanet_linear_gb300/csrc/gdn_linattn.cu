@@ -19,15 +19,20 @@
 // instead of 8); the warps' sums meet in shared memory, one barrier for every
 // 8 tokens.
 //
+// Arithmetic in packed pairs (rows 2 i and 2 i + 1 of a column): half the
+// instructions of the 32 elements of a lane, k and q as they lie in shared
+// memory.  (8 tokens x 64 x 48 heads 111 -> 95 us; 64 registers at 8 CTAs an SM,
+// 80 at 6 took 109.)
+//
 // Determinism.  Every product and sum is an explicit round-to-nearest
-// intrinsic in a fixed tree (a lane's rows in order, the row groups
+// operation in a fixed tree (a lane's even rows and odd rows in order, the row groups
 // (0 + 1) + (2 + 3), the warps (0 + 2) + (1 + 3)), so M tokens in one launch
 // give the bits of M launches.
 //
 // Bound by HBM: 128 KB of state per head against three FP32 lane operations
 // per state element and token.  64 sequences x 48 heads: one token 58.4 us
-// (405 MB, 103 % of the copy rate), 4 tokens 75 us, 8 tokens 111 us, where the
-// shared-memory reads of k and q are the bound.
+// (405 MB, 103 % of the copy rate), 4 tokens 72 us, 8 tokens 95 us, where a CTA's
+// phases (state in, 8 tokens of dependent sums, state out) overlap less.
 
 #include <cuda_bf16.h>
 
@@ -96,6 +101,29 @@ __device__ __forceinline__ void st_state(float *p, const float4 &v) {
                : "memory");
 }
 
+// Two floats in a register pair, and the packed operations on them.
+typedef unsigned long long F2;
+__device__ __forceinline__ F2 pack(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack(F2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // Token inputs of a block of tokens in shared memory, as fp32 (several tokens:
 // converted once for the CTA's four warps, and read again without the latency
 // of a cache miss).
@@ -103,8 +131,8 @@ struct Staged {
   float k[kBlk][kDim], q[kBlk][kDim], v[kBlk][32], a[kBlk];
 };
 
-// kMulti: more than one token: token inputs are staged 8 at a time.  One token: each lane reads its own, beside the state's
-// loads.
+// kMulti: more than one token: token inputs are staged 8 at a time.  One token:
+// each lane reads its own, beside the state's loads.
 template <typename T, bool kMulti>
 __global__ void __launch_bounds__(128, kMulti ? 8 : 5)
     linattn_steps_kernel(const LinattnArgs P) {
@@ -131,29 +159,39 @@ __global__ void __launch_bounds__(128, kMulti ? 8 : 5)
   const size_t qk_step = (size_t)P.kh * kDim, v_step = (size_t)P.vh * kDim;
   const size_t g_step = P.g_head ? 0 : P.vh;
 
-  float4 s[8];
+  F2 s[4][4];  // rows 2 i and 2 i + 1 of a column
   {
     const float *Sp = P.S_in + (size_t)head * kDim * kDim + blk;
+    float4 r[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] = ld_state(Sp + i * kDim);
+    for (int i = 0; i < 8; ++i) r[i] = ld_state(Sp + i * kDim);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s[i][0] = pack(r[2 * i].x, r[2 * i + 1].x);
+      s[i][1] = pack(r[2 * i].y, r[2 * i + 1].y);
+      s[i][2] = pack(r[2 * i].z, r[2 * i + 1].z);
+      s[i][3] = pack(r[2 * i].w, r[2 * i + 1].w);
+    }
   }
   // One token: S = a S + k v^T, and this lane's share of S^T q into part[j].
   const bool up8 = lane & 8, up16 = lane & 16;
   // the column of the group whose sum this lane ends up with
   const int mine = cl + 2 * (up8 ? 1 : 0) + (up16 ? 1 : 0);
-  auto token = [&](const float (&k)[8], const float (&q)[8], const float (&v)[4], float a,
+  auto token = [&](const F2 (&k)[4], const F2 (&q)[4], const float (&v)[4], float a,
                    float (&sums)[4][32]) {
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    float acc[4];
+    const F2 aa = pack(a, a);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      s[i].x = __fmaf_rn(a, s[i].x, __fmul_rn(k[i], v[0]));
-      s[i].y = __fmaf_rn(a, s[i].y, __fmul_rn(k[i], v[1]));
-      s[i].z = __fmaf_rn(a, s[i].z, __fmul_rn(k[i], v[2]));
-      s[i].w = __fmaf_rn(a, s[i].w, __fmul_rn(k[i], v[3]));
-      acc[0] = __fmaf_rn(s[i].x, q[i], acc[0]);
-      acc[1] = __fmaf_rn(s[i].y, q[i], acc[1]);
-      acc[2] = __fmaf_rn(s[i].z, q[i], acc[2]);
-      acc[3] = __fmaf_rn(s[i].w, q[i], acc[3]);
+    for (int c = 0; c < 4; ++c) {
+      const F2 vv = pack(v[c], v[c]);
+      F2 t = 0ull;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[i][c] = fma2(aa, s[i][c], mul2(k[i], vv));
+        t = fma2(s[i][c], q[i], t);
+      }
+      const float2 u = unpack(t);
+      acc[c] = __fadd_rn(u.x, u.y);
     }
     float k0 = up8 ? acc[2] : acc[0], k1 = up8 ? acc[3] : acc[1];
     k0 = __fadd_rn(k0, __shfl_xor_sync(kFull, up8 ? acc[0] : acc[2], 8));
@@ -162,7 +200,12 @@ __global__ void __launch_bounds__(128, kMulti ? 8 : 5)
   };
   auto state_to = [&](float *p) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) st_state(p + blk + i * kDim, s[i]);
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = unpack(s[i][0]), y = unpack(s[i][1]), z = unpack(s[i][2]),
+                   w = unpack(s[i][3]);
+      st_state(p + blk + 2 * i * kDim, make_float4(x.x, y.x, z.x, w.x));
+      st_state(p + blk + (2 * i + 1) * kDim, make_float4(x.y, y.y, z.y, w.y));
+    }
   };
   // The sums of nb tokens from m0 on, from the four warps' parts.
   auto output = [&](int m0, int nb, float (&p)[kBlk][4][32]) {
@@ -177,9 +220,14 @@ __global__ void __launch_bounds__(128, kMulti ? 8 : 5)
     }
   };
   if (!kMulti) {
-    float k[8], q[8], v[4];
-    load8(kp + row, k);
-    load8(qp + row, q);
+    float f[8], v[4];
+    F2 k[4], q[4];
+    load8(kp + row, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) k[i] = pack(f[2 * i], f[2 * i + 1]);
+    load8(qp + row, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = pack(f[2 * i], f[2 * i + 1]);
     load4(vp + cl, v);
     token(k, q, v, expf(__ldg(gp)), part[0][0]);
     if (P.ckpt) state_to(P.ckpt + (size_t)head * kDim * kDim);
@@ -207,14 +255,16 @@ __global__ void __launch_bounds__(128, kMulti ? 8 : 5)
       }
       if (tid < nb) st->a[tid] = expf(__ldg(gp + (m0 + tid) * g_step));
       __syncthreads();
+#pragma unroll 1  // (unrolled, it took 3 % longer)
       for (int j = 0; j < nb; ++j) {
-        float k[8], q[8], v[4];
+        F2 k[4], q[4];
+        float v[4];
 #pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          const float4 x = *reinterpret_cast<const float4 *>(&st->k[j][row + i]);
-          const float4 y = *reinterpret_cast<const float4 *>(&st->q[j][row + i]);
-          k[i] = x.x; k[i + 1] = x.y; k[i + 2] = x.z; k[i + 3] = x.w;
-          q[i] = y.x; q[i + 1] = y.y; q[i + 2] = y.z; q[i + 3] = y.w;
+        for (int i = 0; i < 4; i += 2) {
+          const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(&st->k[j][row + 2 * i]);
+          const ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(&st->q[j][row + 2 * i]);
+          k[i] = x.x; k[i + 1] = x.y;
+          q[i] = y.x; q[i + 1] = y.y;
         }
         const float4 z = *reinterpret_cast<const float4 *>(&st->v[j][cl]);
         v[0] = z.x; v[1] = z.y; v[2] = z.z; v[3] = z.w;
