@@ -613,19 +613,16 @@ int gdn_linattn_prefill(const gdn_shape *s, int T, int dtype, int decay,
   if (s->B == 0) return GDN_OK;
   const size_t need = gdn_linattn_prefill_workspace(s, T, dtype);
   if (need && (!workspace || ws_bytes < need)) return workspace ? GDN_ERANGE : GDN_EINVAL;
-  const Buf out[] = {{S, state_floats(s) * 4},
-                     {o, (size_t)s->B * T * s->vh * s->vd * element_size(dtype)}};
+  const size_t e = element_size(dtype), qkb = (size_t)s->B * T * s->kh * s->kd * e;
+  const size_t vb = (size_t)s->B * T * s->vh * s->vd * e;
+  const Buf ws{workspace, need}, lengths{lens, lens ? (size_t)s->B * 4 : 0},
+      err{err_dev, err_dev ? (size_t)4 : 0};
+  // (S and o have been checked against the inputs)
+  const Buf all[] = {{S, state_floats(s) * 4}, {o, vb}, {q, qkb}, {k, qkb}, {v, vb},
+                     {g, (decay == GDN_DECAY_HEAD ? 1 : (size_t)s->B * T) * s->vh * 4}};
   if (need) {
-    const size_t e = element_size(dtype);
-    const Buf ws{workspace, need};
     r = check_bufs(&ws, 1);
     if (r) return r;
-    const size_t qkb = (size_t)s->B * T * s->kh * s->kd * e;
-    const Buf in[] = {{q, qkb}, {k, qkb}, {v, out[1].bytes},
-                      {g, (decay == GDN_DECAY_HEAD ? 1 : (size_t)s->B * T) * s->vh * 4},
-                      {lens, lens ? (size_t)s->B * 4 : 0}, out[0], out[1]};
-    for (const Buf &x : in)
-      if (overlaps(ws, x)) return GDN_EALIAS;
   }
   const void *ints[] = {lens, err_dev};
   for (const void *p : ints) {
@@ -633,14 +630,22 @@ int gdn_linattn_prefill(const gdn_shape *s, int T, int dtype, int decay,
     if (((uintptr_t)p & 3u) != 0) return GDN_EALIGN;
     r = check_device_ptr(p);
     if (r) return r;
-    for (const Buf &x : out)
-      if (overlaps(x, Buf{p, p == lens ? (size_t)s->B * 4 : 4})) return GDN_EALIAS;
   }
+  for (const Buf &x : all)
+    if ((need && overlaps(ws, x)) || (err_dev && overlaps(err, x))) return GDN_EALIAS;
+  if (lens && (overlaps(lengths, all[0]) || overlaps(lengths, all[1]) ||
+               (need && overlaps(lengths, ws)) || (err_dev && overlaps(lengths, err))))
+    return GDN_EALIAS;
+  if (need && err_dev && overlaps(ws, err)) return GDN_EALIAS;
   P.lens = lens;
   P.err = err_dev;
   cudaGetLastError();
-  return status_of(gdn::launch_linattn_prefill(P, dtype == GDN_BF16, workspace,
-                                               (cudaStream_t)stream));
+  try {
+    return status_of(gdn::launch_linattn_prefill(P, dtype == GDN_BF16, workspace,
+                                                 (cudaStream_t)stream));
+  } catch (...) {  // (host locks; nothing is launched)
+    return GDN_ECUDA;
+  }
 }
 
 int gdn_quant_linear(int rows, int N, int K, int group, int dtype,
@@ -662,9 +667,13 @@ int gdn_quant_linear(int rows, int N, int K, int group, int dtype,
   for (int j = 0; j < 3; ++j)
     if (overlaps(b[3], b[j])) return GDN_EALIAS;
   cudaGetLastError();
-  return status_of(gdn::launch_quant_linear(x, qw, scales, y, rows, N, K, group,
-                                            dtype == GDN_BF16,
-                                            (cudaStream_t)stream));
+  try {
+    return status_of(gdn::launch_quant_linear(x, qw, scales, y, rows, N, K, group,
+                                              dtype == GDN_BF16,
+                                              (cudaStream_t)stream));
+  } catch (...) {  // (host locks and tables; nothing is launched)
+    return GDN_ECUDA;
+  }
 }
 
 }  // extern "C"

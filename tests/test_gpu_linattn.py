@@ -528,6 +528,23 @@ def test_few_heads_long_prompts(dtype, B, kh, vh, T):
     assert gdn.gdn_wait_timeouts() == 0
 
 
+def test_integer_buffers_stay_apart():
+    """lens and err_dev over each other, over tensors and over the workspace."""
+    d = make_linattn(1, 1, 4000, 1, 1)
+    S, o, ws = d["S"].clone(), torch.zeros_like(d["v"]), workspace(d)
+    args = (S, d["q"], d["k"], d["v"], d["g"], o)
+    ints = lambda x: x.flatten()[:4].view(torch.int32)[:1]
+    wsi = ws[:16].view(torch.int32)[:1]
+    lens = torch.full((1,), 4000, dtype=torch.int32, device="cuda")
+    for more in (dict(lens=lens, err_dev=lens), dict(err_dev=ints(d["q"])), dict(err_dev=ints(d["g"])),
+                 dict(err_dev=ints(S)), dict(lens=ints(o)), dict(lens=wsi), dict(err_dev=wsi)):
+        with pytest.raises(gdn.GDNError) as e:
+            gdn.gdn_linattn_prefill(*args, workspace=ws, **more)
+        assert e.value.status == gdn.GDN_EALIAS
+    torch.cuda.synchronize()
+    assert torch.equal(S, d["S"]) and int(lens) == 4000 and not o.any()
+
+
 def test_workspace_refusals():
     d = make_linattn(1, 1, 4000, 1, 1)
     need = workspace(d).numel()
