@@ -208,9 +208,15 @@ __device__ __forceinline__ Two add2(Two a, Two b) {
   return Two{h, e - (h - s)};
 }
 __device__ __forceinline__ Two neg2(Two a) { return Two{-a.h, -a.l}; }
-// 2^x: exp2 of the high part times 1 + ln 2 of the low one
+// 2^x in one instruction (2^-22 relative; 0 where the result is below 2^-126)
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// 2^x: of the high part, times 1 + ln 2 of the low one
 __device__ __forceinline__ float ex2(Two x) {
-  const float e = exp2f(x.h);
+  const float e = ex2(x.h);
   return fmaf(e, x.l * 0.69314718f, e);
 }
 __device__ __forceinline__ Two shfl_up2(Two x, int d) {
@@ -764,8 +770,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int j = 0; j < 8; ++j) {
                 const float2 n = unpack(vb[j]);
                 x[j] = mul2(pair(r + 2 * j),
-                            pack(exp2f(((at - h[2 * j]) - l[2 * j]) + n.x),
-                                 exp2f(((at - h[2 * j + 1]) - l[2 * j + 1]) + n.y)));
+                            pack(ex2(((at - h[2 * j]) - l[2 * j]) + n.x),
+                                 ex2(((at - h[2 * j + 1]) - l[2 * j + 1]) + n.y)));
               }
             }
             if (s0 + 15 > 32 * (quad - 2))
@@ -1099,7 +1105,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int t = 2 * lane + i;
           R[i] = fmaxf(R[i], lo);
           const float n = -22.f - (float)kx[i];
-          vc[VA + t] = fac ? exp2f(-R[i] - c) : -R[i];
+          vc[VA + t] = fac ? ex2(-R[i] - c) : -R[i];
           vc[VB + t] = fac ? ex2(add2(neg2(G[i]), Two{c + n, 0.f})) : n;
           vc[VGH + t] = G[i].h;
           vc[VGL + t] = G[i].l;
