@@ -207,17 +207,13 @@ __device__ __forceinline__ Two add2(Two a, Two b) {
   const float h = s + e;
   return Two{h, e - (h - s)};
 }
-__device__ __forceinline__ Two neg2(Two a) { return Two{-a.h, -a.l}; }
-// 2^x in one instruction (2^-22 relative; 0 where the result is below 2^-126)
+// 2^x in one instruction (2^-22 relative; 0 where the result is below 2^-126).
+// Its arguments are rounded to a float, 2^-24 |x|: less than 2^-24 of the whole for
+// weights 2^x <= 1; larger exponents are taken apart into integer and rest.
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
-}
-// 2^x: of the high part, times 1 + ln 2 of the low one
-__device__ __forceinline__ float ex2(Two x) {
-  const float e = ex2(x.h);
-  return fmaf(e, x.l * 0.69314718f, e);
 }
 __device__ __forceinline__ Two shfl_up2(Two x, int d) {
   return Two{__shfl_up_sync(0xffffffffu, x.h, d), __shfl_up_sync(0xffffffffu, x.l, d)};
@@ -1041,11 +1037,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       total += (double)end.h + (double)end.l;
       float *vc = vec(it);
       // the decay from each token to the chunk's end
-      float wt[2], gm[2];
+      float wt[2], gf[2];  // the weights; Gamma_t = gr + gf
+      int gr[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        wt[i] = ex2(add2(end, neg2(G[i])));
-        gm[i] = P.scale * ex2(G[i]);
+        wt[i] = ex2((end.h - G[i].h) + (end.l - G[i].l));
+        const float whole = rintf(G[i].h);
+        gr[i] = (int)whole;
+        gf[i] = (G[i].h - whole) + G[i].l;
       }
       int grow = 0;
       if (__any_sync(0xffffffffu, up)) {
@@ -1061,7 +1060,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int off = 16; off; off >>= 1) d = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, off));
         grow = (int)ceilf(fminf(d, 80.f));
       }
-      const float gend = ex2(end);
+      const float gend = ex2(end.h + end.l);
       wait_bar(rdy_kq + 8 * (it & 1), (it >> 1) & 1, fail);
       const int *ex = rowexp(it);
       const int2 k2 = *reinterpret_cast<const int2 *>(ex + 2 * lane);
@@ -1099,14 +1098,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         // one factor per row and column while their product cannot leave the
         // normal floats; otherwise an exponential per element
         const bool fac = hi - lo <= 120.f;
-        const float c = -rintf(0.5f * (hi + lo));
+        const int c = -(int)rintf(0.5f * (hi + lo));
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int t = 2 * lane + i;
           R[i] = fmaxf(R[i], lo);
-          const float n = -22.f - (float)kx[i];
-          vc[VA + t] = fac ? ex2(-R[i] - c) : -R[i];
-          vc[VB + t] = fac ? ex2(add2(neg2(G[i]), Two{c + n, 0.f})) : n;
+          const int n = -22 - kx[i];
+          vc[VA + t] = fac ? p2(-(int)R[i] - c) : -R[i];
+          vc[VB + t] = fac ? ex2(-gf[i]) * p2(c + n - gr[i]) : (float)n;
           vc[VGH + t] = G[i].h;
           vc[VGL + t] = G[i].l;
         }
@@ -1128,11 +1127,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int t = 2 * lane + i;
-          vc[VCA + t] = gm[i] * p2(-qx[i]);
+          const float e = P.scale * ex2(gf[i]);
+          vc[VCA + t] = e * p2(gr[i] - qx[i]);
           // what P[t] and q_t are scaled by (finite also where P[t] is all zeros)
-          Two u = add2(G[i], Two{R[i] + (float)(22 - qx[i]), 0.f});
-          if (u.h > 126.f) u = Two{126.f, 0.f};
-          vc[VCB + t] = P.scale * ex2(u);
+          vc[VCB + t] = e * p2(min(gr[i] + (int)R[i] + 22 - qx[i], 100));
         }
       }
       __syncwarp();
