@@ -1081,7 +1081,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) r[i] = kx[i] < 127 ? -G[i].h - (float)kx[i] : none;
         float run_r = fmaxf(r[0], r[1]);
-#pragma unroll 1
+#pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
           const float y = __shfl_up_sync(0xffffffffu, run_r, off);
           if (lane >= off) run_r = fmaxf(run_r, y);
