@@ -44,16 +44,16 @@
 // (KV only), a second kernel chains them into every segment's start state, and
 // the main pass runs over all segments at once.
 //
-// Measured (8 prompts of 4096 tokens, 16 / 48 heads): fp32 709 us (2.20 GB,
-// 46 % of the copy rate), bf16 574 us (1.13 GB, 29 %); 33 prompts of up to 111
-// tokens, fp32, 93 us; one of 32701 tokens, 2 / 8 heads, bf16, 135 us.  Bound by
+// Measured (8 prompts of 4096 tokens, 16 / 48 heads): fp32 669 us (2.20 GB,
+// 49 % of the copy rate), bf16 526 us (1.13 GB, 32 %); 33 prompts of up to 111
+// tokens, fp32, 90 us; one of 32701 tokens, 2 / 8 heads, bf16, 127 us.  Bound by
 // the latency of each chunk's chain (rows - decay vectors - V operands - KV -
 // state, and scores - P - PV - output) on 4 to 5 warps a scheduler: they issue
-// in 54 % of the cycles, the tensor cores are busy in 33 %, DRAM 38 %.  The
-// code of all roles together is as large as the instruction cache bears: more
-// unrolling, or warps for more roles, cost more than they hid (24 and 32 warps
-// with packed arithmetic 9000 cycles a chunk, 16 rows more unrolled +12 %), and
-// rolling the loops of the products and the output gave 10 %.
+// in 58 % of the cycles, the tensor cores are busy in 35 %, DRAM 40 %.  The
+// code of all roles together is more than the instruction cache bears (14 % of
+// its requests miss): more unrolling, or warps for more roles, cost more than
+// they hid (24 and 32 warps with packed arithmetic 9000 cycles a chunk where 20
+// took 7000; the score loop unrolled +12 %), 1.4 KB less of it gave 5 %.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -460,7 +460,7 @@ size_t gdn_linattn_prefill_workspace(const gdn_shape *shape, int T, int dtype);
  * Numbers: chunks of 64 tokens on tensor cores.  fp32 operands are the sum of
  * two fp16 numbers (22 bits) scaled by rows or columns, bf16 ones a single
  * fp16 (the scores and the state that enter o are then rounded to 11 bits;
- * the state itself is kept in fp32), every sum is fp32: about 4e-7 relative
+ * the state itself is kept in fp32), every sum is fp32: about 3e-7 relative
  * error of an fp32 o and 2e-7 of S, where a step's is 1e-7.  Weights e^{sum of g}
  * below 2^-126 may count as 0, and within 64 tokens g may grow by up to a
  * factor of 2^80.  The same call gives the same bits; another B or T may cut
