@@ -321,7 +321,7 @@ __device__ __forceinline__ void wait_bar(uint32_t bar, uint32_t parity, volatile
         : "r"(bar), "r"(parity)
         : "memory");
     if (ok) return;
-    if ((i & 255) == 255 && *fail) return;
+    if (*fail) return;
   }
   *fail = 1;
 }
