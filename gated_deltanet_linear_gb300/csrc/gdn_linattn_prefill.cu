@@ -1195,7 +1195,8 @@ __global__ void __launch_bounds__(256)
 }
 
 // Segments per sequence.  One segment costs its chunks on the critical CTA;
-// more segments run the KV pass too (about 0.6 of the main pass per chunk)
+// more segments run the KV pass too (half of the main pass per chunk, 0.6 with
+// its launch)
 // and read and write a start state each (about 2 chunks).  The cheapest
 // count by that model.
 int plan(int B, int vh, int T) {

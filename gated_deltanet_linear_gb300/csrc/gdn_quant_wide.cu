@@ -63,8 +63,12 @@ __host__ __device__ constexpr int x_bytes() {
 template <bool kBf16, int kNC>
 __host__ __device__ constexpr int smem_bytes() {
   // codes, x, the sums received from the cluster (up to 8 slices of at most
-  // ceil(kNC / c) rows of y), scales, barriers, room to align
-  return kRing * kCodes + x_bytes<kBf16, kNC>() + (kNC + 8) * kRowsW * 4 + kScales + 64 + 1024;
+  // ceil(kNC / c) rows of y), scales, barriers, room to align; and so much that
+  // an SM has one CTA: CTAs of two clusters (on two streams) that hold TMEM on
+  // one SM and wait for it on another would wait for each other
+  constexpr int used =
+      kRing * kCodes + x_bytes<kBf16, kNC>() + (kNC + 8) * kRowsW * 4 + kScales + 64 + 1024;
+  return used > 118 * 1024 ? used : 118 * 1024;
 }
 
 struct WideArgs {

@@ -123,6 +123,26 @@ def test_non_finite_rows_stay_apart(dtype, rows):
     assert (y[0] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_many_rows_on_three_streams(dtype):
+    """Clusters of several calls side by side, of each group size."""
+    jobs = [make_quant(60 + g, rows, 2600, 2048, g, TYPES[dtype])
+            for g, rows in ((32, 20), (64, 30), (128, 50), (32, 64))]
+    ref = [torch.empty(x.shape[0], 2600, device="cuda", dtype=x.dtype) for x, _, _ in jobs]
+    got = [[torch.empty_like(y) for y in ref] for _ in range(3)]
+    for (x, qw, sc), y in zip(jobs, ref):
+        gdn.gdn_quant_linear(x, qw, sc, y)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in got]
+    for turn in range(20):
+        for i, (stream, ys) in enumerate(zip(streams, got)):
+            j = (turn + i) % len(jobs)
+            gdn.gdn_quant_linear(*jobs[j], ys[j], stream=stream)
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, r) for ys in got for y, r in zip(ys, ref))
+    assert gdn.gdn_wait_timeouts() == 0
+
+
 def test_same_bits_and_graph():
     for rows in (1, 8, 50):
         x, qw, sc = make_quant(6, rows, 777, 1024, 128)
