@@ -15,6 +15,7 @@ Layouts (see include/gdn.h):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -148,12 +149,13 @@ def gdn_version() -> int:
 # The current stream's handle without the Stream object around it (0.3 us a
 # call instead of 2.9 us on a GB300 host).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream):
     if stream is None:
         if _raw_stream is not None and torch.cuda.is_initialized():
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -434,6 +436,10 @@ def gdn_layer_hist_rollback(hist, M, m_dev, hist_snap, x, kh, kd=128, vd=128,
         "gdn_layer_hist_rollback")
 
 
+# The C structure of a shape, made once for each (0.3 us).
+_shape5 = functools.lru_cache(maxsize=64)(Shape)
+
+
 def _tok(x, name, shape, dtype):
     """Pointer of a contiguous CUDA tensor of this shape and type.  (On the path
     of every call below: one comparison each, the messages out of the way.)"""
@@ -472,7 +478,7 @@ def _linattn(S, q, k, v, g, o, M):
         lead = (B, M)
     qk, vo = lead + (kh, kd), lead + (vh, vd)
     head = g.dim() == 1
-    return (Shape(B, kh, vh, kd, vd), code,
+    return (_shape5(B, kh, vh, kd, vd), code,
             GDN_DECAY_HEAD if head else GDN_DECAY_TOKEN,
             _tok(q, "q", qk, dtype), _tok(k, "k", qk, dtype),
             _tok(v, "v", vo, dtype),
