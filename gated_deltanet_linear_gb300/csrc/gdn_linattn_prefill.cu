@@ -18,9 +18,11 @@
 // rows each operand is hi + lo (22 bits), a product hi hi + hi lo + lo hi,
 // accumulated in fp32, so results are fp32 results (a bf16 split keeps 16
 // bits).  The products with a lo come first: the accumulation truncates, and
-// only the hi hi steps, a third of all, then do so at the size of the sum.  With bf16 rows q, k and v fit one fp16 each; the scores and the
-// state that enter o are rounded to fp16 (2^-11, below o's own 2^-8), and the
-// decayed values that enter the state stay hi + lo.  The scales: q and k by
+// only the hi hi steps, a third of all, then do so at the size of the sum.  With
+// bf16 rows q, k and v fit one fp16 each; the scores, the state and the decayed
+// values are hi + lo as with fp32 rows, so o is rounded once (with single fp16
+// scores and states it was 9e-4 in norm from the rounded fp32 result, now 3e-5;
+// 8 prompts of 4096 tokens took 528 us, now 588).  The scales: q and k by
 // row, v, the decayed values and the state by column dv (the TMEM lane),
 // chosen so that the largest element lies in [2^14, 2^15) (the decayed values'
 // by the values' and a bound of the factors); elements down to 2^-17 of it keep
@@ -45,8 +47,8 @@
 // the main pass runs over all segments at once.
 //
 // Measured (8 prompts of 4096 tokens, 16 / 48 heads): fp32 669 us (2.20 GB,
-// 49 % of the copy rate), bf16 526 us (1.13 GB, 32 %); 33 prompts of up to 111
-// tokens, fp32, 90 us; one of 32701 tokens, 2 / 8 heads, bf16, 127 us.  Bound by
+// 49 % of the copy rate), bf16 588 us (1.13 GB, 29 %); 33 prompts of up to 111
+// tokens, fp32, 90 us; one of 32701 tokens, 2 / 8 heads, bf16, 137 us.  Bound by
 // the latency of each chunk's chain (rows - decay vectors - V operands - KV -
 // state, and scores - P - PV - output) on 4 to 5 warps a scheduler: they issue
 // in 58 % of the cycles, the tensor cores are busy in 35 %, DRAM 40 %.  The
@@ -470,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                          const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v,
                          const __grid_constant__ Args P) {
-  constexpr bool kLo = !kBf16;                 // second parts of q, k, v, P, S
+  constexpr bool kLo = !kBf16;                 // second parts of q, k, v
   constexpr uint32_t kRow = kBf16 ? 256 : 512; // bytes of a token row
   constexpr uint32_t kGrp = 8 * kRow;          // of 8 rows, staged or converted
   extern __shared__ unsigned char smem_raw[];
@@ -631,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           F2 x[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) x[j] = mul2(s[c0 / 2 + j], f);
-          put16<kLo>(tl + T_SOP, tl + T_SOP + 64, 64 * half + c0, x);
+          put16<true>(tl + T_SOP, tl + T_SOP + 64, 64 * half + c0, x);
         }
         if (half == 0) lanef(it)[myrow] = pow2(-e);
         tmem_wait_st();
@@ -782,15 +784,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           uint32_t hi[8], lo[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) split2<kLo>(x[j], hi[j], lo[j]);
+          for (int j = 0; j < 8; ++j) split2<true>(x[j], hi[j], lo[j]);
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             unsigned char *p = pr + ((((s0 >> 3) + c) ^ (t & 7)) << 4);
             *reinterpret_cast<uint4 *>(p) =
                 make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
-            if (kLo)
-              *reinterpret_cast<uint4 *>(p + 8192) =
-                  make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+            *reinterpret_cast<uint4 *>(p + 8192) =
+                make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
           }
         }
       }
@@ -895,17 +896,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_bar(rdy_s, it & 1, fail);
           if (it > 0) wait_bar(acc_free, (it - 1) & 1, fail);
           fence_after_sync();
-          if (kLo)
 #pragma unroll 1
-            for (int ks = 0; ks < kD / 16; ++ks) {
-              const uint32_t a = tm + T_SOP + 8u * ks;
-              mma_ts(one, tm + T_QS, a, desc64(hi, lo_q + ((kstep(ks) + 2048) >> 4)), idn, ks > 0);
-              mma_ts(one, tm + T_QS, a + 64u, desc64(hi, lo_q + (kstep(ks) >> 4)), idn, 1u);
-            }
+          for (int ks = 0; ks < kD / 16; ++ks) {
+            const uint32_t a = tm + T_SOP + 8u * ks;
+            mma_ts(one, tm + T_QS, a + 64u, desc64(hi, lo_q + (kstep(ks) >> 4)), idn, ks > 0);
+            if (kLo)
+              mma_ts(one, tm + T_QS, a, desc64(hi, lo_q + ((kstep(ks) + 2048) >> 4)), idn, 1u);
+          }
 #pragma unroll 1
           for (int ks = 0; ks < kD / 16; ++ks)
             mma_ts(one, tm + T_QS, tm + T_SOP + 8u * ks, desc64(hi, lo_q + (kstep(ks) >> 4)), idn,
-                   kLo || ks > 0);
+                   1u);
         } else {
           // the KV columns are free once the state has taken the last product
           if (it > 0) wait_bar(rdy_s, (it - 1) & 1, fail);
@@ -933,18 +934,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_bar(rdy_p, it & 1, fail);
           wait_bar(done_kv, it & 1, fail);
           fence_after_sync();
-          if (kLo)
 #pragma unroll 1
-            for (int ks = 0; ks < kC / 16; ++ks) {
-              const uint32_t a = tm + T_VOP + 8u * ks;
-              mma_ts(one, tm + T_PV, a, desc64(hi_p, lo_p + ((kstep(ks) + 8192) >> 4)), idn,
-                     ks > 0);
-              mma_ts(one, tm + T_PV, a + 32u, desc64(hi_p, lo_p + (kstep(ks) >> 4)), idn, 1u);
-            }
+          for (int ks = 0; ks < kC / 16; ++ks) {
+            const uint32_t a = tm + T_VOP + 8u * ks;
+            mma_ts(one, tm + T_PV, a, desc64(hi_p, lo_p + ((kstep(ks) + 8192) >> 4)), idn, ks > 0);
+            if (kLo) mma_ts(one, tm + T_PV, a + 32u, desc64(hi_p, lo_p + (kstep(ks) >> 4)), idn, 1u);
+          }
 #pragma unroll 1
           for (int ks = 0; ks < kC / 16; ++ks)
             mma_ts(one, tm + T_PV, tm + T_VOP + 8u * ks,
-                   desc64(hi_p, lo_p + (kstep(ks) >> 4)), idn, kLo || ks > 0);
+                   desc64(hi_p, lo_p + (kstep(ks) >> 4)), idn, 1u);
           commit_one(one, done_o);
         }
       }

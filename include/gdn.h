@@ -457,11 +457,11 @@ size_t gdn_linattn_prefill_workspace(const gdn_shape *shape, int T, int dtype);
  *          smaller, GDN_EINVAL if NULL where bytes are needed); calls that
  *          may overlap on the GPU need one each.
  * 1 <= T <= GDN_MAX_TOKENS and T * vh < 2^31 (GDN_ERANGE otherwise).
- * Numbers: chunks of 64 tokens on tensor cores.  fp32 operands are the sum of
- * two fp16 numbers (22 bits) scaled by rows or columns, bf16 ones a single
- * fp16 (the scores and the state that enter o are then rounded to 11 bits;
- * the state itself is kept in fp32), every sum is fp32: about 3e-7 relative
- * error of an fp32 o and 2e-7 of S, where a step's is 1e-7.  Weights e^{sum of g}
+ * Numbers: chunks of 64 tokens on tensor cores.  Operands are the sum of two
+ * fp16 numbers (22 bits) scaled by rows or columns, bf16 rows a single fp16
+ * (exact); the state is kept in fp32, every sum is fp32: about 3e-7 relative
+ * error of an fp32 o and 2e-7 of S, where a step's is 1e-7.  A bf16 o is
+ * rounded once.  Weights e^{sum of g}
  * below 2^-126 may count as 0, and within 64 tokens g may grow by up to a
  * factor of 2^80.  The same call gives the same bits; another B or T may cut
  * the sequences elsewhere and differ in the last ones.
