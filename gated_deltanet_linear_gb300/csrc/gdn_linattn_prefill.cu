@@ -1104,7 +1104,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           R[i] = fmaxf(R[i], lo);
           const int n = -22 - kx[i];
           vc[VA + t] = fac ? p2(-(int)R[i] - c) : -R[i];
-          vc[VB + t] = fac ? ex2(-gf[i]) * p2(c + n - gr[i]) : (float)n;
+          // (a key row of zeros: no weight, as R_t does not bound one)
+          vc[VB + t] = kx[i] == 127 ? (fac ? 0.f : -1e30f)
+                       : fac        ? ex2(-gf[i]) * p2(c + n - gr[i])
+                                    : (float)n;
           vc[VGH + t] = G[i].h;
           vc[VGL + t] = G[i].l;
         }

@@ -7,8 +7,8 @@ import pytest
 import torch
 
 import gated_deltanet_linear_gb300 as gdn
-from linattn_ref import assert_within, half_step, linattn, make_linattn
-from test_gpu_linattn import TYPES, check_prompt, prompt_tol, run, workspace
+from linattn_ref import linattn, make_linattn
+from test_gpu_linattn import TYPES, check_prompt, run
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +42,36 @@ def test_bf16_prompts_are_rounded_once(decay, B, kh, vh, T):
     off = (o.double() - ref["o"].bfloat16().double()).norm()
     assert off <= 2.0 ** -13 * ref["o"].norm()
     assert (S - ref["S"]).norm() <= 2.0 ** -19 * ref["S"].norm()
+
+
+def floors(d):
+    """What the magnitudes do not cover.  Weights e^{sum of g} below 2^-126 may
+    count as 0: at most |k v| (or |q.k v|, or |S0 q| over 128 rows) of T tokens
+    times that.  A score is off by up to 2^-30 |q_t| |k| (the largest
+    elements), times |v| of 64 tokens: it shows where the tokens near t have
+    v = 0 (derived in test_gpu_linattn.test_zero_rows)."""
+    top = {x: float(d[x].abs().max()) for x in "qkvS"}
+    norm = {x: float(d[x].float().norm(dim=-1).max()) for x in "qk"}
+    T = d["v"].shape[1]
+    size = max(1.0, norm["q"]) * max(norm["k"] * top["v"], top["S"])
+    return ((T + 128) * size * 2.0 ** -126,
+            2.0 ** -30 * top["q"] * top["k"] * 64 * top["v"])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("start,T", [(0, 150), (1344, 1500)])
+@pytest.mark.parametrize("rows,decay", [
+    (slice(10, 11), -200.0), (slice(10, 11), -float("inf")), (slice(20, 40), -12.0),
+    (slice(20, 40), -50.0), (slice(44, 64), -12.0), (slice(0, 20), -50.0),
+    (slice(63, 64), -float("inf"))])
+def test_zero_key_rows_under_strong_decay(dtype, start, T, rows, decay):
+    """Rows of zeros in k that carry strong decays, between ordinary rows."""
+    d = make_linattn(31, 1, T, 1, 2, TYPES[dtype])
+    d["g"].fill_(-0.05)
+    at = slice(start + rows.start, start + rows.stop)
+    d["g"][:, at] = decay
+    d["k"][:, at] = 0
+    S, o = prompt(d)
+    assert torch.isfinite(o).all() and torch.isfinite(S).all()
+    under, score = floors(d)
+    check_prompt(d, S, o, floor_S=under, floor_o=under + score)
