@@ -24,9 +24,10 @@
 // scores and states it was 9e-4 in norm from the rounded fp32 result, now 3e-5;
 // 8 prompts of 4096 tokens took 528 us, now 588).  The scales: q and k by
 // row, v, the decayed values and the state by column dv (the TMEM lane),
-// chosen so that the largest element lies in [2^14, 2^15) (the decayed values'
-// by the values' and a bound of the factors); elements down to 2^-17 of it keep
-// all their bits.  The scores of row t are scaled by a bound of the largest
+// chosen so that the largest element lies in [2^14, 2^15); elements down to 2^-17
+// of it keep all their bits.  (The decayed values take the values' scale where
+// their largest is within that range all the same, by the factors and the last
+// 8 rows.  Always their own took 655 us where this takes 607, bf16.)  The scores of row t are scaled by a bound of the largest
 // |q_t| |k_s| e^{Gamma_t - Gamma_s}, s <= t, so strong decays and rows of very
 // different sizes leave them their bits.  The state is kept in fp32 registers: a chunk's KV
 // product is read out, unscaled and added, so scales may differ from chunk to
@@ -96,10 +97,12 @@ constexpr int VA = 0, VB = 64, VF = 128, VCA = 192, VCB = 256, VGH = 320,
               VGL = 384, VM = 448;
 constexpr uint32_t OFF_VEC = 212992;
 constexpr uint32_t OFF_EXP = OFF_VEC + 4 * 2048;    // row exponents [2][128]
-constexpr uint32_t OFF_LANE = OFF_EXP + 2 * 512;    // column factors [4][2][128]
-constexpr uint32_t OFF_PV = OFF_LANE + 4 * 1024;    // exchange: V maxima [2][2][128]
+constexpr uint32_t OFF_LANE = OFF_EXP + 2 * 512;    // column factors [2][2][128]
+constexpr uint32_t OFF_PV = OFF_LANE + 2 * 1024;    // exchange: V maxima [2][2][128]
 constexpr uint32_t OFF_PS = OFF_PV + 2048;          // exchange: state maxima
-constexpr uint32_t OFF_BAD = OFF_PS + 1024;         // first bad token [4][2][128]
+constexpr uint32_t OFF_PW = OFF_PS + 1024;          // exchange: decayed V maxima
+constexpr uint32_t OFF_P8 = OFF_PW + 1024;          // V maxima of the last rows [2][128]
+constexpr uint32_t OFF_BAD = OFF_P8 + 1024;         // first bad token [4][2][128]
 constexpr uint32_t OFF_BAR = OFF_BAD + 1024;
 constexpr uint32_t kSmemUsed = OFF_BAR + 256;
 constexpr uint32_t kSmemAlloc = kSmemUsed + 1024;   // room to align the base
@@ -491,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int *fail = reinterpret_cast<volatile int *>(gb + OFF_BAR + 188);
   auto vec = [&](int it) { return reinterpret_cast<float *>(gb + OFF_VEC + (it & 3) * 2048); };
   auto rowexp = [&](int it) { return reinterpret_cast<int *>(gb + OFF_EXP + (it & 1) * 512); };
-  auto lanef = [&](int it) { return reinterpret_cast<float *>(gb + OFF_LANE + (it & 3) * 1024); };
+  auto lanef = [&](int it) { return reinterpret_cast<float *>(gb + OFF_LANE + (it & 1) * 1024); };
 
   // first token of a chunk whose v is not finite, by half and column
   auto badtok = [&](int it) {
@@ -527,7 +530,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ============================================ group A: state, V operands
     F2 s[kC / 2];  // state rows dk = 64 half .. + 63 of column dv = myrow
     float *ps = reinterpret_cast<float *>(gb + OFF_PS);
+    float *pw = reinterpret_cast<float *>(gb + OFF_PW);
     auto px = [&](int it) { return reinterpret_cast<float *>(gb + OFF_PV + (it & 1) * 1024); };
+    auto p8 = [&](int it) { return reinterpret_cast<float *>(gb + OFF_P8 + (it & 1) * 512); };
     // this thread's 32 v values of a chunk: column myrow of rows 32 half ..
     auto vcol = [&](int it) {
       return gb + OFF_V + (it & 1) * kV + 32 * half * kRow + myrow * (kRow / kD);
@@ -541,7 +546,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       return pack(*reinterpret_cast<const float *>(vp + t * kRow),
                   *reinterpret_cast<const float *>(vp + (t + 1) * kRow));
     };
-    // The largest |v| of chunk `it` and what is not finite, to the exchange.
+    // The largest |v| of chunk `it` (and of its last 8 rows) and what is not finite,
+    // to the exchange.
     auto v_max = [&](int it, int valid) {
       wait_bar(vstaged + 8 * (it & 1), (it >> 1) & 1, fail);
       unsigned char *vp = vcol(it);
@@ -556,14 +562,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async();  // the copy engine writes these bytes next
       }
-      float m = 0.f;
+      float m = 0.f, m8;
 #pragma unroll 1
-      for (int t0 = 0; t0 < 32; t0 += 16)
+      for (int t0 = 0; t0 < 32; t0 += 8) {
+        m8 = 0.f;
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {
+        for (int j = 0; j < 8; j += 2) {
           const float2 f = unpack(vload(vp, t0 + j));
-          m = amax(m, f.x, f.y);
+          m8 = amax(m8, f.x, f.y);
         }
+        m = amax(m, m8);
+      }
+      if (half) p8(it)[myrow] = m8;
       // A value that is not finite must not reach the rows before it (its
       // weight there is 0, but 0 * inf is NaN): PV takes 0 for it, and the
       // output becomes NaN from its token on.
@@ -640,9 +650,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         signal_ready<false>(rdy_s);
       }
       // ---- V^T and (V f)^T operands, lane dv, K = t = 32 half .. + 31
-      const int ea = scale_exp(amax(px(it)[myrow], px(it)[128 + myrow]));
+      const float vmax = amax(px(it)[myrow], px(it)[128 + myrow]);
+      const int ea = scale_exp(vmax);
       wait_bar(vecs + 8 * (it & 3), (it >> 2) & 1, fail);
-      const float gC = vec(it)[VM], inv = pow2(-ea) * vec(it)[VM + 2];
+      const unsigned char *vp = vcol(it);
+      // Whether the decayed values need a scale of their own: some rows count for
+      // less than 2^-17 of others (strong decays, key rows of zeros or of very
+      // different sizes) and a column's last 8 values do not outweigh that.
+      const bool need = __any_sync(0xffffffffu, p8(it)[myrow] * vec(it)[VM + 3] < vmax);
+      int ew = ea;
+      const float gC = vec(it)[VM];
+      float inv;
       {
         const F2 fa = pack(pow2(ea), pow2(ea));
         if (!kLocal) {
@@ -652,7 +670,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_after_sync();
           if (half == 0) lanef(it)[128 + myrow] = pow2(-ea);
         }
-        const unsigned char *vp = vcol(it);
         const bool any_bad =
             !kLocal && __any_sync(0xffffffffu, badtok(it)[128 * half + myrow] < kC);
 #pragma unroll 1
@@ -675,6 +692,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             put16<kLo>(tl + T_VOP, tl + T_VOP + 32, 32 * half + t0, x);
           }
         }
+        if (__builtin_expect(need, 0)) {
+          // The decayed values once more, scaled by their own largest, lest fp16
+          // take their bits (or all of them: where v or k are zeros in the rows that
+          // weigh most, the others are the whole state).  The exchange is
+          // written again a chunk later, behind the barrier above.
+          const F2 *vf = reinterpret_cast<const F2 *>(vec(it) + VF + 32 * half);
+          float m = 0.f;
+#pragma unroll 1
+          for (int t = 0; t < 32; t += 2) {
+            const float2 y = unpack(mul2(vload(vp, t), vf[t / 2]));
+            m = amax(m, y.x, y.y);
+          }
+          pw[128 * half + myrow] = m;
+          bar_pair(quad);
+          ew = scale_exp(amax(pw[myrow], pw[128 + myrow]));
+          const F2 fw = pack(pow2(ew), pow2(ew));
+#pragma unroll 1
+          for (int t0 = 0; t0 < 32; t0 += 16) {
+            F2 y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)  // (in this order: no step leaves the floats)
+              y[j] = mul2(mul2(vload(vp, t0 + 2 * j), vf[t0 / 2 + j]), fw);
+            put16<true>(tl + T_WOP, tl + T_WOP + 32, 32 * half + t0, y);
+          }
+        }
+        inv = pow2(-ew) * vec(it)[VM + 2];
         tmem_wait_st();
         signal_ready<false>(rdy_v);
         if (lane == 0) mbar_arrive(v_free + 8 * (it & 1));
@@ -1010,13 +1053,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                    : ((size_t)w.b * P.T + (size_t)w.c * kC) * P.vh + w.vi;
       const size_t step = P.g_head ? 0 : (size_t)P.vh;
       Two G[2];  // cumulative
-      bool up = false;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int t = 2 * lane + i;
         float x = t < nv ? __ldg(P.g + base + t * step) : 0.f;
         if (x < -1e4f) x = -1e4f;  // -inf: a decay that no float survives; NaN stays
-        up |= x > 0.f;
         const float h = x * 1.44269502f;  // log2 e = 1.44269502 + 1.925963e-8
         G[i] = Two{h, fmaf(x, 1.44269502f, -h) + x * 1.925963033e-8f};
       }
@@ -1035,40 +1076,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       total += (double)end.h + (double)end.l;
       float *vc = vec(it);
-      // the decay from each token to the chunk's end
-      float wt[2], gf[2];  // the weights; Gamma_t = gr + gf
-      int gr[2];
+      // Gamma_t = gr + gf, and the decay from each token to the chunk's end,
+      // 2^(dr + df): integer and rest, so that a weight has its bits however
+      // small it is
+      float gf[2], df[2];
+      int gr[2], dr[2];
+      auto parts = [](Two x, int &whole, float &rest) {
+        const float r = rintf(x.h);
+        whole = (int)r;
+        rest = (x.h - r) + x.l;
+      };
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        wt[i] = ex2((end.h - G[i].h) + (end.l - G[i].l));
-        const float whole = rintf(G[i].h);
-        gr[i] = (int)whole;
-        gf[i] = (G[i].h - whole) + G[i].l;
+        parts(G[i], gr[i], gf[i]);
+        parts(add2(end, Two{-G[i].h, -G[i].l}), dr[i], df[i]);
       }
-      int grow = 0;
-      if (__any_sync(0xffffffffu, up)) {
-        // growth: the largest Gamma_t - Gamma_s, s <= t (0 for decays)
-        float lo = fminf(G[0].h, G[1].h), run_lo = lo;
-#pragma unroll 1
-        for (int off = 1; off < 32; off <<= 1) {
-          const float y = __shfl_up_sync(0xffffffffu, run_lo, off);
-          if (lane >= off) run_lo = fminf(run_lo, y);
-        }
-        float d = fmaxf(fmaxf(G[0].h, G[1].h) - run_lo, 0.f);
-#pragma unroll 1
-        for (int off = 16; off; off >>= 1) d = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, off));
-        grow = (int)ceilf(fminf(d, 80.f));
-      }
-      const float gend = ex2(end.h + end.l);
+      int er;
+      float ef;
+      parts(end, er, ef);
       wait_bar(rdy_kq + 8 * (it & 1), (it >> 1) & 1, fail);
       const int *ex = rowexp(it);
       const int2 k2 = *reinterpret_cast<const int2 *>(ex + 2 * lane);
       const int kx[2] = {k2.x, k2.y};
-      // the smallest exponent (the largest k row) of the finite rows
-      const int least = __reduce_min_sync(
-          0xffffffffu, min(k2.x > -114 ? k2.x : 127, k2.y > -114 ? k2.y : 127));
-      // (exactly; 0 below the normal floats)
-      auto p2 = [](int e) { return e < -126 ? 0.f : pow2(min(e, 127)); };
+      // (exactly; 0 below the normal floats, infinity above them)
+      auto p2 = [](int e) { return e < -126 ? 0.f : pow2(min(e, 128)); };
       // The weight of row s in P[t], by its logarithm: r_s = -Gamma_s - kx_s,
       // and Gamma_t for every s.  R_t >= the largest r_s, s <= t, so P[t][s] =
       // G 2^{r_s - R_t - 22} keeps its bits whatever the decays and the rows'
@@ -1114,14 +1145,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) vc[VM + 1] = fac ? 1.f : 0.f;
       }
       // f_t = (decay to the end) / (k row scale), relative to a power of two
-      // that bounds it: the growth's and the largest row's
-      const int fe = min(max(grow - least + 1, -126), 126);
+      // that bounds it: the largest of the rows that are finite and not zeros
+      // (those have f = 0)
+      bool row[2];
+      int top = -1 << 24;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)  // (a k row that is not finite: the state is lost)
-        vc[VF + 2 * lane + i] = kx[i] > -114 ? wt[i] * p2(-kx[i] - fe) : __int_as_float(0x7fffffff);
+      for (int i = 0; i < 2; ++i) {
+        row[i] = kx[i] > -114 && kx[i] < 127;
+        if (row[i]) top = max(top, dr[i] - kx[i]);
+      }
+      const int fe = min(max(__reduce_max_sync(0xffffffffu, top) + 1, -126), 126);
+      bool uneven = false;
+      float f8 = 1.f;  // the least of the last 8 rows
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {  // (a k row that is not finite: the state is lost)
+        const int t = 2 * lane + i;
+        const float f = row[i]          ? ex2(df[i]) * p2(dr[i] - kx[i] - fe)
+                        : kx[i] == 127 ? 0.f
+                                       : __int_as_float(0x7fffffff);
+        vc[VF + t] = f;
+        uneven |= t < nv && f < 0x1p-17f;
+        f8 = fminf(f8, f);
+      }
+      uneven = __any_sync(0xffffffffu, uneven);
+      f8 = __uint_as_float(__reduce_min_sync(0xffffffffu, lane < 28 ? ~0u : __float_as_uint(f8)));
       if (lane == 0) {
-        vc[VM] = gend;
+        vc[VM] = ex2(ef) * p2(er);
         vc[VM + 2] = pow2(fe);
+        vc[VM + 3] = uneven ? 0x1p17f * f8 : __int_as_float(0x7f800000);
       }
       if (!kLocal) {  // the output's factors
         const int2 q2 = *reinterpret_cast<const int2 *>(ex + 64 + 2 * lane);

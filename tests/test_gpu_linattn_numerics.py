@@ -7,8 +7,8 @@ import pytest
 import torch
 
 import gated_deltanet_linear_gb300 as gdn
-from linattn_ref import linattn, make_linattn
-from test_gpu_linattn import TYPES, check_prompt, run
+from linattn_ref import assert_within, linattn, make_linattn
+from test_gpu_linattn import TYPES, check_prompt, prompt_tol, run, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -56,6 +56,54 @@ def floors(d):
     size = max(1.0, norm["q"]) * max(norm["k"] * top["v"], top["S"])
     return ((T + 128) * size * 2.0 ** -126,
             2.0 ** -30 * top["q"] * top["k"] * 64 * top["v"])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("what", ["k", "v", "columns"])
+@pytest.mark.parametrize("decay", [-0.5, -1.0, -2.0])
+@pytest.mark.parametrize("start,T", [(0, 64), (64, 150), (1344, 1500)])
+def test_state_after_rows_of_zeros(dtype, what, decay, start, T):
+    """The last rows of a chunk (and the chunks behind it) are zeros, and the
+    decays leave small weights for the others: they are the whole state.
+    (1500 tokens of 2 heads are cut into segments.)"""
+    for keep in (16, 32, 48, 56):
+        d = make_linattn(keep, 1, T, 1, 2, TYPES[dtype])
+        assert (workspace(d).numel() > 0) == (T == 1500)
+        d["S"].zero_()
+        d["g"].fill_(decay)
+        if what == "columns":  # of v, five of them
+            d["v"][:, start + keep:, :, 7:12] = 0
+        else:
+            d[what][:, start + keep:] = 0
+        S, o = prompt(d)
+        under, score = floors(d)
+        check_prompt(d, S, o, floor_S=under, floor_o=under + score)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("late", [False, True])
+def test_state_of_small_rows(dtype, late):
+    """Key rows 2^-40 of the others', the others with v = 0: they are the whole
+    state; and values beside a zero key row do not count, whatever their
+    size."""
+    d = make_linattn(3, 1, 64, 1, 2, TYPES[dtype])
+    d["S"].zero_()
+    d["g"].zero_()
+    small = slice(32, 64) if late else slice(0, 32)
+    big = slice(0, 32) if late else slice(32, 64)
+    d["k"][:, small] *= 2.0 ** -40
+    d["v"][:, big] = 0
+    S, _ = prompt(d)
+    ref = linattn(d["S"], d["q"], d["k"], d["v"], d["g"])
+    t = prompt_tol(64)[0]
+    assert_within(S, ref["S"], t * ref["mS"], "S of small rows")
+    d = make_linattn(4, 1, 64, 1, 2, TYPES[dtype])
+    d["S"].zero_()
+    d["k"][:, 60 if late else 5] = 0
+    d["v"][:, 60 if late else 5] = 1e14
+    S, _ = prompt(d)
+    ref = linattn(d["S"], d["q"], d["k"], d["v"], d["g"])
+    assert_within(S, ref["S"], t * ref["mS"], "S beside a zero key row")
 
 
 @pytest.mark.parametrize("dtype", TYPES)
