@@ -120,6 +120,11 @@ __host__ __device__ constexpr uint32_t idesc16(int M, int N, int b_mn) {
          ((uint32_t)(M >> 4) << 24);
 }
 
+// The output's factors by column carry 2^-15 and those by row 2^15, so that a
+// product times the first stays below 128 times its column's largest element.
+constexpr float kOut = 0x1p-15f;
+constexpr int kOutExp = 15;
+
 struct Args {
   float *S;             // [B][vh][128][128], in/out
   float *ws_state;      // [B vh][nseg][128][128]: own sums, then start states
@@ -645,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 8; ++j) x[j] = mul2(s[c0 / 2 + j], f);
           put16<true>(tl + T_SOP, tl + T_SOP + 64, 64 * half + c0, x);
         }
-        if (half == 0) lanef(it)[myrow] = pow2(-e);
+        if (half == 0) lanef(it)[myrow] = pow2(-e) * kOut;
         tmem_wait_st();
         signal_ready<false>(rdy_s);
       }
@@ -668,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // decayed ones once the output has been made of it
           if (it > 0) wait_bar(acc_free, (it - 1) & 1, fail);
           fence_after_sync();
-          if (half == 0) lanef(it)[128 + myrow] = pow2(-ea);
+          if (half == 0) lanef(it)[128 + myrow] = pow2(-ea) * kOut;
         }
         const bool any_bad =
             !kLocal && __any_sync(0xffffffffu, badtok(it)[128 * half + myrow] < kC);
@@ -1105,6 +1110,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // G 2^{r_s - R_t - 22} keeps its bits whatever the decays and the rows'
       // sizes (|G| <= 2^37).
       float R[2] = {0.f, 0.f};
+      bool some_row[2];  // some row up to this one is not zeros
       if (!kLocal) {
         const float none = -3e38f;
         float r[2];
@@ -1132,6 +1138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int t = 2 * lane + i;
+          some_row[i] = R[i] > none;
           R[i] = fmaxf(R[i], lo);
           const int n = -22 - kx[i];
           vc[VA + t] = fac ? p2(-(int)R[i] - c) : -R[i];
@@ -1180,10 +1187,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int t = 2 * lane + i;
-          const float e = P.scale * ex2(gf[i]);
-          vc[VCA + t] = e * p2(gr[i] - qx[i]);
-          // what P[t] and q_t are scaled by (finite also where P[t] is all zeros)
-          vc[VCB + t] = e * p2(min(gr[i] + (int)R[i] + 22 - qx[i], 100));
+          const float e = ex2(gf[i]);
+          vc[VCA + t] = P.scale * (e * p2(gr[i] - qx[i] + kOutExp));
+          // what P[t] and q_t are scaled by (where P[t] is all zeros, any)
+          vc[VCB + t] =
+              some_row[i] ? P.scale * (e * p2(gr[i] + (int)R[i] + 22 - qx[i] + kOutExp)) : 0.f;
         }
       }
       __syncwarp();

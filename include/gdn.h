@@ -462,8 +462,10 @@ size_t gdn_linattn_prefill_workspace(const gdn_shape *shape, int T, int dtype);
  * (exact); the state is kept in fp32, every sum is fp32: about 3e-7 relative
  * error of an fp32 o and 2e-7 of S, where a step's is 1e-7.  A bf16 o is
  * rounded once.  Weights e^{sum of g}
- * below 2^-126 may count as 0, and within 64 tokens g may grow by up to a
- * factor of 2^80.  The same call gives the same bits; another B or T may cut
+ * below 2^-126 may count as 0, and within 64 tokens e^{sum of g} may grow by up
+ * to a factor of 2^80.  An o that is finite is met for |v|, |S| up to 2^118 and
+ * products |q_i| |k_j| of elements (times that growth) up to 2^115; beyond that
+ * it may become infinite or NaN.  The same call gives the same bits; another B or T may cut
  * the sequences elsewhere and differ in the last ones.
  * What is not finite stays with its heads and never reaches a token before
  * its own: in q it makes its row of o not finite, in v its column from its

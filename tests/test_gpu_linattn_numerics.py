@@ -123,3 +123,29 @@ def test_zero_key_rows_under_strong_decay(dtype, start, T, rows, decay):
     assert torch.isfinite(o).all() and torch.isfinite(S).all()
     under, score = floors(d)
     check_prompt(d, S, o, floor_S=under, floor_o=under + score)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("size", [dict(q=1e18, k=1e18), dict(v=2.0 ** 118, S=2.0 ** 118),
+                                  dict(k=2.0 ** 100, q=2.0 ** -90), dict(S=2.0 ** 118, q=2.0 ** -60),
+                                  dict(v=2.0 ** -110, S=2.0 ** -110, q=2.0 ** 50)])
+def test_large_and_small_elements(dtype, size):
+    """Elements whose products come near the range of a float, while o and S
+    stay within it: as the token steps have them."""
+    d = make_linattn(13, 1, 100, 1, 2, TYPES[dtype])
+    if "S" in size:  # (make_linattn's state is 0.1 of its values)
+        size = dict(size, S=10 * size["S"])
+    for x, s in size.items():
+        d[x] *= s
+    S, o = prompt(d)
+    # (products of fp32 numbers near 2^-126 are rounded to its subnormals)
+    check_prompt(d, S, o, floor_S=64 * 2.0 ** -126, floor_o=64 * 2.0 ** -126)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_large_scale(dtype):
+    """The factor on o meets small rows before it could leave the floats."""
+    d = make_linattn(14, 1, 100, 1, 2, TYPES[dtype])
+    d["q"] *= 2.0 ** -40
+    S, o = prompt(d, scale=2.9e38)
+    check_prompt(d, S, o, scale=2.9e38)
