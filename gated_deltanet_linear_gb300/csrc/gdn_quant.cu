@@ -489,9 +489,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma<kBf16>(part[j], c0[2], c1[2], c0[3], c1[3], x4.z, x4.w, part[j]);
             }
             if ((i + 1) % kSteps == 0) {
-              // (a group behind the last one has zeros of x against any scale)
+              // (a group behind the last one counts as 0 against any scale)
               const int gi = min(g0 + g, groups - 1);
-              const float f0 = __half2float(s0p[gi]), f1 = __half2float(s1p[gi]);
+              const float f0 = g0 + g < groups ? __half2float(s0p[gi]) : 0.f;
+              const float f1 = g0 + g < groups ? __half2float(s1p[gi]) : 0.f;
 #pragma unroll
               for (int j = 0; j < kNT; ++j) {
                 if (kBf16) {

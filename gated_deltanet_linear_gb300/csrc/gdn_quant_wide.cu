@@ -210,8 +210,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __half sn[2];
     float xv[2][kBf16 ? 1 : kParts][8];
     auto fetch = [&](int u, int s) {
-      // (a group behind the last one has zeros of x against any scale)
-      if (piece < kGroups) sn[u] = __ldg(sp + min((s_lo + s) * kGroups + piece, groups - 1));
+      // (a group behind the last one counts as 0 against any scale)
+      if (piece < kGroups) {
+        const int g = (s_lo + s) * kGroups + piece;
+        sn[u] = g < groups ? __ldg(sp + g) : __half(0.f);
+      }
       if constexpr (!kBf16) {
         const int k = (s_lo + s) * kStage + 8 * (tid & 15);
 #pragma unroll

@@ -223,3 +223,21 @@ def test_refusals():
         gdn.gdn_quant_linear(big, torch.zeros(64, 32, device="cuda", dtype=torch.uint8),
                              torch.ones(64, 1, device="cuda").half(), big)
     assert e.value.status == gdn.GDN_EALIAS
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", [1, 5, 40])
+@pytest.mark.parametrize("K", [32, 96, 288])
+def test_infinite_scales(dtype, rows, K):
+    """An infinite scale of the last group of a row whose length ends inside a
+    block gives an infinity, and NaN stays with its row of weights."""
+    x = torch.ones(rows, K, device="cuda", dtype=TYPES[dtype])
+    qw = torch.full((7, K // 2), 0x11, device="cuda", dtype=torch.uint8)
+    sc = torch.ones(7, K // 32, device="cuda", dtype=torch.float16)
+    sc[2, -1], sc[4, -1], sc[5, -1] = float("inf"), -float("inf"), float("nan")
+    y = torch.empty(rows, 7, device="cuda", dtype=TYPES[dtype])
+    gdn.gdn_quant_linear(x, qw, sc, y)
+    want = torch.full_like(y, K)
+    want[:, 2], want[:, 4], want[:, 5] = float("inf"), -float("inf"), float("nan")
+    assert torch.equal(y.isnan(), want.isnan())
+    assert torch.equal(y.nan_to_num(1.5, 1e38, -1e38), want.nan_to_num(1.5, 1e38, -1e38))
