@@ -149,3 +149,25 @@ def test_large_scale(dtype):
     d["q"] *= 2.0 ** -40
     S, o = prompt(d, scale=2.9e38)
     check_prompt(d, S, o, scale=2.9e38)
+
+
+@pytest.mark.parametrize("slow", [False, True])
+@pytest.mark.parametrize("B,kh,vh,T", [(1, 1, 2, 90), (2, 2, 6, 190), (1, 1, 1, 700),
+                                       (2, 2, 4, 1500), (1, 1, 2, 2500)])
+def test_fp32_prompts_keep_fp32(slow, B, kh, vh, T):
+    """Normwise error of every head's o and state, the same at any length: an
+    operand that lost its second part is off by 2^-12 an element and by 2^-13
+    to 2^-14 in norm; the operands as they should be, 2^-22 each, and the
+    truncating sums of at most 8 steps, 2^-23 each, by 2^-20 if they all went
+    one way.  2^-19 is between.  Slow decays, so that the start states of
+    the segments (T >= 700) matter."""
+    d = make_linattn(T, B, T, kh, vh)
+    assert (workspace(d).numel() > 0) == (T >= 700)
+    if slow:
+        d["g"].mul_(0.01)
+    S, o = prompt(d)
+    ref = linattn(d["S"], d["q"], d["k"], d["v"], d["g"])
+    off = (o - ref["o"]).norm(dim=(1, 3)) / ref["o"].norm(dim=(1, 3))
+    assert float(off.max()) <= 2.0 ** -19
+    off = (S - ref["S"]).norm(dim=(2, 3)) / ref["S"].norm(dim=(2, 3))
+    assert float(off.max()) <= 2.0 ** -19
