@@ -241,3 +241,51 @@ def test_infinite_scales(dtype, rows, K):
     want[:, 2], want[:, 4], want[:, 5] = float("inf"), -float("inf"), float("nan")
     assert torch.equal(y.isnan(), want.isnan())
     assert torch.equal(y.nan_to_num(1.5, 1e38, -1e38), want.nan_to_num(1.5, 1e38, -1e38))
+
+
+@pytest.mark.parametrize("B,T", [(2, 90), (1, 300)])
+def test_layer_run_after_a_prompt(B, T):
+    """The same layer over a padded prompt, then one token: projections of all
+    rows, prompt, token, gated norm, out-projection, against fp64."""
+    kh, vh, hidden = 2, 4, 512
+    conv = 2 * kh * 128 + vh * 128
+    rows = B * (T + 1)
+    x, w_in, s_in = make_quant(11, rows, conv, hidden, 64)
+    z, w_out, s_out = make_quant(12, rows, hidden, vh * 128, 64)
+    d = make_linattn(13, B, 1, kh, vh, decay="head")
+    lens = torch.tensor([T - 17] + [T] * (B - 1), dtype=torch.int32, device="cuda")
+    w = torch.ones(128, device="cuda")
+    proj = torch.empty(rows, conv, device="cuda")
+    gdn.gdn_quant_linear(x, w_in, s_in, proj)
+    parts = proj.view(B, T + 1, conv).split([kh * 128, kh * 128, vh * 128], 2)
+    q, k, v = (t.reshape(B, T + 1, -1, 128) for t in parts)
+    S = d["S"].clone()
+    o = torch.zeros(B, T + 1, vh, 128, device="cuda")
+    n = gdn.gdn_linattn_prefill_workspace(B, kh, vh, T)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    po, to = torch.zeros(B, T, vh, 128, device="cuda"), torch.empty(B, vh, 128, device="cuda")
+    gdn.gdn_linattn_prefill(S, *(t[:, :T].contiguous() for t in (q, k, v)), d["g"], po,
+                            lens=lens, workspace=ws)
+    gdn.gdn_linattn_step(S, *(t[:, T].contiguous() for t in (q, k, v)), d["g"], to)
+    o[:, :T], o[:, T] = po, to
+    y = torch.empty_like(o)
+    gdn.gdn_gated_rmsnorm_m(o, z.view_as(o), w, y)
+    out = torch.empty(rows, hidden, device="cuda")
+    gdn.gdn_quant_linear(y.view(rows, vh * 128), w_out, s_out, out)
+    # fp64
+    p, _ = quant_linear(x, w_in, s_in)
+    parts = p.view(B, T + 1, conv).split([kh * 128, kh * 128, vh * 128], 2)
+    q, k, v = (t.reshape(B, T + 1, -1, 128) for t in parts)
+    first = linattn(d["S"], q[:, :T], k[:, :T], v[:, :T], d["g"], lens=lens.long())
+    token = linattn(first["S"], q[:, T:], k[:, T:], v[:, T:], d["g"])
+    on = torch.arange(T, device="cuda") < lens[:, None]
+    ref = torch.cat([first["o"] * on[..., None, None], token["o"]], 1)
+    r = ref / (ref.square().mean(-1, keepdim=True) + 1e-6).sqrt()
+    zz = z.double().view_as(r)
+    r = (r * zz * torch.sigmoid(zz)).view(rows, vh * 128)
+    want, _ = quant_linear(r, w_out, s_out)
+    # (as in test_layer_run)
+    assert (out - want).norm() <= 2.0 ** -12 * want.norm()
+    assert (S - token["S"]).norm() <= 2.0 ** -12 * token["S"].norm()
+    pad = ~torch.cat([on, on.new_ones(B, 1)], 1).view(rows)
+    assert (out[pad] == 0).all()
