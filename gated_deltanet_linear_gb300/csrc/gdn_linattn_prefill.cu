@@ -100,8 +100,7 @@ constexpr uint32_t OFF_EXP = OFF_VEC + 4 * 2048;    // row exponents [2][128]
 constexpr uint32_t OFF_LANE = OFF_EXP + 2 * 512;    // column factors [2][2][128]
 constexpr uint32_t OFF_PV = OFF_LANE + 2 * 1024;    // exchange: V maxima [2][2][128]
 constexpr uint32_t OFF_PS = OFF_PV + 2048;          // exchange: state maxima
-constexpr uint32_t OFF_PW = OFF_PS + 1024;          // exchange: decayed V maxima
-constexpr uint32_t OFF_P8 = OFF_PW + 1024;          // V maxima of the last rows [2][128]
+constexpr uint32_t OFF_P8 = OFF_PS + 1024;          // V maxima of the last rows [2][128]
 constexpr uint32_t OFF_BAD = OFF_P8 + 1024;         // first bad token [4][2][128]
 constexpr uint32_t OFF_BAR = OFF_BAD + 1024;
 constexpr uint32_t kSmemUsed = OFF_BAR + 256;
@@ -535,7 +534,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ============================================ group A: state, V operands
     F2 s[kC / 2];  // state rows dk = 64 half .. + 63 of column dv = myrow
     float *ps = reinterpret_cast<float *>(gb + OFF_PS);
-    float *pw = reinterpret_cast<float *>(gb + OFF_PW);
     auto px = [&](int it) { return reinterpret_cast<float *>(gb + OFF_PV + (it & 1) * 1024); };
     auto p8 = [&](int it) { return reinterpret_cast<float *>(gb + OFF_P8 + (it & 1) * 512); };
     // this thread's 32 v values of a chunk: column myrow of rows 32 half ..
@@ -700,18 +698,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (__builtin_expect(need, 0)) {
           // The decayed values once more, scaled by their own largest, lest fp16
           // take their bits (or all of them: where v or k are zeros in the rows that
-          // weigh most, the others are the whole state).  The exchange is
-          // written again a chunk later, behind the barrier above.
-          const F2 *vf = reinterpret_cast<const F2 *>(vec(it) + VF + 32 * half);
+          // weigh most, the others are the whole state).  Both halves go through
+          // all 64 rows: a barrier here would be passed by some warps alone where a
+          // wait has run out.
+          const F2 *vf = reinterpret_cast<const F2 *>(vec(it) + VF);
+          const unsigned char *v0 = vp - 32 * half * kRow;
           float m = 0.f;
-#pragma unroll 1
-          for (int t = 0; t < 32; t += 2) {
-            const float2 y = unpack(mul2(vload(vp, t), vf[t / 2]));
+#pragma unroll 2
+          for (int t = 0; t < kC; t += 2) {
+            const float2 y = unpack(mul2(vload(v0, t), vf[t / 2]));
             m = amax(m, y.x, y.y);
           }
-          pw[128 * half + myrow] = m;
-          bar_pair(quad);
-          ew = scale_exp(amax(pw[myrow], pw[128 + myrow]));
+          ew = scale_exp(m);
+          vf += 16 * half;
           const F2 fw = pack(pow2(ew), pow2(ew));
 #pragma unroll 1
           for (int t0 = 0; t0 < 32; t0 += 16) {
