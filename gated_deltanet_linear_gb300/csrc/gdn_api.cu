@@ -597,7 +597,7 @@ int gdn_linattn_step(const gdn_shape *s, int dtype, int decay, float scale,
 
 size_t gdn_linattn_prefill_workspace(const gdn_shape *s, int T, int dtype) {
   if (check_shape(s) || T < 1 || T > GDN_MAX_TOKENS || !element_size(dtype)) return 0;
-  return gdn::linattn_prefill_workspace_bytes(s->B, s->vh, T, dtype == GDN_BF16);
+  return gdn::linattn_prefill_workspace_bytes(s->B, s->vh, T);
 }
 
 int gdn_linattn_prefill(const gdn_shape *s, int T, int dtype, int decay,

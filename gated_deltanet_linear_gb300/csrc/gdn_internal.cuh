@@ -74,7 +74,7 @@ cudaError_t launch_rollback_seq(float *S, const float *snap, const float *ckpt,
 // rows q, k, v, o in fp32 or bf16, states and g in fp32.  S_out may equal
 // S_in, ckpt may be null.  lens (device, or null): sequence b has its first
 // lens[b] of the M tokens; a value outside 0..M leaves the sequence alone
-// and raises *err (may be null).
+// and raises *err (may be null); the prompts alone take lens and err.
 struct LinattnArgs {
   const float *S_in;
   float *S_out, *ckpt;
@@ -90,7 +90,7 @@ struct LinattnArgs {
 cudaError_t launch_linattn_steps(const LinattnArgs &P, bool bf16,
                                  cudaStream_t stream);
 // The same over whole prompts (gdn_linattn_prefill), in place.
-size_t linattn_prefill_workspace_bytes(int B, int vh, int T, bool bf16);
+size_t linattn_prefill_workspace_bytes(int B, int vh, int T);
 cudaError_t launch_linattn_prefill(const LinattnArgs &P, bool bf16,
                                    void *workspace, cudaStream_t stream);
 // CTAs of it that gave up a wait.

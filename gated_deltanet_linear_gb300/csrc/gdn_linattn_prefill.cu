@@ -1331,7 +1331,7 @@ cudaError_t launch(const CUtensorMap *m, const Args &a, cudaStream_t stream) {
 
 }  // namespace
 
-size_t linattn_prefill_workspace_bytes(int B, int vh, int T, bool) {
+size_t linattn_prefill_workspace_bytes(int B, int vh, int T) {
   const size_t heads = (size_t)B * vh;
   const size_t nseg = (size_t)plan(B, vh, T);
   const size_t bytes = heads * nseg * (kD * kD * sizeof(float) + 2 * sizeof(double));

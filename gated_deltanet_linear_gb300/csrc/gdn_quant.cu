@@ -11,7 +11,8 @@
 // columns does not pay for that.)
 //
 //   fp32 x   two columns per row: x 2^e = hi + lo in fp16 (22 bits; e by row
-//            and block of 128, so that the largest element is in [2^14, 2^15))
+//            and block of 256, so that the largest element is in [2^14, 2^15);
+//            elements below 2^-17 of it keep fewer, the lo part ends at 2^-24)
 //   bf16 x   one column per row, as it is; the codes as bf16
 //
 // Weights.  A warp takes blocks of 16 rows x 256 codes (128 bytes of each row)
@@ -214,8 +215,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int gr = lane >> 2, t = lane & 3;
 
   // shared memory: the warps' rings, partial sums, x (a column is round_blocks *
-  // 512 + 64 bytes), then by block: 2^-e of each row (fp32), then by slice and tile: the first warp in it and the number
-  // of warps, then the scales of the round's rows
+  // 512 + 64 bytes), then by block: 2^-e of each row (fp32), then by slice and
+  // tile: the first warp in it and the number of warps, then the scales of the
+  // round's rows
   const uint32_t xstride = (uint32_t)P.round_blocks * kXBlock + 64;
   const uint32_t ring =
       (uint32_t)__cvta_generic_to_shared(smem) + warp * kDepth * kBlockBytes;
@@ -242,327 +244,325 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int groups = P.K / kGroup;
 
   const int nr = P.rows;  // at most kRowsX
-  {
-    for (int t0 = cluster * P.round_tiles; t0 < P.tiles; t0 += clusters * P.round_tiles) {
-      const int nt = min(P.round_tiles, P.tiles - t0);
-      const int own = (unsigned)(nt + csize - 1) / (unsigned)csize;  // tiles a CTA adds up
-      const int most = most_warps(nt, P.round_blocks);
-      for (int kr = 0; kr < P.blocks; kr += csize * P.round_blocks) {
-        int b_lo, nb;
-        slice(P, csize, crank, b_lo, nb);
-        b_lo += kr;
-        const unsigned total = nt * nb;
-        int pos = share(total, warp);
-        const int end = share(total, warp + 1);
+  for (int t0 = cluster * P.round_tiles; t0 < P.tiles; t0 += clusters * P.round_tiles) {
+    const int nt = min(P.round_tiles, P.tiles - t0);
+    const int own = (unsigned)(nt + csize - 1) / (unsigned)csize;  // tiles a CTA adds up
+    const int most = most_warps(nt, P.round_blocks);
+    for (int kr = 0; kr < P.blocks; kr += csize * P.round_blocks) {
+      int b_lo, nb;
+      slice(P, csize, crank, b_lo, nb);
+      b_lo += kr;
+      const unsigned total = nt * nb;
+      int pos = share(total, warp);
+      const int end = share(total, warp + 1);
 
-        // ---- weights: the next block of this warp's list into its ring.  Lane
-        // l copies 16-byte chunk l & 7 of rows (l >> 3) + 4 i; rows and chunks
-        // behind the end are zeros.
-        const int crow = lane >> 3, chunk = lane & 7;
-        const uint32_t step = 4 * (uint32_t)wrow;  // four rows
-        // (row & 7 of rows crow + 4 i alternates between two values)
-        const uint32_t d0 = ring + crow * 128 + ((chunk ^ crow) << 4);
-        const uint32_t d1 = ring + (crow + 4) * 128 + ((chunk ^ (crow + 4)) << 4);
-        int lpos = pos, lb = 0, lt = 0;
-        uint32_t ld = 0;
-        const uint8_t *wp = nullptr;
-        int left = 0;  // rows of the tile from crow on
-        auto aim = [&]() {
-          const int n0 = (t0 + lt) * kTile + crow;
-          left = P.N - n0;
-          wp = P.qw + (size_t)min(n0, P.N - 1) * wrow + (size_t)(b_lo + lb) * (kBlock / 2) +
-               16 * chunk;
-        };
-        if (pos < end) {
-          lt = (unsigned)pos / (unsigned)nb;
-          lb = pos - lt * nb;
-          aim();
-        }
-        auto fetch = [&]() {
-          if (lpos < end) {
-            if ((t0 + lt + 1) * kTile <= P.N && (b_lo + lb + 1) * kBlock <= P.K) {
-              cp_async16(d0 + ld, wp, 16);
-              cp_async16(d1 + ld, wp + step, 16);
-              cp_async16(d0 + ld + 1024, wp + 2 * step, 16);
-              cp_async16(d1 + ld + 1024, wp + 3 * step, 16);
-            } else {
-              const int in = (b_lo + lb) * kBlock + 32 * chunk < P.K ? 16 : 0;
+      // ---- weights: the next block of this warp's list into its ring.  Lane
+      // l copies 16-byte chunk l & 7 of rows (l >> 3) + 4 i; rows and chunks
+      // behind the end are zeros.
+      const int crow = lane >> 3, chunk = lane & 7;
+      const uint32_t step = 4 * (uint32_t)wrow;  // four rows
+      // (row & 7 of rows crow + 4 i alternates between two values)
+      const uint32_t d0 = ring + crow * 128 + ((chunk ^ crow) << 4);
+      const uint32_t d1 = ring + (crow + 4) * 128 + ((chunk ^ (crow + 4)) << 4);
+      int lpos = pos, lb = 0, lt = 0;
+      uint32_t ld = 0;
+      const uint8_t *wp = nullptr;
+      int left = 0;  // rows of the tile from crow on
+      auto aim = [&]() {
+        const int n0 = (t0 + lt) * kTile + crow;
+        left = P.N - n0;
+        wp = P.qw + (size_t)min(n0, P.N - 1) * wrow + (size_t)(b_lo + lb) * (kBlock / 2) +
+             16 * chunk;
+      };
+      if (pos < end) {
+        lt = (unsigned)pos / (unsigned)nb;
+        lb = pos - lt * nb;
+        aim();
+      }
+      auto fetch = [&]() {
+        if (lpos < end) {
+          if ((t0 + lt + 1) * kTile <= P.N && (b_lo + lb + 1) * kBlock <= P.K) {
+            cp_async16(d0 + ld, wp, 16);
+            cp_async16(d1 + ld, wp + step, 16);
+            cp_async16(d0 + ld + 1024, wp + 2 * step, 16);
+            cp_async16(d1 + ld + 1024, wp + 3 * step, 16);
+          } else {
+            const int in = (b_lo + lb) * kBlock + 32 * chunk < P.K ? 16 : 0;
 #pragma unroll 1
-              for (int i = 0; i < 4; ++i) {
-                const int bytes = 4 * i < left ? in : 0;
-                cp_async16((i & 1 ? d1 : d0) + ld + 1024 * (i >> 1), bytes ? wp + i * step : P.qw,
-                           bytes);
-              }
+            for (int i = 0; i < 4; ++i) {
+              const int bytes = 4 * i < left ? in : 0;
+              cp_async16((i & 1 ? d1 : d0) + ld + 1024 * (i >> 1), bytes ? wp + i * step : P.qw,
+                         bytes);
             }
-            if (++lb == nb) {
-              lb = 0;
-              ++lt;
-              aim();
-            } else {
-              wp += kBlock / 2;
-            }
-            ++lpos;
-            ld = ld == (kDepth - 1) * kBlockBytes ? 0 : ld + kBlockBytes;
           }
-          cp_async_commit();
-        };
-        // ---- the scales of the round's rows (contiguous), once a round
-        if (P.sc_shared && !kr) {
-          const int n0 = t0 * kTile, nrows = min(nt * kTile, P.N - n0);
-          const int bytes = nrows * groups * 2;
-          const unsigned char *src = reinterpret_cast<const unsigned char *>(P.sc + (size_t)n0 * groups);
-          const uint32_t dst = (uint32_t)__cvta_generic_to_shared(scs);
-          for (int e = tid * 16; e < bytes; e += kThreads * 16)
-            cp_async16(dst + e, src + e, min(16, bytes - e));
+          if (++lb == nb) {
+            lb = 0;
+            ++lt;
+            aim();
+          } else {
+            wp += kBlock / 2;
+          }
+          ++lpos;
+          ld = ld == (kDepth - 1) * kBlockBytes ? 0 : ld + kBlockBytes;
         }
         cp_async_commit();
+      };
+      // ---- the scales of the round's rows (contiguous), once a round
+      if (P.sc_shared && !kr) {
+        const int n0 = t0 * kTile, nrows = min(nt * kTile, P.N - n0);
+        const int bytes = nrows * groups * 2;
+        const unsigned char *src = reinterpret_cast<const unsigned char *>(P.sc + (size_t)n0 * groups);
+        const uint32_t dst = (uint32_t)__cvta_generic_to_shared(scs);
+        for (int e = tid * 16; e < bytes; e += kThreads * 16)
+          cp_async16(dst + e, src + e, min(16, bytes - e));
+      }
+      cp_async_commit();
 
-        // ---- x: this slice of the rows in the order of use; half a warp to
-        // 128 elements of a row.  The first part is read before the weights
-        // are asked for.
-        if (kr || t0 != cluster * P.round_tiles) __syncthreads();  // readers are done
-        {
-          const int p = lane & 15, halves = 2 * nb;
-          int b = 2 * warp + (lane >> 4), r = 0;
-          auto wrap = [&]() {
-            while (b >= halves && r < kRowsX) {
-              b -= halves;
-              ++r;
-            }
-          };
-          wrap();
-          struct Part {
-            float v[8];
-          };
-          auto read = [&]() {
-            Part x = {};
-            const int k = b_lo * kBlock + b * 128 + 8 * p;
-            if (r < nr && k < P.K) load8(static_cast<const T *>(P.x) + (size_t)r * P.K + k, x.v);
-            return x;
-          };
-          // (both halves run the same number of turns: shuffles inside)
-          const int turns = (nr * halves + 2 * kWarps - 1) / (2 * kWarps);
-          Part x = read();
-          for (int turn = 0; turn < turns || turn == 0; ++turn) {
-            const int cb = b, cr = r;
-            const Part c = x;
-            if (turn == 0) {
-              // The weights are asked for once the first part of x is here: a
-              // burst of weights from every SM would keep it waiting for twice
-              // the time.
-              asm volatile("" ::"f"(c.v[0]) : "memory");
-#pragma unroll
-              for (int d = 0; d < kDepth - 1; ++d) fetch();
-            }
-            b += 2 * kWarps;
-            wrap();
-            if (turn + 1 < turns) x = read();
-            unsigned char *dst = xs + cb * (kXBlock / 2) + p * 16;
-            if (kBf16) {
-              if (cr < nr) {
-                // elements (0, 4), (1, 5), (2, 6), (3, 7)
-                uint32_t o[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  o[j] = __byte_perm(__float_as_uint(c.v[j]), __float_as_uint(c.v[j + 4]), 0x7632);
-                *reinterpret_cast<uint4 *>(dst + cr * xstride) = make_uint4(o[0], o[1], o[2], o[3]);
-              }
-            } else {
-              int m = 0;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) m = max(m, __float_as_int(c.v[i]) & 0x7fffffff);
-              // (the other half warp has the other half of the same block)
-#pragma unroll
-              for (int d = 16; d; d >>= 1) m = max(m, __shfl_xor_sync(kFull, m, d));
-              // 2^e: the block's largest element into [2^14, 2^15)
-              const int ex = min(141 - (m >> 23), 126);
-              const float f = __int_as_float((ex + 127) << 23);
-              uint32_t hi[4], lo[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float x0 = c.v[i] * f, x1 = c.v[i + 4] * f;
-                const __half2 h = __floats2half2_rn(x0, x1);
-                const float2 g = __half22float2(h);
-                const __half2 l = __floats2half2_rn(x0 - g.x, x1 - g.y);
-                hi[i] = *reinterpret_cast<const uint32_t *>(&h);
-                lo[i] = *reinterpret_cast<const uint32_t *>(&l);
-              }
-              if (cr < nr) {
-                dst += 2 * cr * xstride;
-                *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4 *>(dst + xstride) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                if (lane == 0) side[(cb >> 1) * kRowsX + cr] = __int_as_float((127 - ex) << 23);
-              }
-            }
+      // ---- x: this slice of the rows in the order of use; half a warp to
+      // 128 elements of a row.  The first part is read before the weights
+      // are asked for.
+      if (kr || t0 != cluster * P.round_tiles) __syncthreads();  // readers are done
+      {
+        const int p = lane & 15, halves = 2 * nb;
+        int b = 2 * warp + (lane >> 4), r = 0;
+        auto wrap = [&]() {
+          while (b >= halves && r < kRowsX) {
+            b -= halves;
+            ++r;
           }
-        }
-        // the warps in each tile of each slice: share(w) <= i exactly for
-        // w <= (kWarps (i + 1) - 1) / total (lists shorter than the warps: one
-        // pair each, numbered by block)
-        if (!kr)
-          for (int e = tid; e < csize * nt; e += kThreads) {
-            const int q = (unsigned)e / (unsigned)nt, tile = e - q * nt;
-            int q_lo, qb;
-            slice(P, csize, q, q_lo, qb);
-            const unsigned all = nt * qb;
-            int w_lo = 0, n = qb;
-            if (all >= kWarps) {
-              w_lo = (kWarps * (tile * qb + 1) - 1) / all;
-              n = (kWarps * (tile + 1) * qb - 1) / all - w_lo + 1;
-            }
-            tab[2 * e] = (unsigned char)w_lo;
-            tab[2 * e + 1] = (unsigned char)n;
-          }
-        cp_async_wait<kDepth - 1>();  // (the scales)
-        __syncthreads();
-
-        // ---- products
-        float acc[kNT][kSums];
-#pragma unroll
-        for (int j = 0; j < kNT; ++j)
-#pragma unroll
-          for (int i = 0; i < kSums; ++i) acc[j][i] = 0.f;
-        int tile = 0, blk = 0;
-        uint32_t rd = 0;
-        if (pos < end) {
-          tile = (unsigned)pos / (unsigned)nb;
-          blk = pos - tile * nb;
-        }
-        // this lane's ldmatrix row: row lane & 7, chunk lane >> 3 (then + 4, and
-        // rows + 8)
-        const uint32_t lrow = (lane & 7) * 128;
-        const uint32_t lc0 = lrow + ((((uint32_t)lane >> 3) ^ (lane & 7)) << 4);
-        const uint32_t lc1 = lrow + (((((uint32_t)lane >> 3) + 4) ^ (lane & 7)) << 4);
-        const __half *s0p = nullptr, *s1p = nullptr;
-        auto scales_of = [&]() {  // (rows behind the last one: its scales)
-          const int n0 = t0 * kTile, last = P.N - 1 - n0;
-          const __half *sc = P.sc_shared ? scs : P.sc + (size_t)n0 * groups;
-          s0p = sc + (size_t)min(tile * kTile + gr, last) * groups;
-          s1p = sc + (size_t)min(tile * kTile + gr + 8, last) * groups;
         };
-        if (pos < end) scales_of();
-        for (; pos < end; ++pos) {
-          cp_async_wait<kDepth - 2>();
-          __syncwarp();  // every lane's copies of this block have landed
-          const uint32_t st = ring + rd;
-          rd = rd == (kDepth - 1) * kBlockBytes ? 0 : rd + kBlockBytes;
-          uint32_t w0[8], w1[8];  // rows gr, gr + 8: chunks 0..7
-          {
-            uint32_t a[4], b[4], c[4], d[4];
-            ldmatrix4(st + lc0, a);
-            ldmatrix4(st + lc1, b);
-            ldmatrix4(st + 1024 + lc0, c);
-            ldmatrix4(st + 1024 + lc1, d);
+        wrap();
+        struct Part {
+          float v[8];
+        };
+        auto read = [&]() {
+          Part x = {};
+          const int k = b_lo * kBlock + b * 128 + 8 * p;
+          if (r < nr && k < P.K) load8(static_cast<const T *>(P.x) + (size_t)r * P.K + k, x.v);
+          return x;
+        };
+        // (both halves run the same number of turns: shuffles inside)
+        const int turns = (nr * halves + 2 * kWarps - 1) / (2 * kWarps);
+        Part x = read();
+        for (int turn = 0; turn < turns || turn == 0; ++turn) {
+          const int cb = b, cr = r;
+          const Part c = x;
+          if (turn == 0) {
+            // The weights are asked for once the first part of x is here: a
+            // burst of weights from every SM would keep it waiting for twice
+            // the time.
+            asm volatile("" ::"f"(c.v[0]) : "memory");
+#pragma unroll
+            for (int d = 0; d < kDepth - 1; ++d) fetch();
+          }
+          b += 2 * kWarps;
+          wrap();
+          if (turn + 1 < turns) x = read();
+          unsigned char *dst = xs + cb * (kXBlock / 2) + p * 16;
+          if (kBf16) {
+            if (cr < nr) {
+              // elements (0, 4), (1, 5), (2, 6), (3, 7)
+              uint32_t o[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                o[j] = __byte_perm(__float_as_uint(c.v[j]), __float_as_uint(c.v[j + 4]), 0x7632);
+              *reinterpret_cast<uint4 *>(dst + cr * xstride) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+          } else {
+            int m = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max(m, __float_as_int(c.v[i]) & 0x7fffffff);
+            // (the other half warp has the other half of the same block)
+#pragma unroll
+            for (int d = 16; d; d >>= 1) m = max(m, __shfl_xor_sync(kFull, m, d));
+            // 2^e: the block's largest element into [2^14, 2^15)
+            const int ex = min(141 - (m >> 23), 126);
+            const float f = __int_as_float((ex + 127) << 23);
+            uint32_t hi[4], lo[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              w0[i] = a[i];
-              w0[i + 4] = b[i];
-              w1[i] = c[i];
-              w1[i + 4] = d[i];
+              const float x0 = c.v[i] * f, x1 = c.v[i + 4] * f;
+              const __half2 h = __floats2half2_rn(x0, x1);
+              const float2 g = __half22float2(h);
+              const __half2 l = __floats2half2_rn(x0 - g.x, x1 - g.y);
+              hi[i] = *reinterpret_cast<const uint32_t *>(&h);
+              lo[i] = *reinterpret_cast<const uint32_t *>(&l);
+            }
+            if (cr < nr) {
+              dst += 2 * cr * xstride;
+              *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              *reinterpret_cast<uint4 *>(dst + xstride) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+              if (lane == 0) side[(cb >> 1) * kRowsX + cr] = __int_as_float((127 - ex) << 23);
             }
           }
-          // (the slot that is filled now was read a turn ago, and every lane
-          // has passed the barrier above since)
-          fetch();
-          float part[kNT][4], un[kNT];
-          if (!kBf16)
-#pragma unroll
-            for (int j = 0; j < kNT; ++j) un[j] = side[blk * kRowsX + 4 * j + t];
-          const int g0 = (b_lo + blk) * kSc;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            constexpr int kSteps = kGroup / 32;
-            const int g = i / kSteps;
-            if (i % kSteps == 0) {
-#pragma unroll
-              for (int j = 0; j < kNT; ++j)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) part[j][c] = 0.f;
-            }
-            uint32_t c0[4], c1[4];
-            codes<kBf16>(w0[i], c0);
-            codes<kBf16>(w1[i], c1);
-#pragma unroll
-            for (int j = 0; j < kNT; ++j) {
-              const uint4 x4 = *reinterpret_cast<const uint4 *>(xl[j] + blk * kXBlock + i * 64);
-              mma<kBf16>(part[j], c0[0], c1[0], c0[1], c1[1], x4.x, x4.y, part[j]);
-              mma<kBf16>(part[j], c0[2], c1[2], c0[3], c1[3], x4.z, x4.w, part[j]);
-            }
-            if ((i + 1) % kSteps == 0) {
-              // (a group behind the last one counts as 0 against any scale)
-              const int gi = min(g0 + g, groups - 1);
-              const float f0 = g0 + g < groups ? __half2float(s0p[gi]) : 0.f;
-              const float f1 = g0 + g < groups ? __half2float(s1p[gi]) : 0.f;
-#pragma unroll
-              for (int j = 0; j < kNT; ++j) {
-                if (kBf16) {
-                  acc[j][0] = fmaf(f0, part[j][0], acc[j][0]);
-                  acc[j][1] = fmaf(f0, part[j][1], acc[j][1]);
-                  acc[j][2 % kSums] = fmaf(f1, part[j][2], acc[j][2 % kSums]);
-                  acc[j][3 % kSums] = fmaf(f1, part[j][3], acc[j][3 % kSums]);
-                } else {  // the hi and lo columns of one row
-                  acc[j][0] = fmaf(f0 * un[j], part[j][0] + part[j][1], acc[j][0]);
-                  acc[j][1] = fmaf(f1 * un[j], part[j][2] + part[j][3], acc[j][1]);
-                }
-              }
-            }
+        }
+      }
+      // the warps in each tile of each slice: share(w) <= i exactly for
+      // w <= (kWarps (i + 1) - 1) / total (lists shorter than the warps: one
+      // pair each, numbered by block)
+      if (!kr)
+        for (int e = tid; e < csize * nt; e += kThreads) {
+          const int q = (unsigned)e / (unsigned)nt, tile = e - q * nt;
+          int q_lo, qb;
+          slice(P, csize, q, q_lo, qb);
+          const unsigned all = nt * qb;
+          int w_lo = 0, n = qb;
+          if (all >= kWarps) {
+            w_lo = (kWarps * (tile * qb + 1) - 1) / all;
+            n = (kWarps * (tile + 1) * qb - 1) / all - w_lo + 1;
           }
-          ++blk;
-          if (blk == nb || pos + 1 == end) {
-            // partial sums of the tile, to their slot in the CTA that adds it
-            // up: [slice][tile][warp in the tile]
-            const int at = (unsigned)tile / (unsigned)csize, to = tile - at * csize;
-            const int nth = total < kWarps ? blk - 1 : warp - tab[2 * (crank * nt + tile)];
-            float *sl = slots + (size_t)((crank * own + at) * most + nth) * kTile * kRowsX +
-                        gr * kRowsX;
-            if (csize > 1) sl = cl.map_shared_rank(sl, to);
+          tab[2 * e] = (unsigned char)w_lo;
+          tab[2 * e + 1] = (unsigned char)n;
+        }
+      cp_async_wait<kDepth - 1>();  // (the scales)
+      __syncthreads();
+
+      // ---- products
+      float acc[kNT][kSums];
+#pragma unroll
+      for (int j = 0; j < kNT; ++j)
+#pragma unroll
+        for (int i = 0; i < kSums; ++i) acc[j][i] = 0.f;
+      int tile = 0, blk = 0;
+      uint32_t rd = 0;
+      if (pos < end) {
+        tile = (unsigned)pos / (unsigned)nb;
+        blk = pos - tile * nb;
+      }
+      // this lane's ldmatrix row: row lane & 7, chunk lane >> 3 (then + 4, and
+      // rows + 8)
+      const uint32_t lrow = (lane & 7) * 128;
+      const uint32_t lc0 = lrow + ((((uint32_t)lane >> 3) ^ (lane & 7)) << 4);
+      const uint32_t lc1 = lrow + (((((uint32_t)lane >> 3) + 4) ^ (lane & 7)) << 4);
+      const __half *s0p = nullptr, *s1p = nullptr;
+      auto scales_of = [&]() {  // (rows behind the last one: its scales)
+        const int n0 = t0 * kTile, last = P.N - 1 - n0;
+        const __half *sc = P.sc_shared ? scs : P.sc + (size_t)n0 * groups;
+        s0p = sc + (size_t)min(tile * kTile + gr, last) * groups;
+        s1p = sc + (size_t)min(tile * kTile + gr + 8, last) * groups;
+      };
+      if (pos < end) scales_of();
+      for (; pos < end; ++pos) {
+        cp_async_wait<kDepth - 2>();
+        __syncwarp();  // every lane's copies of this block have landed
+        const uint32_t st = ring + rd;
+        rd = rd == (kDepth - 1) * kBlockBytes ? 0 : rd + kBlockBytes;
+        uint32_t w0[8], w1[8];  // rows gr, gr + 8: chunks 0..7
+        {
+          uint32_t a[4], b[4], c[4], d[4];
+          ldmatrix4(st + lc0, a);
+          ldmatrix4(st + lc1, b);
+          ldmatrix4(st + 1024 + lc0, c);
+          ldmatrix4(st + 1024 + lc1, d);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            w0[i] = a[i];
+            w0[i + 4] = b[i];
+            w1[i] = c[i];
+            w1[i + 4] = d[i];
+          }
+        }
+        // (the slot that is filled now was read a turn ago, and every lane
+        // has passed the barrier above since)
+        fetch();
+        float part[kNT][4], un[kNT];
+        if (!kBf16)
+#pragma unroll
+          for (int j = 0; j < kNT; ++j) un[j] = side[blk * kRowsX + 4 * j + t];
+        const int g0 = (b_lo + blk) * kSc;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          constexpr int kSteps = kGroup / 32;
+          const int g = i / kSteps;
+          if (i % kSteps == 0) {
 #pragma unroll
             for (int j = 0; j < kNT; ++j)
 #pragma unroll
-              for (int i = 0; i < kSums; ++i) {
-                // bf16: rows gr, gr + 8 and columns 2 t, 2 t + 1; fp32: the two
-                // rows of x row t
-                const int row = 8 * (kBf16 ? i >> 1 : i);
-                const int col = kBf16 ? 8 * j + 2 * t + (i & 1) : 4 * j + t;
-                if (col < nr) {
-                  float v = acc[j][i];
-                  if (kr) v += sl[row * kRowsX + col];
-                  sl[row * kRowsX + col] = v;
-                }
-                acc[j][i] = 0.f;
+              for (int c = 0; c < 4; ++c) part[j][c] = 0.f;
+          }
+          uint32_t c0[4], c1[4];
+          codes<kBf16>(w0[i], c0);
+          codes<kBf16>(w1[i], c1);
+#pragma unroll
+          for (int j = 0; j < kNT; ++j) {
+            const uint4 x4 = *reinterpret_cast<const uint4 *>(xl[j] + blk * kXBlock + i * 64);
+            mma<kBf16>(part[j], c0[0], c1[0], c0[1], c1[1], x4.x, x4.y, part[j]);
+            mma<kBf16>(part[j], c0[2], c1[2], c0[3], c1[3], x4.z, x4.w, part[j]);
+          }
+          if ((i + 1) % kSteps == 0) {
+            // (a group behind the last one counts as 0 against any scale)
+            const int gi = min(g0 + g, groups - 1);
+            const float f0 = g0 + g < groups ? __half2float(s0p[gi]) : 0.f;
+            const float f1 = g0 + g < groups ? __half2float(s1p[gi]) : 0.f;
+#pragma unroll
+            for (int j = 0; j < kNT; ++j) {
+              if (kBf16) {
+                acc[j][0] = fmaf(f0, part[j][0], acc[j][0]);
+                acc[j][1] = fmaf(f0, part[j][1], acc[j][1]);
+                acc[j][2 % kSums] = fmaf(f1, part[j][2], acc[j][2 % kSums]);
+                acc[j][3 % kSums] = fmaf(f1, part[j][3], acc[j][3 % kSums]);
+              } else {  // the hi and lo columns of one row
+                acc[j][0] = fmaf(f0 * un[j], part[j][0] + part[j][1], acc[j][0]);
+                acc[j][1] = fmaf(f1 * un[j], part[j][2] + part[j][3], acc[j][1]);
               }
-            blk = 0;
-            ++tile;
-            if (pos + 1 < end) scales_of();
+            }
           }
         }
-        cp_async_wait<0>();
-      }
-
-      // ---- the sum over slices and warps, tiles crank, crank + csize, ...
-      if (csize > 1)
-        cl.sync();
-      else
-        __syncthreads();
-      for (int e = tid; e < own * kTile * nr; e += kThreads) {
-        const int r = (unsigned)e / (unsigned)(own * kTile), c = e - r * own * kTile;
-        const int at = c / kTile, tile = at * csize + crank, n = (t0 + tile) * kTile + c % kTile;
-        if (tile >= nt || n >= P.N) continue;
-        float sum = 0.f;
-        for (int q = 0; q < csize; ++q) {
-          const float *sl = slots + ((size_t)((q * own + at) * most) * kTile + c % kTile) * kRowsX + r;
-          const int cnt = tab[2 * (q * nt + tile) + 1];
-          for (int w = 0; w < cnt; ++w, sl += kTile * kRowsX) sum += *sl;
+        ++blk;
+        if (blk == nb || pos + 1 == end) {
+          // partial sums of the tile, to their slot in the CTA that adds it
+          // up: [slice][tile][warp in the tile]
+          const int at = (unsigned)tile / (unsigned)csize, to = tile - at * csize;
+          const int nth = total < kWarps ? blk - 1 : warp - tab[2 * (crank * nt + tile)];
+          float *sl = slots + (size_t)((crank * own + at) * most + nth) * kTile * kRowsX +
+                      gr * kRowsX;
+          if (csize > 1) sl = cl.map_shared_rank(sl, to);
+#pragma unroll
+          for (int j = 0; j < kNT; ++j)
+#pragma unroll
+            for (int i = 0; i < kSums; ++i) {
+              // bf16: rows gr, gr + 8 and columns 2 t, 2 t + 1; fp32: the two
+              // rows of x row t
+              const int row = 8 * (kBf16 ? i >> 1 : i);
+              const int col = kBf16 ? 8 * j + 2 * t + (i & 1) : 4 * j + t;
+              if (col < nr) {
+                float v = acc[j][i];
+                if (kr) v += sl[row * kRowsX + col];
+                sl[row * kRowsX + col] = v;
+              }
+              acc[j][i] = 0.f;
+            }
+          blk = 0;
+          ++tile;
+          if (pos + 1 < end) scales_of();
         }
-        const size_t out = (size_t)r * P.N + n;
-        if (kBf16)
-          static_cast<__nv_bfloat16 *>(P.y)[out] = __float2bfloat16_rn(sum);
-        else
-          static_cast<float *>(P.y)[out] = sum;
       }
-      // the slots are read
-      if (csize > 1 && t0 + clusters * P.round_tiles < P.tiles) cl.sync();
+      cp_async_wait<0>();
     }
+
+    // ---- the sum over slices and warps, tiles crank, crank + csize, ...
+    if (csize > 1)
+      cl.sync();
+    else
+      __syncthreads();
+    for (int e = tid; e < own * kTile * nr; e += kThreads) {
+      const int r = (unsigned)e / (unsigned)(own * kTile), c = e - r * own * kTile;
+      const int at = c / kTile, tile = at * csize + crank, n = (t0 + tile) * kTile + c % kTile;
+      if (tile >= nt || n >= P.N) continue;
+      float sum = 0.f;
+      for (int q = 0; q < csize; ++q) {
+        const float *sl = slots + ((size_t)((q * own + at) * most) * kTile + c % kTile) * kRowsX + r;
+        const int cnt = tab[2 * (q * nt + tile) + 1];
+        for (int w = 0; w < cnt; ++w, sl += kTile * kRowsX) sum += *sl;
+      }
+      const size_t out = (size_t)r * P.N + n;
+      if (kBf16)
+        static_cast<__nv_bfloat16 *>(P.y)[out] = __float2bfloat16_rn(sum);
+      else
+        static_cast<float *>(P.y)[out] = sum;
+    }
+    // the slots are read
+    if (csize > 1 && t0 + clusters * P.round_tiles < P.tiles) cl.sync();
   }
 }
 
