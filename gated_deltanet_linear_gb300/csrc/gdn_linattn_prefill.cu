@@ -60,13 +60,13 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cudaTypedefs.h>
 
-#include <mutex>
 #include <type_traits>
 
 #include "gdn_internal.cuh"
 #include "gdn_tc.cuh"
+#include "gdn_tma.cuh"
+#include "gdn_vec.cuh"
 
 namespace gdn {
 
@@ -226,29 +226,6 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ Two shfl_up2(Two x, int d) {
   return Two{__shfl_up_sync(0xffffffffu, x.h, d), __shfl_up_sync(0xffffffffu, x.l, d)};
-}
-
-// Two floats in a register pair, and the packed operations on them.
-typedef unsigned long long F2;
-__device__ __forceinline__ F2 pack(float x, float y) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ float2 unpack(F2 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
 }
 
 // x - h, exactly
@@ -1274,20 +1251,6 @@ int plan(int B, int vh, int T) {
     if (heads * s >= 4LL * kSms) break;
   }
   return best;
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                         cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
 }
 
 // [B][T][heads][128] rows as a 4-d tensor {128, heads, T, B}; a box is 64

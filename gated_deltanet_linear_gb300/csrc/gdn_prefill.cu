@@ -53,12 +53,11 @@
 // fp32.
 
 #include <cuda_bf16.h>
-#include <cudaTypedefs.h>
 
-#include <mutex>
 
 #include "gdn_internal.cuh"
 #include "gdn_tc.cuh"
+#include "gdn_tma.cuh"
 
 namespace gdn {
 
@@ -1037,22 +1036,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 size_t prefill_workspace_bytes(int, int, int, int, int, int) { return 0; }
 
 namespace {
-
-// cuTensorMapEncodeTiled, from the driver through the runtime (the library
-// does not link the driver library itself); null if it is unavailable.
-PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                         cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
 
 // Tensor map over a [B][T][heads][128] fp32 array (q, k, v or o) as a 4-d
 // tensor {128, heads, T, B}; one box is `rows` token rows of one head of one

@@ -27,7 +27,6 @@
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cudaTypedefs.h>
 
 #include <array>
 #include <map>
@@ -36,6 +35,7 @@
 
 #include "gdn_internal.cuh"
 #include "gdn_tc.cuh"
+#include "gdn_tma.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -423,20 +423,6 @@ cudaError_t cluster_counts(std::array<int, 8> &most) {
   }
   most = it->second;
   return cudaSuccess;
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                         cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
 }
 
 // rows x cols elements, boxes of box_rows x box_cols; zeros outside.
