@@ -22,22 +22,26 @@
 // bf16 rows q, k and v fit one fp16 each; the scores, the state and the decayed
 // values are hi + lo as with fp32 rows, so o is rounded once (with single fp16
 // scores and states it was 9e-4 in norm from the rounded fp32 result, now 3e-5;
-// 8 prompts of 4096 tokens took 528 us, now 588).  The scales: q and k by
-// row, v, the decayed values and the state by column dv (the TMEM lane),
-// chosen so that the largest element lies in [2^14, 2^15); elements down to 2^-17
-// of it keep all their bits.  (The decayed values take the values' scale where
-// their largest is within that range all the same, by the factors and the last
-// 8 rows.  Always their own took 655 us where this takes 607, bf16.)  The scores of row t are scaled by a bound of the largest
-// |q_t| |k_s| e^{Gamma_t - Gamma_s}, s <= t, so strong decays and rows of very
-// different sizes leave them their bits.  The state is kept in fp32 registers: a chunk's KV
+// 8 prompts of 4096 tokens took 528 us, and 588 with the second parts).
+// The scales: q and k by row, v, the decayed values and the state by column dv
+// (the TMEM lane), chosen so that the largest element lies in [2^14, 2^15);
+// elements down to 2^-17 of it keep all their bits.  The scores of row t are
+// scaled by a bound of the largest |q_t| |k_s| e^{Gamma_t - Gamma_s}, s <= t, over
+// the rows that are not zeros, so strong decays and rows of very different
+// sizes leave them their bits.  The decayed values' factors are bounded by the
+// largest of such rows; their columns take the values' scale where their
+// largest is within 2^-17 of it all the same (told by the factors and the
+// last 8 rows), else one of their own.  (Always their own took 655 us where
+// this takes 610, bf16.)  The state is kept in fp32 registers: a chunk's KV
 // product is read out, unscaled and added, so scales may differ from chunk to
-// chunk.  Gamma is summed as two floats (48 bits), so strong decays
-// keep the small differences between near tokens.
+// chunk.  Gamma is summed as two floats (48 bits), so strong decays keep the
+// small differences between near tokens.
 //
 // Roles (20 warps, one CTA per SM, persistent over (sequence, head, segment)
 // units): 8 warps A hold the state and make its operand and the two V
-// operands (the next chunk's V maxima under this one's KV product); 8 warps B turn the staged q and k rows into operands in place,
-// make P from G, and the output from QS and PV; one warp issues the products,
+// operands (the next chunk's V maxima under this one's KV product); 8 warps B
+// turn the staged q and k rows into operands in place, make P from G, and the
+// output from QS and PV; one warp issues the products,
 // one copies rows by TMA (a chunk ahead), two compute the decay vectors.
 // All meet through mbarriers; the chunks of successive units form one
 // sequence, so a unit's first loads run under the previous one's last chunk.
@@ -47,16 +51,17 @@
 // (KV only), a second kernel chains them into every segment's start state, and
 // the main pass runs over all segments at once.
 //
-// Measured (8 prompts of 4096 tokens, 16 / 48 heads): fp32 669 us (2.20 GB,
-// 49 % of the copy rate), bf16 588 us (1.13 GB, 29 %); 33 prompts of up to 111
-// tokens, fp32, 90 us; one of 32701 tokens, 2 / 8 heads, bf16, 137 us.  Bound by
-// the latency of each chunk's chain (rows - decay vectors - V operands - KV -
-// state, and scores - P - PV - output) on 4 to 5 warps a scheduler: they issue
-// in 58 % of the cycles, the tensor cores are busy in 35 %, DRAM 40 %.  The
-// code of all roles together is more than the instruction cache bears (14 % of
-// its requests miss): more unrolling, or warps for more roles, cost more than
-// they hid (24 and 32 warps with packed arithmetic 9000 cycles a chunk where 20
-// took 7000; the score loop unrolled +12 %), 1.4 KB less of it gave 5 %.
+// Measured (8 prompts of 4096 tokens, 16 / 48 heads): fp32 690 us (2.20 GB,
+// 48 % of the copy rate), bf16 610 us (1.13 GB, 28 %); 33 prompts of up to 111
+// tokens, fp32 92 us, bf16 85; one of 32701 tokens, 2 / 8 heads, bf16 140 us, fp32
+// 158.  Bound by the latency of each chunk's chain (rows - decay vectors - V
+// operands - KV - state, and scores - P - PV - output) on 4 to 5 warps a
+// scheduler: fp32 issues in 56 % of the cycles, the tensor cores are busy in
+// 34 %, DRAM 38 %; bf16 61, 21 and 21 %.  The code of all roles together is more
+// than the instruction cache bears (15 % of its requests miss): more unrolling,
+// or warps for more roles, cost more than they hid (24 and 32 warps with packed
+// arithmetic 9000 cycles a chunk where 20 took 7000; the score loop unrolled
+// +12 %), 1.4 KB less of it gave 5 %.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

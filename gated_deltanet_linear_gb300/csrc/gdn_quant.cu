@@ -34,9 +34,10 @@
 // adds up the tile; slots are added in a fixed order, so results are the same
 // bits on every call.
 //
-// One row against 10240 x 5120: 11.1 us (27 MB from L2 and HBM; 2.4 TB/s), 8
-// rows of fp32 14.9, of bf16 14.7, 16 rows of bf16 19.0; 48 x 5120 (a layer's
-// gates) 4.6 us.  What is left is a start of 2 us, the x that every CTA converts,
+// One row against 10240 x 5120, weights from HBM (15 of them in turn, calls back
+// to back): 11.5 us (27 MB, 2.4 TB/s), 8 rows of fp32 15.6, of bf16 14.9, 16 rows of
+// bf16 19.0; a single call behind a flushed L2 14.6 (one row), 18.7 (8 of fp32).
+// 48 x 5120 (a layer's gates) 4.9 us.  What is left is a start of 2 us, the x that every CTA converts,
 // the products' issue (the SIMD lanes unpack 8 codes in 14 instructions) and for
 // clusters two barriers.
 
@@ -689,7 +690,7 @@ cudaError_t launch_quant_linear(const void *x, const unsigned char *qw,
                                 cudaStream_t stream) {
   if (rows == 0 || N == 0) return cudaSuccess;
   // More than 16 columns go to products of 128 weight rows: 64 rows of bf16
-  // against 5120 x 6144 took 54 us here, 32 columns at a time, and take 18.6
+  // against 5120 x 6144 took 54 us here, 32 columns at a time, and take 18.9
   // there; 16 rows take 14 us here (17 there).
   if ((bf16 ? rows : 2 * rows) > 16)
     return launch_quant_linear_wide(x, qw, scales, y, rows, N, K, group, bf16, stream);

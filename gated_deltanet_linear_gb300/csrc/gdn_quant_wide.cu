@@ -21,8 +21,9 @@
 // Bound by the chain of a stage (sums 450 cycles, unpacking 700, with 12 of its 16
 // operations for 8 codes on the half-rate integer pipe, one barrier; 1500 in
 // all), then by start and exchange (6000 cycles a call).  64 rows of 5120 x 6144:
-// bf16 18.6 us (A through shared memory 19.3), fp32 28.5 (35.4); mma.sync with 16
-// rows of x at a time took 54 us.
+// bf16 18.9 us (A through shared memory 19.3), fp32 28.7 (35.4); mma.sync with 16
+// rows of x at a time took 54 us.  More rows go through the weights again for every
+// 64: 512 rows 138 us (fp32 219), 4096 rows 1090 (1740).
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>

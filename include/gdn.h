@@ -405,7 +405,8 @@ enum {
  *     S = exp(g) S + k v^T;   o = scale * S^T q      (with the updated S).
  * The recurrence of gdn_step without its correction (no beta), on the same
  * states and head layout, so gdn_mark, gdn_rollback and gdn_rollback_seq
- * serve these states too, and gdn_gated_rmsnorm_m takes its fp32 o.
+ * serve these states too, and gdn_gated_rmsnorm_m takes its fp32 o (a bf16 o
+ * has to be cast first).
  *   dtype  GDN_F32 or GDN_BF16: the type of q, k, v and o (GDN_EINVAL
  *          otherwise).  S and g are fp32; every product and sum is fp32, and
  *          a bf16 o is rounded once.
@@ -458,15 +459,24 @@ size_t gdn_linattn_prefill_workspace(const gdn_shape *shape, int T, int dtype);
  *          may overlap on the GPU need one each.
  * 1 <= T <= GDN_MAX_TOKENS and T * vh < 2^31 (GDN_ERANGE otherwise).
  * Numbers: chunks of 64 tokens on tensor cores.  Operands are the sum of two
- * fp16 numbers (22 bits) scaled by rows or columns, bf16 rows a single fp16
- * (exact); the state is kept in fp32, every sum is fp32: about 3e-7 relative
- * error of an fp32 o and 2e-7 of S, where a step's is 1e-7.  A bf16 o is
- * rounded once.  Weights e^{sum of g}
- * below 2^-126 may count as 0, and within 64 tokens e^{sum of g} may grow by up
- * to a factor of 2^80.  An o that is finite is met for |v|, |S| up to 2^118 and
- * products |q_i| |k_j| of elements (times that growth) up to 2^115; beyond that
- * it may become infinite or NaN.  The same call gives the same bits; another B or T may cut
- * the sequences elsewhere and differ in the last ones.
+ * fp16 numbers (22 bits) scaled by rows (q, k, scores) or columns (v, state),
+ * bf16 rows of q, k and v a single fp16; the state is kept in fp32, every sum
+ * is fp32: about 3e-7 relative error of an fp32 o and 2e-7 of S, where a step's
+ * is 1e-7.  A bf16 o is rounded once.  The second part of an operand ends 39
+ * bits below the largest element of its row or column (v: of the 64 tokens of
+ * its chunk), so what is smaller than 2^-17 of that keeps fewer bits: o_t may be
+ * off by 2^-29 (largest |q_t|) (largest |k_s| e^{g_{s+1} + .. + g_t}, s <= t) times
+ * 64 (largest |v| of the column).  That shows in an o for which only small
+ * weights or values are left, where the rows near t have v = 0 or a later v is
+ * 2^17 times larger.  S keeps its 2e-7 by columns there too: its values are
+ * scaled by what the decays leave of them.
+ * Weights e^{sum of g} (times the size of their k row against the largest of the
+ * chunk) below 2^-126 may count as 0, and within 64 tokens e^{sum of g} may grow
+ * by up to a factor of 2^80.  An o that is finite is met for |v|, |S| up to
+ * 2^118 and products |q_i| |k_j| of elements (times that growth) up to 2^115;
+ * beyond that it may become infinite or NaN.  The same call gives the same
+ * bits; another B or T may cut the sequences elsewhere and differ in the last
+ * ones.
  * What is not finite stays with its heads and never reaches a token before
  * its own: in q it makes its row of o not finite, in v its column from its
  * token on, in k or g (other than g = -inf, which empties the state) the
@@ -496,8 +506,11 @@ int gdn_linattn_prefill(const gdn_shape *shape, int T, int dtype, int decay,
  *   group   32, 64 or 128; K a positive multiple of it (GDN_ESHAPE otherwise)
  * N, K <= GDN_QUANT_MAX_DIM, rows <= GDN_MAX_TOKENS (GDN_ERANGE otherwise);
  * rows == 0 or N == 0 is a no-op.  Sums are fp32; results are the same bits
- * on every call.  A group's sum of x code is made before its scale is applied:
- * it stays finite for |x| up to 2^112.  A row of x with an element that is not
+ * on every call.  Codes, scales and bf16 x enter as they are, fp32 x in up to 8
+ * rows as the sum of two fp16 numbers (22 bits, scaled by the largest element of
+ * 256; elements below 2^-17 of it keep fewer, down to 2^-39 of it), in more rows
+ * whole.  A group's sum of x code is made before its scale is applied: it stays
+ * finite for |x| up to 2^112.  A row of x with an element that is not
  * finite gives results that are not finite (NaN also where the formula has an
  * infinity), in its own row of y alone.
  */
