@@ -171,3 +171,42 @@ def test_fp32_prompts_keep_fp32(slow, B, kh, vh, T):
     assert float(off.max()) <= 2.0 ** -19
     off = (S - ref["S"]).norm(dim=(2, 3)) / ref["S"].norm(dim=(2, 3))
     assert float(off.max()) <= 2.0 ** -19
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T", [64, 150, 700])
+@pytest.mark.parametrize("rate", [0.1, 0.86])
+def test_growth_within_a_chunk(dtype, T, rate):
+    """Factors above 1: up to e^(64 * 0.86), about 2^79, over a chunk's tokens and
+    back in the next."""
+    d = make_linattn(17, 1, T, 1, 2, TYPES[dtype])
+    up = (torch.arange(T, device="cuda") // 64) % 2 == 0
+    d["g"][:] = torch.where(up, rate, -rate)[None, :, None]
+    S, o = prompt(d)
+    under, score = floors(d)
+    # (a score's error goes with its weight, up to 2^79 here)
+    check_prompt(d, S, o, floor_S=under * 2.0 ** 79, floor_o=(under + score) * 2.0 ** 79)
+    ref = linattn(d["S"], d["q"], d["k"], d["v"], d["g"])
+    assert (S - ref["S"]).norm() <= 2.0 ** -19 * ref["S"].norm()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T", [111, 900])
+def test_lengths_under_strong_decay(dtype, T):
+    """Slopes of 1/2 and less a token over padded prompts that end anywhere in a
+    chunk: the rows behind the end neither count nor scale."""
+    ends = [1, 7, 56, 63, 64, 65, 100, T - 3, T]
+    d = make_linattn(19, len(ends), T, 1, 2, TYPES[dtype], "head")
+    d["g"] = torch.tensor([-0.5, -2.0], device="cuda")
+    lens = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    for b, n in enumerate(ends):
+        for x, bad in (("q", float("nan")), ("k", 1e30), ("v", float("inf"))):
+            d[x][b, n:] = bad
+    S, o = d["S"].clone(), torch.full_like(d["v"], 7.5)
+    run("prefill", S, d, o, lens=lens)
+    on = torch.arange(T, device="cuda") < lens[:, None]
+    assert (o[~on] == 7.5).all()
+    clean = {x: t if x in "Sg" else torch.where(on[..., None, None], t, torch.zeros_like(t))
+             for x, t in d.items()}
+    under, score = floors(clean)
+    check_prompt(d, S, o, lens=lens.long(), floor_S=under, floor_o=under + score)
