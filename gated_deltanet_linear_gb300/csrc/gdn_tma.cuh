@@ -1,4 +1,4 @@
-// The driver's encoder of tensor maps.
+// The encoder of tensor maps.
 #pragma once
 
 #include <cudaTypedefs.h>
