@@ -243,7 +243,7 @@ def prepare(case, seed):
             d["rope"] = gdn.Rope(d["freq"], gdn.GDN_ROPE_HALF if d["layout"] == "half"
                                  else gdn.GDN_ROPE_PAIRS, d["amp"])
         if case["op"] == "attn":
-            n = gdn.gdn_attn_workspace(d["cache"], case["B"], case["M"], case["qh"], dtype=d["q"].dtype)
+            n = gdn.gdn_attn_workspace(d["cache"], case["M"], case["qh"])
             d["workspace"] = torch.empty(n, dtype=torch.uint8, device="cuda")
     return d
 
