@@ -32,7 +32,8 @@ __all__ = [
     "gdn_layer_step_m_noalloc", "GDN_NOALLOC_SCRATCH_BYTES",
     "gdn_gated_rmsnorm_m", "gdn_linattn_step", "gdn_linattn_step_m",
     "gdn_linattn_prefill_workspace", "gdn_linattn_prefill",
-    "gdn_quant_linear",
+    "gdn_quant_linear", "KVCache", "Rope", "gdn_rope_freqs", "gdn_rope_m",
+    "gdn_kv_write_m", "gdn_kv_read", "gdn_attn_workspace", "gdn_attn_step_m",
 ]
 
 GDN_OK, GDN_EINVAL, GDN_ESHAPE, GDN_EALIGN = 0, -1, -2, -3
@@ -44,6 +45,13 @@ GDN_NOALLOC_SCRATCH_BYTES = 16 << 20
 GDN_F32, GDN_BF16 = 0, 1
 GDN_DECAY_TOKEN, GDN_DECAY_HEAD = 0, 1
 GDN_QUANT_MAX_DIM = 1 << 20
+GDN_KV_BF16, GDN_KV_INT8, GDN_KV_E4M3 = 0, 1, 2
+GDN_KV_MAX_HEADS, GDN_KV_MAX_POSITIONS = 4096, 1 << 30
+GDN_ATTN_MAX_TOKENS = 64
+GDN_ROPE_HALF, GDN_ROPE_PAIRS = 0, 1
+GDN_ROPE_PLAIN, GDN_ROPE_LINEAR, GDN_ROPE_NTK, GDN_ROPE_BAND = 0, 1, 2, 3
+_KINDS = {torch.bfloat16: GDN_KV_BF16, torch.int8: GDN_KV_INT8,
+          torch.float8_e4m3fn: GDN_KV_E4M3}
 _DTYPES = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16}
 
 # Every symbol include/gdn.h declares.
@@ -54,7 +62,9 @@ EXPORTS = ("gdn_step", "gdn_step_m", "gdn_mark", "gdn_rollback",
            "gdn_layer_hist_rollback", "gdn_gated_rmsnorm_m",
            "gdn_layer_step_m_noalloc", "gdn_linattn_step",
            "gdn_linattn_step_m", "gdn_linattn_prefill_workspace",
-           "gdn_linattn_prefill", "gdn_quant_linear", "gdn_strerror",
+           "gdn_linattn_prefill", "gdn_quant_linear", "gdn_rope_freqs",
+           "gdn_rope_m", "gdn_kv_write_m", "gdn_kv_read",
+           "gdn_attn_workspace", "gdn_attn_step_m", "gdn_strerror",
            "gdn_version")
 
 
@@ -68,6 +78,16 @@ class Shape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("kh", ctypes.c_int),
                 ("vh", ctypes.c_int), ("kd", ctypes.c_int),
                 ("vd", ctypes.c_int)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [(x, ctypes.c_void_p) for x in ("k", "v", "k_scale", "v_scale")] + \
+        [(x, ctypes.c_int) for x in ("kind", "pages", "kvh", "page", "hd")]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("freq", ctypes.c_void_p), ("rot", ctypes.c_int),
+                ("layout", ctypes.c_int), ("amp", ctypes.c_float)]
 
 
 _lib = None
@@ -127,6 +147,23 @@ def load():
     lib.gdn_linattn_prefill.restype = ctypes.c_int
     lib.gdn_quant_linear.argtypes = [ip] * 5 + [vp] * 5
     lib.gdn_quant_linear.restype = ctypes.c_int
+    dp, kv = ctypes.c_double, ctypes.POINTER(_Cache)
+    rp, ll = ctypes.POINTER(_Rope), ctypes.c_longlong
+    lib.gdn_rope_freqs.argtypes = [ip, dp, ip, dp, dp, dp, dp,
+                                   ctypes.POINTER(ctypes.c_double), ctypes.POINTER(fp)]
+    lib.gdn_rope_freqs.restype = ctypes.c_int
+    lib.gdn_rope_m.argtypes = [ip, ip, ip, ip, rp, vp, ll, vp, vp, vp]
+    lib.gdn_rope_m.restype = ctypes.c_int
+    lib.gdn_kv_write_m.argtypes = [kv, ip, ip, ip, ip, rp, vp, ll, vp, ll, vp,
+                                   ll, vp, vp, ip, vp, vp, vp, vp]
+    lib.gdn_kv_write_m.restype = ctypes.c_int
+    lib.gdn_kv_read.argtypes = [kv, ip, ip, ip, vp, ip, vp, vp, vp, vp, vp, vp]
+    lib.gdn_kv_read.restype = ctypes.c_int
+    lib.gdn_attn_workspace.argtypes = [kv, ip, ip]
+    lib.gdn_attn_workspace.restype = sz
+    lib.gdn_attn_step_m.argtypes = [kv, ip, ip, ip, ip, fp, vp, vp, ip, vp, vp,
+                                    vp, vp, vp, vp, sz, vp]
+    lib.gdn_attn_step_m.restype = ctypes.c_int
     lib.gdn_prefill_timeouts.argtypes = [ctypes.POINTER(ctypes.c_uint)]
     lib.gdn_prefill_timeouts.restype = ctypes.c_int
     lib.gdn_wait_timeouts.argtypes = [ctypes.POINTER(ctypes.c_uint)]
@@ -573,3 +610,195 @@ def gdn_quant_linear(x, qw, scales, y, stream=None):
         _tok(y, "y", (rows, N), dtype), _stream(stream))
     if r:
         raise GDNError(r, "gdn_quant_linear")
+
+
+class KVCache:
+    """A paged key-value cache: k, v [pages][kvh][page][hd] bfloat16, int8 or
+    float8_e4m3fn; the 8-bit types with k_scale, v_scale float32
+    [pages][kvh][page].  It refers to the tensors, which stay the caller's."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "kind", "shape", "c")
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise ValueError("k must be [pages][kvh][page][hd]")
+        self.kind = _KINDS.get(k.dtype)
+        if self.kind is None:
+            raise ValueError("k and v must be bfloat16, int8 or float8_e4m3fn")
+        if (self.kind == GDN_KV_BF16) != (k_scale is None) or \
+                (self.kind == GDN_KV_BF16) != (v_scale is None):
+            raise ValueError("8-bit caches have scales, bfloat16 caches none")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.shape = pages, kvh, page, hd = tuple(k.shape)
+        ptrs = [_tok(k, "k", k.shape, k.dtype), _tok(v, "v", k.shape, k.dtype), None, None]
+        if k_scale is not None:
+            ptrs[2] = _tok(k_scale, "k_scale", k.shape[:3], torch.float32)
+            ptrs[3] = _tok(v_scale, "v_scale", k.shape[:3], torch.float32)
+        self.c = _Cache(*ptrs, self.kind, pages, kvh, page, hd)
+
+
+class Rope:
+    """Rotary positions: freq float64 [rot / 2] radians a position (CUDA), the
+    layout of the pairs, the amplitude (see gdn_rope_freqs)."""
+
+    __slots__ = ("freq", "rot", "layout", "amp", "c")
+
+    def __init__(self, freq, layout=GDN_ROPE_HALF, amp=1.0):
+        if not isinstance(freq, torch.Tensor) or freq.dim() != 1:
+            raise ValueError("freq must be [rot / 2]")
+        ptr = _tok(freq, "freq", freq.shape, torch.float64)
+        self.freq, self.rot, self.layout, self.amp = freq, 2 * freq.numel(), layout, amp
+        self.c = _Rope(ptr, self.rot, layout, amp)
+
+
+def gdn_rope_freqs(rot, base=10000.0, scaling=GDN_ROPE_PLAIN, factor=1.0,
+                   context=0.0, low=1.0, high=32.0, device="cuda"):
+    """(freq, amp) for Rope: float64 [rot / 2] on the device, computed on the
+    host, and the amplitude."""
+    freq = torch.empty(max(0, int(rot) // 2), dtype=torch.float64)
+    amp = ctypes.c_float(1.0)
+    r = (_lib or load()).gdn_rope_freqs(
+        rot, base, scaling, factor, context, low, high,
+        ctypes.cast(freq.data_ptr(), ctypes.POINTER(ctypes.c_double)), ctypes.byref(amp))
+    if r:
+        raise GDNError(r, "gdn_rope_freqs")
+    return freq.to(device), amp.value
+
+
+def _rows(x, name, lead, dtype):
+    """Pointer and stride from token to token of x [*lead][heads][hd]: heads
+    and channels contiguous, tokens evenly spaced (the rows of a projection)."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    shape, st = x.shape, x.stride()
+    if not x.is_cuda or x.dtype is not dtype or len(shape) != len(lead) + 2 or \
+            tuple(shape[:-2]) != tuple(lead):
+        raise ValueError(f"{name} must be a {dtype} CUDA tensor {list(lead)}[heads][hd]")
+    width = shape[-2] * shape[-1]
+    if x.numel() and (st[-1] != 1 or (st[-2] != shape[-1] and shape[-2] > 1)):
+        raise ValueError(f"{name}: heads and channels must be contiguous")
+    step = width
+    if len(lead) == 2:
+        B, M = lead
+        if M > 1:
+            step = st[1]
+            if B > 1 and st[0] != M * st[1]:
+                raise ValueError(f"{name}: tokens must be evenly spaced")
+        elif B > 1:
+            step = st[0]
+    elif lead[0] > 1:
+        step = st[0]
+    return x.data_ptr(), step
+
+
+def _code(dtype):
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError("tokens must be float32 or bfloat16")
+    return code
+
+
+def _ints(x, name, shape):
+    return None if x is None else _tok(x, name, shape, torch.int32)
+
+
+def gdn_rope_m(x, pos, rope, y, stream=None):
+    """y = x turned to positions pos: x, y [rows][heads][hd] float32 or
+    bfloat16 (x may have a stride from row to row; y may be x), pos int32
+    [rows]."""
+    if x.dim() != 3:
+        raise ValueError("x must be [rows][heads][hd]")
+    rows, heads, hd = x.shape
+    ptr, step = _rows(x, "x", (rows,), x.dtype)
+    r = (_lib or load()).gdn_rope_m(
+        rows, heads, hd, _code(x.dtype), ctypes.byref(rope.c), ptr, step,
+        _ints(pos, "pos", (rows,)), _tok(y, "y", x.shape, x.dtype), _stream(stream))
+    if r:
+        raise GDNError(r, "gdn_rope_m")
+
+
+def _paged(cache, B, table, start, counts, err_dev):
+    """Pointers of table, start, counts, err_dev and the table's columns."""
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("table must be [B][columns]")
+    cols = table.shape[1]
+    return (_ints(table, "table", (B, cols)), cols, _ints(start, "start", (B,)),
+            _ints(counts, "counts", (B,)), _ints(err_dev, "err_dev", (1,)))
+
+
+def gdn_kv_write_m(cache, k, v, table, start, rope=None, q=None, q_out=None,
+                   counts=None, err_dev=None, stream=None):
+    """The keys and values k, v [B][M][kvh][hd] of M tokens of every sequence
+    to positions start[b] + m of their pages; rope turns k on the way, and q
+    [B][M][qh][hd] into q_out.  q, k, v may be slices of one projection."""
+    if k.dim() != 4:
+        raise ValueError("k must be [B][M][kvh][hd]")
+    B, M, dtype = k.shape[0], k.shape[1], k.dtype
+    _, kvh, _, hd = cache.shape
+    if k.shape[2:] != (kvh, hd) or v.shape != k.shape:
+        raise ValueError(f"k and v must be [B][M][{kvh}][{hd}]")
+    (kp, ks), (vp, vs) = _rows(k, "k", (B, M), dtype), _rows(v, "v", (B, M), dtype)
+    qp = qo = None
+    qs = qh = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        qp, qs = _rows(q, "q", (B, M), dtype)
+        qh = q.shape[2]
+        if q.shape[3] != hd:
+            raise ValueError(f"q must be [B][M][qh][{hd}]")
+        qo = _tok(q_out, "q_out", q.shape, dtype)
+    tp, cols, sp, cp, ep = _paged(cache, B, table, start, counts, err_dev)
+    r = (_lib or load()).gdn_kv_write_m(
+        ctypes.byref(cache.c), B, M, qh, _code(dtype),
+        None if rope is None else ctypes.byref(rope.c), qp, qs, kp, ks, vp, vs, qo,
+        tp, cols, sp, cp, ep, _stream(stream))
+    if r:
+        raise GDNError(r, "gdn_kv_write_m")
+
+
+def gdn_kv_read(cache, table, start, k, v, counts=None, err_dev=None,
+                stream=None):
+    """Positions start[b] .. start[b] + T - 1 (start None: from 0) of every
+    sequence into k, v [B][T][kvh][hd], float32 or bfloat16."""
+    if k.dim() != 4 or k.shape[2:] != (cache.shape[1], cache.shape[3]):
+        raise ValueError("k must be [B][T][kvh][hd]")
+    B, T, dtype = k.shape[0], k.shape[1], k.dtype
+    tp, cols, sp, cp, ep = _paged(cache, B, table, start, counts, err_dev)
+    r = (_lib or load()).gdn_kv_read(
+        ctypes.byref(cache.c), B, T, _code(dtype), tp, cols, sp, cp,
+        _tok(k, "k", k.shape, dtype), _tok(v, "v", k.shape, dtype), ep,
+        _stream(stream))
+    if r:
+        raise GDNError(r, "gdn_kv_read")
+
+
+def gdn_attn_workspace(cache, M, qh):
+    """Bytes of workspace gdn_attn_step_m needs."""
+    return int((_lib or load()).gdn_attn_workspace(ctypes.byref(cache.c), M, qh))
+
+
+def gdn_attn_step_m(cache, q, table, start, o, scale=None, counts=None,
+                    lse=None, err_dev=None, workspace=None, stream=None):
+    """M = q.shape[1] tokens of every sequence against positions 0 ..
+    start[b] + m of the cache, their own among them: q, o [B][M][qh][hd]
+    float32 or bfloat16, lse float32 [B][M][qh] or None; scale defaults to
+    hd^-0.5."""
+    if q.dim() != 4 or q.shape[3] != cache.shape[3]:
+        raise ValueError("q must be [B][M][qh][hd]")
+    B, M, qh, hd = qs = q.shape
+    dtype = q.dtype
+    tp, cols, sp, cp, ep = _paged(cache, B, table, start, counts, err_dev)
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    r = (_lib or load()).gdn_attn_step_m(
+        ctypes.byref(cache.c), B, M, qh, _code(dtype),
+        hd ** -0.5 if scale is None else scale, _tok(q, "q", qs, dtype), tp, cols,
+        sp, cp, _tok(o, "o", qs, dtype),
+        None if lse is None else _tok(lse, "lse", qs[:3], torch.float32), ep,
+        ws_ptr, ws_bytes, _stream(stream))
+    if r:
+        raise GDNError(r, "gdn_attn_step_m")

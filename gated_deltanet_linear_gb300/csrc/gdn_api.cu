@@ -9,6 +9,7 @@
 // section 8; "34 · batched M rows", section 3.5), and no truncation of a
 // request that does not fit (article 24, section 10).
 
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -674,6 +675,339 @@ int gdn_quant_linear(int rows, int N, int K, int group, int dtype,
   } catch (...) {  // (host locks and tables; nothing is launched)
     return GDN_ECUDA;
   }
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------ attention layers
+
+namespace {
+
+// The checks of a cache's shape alone; fills *c.
+int cache_shape(const gdn_kv_cache *x, gdn::KvCache *c) {
+  if (!x) return GDN_EINVAL;
+  if (x->kind != GDN_KV_BF16 && x->kind != GDN_KV_INT8 && x->kind != GDN_KV_E4M3) return GDN_EINVAL;
+  if (x->hd != 64 && x->hd != 128 && x->hd != 256) return GDN_ESHAPE;
+  if (x->pages < 1 || x->kvh < 1 || x->kvh > GDN_KV_MAX_HEADS) return GDN_ESHAPE;
+  int shift = 4;
+  while (shift < 8 && (1 << shift) != x->page) ++shift;
+  if ((1 << shift) != x->page) return GDN_ESHAPE;
+  const bool scaled = x->kind != GDN_KV_BF16;
+  *c = gdn::KvCache{x->k, x->v, scaled ? x->k_scale : nullptr, scaled ? x->v_scale : nullptr,
+                    x->kind, x->pages, x->kvh, shift};
+  return GDN_OK;
+}
+
+// The buffers of a paged call: what it reads, what it writes, and 4-byte
+// integers of either sort (nullptr: not given).
+struct PagedBufs {
+  Buf in[8], out[8], ints_in[4], ints_out[1];
+  int n_in = 0, n_out = 0, n_ints = 0;
+  void reads(const void *p, size_t bytes) { in[n_in++] = Buf{p, bytes}; }
+  void writes(const void *p, size_t bytes) { out[n_out++] = Buf{p, bytes}; }
+  void reads_ints(const int *p, size_t n) {
+    if (p) ints_in[n_ints++] = Buf{p, n * 4};
+  }
+};
+
+void cache_bufs(const gdn_kv_cache *x, bool written, PagedBufs *b) {
+  const size_t rows = (size_t)x->pages * x->kvh * x->page;
+  const size_t codes = rows * x->hd * (x->kind == GDN_KV_BF16 ? 2 : 1);
+  const bool scaled = x->kind != GDN_KV_BF16;
+  const Buf all[4] = {{x->k, codes}, {x->v, codes}, {x->k_scale, rows * 4}, {x->v_scale, rows * 4}};
+  for (int i = 0; i < (scaled ? 4 : 2); ++i)
+    if (written)
+      b->writes(all[i].p, all[i].bytes);
+    else
+      b->reads(all[i].p, all[i].bytes);
+}
+
+// Alignment, device memory, and that nothing written overlaps anything else
+// (same: an output that may be that input exactly).
+int check_paged(const PagedBufs &b, const int *err, const void *same) {
+  Buf all[16];
+  int n = 0;
+  for (int i = 0; i < b.n_in; ++i) all[n++] = b.in[i];
+  for (int i = 0; i < b.n_out; ++i) all[n++] = b.out[i];
+  int r = check_bufs(all, n);
+  if (r) return r;
+  Buf ints[5];
+  int k = 0;
+  for (int i = 0; i < b.n_ints; ++i) ints[k++] = b.ints_in[i];
+  if (err) ints[k++] = Buf{err, 4};
+  const int dev = current_device();
+  for (int i = 0; i < k; ++i) {
+    if (((uintptr_t)ints[i].p & 3u) != 0) return GDN_EALIGN;
+    r = classify_ptr(ints[i].p, dev, false, nullptr);
+    if (r) return r;
+  }
+  for (int i = 0; i < b.n_out; ++i) {
+    for (int j = 0; j < b.n_in; ++j)
+      if (overlaps(b.out[i], b.in[j]) && !(same && b.out[i].p == same && b.in[j].p == same))
+        return GDN_EALIAS;
+    for (int j = i + 1; j < b.n_out; ++j)
+      if (overlaps(b.out[i], b.out[j])) return GDN_EALIAS;
+    for (int j = 0; j < k; ++j)
+      if (overlaps(b.out[i], ints[j])) return GDN_EALIAS;
+  }
+  if (err) {
+    for (int j = 0; j < b.n_in; ++j)
+      if (overlaps(ints[k - 1], b.in[j])) return GDN_EALIAS;
+    for (int j = 0; j + 1 < k; ++j)
+      if (overlaps(ints[k - 1], ints[j])) return GDN_EALIAS;
+  }
+  return GDN_OK;
+}
+
+int rope_shape(const gdn_rope *p, int hd) {
+  if (!p || !p->freq) return GDN_EINVAL;
+  if (p->layout != GDN_ROPE_HALF && p->layout != GDN_ROPE_PAIRS) return GDN_EINVAL;
+  if (!(p->amp >= -3.0e38f && p->amp <= 3.0e38f)) return GDN_EINVAL;
+  if (p->rot < 16 || p->rot > hd || p->rot % 16) return GDN_ESHAPE;
+  return GDN_OK;
+}
+
+// Rows with a stride: GDN_ESHAPE if they overlap, GDN_EALIGN if one starts
+// off a 16-byte boundary.
+int check_stride(long long stride, long long width, int e) {
+  if (stride < width || stride > (1ll << 40)) return GDN_ESHAPE;
+  return stride * e % 16 ? GDN_EALIGN : GDN_OK;
+}
+size_t strided_bytes(long long tokens, long long stride, long long width, int e) {
+  return (size_t)((tokens - 1) * stride + width) * e;
+}
+
+int check_table(const gdn::KvCache &c, int cols) {
+  if (cols < 1) return GDN_ESHAPE;
+  return ((long long)cols << c.page_shift) > GDN_KV_MAX_POSITIONS ? GDN_ERANGE : GDN_OK;
+}
+
+void set_rope(const gdn_rope *p, gdn::KvRows *r) {
+  r->freq = p ? p->freq : nullptr;
+  r->half = p ? p->rot / 2 : 0;
+  r->pairs = p ? p->layout == GDN_ROPE_PAIRS : 0;
+  r->amp = p ? p->amp : 1.0f;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gdn_rope_freqs(int rot, double base, int scaling, double factor,
+                   double context, double low, double high, double *freq,
+                   float *amp) {
+  if (!freq || !amp) return GDN_EINVAL;
+  if (rot < 2 || rot > 4096 || rot % 2) return GDN_ESHAPE;
+  if (!(base > 0.0) || !isfinite(base)) return GDN_EINVAL;
+  if (scaling < GDN_ROPE_PLAIN || scaling > GDN_ROPE_BAND) return GDN_EINVAL;
+  if (scaling != GDN_ROPE_PLAIN && (!(factor > 0.0) || !isfinite(factor))) return GDN_EINVAL;
+  if (scaling == GDN_ROPE_NTK) {
+    if (rot == 2) return GDN_ESHAPE;
+    base *= pow(factor, rot / (rot - 2.0));
+  }
+  if (scaling == GDN_ROPE_BAND && (!(context > 0.0) || !isfinite(context) || !isfinite(low) ||
+                                   !isfinite(high) || !(low < high)))
+    return GDN_EINVAL;
+  *amp = 1.0f;
+  for (int i = 0; i < rot / 2; ++i) {
+    double f = pow(base, -2.0 * i / rot);
+    if (scaling == GDN_ROPE_LINEAR) f /= factor;
+    if (scaling == GDN_ROPE_BAND) {
+      double w = (context / 6.283185307179586477 * f - low) / (high - low);
+      w = w < 0.0 ? 0.0 : w > 1.0 ? 1.0 : w;
+      f *= w + (1.0 - w) / factor;
+    }
+    freq[i] = f;
+  }
+  if (scaling == GDN_ROPE_BAND) *amp = (float)(0.1 * log(factor) + 1.0);
+  return GDN_OK;
+}
+
+int gdn_rope_m(int rows, int heads, int hd, int dtype, const gdn_rope *rope,
+               const void *x, long long x_stride, const int *pos, void *y,
+               gdn_stream_t stream) {
+  if (hd != 64 && hd != 128 && hd != 256) return GDN_ESHAPE;
+  if (rows < 0 || heads < 1) return GDN_ESHAPE;
+  if (heads > GDN_KV_MAX_HEADS) return GDN_ERANGE;
+  const int e = element_size(dtype);
+  if (!e) return GDN_EINVAL;
+  int r = rope_shape(rope, hd);
+  if (r) return r;
+  const long long width = (long long)heads * hd;
+  r = check_stride(x_stride, width, e);
+  if (r) return r;
+  if (rows == 0) return GDN_OK;
+  if (!pos) return GDN_EINVAL;
+  PagedBufs b;
+  b.reads(x, strided_bytes(rows, x_stride, width, e));
+  b.reads(rope->freq, (size_t)rope->rot / 2 * 8);
+  b.writes(y, (size_t)rows * width * e);
+  b.reads_ints(pos, rows);
+  r = check_paged(b, nullptr, x_stride == width ? x : nullptr);
+  if (r) return r;
+  gdn::KvRows P = {};
+  P.q = x;
+  P.q_out = y;
+  P.q_stride = x_stride;
+  P.tokens = rows;
+  P.pos = pos;
+  P.qh = heads;
+  P.M = 1;
+  set_rope(rope, &P);
+  cudaGetLastError();
+  return status_of(gdn::launch_kv_rows(P, hd, dtype == GDN_BF16, false, (cudaStream_t)stream));
+}
+
+int gdn_kv_write_m(const gdn_kv_cache *cache, int B, int M, int qh, int dtype,
+                   const gdn_rope *rope, const void *q, long long q_stride,
+                   const void *k, long long k_stride, const void *v,
+                   long long v_stride, void *q_out, const int *table, int cols,
+                   const int *start, const int *counts, int *err_dev,
+                   gdn_stream_t stream) {
+  gdn::KvRows P = {};
+  int r = cache_shape(cache, &P.c);
+  if (r) return r;
+  if (B < 0 || qh < 0) return GDN_ESHAPE;
+  if (M < 1 || M > GDN_MAX_TOKENS || qh > GDN_KV_MAX_HEADS) return GDN_ERANGE;
+  if ((long long)B * M > 0x7fffffffll) return GDN_ERANGE;
+  const int e = element_size(dtype);
+  if (!e || (qh > 0) != (q != nullptr) || (qh > 0) != (q_out != nullptr)) return GDN_EINVAL;
+  if (rope && (r = rope_shape(rope, cache->hd)) != 0) return r;
+  const long long wq = (long long)qh * cache->hd, wk = (long long)cache->kvh * cache->hd;
+  if (qh && (r = check_stride(q_stride, wq, e)) != 0) return r;
+  if ((r = check_stride(k_stride, wk, e)) != 0) return r;
+  if ((r = check_stride(v_stride, wk, e)) != 0) return r;
+  if ((r = check_table(P.c, cols)) != 0) return r;
+  if (B == 0) return GDN_OK;
+  if (!table || !start) return GDN_EINVAL;
+  const long long tokens = (long long)B * M;
+  PagedBufs b;
+  b.reads(k, strided_bytes(tokens, k_stride, wk, e));
+  b.reads(v, strided_bytes(tokens, v_stride, wk, e));
+  if (qh) {
+    b.reads(q, strided_bytes(tokens, q_stride, wq, e));
+    b.writes(q_out, (size_t)tokens * wq * e);
+  }
+  if (rope) b.reads(rope->freq, (size_t)rope->rot / 2 * 8);
+  cache_bufs(cache, true, &b);
+  b.reads_ints(table, (size_t)B * cols);
+  b.reads_ints(start, B);
+  b.reads_ints(counts, B);
+  r = check_paged(b, err_dev, qh && q_stride == wq ? q : nullptr);
+  if (r) return r;
+  P.q = q;
+  P.k = k;
+  P.v = v;
+  P.q_out = q_out;
+  P.q_stride = q_stride;
+  P.k_stride = k_stride;
+  P.v_stride = v_stride;
+  P.tokens = tokens;
+  P.start = start;
+  P.counts = counts;
+  P.table = table;
+  P.err = err_dev;
+  P.M = M;
+  P.cols = cols;
+  P.qh = qh;
+  set_rope(rope, &P);
+  cudaGetLastError();
+  return status_of(gdn::launch_kv_rows(P, cache->hd, dtype == GDN_BF16, false, (cudaStream_t)stream));
+}
+
+int gdn_kv_read(const gdn_kv_cache *cache, int B, int T, int dtype,
+                const int *table, int cols, const int *start,
+                const int *counts, void *k, void *v, int *err_dev,
+                gdn_stream_t stream) {
+  gdn::KvRows P = {};
+  int r = cache_shape(cache, &P.c);
+  if (r) return r;
+  if (B < 0) return GDN_ESHAPE;
+  if (T < 1 || T > GDN_KV_MAX_POSITIONS || (long long)B * T > 0x7fffffffll) return GDN_ERANGE;
+  const int e = element_size(dtype);
+  if (!e) return GDN_EINVAL;
+  if ((r = check_table(P.c, cols)) != 0) return r;
+  if (B == 0) return GDN_OK;
+  if (!table) return GDN_EINVAL;
+  const long long tokens = (long long)B * T;
+  const size_t out = (size_t)tokens * cache->kvh * cache->hd * e;
+  PagedBufs b;
+  cache_bufs(cache, false, &b);
+  b.writes(k, out);
+  b.writes(v, out);
+  b.reads_ints(table, (size_t)B * cols);
+  b.reads_ints(start, B);
+  b.reads_ints(counts, B);
+  r = check_paged(b, err_dev, nullptr);
+  if (r) return r;
+  P.q_out = k;
+  P.v_out = v;
+  P.tokens = tokens;
+  P.start = start;
+  P.counts = counts;
+  P.table = table;
+  P.err = err_dev;
+  P.M = T;
+  P.cols = cols;
+  cudaGetLastError();
+  return status_of(gdn::launch_kv_rows(P, cache->hd, dtype == GDN_BF16, true, (cudaStream_t)stream));
+}
+
+size_t gdn_attn_workspace(const gdn_kv_cache *cache, int M, int qh) {
+  gdn::KvCache c;
+  if (cache_shape(cache, &c) || M < 1 || M > GDN_ATTN_MAX_TOKENS || qh < 1 ||
+      qh > GDN_KV_MAX_HEADS || qh % c.kvh)
+    return 0;
+  return gdn::attn_workspace_bytes(c.kind, M, qh / c.kvh, cache->hd);
+}
+
+int gdn_attn_step_m(const gdn_kv_cache *cache, int B, int M, int qh, int dtype,
+                    float scale, const void *q, const int *table, int cols,
+                    const int *start, const int *counts, void *o, float *lse,
+                    int *err_dev, void *workspace, size_t ws_bytes,
+                    gdn_stream_t stream) {
+  gdn::AttnArgs P = {};
+  int r = cache_shape(cache, &P.c);
+  if (r) return r;
+  if (B < 0 || qh < 1 || qh % cache->kvh) return GDN_ESHAPE;
+  if (M < 1 || M > GDN_ATTN_MAX_TOKENS || qh > GDN_KV_MAX_HEADS) return GDN_ERANGE;
+  if ((long long)B * M * qh > 0x7fffffffll) return GDN_ERANGE;
+  const int e = element_size(dtype);
+  if (!e || !(scale >= -3.0e38f && scale <= 3.0e38f)) return GDN_EINVAL;
+  if ((r = check_table(P.c, cols)) != 0) return r;
+  if (B == 0) return GDN_OK;
+  if (!table || !start) return GDN_EINVAL;
+  const size_t need = gdn_attn_workspace(cache, M, qh);
+  if (!workspace) return GDN_EINVAL;
+  if (ws_bytes < need) return GDN_ERANGE;
+  const size_t rows = (size_t)B * M * qh;
+  PagedBufs b;
+  b.reads(q, rows * cache->hd * e);
+  cache_bufs(cache, false, &b);
+  b.writes(o, rows * cache->hd * e);
+  b.writes(workspace, need);
+  if (lse) b.writes(lse, rows * 4);
+  b.reads_ints(table, (size_t)B * cols);
+  b.reads_ints(start, B);
+  b.reads_ints(counts, B);
+  r = check_paged(b, err_dev, nullptr);
+  if (r) return r;
+  P.q = q;
+  P.o = o;
+  P.lse = lse;
+  P.table = table;
+  P.start = start;
+  P.counts = counts;
+  P.err = err_dev;
+  P.scale = (float)(scale * 1.4426950408889634);
+  P.B = B;
+  P.M = M;
+  P.cols = cols;
+  P.qh = qh;
+  P.group = qh / cache->kvh;
+  P.part = static_cast<float *>(workspace);
+  cudaGetLastError();
+  return status_of(gdn::launch_attn(P, cache->hd, dtype == GDN_BF16, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -108,6 +108,50 @@ cudaError_t launch_quant_linear_wide(const void *x, const unsigned char *qw, con
 // Threads of it that gave up a wait for their products.
 cudaError_t quant_timeouts(unsigned int *count);
 
+// A paged key-value cache (gdn_kv_cache, checked): rows of hd channels at
+// ((page * kvh + head) << page_shift) + row of the page, and their scales.
+constexpr int kKvBf16 = 0, kKvInt8 = 1, kKvE4m3 = 2;
+struct KvCache {
+  void *k, *v;
+  float *k_scale, *v_scale;  // null for bf16
+  int kind, pages, kvh, page_shift;
+};
+
+// Rows to turn, to write into a cache or to read from one.  pos given: rope
+// alone, `tokens` rows of qh heads; otherwise B sequences of M tokens at
+// positions start[b] + m of their pages.  Strides in elements from token to
+// token.  Reading: k goes to q_out, v to v_out.
+struct KvRows {
+  KvCache c;
+  const void *q, *k, *v;
+  void *q_out, *v_out;
+  long long q_stride, k_stride, v_stride, tokens;
+  const int *pos, *start, *counts, *table;
+  int *err;
+  const double *freq;
+  float amp;
+  int half, pairs;  // rot / 2; pairs side by side
+  int M, cols, qh;
+  int tpc, spb;  // tokens and heads of a block (set by the launch)
+};
+cudaError_t launch_kv_rows(const KvRows &P, int hd, bool bf16, bool read,
+                           cudaStream_t stream);
+
+// New tokens against a paged cache (gdn_attn_step_m).
+struct AttnArgs {
+  KvCache c;
+  const void *q;
+  void *o;
+  float *lse;
+  const int *table, *start, *counts;
+  int *err;
+  float scale;  // times log2 e
+  int B, M, cols, qh, group;
+  float *part;  // the workspace
+};
+size_t attn_workspace_bytes(int kind, int M, int group, int hd);
+cudaError_t launch_attn(const AttnArgs &P, int hd, bool bf16, cudaStream_t stream);
+
 // Chunked tensor-core prefill (defined in gdn_prefill.cu).
 size_t prefill_workspace_bytes(int B, int kh, int vh, int T, int chunk,
                                int precision);

@@ -518,6 +518,176 @@ int gdn_quant_linear(int rows, int N, int K, int group, int dtype,
                      const void *x, const unsigned char *qw,
                      const void *scales, void *y, gdn_stream_t stream);
 
+/*
+ * ------------------------------------------------------ attention layers
+ * The calls below serve the full-attention layers that stand between the
+ * linear ones ("34 · batched M rows", section 3.6: append the keys and
+ * values of M rows, then grouped-query attention of M tokens with causality
+ * among them).  Rolling back drafted tokens needs no call: a smaller start at
+ * the next write and step is the rollback (section 3.7: attention rolls back
+ * its cursor alone).
+ *
+ * A cache is pages of `page` rows for each key head:
+ *     k, v              [pages][kvh][page][hd]  bf16, int8 or e4m3
+ *     k_scale, v_scale  [pages][kvh][page]      fp32, 8-bit caches alone
+ * Position p of sequence b is row p % page of page table[b][p / page], with
+ * table [B][cols] int32 on the device: pages in any order, shared ones too.
+ * A row holds code * scale with scale = max|row| / 127 (e4m3: 448) and code the
+ * nearest to row / scale, ties to even; a row of zeros has scale 0, and a row
+ * with an element that is not finite has scale NaN, so that it reads as NaN
+ * throughout.  bf16 rows are rounded once.  An e4m3 cache filled elsewhere must
+ * not hold NaN codes (0x7f, 0xff).
+ *
+ * start [B] int32 (device) is the number of positions before the call's
+ * tokens, counts [B] int32 (device) or NULL the number of tokens that sequence b
+ * has of the M (NULL: all of them; 0 leaves it out).  Rows behind a sequence's
+ * last token are not used and keep what they held.  A count outside 0..M, a
+ * start below 0 and an end behind cols * page leave the sequence as it was and
+ * set *err_dev (device int, may be NULL) to 1; so does a page number outside
+ * 0..pages-1, as far as stated at each call.  A table entry is looked at only
+ * where a position of the sequence lies.
+ */
+enum {
+    GDN_KV_BF16 = 0,
+    GDN_KV_INT8 = 1,
+    GDN_KV_E4M3 = 2
+};
+
+typedef struct gdn_kv_cache {
+    void *k, *v;
+    float *k_scale, *v_scale; /* NULL for GDN_KV_BF16                          */
+    int kind;                 /* GDN_KV_BF16, GDN_KV_INT8 or GDN_KV_E4M3        */
+    int pages;                /* >= 1                                           */
+    int kvh;                  /* key heads, 1 .. GDN_KV_MAX_HEADS               */
+    int page;                 /* rows of a page: 16, 32, 64, 128 or 256         */
+    int hd;                   /* channels of a head: 64, 128 or 256             */
+} gdn_kv_cache;
+
+#define GDN_KV_MAX_HEADS 4096
+/* Largest cols * page. */
+#define GDN_KV_MAX_POSITIONS (1 << 30)
+/* Largest M of gdn_attn_step_m. */
+#define GDN_ATTN_MAX_TOKENS 64
+
+/* Which channels make a pair. */
+enum {
+    GDN_ROPE_HALF = 0, /* i and i + rot / 2                                    */
+    GDN_ROPE_PAIRS = 1 /* 2 i and 2 i + 1                                      */
+};
+
+/* How frequencies are stretched for contexts longer than the trained one. */
+enum {
+    GDN_ROPE_PLAIN = 0,  /* f_i = base^(-2 i / rot)                            */
+    GDN_ROPE_LINEAR = 1, /* f_i / factor                                       */
+    GDN_ROPE_NTK = 2,    /* base factor^(rot / (rot - 2)) in place of base     */
+    GDN_ROPE_BAND = 3    /* by the turns r = context f_i / 2 pi that a pair
+                            makes in the trained context: f_i from `high` turns
+                            up, f_i / factor from `low` down, a blend linear in r
+                            between; amplitude 0.1 ln(factor) + 1               */
+};
+
+/* Rotary positions: pair i (i < rot / 2) of the first rot channels of a head
+ * at position p becomes
+ *     amp (x cos(p f_i) - y sin(p f_i)),  amp (y cos(p f_i) + x sin(p f_i)).
+ * Negated frequencies turn back (and, amp aside, give the gradient of x). */
+typedef struct gdn_rope {
+    const double *freq; /* [rot / 2] radians a position, DEVICE memory          */
+    int rot;            /* a multiple of 16, 16 .. hd                           */
+    int layout;         /* GDN_ROPE_HALF or GDN_ROPE_PAIRS                      */
+    float amp;          /* finite                                               */
+} gdn_rope;
+
+/*
+ * gdn_rope_freqs - frequencies and amplitude on the HOST, in 64 bits (no
+ * device work): freq [rot / 2] and *amp, to be copied to the device and kept.
+ * rot even, 2 .. 4096 (GDN_ESHAPE; NTK wants rot > 2); base > 0 and factor > 0
+ * finite, context > 0 and low < high finite for GDN_ROPE_BAND (GDN_EINVAL).
+ */
+int gdn_rope_freqs(int rot, double base, int scaling, double factor,
+                   double context, double low, double high, double *freq,
+                   float *amp);
+
+/*
+ * gdn_rope_m - y = x turned, for `rows` rows of `heads` heads at positions
+ * pos [rows] (int32, device; any value).
+ *   x  rows of heads * hd elements, x_stride elements from row to row (a
+ *      multiple of 16 bytes, >= heads * hd; GDN_EALIGN, GDN_ESHAPE)
+ *   y  [rows][heads][hd], contiguous; may be x if x is contiguous
+ *   dtype  GDN_F32 or GDN_BF16
+ * Angles are exact to 2^-53 p f_i and 1e-7 at any position; the products are
+ * fp32, and a bf16 y is rounded once.
+ */
+int gdn_rope_m(int rows, int heads, int hd, int dtype, const gdn_rope *rope,
+               const void *x, long long x_stride, const int *pos, void *y,
+               gdn_stream_t stream);
+
+/*
+ * gdn_kv_write_m - the keys and values of M tokens of B sequences into the
+ * cache, in one kernel with the rotation of q and k.
+ *   k, v  rows of kvh * hd elements for each of the B * M tokens, k_stride and
+ *         v_stride elements from token to token (as x_stride above), so that
+ *         the rows of one projection [B][M][q | k | v] are taken as they lie
+ *   rope  NULL: nothing is turned;  q, q_out  NULL, or qh heads likewise:
+ *         q_out [B][M][qh][hd] = q turned (q_out may be q if q is contiguous)
+ * start: required.  A row whose page number is not one of the cache's is not
+ * written and sets *err_dev; its q is turned all the same.  New positions of
+ * two sequences must lie in different rows of the cache: of two written to one
+ * row either may stay.  M * B < 2^31, M <= GDN_MAX_TOKENS (GDN_ERANGE).
+ */
+int gdn_kv_write_m(const gdn_kv_cache *cache, int B, int M, int qh, int dtype,
+                   const gdn_rope *rope, const void *q, long long q_stride,
+                   const void *k, long long k_stride, const void *v,
+                   long long v_stride, void *q_out, const int *table, int cols,
+                   const int *start, const int *counts, int *err_dev,
+                   gdn_stream_t stream);
+
+/*
+ * gdn_kv_read - positions start[b] .. start[b] + T - 1 (start NULL: from 0) of
+ * every sequence as rows k, v [B][T][kvh][hd] (GDN_F32 or GDN_BF16: code *
+ * scale in fp32, rounded once).  Rows of a page that the cache has not keep what
+ * they held and set *err_dev.  1 <= T <= GDN_KV_MAX_POSITIONS, B * T < 2^31.
+ */
+int gdn_kv_read(const gdn_kv_cache *cache, int B, int T, int dtype,
+                const int *table, int cols, const int *start,
+                const int *counts, void *k, void *v, int *err_dev,
+                gdn_stream_t stream);
+
+/*
+ * gdn_attn_workspace - bytes of device workspace gdn_attn_step_m needs (0 on
+ * invalid arguments).  It does not grow with B or with lengths.
+ */
+size_t gdn_attn_workspace(const gdn_kv_cache *cache, int M, int qh);
+
+/*
+ * gdn_attn_step_m - attention of M tokens (1 .. GDN_ATTN_MAX_TOKENS) of B
+ * sequences over the cache, which holds their own keys and values already:
+ *     o[b][m][i] = sum_p softmax_p(scale q[b][m][i] . k_p) v_p,
+ *     p = 0 .. start[b] + m, key head i / (qh / kvh).
+ *   q, o  [B][M][qh][hd], dtype GDN_F32 or GDN_BF16; qh a multiple of kvh
+ *   scale finite;  start: required
+ *   lse   NULL, or fp32 [B][M][qh]: log sum_p exp(scale q . k_p)
+ *   workspace  at least gdn_attn_workspace() bytes (GDN_ERANGE if smaller);
+ *         calls that may overlap on the GPU need one each
+ * A page number that the cache has not sets *err_dev, and the rows of o and lse
+ * that attend over that page's group of keys are NaN.
+ * Numbers: every sum, maximum and weight is fp32.  8-bit codes enter the
+ * products as they are; an fp32 q as two fp16 numbers scaled by its row
+ * (22 bits), weights times scales as two fp16 numbers (22 bits, down to 2^-37 of
+ * the largest).  bf16 caches take bf16 operands: q as it is or (fp32) as three
+ * numbers, weights as two (16 bits) or (fp32) three.  A bf16 o is rounded once.
+ * Scores are met for |scale q . k| log2 e below 2^100.
+ * What is not finite: in q, its own row of o; in a row of k or v, the rows of o
+ * that see it (throughout, where it came with the call's own tokens) and no
+ * other, whatever lies behind a sequence's end or in a masked place.
+ * The same lengths, table and values give the same bits; other lengths in the
+ * batch may cut a sequence elsewhere and differ in the last ones.
+ */
+int gdn_attn_step_m(const gdn_kv_cache *cache, int B, int M, int qh, int dtype,
+                    float scale, const void *q, const int *table, int cols,
+                    const int *start, const int *counts, void *o, float *lse,
+                    int *err_dev, void *workspace, size_t ws_bytes,
+                    gdn_stream_t stream);
+
 /* Static description of a status code (never NULL).  The codes are the
  * refusals of "24 · GDN linear attention to GPU", section 8 (a request the
  * library cannot serve as asked is refused with an error, never served by a
