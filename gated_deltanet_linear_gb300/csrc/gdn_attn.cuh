@@ -59,29 +59,32 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr float kNone = -1e30f;  // the reference of rows that have seen nothing
 constexpr float kSlack = 3.0f;   // how far the maximum may pass it (log2)
+constexpr float kUp = 12.0f;     // weights of 8-bit rows reach 2^12 (+ kSlack)
 constexpr int kSms = 152;
 
-// Sizes of a variant.
-template <int kHd, int kKind>
+// Sizes of a variant: R tiles of 8 rows.
+template <int kHd, int kKind, int R>
 struct Sizes {
   static constexpr int kBytes = kKind == kKvBf16 ? 2 : 1;
-  static constexpr int kRow = kHd * kBytes;                   // bytes of a row
-  static constexpr int kTT = kBytes == 1 || kRow <= 128 ? 32 : 16;  // positions of a tile
-  static constexpr int kUnit = kTT * kRow;                    // K or V of a tile
+  static constexpr int kRow = kHd * kBytes;               // bytes of a row
+  // CTAs an SM: a lane has kHd R / 4 sums, and three slots a warp are wanted
+  static constexpr int kCtas = kHd * R > 256 || kRow > 256 ? 1 : 2;
+  static constexpr int kTT = kRow <= 128 ? 32 : 16;       // positions of a tile
+  static constexpr int kUnit = kTT * kRow;                // K or V of a tile
   static constexpr int kSlot = kUnit + (kKind == kKvBf16 ? 0 : 8 * kTT);  // and scales
-  static constexpr int kCtas = kHd == 256 ? 1 : 2;            // CTAs an SM
-  static constexpr int kRing = (kCtas == 1 ? 26 : 13) * 1024;  // a warp's ring
+  static constexpr int kRing = kCtas == 1 ? 25 * 1024 + 512 : 13 * 1024;  // a warp's ring
   static constexpr int kSlots = kRing / kSlot;
   static constexpr int kChunk = kWarps * kTT;
+  // channels of 8 rows of fp32 sums that a slot holds
+  static constexpr int kStage = kSlot >= 32 * kHd ? kHd : kHd / 2;
 };
 
-// Rows of an item: 8 (R = 1) or 16 (R = 2).
+// Parts of q and of the weights.
 template <int kKind, bool kBf16>
 struct Parts {
   static constexpr int kQ = kKind == kKvBf16 ? (kBf16 ? 1 : 3) : (kBf16 ? 1 : 2);
-  static constexpr int kP = kKind == kKvBf16 ? (kBf16 ? 2 : 3) : 2;
+  static constexpr int kP = kKind == kKvBf16 ? (kBf16 ? 2 : 3) : (kBf16 ? 1 : 2);
 };
-__host__ __device__ constexpr int tiles_of(int parts, int R) { return R == 1 ? (parts + 1) / 2 : parts; }
 
 // A CTA's share of the chunks, and where an item's parts lie.
 struct Share {
@@ -136,19 +139,27 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) {
   return r;
 }
 
-// c += a b: 16 rows, 8 columns, 16 channels; fp16 or bf16.
+// c += a b: 16 by 8 by 16; fp16 or bf16.
 template <bool kHalf>
-__device__ __forceinline__ void mma(float (&c)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, const uint2 &b) {
   if (kHalf)
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
   else
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+}
+
+// An 8 x 8 tile of 16-bit numbers, transposed among the lanes.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 // Four codes as two pairs of fp16.
@@ -256,27 +267,25 @@ __device__ __forceinline__ int v_place(int r, int c) {
 
 template <int kHd, int kKind, bool kBf16, int R>
 struct Shared {
-  using Z = Sizes<kHd, kKind>;
-  static constexpr int kQTiles = tiles_of(Parts<kKind, kBf16>::kQ, R);
-  static constexpr int kQBytes = kHd / 16 * kQTiles * 512;
+  using Z = Sizes<kHd, kKind, R>;
+  static constexpr int kQBytes = kHd / 16 * Parts<kKind, kBf16>::kQ * R * 256;
   static constexpr int kRingAt = kQBytes;
   static constexpr int kStatAt = kRingAt + kWarps * Z::kSlots * Z::kSlot;
-  // m and l of every warp's rows, the rows' factors, sums of the search
-  static constexpr int kBytes = kStatAt + kWarps * 16 * 8 + 16 * 4 + 2 * kWarps * 8 + 32;
+  // m and l of every warp's rows, the rows' factors, counts of the search
+  static constexpr int kBytes = kStatAt + kWarps * 8 * R * 8 + 8 * R * 4 + 2 * kWarps * 8 + 32;
 };
 
 template <int kHd, int kKind, bool kBf16, int R>
-__global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind>::kCtas)
+__global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
     attn_kernel(const AttnArgs P) {
-  using Z = Sizes<kHd, kKind>;
+  using Z = Sizes<kHd, kKind, R>;
   using Sh = Shared<kHd, kKind, kBf16, R>;
   using T = typename std::conditional<kBf16, __nv_bfloat16, float>::type;
   constexpr bool kHalf = kKind != kKvBf16;
-  constexpr int kTT = Z::kTT, kRow = Z::kRow, kSlots = Z::kSlots, kNJ = kTT / 8;
+  constexpr int kTT = Z::kTT, kRow = Z::kRow, kSlots = Z::kSlots, kMT = kTT / 16;
   constexpr int kQP = Parts<kKind, kBf16>::kQ, kPP = Parts<kKind, kBf16>::kP;
-  constexpr int kQT = Sh::kQTiles, kPT = tiles_of(kPP, R);
   constexpr int kVec = 16 / Z::kBytes;  // elements of 16 bytes
-  constexpr int kTiles = kHd / 8;       // column tiles of the sums
+  constexpr int kDT = kHd / 16;         // tiles of 16 channels
   extern __shared__ __align__(128) unsigned char smem[];
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -284,57 +293,84 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind>::kCtas)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int nrt = (P.M * P.group + 8 * R - 1) / (8 * R), items = P.c.kvh * nrt;
   uint32_t *const qs = reinterpret_cast<uint32_t *>(smem);
-  float2 *const stat = reinterpret_cast<float2 *>(smem + Sh::kStatAt);  // [warp][16]
-  float *const factor = reinterpret_cast<float *>(stat + kWarps * 16);  // [16]
-  long long *const room = reinterpret_cast<long long *>(factor + 16);
+  float2 *const stat = reinterpret_cast<float2 *>(smem + Sh::kStatAt);  // [warp][8 R]
+  float *const factor = reinterpret_cast<float *>(stat + kWarps * 8 * R);  // [8 R]
+  long long *const room = reinterpret_cast<long long *>(factor + 8 * R);
   int *const found = reinterpret_cast<int *>(room + 2 * kWarps);  // [3]
+  signed char *const rooms = reinterpret_cast<signed char *>(found + 4);  // [kWarps]
 
   // ---- this CTA's share: chunks [u0, u1) of the list, from sequence b0 on
   auto chunks = [&](int b, int &start) {
     return (length_of(P, b, start) + Z::kChunk - 1) / Z::kChunk;
   };
-  long long total = 0, none = 0;
-  for (int b = tid; b < P.B; b += kThreads) {
+  auto counted = [&](int b) {
+    if (b >= P.B) return 0;
     int start;
     const int n = chunks(b, start);
-    total += n;
     if (P.err && blockIdx.x == 0 && n == 0 && !(P.counts && P.counts[b] == 0)) *P.err = 1;
+    return n;
+  };
+  auto scan = [&](int n) {  // up to this lane's, within the warp
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int x = __shfl_up_sync(kFull, n, d);
+      if (lane >= d) n += x;
+    }
+    return n;
+  };
+  // the first 256 sequences lane by lane, the others' sum
+  int n0 = counted(tid), up = scan(n0);
+  long long rest = 0;
+  for (int b = tid + kThreads; b < P.B; b += kThreads) rest += counted(b);
+  if (P.B > kThreads) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) rest += __shfl_xor_sync(kFull, rest, d);
   }
-  block_sums(total, none, room);
-  total *= items;
+  if (lane == 31) {
+    room[warp] = up;
+    room[kWarps + warp] = rest;
+  }
+  __syncthreads();
+  long long lo = 0, before = 0, total = 0;  // chunks (of one item each) before
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) lo += room[w];
+    before += room[w];
+    total += room[kWarps + w];
+  }
+  total = (total + before) * items;
   if (total == 0) return;
   const Share share{total, (int)min((long long)gridDim.x, total)};
   if ((int)blockIdx.x >= share.ctas) return;
   const long long u0 = share.first(blockIdx.x), u1 = share.first(blockIdx.x + 1);
-  long long before = 0;  // chunks (of one item each) of the sequences before
-  for (int base = 0; base < P.B; base += kThreads) {
-    int start, n = base + tid < P.B ? chunks(base + tid, start) : 0, up = n;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int x = __shfl_up_sync(kFull, up, d);
-      if (lane >= d) up += x;
+  auto find = [&](int b, int n, long long first) {
+    first *= items;
+    if (n && u0 >= first && u0 < first + (long long)n * items) {
+      found[0] = b;
+      found[1] = (int)((u0 - first) / n);
+      found[2] = (int)((u0 - first) % n);
     }
+  };
+  find(tid, n0, lo + up - n0);
+  for (int base = kThreads; before * items <= u0; base += kThreads) {
+    n0 = counted(base + tid);
+    up = scan(n0);
     __syncthreads();
     if (lane == 31) room[warp] = up;
     __syncthreads();
-    long long lo = before;
+    lo = before;
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) lo += room[w];
       before += room[w];
     }
-    lo = (lo + up - n) * items;
-    if (n && u0 >= lo && u0 < lo + (long long)n * items) {
-      found[0] = base + tid;
-      found[1] = (int)((u0 - lo) / n);
-      found[2] = (int)((u0 - lo) % n);
-    }
-    if (before * items > u0) break;
+    find(base + tid, n0, lo + up - n0);
   }
   __syncthreads();
 
-  // ---- a walk over the share: (sequence, item, chunk), `left` chunks to go
+  // ---- a walk over the share: (sequence, head, row tile, chunk)
   struct Walk {
-    int b, j, c, n, len, start;
+    int b, h, rt, c, n, len, start;
     long long left;
   };
   auto enter = [&](Walk &w) {
@@ -343,15 +379,16 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind>::kCtas)
   };
   auto next_item = [&](Walk &w) {  // (only while chunks are left)
     w.c = 0;
-    if (++w.j == items) {
-      w.j = 0;
-      do {
-        ++w.b;
-        enter(w);
-      } while (w.n == 0);
-    }
+    if (++w.rt < nrt) return;
+    w.rt = 0;
+    if (++w.h < P.c.kvh) return;
+    w.h = 0;
+    do {
+      ++w.b;
+      enter(w);
+    } while (w.n == 0);
   };
-  Walk ahead{found[0], found[1], found[2], 0, 0, 0, u1 - u0};
+  Walk ahead{found[0], found[1] / nrt, found[1] % nrt, found[2], 0, 0, 0, u1 - u0};
   enter(ahead);
   Walk here = ahead;
 
@@ -360,15 +397,16 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind>::kCtas)
       (uint32_t)__cvta_generic_to_shared(smem + Sh::kRingAt) + warp * (kSlots * Z::kSlot);
   constexpr int kCpr = kRow / 16;             // 16-byte units of a row
   constexpr int kIters = kTT * kCpr / 32;     // of a lane, for K or V of a tile
-  constexpr int kHalves = kTT / 16;           // a tile's pages: one for 16 positions
-  static_assert(kIters % kHalves == 0, "a lane's unit lies in one page");
+  constexpr int kPerPage = kIters / kMT;      // 16 positions lie in one page, one run
+  static_assert(kIters % kMT == 0, "a lane's unit lies in one page");
   const int page_mask = (1 << P.c.page_shift) - 1;
   uint32_t bad = 0;            // slots with a page that is not there
   int put = 0;                 // the slot of the next unit
   bool v_next = false;         // the unit is V of the tile whose K went before
-  long long row_at[kHalves];   // the tile's first rows in the cache, -1: none
+  bool full = false;           // all of the tile's positions and pages are there
+  long long row_at[kMT];       // the tile's first rows in the cache, -1: none
   int rows_on = 0;             // positions of the tile that are there
-  int pages[kHalves];          // of the next tile, asked for a tile ahead
+  int pages[kMT];              // of the next tile, asked for a tile ahead
   auto seek = [&]() {          // to the next chunk in which this warp has a tile
     while (ahead.left > 0 && (ahead.c * kWarps + warp) * kTT >= ahead.len) {
       --ahead.left;
@@ -377,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind>::kCtas)
     if (ahead.left > 0) {
       const int pos = (ahead.c * kWarps + warp) * kTT;
 #pragma unroll
-      for (int i = 0; i < kHalves; ++i) {
+      for (int i = 0; i < kMT; ++i) {
         const int col = (pos + 16 * i) >> P.c.page_shift;
         pages[i] = pos + 16 * i < ahead.len ? __ldg(P.table + (size_t)ahead.b * P.cols + col) : 0;
       }
@@ -389,13 +427,15 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind>::kCtas)
       if (!v_next) {
         const int pos = (ahead.c * kWarps + warp) * kTT;
         rows_on = min(ahead.len - pos, kTT);
+        full = rows_on == kTT;
         bad &= ~(1u << put);
 #pragma unroll
-        for (int i = 0; i < kHalves; ++i) {
+        for (int i = 0; i < kMT; ++i) {
           const bool ok = (unsigned)pages[i] < (unsigned)P.c.pages;
           if (!ok && 16 * i < rows_on) bad |= 1u << put;
+          full &= ok;
           row_at[i] = !ok ? -1
-                          : (((long long)pages[i] * P.c.kvh + ahead.j / nrt) << P.c.page_shift) +
+                          : (((long long)pages[i] * P.c.kvh + ahead.h) << P.c.page_shift) +
                                 ((pos + 16 * i) & page_mask);
         }
         --ahead.left;
@@ -403,19 +443,23 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind>::kCtas)
       }
       const unsigned char *from = static_cast<const unsigned char *>(v_next ? P.c.v : P.c.k);
 #pragma unroll
-      for (int i = 0; i < kIters; ++i) {
-        const int half = i / (kIters / kHalves), u = 32 * i + lane, r = u / kCpr, c = u % kCpr;
-        const bool on = row_at[half] >= 0 && r < rows_on;
-        const int to = v_next ? v_place<kRow, kKind == kKvBf16>(r, c) : k_place<kRow>(r, c);
-        cp16(slot + 16 * to,
-             from + (on ? (size_t)(row_at[half] + (r & 15)) * kRow + 16 * c : (size_t)0), on);
+      for (int half = 0; half < kMT; ++half) {
+        const unsigned char *src =
+            from + (row_at[half] < 0 ? (size_t)0 : (size_t)row_at[half] * kRow) + 16 * lane;
+#pragma unroll
+        for (int j = 0; j < kPerPage; ++j) {
+          const int u = 32 * (half * kPerPage + j) + lane, r = u / kCpr, c = u % kCpr;
+          const int to = v_next ? v_place<kRow, kKind == kKvBf16>(r, c) : k_place<kRow>(r, c);
+          const bool on = full || (row_at[half] >= 0 && r < rows_on);
+          cp16(slot + 16 * to, on ? src + 512 * j : from, on);
+        }
       }
       if (kKind != kKvBf16 && !v_next && lane < 2 * kTT / 4) {  // both scales, with K
-        const int which = lane / (kTT / 4), r = 4 * (lane % (kTT / 4)), half = r / 16;
+        const int which = lane / (kTT / 4), r = 4 * (lane % (kTT / 4));
         const float *s = which ? P.c.v_scale : P.c.k_scale;
-        const bool on = row_at[kHalves == 1 ? 0 : half] >= 0 && r < rows_on;
-        cp16(slot + Z::kUnit + 16 * lane,
-             s + (on ? (size_t)(row_at[kHalves == 1 ? 0 : half] + (r & 15)) : (size_t)0), on);
+        const long long at = row_at[kMT == 1 ? 0 : r / 16];
+        const bool on = at >= 0 && r < rows_on;
+        cp16(slot + Z::kUnit + 16 * lane, s + (on ? (size_t)(at + (r & 15)) : (size_t)0), on);
       }
       if (v_next) seek();
       v_next = !v_next;
@@ -427,19 +471,19 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind>::kCtas)
 #pragma unroll
   for (int i = 0; i < kSlots - 1; ++i) issue();
 
-  float acc[kTiles][4];
-  float m[R], l[R];
-  int lim[R];  // positions that the lane's rows see
+  float acc[kDT][R][4];
+  float m[R][2], l[R][2];
+  int lim[R][2];  // positions that the lane's rows see
   int get = 0;
 
   while (here.left > 0) {
     // ---- an item's part: chunks [here.c, here.c + n)
     const int c0 = here.c, n = (int)min((long long)(here.n - here.c), here.left);
-    const int b = here.b, h = here.j / nrt, row0 = (here.j % nrt) * 8 * R;
+    const int b = here.b, h = here.h, row0 = here.rt * 8 * R;
     const int rows = min(8 * R, P.M * P.group - row0);
     const int len = here.len, start = here.start, seen_by_all = start + 1 + row0 / P.group;
 
-    // q's rows as the products' operands: warp w has rows w and w + 8
+    // q's rows as the products' operands: warp w has rows w, w + 8, ..
     __syncthreads();  // (the last item's are read)
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -447,8 +491,8 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind>::kCtas)
       const int mt = row / P.group, head = h * P.group + row - mt * P.group;
       const T *src = static_cast<const T *>(P.q) +
                      (((size_t)b * P.M + mt) * P.qh + head) * kHd;
-      float x[kHd == 256 ? 2 : 1][4] = {};
       constexpr int kQuads = kHd == 256 ? 2 : 1;
+      float x[kQuads][4] = {};
 #pragma unroll
       for (int e = 0; e < kQuads; ++e)
         if (r < rows && lane + 32 * e < kHd / 4) load4(src + 4 * (lane + 32 * e), x[e]);
@@ -462,9 +506,9 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind>::kCtas)
         top = __reduce_max_sync(kFull, top);
         // below 2^(ex + 1), or not finite: as it is
         const int ex = top < 0x7f800000u ? max((int)(top >> 23) - 127, -126) : 0;
-        const int up = 13 - ex;  // by two factors that are floats
-        const float f0 = __int_as_float((up / 2 + 127) << 23);
-        const float f1 = __int_as_float((up - up / 2 + 127) << 23);
+        const int by = 13 - ex;  // in two factors that are floats
+        const float f0 = __int_as_float((by / 2 + 127) << 23);
+        const float f1 = __int_as_float((by - by / 2 + 127) << 23);
 #pragma unroll
         for (int e = 0; e < kQuads; ++e)
 #pragma unroll
@@ -478,32 +522,33 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind>::kCtas)
         if (d < kHd) {
           // channels d .. d + 3: product ks, lane 4 (r % 8) + tq, both pairs
           const int ks = d / (4 * kVec) * (kVec / 4) + d % kVec / 4, tq = d / kVec % 4;
-          uint32_t lo[kQP], hi[kQP];
-          cut<kHalf, kQP>(x[e][0], x[e][1], lo);
-          cut<kHalf, kQP>(x[e][2], x[e][3], hi);
+          uint32_t a[kQP], c[kQP];
+          cut<kHalf, kQP>(x[e][0], x[e][1], a);
+          cut<kHalf, kQP>(x[e][2], x[e][3], c);
 #pragma unroll
-          for (int p = 0; p < kQT * (R == 1 ? 2 : 1); ++p) {
-            const int tile = R == 1 ? p / 2 : p, up = R == 1 ? p & 1 : i;
-            uint32_t *to = qs + ((ks * kQT + tile) * 32 + 4 * (r & 7) + tq) * 4 + up;
-            to[0] = p < kQP ? lo[p < kQP ? p : 0] : 0u;
-            to[2] = p < kQP ? hi[p < kQP ? p : 0] : 0u;
-          }
+          for (int p = 0; p < kQP; ++p)
+            reinterpret_cast<uint2 *>(qs)[((ks * kQP + p) * R + i) * 32 + 4 * (r & 7) + tq] =
+                make_uint2(a[p], c[p]);
         }
       }
     }
     __syncthreads();
-    float fac[R];
+    float fac[R][2];
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      m[i] = kNone;
-      l[i] = 0.0f;
-      fac[i] = factor[g + 8 * i];
-      lim[i] = start + 1 + (row0 + g + 8 * i) / P.group;
-    }
+    for (int i = 0; i < R; ++i)
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i)
+      for (int e = 0; e < 2; ++e) {
+        m[i][e] = kNone;
+        l[i][e] = 0.0f;
+        fac[i][e] = factor[8 * i + 2 * t + e];
+        lim[i][e] = start + 1 + (row0 + 8 * i + 2 * t + e) / P.group;
+      }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) acc[i][k] = 0.0f;
+    for (int d = 0; d < kDT; ++d)
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[d][i][k] = 0.0f;
 
     int any = 0;
     for (int c = c0; c < c0 + n; ++c) {
@@ -511,130 +556,137 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind>::kCtas)
       if (pos >= len) continue;
       any = 1;
       const bool masked = pos + kTT > seen_by_all || pos + kTT > len;
-      // ---- scores of the tile
+      // ---- scores of the tile: 16 positions by 8 rows a product
       wait_for<kSlots - 2>();
       __syncwarp();
       issue();
       uint32_t slot = ring + get * Z::kSlot;
       const bool broken = bad >> get & 1;
-      float s[kNJ][4] = {};
+      float s[kMT][R][4] = {};
 #pragma unroll
       for (int sg = 0; sg < kHd / (4 * kVec); ++sg) {
-        uint4 raw[kNJ];
+        uint4 raw[kMT][2];
 #pragma unroll
-        for (int j = 0; j < kNJ; ++j)
-          raw[j] = lds128(slot + 16 * k_place<kRow>(8 * j + g, 4 * sg + t));
+        for (int j = 0; j < kMT; ++j)
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            raw[j][q] = lds128(slot + 16 * k_place<kRow>(16 * j + 8 * q + g, 4 * sg + t));
 #pragma unroll
         for (int u = 0; u < kVec / 4; ++u) {
-          uint32_t b0[kNJ], b1[kNJ];
+          uint32_t a[kMT][4];
 #pragma unroll
-          for (int j = 0; j < kNJ; ++j) {
-            const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-            if (kHalf) {
-              widen<kKind>(w[u], b0[j], b1[j]);
-            } else {
-              b0[j] = w[(2 * u) & 3];
-              b1[j] = w[(2 * u + 1) & 3];
+          for (int j = 0; j < kMT; ++j)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const uint32_t w[4] = {raw[j][q].x, raw[j][q].y, raw[j][q].z, raw[j][q].w};
+              if (kHalf) {
+                widen<kKind>(w[u], a[j][q], a[j][2 + q]);
+              } else {
+                a[j][q] = w[(2 * u) & 3];
+                a[j][2 + q] = w[(2 * u + 1) & 3];
+              }
             }
-          }
 #pragma unroll
-          for (int p = 0; p < kQT; ++p) {
-            const uint4 a = *reinterpret_cast<const uint4 *>(
-                qs + (((sg * (kVec / 4) + u) * kQT + p) * 32 + lane) * 4);
+          for (int p = 0; p < kQP; ++p)
 #pragma unroll
-            for (int j = 0; j < kNJ; ++j) mma<kHalf>(s[j], a, b0[j], b1[j]);
-          }
+            for (int i = 0; i < R; ++i) {
+              const uint2 bq = reinterpret_cast<const uint2 *>(
+                  qs)[(((sg * (kVec / 4) + u) * kQP + p) * R + i) * 32 + lane];
+#pragma unroll
+              for (int j = 0; j < kMT; ++j)
+                mma<kHalf>(s[j][i], a[j][0], a[j][1], a[j][2], a[j][3], bq);
+            }
         }
       }
-      // ---- their maximum, weights and sums
-      float x[R][kNJ][2], vs[kNJ][2], top[R];
+      // ---- their maximum, weights and sums: a lane has positions g and g + 8
+      // of 16, rows 2 t and 2 t + 1 of 8
+      float vs[kMT][2], top[R][2];
 #pragma unroll
-      for (int i = 0; i < R; ++i) top[i] = kNone;
+      for (int i = 0; i < R; ++i) top[i][0] = top[i][1] = kNone;
 #pragma unroll
-      for (int j = 0; j < kNJ; ++j) {
-        float2 ks = make_float2(1.0f, 1.0f), lv = make_float2(0.0f, 0.0f);
-        if (kHalf) {
-          const uint2 a = lds64(slot + Z::kUnit + 4 * (8 * j + 2 * t));
-          const uint2 v = lds64(slot + Z::kUnit + 4 * kTT + 4 * (8 * j + 2 * t));
-          ks = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
-          vs[j][0] = __uint_as_float(v.x);
-          vs[j][1] = __uint_as_float(v.y);
-          lv = make_float2(rough_log2(vs[j][0]) - 12.0f, rough_log2(vs[j][1]) - 12.0f);
-        }
+      for (int j = 0; j < kMT; ++j)
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-          const float s0 = R == 1 ? s[j][0] + s[j][2] : s[j][2 * i];
-          const float s1 = R == 1 ? s[j][1] + s[j][3] : s[j][2 * i + 1];
-          x[i][j][0] = s0 * (fac[i] * ks.x);
-          x[i][j][1] = s1 * (fac[i] * ks.y);
-          if (masked) {
-            const int at = pos + 8 * j + 2 * t;
-            if (at >= lim[i] || at >= len) x[i][j][0] = -INFINITY;
-            if (at + 1 >= lim[i] || at + 1 >= len) x[i][j][1] = -INFINITY;
+        for (int q = 0; q < 2; ++q) {
+          const int at = 16 * j + 8 * q + g;
+          float ks = 1.0f, lv = 0.0f;
+          if (kHalf) {
+            const float *sc = reinterpret_cast<const float *>(
+                smem + Sh::kRingAt + (warp * kSlots + get) * Z::kSlot + Z::kUnit);
+            ks = sc[at];
+            vs[j][q] = sc[kTT + at];
+            lv = rough_log2(vs[j][q]) - kUp;
           }
-          top[i] = fmaxf(top[i], fmaxf(x[i][j][0] + lv.x, x[i][j][1] + lv.y));
+#pragma unroll
+          for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = s[j][i][2 * q + e] * (fac[i][e] * ks);
+              if (masked && (pos + at >= lim[i][e] || pos + at >= len)) x = -INFINITY;
+              s[j][i][2 * q + e] = x;
+              top[i][e] = fmaxf(top[i][e], x + lv);
+            }
         }
-      }
       bool grown = false;
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        top[i] = fmaxf(top[i], __shfl_xor_sync(kFull, top[i], 1));
-        top[i] = fmaxf(top[i], __shfl_xor_sync(kFull, top[i], 2));
-        grown |= top[i] > m[i] + kSlack;
-      }
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float &x = top[i][e];
+          x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
+          grown |= x > m[i][e] + kSlack;
+        }
       if (__any_sync(kFull, grown)) {
-        float a[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-          const float to = top[i] > m[i] + kSlack ? top[i] : m[i];
-          a[i] = exp2_(m[i] - to);
-          m[i] = to;
-          l[i] *= a[i];
-        }
+          float a[2];
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
-          acc[i][0] *= a[0];
-          acc[i][1] *= a[0];
-          acc[i][2] *= a[R - 1];
-          acc[i][3] *= a[R - 1];
-        }
-      }
-      uint4 w[kTT / 16][kPT];
-#pragma unroll
-      for (int kk = 0; kk < kTT / 16; ++kk) {
-        uint32_t pr[R][2][kPP];
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int j = 2 * kk + q;
-            float p0 = exp2_(x[i][j][0] - m[i]), p1 = exp2_(x[i][j][1] - m[i]);
-            float w0 = kHalf ? p0 * vs[j][0] : p0, w1 = kHalf ? p1 * vs[j][1] : p1;
-            if (masked) {  // (a masked scale or key may be anything)
-              const int at = pos + 8 * j + 2 * t;
-              if (at >= lim[i] || at >= len) p0 = w0 = 0.0f;
-              if (at + 1 >= lim[i] || at + 1 >= len) p1 = w1 = 0.0f;
-            }
-            l[i] += p0 + p1;
-            cut<kHalf, kPP>(w0, w1, pr[i][q]);
+          for (int e = 0; e < 2; ++e) {
+            const float to = top[i][e] > m[i][e] + kSlack ? top[i][e] : m[i][e];
+            a[e] = exp2_(m[i][e] - to);
+            m[i][e] = to;
+            l[i][e] *= a[e];
           }
 #pragma unroll
-        for (int p = 0; p < kPT; ++p) {
-          if (R == 1)
-            w[kk][p] = make_uint4(pr[0][0][2 * p], 2 * p + 1 < kPP ? pr[0][0][(2 * p + 1) % kPP] : 0u,
-                                  pr[0][1][2 * p], 2 * p + 1 < kPP ? pr[0][1][(2 * p + 1) % kPP] : 0u);
-          else
-            w[kk][p] = make_uint4(pr[0][0][p], pr[R - 1][0][p], pr[0][1][p], pr[R - 1][1][p]);
+          for (int d = 0; d < kDT; ++d)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[d][i][k] *= a[k & 1];
         }
       }
+      uint2 w[kMT][R][kPP];
+#pragma unroll
+      for (int j = 0; j < kMT; ++j)
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          uint32_t pr[2][kPP];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            float y[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float p = exp2_(s[j][i][2 * q + e] - m[i][e]);
+              y[e] = kHalf ? p * vs[j][q] : p;
+              if (masked) {  // (a masked scale or key may be anything)
+                const int at = pos + 16 * j + 8 * q + g;
+                if (at >= lim[i][e] || at >= len) p = y[e] = 0.0f;
+              }
+              l[i][e] += p;
+            }
+            cut<kHalf, kPP>(y[0], y[1], pr[q]);
+          }
+#pragma unroll
+          for (int p = 0; p < kPP; ++p)
+            w[j][i][p] = make_uint2(transposed(pr[0][p]), transposed(pr[1][p]));
+        }
       if (broken) {
         if (P.err) *P.err = 1;
 #pragma unroll
-        for (int i = 0; i < R; ++i) l[i] = __uint_as_float(0x7fc00000u);
+        for (int i = 0; i < R; ++i) l[i][0] = l[i][1] = __uint_as_float(0x7fc00000u);
       }
       get = get + 1 == kSlots ? 0 : get + 1;
 
-      // ---- the sums over v
+      // ---- the sums over v: 16 channels by 8 rows a product
       wait_for<kSlots - 2>();
       __syncwarp();
       issue();
@@ -661,60 +713,60 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind>::kCtas)
                          : "memory");
 #pragma unroll
           for (int i = 0; i < R; ++i)
-            if (pos + r < lim[i]) l[i] = __uint_as_float(0x7fc00000u);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (pos + r < lim[i][e]) l[i][e] = __uint_as_float(0x7fc00000u);
         }
         __syncwarp();
       }
-      if (kKind == kKvBf16) {
 #pragma unroll
-        for (int kk = 0; kk < kTT / 16; ++kk)
+      for (int j = 0; j < kMT; ++j) {
+        if (kKind == kKvBf16) {
 #pragma unroll
-          for (int i = 0; i < kTiles / 2; ++i) {
-            uint32_t v0, v1, v2, v3;
-            const int r = 16 * kk + (lane & 15), cc = 2 * i + (lane >> 4);
+          for (int d = 0; d < kDT; ++d) {
+            uint32_t a0, a1, a2, a3;
+            const int r = 16 * j + (lane & 7) + 8 * (lane >> 4), cc = 2 * d + (lane >> 3 & 1);
             asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(v0), "=r"(v1), "=r"(v2), "=r"(v3)
+                         : "=r"(a0), "=r"(a1), "=r"(a2), "=r"(a3)
                          : "r"(slot + 16 * v_place<kRow, true>(r, cc)));
 #pragma unroll
-            for (int p = 0; p < kPT; ++p) {
-              mma<false>(acc[2 * i], w[kk][p], v0, v1);
-              mma<false>(acc[2 * i + 1], w[kk][p], v2, v3);
-            }
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+              for (int p = 0; p < kPP; ++p) mma<false>(acc[d][i], a0, a1, a2, a3, w[j][i][p]);
           }
-      } else {
-        // four positions a lane, 16 channels of each (8 of 64): bytes of
-        // neighbouring positions side by side make the pairs of an operand
-        constexpr int kWords = kHd == 64 ? 2 : 4;
+        } else {
+          // four positions a lane, 16 channels of each (8 of 64): bytes of
+          // neighbouring positions side by side make the pairs of an operand
+          constexpr int kWords = kHd == 64 ? 2 : 4;
 #pragma unroll
-        for (int kk = 0; kk < kTT / 16; ++kk)
-#pragma unroll
-          for (int i = 0; i < (kHd == 256 ? 2 : 1); ++i) {
+          for (int half = 0; half < (kHd == 256 ? 2 : 1); ++half) {
             uint32_t e[4][4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const int r = 16 * kk + 2 * t + (q & 1) + 8 * (q >> 1);
+              const int r = 16 * j + 2 * t + (q & 1) + 8 * (q >> 1);
               if (kHd == 64) {
                 const uint2 v = lds64(slot + 16 * v_place<kRow, false>(r, g >> 1) + 8 * (g & 1));
                 e[q][0] = v.x; e[q][1] = v.y;
               } else {
-                const uint4 v = lds128(slot + 16 * v_place<kRow, false>(r, g + 8 * i));
+                const uint4 v = lds128(slot + 16 * v_place<kRow, false>(r, g + 8 * half));
                 e[q][0] = v.x; e[q][1] = v.y; e[q][2] = v.z; e[q][3] = v.w;
               }
             }
 #pragma unroll
-            for (int k = 0; k < kWords; ++k) {
-              uint32_t b0[4], b1[4];
-              widen<kKind>(prmt(e[0][k], e[1][k], 0x5140), b0[0], b0[1]);
-              widen<kKind>(prmt(e[0][k], e[1][k], 0x7362), b0[2], b0[3]);
-              widen<kKind>(prmt(e[2][k], e[3][k], 0x5140), b1[0], b1[1]);
-              widen<kKind>(prmt(e[2][k], e[3][k], 0x7362), b1[2], b1[3]);
+            for (int k = 0; k < kWords; ++k)
 #pragma unroll
-              for (int q = 0; q < 4; ++q)
+              for (int q = 0; q < 2; ++q) {
+                uint32_t a[4];
+                widen<kKind>(prmt(e[0][k], e[1][k], q ? 0x7362 : 0x5140), a[0], a[1]);
+                widen<kKind>(prmt(e[2][k], e[3][k], q ? 0x7362 : 0x5140), a[2], a[3]);
 #pragma unroll
-                for (int p = 0; p < kPT; ++p)
-                  mma<true>(acc[16 * i + 4 * k + q], w[kk][p], b0[q], b1[q]);
-            }
+                for (int i = 0; i < R; ++i)
+#pragma unroll
+                  for (int p = 0; p < kPP; ++p)
+                    mma<true>(acc[8 * half + 2 * k + q][i], a[0], a[1], a[2], a[3], w[j][i][p]);
+              }
           }
+        }
       }
       get = get + 1 == kSlots ? 0 : get + 1;
     }
@@ -724,84 +776,90 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind>::kCtas)
     const bool whole = c0 == 0 && n == here.n;
     here.left -= n;
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      l[i] += __shfl_xor_sync(kFull, l[i], 1);
-      l[i] += __shfl_xor_sync(kFull, l[i], 2);
-      if (t == 0) stat[warp * 16 + g + 8 * i] = make_float2(m[i], any ? l[i] : 0.0f);
-    }
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float &x = l[i][e];
+        x += __shfl_xor_sync(kFull, x, 4);
+        x += __shfl_xor_sync(kFull, x, 8);
+        x += __shfl_xor_sync(kFull, x, 16);
+        if (g == 0) stat[warp * 8 * R + 8 * i + 2 * t + e] = make_float2(m[i][e], x);
+      }
     const int mine = get == 0 ? kSlots - 1 : get - 1;
-    float4 *const own = reinterpret_cast<float4 *>(smem + Sh::kRingAt) +
-                        (warp * kSlots + mine) * (Z::kSlot / 16);
+    if (lane == 0) rooms[warp] = any ? (signed char)mine : (signed char)-1;
+    float *const own = reinterpret_cast<float *>(smem + Sh::kRingAt + (warp * kSlots + mine) * Z::kSlot);
     // 16-byte unit q of a row of fp32 sums
-    auto unit = [](int r, int q) { return r * (kHd / 4) + (q ^ (((q >> 3) ^ (r << 2)) & 7)); };
+    constexpr int kStage = Z::kStage, kRounds = kHd / kStage;
+    auto unit = [](int r, int q) { return r * (kStage / 4) + (q ^ (((q >> 2) ^ (q >> 5) ^ r) & 7)); };
     __syncwarp();
-    int *const slots = found + 4;  // [8] bytes: the warps' rooms, -1: nothing
-    if (lane == 0) reinterpret_cast<signed char *>(slots)[warp] = any ? (signed char)mine : -1;
     float *const part =
         P.part + ((size_t)blockIdx.x * 2 + (c0 == 0 ? 1 : 0)) * (8 * R) * (kHd + 4);
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      if (any) {
-        if (kKind == kKvBf16) {
+    for (int i = 0; i < R; ++i)
 #pragma unroll
-          for (int q = 0; q < kTiles; ++q) {
-            const float a = R == 1 ? acc[q][0] + acc[q][2] : acc[q][2 * i];
-            const float d = R == 1 ? acc[q][1] + acc[q][3] : acc[q][2 * i + 1];
-            *(reinterpret_cast<float2 *>(own + unit(g, 2 * q + t / 2)) + (t & 1)) = make_float2(a, d);
+      for (int rd = 0; rd < kRounds; ++rd) {
+        if (any) {
+          if (kKind == kKvBf16) {
+#pragma unroll
+            for (int d = 0; d < kStage / 16; ++d)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int ch = 16 * d + g + 8 * (k >> 1);
+                own[4 * unit(2 * t + (k & 1), ch / 4) + (ch & 3)] = acc[rd * (kStage / 16) + d][i][k];
+              }
+          } else {
+            // tile 8 half + j: channels 128 half + kRun g + 2 j and 2 j + 1
+            constexpr int kRun = kHd == 64 ? 8 : 16;
+            static_assert(kStage == kHd || kStage == 128, "a round is a half of 256 channels");
+#pragma unroll
+            for (int d = 0; d < kStage / 16; d += 2)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int tile = rd * (kStage / 16) + d;
+                const int ch = (kHd == 256 ? 128 * (d / 8) : 0) + kRun * g + 2 * (d % 8);
+                *reinterpret_cast<float4 *>(own + 4 * unit(2 * t + e, ch / 4)) =
+                    make_float4(acc[tile][i][e], acc[tile][i][2 + e], acc[tile + 1][i][e],
+                                acc[tile + 1][i][2 + e]);
+              }
           }
-        } else {
-          constexpr int kRun = kHd == 64 ? 8 : 16;  // channels side by side of a lane
+        }
+        __syncthreads();
+        for (int q = tid; q < 8 * (kStage / 4); q += kThreads) {
+          const int r8 = q / (kStage / 4), cq = q % (kStage / 4), r = r8 + 8 * i, row = row0 + r;
+          if (r >= rows) continue;
+          float top = kNone, sum = 0.0f;
 #pragma unroll
-          for (int q = 0; q < kTiles / 4; ++q) {
-            const int blk = 4 * q / kRun, e = 4 * q % kRun;
-            float a[4], d[4];
+          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w * 8 * R + r].x);
+          float o[4] = {};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              a[k] = R == 1 ? acc[4 * q + k][0] + acc[4 * q + k][2] : acc[4 * q + k][2 * i];
-              d[k] = R == 1 ? acc[4 * q + k][1] + acc[4 * q + k][3] : acc[4 * q + k][2 * i + 1];
-            }
-            const int at = (128 * blk + 2 * t * kRun + e) / 4;
-            own[unit(g, at)] = make_float4(a[0], a[1], a[2], a[3]);
-            own[unit(g, at + kRun / 4)] = make_float4(d[0], d[1], d[2], d[3]);
+          for (int w = 0; w < kWarps; ++w) {
+            const int sl = rooms[w];
+            if (sl < 0) continue;
+            const float2 ml = stat[w * 8 * R + r];
+            const float f = exp2_(ml.x - top);
+            sum += ml.y * f;
+            const float4 v = reinterpret_cast<const float4 *>(
+                smem + Sh::kRingAt + (w * kSlots + sl) * Z::kSlot)[unit(r8, cq)];
+            o[0] += v.x * f; o[1] += v.y * f; o[2] += v.z * f; o[3] += v.w * f;
+          }
+          const int ch = rd * kStage + 4 * cq;
+          if (whole) {
+            const int mt = row / P.group, head = h * P.group + row - mt * P.group;
+            const size_t at = ((size_t)b * P.M + mt) * P.qh + head;
+            if (mt + start >= len) continue;  // a token that the sequence has not
+            const float inv = 1.0f / sum;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] *= inv;
+            store4(static_cast<T *>(P.o) + at * kHd + ch, o);
+            if (P.lse && ch == 0) P.lse[at] = (top + log2f(sum)) * 0.693147180559945f;
+          } else {
+            float *to = part + (size_t)r * (kHd + 4);
+            store4(to + ch, o);
+            if (ch == 0) *reinterpret_cast<float2 *>(to + kHd) = make_float2(top, sum);
           }
         }
+        __syncthreads();
       }
-      __syncthreads();
-      for (int q = tid; q < 8 * (kHd / 4); q += kThreads) {
-        const int r = q / (kHd / 4), cq = q % (kHd / 4), row = row0 + r + 8 * i;
-        if (r + 8 * i >= rows) continue;
-        float top = kNone, sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w * 16 + r + 8 * i].x);
-        float o[4] = {};
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const int sl = reinterpret_cast<const signed char *>(slots)[w];
-          if (sl < 0) continue;
-          const float2 ml = stat[w * 16 + r + 8 * i];
-          const float f = exp2_(ml.x - top);
-          sum += ml.y * f;
-          const float4 v = reinterpret_cast<const float4 *>(
-              smem + Sh::kRingAt)[(w * kSlots + sl) * (Z::kSlot / 16) + unit(r, cq)];
-          o[0] += v.x * f; o[1] += v.y * f; o[2] += v.z * f; o[3] += v.w * f;
-        }
-        if (whole) {
-          const int mt = row / P.group, head = h * P.group + row - mt * P.group;
-          const size_t at = ((size_t)b * P.M + mt) * P.qh + head;
-          if (mt + start >= len) continue;  // a token that the sequence has not
-          const float inv = 1.0f / sum;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) o[k] *= inv;
-          store4(static_cast<T *>(P.o) + at * kHd + 4 * cq, o);
-          if (P.lse && cq == 0) P.lse[at] = (top + log2f(sum)) * 0.693147180559945f;
-        } else {
-          float *to = part + (size_t)(r + 8 * i) * (kHd + 4);
-          store4(to + 4 * cq, o);
-          if (cq == 0) *reinterpret_cast<float2 *>(to + kHd) = make_float2(top, sum);
-        }
-      }
-      __syncthreads();
-    }
     here.c += n;
     if (here.left > 0) next_item(here);
   }
@@ -813,14 +871,14 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind>::kCtas)
 template <int kHd, int kKind, bool kBf16, int R>
 __global__ void __launch_bounds__(kThreads)
     attn_join_kernel(const AttnArgs P, int grid) {
-  using Z = Sizes<kHd, kKind>;
+  using Z = Sizes<kHd, kKind, R>;
   using T = typename std::conditional<kBf16, __nv_bfloat16, float>::type;
   constexpr int kQ = kHd / 4, kGroups = kThreads / kQ;
   __shared__ long long room[2 * kWarps];
   __shared__ float4 sums[kGroups][kQ];
   __shared__ float tops[kGroups], ls[kGroups];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // (what came before attn_kernel has ended, and attn_kernel writes no lengths:
+  // they may be read beside it)
   const int tid = threadIdx.x, rows = P.M * P.group;
   const int nrt = (rows + 8 * R - 1) / (8 * R), items = P.c.kvh * nrt;
   const int row = blockIdx.x % rows, h = blockIdx.x / rows % P.c.kvh;
@@ -841,6 +899,8 @@ __global__ void __launch_bounds__(kThreads)
   const long long u = before * items + (long long)n * (h * nrt + row / (8 * R));
   const int i0 = share.of(u), i1 = share.of(u + n - 1);
   if (i0 == i1) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int q = tid % kQ, group = tid / kQ;
   const float *part = P.part + (size_t)(row % (8 * R)) * (kHd + 4);
   constexpr size_t kStep = (size_t)(8 * R) * (kHd + 4);
@@ -894,9 +954,8 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // CTAs of a call: at most one share each for the longest that the table holds.
-template <int kHd, int kKind>
+template <class Z>
 int grid_of(int B, int M, int group, int kvh, int R, long long room) {
-  using Z = Sizes<kHd, kKind>;
   const long long nrt = (M * group + 8 * R - 1) / (8 * R);
   const long long most = (room + Z::kChunk - 1) / Z::kChunk * nrt * kvh * B;
   const int all = kSms * Z::kCtas;
@@ -905,11 +964,11 @@ int grid_of(int B, int M, int group, int kvh, int R, long long room) {
 
 template <int kHd, int kKind, bool kBf16, int R>
 cudaError_t go(const AttnArgs &P, cudaStream_t stream) {
-  using Z = Sizes<kHd, kKind>;
+  using Z = Sizes<kHd, kKind, R>;
   using Sh = Shared<kHd, kKind, kBf16, R>;
   static_assert(Sh::kBytes * Z::kCtas <= 227 * 1024 - 1024 * (Z::kCtas - 1), "shared memory");
-  static_assert(Z::kSlots >= 3 && 8 * kHd * 4 <= Z::kSlot, "rings");
-  const int grid = grid_of<kHd, kKind>(P.B, P.M, P.group, P.c.kvh, R,
+  static_assert(Z::kSlots >= 3 && 32 * Z::kStage <= Z::kSlot, "rings");
+  const int grid = grid_of<Z>(P.B, P.M, P.group, P.c.kvh, R,
                                        (long long)P.cols << P.c.page_shift);
   const long long rows = (long long)P.B * P.M * P.qh;
   if (rows > 0x7fffffffll) return cudaErrorInvalidConfiguration;
@@ -934,7 +993,7 @@ cudaError_t go(const AttnArgs &P, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, attn_join_kernel<kHd, kKind, kBf16, R>, P, grid);
 }
 
-// Up to 8 rows of an item share a tile with their second parts.
+// Row tiles of 8 or 16.
 inline int tile_rows(int M, int group) { return (long long)M * group <= 8 ? 1 : 2; }
 
 template <int kHd, int kKind>
@@ -953,9 +1012,9 @@ cudaError_t launch(const AttnArgs &P, bool bf16, cudaStream_t stream) {
 
 // Bytes of the parts: two for each CTA.
 template <int kHd>
-size_t bytes(int kind, int M, int group) {
+size_t bytes(int M, int group) {
   const int R = tile_rows(M, group);
-  const int ctas = kSms * (kind == kKvBf16 ? Sizes<kHd, kKvBf16>::kCtas : Sizes<kHd, kKvInt8>::kCtas);
+  const int ctas = kSms * (R == 1 ? Sizes<kHd, kKvInt8, 1>::kCtas : Sizes<kHd, kKvInt8, 2>::kCtas);
   return (size_t)ctas * 2 * (8 * R) * (kHd + 4) * 4;
 }
 

@@ -135,13 +135,16 @@ def attn_bounds(kind, dtype, hd, T, o, lse, mag, big):
     magnitudes `big`), the operands' cut 2^-22, scales, factor and the base-2
     exponent's rounding 4 x 2^-23; ex2.approx 2^-22.  A weight's relative error
     is that of its score; it enters the sum and the normaliser: twice.  The
-    weights' cut: 2^-21 (bf16 tokens on a bf16 cache, two 8-bit parts: 2^-16);
+    weights' cut: 2^-21 (bf16 tokens: on a bf16 cache two 8-bit parts, 2^-16, on an 8-bit
+    one a single fp16, 2^-11);
     sums of T / 16 products over 8 warps and at most a few parts, in fp32, and
     the joins: (T / 128 + 40) 2^-23.  bf16 results: half a step, 2^-8, once."""
     d = (hd / 16 + 6) * 2.0 ** -23 * big + 2.0 ** -22
     tol = 2 * d + (T / 128 + 40) * 2.0 ** -23 + 2.0 ** -21
     if kind == "bf16" and dtype == "bf16":
         tol = tol + 2.0 ** -16
+    if kind != "bf16" and dtype == "bf16":
+        tol = tol + 2.0 ** -11
     bo = tol[..., None] * mag
     if dtype == "bf16":
         bo = bo * (1 + 2.0 ** -8) + 2.0 ** -8 * o.abs()
