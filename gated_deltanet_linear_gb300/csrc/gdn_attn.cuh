@@ -69,7 +69,8 @@ struct Sizes {
   static constexpr int kRow = kHd * kBytes;               // bytes of a row
   // CTAs an SM: a lane has kHd R / 4 sums, and three slots a warp are wanted
   static constexpr int kCtas = kHd * R > 256 || kRow > 256 ? 1 : 2;
-  static constexpr int kTT = kRow <= 128 ? 32 : 16;       // positions of a tile
+  // positions of a tile (32 of 128 channels and 16 rows would not fit the registers)
+  static constexpr int kTT = kRow <= 128 && kHd * R <= 128 ? 32 : 16;
   static constexpr int kUnit = kTT * kRow;                // K or V of a tile
   static constexpr int kSlot = kUnit + (kKind == kKvBf16 ? 0 : 8 * kTT);  // and scales
   static constexpr int kRing = kCtas == 1 ? 25 * 1024 + 512 : 13 * 1024;  // a warp's ring
@@ -110,6 +111,9 @@ __device__ __forceinline__ void cp16(uint32_t to, const void *from, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from),
                "r"(on ? 16 : 0)
                : "memory");
+}
+__device__ __forceinline__ void cp16(uint32_t to, const void *from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int n>
@@ -162,24 +166,36 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   return y;
 }
 
-// Four codes as two pairs of fp16.
+// Four codes as two pairs of fp16: bytes 0 and 2, 1 and 3 (e4m3: 0 and 1, 2 and 3).
 template <int kKind>
-__device__ __forceinline__ void widen(uint32_t w, uint32_t &lo, uint32_t &hi) {
+__device__ __forceinline__ void widen(uint32_t w, uint32_t &even, uint32_t &odd) {
   if (kKind == kKvInt8) {
     // u = code + 128 behind the bits of 1024, which is 1024 + u; less 1152
-    w ^= 0x80808080u;
-    lo = prmt(w, 0x64646464u, 0x4140);
-    hi = prmt(w, 0x64646464u, 0x4342);
+    even = (w & 0x00ff00ffu) ^ 0x64806480u;
+    odd = ((w >> 8) & 0x00ff00ffu) ^ 0x64806480u;
     const __half2 off = __half2(__half_raw{0x6480}, __half_raw{0x6480});
-    __half2 a = __hsub2(*reinterpret_cast<__half2 *>(&lo), off);
-    __half2 b = __hsub2(*reinterpret_cast<__half2 *>(&hi), off);
-    lo = *reinterpret_cast<uint32_t *>(&a);
-    hi = *reinterpret_cast<uint32_t *>(&b);
+    __half2 a = __hsub2(*reinterpret_cast<__half2 *>(&even), off);
+    __half2 b = __hsub2(*reinterpret_cast<__half2 *>(&odd), off);
+    even = *reinterpret_cast<uint32_t *>(&a);
+    odd = *reinterpret_cast<uint32_t *>(&b);
+  } else {
+    asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\n"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\ncvt.rn.f16x2.e4m3x2 %1, h;\n}"
+        : "=r"(even), "=r"(odd)
+        : "r"(w));
+  }
+}
+// The same of two words, the pairs' first numbers from the first: bytes k and
+// k + 1 (k = 0 or 2) of both.
+template <int kKind>
+__device__ __forceinline__ void widen2(uint32_t v, uint32_t w, int k, uint32_t &lo, uint32_t &hi) {
+  if (kKind == kKvInt8) {
+    widen<kKind>(prmt(v, w, k ? 0x7632 : 0x5410), lo, hi);
   } else {
     asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\n"
         "cvt.rn.f16x2.e4m3x2 %0, l;\ncvt.rn.f16x2.e4m3x2 %1, h;\n}"
         : "=r"(lo), "=r"(hi)
-        : "r"(w));
+        : "r"(prmt(v, w, k ? 0x7362 : 0x5140)));
   }
 }
 
@@ -254,15 +270,24 @@ __device__ __forceinline__ void block_sums(long long &x, long long &y, long long
   }
 }
 
-// Where a 16-byte unit of a row lies in a tile (see the reads).
+// Where a 16-byte unit of a row lies in a tile: in its row (rows of 64 bytes of
+// V: in its pair of rows), permuted by an exclusive or with bits of the row, so
+// that the reads meet no bank twice.
+template <int kRow>
+__host__ __device__ constexpr int k_twist(int r) {
+  return kRow == 64 ? 0 : (r & 1) << 2;
+}
+template <int kRow, bool kBf16Cache>
+__host__ __device__ constexpr int v_twist(int r) {
+  return kBf16Cache ? r & 7 : ((r >> 1) & 3) << 1;
+}
 template <int kRow>
 __device__ __forceinline__ int k_place(int r, int c) {
-  return kRow == 64 ? r * 4 + c : r * (kRow / 16) + (c ^ ((r & 1) << 2));
+  return r * (kRow / 16) + (c ^ k_twist<kRow>(r));
 }
 template <int kRow, bool kBf16Cache>
 __device__ __forceinline__ int v_place(int r, int c) {
-  if (kRow == 64) return (r >> 1) * 8 + ((((r & 1) << 2) + c) ^ (((r >> 1) & 3) << 1));
-  return r * (kRow / 16) + (kBf16Cache ? c ^ (r & 7) : c ^ (((r >> 1) & 3) << 1));
+  return (r * (kRow / 16) + c) ^ v_twist<kRow, kBf16Cache>(r);
 }
 
 template <int kHd, int kKind, bool kBf16, int R>
@@ -399,10 +424,12 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
   constexpr int kIters = kTT * kCpr / 32;     // of a lane, for K or V of a tile
   constexpr int kPerPage = kIters / kMT;      // 16 positions lie in one page, one run
   static_assert(kIters % kMT == 0, "a lane's unit lies in one page");
+  const uint32_t k_lane = 16 * k_place<kRow>(lane / kCpr, lane % kCpr);
+  const uint32_t v_lane = 16 * v_place<kRow, kKind == kKvBf16>(lane / kCpr, lane % kCpr);
   const int page_mask = (1 << P.c.page_shift) - 1;
   uint32_t bad = 0;            // slots with a page that is not there
   int put = 0;                 // the slot of the next unit
-  bool v_next = false;         // the unit is V of the tile whose K went before
+  bool begun = false;          // K of a tile is under way, its V comes next
   bool full = false;           // all of the tile's positions and pages are there
   long long row_at[kMT];       // the tile's first rows in the cache, -1: none
   int rows_on = 0;             // positions of the tile that are there
@@ -421,8 +448,9 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
       }
     }
   };
-  auto issue = [&]() {
-    if (ahead.left > 0 || v_next) {
+  auto issue = [&](auto which_unit) {  // K of the next tile, or V of it
+    constexpr bool v_next = decltype(which_unit)::value;
+    if (v_next ? begun : ahead.left > 0) {
       const uint32_t slot = ring + put * Z::kSlot;
       if (!v_next) {
         const int pos = (ahead.c * kWarps + warp) * kTT;
@@ -444,14 +472,25 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
       const unsigned char *from = static_cast<const unsigned char *>(v_next ? P.c.v : P.c.k);
 #pragma unroll
       for (int half = 0; half < kMT; ++half) {
-        const unsigned char *src =
-            from + (row_at[half] < 0 ? (size_t)0 : (size_t)row_at[half] * kRow) + 16 * lane;
+        const unsigned char *src = from + (size_t)max(row_at[half], 0ll) * kRow + 16 * lane;
+        // (a step's rows and the lane's row within it have no bit in common, so
+        // their twists add up to the row's)
+        auto place = [&](int j) {
+          const int step = half * kPerPage + j, r = step * (32 / kCpr);
+          return slot + 512 * step +
+                 (v_next ? v_lane ^ (16 * v_twist<kRow, kKind == kKvBf16>(r))
+                         : k_lane ^ (16 * k_twist<kRow>(r)));
+        };
+        if (full) {
 #pragma unroll
-        for (int j = 0; j < kPerPage; ++j) {
-          const int u = 32 * (half * kPerPage + j) + lane, r = u / kCpr, c = u % kCpr;
-          const int to = v_next ? v_place<kRow, kKind == kKvBf16>(r, c) : k_place<kRow>(r, c);
-          const bool on = full || (row_at[half] >= 0 && r < rows_on);
-          cp16(slot + 16 * to, on ? src + 512 * j : from, on);
+          for (int j = 0; j < kPerPage; ++j) cp16(place(j), src + 512 * j);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kPerPage; ++j) {
+            const int r = (32 * (half * kPerPage + j) + lane) / kCpr;
+            const bool on = row_at[half] >= 0 && r < rows_on;
+            cp16(place(j), on ? src + 512 * j : from, on);
+          }
         }
       }
       if (kKind != kKvBf16 && !v_next && lane < 2 * kTT / 4) {  // both scales, with K
@@ -462,14 +501,21 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
         cp16(slot + Z::kUnit + 16 * lane, s + (on ? (size_t)(at + (r & 15)) : (size_t)0), on);
       }
       if (v_next) seek();
-      v_next = !v_next;
+      begun = !v_next;
       put = put + 1 == kSlots ? 0 : put + 1;
     }
     commit();
   };
+  constexpr std::false_type kK{};
+  constexpr std::true_type kV{};
   seek();
 #pragma unroll
-  for (int i = 0; i < kSlots - 1; ++i) issue();
+  for (int i = 0; i < kSlots - 1; ++i) {
+    if (i & 1)
+      issue(kV);
+    else
+      issue(kK);
+  }
 
   float acc[kDT][R][4];
   float m[R][2], l[R][2];
@@ -523,8 +569,10 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
           // channels d .. d + 3: product ks, lane 4 (r % 8) + tq, both pairs
           const int ks = d / (4 * kVec) * (kVec / 4) + d % kVec / 4, tq = d / kVec % 4;
           uint32_t a[kQP], c[kQP];
-          cut<kHalf, kQP>(x[e][0], x[e][1], a);
-          cut<kHalf, kQP>(x[e][2], x[e][3], c);
+          // (int8 codes come out as bytes 0 and 2, 1 and 3)
+          constexpr int k1 = kKind == kKvInt8 ? 2 : 1, k2 = 3 - k1;
+          cut<kHalf, kQP>(x[e][0], x[e][k1], a);
+          cut<kHalf, kQP>(x[e][k2], x[e][3], c);
 #pragma unroll
           for (int p = 0; p < kQP; ++p)
             reinterpret_cast<uint2 *>(qs)[((ks * kQP + p) * R + i) * 32 + 4 * (r & 7) + tq] =
@@ -559,10 +607,13 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
       // ---- scores of the tile: 16 positions by 8 rows a product
       wait_for<kSlots - 2>();
       __syncwarp();
-      issue();
+      issue(std::bool_constant<(kSlots - 1) % 2 == 1>{});
       uint32_t slot = ring + get * Z::kSlot;
       const bool broken = bad >> get & 1;
-      float s[kMT][R][4] = {};
+      // (several sums where there are few: a product waits for the last one of
+      // its sum)
+      constexpr int kC = kMT * R <= 2 ? 2 : 1;
+      float part[kC][kMT][R][4] = {};
 #pragma unroll
       for (int sg = 0; sg < kHd / (4 * kVec); ++sg) {
         uint4 raw[kMT][2];
@@ -594,37 +645,71 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
                   qs)[(((sg * (kVec / 4) + u) * kQP + p) * R + i) * 32 + lane];
 #pragma unroll
               for (int j = 0; j < kMT; ++j)
-                mma<kHalf>(s[j][i], a[j][0], a[j][1], a[j][2], a[j][3], bq);
+                mma<kHalf>(part[(kQP > 1 ? p : u) % kC][j][i], a[j][0], a[j][1], a[j][2], a[j][3], bq);
             }
         }
       }
       // ---- their maximum, weights and sums: a lane has positions g and g + 8
       // of 16, rows 2 t and 2 t + 1 of 8
-      float vs[kMT][2], top[R][2];
+      float (&s)[kMT][R][4] = part[0];
+      if (kC == 2) {
 #pragma unroll
-      for (int i = 0; i < R; ++i) top[i][0] = top[i][1] = kNone;
+        for (int j = 0; j < kMT; ++j)
+#pragma unroll
+          for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[j][i][k] += part[kC - 1][j][i][k];
+      }
+      float vs[kMT][2], lv[kMT][2], top[R][2];
 #pragma unroll
       for (int j = 0; j < kMT; ++j)
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const int at = 16 * j + 8 * q + g;
-          float ks = 1.0f, lv = 0.0f;
+          float ks = 1.0f;
           if (kHalf) {
             const float *sc = reinterpret_cast<const float *>(
                 smem + Sh::kRingAt + (warp * kSlots + get) * Z::kSlot + Z::kUnit);
+            const int at = 16 * j + 8 * q + g;
             ks = sc[at];
             vs[j][q] = sc[kTT + at];
-            lv = rough_log2(vs[j][q]) - kUp;
+            lv[j][q] = rough_log2(vs[j][q]) - kUp;
           }
 #pragma unroll
           for (int i = 0; i < R; ++i)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float x = s[j][i][2 * q + e] * (fac[i][e] * ks);
-              if (masked && (pos + at >= lim[i][e] || pos + at >= len)) x = -INFINITY;
-              s[j][i][2 * q + e] = x;
-              top[i][e] = fmaxf(top[i][e], x + lv);
-            }
+            for (int e = 0; e < 2; ++e) s[j][i][2 * q + e] *= fac[i][e] * ks;
+        }
+      if (masked) {
+        // out of a row's sight: no weight.  A value's scale that is not finite
+        // makes the rows that see it NaN by their sum, and counts as 0.
+#pragma unroll
+        for (int j = 0; j < kMT; ++j)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int at = pos + 16 * j + 8 * q + g;
+            const bool odd = kHalf && !(fabsf(vs[j][q]) <= 3.4e38f);
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                if (at >= lim[i][e] || at >= len)
+                  s[j][i][2 * q + e] = -INFINITY;
+                else if (odd)
+                  l[i][e] = __uint_as_float(0x7fc00000u);
+              }
+            if (odd) vs[j][q] = 0.0f;
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          top[i][e] = kNone;
+#pragma unroll
+          for (int j = 0; j < kMT; ++j)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              top[i][e] = fmaxf(top[i][e], kHalf ? s[j][i][2 * q + e] + lv[j][q] : s[j][i][2 * q + e]);
         }
       bool grown = false;
 #pragma unroll
@@ -665,12 +750,8 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
             float y[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float p = exp2_(s[j][i][2 * q + e] - m[i][e]);
+              const float p = exp2_(s[j][i][2 * q + e] - m[i][e]);
               y[e] = kHalf ? p * vs[j][q] : p;
-              if (masked) {  // (a masked scale or key may be anything)
-                const int at = pos + 16 * j + 8 * q + g;
-                if (at >= lim[i][e] || at >= len) p = y[e] = 0.0f;
-              }
               l[i][e] += p;
             }
             cut<kHalf, kPP>(y[0], y[1], pr[q]);
@@ -689,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
       // ---- the sums over v: 16 channels by 8 rows a product
       wait_for<kSlots - 2>();
       __syncwarp();
-      issue();
+      issue(std::bool_constant<(kSlots - 1) % 2 == 0>{});
       slot = ring + get * Z::kSlot;
       if (kKind == kKvBf16 && masked && P.M > 1) {
         // A row that some tokens do not see must not reach them, whatever it
@@ -757,8 +838,8 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
                 uint32_t a[4];
-                widen<kKind>(prmt(e[0][k], e[1][k], q ? 0x7362 : 0x5140), a[0], a[1]);
-                widen<kKind>(prmt(e[2][k], e[3][k], q ? 0x7362 : 0x5140), a[2], a[3]);
+                widen2<kKind>(e[0][k], e[1][k], 2 * q, a[0], a[1]);
+                widen2<kKind>(e[2][k], e[3][k], 2 * q, a[2], a[3]);
 #pragma unroll
                 for (int i = 0; i < R; ++i)
 #pragma unroll
@@ -790,9 +871,11 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
     float *const own = reinterpret_cast<float *>(smem + Sh::kRingAt + (warp * kSlots + mine) * Z::kSlot);
     // 16-byte unit q of a row of fp32 sums
     constexpr int kStage = Z::kStage, kRounds = kHd / kStage;
+    // channels side by side of a lane, in a round (8 bits)
+    constexpr int kRun = kHd == 64 || (kHd == 128 && kRounds == 2) ? 8 : 16;
     auto unit = [](int r, int q) { return r * (kStage / 4) + (q ^ (((q >> 2) ^ (q >> 5) ^ r) & 7)); };
     __syncwarp();
-    float *const part =
+    float *const parts =
         P.part + ((size_t)blockIdx.x * 2 + (c0 == 0 ? 1 : 0)) * (8 * R) * (kHd + 4);
 #pragma unroll
     for (int i = 0; i < R; ++i)
@@ -808,9 +891,8 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
                 own[4 * unit(2 * t + (k & 1), ch / 4) + (ch & 3)] = acc[rd * (kStage / 16) + d][i][k];
               }
           } else {
-            // tile 8 half + j: channels 128 half + kRun g + 2 j and 2 j + 1
-            constexpr int kRun = kHd == 64 ? 8 : 16;
-            static_assert(kStage == kHd || kStage == 128, "a round is a half of 256 channels");
+            // tile 8 half + j: channels 2 j and 2 j + 1 of lane g's run
+            static_assert(kStage == kHd || kHd >= 128, "a round is a half");
 #pragma unroll
             for (int d = 0; d < kStage / 16; d += 2)
 #pragma unroll
@@ -842,7 +924,9 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
                 smem + Sh::kRingAt + (w * kSlots + sl) * Z::kSlot)[unit(r8, cq)];
             o[0] += v.x * f; o[1] += v.y * f; o[2] += v.z * f; o[3] += v.w * f;
           }
-          const int ch = rd * kStage + 4 * cq;
+          const int ch = kKind != kKvBf16 && kHd == 128 && kRounds == 2
+                             ? 16 * (cq / 2) + 8 * rd + 4 * (cq & 1)
+                             : rd * kStage + 4 * cq;
           if (whole) {
             const int mt = row / P.group, head = h * P.group + row - mt * P.group;
             const size_t at = ((size_t)b * P.M + mt) * P.qh + head;
@@ -853,7 +937,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
             store4(static_cast<T *>(P.o) + at * kHd + ch, o);
             if (P.lse && ch == 0) P.lse[at] = (top + log2f(sum)) * 0.693147180559945f;
           } else {
-            float *to = part + (size_t)r * (kHd + 4);
+            float *to = parts + (size_t)r * (kHd + 4);
             store4(to + ch, o);
             if (ch == 0) *reinterpret_cast<float2 *>(to + kHd) = make_float2(top, sum);
           }

@@ -132,7 +132,7 @@ struct KvRows {
   float amp;
   int half, pairs;  // rot / 2; pairs side by side
   int M, cols, qh;
-  int tpc, spb;  // tokens and heads of a block (set by the launch)
+  int run;  // heads of a token side by side (set by the launch)
 };
 cudaError_t launch_kv_rows(const KvRows &P, int hd, bool bf16, bool read,
                            cudaStream_t stream);

@@ -13,13 +13,14 @@
 // in 64-bit fixed point: pos times it is exact modulo one turn, an integer
 // product drops the whole turns, and the rest goes to sincospif as a number in
 // [-1, 1].  Error of an angle: 2^-53 pos of the frequency's own rounding plus 1e-7.
-// A block makes the angles of its tokens once, in shared memory, for all of
-// their heads.
+// hd / 8 lanes take a token and a run of its heads, and keep its cosines and sines
+// in registers.
 //
-// Borders between codes.  x / scale is divided to nearest and then made odd in
-// its last bit where the division left a rest (the sign of the rest, exact by a
-// fused multiply-add, says on which side), so that rounding it again to a code
-// gives the code nearest to the true quotient.
+// Borders between codes.  x (1 / scale) is within 2^-22 of the quotient, which
+// settles the code but where a border lies that near; there x / scale is divided
+// to nearest and made odd in its last bit where the division left a rest (the sign
+// of the rest, exact by a fused multiply-add, says on which side), so that
+// rounding it again gives the code nearest to the true quotient.
 //
 // Layout.  8 channels a lane: 16 bytes of bf16 in and out, hd / 8 lanes a row,
 // several rows a lane asked for at once.  Bound by HBM for prompts and by
@@ -36,8 +37,7 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 64;  // tokens a block takes at most
-constexpr int kRows = 4;        // rows a lane asks for at once
+constexpr int kMaxHalf = 128;  // pairs of a head
 
 // What a block knows of a token.
 struct Token {
@@ -97,11 +97,18 @@ __device__ __forceinline__ uint32_t two_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
-  reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+// 8 elements of a row to p; `group`: the row's lanes, all of which store.  fp32:
+// neighbours exchange halves, so that a store fills whole sectors.
+__device__ __forceinline__ void store8(float *p, const float (&x)[8], unsigned group) {
+  const bool odd = threadIdx.x & 1;
+  float y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = __shfl_xor_sync(group, odd ? x[i] : x[4 + i], 1);
+  float4 *to = reinterpret_cast<float4 *>(p) - (odd ? 1 : 0);
+  to[0] = odd ? make_float4(y[0], y[1], y[2], y[3]) : make_float4(x[0], x[1], x[2], x[3]);
+  to[2] = odd ? make_float4(x[4], x[5], x[6], x[7]) : make_float4(y[0], y[1], y[2], y[3]);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8], unsigned) {
   *reinterpret_cast<uint4 *>(p) = make_uint4(two_bf16(x[0], x[1]), two_bf16(x[2], x[3]),
                                              two_bf16(x[4], x[5]), two_bf16(x[6], x[7]));
 }
@@ -122,13 +129,59 @@ __device__ __forceinline__ uint32_t code(float q) {
   return __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
 }
 
+// The codes nearest to x / s in place of the bytes of w that `which` has bits of.
+template <int kKind>
+__device__ __forceinline__ uint32_t settle(uint32_t w, uint32_t which, const float *x, float s) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (which >> (8 * i) & 0xffu)
+      w = (w & ~(0xffu << (8 * i))) | code<kKind>(odd_quotient(x[i], s)) << (8 * i);
+  return w;
+}
+
+// The codes of four elements of a row with scale s.
+template <int kKind>
+__device__ __forceinline__ uint32_t codes4(const float *x, float s, float inv) {
+  uint32_t w;
+  if (kKind == kKvInt8) {
+    // rounded by the addition of 1.5 2^23; what that took off says how near the
+    // border is (the quotient is within 127 2^-22 of x inv)
+    constexpr float kBig = 12582912.0f;
+    uint32_t u[4];
+    float far = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float q = x[i] * inv, t = q + kBig;
+      u[i] = __float_as_uint(t);
+      far = fmaxf(far, fabsf(q - (t - kBig)));
+    }
+    w = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
+    if (far > 0.4999f) w = settle<kKind>(w, ~0u, x, s);
+  } else {
+    // the codes of both ends of where the quotient may lie
+    const float up = inv * (1.0f + 0x1p-21f), dn = inv * (1.0f - 0x1p-21f);
+    uint32_t a[2], b[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      a[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * dn, x[2 * i + 1] * dn), __NV_SATFINITE,
+                                      __NV_E4M3);
+      b[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * up, x[2 * i + 1] * up), __NV_SATFINITE,
+                                      __NV_E4M3);
+    }
+    w = a[0] | a[1] << 16;
+    const uint32_t d = w ^ (b[0] | b[1] << 16);
+    if (d) w = settle<kKind>(w, d, x, s);
+  }
+  return w;
+}
+
 // A row of 8 x kLanes values to its place in the cache.  Every lane of the warp
 // takes part; `on`: this row is stored.
 template <int kKind, int kLanes>
 __device__ __forceinline__ void hold(const float (&x)[8], void *codes, float *scales, size_t row,
                                      int gl, bool on) {
   if (kKind == kKvBf16) {
-    if (on) store8(static_cast<__nv_bfloat16 *>(codes) + row * (8 * kLanes) + 8 * gl, x);
+    if (on) store8(static_cast<__nv_bfloat16 *>(codes) + row * (8 * kLanes) + 8 * gl, x, 0u);
     return;
   }
   // the largest as bits: infinities and NaN are above every number
@@ -142,12 +195,13 @@ __device__ __forceinline__ void hold(const float (&x)[8], void *codes, float *sc
   const float scale = finite ? __fdiv_rn(__uint_as_float(top), kKind == kKvInt8 ? 127.0f : 448.0f)
                              : __uint_as_float(0x7fc00000u);
   uint2 w = make_uint2(0, 0);
-  if (finite && scale > 0.0f) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w.x |= code<kKind>(odd_quotient(x[i], scale)) << (8 * i);
-      w.y |= code<kKind>(odd_quotient(x[4 + i], scale)) << (8 * i);
-    }
+  if (finite && scale >= 0x1p-100f) {
+    const float inv = __frcp_rn(scale);
+    w.x = codes4<kKind>(x, scale, inv);
+    w.y = codes4<kKind>(x + 4, scale, inv);
+  } else if (finite && scale > 0.0f) {  // (its reciprocal or the rests would not be exact enough)
+    w.x = settle<kKind>(0u, ~0u, x, scale);
+    w.y = settle<kKind>(0u, ~0u, x + 4, scale);
   }
   *reinterpret_cast<uint2 *>(static_cast<unsigned char *>(codes) + row * (8 * kLanes) + 8 * gl) = w;
   if (gl == 0) scales[row] = scale;
@@ -179,112 +233,144 @@ __device__ __forceinline__ Token place(const KvRows &P, long long tok) {
   return t;
 }
 
-// Turns and (kKind >= 0) the cache's rows.  A block takes P.tpc tokens and the
-// heads [s0, s1) of q, k, v side by side that blockIdx.y has.
+// The lanes of a row, of kLanes.
+template <int kLanes>
+__device__ __forceinline__ unsigned lanes_of_row() {
+  return kLanes == 32 ? kFull : ((1u << (kLanes & 31)) - 1) << (threadIdx.x & 31 & ~(kLanes - 1));
+}
+
+// Turns and (kKind >= 0) the cache's rows.  A warp takes 32 / kLanes tokens, each
+// with kLanes lanes, and a run of P.run of their heads (q, k and v side by side),
+// the same for all of them.
 template <typename T, int kKind, int kLanes>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
     kv_rows_kernel(const KvRows P) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  constexpr int kHd = 8 * kLanes, kGroups = kThreads / kLanes;
-  __shared__ Token tokens[kMaxTokens];
+  constexpr int kHd = 8 * kLanes, kTokens = 32 / kLanes;
+  __shared__ unsigned long long phase[kMaxHalf];
+  __shared__ float2 angles[4 * kThreads];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int tid = threadIdx.x, gl = tid % kLanes, group = tid / kLanes, lane = tid & 31;
-  const long long tok0 = (long long)blockIdx.x * P.tpc;
-  const int n = (int)min((long long)P.tpc, P.tokens - tok0);
-  const int slots = P.qh + (kKind >= 0 ? 2 * P.c.kvh : 0);
-  const int s0 = (int)blockIdx.y * P.spb, ns = min(P.spb, slots - s0), all = n * ns;
-  const int half = P.half;
-  unsigned long long *phase = reinterpret_cast<unsigned long long *>(smem);
-  float2 *cs = reinterpret_cast<float2 *>(phase + half);
+  const int tid = threadIdx.x, gl = tid % kLanes, lane = tid & 31, half = P.half;
+  const unsigned group = lanes_of_row<kLanes>();
+  const int turned_heads = P.qh + (kKind >= 0 ? P.c.kvh : 0);
+  const int slots = turned_heads + (kKind >= 0 ? P.c.kvh : 0);
+  const int runs = (slots + P.run - 1) / P.run;
+  const long long job = (long long)blockIdx.x * (kThreads / 32) + (tid >> 5);
+  const long long first = job / runs * kTokens;  // the warp's first token
+  const int s0 = (int)(job % runs) * P.run, s1 = min(s0 + P.run, slots);
+  const bool there = first + lane / kLanes < P.tokens;
+  // (past the end: the last token again, storing nothing)
+  const long long tok = there ? first + lane / kLanes : P.tokens - 1;
 
-  auto source = [&](int r) -> const T * {
-    const int t = r / ns, s = s0 + r - t * ns;
-    const long long tok = tok0 + t;
-    if (s < P.qh) return static_cast<const T *>(P.q) + tok * P.q_stride + s * kHd + 8 * gl;
-    if (s < P.qh + P.c.kvh)
-      return static_cast<const T *>(P.k) + tok * P.k_stride + (s - P.qh) * kHd + 8 * gl;
-    return static_cast<const T *>(P.v) + tok * P.v_stride + (s - P.qh - P.c.kvh) * kHd + 8 * gl;
+  auto fetch = [&](Raw<T> &raw, int x) {
+    const T *p = x < P.qh ? static_cast<const T *>(P.q) + tok * P.q_stride + x * kHd
+                 : x < turned_heads
+                     ? static_cast<const T *>(P.k) + tok * P.k_stride + (x - P.qh) * kHd
+                     : static_cast<const T *>(P.v) + tok * P.v_stride + (x - turned_heads) * kHd;
+    raw.load(p + 8 * gl);
   };
-  Raw<T> raw[kRows];
-  auto fetch = [&](int r0) {
-#pragma unroll
-    for (int j = 0; j < kRows; ++j)  // (rows past the end: the last one again)
-      raw[j].load(source(min(r0 + j * kGroups + group, all - 1)));
-  };
-  fetch(0);
+  // One row a lane: it is asked for beside the lengths and pages.  Longer runs
+  // ask behind them, so that rows of padding are left where they are (8 padded
+  // prompts of 4096 tokens: half of the bytes).
+  const bool single = P.run == 1;
+  Raw<T> one;
+  if (single) fetch(one, s0);
+  const Token tk = place(P, tok);
+  const bool on = there && tk.on;
 
-  if (tid < n) tokens[tid] = place(P, tok0 + tid);
-  for (int i = tid; i < half; i += kThreads) {
-    const double turns = P.freq[i] * 0.15915494309189533576888;  // 1 / 2 pi
-    phase[i] = __double2ull_rd((turns - floor(turns)) * 18446744073709551616.0);
-  }
-  __syncthreads();
-  for (int e = tid; e < n * half; e += kThreads) {
-    const int t = e / half;
-    const long long a = (long long)(phase[e - t * half] * (unsigned long long)(long long)tokens[t].pos);
-    float s, c;
-    sincospif(__ll2float_rn(a) * 1.0842021724855044e-19f, &s, &c);  // 2^-63
-    cs[e] = make_float2(P.amp * c, P.amp * s);
-  }
-  __syncthreads();
-
-  // the lane's place among the turned channels
-  const int hl = half / 8;
-  const bool pairs = P.pairs, upper = !pairs && gl >= hl;
+  // the lane's place among the turned channels, and its angles
+  const bool pairs = P.pairs, upper = !pairs && 8 * gl >= half;
   const bool turned = 8 * gl < 2 * half;
-  const int f0 = pairs ? 4 * gl : 8 * (upper ? gl - hl : gl);
-  const int other = lane - gl + (turned ? (upper ? gl - hl : gl + hl) : gl);
-  for (int r0 = 0; r0 < all; r0 += kRows * kGroups) {
-    Raw<T> now[kRows];
-#pragma unroll
-    for (int j = 0; j < kRows; ++j) now[j] = raw[j];
-    if (r0 + kRows * kGroups < all) fetch(r0 + kRows * kGroups);
-#pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-      const int r = r0 + j * kGroups + group;
-      // (uniform over the warp: the rows of its first group come first)
-      if (r0 + j * kGroups + (tid & ~31) / kLanes >= all) break;
-      const int rc = min(r, all - 1), t = rc / ns, s = s0 + rc - t * ns;
-      const Token &tk = tokens[t];
-      const bool on = r < all && tk.on;
-      float x[8];
-      now[j].values(x);
-      // v is not turned; whole warps skip the exchange where no row wants it
-      const bool turn = half && s < P.qh + (kKind >= 0 ? P.c.kvh : 0);
-      if (__any_sync(kFull, turn)) {
-        const float2 *w = cs + t * half + f0;
-        if (pairs) {
-          if (turn && turned) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float a = x[2 * i], b = x[2 * i + 1];
-              x[2 * i] = a * w[i].x - b * w[i].y;
-              x[2 * i + 1] = b * w[i].x + a * w[i].y;
-            }
-          }
-        } else {
-          float y[8];
-          now[j].partner(other, y);
-          if (turn && turned) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = x[i] * w[i].x + (upper ? y[i] : -y[i]) * w[i].y;
-          }
-        }
-      }
-      const long long tok = tok0 + t;
-      if (s < P.qh && on)
-        store8(static_cast<T *>(P.q_out) + (tok * P.qh + s) * kHd + 8 * gl, x);
-      if (kKind >= 0) {
-        const bool is_v = s >= P.qh + P.c.kvh, cached = s >= P.qh;
-        if (__any_sync(kFull, cached)) {
-          const int h = s - P.qh - (is_v ? P.c.kvh : 0);
-          const size_t row = (size_t)tk.at + ((size_t)h << P.c.page_shift);
-          hold<kKind < 0 ? 0 : kKind, kLanes>(x, is_v ? P.c.v : P.c.k, is_v ? P.c.v_scale : P.c.k_scale,
-                                              row, gl, on && cached && tk.at >= 0);
-        }
-      }
+  const int other = lane + (turned && !pairs ? (upper ? -(half / 8) : half / 8) : 0);
+  float c[8], w[8];  // (pairs side by side: the first four)
+  if (half) {
+    for (int i = tid; i < half; i += kThreads) {
+      const double turns = P.freq[i] * 0.15915494309189533576888;  // 1 / 2 pi
+      phase[i] = __double2ull_rd((turns - floor(turns)) * 18446744073709551616.0);
     }
+    __syncthreads();
+  }
+  if (!__any_sync(kFull, on)) return;
+  if (half && s0 < turned_heads) {
+    // the token's angles, each by one of its lanes
+    float2 *const cs = angles + (tid / kLanes) * (4 * kLanes);
+#pragma unroll 1
+    for (int i = gl; i < half; i += kLanes) {
+      const long long a = (long long)(phase[i] * (unsigned long long)(long long)tk.pos);
+      float x, y;
+      sincospif(__ll2float_rn(a) * 1.0842021724855044e-19f, &y, &x);  // 2^-63
+      cs[i] = make_float2(P.amp * x, P.amp * y);
+    }
+    __syncwarp();
+    const int f0 = !turned ? 0 : pairs ? 4 * gl : 8 * gl - (upper ? half : 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 x = cs[pairs ? f0 + (i & 3) : f0 + i];
+      c[i] = x.x;
+      w[i] = upper || pairs ? x.y : -x.y;  // (of the partner)
+    }
+  }
+  // (every lane of the warp is at the same head)
+  auto turn = [&](const Raw<T> &raw, float (&y)[8]) {
+    if (pairs) {
+      if (!turned) return;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float a = y[2 * i], b = y[2 * i + 1];
+        y[2 * i] = a * c[i] - b * w[i];
+        y[2 * i + 1] = b * c[i] + a * w[i];
+      }
+    } else {
+      float z[8];
+      raw.partner(other, z);
+      if (!turned) return;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = y[i] * c[i] + z[i] * w[i];
+    }
+  };
+  auto row_q = [&](const Raw<T> &raw, int x) {
+    float y[8];
+    raw.values(y);
+    if (half) turn(raw, y);
+    if (on) store8(static_cast<T *>(P.q_out) + (tok * P.qh + x) * kHd + 8 * gl, y, group);
+  };
+  auto row_kv = [&](const Raw<T> &raw, int x) {
+    if constexpr (kKind >= 0) {
+      float y[8];
+      raw.values(y);
+      if (half && x < turned_heads) turn(raw, y);
+      const bool is_v = x >= turned_heads;
+      const int h = x - (is_v ? turned_heads : P.qh);
+      hold<kKind, kLanes>(y, is_v ? P.c.v : P.c.k, is_v ? P.c.v_scale : P.c.k_scale,
+                          (size_t)tk.at + ((size_t)h << P.c.page_shift), gl, on && tk.at >= 0);
+    }
+  };
+  if (single) {
+    if (s0 < P.qh)
+      row_q(one, s0);
+    else
+      row_kv(one, s0);
+    return;
+  }
+  constexpr int kQ = sizeof(T) == 2 ? 4 : 2, kKv = 2;  // rows under way
+  const int q1 = min(s1, P.qh);
+#pragma unroll 1
+  for (int x = s0; x < q1; x += kQ) {
+    Raw<T> raw[kQ];
+#pragma unroll
+    for (int j = 0; j < kQ; ++j) fetch(raw[j], min(x + j, q1 - 1));
+#pragma unroll
+    for (int j = 0; j < kQ; ++j)
+      if (x + j < q1) row_q(raw[j], x + j);
+  }
+#pragma unroll 1
+  for (int x = max(s0, P.qh); x < s1; x += kKv) {
+    Raw<T> raw[kKv];
+#pragma unroll
+    for (int j = 0; j < kKv; ++j) fetch(raw[j], min(x + j, s1 - 1));
+#pragma unroll
+    for (int j = 0; j < kKv; ++j)
+      if (x + j < s1) row_kv(raw[j], x + j);
   }
 }
 
@@ -296,14 +382,19 @@ struct Codes {
     a = __ldg(reinterpret_cast<const uint2 *>(static_cast<const unsigned char *>(p) + at));
   }
   __device__ __forceinline__ void values(float (&x)[8]) const {
+    if (kKind == kKvInt8) {  // code + 128 behind the bits of 2^23
+      const uint32_t w[2] = {a.x ^ 0x80808080u, a.y ^ 0x80808080u};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t c = ((i < 4 ? a.x : a.y) >> (8 * (i & 3))) & 0xffu;
-      if (kKind == kKvInt8) {
-        x[i] = (float)(int)(signed char)c;
-      } else {
-        const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)c, __NV_E4M3);
-        x[i] = __half2float(__half(h));
+      for (int i = 0; i < 8; ++i)
+        x[i] = __uint_as_float(__byte_perm(w[i / 4], 0x4b000000u, 0x7540 + (i & 3))) - 8388736.0f;
+    } else {
+      const uint32_t w[4] = {a.x, a.x >> 16, a.y, a.y >> 16};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(
+            __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i] & 0xffffu), __NV_E4M3)));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
       }
     }
   }
@@ -317,31 +408,32 @@ struct Codes<kKvBf16> {
   __device__ __forceinline__ void values(float (&x)[8]) const { r.values(x); }
 };
 
-// Rows of the cache as k and v [B][M][kvh][hd].  A block takes P.tpc tokens.
+// Rows of the cache as k and v [B][M][kvh][hd]: kLanes lanes take a token and
+// P.run of its heads.
 template <typename T, int kKind, int kLanes>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     kv_read_kernel(const KvRows P) {
   constexpr int kHd = 8 * kLanes, kGroups = kThreads / kLanes;
-  __shared__ Token tokens[kMaxTokens];
+  constexpr int kRows = 4;  // K and V of so many under way
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int tid = threadIdx.x, gl = tid % kLanes, group = tid / kLanes;
-  const long long tok0 = (long long)blockIdx.x * P.tpc;
-  const int n = (int)min((long long)P.tpc, P.tokens - tok0);
-  if (tid < n) tokens[tid] = place(P, tok0 + tid);
-  __syncthreads();
-  const int all = n * P.c.kvh;
-  for (int r0 = group; r0 < all; r0 += kRows * kGroups) {
+  const int tid = threadIdx.x, gl = tid % kLanes;
+  const unsigned group = lanes_of_row<kLanes>();
+  const int runs = (P.c.kvh + P.run - 1) / P.run;
+  const long long job = (long long)blockIdx.x * kGroups + tid / kLanes;
+  if (job >= P.tokens * runs) return;
+  const long long tok = job / runs;
+  const int h0 = (int)(job - tok * runs) * P.run, h1 = min(h0 + P.run, P.c.kvh);
+  const Token tk = place(P, tok);
+  if (!tk.on || tk.at < 0) return;
+#pragma unroll 1
+  for (int h = h0; h < h1; h += kRows) {
     Codes<kKind> k[kRows], v[kRows];
     float ks[kRows], vs[kRows];
-    long long to[kRows];
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
-      const int r = r0 + j * kGroups, t = r / P.c.kvh, h = r - t * P.c.kvh;
-      to[j] = -1;
-      if (r >= all || !tokens[t].on || tokens[t].at < 0) continue;
-      const size_t row = (size_t)tokens[t].at + ((size_t)h << P.c.page_shift);
-      to[j] = ((tok0 + t) * P.c.kvh + h) * kHd + 8 * gl;
+      if (h + j >= h1) continue;
+      const size_t row = (size_t)tk.at + ((size_t)(h + j) << P.c.page_shift);
       k[j].load(P.c.k, row * kHd + 8 * gl);
       v[j].load(P.c.v, row * kHd + 8 * gl);
       ks[j] = kKind == kKvBf16 ? 1.0f : __ldg(P.c.k_scale + row);
@@ -349,20 +441,21 @@ __global__ void __launch_bounds__(kThreads)
     }
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
-      if (to[j] < 0) continue;
+      if (h + j >= h1) continue;
+      const long long to = (tok * P.c.kvh + h + j) * kHd + 8 * gl;
       float x[8];
       k[j].values(x);
       if (kKind != kKvBf16) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] *= ks[j];
       }
-      store8(static_cast<T *>(P.q_out) + to[j], x);
+      store8(static_cast<T *>(P.q_out) + to, x, group);
       v[j].values(x);
       if (kKind != kKvBf16) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] *= vs[j];
       }
-      store8(static_cast<T *>(P.v_out) + to[j], x);
+      store8(static_cast<T *>(P.v_out) + to, x, group);
     }
   }
 }
@@ -371,24 +464,23 @@ template <typename T, int kKind, int kLanes>
 cudaError_t rows_go(KvRows P, cudaStream_t stream, bool read) {
   const int heads = read ? P.c.kvh : P.qh + (kKind >= 0 ? 2 * P.c.kvh : 0);
   constexpr int kGroups = kThreads / kLanes;
-  // Tokens of a block: as many as its groups' first rows cover, so that every
-  // lane has kRows loads in flight.  Few tokens are cut by heads too: one
-  // row a group then (64 tokens of 24 + 8 heads fill the GPU).
-  constexpr int kFew = 152 * 4 * kGroups;  // rows that one row a group spreads over the SMs
-  P.spb = heads;
-  if (P.tokens * heads <= kFew) {
-    P.tpc = kGroups / heads > 1 ? kGroups / heads : 1;
-    if (!read && heads > kGroups) P.spb = kGroups;
-  } else {
-    P.tpc = kRows * kGroups / heads > 1 ? kRows * kGroups / heads : 1;
-  }
-  if (P.tpc > kMaxTokens) P.tpc = kMaxTokens;
-  const long long blocks = (P.tokens + P.tpc - 1) / P.tpc;
+  // A run is as long as leaves four blocks for every SM, in steps of the rows
+  // under way: single tokens are cut down to a row a group (64 tokens of
+  // 24 + 8 heads fill the GPU), prompts take all of a token's heads for one
+  // set of angles.
+  const long long rows = P.tokens * heads, full = 152ll * 4 * kGroups;
+  const int step = read || sizeof(T) == 2 ? 4 : 2;
+  long long run = (rows + full - 1) / full;
+  if (run > 1) run = (run + step - 1) / step * step;
+  P.run = (int)(run < heads ? run : heads);
+  const long long runs = (heads + P.run - 1) / P.run;
+  constexpr int kTokens = 32 / kLanes;
+  const long long blocks = read ? (P.tokens * runs + kGroups - 1) / kGroups
+                                : ((P.tokens + kTokens - 1) / kTokens * runs + 7) / 8;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks, (unsigned)((heads + P.spb - 1) / P.spb));
+  cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = read ? 0 : (size_t)P.half * 8 * (1 + P.tpc);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -398,13 +490,7 @@ cudaError_t rows_go(KvRows P, cudaStream_t stream, bool read) {
   if constexpr (kKind >= 0) {
     if (read) return cudaLaunchKernelEx(&cfg, kv_read_kernel<T, kKind, kLanes>, P);
   }
-  const auto kernel = kv_rows_kernel<T, kKind, kLanes>;
-  if (cfg.dynamicSmemBytes > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)cfg.dynamicSmemBytes);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaLaunchKernelEx(&cfg, kernel, P);
+  return cudaLaunchKernelEx(&cfg, kv_rows_kernel<T, kKind, kLanes>, P);
 }
 
 template <typename T, int kKind>
