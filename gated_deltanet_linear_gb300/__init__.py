@@ -617,7 +617,7 @@ class KVCache:
     float8_e4m3fn; the 8-bit types with k_scale, v_scale float32
     [pages][kvh][page].  It refers to the tensors, which stay the caller's."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "kind", "shape", "c")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "kind", "shape", "c", "ref")
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         if not isinstance(k, torch.Tensor) or k.dim() != 4:
@@ -635,13 +635,14 @@ class KVCache:
             ptrs[2] = _tok(k_scale, "k_scale", k.shape[:3], torch.float32)
             ptrs[3] = _tok(v_scale, "v_scale", k.shape[:3], torch.float32)
         self.c = _Cache(*ptrs, self.kind, pages, kvh, page, hd)
+        self.ref = ctypes.byref(self.c)
 
 
 class Rope:
     """Rotary positions: freq float64 [rot / 2] radians a position (CUDA), the
     layout of the pairs, the amplitude (see gdn_rope_freqs)."""
 
-    __slots__ = ("freq", "rot", "layout", "amp", "c")
+    __slots__ = ("freq", "rot", "layout", "amp", "c", "ref")
 
     def __init__(self, freq, layout=GDN_ROPE_HALF, amp=1.0):
         if not isinstance(freq, torch.Tensor) or freq.dim() != 1:
@@ -649,6 +650,7 @@ class Rope:
         ptr = _tok(freq, "freq", freq.shape, torch.float64)
         self.freq, self.rot, self.layout, self.amp = freq, 2 * freq.numel(), layout, amp
         self.c = _Rope(ptr, self.rot, layout, amp)
+        self.ref = ctypes.byref(self.c)
 
 
 def gdn_rope_freqs(rot, base=10000.0, scaling=GDN_ROPE_PLAIN, factor=1.0,
@@ -665,30 +667,33 @@ def gdn_rope_freqs(rot, base=10000.0, scaling=GDN_ROPE_PLAIN, factor=1.0,
     return freq.to(device), amp.value
 
 
-def _rows(x, name, lead, dtype):
-    """Pointer and stride from token to token of x [*lead][heads][hd]: heads
-    and channels contiguous, tokens evenly spaced (the rows of a projection)."""
+def _rows(x, name, shape, dtype):
+    """Pointer and stride from token to token of x, shape [B][M][heads][hd] or
+    [rows][heads][hd]: heads and channels contiguous, tokens evenly spaced (the
+    rows of a projection).  (On the path of every call, as _tok; that it is
+    device memory the library checks.)"""
+    try:
+        if x.dtype is dtype and x.shape == shape:
+            st = x.stride()
+            heads, hd = shape[-2:]
+            if st[-1] == 1 and (st[-2] == hd or heads == 1):
+                if len(shape) == 3:
+                    return x.data_ptr(), st[0] if shape[0] > 1 else heads * hd
+                B, M = shape[:2]
+                if M > 1:
+                    if B <= 1 or st[0] == M * st[1]:
+                        return x.data_ptr(), st[1]
+                else:
+                    return x.data_ptr(), st[0] if B > 1 else heads * hd
+    except AttributeError:
+        pass
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    shape, st = x.shape, x.stride()
-    if not x.is_cuda or x.dtype is not dtype or len(shape) != len(lead) + 2 or \
-            tuple(shape[:-2]) != tuple(lead):
-        raise ValueError(f"{name} must be a {dtype} CUDA tensor {list(lead)}[heads][hd]")
-    width = shape[-2] * shape[-1]
-    if x.numel() and (st[-1] != 1 or (st[-2] != shape[-1] and shape[-2] > 1)):
-        raise ValueError(f"{name}: heads and channels must be contiguous")
-    step = width
-    if len(lead) == 2:
-        B, M = lead
-        if M > 1:
-            step = st[1]
-            if B > 1 and st[0] != M * st[1]:
-                raise ValueError(f"{name}: tokens must be evenly spaced")
-        elif B > 1:
-            step = st[0]
-    elif lead[0] > 1:
-        step = st[0]
-    return x.data_ptr(), step
+    if not x.is_cuda or x.dtype is not dtype or x.shape != shape:
+        raise ValueError(f"{name} must be a {dtype} CUDA tensor of shape {tuple(shape)}")
+    if not x.numel():
+        return x.data_ptr(), shape[-2] * shape[-1]
+    raise ValueError(f"{name}: heads and channels must be contiguous, tokens evenly spaced")
 
 
 def _code(dtype):
@@ -699,7 +704,14 @@ def _code(dtype):
 
 
 def _ints(x, name, shape):
-    return None if x is None else _tok(x, name, shape, torch.int32)
+    if x is None:
+        return None
+    try:
+        if x.dtype is torch.int32 and x.shape == shape and x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
+        pass
+    return _tok(x, name, shape, torch.int32)
 
 
 def gdn_rope_m(x, pos, rope, y, stream=None):
@@ -709,9 +721,9 @@ def gdn_rope_m(x, pos, rope, y, stream=None):
     if x.dim() != 3:
         raise ValueError("x must be [rows][heads][hd]")
     rows, heads, hd = x.shape
-    ptr, step = _rows(x, "x", (rows,), x.dtype)
+    ptr, step = _rows(x, "x", x.shape, x.dtype)
     r = (_lib or load()).gdn_rope_m(
-        rows, heads, hd, _code(x.dtype), ctypes.byref(rope.c), ptr, step,
+        rows, heads, hd, _code(x.dtype), rope.ref, ptr, step,
         _ints(pos, "pos", (rows,)), _tok(y, "y", x.shape, x.dtype), _stream(stream))
     if r:
         raise GDNError(r, "gdn_rope_m")
@@ -719,10 +731,9 @@ def gdn_rope_m(x, pos, rope, y, stream=None):
 
 def _paged(cache, B, table, start, counts, err_dev):
     """Pointers of table, start, counts, err_dev and the table's columns."""
-    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+    if not isinstance(table, torch.Tensor) or len(ts := table.shape) != 2 or ts[0] != B:
         raise ValueError("table must be [B][columns]")
-    cols = table.shape[1]
-    return (_ints(table, "table", (B, cols)), cols, _ints(start, "start", (B,)),
+    return (_ints(table, "table", ts), ts[1], _ints(start, "start", (B,)),
             _ints(counts, "counts", (B,)), _ints(err_dev, "err_dev", (1,)))
 
 
@@ -731,27 +742,27 @@ def gdn_kv_write_m(cache, k, v, table, start, rope=None, q=None, q_out=None,
     """The keys and values k, v [B][M][kvh][hd] of M tokens of every sequence
     to positions start[b] + m of their pages; rope turns k on the way, and q
     [B][M][qh][hd] into q_out.  q, k, v may be slices of one projection."""
-    if k.dim() != 4:
-        raise ValueError("k must be [B][M][kvh][hd]")
-    B, M, dtype = k.shape[0], k.shape[1], k.dtype
     _, kvh, _, hd = cache.shape
-    if k.shape[2:] != (kvh, hd) or v.shape != k.shape:
+    shape, dtype = k.shape, k.dtype
+    if len(shape) != 4 or shape[2] != kvh or shape[3] != hd:
         raise ValueError(f"k and v must be [B][M][{kvh}][{hd}]")
-    (kp, ks), (vp, vs) = _rows(k, "k", (B, M), dtype), _rows(v, "v", (B, M), dtype)
+    B, M = shape[:2]
+    (kp, ks), (vp, vs) = _rows(k, "k", shape, dtype), _rows(v, "v", shape, dtype)
     qp = qo = None
     qs = qh = 0
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     if q is not None:
-        qp, qs = _rows(q, "q", (B, M), dtype)
-        qh = q.shape[2]
-        if q.shape[3] != hd:
+        qshape = q.shape
+        if len(qshape) != 4 or qshape[3] != hd or qshape[:2] != shape[:2]:
             raise ValueError(f"q must be [B][M][qh][{hd}]")
-        qo = _tok(q_out, "q_out", q.shape, dtype)
+        qp, qs = _rows(q, "q", qshape, dtype)
+        qh = qshape[2]
+        qo = _tok(q_out, "q_out", qshape, dtype)
     tp, cols, sp, cp, ep = _paged(cache, B, table, start, counts, err_dev)
     r = (_lib or load()).gdn_kv_write_m(
-        ctypes.byref(cache.c), B, M, qh, _code(dtype),
-        None if rope is None else ctypes.byref(rope.c), qp, qs, kp, ks, vp, vs, qo,
+        cache.ref, B, M, qh, _code(dtype),
+        None if rope is None else rope.ref, qp, qs, kp, ks, vp, vs, qo,
         tp, cols, sp, cp, ep, _stream(stream))
     if r:
         raise GDNError(r, "gdn_kv_write_m")
@@ -761,13 +772,14 @@ def gdn_kv_read(cache, table, start, k, v, counts=None, err_dev=None,
                 stream=None):
     """Positions start[b] .. start[b] + T - 1 (start None: from 0) of every
     sequence into k, v [B][T][kvh][hd], float32 or bfloat16."""
-    if k.dim() != 4 or k.shape[2:] != (cache.shape[1], cache.shape[3]):
+    shape, dtype = k.shape, k.dtype
+    if len(shape) != 4 or shape[2] != cache.shape[1] or shape[3] != cache.shape[3]:
         raise ValueError("k must be [B][T][kvh][hd]")
-    B, T, dtype = k.shape[0], k.shape[1], k.dtype
+    B, T = shape[:2]
     tp, cols, sp, cp, ep = _paged(cache, B, table, start, counts, err_dev)
     r = (_lib or load()).gdn_kv_read(
-        ctypes.byref(cache.c), B, T, _code(dtype), tp, cols, sp, cp,
-        _tok(k, "k", k.shape, dtype), _tok(v, "v", k.shape, dtype), ep,
+        cache.ref, B, T, _code(dtype), tp, cols, sp, cp,
+        _tok(k, "k", shape, dtype), _tok(v, "v", shape, dtype), ep,
         _stream(stream))
     if r:
         raise GDNError(r, "gdn_kv_read")
@@ -775,7 +787,7 @@ def gdn_kv_read(cache, table, start, k, v, counts=None, err_dev=None,
 
 def gdn_attn_workspace(cache, M, qh):
     """Bytes of workspace gdn_attn_step_m needs."""
-    return int((_lib or load()).gdn_attn_workspace(ctypes.byref(cache.c), M, qh))
+    return int((_lib or load()).gdn_attn_workspace(cache.ref, M, qh))
 
 
 def gdn_attn_step_m(cache, q, table, start, o, scale=None, counts=None,
@@ -784,10 +796,10 @@ def gdn_attn_step_m(cache, q, table, start, o, scale=None, counts=None,
     start[b] + m of the cache, their own among them: q, o [B][M][qh][hd]
     float32 or bfloat16, lse float32 [B][M][qh] or None; scale defaults to
     hd^-0.5."""
-    if q.dim() != 4 or q.shape[3] != cache.shape[3]:
+    qs, dtype = q.shape, q.dtype
+    if len(qs) != 4 or qs[3] != cache.shape[3]:
         raise ValueError("q must be [B][M][qh][hd]")
-    B, M, qh, hd = qs = q.shape
-    dtype = q.dtype
+    B, M, qh, hd = qs
     tp, cols, sp, cp, ep = _paged(cache, B, table, start, counts, err_dev)
     ws_ptr, ws_bytes = None, 0
     if workspace is not None:
@@ -795,7 +807,7 @@ def gdn_attn_step_m(cache, q, table, start, o, scale=None, counts=None,
             raise ValueError("workspace must be a contiguous CUDA tensor")
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.nbytes
     r = (_lib or load()).gdn_attn_step_m(
-        ctypes.byref(cache.c), B, M, qh, _code(dtype),
+        cache.ref, B, M, qh, _code(dtype),
         hd ** -0.5 if scale is None else scale, _tok(q, "q", qs, dtype), tp, cols,
         sp, cp, _tok(o, "o", qs, dtype),
         None if lse is None else _tok(lse, "lse", qs[:3], torch.float32), ep,

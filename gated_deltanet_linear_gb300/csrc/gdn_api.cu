@@ -958,7 +958,7 @@ size_t gdn_attn_workspace(const gdn_kv_cache *cache, int M, int qh) {
   if (cache_shape(cache, &c) || M < 1 || M > GDN_ATTN_MAX_TOKENS || qh < 1 ||
       qh > GDN_KV_MAX_HEADS || qh % c.kvh)
     return 0;
-  return gdn::attn_workspace_bytes(M, qh / c.kvh, cache->hd);
+  return gdn::attn_workspace_bytes(c.kind, M, qh / c.kvh, cache->hd);
 }
 
 int gdn_attn_step_m(const gdn_kv_cache *cache, int B, int M, int qh, int dtype,

@@ -56,28 +56,42 @@ namespace gdn {
 namespace attn {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kWarps = 8, kThreads = 32 * kWarps;  // of attn_join_kernel
 constexpr float kNone = -1e30f;  // the reference of rows that have seen nothing
 constexpr float kSlack = 3.0f;   // how far the maximum may pass it (log2)
 constexpr float kUp = 12.0f;     // weights of 8-bit rows reach 2^12 (+ kSlack)
 constexpr int kSms = 152;
 
-// Sizes of a variant: R tiles of 8 rows.
+// Sizes of a variant: R tiles of 8 rows.  kS warps share a tile of positions (a
+// team): each takes its share of them for the scores, and its share of the
+// channels for the sums over v, so that the sums of 16 rows fit the registers of
+// two CTAs an SM (one warp for all of 256 channels: one CTA, 78 against ?? us for
+// 4 tokens x 24 rows of 16 sequences).
 template <int kHd, int kKind, int R>
 struct Sizes {
   static constexpr int kBytes = kKind == kKvBf16 ? 2 : 1;
+  static constexpr int kS = R > 1 && kHd > 64 && kKind != kKvBf16 ? 2 : 1;
+  // of a CTA: what the registers of the sums leave
+  static constexpr int kWarps = kS == 1 || (kHd == 128 && R == 2) ? 8 : 12;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kTeams = kWarps / kS;
   static constexpr int kRow = kHd * kBytes;               // bytes of a row
-  // CTAs an SM: a lane has kHd R / 4 sums, and three slots a warp are wanted
-  static constexpr int kCtas = kHd * R > 256 || kRow > 256 ? 1 : 2;
-  // positions of a tile (32 of 128 channels and 16 rows would not fit the registers)
-  static constexpr int kTT = kRow <= 128 && kHd * R <= 128 ? 32 : 16;
-  static constexpr int kUnit = kTT * kRow;                // K or V of a tile
-  static constexpr int kSlot = kUnit + (kKind == kKvBf16 ? 0 : 8 * kTT);  // and scales
-  static constexpr int kRing = kCtas == 1 ? 25 * 1024 + 512 : 13 * 1024;  // a warp's ring
+  static constexpr int kTile = kRow <= 128 || kS == 2 ? 32 : 16;  // positions of a tile
+  static constexpr int kOwn = kTile / kS;                 // of them a warp's, for the scores
+  static constexpr int kVHd = kHd / kS;                   // a warp's channels of v
+  static constexpr int kVRow = kRow / kS;
+  static constexpr int kUnit = kOwn * kRow;               // a warp's part of K or V
+  static constexpr int kSlot = kUnit + (kKind == kKvBf16 ? 0 : 8 * kOwn);  // and scales
+  // CTAs an SM: three slots a warp are wanted
+  static constexpr int kCtas = kUnit > 4096 || (kHd == 256 && R > 1) || R > 2 ? 1 : 2;
+  // a warp's ring
+  static constexpr int kRing = kWarps > 8   ? 13 * 1024 : kCtas == 1 ? 25 * 1024 + 512
+                               : kS == 2    ? 11 * 1024
+                                            : 13 * 1024;
   static constexpr int kSlots = kRing / kSlot;
-  static constexpr int kChunk = kWarps * kTT;
+  static constexpr int kChunk = kTeams * kTile;
   // channels of 8 rows of fp32 sums that a slot holds
-  static constexpr int kStage = kSlot >= 32 * kHd ? kHd : kHd / 2;
+  static constexpr int kStage = kSlot >= 32 * kVHd ? kVHd : kVHd / 2;
 };
 
 // Parts of q and of the weights.
@@ -157,6 +171,11 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+}
+
+// The two warps of a team.
+__device__ __forceinline__ void team_sync(int team) {
+  asm volatile("bar.sync %0, 64;" ::"r"(team + 1) : "memory");
 }
 
 // An 8 x 8 tile of 16-bit numbers, transposed among the lanes.
@@ -295,33 +314,45 @@ struct Shared {
   using Z = Sizes<kHd, kKind, R>;
   static constexpr int kQBytes = kHd / 16 * Parts<kKind, kBf16>::kQ * R * 256;
   static constexpr int kRingAt = kQBytes;
-  static constexpr int kStatAt = kRingAt + kWarps * Z::kSlots * Z::kSlot;
+  static constexpr int kStatAt = kRingAt + Z::kWarps * Z::kSlots * Z::kSlot;
   // m and l of every warp's rows, the rows' factors, counts of the search
-  static constexpr int kBytes = kStatAt + kWarps * 8 * R * 8 + 8 * R * 4 + 2 * kWarps * 8 + 32;
+  static constexpr int kWeightsAt =
+      kStatAt + Z::kWarps * 8 * R * 8 + 8 * R * 4 + 2 * Z::kWarps * 8 + 32;
+  // between the warps of a team: maxima, and a tile's weights
+  static constexpr int kWeights = Z::kOwn / 16 * R * Parts<kKind, kBf16>::kP * 256;
+  static constexpr int kBytes =
+      kWeightsAt + (Z::kS == 1 ? 0 : Z::kWarps * (kWeights + 8 * R * 4));
 };
 
 template <int kHd, int kKind, bool kBf16, int R>
-__global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
+__global__ void __launch_bounds__(Sizes<kHd, kKind, R>::kThreads, Sizes<kHd, kKind, R>::kCtas)
     attn_kernel(const AttnArgs P) {
   using Z = Sizes<kHd, kKind, R>;
   using Sh = Shared<kHd, kKind, kBf16, R>;
   using T = typename std::conditional<kBf16, __nv_bfloat16, float>::type;
   constexpr bool kHalf = kKind != kKvBf16;
-  constexpr int kTT = Z::kTT, kRow = Z::kRow, kSlots = Z::kSlots, kMT = kTT / 16;
+  constexpr int kRow = Z::kRow, kSlots = Z::kSlots, kS = Z::kS, kTile = Z::kTile;
+  constexpr int kVHd = Z::kVHd, kVRow = Z::kVRow, kWarps = Z::kWarps, kThreads = Z::kThreads;
+  constexpr int kMT = Z::kOwn / 16, kVT = kTile / 16;  // 16 positions: of scores, of V
   constexpr int kQP = Parts<kKind, kBf16>::kQ, kPP = Parts<kKind, kBf16>::kP;
   constexpr int kVec = 16 / Z::kBytes;  // elements of 16 bytes
-  constexpr int kDT = kHd / 16;         // tiles of 16 channels
+  constexpr int kDT = kVHd / 16;        // tiles of 16 channels
   extern __shared__ __align__(128) unsigned char smem[];
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  // (the same for all lanes, and known to be)
+  const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0);
+  const int lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int team = warp / kS, sub = warp % kS;
   const int nrt = (P.M * P.group + 8 * R - 1) / (8 * R), items = P.c.kvh * nrt;
   uint32_t *const qs = reinterpret_cast<uint32_t *>(smem);
   float2 *const stat = reinterpret_cast<float2 *>(smem + Sh::kStatAt);  // [warp][8 R]
   float *const factor = reinterpret_cast<float *>(stat + kWarps * 8 * R);  // [8 R]
   long long *const room = reinterpret_cast<long long *>(factor + 8 * R);
   int *const found = reinterpret_cast<int *>(room + 2 * kWarps);  // [3]
+  uint2 *const weights = reinterpret_cast<uint2 *>(smem + Sh::kWeightsAt);
+  float *const maxima = reinterpret_cast<float *>(smem + Sh::kWeightsAt + kWarps * Sh::kWeights);
   signed char *const rooms = reinterpret_cast<signed char *>(found + 4);  // [kWarps]
 
   // ---- this CTA's share: chunks [u0, u1) of the list, from sequence b0 on
@@ -343,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
     }
     return n;
   };
-  // the first 256 sequences lane by lane, the others' sum
+  // the first sequences lane by lane, the others' sum
   int n0 = counted(tid), up = scan(n0);
   long long rest = 0;
   for (int b = tid + kThreads; b < P.B; b += kThreads) rest += counted(b);
@@ -420,29 +451,28 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
   // ---- the copies: this warp's tiles in order, K and V of each in turn
   const uint32_t ring =
       (uint32_t)__cvta_generic_to_shared(smem + Sh::kRingAt) + warp * (kSlots * Z::kSlot);
-  constexpr int kCpr = kRow / 16;             // 16-byte units of a row
-  constexpr int kIters = kTT * kCpr / 32;     // of a lane, for K or V of a tile
-  constexpr int kPerPage = kIters / kMT;      // 16 positions lie in one page, one run
-  static_assert(kIters % kMT == 0, "a lane's unit lies in one page");
+  constexpr int kCpr = kRow / 16, kVCpr = kVRow / 16;  // 16-byte units of a row
+  constexpr int kSteps = Z::kUnit / 512;               // of a warp, for its part of K or V
   const uint32_t k_lane = 16 * k_place<kRow>(lane / kCpr, lane % kCpr);
-  const uint32_t v_lane = 16 * v_place<kRow, kKind == kKvBf16>(lane / kCpr, lane % kCpr);
+  const uint32_t v_lane = 16 * v_place<kVRow, kKind == kKvBf16>(lane / kVCpr, lane % kVCpr);
+  const int v_from = lane / kVCpr * kRow + sub * kVRow + lane % kVCpr * 16;
   const int page_mask = (1 << P.c.page_shift) - 1;
   uint32_t bad = 0;            // slots with a page that is not there
   int put = 0;                 // the slot of the next unit
   bool begun = false;          // K of a tile is under way, its V comes next
   bool full = false;           // all of the tile's positions and pages are there
-  long long row_at[kMT];       // the tile's first rows in the cache, -1: none
+  long long row_at[kVT];       // the tile's first rows in the cache, -1: none
   int rows_on = 0;             // positions of the tile that are there
-  int pages[kMT];              // of the next tile, asked for a tile ahead
-  auto seek = [&]() {          // to the next chunk in which this warp has a tile
-    while (ahead.left > 0 && (ahead.c * kWarps + warp) * kTT >= ahead.len) {
+  int pages[kVT];              // of the next tile, asked for a tile ahead
+  auto seek = [&]() {          // to the next chunk in which this team has a tile
+    while (ahead.left > 0 && (ahead.c * Z::kTeams + team) * kTile >= ahead.len) {
       --ahead.left;
       if (++ahead.c == ahead.n && ahead.left > 0) next_item(ahead);
     }
     if (ahead.left > 0) {
-      const int pos = (ahead.c * kWarps + warp) * kTT;
+      const int pos = (ahead.c * Z::kTeams + team) * kTile;
 #pragma unroll
-      for (int i = 0; i < kMT; ++i) {
+      for (int i = 0; i < kVT; ++i) {
         const int col = (pos + 16 * i) >> P.c.page_shift;
         pages[i] = pos + 16 * i < ahead.len ? __ldg(P.table + (size_t)ahead.b * P.cols + col) : 0;
       }
@@ -453,12 +483,12 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
     if (v_next ? begun : ahead.left > 0) {
       const uint32_t slot = ring + put * Z::kSlot;
       if (!v_next) {
-        const int pos = (ahead.c * kWarps + warp) * kTT;
-        rows_on = min(ahead.len - pos, kTT);
-        full = rows_on == kTT;
+        const int pos = (ahead.c * Z::kTeams + team) * kTile;
+        rows_on = min(ahead.len - pos, kTile);
+        full = rows_on == kTile;
         bad &= ~(1u << put);
 #pragma unroll
-        for (int i = 0; i < kMT; ++i) {
+        for (int i = 0; i < kVT; ++i) {
           const bool ok = (unsigned)pages[i] < (unsigned)P.c.pages;
           if (!ok && 16 * i < rows_on) bad |= 1u << put;
           full &= ok;
@@ -470,33 +500,41 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
         if (++ahead.c == ahead.n && ahead.left > 0) next_item(ahead);
       }
       const unsigned char *from = static_cast<const unsigned char *>(v_next ? P.c.v : P.c.k);
+      // runs of 16 positions lie in one page
+      constexpr int kRuns = v_next ? kVT : kMT, kPer = kSteps / kRuns;
+      constexpr int kRowsStep = 32 / (v_next ? kVCpr : kCpr);
+      static_assert(kSteps % kRuns == 0 && kPer >= 1, "a step's rows lie in one page");
 #pragma unroll
-      for (int half = 0; half < kMT; ++half) {
-        const unsigned char *src = from + (size_t)max(row_at[half], 0ll) * kRow + 16 * lane;
+      for (int run = 0; run < kRuns; ++run) {
+        const int i = v_next ? run : kS == 1 ? run : sub;  // (kMT == 1 in teams)
+        const long long at = row_at[kVT == 1 ? 0 : kS == 1 || v_next ? run : 0];
+        const long long mine = kS == 1 || v_next ? at : sub ? row_at[kVT - 1] : row_at[0];
+        const unsigned char *src =
+            from + (size_t)max(mine, 0ll) * kRow + (v_next ? v_from : 16 * lane);
         // (a step's rows and the lane's row within it have no bit in common, so
         // their twists add up to the row's)
         auto place = [&](int j) {
-          const int step = half * kPerPage + j, r = step * (32 / kCpr);
+          const int step = run * kPer + j, r = step * kRowsStep;
           return slot + 512 * step +
-                 (v_next ? v_lane ^ (16 * v_twist<kRow, kKind == kKvBf16>(r))
+                 (v_next ? v_lane ^ (16 * v_twist<kVRow, kKind == kKvBf16>(r))
                          : k_lane ^ (16 * k_twist<kRow>(r)));
         };
         if (full) {
 #pragma unroll
-          for (int j = 0; j < kPerPage; ++j) cp16(place(j), src + 512 * j);
+          for (int j = 0; j < kPer; ++j) cp16(place(j), src + j * kRowsStep * kRow);
         } else {
 #pragma unroll
-          for (int j = 0; j < kPerPage; ++j) {
-            const int r = (32 * (half * kPerPage + j) + lane) / kCpr;
-            const bool on = row_at[half] >= 0 && r < rows_on;
-            cp16(place(j), on ? src + 512 * j : from, on);
+          for (int j = 0; j < kPer; ++j) {
+            const int r = 16 * i + j * kRowsStep + lane / (v_next ? kVCpr : kCpr);
+            const bool on = mine >= 0 && r < rows_on;
+            cp16(place(j), on ? src + j * kRowsStep * kRow : from, on);
           }
         }
       }
-      if (kKind != kKvBf16 && !v_next && lane < 2 * kTT / 4) {  // both scales, with K
-        const int which = lane / (kTT / 4), r = 4 * (lane % (kTT / 4));
+      if (kKind != kKvBf16 && !v_next && lane < 2 * Z::kOwn / 4) {  // both scales, with K
+        const int which = lane / (Z::kOwn / 4), r = 4 * (lane % (Z::kOwn / 4)) + sub * Z::kOwn;
         const float *s = which ? P.c.v_scale : P.c.k_scale;
-        const long long at = row_at[kMT == 1 ? 0 : r / 16];
+        const long long at = kVT == 1 || r < 16 ? row_at[0] : row_at[kVT - 1];
         const bool on = at >= 0 && r < rows_on;
         cp16(slot + Z::kUnit + 16 * lane, s + (on ? (size_t)(at + (r & 15)) : (size_t)0), on);
       }
@@ -519,7 +557,6 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
 
   float acc[kDT][R][4];
   float m[R][2], l[R][2];
-  int lim[R][2];  // positions that the lane's rows see
   int get = 0;
 
   while (here.left > 0) {
@@ -529,11 +566,11 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
     const int rows = min(8 * R, P.M * P.group - row0);
     const int len = here.len, start = here.start, seen_by_all = start + 1 + row0 / P.group;
 
-    // q's rows as the products' operands: warp w has rows w, w + 8, ..
+    // q's rows as the products' operands, a row a warp
     __syncthreads();  // (the last item's are read)
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int r = warp + 8 * i, row = row0 + r;
+#pragma unroll 1
+    for (int r = warp; r < 8 * R; r += kWarps) {
+      const int row = row0 + r, i = r / 8;
       const int mt = row / P.group, head = h * P.group + row - mt * P.group;
       const T *src = static_cast<const T *>(P.q) +
                      (((size_t)b * P.M + mt) * P.qh + head) * kHd;
@@ -581,16 +618,15 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
       }
     }
     __syncthreads();
-    float fac[R][2];
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         m[i][e] = kNone;
         l[i][e] = 0.0f;
-        fac[i][e] = factor[8 * i + 2 * t + e];
-        lim[i][e] = start + 1 + (row0 + 8 * i + 2 * t + e) / P.group;
       }
+    // positions that row r of the item sees
+    auto limit = [&](int r) { return min(len, start + 1 + (row0 + r) / P.group); };
 #pragma unroll
     for (int d = 0; d < kDT; ++d)
 #pragma unroll
@@ -600,10 +636,10 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
 
     int any = 0;
     for (int c = c0; c < c0 + n; ++c) {
-      const int pos = (c * kWarps + warp) * kTT;
+      const int pos = (c * Z::kTeams + team) * kTile, mypos = pos + sub * Z::kOwn;
       if (pos >= len) continue;
       any = 1;
-      const bool masked = pos + kTT > seen_by_all || pos + kTT > len;
+      const bool masked = pos + kTile > seen_by_all || pos + kTile > len;
       // ---- scores of the tile: 16 positions by 8 rows a product
       wait_for<kSlots - 2>();
       __syncwarp();
@@ -671,34 +707,37 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
                 smem + Sh::kRingAt + (warp * kSlots + get) * Z::kSlot + Z::kUnit);
             const int at = 16 * j + 8 * q + g;
             ks = sc[at];
-            vs[j][q] = sc[kTT + at];
+            vs[j][q] = sc[Z::kOwn + at];
             lv[j][q] = rough_log2(vs[j][q]) - kUp;
           }
 #pragma unroll
           for (int i = 0; i < R; ++i)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) s[j][i][2 * q + e] *= fac[i][e] * ks;
+            for (int e = 0; e < 2; ++e) s[j][i][2 * q + e] *= factor[8 * i + 2 * t + e] * ks;
         }
       if (masked) {
         // out of a row's sight: no weight.  A value's scale that is not finite
         // makes the rows that see it NaN by their sum, and counts as 0.
 #pragma unroll
-        for (int j = 0; j < kMT; ++j)
+        for (int i = 0; i < R; ++i)
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int at = pos + 16 * j + 8 * q + g;
-            const bool odd = kHalf && !(fabsf(vs[j][q]) <= 3.4e38f);
+          for (int e = 0; e < 2; ++e) {
+            const int lim = limit(8 * i + 2 * t + e) - mypos - g;
 #pragma unroll
-            for (int i = 0; i < R; ++i)
+            for (int j = 0; j < kMT; ++j)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                if (at >= lim[i][e] || at >= len)
+              for (int q = 0; q < 2; ++q) {
+                if (16 * j + 8 * q >= lim)
                   s[j][i][2 * q + e] = -INFINITY;
-                else if (odd)
+                else if (kHalf && !(fabsf(vs[j][q]) <= 3.4e38f))
                   l[i][e] = __uint_as_float(0x7fc00000u);
               }
-            if (odd) vs[j][q] = 0.0f;
           }
+#pragma unroll
+        for (int j = 0; j < kMT; ++j)
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            if (kHalf && !(fabsf(vs[j][q]) <= 3.4e38f)) vs[j][q] = 0.0f;
       }
 #pragma unroll
       for (int i = 0; i < R; ++i)
@@ -720,7 +759,16 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
           x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
           x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
           x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
-          grown |= x > m[i][e] + kSlack;
+          if (kS > 1 && g == 0) maxima[warp * 8 * R + 8 * i + 2 * t + e] = x;
+        }
+      if (kS > 1) team_sync(team);
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (kS > 1)
+            top[i][e] = fmaxf(top[i][e], maxima[(warp ^ 1) * 8 * R + 8 * i + 2 * t + e]);
+          grown |= top[i][e] > m[i][e] + kSlack;
         }
       if (__any_sync(kFull, grown)) {
 #pragma unroll
@@ -739,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
             for (int k = 0; k < 4; ++k) acc[d][i][k] *= a[k & 1];
         }
       }
-      uint2 w[kMT][R][kPP];
+      uint2 w[kVT][R][kPP];  // of the whole tile: the team's own first
 #pragma unroll
       for (int j = 0; j < kMT; ++j)
 #pragma unroll
@@ -760,6 +808,19 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
           for (int p = 0; p < kPP; ++p)
             w[j][i][p] = make_uint2(transposed(pr[0][p]), transposed(pr[1][p]));
         }
+      if (kS > 1) {
+        uint2 *const mine = weights + warp * (Sh::kWeights / 8) + lane;
+        const uint2 *const theirs = weights + (warp ^ 1) * (Sh::kWeights / 8) + lane;
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+          for (int p = 0; p < kPP; ++p) mine[(i * kPP + p) * 32] = w[0][i][p];
+        team_sync(team);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+          for (int p = 0; p < kPP; ++p) w[kVT - 1][i][p] = theirs[(i * kPP + p) * 32];
+      }
       if (broken) {
         if (P.err) *P.err = 1;
 #pragma unroll
@@ -776,40 +837,42 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
         // A row that some tokens do not see must not reach them, whatever it
         // holds: one with an element that is not finite is taken out, and the
         // rows that see it become NaN by their sum.
-        for (int r = 0; r < kTT; ++r) {
+        for (int r = 0; r < kTile; ++r) {
           if (pos + r <= start || pos + r >= len) continue;
           bool odd = false;
-          for (int c4 = lane; c4 < kCpr; c4 += 32) {
-            const uint4 q = lds128(slot + 16 * v_place<kRow, true>(r, c4));
+          for (int c4 = lane; c4 < kVCpr; c4 += 32) {
+            const uint4 q = lds128(slot + 16 * v_place<kVRow, true>(r, c4));
             const uint32_t e[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               odd |= (e[k] & 0x7f80u) == 0x7f80u || (e[k] & 0x7f800000u) == 0x7f800000u;
           }
           if (!__any_sync(kFull, odd)) continue;
-          for (int c4 = lane; c4 < kCpr; c4 += 32)
+          for (int c4 = lane; c4 < kVCpr; c4 += 32)
             asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                             slot + 16 * v_place<kRow, true>(r, c4)),
+                             slot + 16 * v_place<kVRow, true>(r, c4)),
                          "r"(0u)
                          : "memory");
 #pragma unroll
           for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              if (pos + r < lim[i][e]) l[i][e] = __uint_as_float(0x7fc00000u);
+              if (pos + r < limit(8 * i + 2 * t + e)) l[i][e] = __uint_as_float(0x7fc00000u);
         }
         __syncwarp();
       }
 #pragma unroll
-      for (int j = 0; j < kMT; ++j) {
+      for (int j = 0; j < kVT; ++j) {
+        // (in teams: the own 16 positions, then the other warp's)
+        const int row = kS == 1 ? 16 * j : 16 * (j ^ sub);
         if (kKind == kKvBf16) {
 #pragma unroll
           for (int d = 0; d < kDT; ++d) {
             uint32_t a0, a1, a2, a3;
-            const int r = 16 * j + (lane & 7) + 8 * (lane >> 4), cc = 2 * d + (lane >> 3 & 1);
+            const int r = row + (lane & 7) + 8 * (lane >> 4), cc = 2 * d + (lane >> 3 & 1);
             asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                          : "=r"(a0), "=r"(a1), "=r"(a2), "=r"(a3)
-                         : "r"(slot + 16 * v_place<kRow, true>(r, cc)));
+                         : "r"(slot + 16 * v_place<kVRow, true>(r, cc)));
 #pragma unroll
             for (int i = 0; i < R; ++i)
 #pragma unroll
@@ -818,18 +881,18 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
         } else {
           // four positions a lane, 16 channels of each (8 of 64): bytes of
           // neighbouring positions side by side make the pairs of an operand
-          constexpr int kWords = kHd == 64 ? 2 : 4;
+          constexpr int kWords = kVHd == 64 ? 2 : 4;
 #pragma unroll
-          for (int half = 0; half < (kHd == 256 ? 2 : 1); ++half) {
+          for (int half = 0; half < (kVHd == 256 ? 2 : 1); ++half) {
             uint32_t e[4][4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const int r = 16 * j + 2 * t + (q & 1) + 8 * (q >> 1);
-              if (kHd == 64) {
-                const uint2 v = lds64(slot + 16 * v_place<kRow, false>(r, g >> 1) + 8 * (g & 1));
+              const int r = row + 2 * t + (q & 1) + 8 * (q >> 1);
+              if (kVHd == 64) {
+                const uint2 v = lds64(slot + 16 * v_place<kVRow, false>(r, g >> 1) + 8 * (g & 1));
                 e[q][0] = v.x; e[q][1] = v.y;
               } else {
-                const uint4 v = lds128(slot + 16 * v_place<kRow, false>(r, g + 8 * half));
+                const uint4 v = lds128(slot + 16 * v_place<kVRow, false>(r, g + 8 * half));
                 e[q][0] = v.x; e[q][1] = v.y; e[q][2] = v.z; e[q][3] = v.w;
               }
             }
@@ -870,9 +933,9 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
     if (lane == 0) rooms[warp] = any ? (signed char)mine : (signed char)-1;
     float *const own = reinterpret_cast<float *>(smem + Sh::kRingAt + (warp * kSlots + mine) * Z::kSlot);
     // 16-byte unit q of a row of fp32 sums
-    constexpr int kStage = Z::kStage, kRounds = kHd / kStage;
+    constexpr int kStage = Z::kStage, kRounds = kVHd / kStage;
     // channels side by side of a lane, in a round (8 bits)
-    constexpr int kRun = kHd == 64 || (kHd == 128 && kRounds == 2) ? 8 : 16;
+    constexpr int kRun = kVHd == 64 || (kVHd == 128 && kRounds == 2) ? 8 : 16;
     auto unit = [](int r, int q) { return r * (kStage / 4) + (q ^ (((q >> 2) ^ (q >> 5) ^ r) & 7)); };
     __syncwarp();
     float *const parts =
@@ -892,13 +955,13 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
               }
           } else {
             // tile 8 half + j: channels 2 j and 2 j + 1 of lane g's run
-            static_assert(kStage == kHd || kHd >= 128, "a round is a half");
+            static_assert(kStage == kVHd || kVHd >= 128, "a round is a half");
 #pragma unroll
             for (int d = 0; d < kStage / 16; d += 2)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const int tile = rd * (kStage / 16) + d;
-                const int ch = (kHd == 256 ? 128 * (d / 8) : 0) + kRun * g + 2 * (d % 8);
+                const int ch = (kVHd == 256 ? 128 * (d / 8) : 0) + kRun * g + 2 * (d % 8);
                 *reinterpret_cast<float4 *>(own + 4 * unit(2 * t + e, ch / 4)) =
                     make_float4(acc[tile][i][e], acc[tile][i][2 + e], acc[tile + 1][i][e],
                                 acc[tile + 1][i][2 + e]);
@@ -906,8 +969,9 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
           }
         }
         __syncthreads();
-        for (int q = tid; q < 8 * (kStage / 4); q += kThreads) {
-          const int r8 = q / (kStage / 4), cq = q % (kStage / 4), r = r8 + 8 * i, row = row0 + r;
+        for (int q = tid; q < 8 * kS * (kStage / 4); q += kThreads) {
+          const int r8 = q / (kS * (kStage / 4)), cs = q / (kStage / 4) % kS, cq = q % (kStage / 4);
+          const int r = r8 + 8 * i, row = row0 + r;
           if (r >= rows) continue;
           float top = kNone, sum = 0.0f;
 #pragma unroll
@@ -920,13 +984,14 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
             const float2 ml = stat[w * 8 * R + r];
             const float f = exp2_(ml.x - top);
             sum += ml.y * f;
+            if (w % kS != cs) continue;  // (the other half of the channels)
             const float4 v = reinterpret_cast<const float4 *>(
                 smem + Sh::kRingAt + (w * kSlots + sl) * Z::kSlot)[unit(r8, cq)];
             o[0] += v.x * f; o[1] += v.y * f; o[2] += v.z * f; o[3] += v.w * f;
           }
-          const int ch = kKind != kKvBf16 && kHd == 128 && kRounds == 2
-                             ? 16 * (cq / 2) + 8 * rd + 4 * (cq & 1)
-                             : rd * kStage + 4 * cq;
+          const int ch = cs * kVHd + (kKind != kKvBf16 && kVHd == 128 && kRounds == 2
+                                          ? 16 * (cq / 2) + 8 * rd + 4 * (cq & 1)
+                                          : rd * kStage + 4 * cq);
           if (whole) {
             const int mt = row / P.group, head = h * P.group + row - mt * P.group;
             const size_t at = ((size_t)b * P.M + mt) * P.qh + head;
@@ -1051,6 +1116,7 @@ cudaError_t go(const AttnArgs &P, cudaStream_t stream) {
   using Z = Sizes<kHd, kKind, R>;
   using Sh = Shared<kHd, kKind, kBf16, R>;
   static_assert(Sh::kBytes * Z::kCtas <= 227 * 1024 - 1024 * (Z::kCtas - 1), "shared memory");
+  static_assert(Z::kCtas <= ((kHd == 256 && R > 1) || R > 2 ? 1 : 2), "parts of the workspace");
   static_assert(Z::kSlots >= 3 && 32 * Z::kStage <= Z::kSlot, "rings");
   const int grid = grid_of<Z>(P.B, P.M, P.group, P.c.kvh, R,
                                        (long long)P.cols << P.c.page_shift);
@@ -1062,7 +1128,7 @@ cudaError_t go(const AttnArgs &P, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Z::kThreads);
   cfg.dynamicSmemBytes = Sh::kBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1073,33 +1139,47 @@ cudaError_t go(const AttnArgs &P, cudaStream_t stream) {
   e = cudaLaunchKernelEx(&cfg, kernel, P);
   if (e != cudaSuccess || grid == 1) return e;
   cfg.gridDim = dim3((unsigned)rows);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, attn_join_kernel<kHd, kKind, kBf16, R>, P, grid);
 }
 
-// Row tiles of 8 or 16.
-inline int tile_rows(int M, int group) { return (long long)M * group <= 8 ? 1 : 2; }
+// Row tiles of 8, 16 or (8 bits, teams) 24: the fewest eights of rows, and of two
+// ways with as many the one with fewer passes over the cache.
+inline int tile_rows(int kind, int hd, int M, int group) {
+  const long long rows = (long long)M * group;
+  if (rows <= 8) return 1;
+  const bool three = kind != kKvBf16 && hd > 64;
+  return three && (rows + 23) / 24 * 3 <= (rows + 15) / 16 * 2 ? 3 : 2;
+}
+
+template <int kHd, int kKind, int R>
+cudaError_t by_type(const AttnArgs &P, bool bf16, cudaStream_t stream) {
+  return bf16 ? go<kHd, kKind, true, R>(P, stream) : go<kHd, kKind, false, R>(P, stream);
+}
 
 template <int kHd, int kKind>
-cudaError_t by_type(const AttnArgs &P, bool bf16, cudaStream_t stream) {
-  if (tile_rows(P.M, P.group) == 1)
-    return bf16 ? go<kHd, kKind, true, 1>(P, stream) : go<kHd, kKind, false, 1>(P, stream);
-  return bf16 ? go<kHd, kKind, true, 2>(P, stream) : go<kHd, kKind, false, 2>(P, stream);
+cudaError_t by_rows(const AttnArgs &P, bool bf16, cudaStream_t stream) {
+  const int R = tile_rows(kKind, kHd, P.M, P.group);
+  if (R == 1) return by_type<kHd, kKind, 1>(P, bf16, stream);
+  if constexpr (kKind != kKvBf16 && kHd > 64) {
+    if (R == 3) return by_type<kHd, kKind, 3>(P, bf16, stream);
+  }
+  return by_type<kHd, kKind, 2>(P, bf16, stream);
 }
 
 template <int kHd>
 cudaError_t launch(const AttnArgs &P, bool bf16, cudaStream_t stream) {
-  return P.c.kind == kKvBf16   ? by_type<kHd, kKvBf16>(P, bf16, stream)
-         : P.c.kind == kKvInt8 ? by_type<kHd, kKvInt8>(P, bf16, stream)
-                               : by_type<kHd, kKvE4m3>(P, bf16, stream);
+  return P.c.kind == kKvBf16   ? by_rows<kHd, kKvBf16>(P, bf16, stream)
+         : P.c.kind == kKvInt8 ? by_rows<kHd, kKvInt8>(P, bf16, stream)
+                               : by_rows<kHd, kKvE4m3>(P, bf16, stream);
 }
 
-// Bytes of the parts: two for each CTA.
-template <int kHd>
-size_t bytes(int M, int group) {
-  const int R = tile_rows(M, group);
-  const int ctas = kSms * (R == 1 ? Sizes<kHd, kKvInt8, 1>::kCtas : Sizes<kHd, kKvInt8, 2>::kCtas);
-  return (size_t)ctas * 2 * (8 * R) * (kHd + 4) * 4;
+// Bytes of the parts: two for each CTA, of which an SM has at most two.
+inline size_t bytes(int kind, int M, int group, int hd) {
+  const int R = tile_rows(kind, hd, M, group);
+  const int ctas = kSms * ((hd == 256 && R > 1) || R > 2 ? 1 : 2);
+  return (size_t)ctas * 2 * (8 * R) * (hd + 4) * 4;
 }
 
 }  // namespace attn

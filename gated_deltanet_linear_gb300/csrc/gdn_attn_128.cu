@@ -15,10 +15,8 @@ cudaError_t launch_attn(const AttnArgs &P, int hd, bool bf16, cudaStream_t strea
                      : launch_attn_256(P, bf16, stream);
 }
 
-size_t attn_workspace_bytes(int M, int group, int hd) {
-  return hd == 64    ? attn::bytes<64>(M, group)
-         : hd == 128 ? attn::bytes<128>(M, group)
-                     : attn::bytes<256>(M, group);
+size_t attn_workspace_bytes(int kind, int M, int group, int hd) {
+  return attn::bytes(kind, M, group, hd);
 }
 
 }  // namespace gdn

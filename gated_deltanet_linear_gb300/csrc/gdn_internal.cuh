@@ -149,7 +149,7 @@ struct AttnArgs {
   int B, M, cols, qh, group;
   float *part;  // the workspace
 };
-size_t attn_workspace_bytes(int M, int group, int hd);
+size_t attn_workspace_bytes(int kind, int M, int group, int hd);
 cudaError_t launch_attn(const AttnArgs &P, int hd, bool bf16, cudaStream_t stream);
 
 // Chunked tensor-core prefill (defined in gdn_prefill.cu).

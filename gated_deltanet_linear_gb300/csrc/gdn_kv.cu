@@ -243,7 +243,7 @@ __device__ __forceinline__ unsigned lanes_of_row() {
 // with kLanes lanes, and a run of P.run of their heads (q, k and v side by side),
 // the same for all of them.
 template <typename T, int kKind, int kLanes>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 4)
     kv_rows_kernel(const KvRows P) {
   constexpr int kHd = 8 * kLanes, kTokens = 32 / kLanes;
   __shared__ unsigned long long phase[kMaxHalf];

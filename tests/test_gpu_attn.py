@@ -57,7 +57,7 @@ LENS = [1, 2, 15, 16, 17, 31, 33, 64, 127, 128, 129, 255, 256, 257, 400, 513, 10
 @pytest.mark.parametrize("kind", ["bf16", "int8", "e4m3"])
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("M,kvh,group,page", [(1, 2, 4, 16), (1, 1, 8, 64), (2, 3, 1, 32), (1, 2, 13, 128),
-                                              (4, 1, 6, 256), (3, 2, 5, 16)])
+                                              (4, 1, 6, 256), (3, 2, 5, 16), (7, 2, 3, 64), (5, 1, 9, 32)])
 def test_against_64_bits(hd, kind, dtype, M, kvh, group, page):
     gen = gen_of(hd + M + group)
     lens = [n for n in LENS if n >= M]
