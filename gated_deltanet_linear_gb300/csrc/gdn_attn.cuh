@@ -58,8 +58,8 @@ namespace attn {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kWarps = 8, kThreads = 32 * kWarps;  // of attn_join_kernel
 constexpr float kNone = -1e30f;  // the reference of rows that have seen nothing
-constexpr float kSlack = 3.0f;   // how far the maximum may pass it (log2)
-constexpr float kUp = 12.0f;     // weights of 8-bit rows reach 2^12 (+ kSlack)
+constexpr float kUp = 12.0f;     // weights of 8-bit rows are brought to 2^12,
+constexpr float kTop = 32768.0f;  // and may grow to this before they are again
 constexpr int kSms = 152;
 
 // Sizes of a variant: R tiles of 8 rows.  kS warps share a tile of positions (a
@@ -76,7 +76,10 @@ struct Sizes {
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kTeams = kWarps / kS;
   static constexpr int kRow = kHd * kBytes;               // bytes of a row
-  static constexpr int kTile = kRow <= 128 || kS == 2 ? 32 : 16;  // positions of a tile
+  // positions of a tile: 32, or as many as leave a ring of three parts, or (64
+  // channels, 16 rows) as fit the registers
+  static constexpr int kTile =
+      kS == 2 ? 32 : kRow > 128 || (kHd == 64 && R == 2) ? 16 : 32;
   static constexpr int kOwn = kTile / kS;                 // of them a warp's, for the scores
   static constexpr int kVHd = kHd / kS;                   // a warp's channels of v
   static constexpr int kVRow = kRow / kS;
@@ -119,6 +122,13 @@ __device__ __forceinline__ int length_of(const AttnArgs &P, int b, int &start) {
   const long long room = (long long)P.cols << P.c.page_shift;
   if (n <= 0 || n > P.M || start < 0 || (long long)start + n > room) return 0;
   return start + n;
+}
+
+// Units of an item in the list: its chunks and one more without positions, which
+// is what its start and its join cost (64 sequences of up to 8192: 113 us without).
+template <class Z>
+__host__ __device__ __forceinline__ int units_of(int len) {
+  return (len + Z::kChunk - 1) / Z::kChunk + (len > 0);
 }
 
 __device__ __forceinline__ void cp16(uint32_t to, const void *from, bool on) {
@@ -204,18 +214,10 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t &even, uint32_t &odd)
         : "r"(w));
   }
 }
-// The same of two words, the pairs' first numbers from the first: bytes k and
-// k + 1 (k = 0 or 2) of both.
+// Bytes 0 and 2, 1 and 3 of any kind.
 template <int kKind>
-__device__ __forceinline__ void widen2(uint32_t v, uint32_t w, int k, uint32_t &lo, uint32_t &hi) {
-  if (kKind == kKvInt8) {
-    widen<kKind>(prmt(v, w, k ? 0x7632 : 0x5410), lo, hi);
-  } else {
-    asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\n"
-        "cvt.rn.f16x2.e4m3x2 %0, l;\ncvt.rn.f16x2.e4m3x2 %1, h;\n}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(prmt(v, w, k ? 0x7362 : 0x5140)));
-  }
+__device__ __forceinline__ void widen_v(uint32_t w, uint32_t &even, uint32_t &odd) {
+  widen<kKind>(kKind == kKvInt8 ? w : prmt(w, w, 0x3120), even, odd);
 }
 
 // Two numbers as pairs of 16-bit parts: p[0] the nearest, p[i] of what is left.
@@ -296,17 +298,17 @@ template <int kRow>
 __host__ __device__ constexpr int k_twist(int r) {
   return kRow == 64 ? 0 : (r & 1) << 2;
 }
-template <int kRow, bool kBf16Cache>
+template <int kRow>
 __host__ __device__ constexpr int v_twist(int r) {
-  return kBf16Cache ? r & 7 : ((r >> 1) & 3) << 1;
+  return kRow == 64 ? (r >> 1) & 3 : r & 7;
 }
 template <int kRow>
 __device__ __forceinline__ int k_place(int r, int c) {
   return r * (kRow / 16) + (c ^ k_twist<kRow>(r));
 }
-template <int kRow, bool kBf16Cache>
+template <int kRow>
 __device__ __forceinline__ int v_place(int r, int c) {
-  return (r * (kRow / 16) + c) ^ v_twist<kRow, kBf16Cache>(r);
+  return (r * (kRow / 16) + c) ^ v_twist<kRow>(r);
 }
 
 template <int kHd, int kKind, bool kBf16, int R>
@@ -321,7 +323,7 @@ struct Shared {
   // between the warps of a team: maxima, and a tile's weights
   static constexpr int kWeights = Z::kOwn / 16 * R * Parts<kKind, kBf16>::kP * 256;
   static constexpr int kBytes =
-      kWeightsAt + (Z::kS == 1 ? 0 : Z::kWarps * (kWeights + 8 * R * 4));
+      kWeightsAt + (Z::kS == 1 ? 0 : Z::kWarps * (2 * kWeights + 8 * R * 4 + 8));
 };
 
 template <int kHd, int kKind, bool kBf16, int R>
@@ -352,12 +354,13 @@ __global__ void __launch_bounds__(Sizes<kHd, kKind, R>::kThreads, Sizes<kHd, kKi
   long long *const room = reinterpret_cast<long long *>(factor + 8 * R);
   int *const found = reinterpret_cast<int *>(room + 2 * kWarps);  // [3]
   uint2 *const weights = reinterpret_cast<uint2 *>(smem + Sh::kWeightsAt);
-  float *const maxima = reinterpret_cast<float *>(smem + Sh::kWeightsAt + kWarps * Sh::kWeights);
+  float *const maxima = reinterpret_cast<float *>(smem + Sh::kWeightsAt + 2 * kWarps * Sh::kWeights);
+  volatile int *const flags = reinterpret_cast<int *>(maxima + kWarps * 8 * R);  // [warp][2]
   signed char *const rooms = reinterpret_cast<signed char *>(found + 4);  // [kWarps]
 
   // ---- this CTA's share: chunks [u0, u1) of the list, from sequence b0 on
   auto chunks = [&](int b, int &start) {
-    return (length_of(P, b, start) + Z::kChunk - 1) / Z::kChunk;
+    return units_of<Z>(length_of(P, b, start));
   };
   auto counted = [&](int b) {
     if (b >= P.B) return 0;
@@ -431,7 +434,7 @@ __global__ void __launch_bounds__(Sizes<kHd, kKind, R>::kThreads, Sizes<kHd, kKi
   };
   auto enter = [&](Walk &w) {
     w.len = length_of(P, w.b, w.start);
-    w.n = (w.len + Z::kChunk - 1) / Z::kChunk;
+    w.n = units_of<Z>(w.len);
   };
   auto next_item = [&](Walk &w) {  // (only while chunks are left)
     w.c = 0;
@@ -454,7 +457,7 @@ __global__ void __launch_bounds__(Sizes<kHd, kKind, R>::kThreads, Sizes<kHd, kKi
   constexpr int kCpr = kRow / 16, kVCpr = kVRow / 16;  // 16-byte units of a row
   constexpr int kSteps = Z::kUnit / 512;               // of a warp, for its part of K or V
   const uint32_t k_lane = 16 * k_place<kRow>(lane / kCpr, lane % kCpr);
-  const uint32_t v_lane = 16 * v_place<kVRow, kKind == kKvBf16>(lane / kVCpr, lane % kVCpr);
+  const uint32_t v_lane = 16 * v_place<kVRow>(lane / kVCpr, lane % kVCpr);
   const int v_from = lane / kVCpr * kRow + sub * kVRow + lane % kVCpr * 16;
   const int page_mask = (1 << P.c.page_shift) - 1;
   uint32_t bad = 0;            // slots with a page that is not there
@@ -516,7 +519,7 @@ __global__ void __launch_bounds__(Sizes<kHd, kKind, R>::kThreads, Sizes<kHd, kKi
         auto place = [&](int j) {
           const int step = run * kPer + j, r = step * kRowsStep;
           return slot + 512 * step +
-                 (v_next ? v_lane ^ (16 * v_twist<kVRow, kKind == kKvBf16>(r))
+                 (v_next ? v_lane ^ (16 * v_twist<kVRow>(r))
                          : k_lane ^ (16 * k_twist<kRow>(r)));
         };
         if (full) {
@@ -557,7 +560,7 @@ __global__ void __launch_bounds__(Sizes<kHd, kKind, R>::kThreads, Sizes<kHd, kKi
 
   float acc[kDT][R][4];
   float m[R][2], l[R][2];
-  int get = 0;
+  int get = 0, turn = 0;  // (turn: of two buffers between the warps of a team)
 
   while (here.left > 0) {
     // ---- an item's part: chunks [here.c, here.c + n)
@@ -696,28 +699,29 @@ __global__ void __launch_bounds__(Sizes<kHd, kKind, R>::kThreads, Sizes<kHd, kKi
 #pragma unroll
             for (int k = 0; k < 4; ++k) s[j][i][k] += part[kC - 1][j][i][k];
       }
-      float vs[kMT][2], lv[kMT][2], top[R][2];
+      float ks[kMT][2], vs[kMT][2];
 #pragma unroll
       for (int j = 0; j < kMT; ++j)
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          float ks = 1.0f;
+          ks[j][q] = vs[j][q] = 1.0f;
           if (kHalf) {
             const float *sc = reinterpret_cast<const float *>(
                 smem + Sh::kRingAt + (warp * kSlots + get) * Z::kSlot + Z::kUnit);
             const int at = 16 * j + 8 * q + g;
-            ks = sc[at];
+            ks[j][q] = sc[at];
             vs[j][q] = sc[Z::kOwn + at];
-            lv[j][q] = rough_log2(vs[j][q]) - kUp;
           }
-#pragma unroll
-          for (int i = 0; i < R; ++i)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) s[j][i][2 * q + e] *= factor[8 * i + 2 * t + e] * ks;
         }
+      float f[R][2];  // a row's factor
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) f[i][e] = factor[8 * i + 2 * t + e];
       if (masked) {
-        // out of a row's sight: no weight.  A value's scale that is not finite
-        // makes the rows that see it NaN by their sum, and counts as 0.
+        // Out of a row's sight: no weight, whatever key and scales may be.  A
+        // value's scale that is not finite makes the rows that see it NaN by
+        // their sum, and counts as 0.
 #pragma unroll
         for (int i = 0; i < R; ++i)
 #pragma unroll
@@ -727,56 +731,91 @@ __global__ void __launch_bounds__(Sizes<kHd, kKind, R>::kThreads, Sizes<kHd, kKi
             for (int j = 0; j < kMT; ++j)
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
-                if (16 * j + 8 * q >= lim)
-                  s[j][i][2 * q + e] = -INFINITY;
-                else if (kHalf && !(fabsf(vs[j][q]) <= 3.4e38f))
-                  l[i][e] = __uint_as_float(0x7fc00000u);
+                float &x = s[j][i][2 * q + e];
+                const bool seen = 16 * j + 8 * q < lim;
+                x = seen ? x * (f[i][e] * ks[j][q]) : -INFINITY;
+                if (kHalf && seen && !(fabsf(vs[j][q]) <= 3.4e38f)) l[i][e] = __uint_as_float(0x7fc00000u);
               }
+            f[i][e] = 1.0f;
           }
 #pragma unroll
         for (int j = 0; j < kMT; ++j)
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
+          for (int q = 0; q < 2; ++q) {
+            ks[j][q] = 1.0f;
             if (kHalf && !(fabsf(vs[j][q]) <= 3.4e38f)) vs[j][q] = 0.0f;
+          }
       }
+      // Weights with the reference as it is; where one is too large for that
+      // (or NaN, which the first tile's may be) the reference is set anew.
+      uint2 w[kVT][R][kPP];  // of the whole tile: the team's own first
+      float p[kMT][R][4];
+      auto weigh = [&]() {  // true: one does not fit
+        bool off = false;
 #pragma unroll
-      for (int i = 0; i < R; ++i)
+        for (int j = 0; j < kMT; ++j)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          top[i][e] = kNone;
+          for (int i = 0; i < R; ++i) {
+            uint32_t pr[2][kPP];
 #pragma unroll
-          for (int j = 0; j < kMT; ++j)
+            for (int q = 0; q < 2; ++q) {
+              float y[2];
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-              top[i][e] = fmaxf(top[i][e], kHalf ? s[j][i][2 * q + e] + lv[j][q] : s[j][i][2 * q + e]);
-        }
-      bool grown = false;
+              for (int e = 0; e < 2; ++e) {
+                float &x = p[j][i][2 * q + e];
+                x = exp2_(fmaf(s[j][i][2 * q + e], f[i][e] * ks[j][q], -m[i][e]));
+                y[e] = kHalf ? x * vs[j][q] : x;
+                off |= !(y[e] <= kTop);
+              }
+              cut<kHalf, kPP>(y[0], y[1], pr[q]);
+            }
 #pragma unroll
-      for (int i = 0; i < R; ++i)
+            for (int k = 0; k < kPP; ++k)
+              w[j][i][k] = make_uint2(transposed(pr[0][k]), transposed(pr[1][k]));
+          }
+        return __any_sync(kFull, off) != 0;
+      };
+      // to the other warp of the team, with whether the weights fit
+      auto hand_over = [&](bool off) {
+        uint2 *const mine = weights + (warp * 2 + turn) * (Sh::kWeights / 8) + lane;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float &x = top[i][e];
-          x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
-          if (kS > 1 && g == 0) maxima[warp * 8 * R + 8 * i + 2 * t + e] = x;
-        }
-      if (kS > 1) team_sync(team);
+        for (int i = 0; i < R; ++i)
 #pragma unroll
-      for (int i = 0; i < R; ++i)
+          for (int k = 0; k < kPP; ++k) mine[(i * kPP + k) * 32] = w[0][i][k];
+        if (lane == 0) flags[warp * 2 + turn] = off;
+        team_sync(team);
+        return flags[(warp ^ 1) * 2 + turn] != 0;
+      };
+      bool off = weigh();
+      if (kS > 1) off |= hand_over(off);
+      if (off) {
+        float top[R][2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (kS > 1)
-            top[i][e] = fmaxf(top[i][e], maxima[(warp ^ 1) * 8 * R + 8 * i + 2 * t + e]);
-          grown |= top[i][e] > m[i][e] + kSlack;
-        }
-      if (__any_sync(kFull, grown)) {
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float &x = top[i][e];
+            x = kNone;
+#pragma unroll
+            for (int j = 0; j < kMT; ++j)
+#pragma unroll
+              for (int q = 0; q < 2; ++q)
+                x = fmaxf(x, s[j][i][2 * q + e] * (f[i][e] * ks[j][q]) +
+                                 (kHalf ? rough_log2(vs[j][q]) - kUp : 0.0f));
+            x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
+            if (kS > 1 && g == 0) maxima[warp * 8 * R + 8 * i + 2 * t + e] = x;
+          }
+        if (kS > 1) team_sync(team);
 #pragma unroll
         for (int i = 0; i < R; ++i) {
           float a[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float to = top[i][e] > m[i][e] + kSlack ? top[i][e] : m[i][e];
+            if (kS > 1)
+              top[i][e] = fmaxf(top[i][e], maxima[(warp ^ 1) * 8 * R + 8 * i + 2 * t + e]);
+            const float to = fmaxf(top[i][e], m[i][e]);
             a[e] = exp2_(m[i][e] - to);
             m[i][e] = to;
             l[i][e] *= a[e];
@@ -786,40 +825,25 @@ __global__ void __launch_bounds__(Sizes<kHd, kKind, R>::kThreads, Sizes<kHd, kKi
 #pragma unroll
             for (int k = 0; k < 4; ++k) acc[d][i][k] *= a[k & 1];
         }
+        weigh();
+        if (kS > 1) {
+          turn ^= 1;  // (the other has read the first ones' flag by the second barrier)
+          hand_over(false);
+        }
       }
-      uint2 w[kVT][R][kPP];  // of the whole tile: the team's own first
 #pragma unroll
       for (int j = 0; j < kMT; ++j)
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-          uint32_t pr[2][kPP];
+        for (int i = 0; i < R; ++i)
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            float y[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float p = exp2_(s[j][i][2 * q + e] - m[i][e]);
-              y[e] = kHalf ? p * vs[j][q] : p;
-              l[i][e] += p;
-            }
-            cut<kHalf, kPP>(y[0], y[1], pr[q]);
-          }
-#pragma unroll
-          for (int p = 0; p < kPP; ++p)
-            w[j][i][p] = make_uint2(transposed(pr[0][p]), transposed(pr[1][p]));
-        }
+          for (int e = 0; e < 2; ++e) l[i][e] += p[j][i][e] + p[j][i][2 + e];
       if (kS > 1) {
-        uint2 *const mine = weights + warp * (Sh::kWeights / 8) + lane;
-        const uint2 *const theirs = weights + (warp ^ 1) * (Sh::kWeights / 8) + lane;
+        const uint2 *const theirs = weights + ((warp ^ 1) * 2 + turn) * (Sh::kWeights / 8) + lane;
 #pragma unroll
         for (int i = 0; i < R; ++i)
 #pragma unroll
-          for (int p = 0; p < kPP; ++p) mine[(i * kPP + p) * 32] = w[0][i][p];
-        team_sync(team);
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-#pragma unroll
-          for (int p = 0; p < kPP; ++p) w[kVT - 1][i][p] = theirs[(i * kPP + p) * 32];
+          for (int k = 0; k < kPP; ++k) w[kVT - 1][i][k] = theirs[(i * kPP + k) * 32];
+        turn ^= 1;
       }
       if (broken) {
         if (P.err) *P.err = 1;
@@ -841,7 +865,7 @@ __global__ void __launch_bounds__(Sizes<kHd, kKind, R>::kThreads, Sizes<kHd, kKi
           if (pos + r <= start || pos + r >= len) continue;
           bool odd = false;
           for (int c4 = lane; c4 < kVCpr; c4 += 32) {
-            const uint4 q = lds128(slot + 16 * v_place<kVRow, true>(r, c4));
+            const uint4 q = lds128(slot + 16 * v_place<kVRow>(r, c4));
             const uint32_t e[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -850,7 +874,7 @@ __global__ void __launch_bounds__(Sizes<kHd, kKind, R>::kThreads, Sizes<kHd, kKi
           if (!__any_sync(kFull, odd)) continue;
           for (int c4 = lane; c4 < kVCpr; c4 += 32)
             asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                             slot + 16 * v_place<kVRow, true>(r, c4)),
+                             slot + 16 * v_place<kVRow>(r, c4)),
                          "r"(0u)
                          : "memory");
 #pragma unroll
@@ -865,50 +889,30 @@ __global__ void __launch_bounds__(Sizes<kHd, kKind, R>::kThreads, Sizes<kHd, kKi
       for (int j = 0; j < kVT; ++j) {
         // (in teams: the own 16 positions, then the other warp's)
         const int row = kS == 1 ? 16 * j : 16 * (j ^ sub);
-        if (kKind == kKvBf16) {
+        // four 8 x 8 tiles of 16 bits, transposed: neighbouring positions of a
+        // channel side by side (bf16), or of two channels (8 bits: two tiles of
+        // 16 channels, even ones in the upper half of a product's rows)
+        constexpr int kStep = kKind == kKvBf16 ? 1 : 2;
 #pragma unroll
-          for (int d = 0; d < kDT; ++d) {
-            uint32_t a0, a1, a2, a3;
-            const int r = row + (lane & 7) + 8 * (lane >> 4), cc = 2 * d + (lane >> 3 & 1);
-            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(a0), "=r"(a1), "=r"(a2), "=r"(a3)
-                         : "r"(slot + 16 * v_place<kVRow, true>(r, cc)));
+        for (int d = 0; d < kDT; d += kStep) {
+          uint32_t x[4];
+          const int r = row + (lane & 7) + 8 * (kStep == 1 ? lane >> 4 : lane >> 3 & 1);
+          const int cc = kStep == 1 ? 2 * d + (lane >> 3 & 1) : d + (lane >> 4);
+          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                       : "r"(slot + 16 * v_place<kVRow>(r, cc)));
+#pragma unroll
+          for (int q = 0; q < kStep; ++q) {
+            uint32_t a[4] = {x[0], x[1], x[2], x[3]};
+            if (kHalf) {
+              widen_v<kKind>(x[2 * q], a[0], a[1]);
+              widen_v<kKind>(x[2 * q + 1], a[2], a[3]);
+            }
 #pragma unroll
             for (int i = 0; i < R; ++i)
 #pragma unroll
-              for (int p = 0; p < kPP; ++p) mma<false>(acc[d][i], a0, a1, a2, a3, w[j][i][p]);
-          }
-        } else {
-          // four positions a lane, 16 channels of each (8 of 64): bytes of
-          // neighbouring positions side by side make the pairs of an operand
-          constexpr int kWords = kVHd == 64 ? 2 : 4;
-#pragma unroll
-          for (int half = 0; half < (kVHd == 256 ? 2 : 1); ++half) {
-            uint32_t e[4][4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int r = row + 2 * t + (q & 1) + 8 * (q >> 1);
-              if (kVHd == 64) {
-                const uint2 v = lds64(slot + 16 * v_place<kVRow, false>(r, g >> 1) + 8 * (g & 1));
-                e[q][0] = v.x; e[q][1] = v.y;
-              } else {
-                const uint4 v = lds128(slot + 16 * v_place<kVRow, false>(r, g + 8 * half));
-                e[q][0] = v.x; e[q][1] = v.y; e[q][2] = v.z; e[q][3] = v.w;
-              }
-            }
-#pragma unroll
-            for (int k = 0; k < kWords; ++k)
-#pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                uint32_t a[4];
-                widen2<kKind>(e[0][k], e[1][k], 2 * q, a[0], a[1]);
-                widen2<kKind>(e[2][k], e[3][k], 2 * q, a[2], a[3]);
-#pragma unroll
-                for (int i = 0; i < R; ++i)
-#pragma unroll
-                  for (int p = 0; p < kPP; ++p)
-                    mma<true>(acc[8 * half + 2 * k + q][i], a[0], a[1], a[2], a[3], w[j][i][p]);
-              }
+              for (int p = 0; p < kPP; ++p)
+                mma<kHalf>(acc[d + q][i], a[0], a[1], a[2], a[3], w[j][i][p]);
           }
         }
       }
@@ -934,8 +938,6 @@ __global__ void __launch_bounds__(Sizes<kHd, kKind, R>::kThreads, Sizes<kHd, kKi
     float *const own = reinterpret_cast<float *>(smem + Sh::kRingAt + (warp * kSlots + mine) * Z::kSlot);
     // 16-byte unit q of a row of fp32 sums
     constexpr int kStage = Z::kStage, kRounds = kVHd / kStage;
-    // channels side by side of a lane, in a round (8 bits)
-    constexpr int kRun = kVHd == 64 || (kVHd == 128 && kRounds == 2) ? 8 : 16;
     auto unit = [](int r, int q) { return r * (kStage / 4) + (q ^ (((q >> 2) ^ (q >> 5) ^ r) & 7)); };
     __syncwarp();
     float *const parts =
@@ -945,27 +947,19 @@ __global__ void __launch_bounds__(Sizes<kHd, kKind, R>::kThreads, Sizes<kHd, kKi
 #pragma unroll
       for (int rd = 0; rd < kRounds; ++rd) {
         if (any) {
-          if (kKind == kKvBf16) {
 #pragma unroll
-            for (int d = 0; d < kStage / 16; ++d)
+          for (int d = 0; d < kStage / 16; ++d) {
+            const float (&x)[4] = acc[rd * (kStage / 16) + d][i];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int ch = 16 * d + g + 8 * (k >> 1);
-                own[4 * unit(2 * t + (k & 1), ch / 4) + (ch & 3)] = acc[rd * (kStage / 16) + d][i][k];
+            for (int e = 0; e < 2; ++e) {
+              if (kKind == kKvBf16) {  // channels g and g + 8 of 16
+                own[4 * unit(2 * t + e, 4 * d + g / 4) + (g & 3)] = x[e];
+                own[4 * unit(2 * t + e, 4 * d + 2 + g / 4) + (g & 3)] = x[2 + e];
+              } else {  // 2 g and 2 g + 1
+                *reinterpret_cast<float2 *>(own + 4 * unit(2 * t + e, 4 * d + g / 2) + 2 * (g & 1)) =
+                    make_float2(x[e], x[2 + e]);
               }
-          } else {
-            // tile 8 half + j: channels 2 j and 2 j + 1 of lane g's run
-            static_assert(kStage == kVHd || kVHd >= 128, "a round is a half");
-#pragma unroll
-            for (int d = 0; d < kStage / 16; d += 2)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int tile = rd * (kStage / 16) + d;
-                const int ch = (kVHd == 256 ? 128 * (d / 8) : 0) + kRun * g + 2 * (d % 8);
-                *reinterpret_cast<float4 *>(own + 4 * unit(2 * t + e, ch / 4)) =
-                    make_float4(acc[tile][i][e], acc[tile][i][2 + e], acc[tile + 1][i][e],
-                                acc[tile + 1][i][2 + e]);
-              }
+            }
           }
         }
         __syncthreads();
@@ -989,9 +983,7 @@ __global__ void __launch_bounds__(Sizes<kHd, kKind, R>::kThreads, Sizes<kHd, kKi
                 smem + Sh::kRingAt + (w * kSlots + sl) * Z::kSlot)[unit(r8, cq)];
             o[0] += v.x * f; o[1] += v.y * f; o[2] += v.z * f; o[3] += v.w * f;
           }
-          const int ch = cs * kVHd + (kKind != kKvBf16 && kVHd == 128 && kRounds == 2
-                                          ? 16 * (cq / 2) + 8 * rd + 4 * (cq & 1)
-                                          : rd * kStage + 4 * cq);
+          const int ch = cs * kVHd + rd * kStage + 4 * cq;
           if (whole) {
             const int mt = row / P.group, head = h * P.group + row - mt * P.group;
             const size_t at = ((size_t)b * P.M + mt) * P.qh + head;
@@ -1035,13 +1027,13 @@ __global__ void __launch_bounds__(kThreads)
   long long total = 0, before = 0;
   for (int i = tid; i < P.B; i += kThreads) {
     int start;
-    const int n = (length_of(P, i, start) + Z::kChunk - 1) / Z::kChunk;
+    const int n = units_of<Z>(length_of(P, i, start));
     total += n;
     if (i < b) before += n;
   }
   block_sums(total, before, room);
   int start;
-  const int len = length_of(P, b, start), n = (len + Z::kChunk - 1) / Z::kChunk;
+  const int len = length_of(P, b, start), n = units_of<Z>(len);
   const int mt = row / P.group;
   if (n == 0 || start + mt >= len) return;
   const Share share{total * items, (int)min((long long)grid, total * items)};
@@ -1106,7 +1098,7 @@ __global__ void __launch_bounds__(kThreads)
 template <class Z>
 int grid_of(int B, int M, int group, int kvh, int R, long long room) {
   const long long nrt = (M * group + 8 * R - 1) / (8 * R);
-  const long long most = (room + Z::kChunk - 1) / Z::kChunk * nrt * kvh * B;
+  const long long most = (long long)units_of<Z>((int)room) * nrt * kvh * B;
   const int all = kSms * Z::kCtas;
   return (int)(most < all ? most : all);
 }

@@ -272,3 +272,17 @@ def test_offsets_beyond_32_bits():
     k1, v1 = torch.zeros_like(k2), torch.zeros_like(k2)
     gdn.gdn_kv_read(cache_of(near), ints([list(range(8))]), None, k1, v1)
     assert torch.equal(k1, k2) and torch.equal(v1, v2)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8", "e4m3"])
+@pytest.mark.parametrize("scale", [0.0, -0.7, 3.0])
+def test_scales_of_scores(kind, scale):
+    """Zero (the mean of what is seen), negative and large ones, with masks."""
+    gen = gen_of(14)
+    hd, page, M, lens = 128, 32, 3, [3, 50, 259]
+    c = make_cache(kind, 30, 2, page, hd, gen, "cuda")
+    table = make_table(30, 3, 10, gen, "cuda")
+    junk_behind(c, table, lens, page, kind)
+    for group in (2, 5):
+        q = torch.randn(3, M, 2 * group, hd, generator=gen, device="cuda")
+        check(c, kind, "fp32", q, table, [n - M for n in lens], None, scale, page)
