@@ -56,7 +56,7 @@ namespace gdn {
 namespace attn {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kWarps = 8, kThreads = 32 * kWarps;  // of attn_join_kernel
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr float kNone = -1e30f;  // the reference of rows that have seen nothing
 constexpr float kUp = 12.0f;     // weights of 8-bit rows are brought to 2^12,
 constexpr float kTop = 32768.0f;  // and may grow to this before they are again
@@ -70,27 +70,25 @@ constexpr int kSms = 152;
 template <int kHd, int kKind, int R>
 struct Sizes {
   static constexpr int kBytes = kKind == kKvBf16 ? 2 : 1;
-  static constexpr int kS = R > 1 && kHd > 64 && kKind != kKvBf16 ? 2 : 1;
-  // of a CTA: what the registers of the sums leave
-  static constexpr int kWarps = kS == 1 || (kHd == 128 && R == 2) ? 8 : 12;
-  static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kTeams = kWarps / kS;
   static constexpr int kRow = kHd * kBytes;               // bytes of a row
+  static constexpr int kS = R > 1 && kHd == 256 && kKind != kKvBf16 ? 2 : 1;
+  // CTAs an SM: two of 128 registers a lane, or one
+  static constexpr int kCtas = kHd == 64 || (R == 1 && kRow <= 256) ? 2 : 1;
+  static constexpr int kTeams = kWarps / kS;
   // positions of a tile: 32, or as many as leave a ring of three parts, or (64
   // channels, 16 rows) as fit the registers
-  static constexpr int kTile =
-      kS == 2 ? 32 : kRow > 128 || (kHd == 64 && R == 2) ? 16 : 32;
+  static constexpr int kTile = kS == 2 || (kCtas == 1 && kRow <= 256)    ? 32
+                               : kRow > 128 || (kHd == 64 && R == 2) ? 16
+                                                                     : 32;
   static constexpr int kOwn = kTile / kS;                 // of them a warp's, for the scores
   static constexpr int kVHd = kHd / kS;                   // a warp's channels of v
   static constexpr int kVRow = kRow / kS;
   static constexpr int kUnit = kOwn * kRow;               // a warp's part of K or V
   static constexpr int kSlot = kUnit + (kKind == kKvBf16 ? 0 : 8 * kOwn);  // and scales
-  // CTAs an SM: three slots a warp are wanted
-  static constexpr int kCtas = kUnit > 4096 || (kHd == 256 && R > 1) || R > 2 ? 1 : 2;
-  // a warp's ring
-  static constexpr int kRing = kWarps > 8   ? 13 * 1024 : kCtas == 1 ? 25 * 1024 + 512
-                               : kS == 2    ? 11 * 1024
-                                            : 13 * 1024;
+  // a warp's ring: three parts or more (teams: beside their q)
+  static constexpr int kRing = kCtas == 2 ? 13 * 1024
+                               : kS == 2  ? (R == 2 ? 21 : 17) * 1024
+                                          : 25 * 1024 + 512;
   static constexpr int kSlots = kRing / kSlot;
   static constexpr int kChunk = kTeams * kTile;
   // channels of 8 rows of fp32 sums that a slot holds
@@ -316,25 +314,25 @@ struct Shared {
   using Z = Sizes<kHd, kKind, R>;
   static constexpr int kQBytes = kHd / 16 * Parts<kKind, kBf16>::kQ * R * 256;
   static constexpr int kRingAt = kQBytes;
-  static constexpr int kStatAt = kRingAt + Z::kWarps * Z::kSlots * Z::kSlot;
+  static constexpr int kStatAt = kRingAt + kWarps * Z::kSlots * Z::kSlot;
   // m and l of every warp's rows, the rows' factors, counts of the search
   static constexpr int kWeightsAt =
-      kStatAt + Z::kWarps * 8 * R * 8 + 8 * R * 4 + 2 * Z::kWarps * 8 + 32;
+      kStatAt + kWarps * 8 * R * 8 + 8 * R * 4 + 2 * kWarps * 8 + 32;
   // between the warps of a team: maxima, and a tile's weights
   static constexpr int kWeights = Z::kOwn / 16 * R * Parts<kKind, kBf16>::kP * 256;
   static constexpr int kBytes =
-      kWeightsAt + (Z::kS == 1 ? 0 : Z::kWarps * (2 * kWeights + 8 * R * 4 + 8));
+      kWeightsAt + (Z::kS == 1 ? 0 : kWarps * (2 * kWeights + 8 * R * 4 + 8));
 };
 
 template <int kHd, int kKind, bool kBf16, int R>
-__global__ void __launch_bounds__(Sizes<kHd, kKind, R>::kThreads, Sizes<kHd, kKind, R>::kCtas)
+__global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
     attn_kernel(const AttnArgs P) {
   using Z = Sizes<kHd, kKind, R>;
   using Sh = Shared<kHd, kKind, kBf16, R>;
   using T = typename std::conditional<kBf16, __nv_bfloat16, float>::type;
   constexpr bool kHalf = kKind != kKvBf16;
   constexpr int kRow = Z::kRow, kSlots = Z::kSlots, kS = Z::kS, kTile = Z::kTile;
-  constexpr int kVHd = Z::kVHd, kVRow = Z::kVRow, kWarps = Z::kWarps, kThreads = Z::kThreads;
+  constexpr int kVHd = Z::kVHd, kVRow = Z::kVRow;
   constexpr int kMT = Z::kOwn / 16, kVT = kTile / 16;  // 16 positions: of scores, of V
   constexpr int kQP = Parts<kKind, kBf16>::kQ, kPP = Parts<kKind, kBf16>::kP;
   constexpr int kVec = 16 / Z::kBytes;  // elements of 16 bytes
@@ -1108,7 +1106,7 @@ cudaError_t go(const AttnArgs &P, cudaStream_t stream) {
   using Z = Sizes<kHd, kKind, R>;
   using Sh = Shared<kHd, kKind, kBf16, R>;
   static_assert(Sh::kBytes * Z::kCtas <= 227 * 1024 - 1024 * (Z::kCtas - 1), "shared memory");
-  static_assert(Z::kCtas <= ((kHd == 256 && R > 1) || R > 2 ? 1 : 2), "parts of the workspace");
+  static_assert(Z::kCtas <= (kHd > 64 && R > 1 ? 1 : 2), "parts of the workspace");
   static_assert(Z::kSlots >= 3 && 32 * Z::kStage <= Z::kSlot, "rings");
   const int grid = grid_of<Z>(P.B, P.M, P.group, P.c.kvh, R,
                                        (long long)P.cols << P.c.page_shift);
@@ -1120,7 +1118,7 @@ cudaError_t go(const AttnArgs &P, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(Z::kThreads);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Sh::kBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1141,7 +1139,7 @@ cudaError_t go(const AttnArgs &P, cudaStream_t stream) {
 inline int tile_rows(int kind, int hd, int M, int group) {
   const long long rows = (long long)M * group;
   if (rows <= 8) return 1;
-  const bool three = kind != kKvBf16 && hd > 64;
+  const bool three = hd == 128 || (hd == 256 && kind != kKvBf16);
   return three && (rows + 23) / 24 * 3 <= (rows + 15) / 16 * 2 ? 3 : 2;
 }
 
@@ -1154,7 +1152,7 @@ template <int kHd, int kKind>
 cudaError_t by_rows(const AttnArgs &P, bool bf16, cudaStream_t stream) {
   const int R = tile_rows(kKind, kHd, P.M, P.group);
   if (R == 1) return by_type<kHd, kKind, 1>(P, bf16, stream);
-  if constexpr (kKind != kKvBf16 && kHd > 64) {
+  if constexpr (kHd == 128 || (kHd == 256 && kKind != kKvBf16)) {
     if (R == 3) return by_type<kHd, kKind, 3>(P, bf16, stream);
   }
   return by_type<kHd, kKind, 2>(P, bf16, stream);
@@ -1170,7 +1168,7 @@ cudaError_t launch(const AttnArgs &P, bool bf16, cudaStream_t stream) {
 // Bytes of the parts: two for each CTA, of which an SM has at most two.
 inline size_t bytes(int kind, int M, int group, int hd) {
   const int R = tile_rows(kind, hd, M, group);
-  const int ctas = kSms * ((hd == 256 && R > 1) || R > 2 ? 1 : 2);
+  const int ctas = kSms * (hd > 64 && R > 1 ? 1 : 2);
   return (size_t)ctas * 2 * (8 * R) * (hd + 4) * 4;
 }
 
