@@ -1033,13 +1033,15 @@ __global__ void __launch_bounds__(kThreads)
   int start;
   const int len = length_of(P, b, start), n = units_of<Z>(len);
   const int mt = row / P.group;
+  // (every block waits, also one that has nothing to do: the kernel behind this
+  // one waits for this one alone)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (n == 0 || start + mt >= len) return;
   const Share share{total * items, (int)min((long long)grid, total * items)};
   const long long u = before * items + (long long)n * (h * nrt + row / (8 * R));
   const int i0 = share.of(u), i1 = share.of(u + n - 1);
   if (i0 == i1) return;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int q = tid % kQ, group = tid / kQ;
   const float *part = P.part + (size_t)(row % (8 * R)) * (kHd + 4);
   constexpr size_t kStep = (size_t)(8 * R) * (kHd + 4);
