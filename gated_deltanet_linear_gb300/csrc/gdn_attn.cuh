@@ -106,9 +106,14 @@ struct Parts {
 struct Share {
   long long total;
   int ctas;
-  __host__ __device__ long long first(int cta) const { return total * cta / ctas; }
-  __host__ __device__ int of(long long unit) const {
-    return (int)(((unit + 1) * ctas - 1) / total);
+  // (products below 2^32: a 64-bit division takes several hundred cycles)
+  __device__ bool small() const { return total < (1 << 23); }
+  __device__ long long first(int cta) const {
+    return small() ? (long long)((unsigned)total * (unsigned)cta / (unsigned)ctas) : total * cta / ctas;
+  }
+  __device__ int of(long long unit) const {
+    return small() ? (int)((((unsigned)unit + 1) * (unsigned)ctas - 1) / (unsigned)total)
+                   : (int)(((unit + 1) * ctas - 1) / total);
   }
 };
 
@@ -123,7 +128,9 @@ __device__ __forceinline__ int length_of(const AttnArgs &P, int b, int &start) {
 }
 
 // Units of an item in the list: its chunks and one more without positions, which
-// is what its start and its join cost (64 sequences of up to 8192: 113 us without).
+// is what its start and its join cost (64 sequences of up to 8192: 113 us
+// without, 103 with it).  A share that would start with such a unit starts behind
+// it: an item whose chunks lie in one CTA is finished there.
 template <class Z>
 __host__ __device__ __forceinline__ int units_of(int len) {
   return (len + Z::kChunk - 1) / Z::kChunk + (len > 0);
@@ -317,7 +324,7 @@ struct Shared {
   static constexpr int kStatAt = kRingAt + kWarps * Z::kSlots * Z::kSlot;
   // m and l of every warp's rows, the rows' factors, counts of the search
   static constexpr int kWeightsAt =
-      kStatAt + kWarps * 8 * R * 8 + 8 * R * 4 + 2 * kWarps * 8 + 32;
+      kStatAt + kWarps * 8 * R * 8 + 8 * R * 4 + 2 * kWarps * 8 + 48;
   // between the warps of a team: maxima, and a tile's weights
   static constexpr int kWeights = Z::kOwn / 16 * R * Parts<kKind, kBf16>::kP * 256;
   static constexpr int kBytes =
@@ -350,20 +357,18 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
   float2 *const stat = reinterpret_cast<float2 *>(smem + Sh::kStatAt);  // [warp][8 R]
   float *const factor = reinterpret_cast<float *>(stat + kWarps * 8 * R);  // [8 R]
   long long *const room = reinterpret_cast<long long *>(factor + 8 * R);
-  int *const found = reinterpret_cast<int *>(room + 2 * kWarps);  // [3]
+  int *const found = reinterpret_cast<int *>(room + 2 * kWarps);  // [5]
   uint2 *const weights = reinterpret_cast<uint2 *>(smem + Sh::kWeightsAt);
   float *const maxima = reinterpret_cast<float *>(smem + Sh::kWeightsAt + 2 * kWarps * Sh::kWeights);
   volatile int *const flags = reinterpret_cast<int *>(maxima + kWarps * 8 * R);  // [warp][2]
-  signed char *const rooms = reinterpret_cast<signed char *>(found + 4);  // [kWarps]
+  signed char *const rooms = reinterpret_cast<signed char *>(found + 8);  // [kWarps]
 
   // ---- this CTA's share: chunks [u0, u1) of the list, from sequence b0 on
-  auto chunks = [&](int b, int &start) {
-    return units_of<Z>(length_of(P, b, start));
-  };
+  int len0 = 0, start0 = 0;  // of the sequence that this lane looks at
   auto counted = [&](int b) {
     if (b >= P.B) return 0;
-    int start;
-    const int n = chunks(b, start);
+    len0 = length_of(P, b, start0);
+    const int n = units_of<Z>(len0);
     if (P.err && blockIdx.x == 0 && n == 0 && !(P.counts && P.counts[b] == 0)) *P.err = 1;
     return n;
   };
@@ -376,9 +381,9 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
     return n;
   };
   // the first sequences lane by lane, the others' sum
-  int n0 = counted(tid), up = scan(n0);
   long long rest = 0;
   for (int b = tid + kThreads; b < P.B; b += kThreads) rest += counted(b);
+  int n0 = counted(tid), up = scan(n0);
   if (P.B > kThreads) {
 #pragma unroll
     for (int d = 16; d; d >>= 1) rest += __shfl_xor_sync(kFull, rest, d);
@@ -403,9 +408,13 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
   auto find = [&](int b, int n, long long first) {
     first *= items;
     if (n && u0 >= first && u0 < first + (long long)n * items) {
+      const int j = share.small() ? (int)((unsigned)(u0 - first) / (unsigned)n)
+                                  : (int)((u0 - first) / n);
       found[0] = b;
-      found[1] = (int)((u0 - first) / n);
-      found[2] = (int)((u0 - first) % n);
+      found[1] = j;
+      found[2] = (int)(u0 - first - (long long)j * n);
+      found[3] = len0;
+      found[4] = start0;
     }
   };
   find(tid, n0, lo + up - n0);
@@ -445,8 +454,9 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
       enter(w);
     } while (w.n == 0);
   };
-  Walk ahead{found[0], found[1] / nrt, found[1] % nrt, found[2], 0, 0, 0, u1 - u0};
-  enter(ahead);
+  Walk ahead{found[0], found[1] / nrt, found[1] % nrt, found[2], units_of<Z>(found[3]),
+             found[3], found[4], u1 - u0};
+  if (ahead.c == ahead.n - 1 && --ahead.left > 0) next_item(ahead);
   Walk here = ahead;
 
   // ---- the copies: this warp's tiles in order, K and V of each in turn
@@ -545,6 +555,24 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
     }
     commit();
   };
+  // q's rows of an item, a row a warp (R times), asked for ahead of their use
+  constexpr int kQuads = kHd == 256 ? 2 : 1;
+  float xq[R][kQuads][4];
+  auto ask_q = [&](const Walk &w) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int row = w.rt * 8 * R + warp + 8 * i;
+      const int mt = row / P.group, head = w.h * P.group + row - mt * P.group;
+      const T *src = static_cast<const T *>(P.q) + (((size_t)w.b * P.M + mt) * P.qh + head) * kHd;
+#pragma unroll
+      for (int e = 0; e < kQuads; ++e) {
+        xq[i][e][0] = xq[i][e][1] = xq[i][e][2] = xq[i][e][3] = 0.0f;
+        if (mt < P.M && lane + 32 * e < kHd / 4) load4(src + 4 * (lane + 32 * e), xq[i][e]);
+      }
+    }
+  };
+  if (here.left > 0) ask_q(here);
+
   constexpr std::false_type kK{};
   constexpr std::true_type kV{};
   seek();
@@ -569,17 +597,10 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
 
     // q's rows as the products' operands, a row a warp
     __syncthreads();  // (the last item's are read)
-#pragma unroll 1
-    for (int r = warp; r < 8 * R; r += kWarps) {
-      const int row = row0 + r, i = r / 8;
-      const int mt = row / P.group, head = h * P.group + row - mt * P.group;
-      const T *src = static_cast<const T *>(P.q) +
-                     (((size_t)b * P.M + mt) * P.qh + head) * kHd;
-      constexpr int kQuads = kHd == 256 ? 2 : 1;
-      float x[kQuads][4] = {};
 #pragma unroll
-      for (int e = 0; e < kQuads; ++e)
-        if (r < rows && lane + 32 * e < kHd / 4) load4(src + 4 * (lane + 32 * e), x[e]);
+    for (int i = 0; i < R; ++i) {
+      const int r = warp + 8 * i;
+      float (&x)[kQuads][4] = xq[i];
       float f = P.scale;
       if (kHalf) {
         uint32_t top = 0;
@@ -919,8 +940,13 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
 
     // ---- the warps' sums meet.  The slot that was read last is this warp's
     // room: the copies that are under way go to the others.
-    const bool whole = c0 == 0 && n == here.n;
+    const bool whole = c0 == 0 && n >= here.n - 1;
     here.left -= n;
+    here.c += n;
+    if (here.left > 0) {
+      next_item(here);
+      ask_q(here);
+    }
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
@@ -965,20 +991,27 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
           const int r8 = q / (kS * (kStage / 4)), cs = q / (kStage / 4) % kS, cq = q % (kStage / 4);
           const int r = r8 + 8 * i, row = row0 + r;
           if (r >= rows) continue;
+          float2 ml[kWarps];
           float top = kNone, sum = 0.0f;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w * 8 * R + r].x);
-          float o[4] = {};
+          for (int w = 0; w < kWarps; ++w) {
+            ml[w] = stat[w * 8 * R + r];
+            top = fmaxf(top, ml[w].x);
+          }
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
-            const int sl = rooms[w];
-            if (sl < 0) continue;
-            const float2 ml = stat[w * 8 * R + r];
-            const float f = exp2_(ml.x - top);
-            sum += ml.y * f;
-            if (w % kS != cs) continue;  // (the other half of the channels)
-            const float4 v = reinterpret_cast<const float4 *>(
-                smem + Sh::kRingAt + (w * kSlots + sl) * Z::kSlot)[unit(r8, cq)];
+            ml[w].x = exp2_(ml[w].x - top);
+            sum += ml[w].y * ml[w].x;
+          }
+          float o[4] = {};
+#pragma unroll
+          for (int w = 0; w < kWarps; w += kS) {
+            const int sl = rooms[w + cs];  // (the warp that has these channels)
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (sl >= 0)
+              v = reinterpret_cast<const float4 *>(
+                  smem + Sh::kRingAt + ((w + cs) * kSlots + sl) * Z::kSlot)[unit(r8, cq)];
+            const float f = ml[w].x;  // (the same for a team)
             o[0] += v.x * f; o[1] += v.y * f; o[2] += v.z * f; o[3] += v.w * f;
           }
           const int ch = cs * kVHd + rd * kStage + 4 * cq;
@@ -999,8 +1032,6 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
         }
         __syncthreads();
       }
-    here.c += n;
-    if (here.left > 0) next_item(here);
   }
   wait_for<0>();
 }
@@ -1040,7 +1071,7 @@ __global__ void __launch_bounds__(kThreads)
   if (n == 0 || start + mt >= len) return;
   const Share share{total * items, (int)min((long long)grid, total * items)};
   const long long u = before * items + (long long)n * (h * nrt + row / (8 * R));
-  const int i0 = share.of(u), i1 = share.of(u + n - 1);
+  const int i0 = share.of(u), i1 = share.of(u + n - 2);
   if (i0 == i1) return;
   const int q = tid % kQ, group = tid / kQ;
   const float *part = P.part + (size_t)(row % (8 * R)) * (kHd + 4);

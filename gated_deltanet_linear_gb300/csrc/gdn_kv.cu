@@ -241,7 +241,8 @@ __device__ __forceinline__ unsigned lanes_of_row() {
 
 // Turns and (kKind >= 0) the cache's rows.  A warp takes 32 / kLanes tokens, each
 // with kLanes lanes, and a run of P.run of their heads (q, k and v side by side),
-// the same for all of them.
+// the same for all warps of a block: blocks with rows to round and blocks without
+// end apart.
 template <typename T, int kKind, int kLanes>
 __global__ void __launch_bounds__(kThreads, 4)
     kv_rows_kernel(const KvRows P) {
@@ -255,9 +256,8 @@ __global__ void __launch_bounds__(kThreads, 4)
   const int turned_heads = P.qh + (kKind >= 0 ? P.c.kvh : 0);
   const int slots = turned_heads + (kKind >= 0 ? P.c.kvh : 0);
   const int runs = (slots + P.run - 1) / P.run;
-  const long long job = (long long)blockIdx.x * (kThreads / 32) + (tid >> 5);
-  const long long first = job / runs * kTokens;  // the warp's first token
-  const int s0 = (int)(job % runs) * P.run, s1 = min(s0 + P.run, slots);
+  const long long first = ((long long)(blockIdx.x / runs) * (kThreads / 32) + (tid >> 5)) * kTokens;
+  const int s0 = (int)(blockIdx.x % runs) * P.run, s1 = min(s0 + P.run, slots);
   const bool there = first + lane / kLanes < P.tokens;
   // (past the end: the last token again, storing nothing)
   const long long tok = there ? first + lane / kLanes : P.tokens - 1;
@@ -476,7 +476,7 @@ cudaError_t rows_go(KvRows P, cudaStream_t stream, bool read) {
   const long long runs = (heads + P.run - 1) / P.run;
   constexpr int kTokens = 32 / kLanes;
   const long long blocks = read ? (P.tokens * runs + kGroups - 1) / kGroups
-                                : ((P.tokens + kTokens - 1) / kTokens * runs + 7) / 8;
+                                : (P.tokens + 8 * kTokens - 1) / (8 * kTokens) * runs;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
