@@ -109,6 +109,7 @@ struct Share {
   // (products below 2^32: a 64-bit division takes several hundred cycles)
   __device__ bool small() const { return total < (1 << 23); }
   __device__ long long first(int cta) const {
+    if (ctas == total) return cta;
     return small() ? (long long)((unsigned)total * (unsigned)cta / (unsigned)ctas) : total * cta / ctas;
   }
   __device__ int of(long long unit) const {
@@ -363,6 +364,9 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
   volatile int *const flags = reinterpret_cast<int *>(maxima + kWarps * 8 * R);  // [warp][2]
   signed char *const rooms = reinterpret_cast<signed char *>(found + 8);  // [kWarps]
 
+  // the token of a row (of M; at least M: none)
+  auto token_of = [&](int row) { return P.M == 1 ? (int)(row >= P.group) : row / P.group; };
+
   // ---- this CTA's share: chunks [u0, u1) of the list, from sequence b0 on
   int len0 = 0, start0 = 0;  // of the sequence that this lane looks at
   auto counted = [&](int b) {
@@ -394,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
   }
   __syncthreads();
   long long lo = 0, before = 0, total = 0;  // chunks (of one item each) before
-#pragma unroll
+#pragma unroll 1
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) lo += room[w];
     before += room[w];
@@ -425,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
     if (lane == 31) room[warp] = up;
     __syncthreads();
     lo = before;
-#pragma unroll
+#pragma unroll 1
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) lo += room[w];
       before += room[w];
@@ -454,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
       enter(w);
     } while (w.n == 0);
   };
-  Walk ahead{found[0], found[1] / nrt, found[1] % nrt, found[2], units_of<Z>(found[3]),
+  Walk ahead{found[0], nrt == 1 ? found[1] : found[1] / nrt, nrt == 1 ? 0 : found[1] % nrt, found[2], units_of<Z>(found[3]),
              found[3], found[4], u1 - u0};
   if (ahead.c == ahead.n - 1 && --ahead.left > 0) next_item(ahead);
   Walk here = ahead;
@@ -562,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const int row = w.rt * 8 * R + warp + 8 * i;
-      const int mt = row / P.group, head = w.h * P.group + row - mt * P.group;
+      const int mt = token_of(row), head = w.h * P.group + row - mt * P.group;
       const T *src = static_cast<const T *>(P.q) + (((size_t)w.b * P.M + mt) * P.qh + head) * kHd;
 #pragma unroll
       for (int e = 0; e < kQuads; ++e) {
@@ -1016,7 +1020,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
           }
           const int ch = cs * kVHd + rd * kStage + 4 * cq;
           if (whole) {
-            const int mt = row / P.group, head = h * P.group + row - mt * P.group;
+            const int mt = token_of(row), head = h * P.group + row - mt * P.group;
             const size_t at = ((size_t)b * P.M + mt) * P.qh + head;
             if (mt + start >= len) continue;  // a token that the sequence has not
             const float inv = 1.0f / sum;

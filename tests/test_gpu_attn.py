@@ -286,3 +286,23 @@ def test_scales_of_scores(kind, scale):
     for group in (2, 5):
         q = torch.randn(3, M, 2 * group, hd, generator=gen, device="cuda")
         check(c, kind, "fp32", q, table, [n - M for n in lens], None, scale, page)
+
+
+@pytest.mark.parametrize("B", [32, 33, 255, 256, 257, 700])
+def test_batches_around_the_search(B):
+    """Batches on both sides of the sizes that the lengths are searched by,
+    with sequences left out at both ends and in the middle."""
+    gen = gen_of(15)
+    hd, page, cols = 64, 16, 5
+    c = make_cache("int8", B * cols, 1, page, hd, gen, "cuda")
+    table = make_table(B * cols, B, cols, gen, "cuda")
+    start = torch.randint(0, cols * page - 2, (B,), generator=gen, device="cuda").tolist()
+    counts = (torch.rand(B, generator=gen, device="cuda") > 0.3).long().mul(2).tolist()
+    counts[0] = counts[-1] = 0
+    counts[B // 2] = 2
+    lens = [s + n for s, n in zip(start, counts)]
+    junk_behind(c, table, lens, page, "int8")
+    q = torch.randn(B, 2, 2, hd, generator=gen, device="cuda")
+    check(c, "int8", "fp32", q, table, start, counts, 0.2, page)
+    o, _ = call(c, q, table, ints(start), 0.2, counts=ints([0] * B))
+    assert bool((o == 7.0).all())
