@@ -118,6 +118,14 @@ struct Share {
   }
 };
 
+// An item that begins in a CTA and ends in another: what attn_join_kernel has to
+// know of it (last < 0: none).
+struct __align__(16) Split {
+  int last;  // the last CTA with a part of it
+  int b, h, row0, start, len, room[2];
+};
+constexpr size_t kSplitBytes = 2 * kSms * sizeof(Split);
+
 // Positions that a sequence's new tokens see, and its first new one; 0 where
 // there is nothing to do.
 __device__ __forceinline__ int length_of(const AttnArgs &P, int b, int &start) {
@@ -275,28 +283,6 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, const float (&x)[4]) {
                                              *reinterpret_cast<const uint32_t *>(&b));
 }
 
-// Sum over the block of two counts.
-__device__ __forceinline__ void block_sums(long long &x, long long &y, long long *room) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) {
-    x += __shfl_xor_sync(kFull, x, d);
-    y += __shfl_xor_sync(kFull, y, d);
-  }
-  const int warp = threadIdx.x >> 5;
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) {
-    room[warp] = x;
-    room[kWarps + warp] = y;
-  }
-  __syncthreads();
-  x = y = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    x += room[w];
-    y += room[kWarps + w];
-  }
-}
-
 // Where a 16-byte unit of a row lies in a tile: in its row (rows of 64 bytes of
 // V: in its pair of rows), permuted by an exclusive or with bits of the row, so
 // that the reads meet no bank twice.
@@ -353,6 +339,8 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
   const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0);
   const int lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int team = warp / kS, sub = warp % kS;
+  Split *const split = reinterpret_cast<Split *>(P.part) + blockIdx.x;
+  if (tid == 0) split->last = -1;
   const int nrt = (P.M * P.group + 8 * R - 1) / (8 * R), items = P.c.kvh * nrt;
   uint32_t *const qs = reinterpret_cast<uint32_t *>(smem);
   float2 *const stat = reinterpret_cast<float2 *>(smem + Sh::kStatAt);  // [warp][8 R]
@@ -945,6 +933,10 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
     // ---- the warps' sums meet.  The slot that was read last is this warp's
     // room: the copies that are under way go to the others.
     const bool whole = c0 == 0 && n >= here.n - 1;
+    if (c0 == 0 && !whole && tid == 0) {
+      const long long unit0 = u1 - here.left;  // the item's first of the list
+      *split = Split{share.of(unit0 + here.n - 2), b, h, row0, start, len, {0, 0}};
+    }
     here.left -= n;
     here.c += n;
     if (here.left > 0) {
@@ -969,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
     auto unit = [](int r, int q) { return r * (kStage / 4) + (q ^ (((q >> 2) ^ (q >> 5) ^ r) & 7)); };
     __syncwarp();
     float *const parts =
-        P.part + ((size_t)blockIdx.x * 2 + (c0 == 0 ? 1 : 0)) * (8 * R) * (kHd + 4);
+        P.part + kSplitBytes / 4 + ((size_t)blockIdx.x * 2 + (c0 == 0 ? 1 : 0)) * (8 * R) * (kHd + 4);
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
@@ -1040,66 +1032,46 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
   wait_for<0>();
 }
 
-// Rows whose item lies in several CTAs: the parts in the CTAs' order, a row for
-// each block, four groups of threads (hd 256) to sixteen over the parts.
-template <int kHd, int kKind, bool kBf16, int R>
-__global__ void __launch_bounds__(kThreads)
-    attn_join_kernel(const AttnArgs P, int grid) {
-  using Z = Sizes<kHd, kKind, R>;
+// Row r of an item with parts in the CTAs i0 .. last, added in their order by a
+// block: kHd / 4 threads for each of kThr / (kHd / 4) streams of them.  It is token mt
+// of sequence b, query head `head`.
+template <int kHd, bool kBf16, int R, int kThr>
+__device__ __forceinline__ void join_row(const AttnArgs &P, int i0, int last, int r, int b, int mt,
+                                         int head) {
   using T = typename std::conditional<kBf16, __nv_bfloat16, float>::type;
-  constexpr int kQ = kHd / 4, kGroups = kThreads / kQ;
-  __shared__ long long room[2 * kWarps];
+  constexpr int kQ = kHd / 4, kGroups = kThr / kQ;
   __shared__ float4 sums[kGroups][kQ];
   __shared__ float tops[kGroups], ls[kGroups];
-  // (what came before attn_kernel has ended, and attn_kernel writes no lengths:
-  // they may be read beside it)
-  const int tid = threadIdx.x, rows = P.M * P.group;
-  const int nrt = (rows + 8 * R - 1) / (8 * R), items = P.c.kvh * nrt;
-  const int row = blockIdx.x % rows, h = blockIdx.x / rows % P.c.kvh;
-  const int b = blockIdx.x / rows / P.c.kvh;
-  long long total = 0, before = 0;
-  for (int i = tid; i < P.B; i += kThreads) {
-    int start;
-    const int n = units_of<Z>(length_of(P, i, start));
-    total += n;
-    if (i < b) before += n;
-  }
-  block_sums(total, before, room);
-  int start;
-  const int len = length_of(P, b, start), n = units_of<Z>(len);
-  const int mt = row / P.group;
-  // (every block waits, also one that has nothing to do: the kernel behind this
-  // one waits for this one alone)
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (n == 0 || start + mt >= len) return;
-  const Share share{total * items, (int)min((long long)grid, total * items)};
-  const long long u = before * items + (long long)n * (h * nrt + row / (8 * R));
-  const int i0 = share.of(u), i1 = share.of(u + n - 2);
-  if (i0 == i1) return;
-  const int q = tid % kQ, group = tid / kQ;
-  const float *part = P.part + (size_t)(row % (8 * R)) * (kHd + 4);
-  constexpr size_t kStep = (size_t)(8 * R) * (kHd + 4);
-  auto at = [&](int i) { return part + ((size_t)i * 2 + (i == i0 ? 1 : 0)) * kStep; };
+  const int tid = threadIdx.x, q = tid % kQ, group = tid / kQ;
+  constexpr size_t kPart = (size_t)(8 * R) * (kHd + 4);
+  const float *part = P.part + kSplitBytes / 4 + (size_t)r * (kHd + 4);
+  auto at = [&](int i) { return part + ((size_t)i * 2 + (i == i0 ? 1 : 0)) * kPart; };
   float top = kNone, sum = 0.0f, o[4] = {};
-  constexpr int kU = 4;
-  for (int i = i0 + group; i <= i1; i += kU * kGroups) {
+  constexpr int kU = 8;  // parts under way
+#pragma unroll 1
+  for (int i = i0 + group; i <= last; i += kU * kGroups) {
     float2 ml[kU];
     float x[kU][4];
+    float to = top;
 #pragma unroll
-    for (int k = 0; k < kU; ++k) {
-      if (i + k * kGroups > i1) continue;
-      ml[k] = *reinterpret_cast<const float2 *>(at(i + k * kGroups) + kHd);
-      load4(at(i + k * kGroups) + 4 * q, x[k]);
+    for (int k = 0; k < kU; ++k) {  // (past the end: the first one, without weight)
+      const float *from = at(i + k * kGroups <= last ? i + k * kGroups : i);
+      ml[k] = *reinterpret_cast<const float2 *>(from + kHd);
+      load4(from + 4 * q, x[k]);
+      to = fmaxf(to, ml[k].x);
     }
+    const float f = exp2_(top - to);
+    top = to;
+    sum *= f;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) o[d] *= f;
 #pragma unroll
     for (int k = 0; k < kU; ++k) {
-      if (i + k * kGroups > i1) continue;
-      const float to = fmaxf(top, ml[k].x), f = exp2_(top - to), e = exp2_(ml[k].x - to);
-      top = to;
-      sum = sum * f + ml[k].y * e;
+      if (i + k * kGroups > last) continue;
+      const float e = exp2_(ml[k].x - to);
+      sum += ml[k].y * e;
 #pragma unroll
-      for (int d = 0; d < 4; ++d) o[d] = o[d] * f + x[k][d] * e;
+      for (int d = 0; d < 4; ++d) o[d] += x[k][d] * e;
     }
   }
   sums[group][q] = make_float4(o[0], o[1], o[2], o[3]);
@@ -1124,9 +1096,58 @@ __global__ void __launch_bounds__(kThreads)
   const float inv = 1.0f / sum;
 #pragma unroll
   for (int d = 0; d < 4; ++d) y[d] *= inv;
-  const size_t to = ((size_t)b * P.M + mt) * P.qh + h * P.group + row - mt * P.group;
+  const size_t to = ((size_t)b * P.M + mt) * P.qh + head;
   store4(static_cast<T *>(P.o) + to * kHd + 4 * q, y);
   if (P.lse && q == 0) P.lse[to] = (all + log2f(sum)) * 0.693147180559945f;
+}
+
+// Many items in several CTAs: a block for a row of the one that begins in CTA
+// blockIdx / rows, if one does, as that CTA left word of it.
+template <int kHd, bool kBf16, int R>
+__global__ void __launch_bounds__(128)
+    attn_join_kernel(const AttnArgs P, int rows) {
+  // (every block waits, also one that has nothing to do: the kernel behind this
+  // one waits for this one alone)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int i0 = blockIdx.x / rows, r = blockIdx.x - i0 * rows;
+  const Split s = reinterpret_cast<const Split *>(P.part)[i0];
+  if (s.last < 0) return;
+  const int row = s.row0 + r, mt = row / P.group;
+  if (mt >= P.M || s.start + mt >= s.len) return;  // (no token of the sequence)
+  join_row<kHd, kBf16, R, 128>(P, i0, s.last, r, s.b, mt, s.h * P.group + row - mt * P.group);
+}
+
+// Few items of many parts (at most 32 sequences): a block for each row, which finds
+// the item's CTAs from the lengths while attn_kernel runs.
+template <int kHd, int kKind, bool kBf16, int R>
+__global__ void __launch_bounds__(512)
+    attn_join_few_kernel(const AttnArgs P, int grid) {
+  using Z = Sizes<kHd, kKind, R>;
+  // (what came before attn_kernel has ended, and attn_kernel writes no lengths)
+  const int rows = P.M * P.group, lane = threadIdx.x & 31;
+  const int nrt = (rows + 8 * R - 1) / (8 * R), items = P.c.kvh * nrt;
+  const int row = blockIdx.x % rows, h = blockIdx.x / rows % P.c.kvh;
+  const int b = blockIdx.x / rows / P.c.kvh, mt = row / P.group;
+  int start = 0, len = lane < P.B ? length_of(P, lane, start) : 0, up = units_of<Z>(len);
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int x = __shfl_up_sync(kFull, up, d);
+    if (lane >= d) up += x;
+  }
+  const long long total = (long long)__shfl_sync(kFull, up, 31) * items;
+  start = __shfl_sync(kFull, start, b);
+  len = __shfl_sync(kFull, len, b);
+  const int n = units_of<Z>(len);
+  const long long before = __shfl_sync(kFull, up, b) - n;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (n == 0 || start + mt >= len) return;
+  const Share share{total, (int)min((long long)grid, total)};
+  const long long u = before * items + (long long)n * (h * nrt + row / (8 * R));
+  const int i0 = share.of(u), last = share.of(u + n - 2);
+  if (i0 == last) return;
+  join_row<kHd, kBf16, R, 512>(P, i0, last, row % (8 * R), b, mt, h * P.group + row - mt * P.group);
 }
 
 // CTAs of a call: at most one share each for the longest that the table holds.
@@ -1147,8 +1168,6 @@ cudaError_t go(const AttnArgs &P, cudaStream_t stream) {
   static_assert(Z::kSlots >= 3 && 32 * Z::kStage <= Z::kSlot, "rings");
   const int grid = grid_of<Z>(P.B, P.M, P.group, P.c.kvh, R,
                                        (long long)P.cols << P.c.page_shift);
-  const long long rows = (long long)P.B * P.M * P.qh;
-  if (rows > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   if (grid == 0) return cudaSuccess;
   const auto kernel = attn_kernel<kHd, kKind, kBf16, R>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kBytes);
@@ -1165,10 +1184,20 @@ cudaError_t go(const AttnArgs &P, cudaStream_t stream) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kernel, P);
   if (e != cudaSuccess || grid == 1) return e;
-  cfg.gridDim = dim3((unsigned)rows);
-  cfg.blockDim = dim3(kThreads);
+  // Joins: by items where each has eight CTAs or more (one sequence of 4099 x 4
+  // heads of 256: 9.3 us, 11.4 by CTAs), by CTAs otherwise (64 sequences x 8 heads:
+  // 93 us, 96.5 by items).
+  const long long heads = (long long)P.B * P.c.kvh;
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, attn_join_kernel<kHd, kKind, kBf16, R>, P, grid);
+  if (P.B <= 32 && grid >= 8 * heads) {
+    cfg.gridDim = dim3((unsigned)(heads * P.M * P.group));
+    cfg.blockDim = dim3(512);
+    return cudaLaunchKernelEx(&cfg, attn_join_few_kernel<kHd, kKind, kBf16, R>, P, grid);
+  }
+  const int rows = P.M * P.group < 8 * R ? P.M * P.group : 8 * R;
+  cfg.gridDim = dim3((unsigned)(grid * rows));
+  cfg.blockDim = dim3(128);
+  return cudaLaunchKernelEx(&cfg, attn_join_kernel<kHd, kBf16, R>, P, rows);
 }
 
 // Row tiles of 8, 16 or (8 bits, teams) 24: the fewest eights of rows, and of two
@@ -1202,11 +1231,12 @@ cudaError_t launch(const AttnArgs &P, bool bf16, cudaStream_t stream) {
                                : by_rows<kHd, kKvE4m3>(P, bf16, stream);
 }
 
-// Bytes of the parts: two for each CTA, of which an SM has at most two.
+// Bytes of the items' ends and the parts: one and two for each CTA, of which an SM
+// has at most two.
 inline size_t bytes(int kind, int M, int group, int hd) {
   const int R = tile_rows(kind, hd, M, group);
   const int ctas = kSms * (hd > 64 && R > 1 ? 1 : 2);
-  return (size_t)ctas * 2 * (8 * R) * (hd + 4) * 4;
+  return kSplitBytes + (size_t)ctas * 2 * (8 * R) * (hd + 4) * 4;
 }
 
 }  // namespace attn

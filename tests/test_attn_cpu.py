@@ -75,10 +75,11 @@ def test_attn_refusals(lib):
     assert attn_call(lib, cache(scale=None), ws=FAKE, q=FAKE) == gdn.GDN_EINVAL
     size = lib.gdn_attn_workspace
     assert size(ok, 0, 4) == size(ok, 65, 4) == size(ok, 1, 3) == size(ok, 1, 0) == 0
-    # two parts of 8 to 24 rows of 128 sums and 4 floats for each CTA
-    assert size(ok, 1, 4) == 2 * 304 * 8 * 132 * 4 and size(ok, 8, 4) == 2 * size(ok, 1, 4)
-    # 20 rows: 24 of an 8-bit cache, twice 16 of a bf16 one
-    assert 2 * size(ok, 10, 4) == 3 * size(ok, 1, 4) and size(cache(kind=0), 10, 4) == 2 * size(ok, 1, 4)
+    # two parts of 8 to 24 rows of 128 sums and 4 floats for each CTA, and 32 bytes
+    assert size(ok, 1, 4) == 9728 + 2 * 304 * 8 * 132 * 4
+    assert size(ok, 8, 4) == 9728 + 2 * 152 * 16 * 132 * 4
+    assert size(ok, 10, 4) == size(cache(kind=0), 10, 4) == 9728 + 2 * 152 * 24 * 132 * 4
+    assert size(cache(hd=64), 10, 4) == 9728 + 2 * 304 * 16 * 68 * 4
 
 
 def test_write_and_read_refusals(lib):

@@ -306,3 +306,28 @@ def test_batches_around_the_search(B):
     check(c, "int8", "fp32", q, table, start, counts, 0.2, page)
     o, _ = call(c, q, table, ints(start), 0.2, counts=ints([0] * B))
     assert bool((o == 7.0).all())
+
+
+@pytest.mark.parametrize("fill", [0, 0xff, 0x5a, None])
+def test_workspaces_may_hold_anything(fill):
+    """Joins over many CTAs with a workspace of zeros, ones, noise and what
+    another call has left, four times each."""
+    gen = gen_of(16)
+    hd, page, T = 128, 64, 20000
+    cols = -(-T // page)
+    c = make_cache("int8", 2 * cols, 2, page, hd, gen, "cuda")
+    table = make_table(2 * cols, 2, cols, gen, "cuda")
+    start = ints([19999, 7000])
+    q = torch.randn(2, 1, 8, hd, generator=gen, device="cuda")
+    want, _ = call(c, q, table, start, 0.1)
+    cache = cache_of(c)
+    ws = torch.empty(gdn.gdn_attn_workspace(cache, 1, 8), dtype=torch.uint8, device="cuda")
+    for _ in range(4):
+        if fill is None:
+            ws.copy_(torch.randint(0, 256, ws.shape, generator=gen, device="cuda", dtype=torch.uint8))
+        else:
+            ws.fill_(fill)
+        for _ in range(2):
+            o = torch.zeros_like(q)
+            gdn.gdn_attn_step_m(cache, q, table, start, o, scale=0.1, workspace=ws)
+            assert torch.equal(o, want)
