@@ -667,33 +667,35 @@ def gdn_rope_freqs(rot, base=10000.0, scaling=GDN_ROPE_PLAIN, factor=1.0,
     return freq.to(device), amp.value
 
 
-def _rows(x, name, shape, dtype):
-    """Pointer and stride from token to token of x, shape [B][M][heads][hd] or
+def _rows(x, name, shape):
+    """Stride from token to token of x, of this shape [B][M][heads][hd] or
     [rows][heads][hd]: heads and channels contiguous, tokens evenly spaced (the
-    rows of a projection).  (On the path of every call, as _tok; that it is
-    device memory the library checks.)"""
+    rows of a projection).  (On the path of every call; that x is device memory
+    the library checks.)"""
+    st = x.stride()
+    heads, hd = shape[-2:]
+    if st[-1] == 1 and (st[-2] == hd or heads == 1):
+        if len(shape) == 3:
+            return st[0] if shape[0] > 1 else heads * hd
+        B, M = shape[:2]
+        if M == 1:
+            return st[0] if B > 1 else heads * hd
+        if B <= 1 or st[0] == M * st[1]:
+            return st[1]
+    if not x.numel():
+        return heads * hd
+    raise ValueError(f"{name}: heads and channels must be contiguous, tokens evenly spaced")
+
+
+def _same(x, name, shape, dtype):
+    """Pointer of a contiguous tensor of this shape and type (device memory or
+    not is the library's to say)."""
     try:
-        if x.dtype is dtype and x.shape == shape:
-            st = x.stride()
-            heads, hd = shape[-2:]
-            if st[-1] == 1 and (st[-2] == hd or heads == 1):
-                if len(shape) == 3:
-                    return x.data_ptr(), st[0] if shape[0] > 1 else heads * hd
-                B, M = shape[:2]
-                if M > 1:
-                    if B <= 1 or st[0] == M * st[1]:
-                        return x.data_ptr(), st[1]
-                else:
-                    return x.data_ptr(), st[0] if B > 1 else heads * hd
+        if x.dtype is dtype and x.shape == shape and x.is_contiguous():
+            return x.data_ptr()
     except AttributeError:
         pass
-    if not isinstance(x, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not x.is_cuda or x.dtype is not dtype or x.shape != shape:
-        raise ValueError(f"{name} must be a {dtype} CUDA tensor of shape {tuple(shape)}")
-    if not x.numel():
-        return x.data_ptr(), shape[-2] * shape[-1]
-    raise ValueError(f"{name}: heads and channels must be contiguous, tokens evenly spaced")
+    return _tok(x, name, shape, dtype)
 
 
 def _code(dtype):
@@ -704,37 +706,35 @@ def _code(dtype):
 
 
 def _ints(x, name, shape):
-    if x is None:
-        return None
-    try:
-        if x.dtype is torch.int32 and x.shape == shape and x.is_contiguous():
-            return x.data_ptr()
-    except AttributeError:
-        pass
-    return _tok(x, name, shape, torch.int32)
+    return None if x is None else _same(x, name, shape, torch.int32)
 
 
 def gdn_rope_m(x, pos, rope, y, stream=None):
     """y = x turned to positions pos: x, y [rows][heads][hd] float32 or
     bfloat16 (x may have a stride from row to row; y may be x), pos int32
     [rows]."""
-    if x.dim() != 3:
+    shape, dtype = x.shape, x.dtype
+    if len(shape) != 3:
         raise ValueError("x must be [rows][heads][hd]")
-    rows, heads, hd = x.shape
-    ptr, step = _rows(x, "x", x.shape, x.dtype)
+    rows, heads, hd = shape
     r = (_lib or load()).gdn_rope_m(
-        rows, heads, hd, _code(x.dtype), rope.ref, ptr, step,
-        _ints(pos, "pos", (rows,)), _tok(y, "y", x.shape, x.dtype), _stream(stream))
+        rows, heads, hd, _code(dtype), rope.ref, x.data_ptr(), _rows(x, "x", shape),
+        _ints(pos, "pos", (rows,)), _same(y, "y", shape, dtype), _stream(stream))
     if r:
         raise GDNError(r, "gdn_rope_m")
 
 
 def _paged(cache, B, table, start, counts, err_dev):
     """Pointers of table, start, counts, err_dev and the table's columns."""
-    if not isinstance(table, torch.Tensor) or len(ts := table.shape) != 2 or ts[0] != B:
-        raise ValueError("table must be [B][columns]")
-    return (_ints(table, "table", ts), ts[1], _ints(start, "start", (B,)),
-            _ints(counts, "counts", (B,)), _ints(err_dev, "err_dev", (1,)))
+    ts = table.shape
+    if len(ts) != 2 or ts[0] != B or table.dtype is not torch.int32 or \
+            not table.is_contiguous():
+        raise ValueError(f"table must be a contiguous int32 tensor [{B}][columns]")
+    one = (B,)
+    return (table.data_ptr(), ts[1],
+            None if start is None else _same(start, "start", one, torch.int32),
+            None if counts is None else _same(counts, "counts", one, torch.int32),
+            None if err_dev is None else _same(err_dev, "err_dev", (1,), torch.int32))
 
 
 def gdn_kv_write_m(cache, k, v, table, start, rope=None, q=None, q_out=None,
@@ -744,25 +744,26 @@ def gdn_kv_write_m(cache, k, v, table, start, rope=None, q=None, q_out=None,
     [B][M][qh][hd] into q_out.  q, k, v may be slices of one projection."""
     _, kvh, _, hd = cache.shape
     shape, dtype = k.shape, k.dtype
-    if len(shape) != 4 or shape[2] != kvh or shape[3] != hd:
-        raise ValueError(f"k and v must be [B][M][{kvh}][{hd}]")
+    if len(shape) != 4 or shape[2] != kvh or shape[3] != hd or v.shape != shape or \
+            v.dtype is not dtype:
+        raise ValueError(f"k and v must be [B][M][{kvh}][{hd}] of one type")
     B, M = shape[:2]
-    (kp, ks), (vp, vs) = _rows(k, "k", shape, dtype), _rows(v, "v", shape, dtype)
     qp = qo = None
     qs = qh = 0
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     if q is not None:
         qshape = q.shape
-        if len(qshape) != 4 or qshape[3] != hd or qshape[:2] != shape[:2]:
-            raise ValueError(f"q must be [B][M][qh][{hd}]")
-        qp, qs = _rows(q, "q", qshape, dtype)
-        qh = qshape[2]
-        qo = _tok(q_out, "q_out", qshape, dtype)
+        qh = qshape[2] if len(qshape) == 4 else 0
+        if qshape != (B, M, qh, hd) or q.dtype is not dtype:
+            raise ValueError(f"q must be [B][M][qh][{hd}] of the type of k")
+        qp, qs = q.data_ptr(), _rows(q, "q", qshape)
+        qo = _same(q_out, "q_out", qshape, dtype)
     tp, cols, sp, cp, ep = _paged(cache, B, table, start, counts, err_dev)
     r = (_lib or load()).gdn_kv_write_m(
         cache.ref, B, M, qh, _code(dtype),
-        None if rope is None else rope.ref, qp, qs, kp, ks, vp, vs, qo,
+        None if rope is None else rope.ref, qp, qs, k.data_ptr(), _rows(k, "k", shape),
+        v.data_ptr(), _rows(v, "v", shape), qo,
         tp, cols, sp, cp, ep, _stream(stream))
     if r:
         raise GDNError(r, "gdn_kv_write_m")
@@ -779,7 +780,7 @@ def gdn_kv_read(cache, table, start, k, v, counts=None, err_dev=None,
     tp, cols, sp, cp, ep = _paged(cache, B, table, start, counts, err_dev)
     r = (_lib or load()).gdn_kv_read(
         cache.ref, B, T, _code(dtype), tp, cols, sp, cp,
-        _tok(k, "k", shape, dtype), _tok(v, "v", shape, dtype), ep,
+        _same(k, "k", shape, dtype), _same(v, "v", shape, dtype), ep,
         _stream(stream))
     if r:
         raise GDNError(r, "gdn_kv_read")
@@ -808,9 +809,9 @@ def gdn_attn_step_m(cache, q, table, start, o, scale=None, counts=None,
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.nbytes
     r = (_lib or load()).gdn_attn_step_m(
         cache.ref, B, M, qh, _code(dtype),
-        hd ** -0.5 if scale is None else scale, _tok(q, "q", qs, dtype), tp, cols,
-        sp, cp, _tok(o, "o", qs, dtype),
-        None if lse is None else _tok(lse, "lse", qs[:3], torch.float32), ep,
+        hd ** -0.5 if scale is None else scale, _same(q, "q", qs, dtype), tp, cols,
+        sp, cp, _same(o, "o", qs, dtype),
+        None if lse is None else _same(lse, "lse", qs[:3], torch.float32), ep,
         ws_ptr, ws_bytes, _stream(stream))
     if r:
         raise GDNError(r, "gdn_attn_step_m")

@@ -77,7 +77,7 @@ struct Sizes {
   static constexpr int kTeams = kWarps / kS;
   // positions of a tile: 32, or as many as leave a ring of three parts, or (64
   // channels, 16 rows) as fit the registers
-  static constexpr int kTile = kS == 2 || (kCtas == 1 && kRow <= 256)    ? 32
+  static constexpr int kTile = kRow == 64 && R == 1 ? 64 : kS == 2 || (kCtas == 1 && kRow <= 256)    ? 32
                                : kRow > 128 || (kHd == 64 && R == 2) ? 16
                                                                      : 32;
   static constexpr int kOwn = kTile / kS;                 // of them a warp's, for the scores
@@ -86,7 +86,7 @@ struct Sizes {
   static constexpr int kUnit = kOwn * kRow;               // a warp's part of K or V
   static constexpr int kSlot = kUnit + (kKind == kKvBf16 ? 0 : 8 * kOwn);  // and scales
   // a warp's ring: three parts or more (teams: beside their q)
-  static constexpr int kRing = kCtas == 2 ? 13 * 1024
+  static constexpr int kRing = kRow == 64 && R == 1 ? 13 * 1024 + 512 : kCtas == 2 ? 13 * 1024
                                : kS == 2  ? (R == 2 ? 21 : 17) * 1024
                                           : 25 * 1024 + 512;
   static constexpr int kSlots = kRing / kSlot;
@@ -537,7 +537,9 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
       if (kKind != kKvBf16 && !v_next && lane < 2 * Z::kOwn / 4) {  // both scales, with K
         const int which = lane / (Z::kOwn / 4), r = 4 * (lane % (Z::kOwn / 4)) + sub * Z::kOwn;
         const float *s = which ? P.c.v_scale : P.c.k_scale;
-        const long long at = kVT == 1 || r < 16 ? row_at[0] : row_at[kVT - 1];
+        long long at = row_at[0];
+#pragma unroll
+        for (int i = 1; i < kVT; ++i) at = r >= 16 * i ? row_at[i] : at;
         const bool on = at >= 0 && r < rows_on;
         cp16(slot + Z::kUnit + 16 * lane, s + (on ? (size_t)(at + (r & 15)) : (size_t)0), on);
       }

@@ -363,11 +363,20 @@ __global__ void __launch_bounds__(kThreads, 4)
     for (int j = 0; j < kQ; ++j)
       if (x + j < q1) row_q(raw[j], x + j);
   }
+  const int k0 = max(s0, P.qh);
+  Raw<T> next[kKv];
+  if (k0 < s1) {
+#pragma unroll
+    for (int j = 0; j < kKv; ++j) fetch(next[j], min(k0 + j, s1 - 1));
+  }
 #pragma unroll 1
-  for (int x = max(s0, P.qh); x < s1; x += kKv) {
+  for (int x = k0; x < s1; x += kKv) {
     Raw<T> raw[kKv];
 #pragma unroll
-    for (int j = 0; j < kKv; ++j) fetch(raw[j], min(x + j, s1 - 1));
+    for (int j = 0; j < kKv; ++j) {
+      raw[j] = next[j];
+      fetch(next[j], min(x + kKv + j, s1 - 1));
+    }
 #pragma unroll
     for (int j = 0; j < kKv; ++j)
       if (x + j < s1) row_kv(raw[j], x + j);
