@@ -1045,90 +1045,77 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
   wait_for<0>();
 }
 
-// Row r of an item with parts in the CTAs i0 .. last, added in their order by a
-// block: kHd / 4 threads for each of kThr / (kHd / 4) streams of them.  It is token mt
-// of sequence b, query head `head`.
-template <int kHd, bool kBf16, int R, int kThr>
-__device__ __forceinline__ void join_row(const AttnArgs &P, int i0, int last, int r, int b, int mt,
-                                         int head) {
-  using T = typename std::conditional<kBf16, __nv_bfloat16, float>::type;
-  constexpr int kQ = kHd / 4, kGroups = kThr / kQ;
-  __shared__ float4 sums[kGroups][kQ];
-  __shared__ float tops[kGroups], ls[kGroups];
-  const int tid = threadIdx.x, q = tid % kQ, group = tid / kQ;
-  constexpr size_t kPart = (size_t)(8 * R) * (kHd + 4);
-  const float *part = P.part + kSplitBytes / 4 + (size_t)r * (kHd + 4);
-  auto at = [&](int i) { return part + ((size_t)i * 2 + (i == i0 ? 1 : 0)) * kPart; };
+// Channels 4 q on of row r of an item with parts in the CTAs i0 .. last: every
+// `step`-th part from CTA i on, added in order.
+struct Sums {
   float top = kNone, sum = 0.0f, o[4] = {};
-  constexpr int kU = 8;  // parts under way
-#pragma unroll 1
-  for (int i = i0 + group; i <= last; i += kU * kGroups) {
-    float2 ml[kU];
-    float x[kU][4];
-    float to = top;
-#pragma unroll
-    for (int k = 0; k < kU; ++k) {  // (past the end: the first one, without weight)
-      const float *from = at(i + k * kGroups <= last ? i + k * kGroups : i);
-      ml[k] = *reinterpret_cast<const float2 *>(from + kHd);
-      load4(from + 4 * q, x[k]);
-      to = fmaxf(to, ml[k].x);
-    }
+  __device__ __forceinline__ void rescale(float to) {
     const float f = exp2_(top - to);
     top = to;
     sum *= f;
 #pragma unroll
     for (int d = 0; d < 4; ++d) o[d] *= f;
+  }
+  __device__ __forceinline__ void add(float s, const float (&x)[4], float e) {
+    sum += s * e;
 #pragma unroll
-    for (int k = 0; k < kU; ++k) {
-      if (i + k * kGroups > last) continue;
-      const float e = exp2_(ml[k].x - to);
-      sum += ml[k].y * e;
+    for (int d = 0; d < 4; ++d) o[d] += x[d] * e;
+  }
+};
+template <int kHd, int R, int kU>
+__device__ __forceinline__ Sums add_parts(const AttnArgs &P, int i0, int last, int r, int q, int i,
+                                          int step) {
+  constexpr size_t kPart = (size_t)(8 * R) * (kHd + 4);
+  const float *part = P.part + kSplitBytes / 4 + (size_t)r * (kHd + 4);
+  Sums s;
+#pragma unroll 1
+  for (; i <= last; i += kU * step) {
+    float2 ml[kU];
+    float x[kU][4], to = s.top;
 #pragma unroll
-      for (int d = 0; d < 4; ++d) o[d] += x[k][d] * e;
+    for (int k = 0; k < kU; ++k) {  // (past the end: the first one, without weight)
+      const int c = i + k * step <= last ? i + k * step : i;
+      const float *from = part + ((size_t)c * 2 + (c == i0 ? 1 : 0)) * kPart;
+      ml[k] = *reinterpret_cast<const float2 *>(from + kHd);
+      load4(from + 4 * q, x[k]);
+      to = fmaxf(to, ml[k].x);
     }
-  }
-  sums[group][q] = make_float4(o[0], o[1], o[2], o[3]);
-  if (q == 0) {
-    tops[group] = top;
-    ls[group] = sum;
-  }
-  __syncthreads();
-  if (group) return;
-  float all = kNone;
+    s.rescale(to);
 #pragma unroll
-  for (int i = 0; i < kGroups; ++i) all = fmaxf(all, tops[i]);
-  float y[4] = {};
-  sum = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kGroups; ++i) {
-    const float f = exp2_(tops[i] - all);
-    const float4 v = sums[i][q];
-    sum += ls[i] * f;
-    y[0] += v.x * f; y[1] += v.y * f; y[2] += v.z * f; y[3] += v.w * f;
+    for (int k = 0; k < kU; ++k)
+      if (i + k * step <= last) s.add(ml[k].y, x[k], exp2_(ml[k].x - to));
   }
-  const float inv = 1.0f / sum;
-#pragma unroll
-  for (int d = 0; d < 4; ++d) y[d] *= inv;
-  const size_t to = ((size_t)b * P.M + mt) * P.qh + head;
-  store4(static_cast<T *>(P.o) + to * kHd + 4 * q, y);
-  if (P.lse && q == 0) P.lse[to] = (all + log2f(sum)) * 0.693147180559945f;
+  return s;
 }
 
-// Many items in several CTAs: a block for a row of the one that begins in CTA
-// blockIdx / rows, if one does, as that CTA left word of it.
+template <int kHd, bool kBf16>
+__device__ __forceinline__ void put_row(const AttnArgs &P, Sums &s, int b, int mt, int head, int q) {
+  using T = typename std::conditional<kBf16, __nv_bfloat16, float>::type;
+  const float inv = 1.0f / s.sum;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) s.o[d] *= inv;
+  const size_t to = ((size_t)b * P.M + mt) * P.qh + head;
+  store4(static_cast<T *>(P.o) + to * kHd + 4 * q, s.o);
+  if (P.lse && q == 0) P.lse[to] = (s.top + log2f(s.sum)) * 0.693147180559945f;
+}
+
+// Many items in several CTAs, of few parts each: kHd / 4 threads for a row of the
+// one that begins in CTA blockIdx.x, if one does, as that CTA left word of it.
 template <int kHd, bool kBf16, int R>
-__global__ void __launch_bounds__(128)
-    attn_join_kernel(const AttnArgs P, int rows) {
+__global__ void __launch_bounds__(kThreads)
+    attn_join_kernel(const AttnArgs P) {
+  constexpr int kQ = kHd / 4;
   // (every block waits, also one that has nothing to do: the kernel behind this
   // one waits for this one alone)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int i0 = blockIdx.x / rows, r = blockIdx.x - i0 * rows;
-  const Split s = reinterpret_cast<const Split *>(P.part)[i0];
+  const Split s = reinterpret_cast<const Split *>(P.part)[blockIdx.x];
   if (s.last < 0) return;
+  const int r = blockIdx.y * (kThreads / kQ) + threadIdx.x / kQ, q = threadIdx.x % kQ;
   const int row = s.row0 + r, mt = row / P.group;
-  if (mt >= P.M || s.start + mt >= s.len) return;  // (no token of the sequence)
-  join_row<kHd, kBf16, R, 128>(P, i0, s.last, r, s.b, mt, s.h * P.group + row - mt * P.group);
+  if (r >= 8 * R || mt >= P.M || s.start + mt >= s.len) return;  // (no token of the sequence)
+  Sums x = add_parts<kHd, R, 4>(P, blockIdx.x, s.last, r, q, blockIdx.x, 1);
+  put_row<kHd, kBf16>(P, x, s.b, mt, s.h * P.group + row - mt * P.group, q);
 }
 
 // Few items of many parts (at most 32 sequences): a block for each row, which finds
@@ -1160,7 +1147,22 @@ __global__ void __launch_bounds__(512)
   const long long u = before * items + (long long)n * (h * nrt + row / (8 * R));
   const int i0 = share.of(u), last = share.of(u + n - 2);
   if (i0 == last) return;
-  join_row<kHd, kBf16, R, 512>(P, i0, last, row % (8 * R), b, mt, h * P.group + row - mt * P.group);
+  // streams of parts, joined in their order
+  constexpr int kQ = kHd / 4, kGroups = 512 / kQ;
+  __shared__ Sums sums[kGroups][kQ];
+  const int q = threadIdx.x % kQ, group = threadIdx.x / kQ;
+  sums[group][q] = add_parts<kHd, R, 8>(P, i0, last, row % (8 * R), q, i0 + group, kGroups);
+  __syncthreads();
+  if (group) return;
+  Sums all = sums[0][q];
+#pragma unroll
+  for (int i = 1; i < kGroups; ++i) {
+    const Sums &x = sums[i][q];
+    const float to = fmaxf(all.top, x.top);
+    all.rescale(to);
+    all.add(x.sum, x.o, exp2_(x.top - to));
+  }
+  put_row<kHd, kBf16>(P, all, b, mt, h * P.group + row - mt * P.group, q);
 }
 
 // CTAs of a call: at most one share each for the longest that the table holds.
@@ -1208,9 +1210,9 @@ cudaError_t go(const AttnArgs &P, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, attn_join_few_kernel<kHd, kKind, kBf16, R>, P, grid);
   }
   const int rows = P.M * P.group < 8 * R ? P.M * P.group : 8 * R;
-  cfg.gridDim = dim3((unsigned)(grid * rows));
-  cfg.blockDim = dim3(128);
-  return cudaLaunchKernelEx(&cfg, attn_join_kernel<kHd, kBf16, R>, P, rows);
+  constexpr int kRowsBlock = kThreads / (kHd / 4);
+  cfg.gridDim = dim3((unsigned)grid, (unsigned)((rows + kRowsBlock - 1) / kRowsBlock));
+  return cudaLaunchKernelEx(&cfg, attn_join_kernel<kHd, kBf16, R>, P);
 }
 
 // Row tiles of 8, 16 or (8 bits, teams) 24: the fewest eights of rows, and of two
