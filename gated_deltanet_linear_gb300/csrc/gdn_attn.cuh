@@ -789,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
                 float &x = p[j][i][2 * q + e];
                 x = exp2_(fmaf(s[j][i][2 * q + e], f[i][e] * ks[j][q], -m[i][e]));
                 y[e] = kHalf ? x * vs[j][q] : x;
-                off |= !(y[e] <= kTop);
+                off |= !(fabsf(y[e]) <= kTop);
               }
               cut<kHalf, kPP>(y[0], y[1], pr[q]);
             }
@@ -825,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
 #pragma unroll
               for (int q = 0; q < 2; ++q)
                 x = fmaxf(x, s[j][i][2 * q + e] * (f[i][e] * ks[j][q]) +
-                                 (kHalf ? rough_log2(vs[j][q]) - kUp : 0.0f));
+                                 (kHalf ? rough_log2(fabsf(vs[j][q])) - kUp : 0.0f));
             x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
             x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
             x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));

@@ -331,3 +331,123 @@ def test_workspaces_may_hold_anything(fill):
             o = torch.zeros_like(q)
             gdn.gdn_attn_step_m(cache, q, table, start, o, scale=0.1, workspace=ws)
             assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("kind,hd,dtype", [("int8", 128, "bf16"), ("bf16", 256, "fp32"), ("e4m3", 256, "fp32"),
+                                           ("bf16", 64, "bf16")])
+@pytest.mark.parametrize("M,kvh,group", [(64, 1, 3), (33, 2, 1), (17, 1, 5)])
+def test_many_tokens(kind, hd, dtype, M, kvh, group):
+    """Up to 64 tokens: several row tiles, masks over several tiles of
+    positions, and values that are not finite among the call's own."""
+    gen = gen_of(17)
+    page, lens = 16, [M, M + 1, 200]
+    cols = -(-max(lens) // page)
+    c = make_cache(kind, 3 * cols, kvh, page, hd, gen, "cuda")
+    table = make_table(3 * cols, 3, cols, gen, "cuda")
+    junk_behind(c, table, lens, page, kind)
+    q = torch.randn(3, M, kvh * group, hd, generator=gen, device="cuda").to(TYPES[dtype])
+    start = [n - M for n in lens]
+    o, _ = check(c, kind, dtype, q, table, start, None, hd ** -0.5, page)
+    p = lens[2] - M // 2                                 # seen by the later half
+    if kind == "bf16":
+        c["v"][int(table[2, p // page]), 0, p % page, 3] = float("inf")
+    else:
+        c["vs"][int(table[2, p // page]), 0, p % page] = float("nan")
+    o2, _ = call(c, q, table, ints(start), hd ** -0.5)
+    m = p - start[2]
+    assert torch.equal(o2[:2], o[:2]) and torch.equal(o2[2, :m], o[2, :m])
+    assert not bool(torch.isfinite(o2[2, m:, :group, 3]).any())
+
+
+def test_many_heads():
+    gen = gen_of(18)
+    for kvh, group in ((300, 1), (2, 100), (1, 257)):
+        c = make_cache("int8", 6, kvh, 16, 64, gen, "cuda")
+        table = make_table(6, 2, 3, gen, "cuda")
+        q = torch.randn(2, 1, kvh * group, 64, generator=gen, device="cuda")
+        check(c, "int8", "fp32", q, table, [40, 3], None, 0.125, 16)
+
+
+def test_negative_scales():
+    """A cache filled elsewhere may hold them: they are numbers like others."""
+    gen = gen_of(19)
+    hd, page, n = 128, 32, 500
+    c = make_cache("int8", 16, 2, page, hd, gen, "cuda")
+    for x in ("ks", "vs"):
+        c[x] *= torch.where(torch.rand(c[x].shape, generator=gen, device="cuda") < 0.5, -1.0, 1.0)
+    c["vs"][:, :, ::3] *= 1e6
+    table = make_table(16, 1, 16, gen, "cuda")
+    q = torch.randn(1, 1, 8, hd, generator=gen, device="cuda")
+    check(c, "int8", "fp32", q, table, [n - 1], None, 0.1, page)
+
+
+def test_empty_batches_and_refusals():
+    c = make_cache("int8", 4, 2, 16, 64, gen_of(20), "cuda")
+    cache = cache_of(c)
+    ws = torch.empty(gdn.gdn_attn_workspace(cache, 2, 4), dtype=torch.uint8, device="cuda")
+    q = torch.zeros(0, 2, 4, 64, device="cuda")
+    table = torch.zeros(0, 3, dtype=torch.int32, device="cuda")
+    gdn.gdn_attn_step_m(cache, q, table, table[:, 0].contiguous(), torch.empty_like(q), workspace=ws)
+    k = torch.zeros(0, 2, 2, 64, device="cuda")
+    gdn.gdn_kv_write_m(cache, k, k, table, table[:, 0].contiguous())
+    gdn.gdn_kv_read(cache, table, None, k, k)
+    q = torch.zeros(1, 2, 4, 64, device="cuda")
+    table = ints([[0, 1]])
+    ok = dict(workspace=ws)
+    call_ = gdn.gdn_attn_step_m
+    o = torch.empty_like(q)
+    call_(cache, q, table, ints([3]), o, **ok)
+    for args, kw, status in (((q, table, ints([3]), q), ok, gdn.GDN_EALIAS),
+                             ((q, table, ints([3]), o), dict(workspace=ws[:100]), gdn.GDN_ERANGE),
+                             ((q, table, ints([3]), o), {}, gdn.GDN_EINVAL),
+                             ((q, table, ints([3]), o), dict(workspace=o.view(torch.uint8)), gdn.GDN_ERANGE),
+                             ((q.cpu(), table, ints([3]), o), ok, gdn.GDN_EPTR),
+                             ((q, table.cpu(), ints([3]), o), ok, gdn.GDN_EPTR)):
+        with pytest.raises(gdn.GDNError) as e:
+            call_(cache, *args, **kw)
+        assert e.value.status == status
+    big = torch.empty(ws.numel() + o.numel() * 4, dtype=torch.uint8, device="cuda")
+    inside = big[:o.numel() * 4].view(torch.float32).view(o.shape)
+    with pytest.raises(gdn.GDNError) as e:
+        call_(cache, q, table, ints([3]), inside, workspace=big)
+    assert e.value.status == gdn.GDN_EALIAS
+    with pytest.raises(gdn.GDNError) as e:                # a cache that is its own values
+        gdn.gdn_kv_write_m(gdn.KVCache(c["k"], c["k"], c["ks"], c["vs"]), q[:, :, :2].contiguous(),
+                           q[:, :, :2].contiguous(), table, ints([0]))
+    assert e.value.status == gdn.GDN_EALIAS
+    with pytest.raises(gdn.GDNError) as e:                # one row for all tokens
+        gdn.gdn_kv_write_m(cache, q[:, :1, :2].expand(1, 2, 2, 64), q[:, :, :2].contiguous(), table, ints([0]))
+    assert e.value.status == gdn.GDN_ESHAPE
+    for bad in (dict(q=q.double()), dict(q=q[..., :32]), dict(table=table.long()), dict(start=ints([1, 2])),
+                dict(o=o.bfloat16()), dict(o=o[:, :1])):
+        a = dict(q=q, table=table, start=ints([3]), o=o)
+        a.update(bad)
+        with pytest.raises(ValueError):
+            call_(cache, a["q"], a["table"], a["start"], a["o"], **ok)
+
+
+@pytest.mark.parametrize("kind,hd,M,group", [("int8", 128, 1, 4), ("bf16", 256, 1, 8), ("e4m3", 256, 4, 6),
+                                             ("int8", 64, 2, 5), ("bf16", 128, 3, 7)])
+def test_nothing_outside_o_lse_and_the_workspace(kind, hd, M, group):
+    """Guard bands around what a call writes, with joins over all CTAs."""
+    gen = gen_of(23)
+    page, T, kvh = 64, 60000, 2
+    cols = -(-T // page)
+    c = make_cache(kind, cols, kvh, page, hd, gen, "cuda")
+    table = make_table(cols, 1, cols, gen, "cuda")
+    cache = cache_of(c)
+    n = gdn.gdn_attn_workspace(cache, M, kvh * group)
+    room = torch.full((n + 8192,), 0xa5, dtype=torch.uint8, device="cuda")
+    q = torch.randn(1, M, kvh * group, hd, generator=gen, device="cuda")
+    out = torch.full((q.numel() + 512,), 7.0, device="cuda")
+    o = out[256:256 + q.numel()].view(q.shape)
+    ls = torch.full((M * kvh * group + 256,), 7.0, device="cuda")
+    lse = ls[128:128 + M * kvh * group].view(1, M, -1)
+    before = {x: None if c[x] is None else c[x].view(torch.uint8).clone() for x in ("k", "v", "ks", "vs")}
+    gdn.gdn_attn_step_m(cache, q, table, ints([T - M]), o, scale=0.1, lse=lse, workspace=room[4096:4096 + n])
+    assert bool((room[:4096] == 0xa5).all()) and bool((room[4096 + n:] == 0xa5).all())
+    assert bool((out[:256] == 7.0).all()) and bool((out[-256:] == 7.0).all())
+    assert bool((ls[:128] == 7.0).all()) and bool((ls[-128:] == 7.0).all())
+    assert bool((o != 7.0).all()) and bool((lse != 7.0).all())
+    for x, was in before.items():
+        assert was is None or torch.equal(c[x].view(torch.uint8), was)

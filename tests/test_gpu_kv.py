@@ -249,3 +249,56 @@ def test_bad_pages_and_lengths_write_nothing():
     assert int(err) == 1 and not torch.equal(cache.k[5, :, 15], before[5, :, 15])
     before[5, :, 15] = cache.k[5, :, 15]
     assert torch.equal(cache.k, before)
+
+
+def test_far_positions_and_far_pages():
+    """The last positions of the longest table, in pages behind 2^32 bytes of
+    a cache."""
+    hd, page, kvh = 256, 256, 8
+    pages = 2 ** 32 // (page * kvh * hd) + 5
+    k = torch.zeros(pages, kvh, page, hd, dtype=torch.int8, device="cuda")
+    cache = gdn.KVCache(k, torch.zeros_like(k), torch.zeros(pages, kvh, page, device="cuda"),
+                        torch.zeros(pages, kvh, page, device="cuda"))
+    cols = gdn.GDN_KV_MAX_POSITIONS // page
+    table = torch.full((1, cols), -1, dtype=torch.int32, device="cuda")
+    table[0, -1] = pages - 1
+    gen = gen_of(21)
+    x = torch.randn(1, 40, kvh, hd, generator=gen, device="cuda")
+    f, _ = gdn.gdn_rope_freqs(64, 1e6)
+    start = ints([gdn.GDN_KV_MAX_POSITIONS - 40])
+    err = ints([0])
+    gdn.gdn_kv_write_m(cache, x, x, table, start, rope=gdn.Rope(f), err_dev=err)
+    ko, vo = torch.empty_like(x), torch.empty_like(x)
+    gdn.gdn_kv_read(cache, table, start, ko, vo, err_dev=err)
+    assert int(err) == 0
+    pos = start.long()[:, None] + torch.arange(40, device="cuda")
+    rk, bk = near(x, pos, f, False, 1.0, "fp32")
+    top = rk.abs().amax(-1, keepdim=True)
+    # half a code, the turn's error, and the frequency's rounding at 2^30
+    lim = 0.5 * top / 127 * (1 + 2.0 ** -20) + bk.amax(-1, keepdim=True) + 2.0 ** -19 * top
+    assert ((ko.double() - rk).abs() <= lim).all()
+    c, s = codes(x.double(), "int8")
+    assert torch.equal(vo, c.float() * s[..., None])
+    assert not bool(cache.k[:-1].any())
+    gdn.gdn_kv_write_m(cache, x, x, table, start + 1, err_dev=err)     # one behind the end
+    assert int(err) == 1
+
+
+def test_calls_on_several_streams():
+    """Writes of different sequences into one cache on three streams at once
+    are those of one call."""
+    gen = gen_of(22)
+    B, M, hd, kvh, page = 9, 50, 128, 2, 16
+    k, v = (torch.randn(B, M, kvh, hd, generator=gen, device="cuda") for _ in "kv")
+    table = torch.randperm(B * 4, generator=gen, device="cuda").int().view(B, 4)
+    start = ints([3] * B)
+    one, many = empty_cache("int8", B * 4, kvh, page, hd), empty_cache("int8", B * 4, kvh, page, hd)
+    gdn.gdn_kv_write_m(one, k, v, table, start)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for i, s in enumerate(streams):
+        b = slice(3 * i, 3 * i + 3)
+        gdn.gdn_kv_write_m(many, k[b], v[b], table[b], start[b], stream=s)
+    torch.cuda.synchronize()
+    for x in ("k", "v", "k_scale", "v_scale"):
+        assert torch.equal(getattr(one, x), getattr(many, x))
