@@ -43,7 +43,7 @@
 //            passes 2^15: an fp16 part ends 2^-37 of the largest below.  w as two
 //            parts (22 bits); of bf16 tokens as one: 2^-11 of each weight,
 //            beside the 2^-8 that the result is rounded by (64 sequences of 4096:
-//            91 us; fp32 tokens, with two parts of q and weights, 98).
+//            91 us; fp32 tokens, with two parts of q and weights, 99).
 //   bf16     q one bf16 part or (fp32) three, weights two parts (16 bits: one
 //            would be rounded as much as the result) or (fp32) three.
 //
@@ -673,9 +673,9 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
       issue(std::bool_constant<(kSlots - 1) % 2 == 1>{});
       uint32_t slot = ring + get * Z::kSlot;
       const bool broken = bad >> get & 1;
-      // (several sums where there are few: a product waits for the last one of
-      // its sum)
-      constexpr int kC = kMT * R <= 2 ? 2 : 1;
+      // (several sums where there are few, as a product waits for the last one of
+      // its sum; and one for each of three parts, small parts apart from large)
+      constexpr int kC = kQP == 3 ? 3 : kMT * R <= 2 ? 2 : 1;
       float part[kC][kMT][R][4] = {};
 #pragma unroll
       for (int sg = 0; sg < kHd / (4 * kVec); ++sg) {
@@ -715,14 +715,14 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
       // ---- their maximum, weights and sums: a lane has positions g and g + 8
       // of 16, rows 2 t and 2 t + 1 of 8
       float (&s)[kMT][R][4] = part[0];
-      if (kC == 2) {
+#pragma unroll
+      for (int c = kC - 1; c > 0; --c)
 #pragma unroll
         for (int j = 0; j < kMT; ++j)
 #pragma unroll
           for (int i = 0; i < R; ++i)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s[j][i][k] += part[kC - 1][j][i][k];
-      }
+            for (int k = 0; k < 4; ++k) part[c - 1][j][i][k] += part[c][j][i][k];
       float ks[kMT][2], vs[kMT][2];
 #pragma unroll
       for (int j = 0; j < kMT; ++j)
@@ -909,35 +909,54 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
         }
         __syncwarp();
       }
-#pragma unroll
-      for (int j = 0; j < kVT; ++j) {
+      // Four 8 x 8 tiles of 16 bits, transposed: neighbouring positions of a
+      // channel side by side (bf16), or of two channels (8 bits: two tiles of
+      // 16 channels, even ones in the upper half of a product's rows).
+      constexpr int kStep = kKind == kKvBf16 ? 1 : 2;
+      auto products = [&](int j, int d, float (*to)[R][4]) {
         // (in teams: the own 16 positions, then the other warp's)
         const int row = kS == 1 ? 16 * j : 16 * (j ^ sub);
-        // four 8 x 8 tiles of 16 bits, transposed: neighbouring positions of a
-        // channel side by side (bf16), or of two channels (8 bits: two tiles of
-        // 16 channels, even ones in the upper half of a product's rows)
-        constexpr int kStep = kKind == kKvBf16 ? 1 : 2;
+        uint32_t x[4];
+        const int r = row + (lane & 7) + 8 * (kStep == 1 ? lane >> 4 : lane >> 3 & 1);
+        const int cc = kStep == 1 ? 2 * d + (lane >> 3 & 1) : d + (lane >> 4);
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                     : "r"(slot + 16 * v_place<kVRow>(r, cc)));
+#pragma unroll
+        for (int q = 0; q < kStep; ++q) {
+          uint32_t a[4] = {x[0], x[1], x[2], x[3]};
+          if (kHalf) {
+            widen_v<kKind>(x[2 * q], a[0], a[1]);
+            widen_v<kKind>(x[2 * q + 1], a[2], a[3]);
+          }
+#pragma unroll
+          for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int p = kPP - 1; p >= 0; --p)  // (small parts first)
+              mma<kHalf>(to[q][i], a[0], a[1], a[2], a[3], w[j][i][p]);
+        }
+      };
+      if (kBf16 || R == 3) {
+#pragma unroll
+        for (int j = 0; j < kVT; ++j)
+#pragma unroll
+          for (int d = 0; d < kDT; d += kStep) products(j, d, acc + d);
+      } else {
+        // A product's sum is cut off, not rounded: over long sequences that adds up,
+        // so a tile's sums are made from 0 and added to the others rounded.  (24
+        // rows have no registers for it: over 60000 positions of int8 1.4e-6 of o
+        // in place of 0.9e-6, but 54 us in place of 60 for 4 tokens.)
 #pragma unroll
         for (int d = 0; d < kDT; d += kStep) {
-          uint32_t x[4];
-          const int r = row + (lane & 7) + 8 * (kStep == 1 ? lane >> 4 : lane >> 3 & 1);
-          const int cc = kStep == 1 ? 2 * d + (lane >> 3 & 1) : d + (lane >> 4);
-          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                       : "r"(slot + 16 * v_place<kVRow>(r, cc)));
+          float tile[kStep][R][4] = {};
 #pragma unroll
-          for (int q = 0; q < kStep; ++q) {
-            uint32_t a[4] = {x[0], x[1], x[2], x[3]};
-            if (kHalf) {
-              widen_v<kKind>(x[2 * q], a[0], a[1]);
-              widen_v<kKind>(x[2 * q + 1], a[2], a[3]);
-            }
+          for (int j = 0; j < kVT; ++j) products(j, d, tile);
+#pragma unroll
+          for (int q = 0; q < kStep; ++q)
 #pragma unroll
             for (int i = 0; i < R; ++i)
 #pragma unroll
-              for (int p = 0; p < kPP; ++p)
-                mma<kHalf>(acc[d + q][i], a[0], a[1], a[2], a[3], w[j][i][p]);
-          }
+              for (int k = 0; k < 4; ++k) acc[d + q][i][k] += tile[q][i][k];
         }
       }
       get = get + 1 == kSlots ? 0 : get + 1;

@@ -12,7 +12,8 @@
 // at far positions (2^20 x 2^-24), so a frequency is held as turns a position
 // in 64-bit fixed point: pos times it is exact modulo one turn, an integer
 // product drops the whole turns, and the rest goes to sincospif as a number in
-// [-1, 1].  Error of an angle: 2^-53 pos of the frequency's own rounding plus 1e-7.
+// [-1, 1], with what its rounding to a float left of it added to first order.
+// Error of an angle: 2^-53 pos of the frequency's own rounding.
 // hd / 8 lanes take a token and a run of its heads, and keep its cosines and sines
 // in registers.
 //
@@ -307,9 +308,12 @@ __global__ void __launch_bounds__(kThreads, 4)
 #pragma unroll 1
     for (int i = gl; i < half; i += kLanes) {
       const long long a = (long long)(phase[i] * (unsigned long long)(long long)tk.pos);
+      // the angle as a float and what its rounding left of it, to first order
+      const float near = __ll2float_rn(a);
+      const float rest = __ll2float_rn(a - __float2ll_rn(near)) * 3.4061215800865545e-19f;  // pi 2^-63
       float x, y;
-      sincospif(__ll2float_rn(a) * 1.0842021724855044e-19f, &y, &x);  // 2^-63
-      cs[i] = make_float2(P.amp * x, P.amp * y);
+      sincospif(near * 1.0842021724855044e-19f, &y, &x);  // 2^-63
+      cs[i] = make_float2(P.amp * (x - y * rest), P.amp * (y + x * rest));
     }
     __syncwarp();
     const int f0 = !turned ? 0 : pairs ? 4 * gl : 8 * gl - (upper ? half : 0);
