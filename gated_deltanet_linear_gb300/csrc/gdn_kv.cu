@@ -30,7 +30,7 @@
 // 94 % of the copy rate).  8 padded prompts of up to 4096 tokens x 32 + 16 heads
 // into e4m3 70 us (369 MB, 5.3 TB/s: the rounding of k and v, 40 % of the
 // instructions, beside the loads) and back 16 us.  65531 positions x 4 heads of 256,
-// int8 to bf16: 62 us (96 %).  64 tokens of 24 + 8 heads: 3.1 us a kernel,
+// int8 to bf16: 62 to 66 us (90 to 96 %).  64 tokens of 24 + 8 heads: 3.1 us a kernel,
 // the chain from lengths to pages and rows to stores.
 
 #include <cuda_bf16.h>
@@ -432,31 +432,40 @@ struct Codes<kKvBf16> {
 };
 
 // Rows of the cache as k and v [B][M][kvh][hd]: kLanes lanes take a token and
-// P.run of its heads.
-template <typename T, int kKind, int kLanes>
+// P.run of its heads, K and V of four at a time; of a single head (kOne) the rows
+// of four tokens, so that as much is under way.
+template <typename T, int kKind, int kLanes, bool kOne>
 __global__ void __launch_bounds__(kThreads, 4)
     kv_read_kernel(const KvRows P) {
   constexpr int kHd = 8 * kLanes, kGroups = kThreads / kLanes;
-  constexpr int kRows = 4;  // K and V of so many under way
+  constexpr int kRows = 4;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int tid = threadIdx.x, gl = tid % kLanes;
+  const int tid = threadIdx.x, gl = tid % kLanes, kvh = P.c.kvh;
   const unsigned group = lanes_of_row<kLanes>();
-  const int runs = (P.c.kvh + P.run - 1) / P.run;
   const long long job = (long long)blockIdx.x * kGroups + tid / kLanes;
-  if (job >= P.tokens * runs) return;
-  const long long tok = job / runs;
-  const int h0 = (int)(job - tok * runs) * P.run, h1 = min(h0 + P.run, P.c.kvh);
-  const Token tk = place(P, tok);
-  if (!tk.on || tk.at < 0) return;
+  const int runs = (kvh + P.run - 1) / P.run;
+  const long long tok = kOne ? job * kRows : job / runs;
+  if (tok >= P.tokens) return;
+  const int h0 = kOne ? 0 : (int)(job - tok * runs) * P.run, h1 = kOne ? kRows : min(h0 + P.run, kvh);
+  Token tk[kOne ? kRows : 1];
+#pragma unroll
+  for (int i = 0; i < (kOne ? kRows : 1); ++i) {
+    tk[i] = Token{-1, 0, 0};
+    if (tok + i < P.tokens) tk[i] = place(P, tok + i);
+  }
+  if (!kOne && (!tk[0].on || tk[0].at < 0)) return;
 #pragma unroll 1
   for (int h = h0; h < h1; h += kRows) {
     Codes<kKind> k[kRows], v[kRows];
     float ks[kRows], vs[kRows];
+    bool there[kRows];
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
-      if (h + j >= h1) continue;
-      const size_t row = (size_t)tk.at + ((size_t)(h + j) << P.c.page_shift);
+      const Token &t = tk[kOne ? j : 0];
+      there[j] = kOne ? t.on && t.at >= 0 : h + j < h1;
+      if (!there[j]) continue;
+      const size_t row = (size_t)t.at + ((size_t)(kOne ? 0 : h + j) << P.c.page_shift);
       k[j].load(P.c.k, row * kHd + 8 * gl);
       v[j].load(P.c.v, row * kHd + 8 * gl);
       ks[j] = kKind == kKvBf16 ? 1.0f : __ldg(P.c.k_scale + row);
@@ -464,8 +473,8 @@ __global__ void __launch_bounds__(kThreads, 4)
     }
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
-      if (h + j >= h1) continue;
-      const long long to = (tok * P.c.kvh + h + j) * kHd + 8 * gl;
+      if (!there[j]) continue;
+      const long long to = (tok * kvh + h + j) * kHd + 8 * gl;  // (kOne: of token tok + j)
       float x[8];
       k[j].values(x);
       if (kKind != kKvBf16) {
@@ -498,7 +507,11 @@ cudaError_t rows_go(KvRows P, cudaStream_t stream, bool read) {
   P.run = (int)(run < heads ? run : heads);
   const long long runs = (heads + P.run - 1) / P.run;
   constexpr int kTokens = 32 / kLanes;
-  const long long blocks = read ? (P.tokens * runs + kGroups - 1) / kGroups
+  // Four tokens a job pay where there are many (37 x 48751 positions of 64, bf16:
+  // 149 us with one, 77 with four; 3 x 16962 of 128, int8: 9.9 and 11.9 us).
+  const bool one = read && heads == 1 && rows > 16 * full;
+  const long long jobs = one ? (P.tokens + 3) / 4 : P.tokens * runs;
+  const long long blocks = read ? (jobs + kGroups - 1) / kGroups
                                 : (P.tokens + 8 * kTokens - 1) / (8 * kTokens) * runs;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
@@ -511,7 +524,9 @@ cudaError_t rows_go(KvRows P, cudaStream_t stream, bool read) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if constexpr (kKind >= 0) {
-    if (read) return cudaLaunchKernelEx(&cfg, kv_read_kernel<T, kKind, kLanes>, P);
+    if (read)
+      return one ? cudaLaunchKernelEx(&cfg, kv_read_kernel<T, kKind, kLanes, true>, P)
+                 : cudaLaunchKernelEx(&cfg, kv_read_kernel<T, kKind, kLanes, false>, P);
   }
   return cudaLaunchKernelEx(&cfg, kv_rows_kernel<T, kKind, kLanes>, P);
 }

@@ -302,3 +302,36 @@ def test_calls_on_several_streams():
     torch.cuda.synchronize()
     for x in ("k", "v", "k_scale", "v_scale"):
         assert torch.equal(getattr(one, x), getattr(many, x))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8"])
+@pytest.mark.parametrize("kvh,hd,T", [(1, 64, 65003), (2, 128, 4003), (1, 256, 20003), (1, 128, 4003), (3, 64, 4003)])
+def test_reads_of_few_heads(kind, kvh, hd, T):
+    """Many positions of one to three heads, ends in the middle of what a group
+    of lanes takes, a page that the cache has not."""
+    gen = gen_of(24)
+    page, B = 16, 5
+    cols = -(-T // page)
+    pages = B * cols
+    k = torch.randn(pages, kvh, page, hd, generator=gen, device="cuda")
+    k = (k * 30).round().clamp(-127, 127).to(torch.int8) if kind == "int8" else k.bfloat16()
+    v = k.flip(0).contiguous()
+    s = None if kind == "bf16" else torch.rand(pages, kvh, page, generator=gen, device="cuda")
+    cache = gdn.KVCache(k, v, s, None if s is None else s.flip(0).contiguous())
+    table = torch.randperm(pages, generator=gen, device="cuda").int().view(B, cols)
+    counts = [T, 0, 1, 2001, T - 5]
+    bad = table.clone()
+    bad[3, 7] = pages
+    err = ints([0])
+    out = [torch.full((B, T, kvh, hd), 9.0, device="cuda") for _ in "kv"]
+    gdn.gdn_kv_read(cache, bad, None, *out, counts=ints(counts), err_dev=err)
+    assert int(err) == 1
+    for got, c, sc in ((out[0], k, cache.k_scale), (out[1], v, cache.v_scale)):
+        x = c[table.long()].float()
+        if sc is not None:
+            x = x * sc[table.long()][..., None]
+        x = x.transpose(2, 3).reshape(B, -1, kvh, hd)[:, :T].clone()
+        for b, n in enumerate(counts):
+            x[b, n:] = 9.0
+        x[3, 7 * page:8 * page] = 9.0
+        assert torch.equal(got, x)
