@@ -668,8 +668,8 @@ size_t gdn_attn_workspace(const gdn_kv_cache *cache, int M, int qh);
  *   lse   NULL, or fp32 [B][M][qh]: log sum_p exp(scale q . k_p)
  *   workspace  at least gdn_attn_workspace() bytes (GDN_ERANGE if smaller);
  *         calls that may overlap on the GPU need one each
- * A page number that the cache has not sets *err_dev, and the rows of o and lse
- * that attend over that page's group of keys are NaN.
+ * A page number that the cache has not sets *err_dev, and the sequence's rows of
+ * o and lse are NaN, also those of tokens in front of that page.
  * Numbers: every sum, maximum and weight is fp32.  8-bit codes enter the
  * products as they are; an fp32 q as two fp16 numbers scaled by its row
  * (22 bits), weights times scales as two fp16 numbers (22 bits, down to 2^-37 of
