@@ -41,11 +41,13 @@
 //            applied to the scores, and to the weights: w_j = p_j vscale_j.  The
 //            reference is set so that the largest w is 2^12, and anew when one
 //            passes 2^15: an fp16 part ends 2^-37 of the largest below.  w as two
-//            parts (22 bits); of bf16 tokens as one: 2^-11 of each weight,
-//            beside the 2^-8 that the result is rounded by (64 sequences of 4096:
-//            91 us; fp32 tokens, with two parts of q and weights, 99).
-//   bf16     q one bf16 part or (fp32) three, weights two parts (16 bits: one
-//            would be rounded as much as the result) or (fp32) three.
+//            parts (22 bits).
+//   bf16     q one bf16 part or (fp32) three, weights three parts (24 bits).
+// The weights keep these parts for bf16 tokens too: a single fp16 part (2^-11 of
+// each weight) or two bf16 ones (2^-17) put a bf16 result on the other side of a
+// border many times as often as fp32 sums do (64 sequences of 4096 in int8: 91 us
+// and 1.1e-3 from the rounded 64-bit result with one part, 95 us and 5e-5 with two;
+// 24 rows over bf16, 53 and 58 us).
 //
 // Measured (uniform lengths, copies from HBM at 6.8 TB/s): bf16 caches 91 to 94 %
 // of the copy rate with 4 rows a head, 8 bits 86 to 90 % (64 channels 78), where the
@@ -110,7 +112,7 @@ struct Sizes {
 template <int kKind, bool kBf16>
 struct Parts {
   static constexpr int kQ = kKind == kKvBf16 ? (kBf16 ? 1 : 3) : (kBf16 ? 1 : 2);
-  static constexpr int kP = kKind == kKvBf16 ? (kBf16 ? 2 : 3) : (kBf16 ? 1 : 2);
+  static constexpr int kP = kKind == kKvBf16 ? 3 : 2;
 };
 
 // A CTA's share of the chunks, and where an item's parts lie.

@@ -673,9 +673,8 @@ size_t gdn_attn_workspace(const gdn_kv_cache *cache, int M, int qh);
  * Numbers: every sum, maximum and weight is fp32.  8-bit codes enter the
  * products as they are; an fp32 q as two fp16 numbers scaled by its row
  * (22 bits), weights times scales as two fp16 numbers (22 bits, down to 2^-37 of
- * the largest), of bf16 tokens as one (2^-11, an eighth of what o is
- * rounded by).  bf16 caches take bf16 operands: q as it is or (fp32) as three
- * numbers, weights as two (16 bits) or (fp32) three.  A bf16 o is rounded once.
+ * the largest).  bf16 caches take bf16 operands: q as it is or (fp32) as three
+ * numbers, weights as three (24 bits).  A bf16 o is rounded once.
  * Scores are met for |scale q . k| log2 e below 2^100.
  * What is not finite: in q, its own row of o; in a row of k or v, the rows of o
  * that see it (throughout, where it came with the call's own tokens) and no
