@@ -6,9 +6,9 @@
 // h's group)):
 //     s_j = scale q_r . k_j,  j <= start[b] + m;
 //     o_r = sum_j e^{s_j} v_j / sum_j e^{s_j}.
-// One pass over the cache: each warp keeps a reference m_r (near the largest
-// score so far), the sum l_r of the weights 2^{s_j log2 e - m_r} and the sums over v
-// of its rows.  Parts of a sequence meet by
+// One pass over the cache: each warp keeps a reference m_r (the largest score when
+// it was last set), the sum l_r of the weights p_j = 2^{s_j log2 e - m_r} and the sums
+// over v of its rows.  Parts of a sequence meet by
 //     l = sum_p l_p 2^{m_p - m},  o = sum_p acc_p 2^{m_p - m} / l.
 //
 // Work split.  A sequence's positions are cut into chunks, a tile of 16 to 64
@@ -38,10 +38,14 @@
 //   8 bits   codes are exact in fp16; q of a row is scaled by a power of two to
 //            below 2^14 and cut into fp16 parts (bf16: one, exact for elements
 //            above 2^-28 of the row's largest; fp32: two, 22 bits); scales are
-//            applied to the scores, and to the weights: w_j = p_j vscale_j.  The
-//            reference is set so that the largest w is 2^12, and anew when one
-//            passes 2^15: an fp16 part ends 2^-37 of the largest below.  w as two
-//            parts (22 bits).
+//            applied to the scores, and to the weights: w_j = p_j vscale_j 2^k_r.  k_r
+//            is set with the reference so that the largest w is from 2^12 on, and
+//            anew when one passes 65000: an fp16 part ends 2^-37 of the largest
+//            below.  w as two parts (22 bits).  The sums over v are in units of
+//            2^(m_r - k_r), l_r in those of 2^m_r: the scales of v, from 0 to any
+//            size, have no say in the weights' sum (one reference for both,
+//            log2 vscale above the scores, let l leave the floats over rows of zeros;
+//            64 sequences of 4096, int8: 95 us with one, 97 with two).
 //   bf16     q one bf16 part or (fp32) three, weights three parts (24 bits).
 // The weights keep these parts for bf16 tokens too: a single fp16 part (2^-11 of
 // each weight) or two bf16 ones (2^-17) put a bf16 result on the other side of a
@@ -70,8 +74,11 @@ namespace attn {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr float kNone = -1e30f;  // the reference of rows that have seen nothing
-constexpr float kUp = 12.0f;     // weights of 8-bit rows are brought to 2^12,
-constexpr float kTop = 32768.0f;  // and may grow to this before they are again
+constexpr int kUp = 12;           // weights times scales (8 bits) are brought to 2^12,
+constexpr float kTop = 65000.0f;  // and weights and these may grow to this before they are again,
+constexpr int kFar = 126;         // by factors from 2^-126 to 2^126.  Sums over v are taken
+constexpr float kLarge = 0x1p80f, kSmall = 0x1p-60f;  // back by those between these: 2^31 weights of
+                                                      // up to 2^16 x 448 / kSmall stay floats
 constexpr int kSms = 152;
 
 // Sizes of a variant: R tiles of 8 rows.  kS warps share a tile of positions (a
@@ -270,9 +277,13 @@ __device__ __forceinline__ void cut(float x, float y, uint32_t (&p)[kN]) {
   }
 }
 
-// log2 of a scale to about 0.1, from its bits, between -90 and 129.
-__device__ __forceinline__ float rough_log2(float s) {
-  return fmaxf(fmaf((float)__float_as_int(s), 0x1p-23f, -127.0f), -90.0f);
+// 2^n for whole n from -126 on; 0 below, 2^127 above.
+__device__ __forceinline__ float power(float n) {
+  return __int_as_float((int)(fminf(fmaxf(n, -127.0f), 127.0f) + 127.0f) << 23);
+}
+// The floor of log2 x, x >= 0; -127 for numbers below the normal ones, 128 for infinity.
+__device__ __forceinline__ float whole_log2(float x) {
+  return (float)((__float_as_int(x) >> 23) - 127);
 }
 
 __device__ __forceinline__ void load4(const float *p, float (&x)[4]) {
@@ -322,13 +333,14 @@ struct Shared {
   static constexpr int kQBytes = kHd / 16 * Parts<kKind, kBf16>::kQ * R * 256;
   static constexpr int kRingAt = kQBytes;
   static constexpr int kStatAt = kRingAt + kWarps * Z::kSlots * Z::kSlot;
-  // m and l of every warp's rows, the rows' factors, counts of the search
+  // m, l and the weights' factor of every warp's rows, the rows' factors, counts of
+  // the search
   static constexpr int kWeightsAt =
-      kStatAt + kWarps * 8 * R * 8 + 8 * R * 4 + 2 * kWarps * 8 + 48;
+      kStatAt + kWarps * 8 * R * 12 + 8 * R * 4 + 2 * kWarps * 8 + 48;
   // between the warps of a team: maxima, and a tile's weights
   static constexpr int kWeights = Z::kOwn / 16 * R * Parts<kKind, kBf16>::kP * 256;
   static constexpr int kBytes =
-      kWeightsAt + (Z::kS == 1 ? 0 : kWarps * (2 * kWeights + 8 * R * 4 + 8));
+      kWeightsAt + (Z::kS == 1 ? 0 : kWarps * (2 * kWeights + 2 * 8 * R * 4 + 8));
 };
 
 template <int kHd, int kKind, bool kBf16, int R>
@@ -357,13 +369,15 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
   const int nrt = (P.M * P.group + 8 * R - 1) / (8 * R), items = P.c.kvh * nrt;
   uint32_t *const qs = reinterpret_cast<uint32_t *>(smem);
   float2 *const stat = reinterpret_cast<float2 *>(smem + Sh::kStatAt);  // [warp][8 R]
-  float *const factor = reinterpret_cast<float *>(stat + kWarps * 8 * R);  // [8 R]
+  float *const units = reinterpret_cast<float *>(stat + kWarps * 8 * R);  // [warp][8 R]
+  float *const factor = units + kWarps * 8 * R;                           // [8 R]
   long long *const room = reinterpret_cast<long long *>(factor + 8 * R);
   int *const found = reinterpret_cast<int *>(room + 2 * kWarps);  // [5]
   uint2 *const weights = reinterpret_cast<uint2 *>(smem + Sh::kWeightsAt);
   float *const maxima = reinterpret_cast<float *>(smem + Sh::kWeightsAt + 2 * kWarps * Sh::kWeights);
-  volatile int *const flags = reinterpret_cast<int *>(maxima + kWarps * 8 * R);  // [warp][2]
+  volatile int *const flags = reinterpret_cast<int *>(maxima + 2 * kWarps * 8 * R);  // [warp][2]
   signed char *const rooms = reinterpret_cast<signed char *>(found + 8);  // [kWarps]
+  signed char *const wides = rooms + kWarps;                              // [kWarps]
 
   // the token of a row (of M; at least M: none)
   auto token_of = [&](int row) { return P.M == 1 ? (int)(row >= P.group) : row / P.group; };
@@ -593,6 +607,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
 
   float acc[kDT][R][4];
   float m[R][2], l[R][2];
+  float gain[R][2];  // (8 bits) the power of two that weights times scales are brought up by
   int get = 0, turn = 0;  // (turn: of two buffers between the warps of a team)
 
   while (here.left > 0) {
@@ -653,6 +668,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
       for (int e = 0; e < 2; ++e) {
         m[i][e] = kNone;
         l[i][e] = 0.0f;
+        gain[i][e] = 1.0f;
       }
     // positions that row r of the item sees
     auto limit = [&](int r) { return min(len, start + 1 + (row0 + r) / P.group); };
@@ -667,6 +683,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
     for (int c = c0; c < c0 + n; ++c) {
       const int pos = (c * Z::kTeams + team) * kTile, mypos = pos + sub * Z::kOwn;
       if (pos >= len) continue;
+      const bool first = !any;
       any = 1;
       const bool masked = pos + kTile > seen_by_all || pos + kTile > len;
       // ---- scores of the tile: 16 positions by 8 rows a product
@@ -772,12 +789,14 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
             if (kHalf && !(fabsf(vs[j][q]) <= 3.4e38f)) vs[j][q] = 0.0f;
           }
       }
-      // Weights with the reference as it is; where one is too large for that
-      // (or NaN, which the first tile's may be) the reference is set anew.
+      // Weights with the reference and the factor as they are; where one is too
+      // large for that, and for the first tile, these are set anew.
       uint2 w[kVT][R][kPP];  // of the whole tile: the team's own first
-      float p[kMT][R][4];
+      float sum[R][2];
       auto weigh = [&]() {  // true: one does not fit
-        bool off = false;
+        float big = 0.0f;  // (a row's sum stands for its weights; NaN are no reason)
+#pragma unroll
+        for (int i = 0; i < R; ++i) sum[i][0] = sum[i][1] = 0.0f;
 #pragma unroll
         for (int j = 0; j < kMT; ++j)
 #pragma unroll
@@ -788,18 +807,20 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
               float y[2];
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                float &x = p[j][i][2 * q + e];
-                x = exp2_(fmaf(s[j][i][2 * q + e], f[i][e] * ks[j][q], -m[i][e]));
-                y[e] = kHalf ? x * vs[j][q] : x;
-                off |= !(fabsf(y[e]) <= kTop);
+                const float x = exp2_(fmaf(s[j][i][2 * q + e], f[i][e] * ks[j][q], -m[i][e]));
+                sum[i][e] += x;
+                y[e] = kHalf ? x * vs[j][q] * gain[i][e] : x;
               }
+              if (kHalf) big = fmaxf(big, fmaxf(fabsf(y[0]), fabsf(y[1])));
               cut<kHalf, kPP>(y[0], y[1], pr[q]);
             }
 #pragma unroll
             for (int k = 0; k < kPP; ++k)
               w[j][i][k] = make_uint2(transposed(pr[0][k]), transposed(pr[1][k]));
           }
-        return __any_sync(kFull, off) != 0;
+#pragma unroll
+        for (int i = 0; i < R; ++i) big = fmaxf(big, fmaxf(sum[i][0], sum[i][1]));
+        return __any_sync(kFull, big > kTop) != 0;
       };
       // to the other warp of the team, with whether the weights fit
       auto hand_over = [&](bool off) {
@@ -812,45 +833,88 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
         team_sync(team);
         return flags[(warp ^ 1) * 2 + turn] != 0;
       };
-      bool off = weigh();
-      if (kS > 1) off |= hand_over(off);
+      bool off = true;
+      if (!first) {
+        off = weigh();
+        if (kS > 1) off |= hand_over(off);
+      }
       if (off) {
-        float top[R][2];
+        // the largest of a row, over the lanes that have its positions
+        auto largest = [&](float (&x)[R][2], float *shared) {
+#pragma unroll
+          for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              x[i][e] = fmaxf(x[i][e], __shfl_xor_sync(kFull, x[i][e], 4));
+              x[i][e] = fmaxf(x[i][e], __shfl_xor_sync(kFull, x[i][e], 8));
+              x[i][e] = fmaxf(x[i][e], __shfl_xor_sync(kFull, x[i][e], 16));
+              if (kS > 1 && g == 0) shared[warp * 8 * R + 8 * i + 2 * t + e] = x[i][e];
+            }
+          if (kS == 1) return;
+          team_sync(team);
+#pragma unroll
+          for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              x[i][e] = fmaxf(x[i][e], shared[(warp ^ 1) * 8 * R + 8 * i + 2 * t + e]);
+        };
+        float top[R][2], a[R][2], more[R][2];
 #pragma unroll
         for (int i = 0; i < R; ++i)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float &x = top[i][e];
-            x = kNone;
+            top[i][e] = kNone;
 #pragma unroll
             for (int j = 0; j < kMT; ++j)
 #pragma unroll
               for (int q = 0; q < 2; ++q)
-                x = fmaxf(x, s[j][i][2 * q + e] * (f[i][e] * ks[j][q]) +
-                                 (kHalf ? rough_log2(fabsf(vs[j][q])) - kUp : 0.0f));
-            x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
-            if (kS > 1 && g == 0) maxima[warp * 8 * R + 8 * i + 2 * t + e] = x;
+                top[i][e] = fmaxf(top[i][e], s[j][i][2 * q + e] * (f[i][e] * ks[j][q]));
           }
-        if (kS > 1) team_sync(team);
+        largest(top, maxima);
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-          float a[2];
+        for (int i = 0; i < R; ++i)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            if (kS > 1)
-              top[i][e] = fmaxf(top[i][e], maxima[(warp ^ 1) * 8 * R + 8 * i + 2 * t + e]);
             const float to = fmaxf(top[i][e], m[i][e]);
-            a[e] = exp2_(m[i][e] - to);
+            more[i][e] = to - m[i][e];
+            a[i][e] = exp2_(m[i][e] - to);
             m[i][e] = to;
-            l[i][e] *= a[e];
+            l[i][e] *= a[i][e];
+            top[i][e] = 0.0f;
           }
+        if (kHalf) {
+          // The weights' unit is that of the largest weight times scale so far: it
+          // does not come down, so the factor grows by no more than the
+          // reference has (the sums over v are in that unit, l is in the
+          // reference's: a row of zeros, whose scale is 0, moves the one alone).
+#pragma unroll
+          for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int j = 0; j < kMT; ++j)
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                  top[i][e] = fmaxf(top[i][e], exp2_(fmaf(s[j][i][2 * q + e], f[i][e] * ks[j][q], -m[i][e])) *
+                                                   fabsf(vs[j][q]));
+          largest(top, maxima + kWarps * 8 * R);
+#pragma unroll
+          for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float was = whole_log2(gain[i][e]);
+              float to = fminf((float)kUp - whole_log2(top[i][e]), floorf(was + more[i][e]));
+              to = fminf(fmaxf(to, -(float)kFar), (float)kFar);
+              gain[i][e] = power(to);
+              a[i][e] *= power(to - was);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i)
 #pragma unroll
           for (int d = 0; d < kDT; ++d)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) acc[d][i][k] *= a[k & 1];
-        }
+            for (int k = 0; k < 4; ++k) acc[d][i][k] *= a[i][k & 1];
         weigh();
         if (kS > 1) {
           turn ^= 1;  // (the other has read the first ones' flag by the second barrier)
@@ -858,11 +922,9 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
         }
       }
 #pragma unroll
-      for (int j = 0; j < kMT; ++j)
+      for (int i = 0; i < R; ++i)
 #pragma unroll
-        for (int i = 0; i < R; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) l[i][e] += p[j][i][e] + p[j][i][2 + e];
+        for (int e = 0; e < 2; ++e) l[i][e] += sum[i][e];
       if (kS > 1) {
         const uint2 *const theirs = weights + ((warp ^ 1) * 2 + turn) * (Sh::kWeights / 8) + lane;
 #pragma unroll
@@ -985,8 +1047,33 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
         x += __shfl_xor_sync(kFull, x, 4);
         x += __shfl_xor_sync(kFull, x, 8);
         x += __shfl_xor_sync(kFull, x, 16);
-        if (g == 0) stat[warp * 8 * R + 8 * i + 2 * t + e] = make_float2(m[i][e], x);
+        if (g == 0) {
+          const int r = warp * 8 * R + 8 * i + 2 * t + e;
+          stat[r] = make_float2(m[i][e], x);
+          if (kHalf) units[r] = -whole_log2(gain[i][e]);
+        }
       }
+    if (kHalf) {
+      // the sums over v as they are, but where they might leave the floats
+      bool wide = false;
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        wide |= fmaxf(gain[i][0], gain[i][1]) > kLarge || fminf(gain[i][0], gain[i][1]) < kSmall;
+      wide = __any_sync(kFull, wide) != 0;
+      if (lane == 0) wides[warp] = wide;
+      if (!wide) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) gain[i][e] = power(-whole_log2(gain[i][e]));
+#pragma unroll
+        for (int d = 0; d < kDT; ++d)
+#pragma unroll
+          for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[d][i][k] *= gain[i][k & 1];
+      }
+    }
     const int mine = get == 0 ? kSlots - 1 : get - 1;
     if (lane == 0) rooms[warp] = any ? (signed char)mine : (signed char)-1;
     float *const own = reinterpret_cast<float *>(smem + Sh::kRingAt + (warp * kSlots + mine) * Z::kSlot);
@@ -1028,10 +1115,21 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
             ml[w] = stat[w * 8 * R + r];
             top = fmaxf(top, ml[w].x);
           }
+          float all_in = 0.0f;  // the sums over v are in units of 2^this
+          float by[kWarps];
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
-            ml[w].x = exp2_(ml[w].x - top);
-            sum += ml[w].y * ml[w].x;
+            by[w] = exp2_(ml[w].x - top);
+            sum += ml[w].y * by[w];
+          }
+          if (kHalf && *reinterpret_cast<const volatile long long *>(wides) != 0) {
+            all_in = -1e30f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+              all_in = fmaxf(all_in, floorf(ml[w].x - top) + (wides[w] ? units[w * 8 * R + r] : 0.0f));
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+              by[w] *= power((wides[w] ? units[w * 8 * R + r] : 0.0f) - all_in);
           }
           float o[4] = {};
 #pragma unroll
@@ -1041,7 +1139,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
             if (sl >= 0)
               v = reinterpret_cast<const float4 *>(
                   smem + Sh::kRingAt + ((w + cs) * kSlots + sl) * Z::kSlot)[unit(r8, cq)];
-            const float f = ml[w].x;  // (the same for a team)
+            const float f = by[w];  // (the same for a team)
             o[0] += v.x * f; o[1] += v.y * f; o[2] += v.z * f; o[3] += v.w * f;
           }
           const int ch = cs * kVHd + rd * kStage + 4 * cq;
@@ -1052,12 +1150,16 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
             const float inv = 1.0f / sum;
 #pragma unroll
             for (int k = 0; k < 4; ++k) o[k] *= inv;
+            if (kHalf && all_in != 0.0f) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[k] *= power(all_in);
+            }
             store4(static_cast<T *>(P.o) + at * kHd + ch, o);
             if (P.lse && ch == 0) P.lse[at] = (top + log2f(sum)) * 0.693147180559945f;
           } else {
             float *to = parts + (size_t)r * (kHd + 4);
             store4(to + ch, o);
-            if (ch == 0) *reinterpret_cast<float2 *>(to + kHd) = make_float2(top, sum);
+            if (ch == 0) *reinterpret_cast<float4 *>(to + kHd) = make_float4(top, sum, all_in, 0.0f);
           }
         }
         __syncthreads();
@@ -1067,9 +1169,10 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
 }
 
 // Channels 4 q on of row r of an item with parts in the CTAs i0 .. last: every
-// `step`-th part from CTA i on, added in order.
+// `step`-th part from CTA i on, added in order.  The sums over v are in units of
+// 2^unit, 0 but for scales far from 1.
 struct Sums {
-  float top = kNone, sum = 0.0f, o[4] = {};
+  float top = kNone, sum = 0.0f, unit = 0.0f, o[4] = {};
   __device__ __forceinline__ void rescale(float to) {
     const float f = exp2_(top - to);
     top = to;
@@ -1082,39 +1185,66 @@ struct Sums {
 #pragma unroll
     for (int d = 0; d < 4; ++d) o[d] += x[d] * e;
   }
+  // one more, where the units may differ
+  __device__ __forceinline__ void join(float t, float s, float un, const float (&x)[4]) {
+    const float to = fmaxf(top, t), f = exp2_(top - to), e = exp2_(t - to);
+    const float in = fmaxf(floorf(top - to) + unit, floorf(t - to) + un);
+    const float fo = f * power(unit - in), eo = e * power(un - in);
+    top = to;
+    unit = in;
+    sum = sum * f + s * e;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) o[d] = o[d] * fo + x[d] * eo;
+  }
 };
-template <int kHd, int R, int kU>
+template <int kHd, int R, int kU, bool kHalf>
 __device__ __forceinline__ Sums add_parts(const AttnArgs &P, int i0, int last, int r, int q, int i,
                                           int step) {
   constexpr size_t kPart = (size_t)(8 * R) * (kHd + 4);
   const float *part = P.part + kSplitBytes / 4 + (size_t)r * (kHd + 4);
   Sums s;
+  bool units = false;
 #pragma unroll 1
-  for (; i <= last; i += kU * step) {
+  for (int c = i; c <= last; c += kU * step) {
     float2 ml[kU];
     float x[kU][4], to = s.top;
 #pragma unroll
     for (int k = 0; k < kU; ++k) {  // (past the end: the first one, without weight)
-      const int c = i + k * step <= last ? i + k * step : i;
-      const float *from = part + ((size_t)c * 2 + (c == i0 ? 1 : 0)) * kPart;
+      const int cta = c + k * step <= last ? c + k * step : c;
+      const float *from = part + ((size_t)cta * 2 + (cta == i0 ? 1 : 0)) * kPart;
       ml[k] = *reinterpret_cast<const float2 *>(from + kHd);
+      if (kHalf) units |= from[kHd + 2] != 0.0f;
       load4(from + 4 * q, x[k]);
       to = fmaxf(to, ml[k].x);
     }
     s.rescale(to);
 #pragma unroll
     for (int k = 0; k < kU; ++k)
-      if (i + k * step <= last) s.add(ml[k].y, x[k], exp2_(ml[k].x - to));
+      if (c + k * step <= last) s.add(ml[k].y, x[k], exp2_(ml[k].x - to));
+  }
+  if (kHalf && units) {  // once more, one by one
+    s = Sums{};
+#pragma unroll 1
+    for (int c = i; c <= last; c += step) {
+      const float *from = part + ((size_t)c * 2 + (c == i0 ? 1 : 0)) * kPart;
+      float x[4];
+      load4(from + 4 * q, x);
+      s.join(from[kHd], from[kHd + 1], from[kHd + 2], x);
+    }
   }
   return s;
 }
 
-template <int kHd, bool kBf16>
-__device__ __forceinline__ void put_row(const AttnArgs &P, Sums &s, int b, int mt, int head, int q) {
+template <int kHd, bool kBf16, bool kHalf>
+__device__ __forceinline__ void put_row(const AttnArgs &P, Sums &s, int b, int mt, int head,
+                                        int q) {
   using T = typename std::conditional<kBf16, __nv_bfloat16, float>::type;
   const float inv = 1.0f / s.sum;
 #pragma unroll
-  for (int d = 0; d < 4; ++d) s.o[d] *= inv;
+  for (int d = 0; d < 4; ++d) {
+    s.o[d] *= inv;
+    if (kHalf && s.unit != 0.0f) s.o[d] *= power(s.unit);
+  }
   const size_t to = ((size_t)b * P.M + mt) * P.qh + head;
   store4(static_cast<T *>(P.o) + to * kHd + 4 * q, s.o);
   if (P.lse && q == 0) P.lse[to] = (s.top + log2f(s.sum)) * 0.693147180559945f;
@@ -1122,7 +1252,7 @@ __device__ __forceinline__ void put_row(const AttnArgs &P, Sums &s, int b, int m
 
 // Many items in several CTAs, of few parts each: kHd / 4 threads for a row of the
 // one that begins in CTA blockIdx.x, if one does, as that CTA left word of it.
-template <int kHd, bool kBf16, int R>
+template <int kHd, bool kHalf, bool kBf16, int R>
 __global__ void __launch_bounds__(kThreads)
     attn_join_kernel(const AttnArgs P) {
   constexpr int kQ = kHd / 4;
@@ -1135,14 +1265,14 @@ __global__ void __launch_bounds__(kThreads)
   const int r = blockIdx.y * (kThreads / kQ) + threadIdx.x / kQ, q = threadIdx.x % kQ;
   const int row = s.row0 + r, mt = row / P.group;
   if (r >= 8 * R || mt >= P.M || s.start + mt >= s.len) return;  // (no token of the sequence)
-  Sums x = add_parts<kHd, R, 4>(P, blockIdx.x, s.last, r, q, blockIdx.x, 1);
-  put_row<kHd, kBf16>(P, x, s.b, mt, s.h * P.group + row - mt * P.group, q);
+  Sums x = add_parts<kHd, R, 4, kHalf>(P, blockIdx.x, s.last, r, q, blockIdx.x, 1);
+  put_row<kHd, kBf16, kHalf>(P, x, s.b, mt, s.h * P.group + row - mt * P.group, q);
 }
 
 // Few items of many parts (at most 32 sequences): a block for each row, which finds
 // the item's CTAs from the lengths while attn_kernel runs.
 template <int kHd, int kKind, bool kBf16, int R>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(512, 2)  // (beside a CTA of attn_kernel)
     attn_join_few_kernel(const AttnArgs P, int grid) {
   using Z = Sizes<kHd, kKind, R>;
   // (what came before attn_kernel has ended, and attn_kernel writes no lengths)
@@ -1170,20 +1300,28 @@ __global__ void __launch_bounds__(512)
   if (i0 == last) return;
   // streams of parts, joined in their order
   constexpr int kQ = kHd / 4, kGroups = 512 / kQ;
+  constexpr bool kHalf = kKind != kKvBf16;
   __shared__ Sums sums[kGroups][kQ];
   const int q = threadIdx.x % kQ, group = threadIdx.x / kQ;
-  sums[group][q] = add_parts<kHd, R, 8>(P, i0, last, row % (8 * R), q, i0 + group, kGroups);
-  __syncthreads();
+  const Sums mine = add_parts<kHd, R, 8, kHalf>(P, i0, last, row % (8 * R), q, i0 + group, kGroups);
+  sums[group][q] = mine;
+  const bool units = __syncthreads_or(kHalf && mine.unit != 0.0f) != 0;
   if (group) return;
   Sums all = sums[0][q];
+  if (kHalf && units) {
+#pragma unroll 1
+    for (int i = 1; i < kGroups; ++i)
+      all.join(sums[i][q].top, sums[i][q].sum, sums[i][q].unit, sums[i][q].o);
+  } else {
 #pragma unroll
-  for (int i = 1; i < kGroups; ++i) {
-    const Sums &x = sums[i][q];
-    const float to = fmaxf(all.top, x.top);
-    all.rescale(to);
-    all.add(x.sum, x.o, exp2_(x.top - to));
+    for (int i = 1; i < kGroups; ++i) {
+      const Sums &x = sums[i][q];
+      const float to = fmaxf(all.top, x.top);
+      all.rescale(to);
+      all.add(x.sum, x.o, exp2_(x.top - to));
+    }
   }
-  put_row<kHd, kBf16>(P, all, b, mt, h * P.group + row - mt * P.group, q);
+  put_row<kHd, kBf16, kHalf>(P, all, b, mt, h * P.group + row - mt * P.group, q);
 }
 
 // CTAs of a call: at most one share each for the longest that the table holds.
@@ -1233,7 +1371,7 @@ cudaError_t go(const AttnArgs &P, cudaStream_t stream) {
   const int rows = P.M * P.group < 8 * R ? P.M * P.group : 8 * R;
   constexpr int kRowsBlock = kThreads / (kHd / 4);
   cfg.gridDim = dim3((unsigned)grid, (unsigned)((rows + kRowsBlock - 1) / kRowsBlock));
-  return cudaLaunchKernelEx(&cfg, attn_join_kernel<kHd, kBf16, R>, P);
+  return cudaLaunchKernelEx(&cfg, attn_join_kernel<kHd, kKind != kKvBf16, kBf16, R>, P);
 }
 
 // Row tiles of 8, 16 or (8 bits, teams) 24: the fewest eights of rows, and of two

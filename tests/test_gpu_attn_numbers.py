@@ -3,7 +3,7 @@
 import pytest
 import torch
 
-from attn_ref import attn, attn_bounds, make_cache, make_table
+from attn_ref import TYPES, attn, attn_bounds, make_cache, make_table
 from test_gpu_attn import call, gen_of, ints
 
 pytestmark = pytest.mark.gpu
@@ -38,3 +38,76 @@ def test_bf16_results_are_rounded_once(kind, hd, group, M, T):
     far = (o.double() - ro.bfloat16().double()).square().sum()
     lim = (2 * 2.0 ** -21 * mag * bf16_steps(ro)).sum()
     assert far <= lim, f"{(far / ro.square().sum()).sqrt().item():.2e} from the rounded result"
+
+
+def sequences(kind, hd, page, scores, vs, gen):
+    """A cache of one key head whose key rows give a query (1, 0, 0, ..) the scores
+    [n][T], and whose value rows have the scales vs [n][T]; its table."""
+    n, T = scores.shape
+    cols = -(-T // page)
+    c = make_cache(kind, n * cols, 1, page, hd, gen, "cuda", spread=0.0)
+    table = make_table(n * cols, n, cols, gen, "cuda")
+    at = (table.long().repeat_interleave(page, 1)[:, :T], 0, torch.arange(T, device="cuda").expand(n, T) % page)
+    if kind == "bf16":
+        k = torch.zeros(n, T, hd, device="cuda")
+        k[..., 0] = scores
+        c["k"][at] = k.bfloat16()
+        c["v"][at] = (c["v"][at].float() * vs[..., None]).bfloat16()
+    else:
+        k = torch.zeros(n, T, hd, device="cuda")
+        k[..., 0] = 1.0
+        c["k"][at] = k.to(c["k"].dtype)
+        c["ks"][at], c["vs"][at] = scores.float(), vs.float()
+    return c, table
+
+
+def check_many(c, table, kind, dtype, q, T, page, copies=48):
+    """Every sequence `copies` times, so that one warp has many of its tiles,
+    against 64 bits; q [n][M][qh][hd]."""
+    n, M, _, hd = q.shape
+    start = [T - M] * n
+    o, lse = call(c, q.repeat(copies, 1, 1, 1), table.repeat(copies, 1), ints(start * copies), 1.0)
+    ro, rl, mag, big = attn(c, table, start, None, q, 1.0, page)
+    bo, bl = attn_bounds(kind, dtype, hd, T, ro, rl, mag, big)
+    for x, r, b, name in ((lse, rl, bl, "lse"), (o, ro, bo, "o")):
+        x = x.double().view(copies, *r.shape)
+        assert bool(torch.isfinite(x).all()), name
+        assert ((x - r).abs() <= b).all(), f"{name} at {((x - r).abs() / b.clamp(min=1e-300)).max().item():.3g} of its bound"
+    return o, lse
+
+
+LN2 = 0.6931471805599453
+BEHIND = {"zeros, zeros 24 above, others": ((0, 0), (24, 0), (0, 1)),
+          "zeros, others 40 above": ((0, 0), (40, 1), (3, 1)),
+          "others, zeros 60 above": ((0, 1), (60, 0), (1, 1)),
+          "others, zeros 110.5 above": ((0, 1), (110.5, 0), (0, 0)),
+          "others, zeros 124 above": ((0, 1), (124, 0), (0, 0)),
+          "others, zeros 130 above, others": ((0, 1), (130, 0), (130, 1)),
+          "zeros, values of 2^40": ((0, 0), (0, 2.0 ** 40), (0, 0)),
+          "values of 2^-60, 2^60, 2^-60": ((0, 2.0 ** -60), (0, 2.0 ** 60), (5, 2.0 ** -60)),
+          "values of 2^-90": ((0, 2.0 ** -90), (10, 2.0 ** -90), (3, 2.0 ** -90)),
+          "values of 2^100, zeros above": ((0, 2.0 ** 100), (90, 0), (0, 2.0 ** 90)),
+          "zeros alone": ((0, 0), (30, 0), (90, 0))}
+
+
+@pytest.mark.parametrize("name", BEHIND)
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("hd,group,M,dtype", [(128, 4, 1, "bf16"), (64, 4, 1, "fp32"), (256, 6, 4, "fp32"), (128, 5, 2, "fp32")])
+def test_scales_move_no_weights(name, kind, hd, group, M, dtype):
+    """Rows of zeros have scale 0 and their weight all the same, whatever the
+    scales of other rows and however far apart (scores in base 2, scales; each
+    for a third of the positions, and mixed)."""
+    gen = gen_of(hd)
+    T, page, n = 960, 32, 4
+    part = torch.arange(T, device="cuda").expand(n, T) * 3 // T
+    part = torch.where(torch.arange(n, device="cuda")[:, None] < 2, part,
+                       torch.randint(0, 3, (n, T), generator=gen, device="cuda"))
+    sc, vs = (torch.tensor([float(p[i]) for p in BEHIND[name]], dtype=torch.float64, device="cuda")[part] for i in (0, 1))
+    sc = (sc + torch.rand(n, T, generator=gen, device="cuda")) * LN2
+    c, table = sequences(kind, hd, page, sc, vs, gen)
+    q = torch.zeros(n, M, group, hd, device="cuda")
+    q[..., 0] = 1.0
+    q[:, :, 1::2, 0] = 0.75
+    o, _ = check_many(c, table, kind, dtype, q.to(TYPES[dtype]), T, page)
+    if name == "zeros alone":
+        assert bool((o == 0).all())
