@@ -73,7 +73,7 @@ namespace attn {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr float kNone = -1e30f;  // the reference of rows that have seen nothing
+constexpr float kNone = -3e30f;  // the reference of rows that have seen nothing: below any score
 constexpr int kUp = 12;           // weights times scales (8 bits) are brought to 2^12,
 constexpr float kTop = 65000.0f;  // and weights and these may grow to this before they are again,
 constexpr int kFar = 126;         // by factors from 2^-126 to 2^126.  Sums over v are taken
@@ -761,6 +761,14 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
       for (int i = 0; i < R; ++i)
 #pragma unroll
         for (int e = 0; e < 2; ++e) f[i][e] = factor[8 * i + 2 * t + e];
+      // In base 2, rounded once: the largest less the reference made of it is 0 at
+      // any size.
+#pragma unroll
+      for (int j = 0; j < kMT; ++j)
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[j][i][k] = __fmul_rn(s[j][i][k], f[i][k & 1] * ks[j][k >> 1]);
       if (masked) {
         // Out of a row's sight: no weight, whatever key and scales may be.  A
         // value's scale that is not finite makes the rows that see it NaN by
@@ -774,20 +782,16 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
             for (int j = 0; j < kMT; ++j)
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
-                float &x = s[j][i][2 * q + e];
                 const bool seen = 16 * j + 8 * q < lim;
-                x = seen ? x * (f[i][e] * ks[j][q]) : -INFINITY;
+                if (!seen) s[j][i][2 * q + e] = -INFINITY;
                 if (kHalf && seen && !(fabsf(vs[j][q]) <= 3.4e38f)) l[i][e] = __uint_as_float(0x7fc00000u);
               }
-            f[i][e] = 1.0f;
           }
 #pragma unroll
         for (int j = 0; j < kMT; ++j)
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            ks[j][q] = 1.0f;
+          for (int q = 0; q < 2; ++q)
             if (kHalf && !(fabsf(vs[j][q]) <= 3.4e38f)) vs[j][q] = 0.0f;
-          }
       }
       // Weights with the reference and the factor as they are; where one is too
       // large for that, and for the first tile, these are set anew.
@@ -807,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
               float y[2];
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const float x = exp2_(fmaf(s[j][i][2 * q + e], f[i][e] * ks[j][q], -m[i][e]));
+                const float x = exp2_(s[j][i][2 * q + e] - m[i][e]);
                 sum[i][e] += x;
                 y[e] = kHalf ? x * vs[j][q] * gain[i][e] : x;
               }
@@ -868,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
             for (int j = 0; j < kMT; ++j)
 #pragma unroll
               for (int q = 0; q < 2; ++q)
-                top[i][e] = fmaxf(top[i][e], s[j][i][2 * q + e] * (f[i][e] * ks[j][q]));
+                top[i][e] = fmaxf(top[i][e], s[j][i][2 * q + e]);
           }
         largest(top, maxima);
 #pragma unroll
@@ -895,8 +899,7 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
               for (int j = 0; j < kMT; ++j)
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
-                  top[i][e] = fmaxf(top[i][e], exp2_(fmaf(s[j][i][2 * q + e], f[i][e] * ks[j][q], -m[i][e])) *
-                                                   fabsf(vs[j][q]));
+                  top[i][e] = fmaxf(top[i][e], exp2_(s[j][i][2 * q + e] - m[i][e]) * fabsf(vs[j][q]));
           largest(top, maxima + kWarps * 8 * R);
 #pragma unroll
           for (int i = 0; i < R; ++i)

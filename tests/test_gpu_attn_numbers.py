@@ -1,9 +1,11 @@
 """What gdn_attn_step_m keeps of its numbers."""
 
+import math
+
 import pytest
 import torch
 
-from attn_ref import TYPES, attn, attn_bounds, make_cache, make_table
+from attn_ref import TYPES, attn, attn_bounds, held, make_cache, make_table
 from test_gpu_attn import call, gen_of, ints
 
 pytestmark = pytest.mark.gpu
@@ -111,3 +113,36 @@ def test_scales_move_no_weights(name, kind, hd, group, M, dtype):
     o, _ = check_many(c, table, kind, dtype, q.to(TYPES[dtype]), T, page)
     if name == "zeros alone":
         assert bool((o == 0).all())
+
+
+@pytest.mark.parametrize("size", [2.0 ** 20, 2.0 ** 27, 2.0 ** 28.5, 2.0 ** 31, 2.0 ** 40, 2.0 ** 70, 2.0 ** 98, 1.2e30])
+@pytest.mark.parametrize("kind,hd,group,M,dtype", [("int8", 128, 4, 1, "bf16"), ("e4m3", 64, 2, 1, "fp32"),
+                                                   ("bf16", 128, 4, 1, "bf16"), ("bf16", 64, 1, 1, "fp32"),
+                                                   ("int8", 256, 6, 4, "fp32"), ("bf16", 128, 7, 3, "fp32")])
+def test_scores_of_any_size(size, kind, hd, group, M, dtype):
+    """Scores up to 2^100 in base 2, of either sign or all far below zero: the
+    largest takes all (the next is 2^-12 of it below, thousands in base 2 from
+    2^27 on; at 2^20 some 300), equal ones share it.  o is within the cut of
+    weights and sums of it, lse within six roundings, 2^-24 each, of the score."""
+    gen = gen_of(int(math.log2(size)) + hd)
+    T, page, n = 960, 32, 5
+    step = torch.stack([torch.randperm(T, generator=gen, device="cuda") for _ in range(n)])
+    sc = size * (1 - 2.0 * step / T)                         # from size down to -size
+    sc[1] = size * (-0.8 - 0.15 * step[1] / T)               # all below zero
+    sc[2] = -size * 0.9                                      # all the same
+    sc[3] = torch.where(step[3] < 40, size, sc[3] / 2)       # 40 of them the same
+    c, table = sequences(kind, hd, page, sc * LN2, torch.ones_like(sc), gen)
+    q = torch.zeros(n, M, group, hd, device="cuda", dtype=TYPES[dtype])
+    q[..., 0] = 1.0
+    copies, start = 48, [T - M] * n
+    o, lse = call(c, q.repeat(copies, 1, 1, 1), table.repeat(copies, 1), ints(start * copies), 1.0)
+    for i in range(n):
+        k, v = (held(c, x, table, i, T, page)[0] for x in "kv")
+        for m in range(M):
+            s = k[:T - M + m + 1, 0]
+            top = s.max()
+            best = s == top
+            want, wl = v[:T - M + m + 1][best].mean(0), top + best.sum().double().log()
+            tol = 2.0 ** -18 * v.abs().max() + (2.0 ** -8 * want.abs() if dtype == "bf16" else 0)
+            assert ((o.view(copies, n, M, group, hd)[:, i, m].double() - want).abs() <= tol).all()
+            assert ((lse.view(copies, n, M, group)[:, i, m].double() - wl).abs() <= 2.0 ** -21 * wl.abs()).all()
