@@ -588,7 +588,9 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
 #pragma unroll
       for (int e = 0; e < kQuads; ++e) {
         xq[i][e][0] = xq[i][e][1] = xq[i][e][2] = xq[i][e][3] = 0.0f;
-        if (mt < P.M && lane + 32 * e < kHd / 4) load4(src + 4 * (lane + 32 * e), xq[i][e]);
+        // (tokens that the sequence has: the others' rows may hold anything, and one
+        // row's weights can have the references of all set anew)
+        if (mt < w.len - w.start && lane + 32 * e < kHd / 4) load4(src + 4 * (lane + 32 * e), xq[i][e]);
       }
     }
   };

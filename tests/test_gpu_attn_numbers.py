@@ -146,3 +146,30 @@ def test_scores_of_any_size(size, kind, hd, group, M, dtype):
             tol = 2.0 ** -18 * v.abs().max() + (2.0 ** -8 * want.abs() if dtype == "bf16" else 0)
             assert ((o.view(copies, n, M, group, hd)[:, i, m].double() - want).abs() <= tol).all()
             assert ((lse.view(copies, n, M, group)[:, i, m].double() - wl).abs() <= 2.0 ** -21 * wl.abs()).all()
+
+
+@pytest.mark.parametrize("kind,hd,group,M,dtype", [("int8", 128, 4, 2, "bf16"), ("e4m3", 64, 2, 4, "fp32"),
+                                                   ("bf16", 128, 2, 3, "bf16"), ("bf16", 64, 3, 5, "fp32"),
+                                                   ("int8", 256, 6, 4, "fp32"), ("bf16", 128, 8, 3, "fp32"),
+                                                   ("e4m3", 256, 8, 2, "bf16")])
+@pytest.mark.parametrize("copies", [1, 60])
+def test_rows_of_padding_touch_no_other(kind, hd, group, M, dtype, copies):
+    """The bits of a sequence's tokens, whatever the rows of tokens hold that it
+    has not."""
+    gen = gen_of(hd + M)
+    page, T, n = 32, 1500, 3
+    cols = -(-T // page)
+    c = make_cache(kind, n * cols, 1, page, hd, gen, "cuda")
+    table = make_table(n * cols, n, cols, gen, "cuda").repeat(copies, 1)
+    q = 3 * torch.randn(n, M, group, hd, generator=gen, device="cuda")
+    counts = [1, M - 1, M]
+    start = ints([T - m for m in counts] * copies)
+    have = torch.arange(M, device="cuda") < torch.tensor(counts, device="cuda")[:, None]
+
+    def run(x):
+        return call(c, x.to(TYPES[dtype]).repeat(copies, 1, 1, 1), table, start, 0.2, counts=ints(counts * copies))
+
+    o, lse = run(torch.where(have[..., None, None], q, torch.zeros_like(q)))
+    for junk in (1e30, float("nan"), -float("inf"), 5.0):
+        o2, lse2 = run(torch.where(have[..., None, None], q, torch.full_like(q, junk)))
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
