@@ -1005,16 +1005,19 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
               mma<kHalf>(to[q][i], a[0], a[1], a[2], a[3], w[j][i][p]);
         }
       };
-      if (kBf16 || R == 3) {
+      // A product's sum is cut off, not rounded: over long sequences that adds up,
+      // so fp32 tokens make a tile's sums from 0 and add them to the others rounded
+      // (24 rows of 60000 positions, 234 tiles a warp: 7e-6 to 10e-6 of o without,
+      // 0.9e-6 to 1.5e-6 with, the plain fp32 form 3e-6 to 5e-6; 4 tokens x 6 heads e4m3
+      // 92 and 101 us, 128 channels int8 61 and 69).  bf16 tokens do not: 1e-5 of o
+      // is a 200th of its rounding (o 23e-5 from the rounded 64-bit result, the plain
+      // form 19e-5, tile by tile 5e-5; 128 channels int8 59 us, tile by tile 65).
+      if (kBf16) {
 #pragma unroll
         for (int j = 0; j < kVT; ++j)
 #pragma unroll
           for (int d = 0; d < kDT; d += kStep) products(j, d, acc + d);
       } else {
-        // A product's sum is cut off, not rounded: over long sequences that adds up,
-        // so a tile's sums are made from 0 and added to the others rounded.  (24
-        // rows have no registers for it: over 60000 positions of int8 1.4e-6 of o
-        // in place of 0.9e-6, but 54 us in place of 60 for 4 tokens.)
 #pragma unroll
         for (int d = 0; d < kDT; d += kStep) {
           float tile[kStep][R][4] = {};

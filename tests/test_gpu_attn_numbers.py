@@ -173,3 +173,29 @@ def test_rows_of_padding_touch_no_other(kind, hd, group, M, dtype, copies):
     for junk in (1e30, float("nan"), -float("inf"), 5.0):
         o2, lse2 = run(torch.where(have[..., None, None], q, torch.full_like(q, junk)))
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("kind,hd,group,M", [("int8", 128, 8, 3), ("e4m3", 128, 8, 3), ("bf16", 128, 8, 3),
+                                             ("int8", 256, 8, 3), ("e4m3", 256, 6, 4), ("bf16", 256, 8, 2),
+                                             ("int8", 64, 8, 2), ("int8", 128, 8, 2), ("int8", 128, 8, 1)])
+def test_sums_do_not_drift(kind, hd, group, M):
+    """Equal weights over values of one sign, in a batch that gives every warp
+    a sequence's tiles of its own: o is their mean.  A tile's sum is cut off at
+    most four times (2^-23 each) and its weights are held to 2^-22; n tiles are
+    added to o and their weights to l, rounded, 2^-25 each, in either
+    direction: 2 n^0.5 2^-25.  Sums that are cut off n times instead lose some
+    n 2^-24."""
+    gen = gen_of(hd + M)
+    page, T, kvh, B = 64, 60000, 4, 40
+    cols = -(-T // page)
+    c = make_cache(kind, cols, kvh, page, hd, gen, "cuda", spread=0.0)
+    c["v"] = (c["v"].float().abs() + 0.5).to(c["v"].dtype)
+    table = make_table(cols, 1, cols, gen, "cuda").expand(B, cols).contiguous()
+    q = torch.zeros(B, M, kvh * group, hd, device="cuda")
+    o, _ = call(c, q, table, ints([T - M] * B), 1.0)
+    v = held(c, "v", table, 0, T, page)
+    n = T / 128
+    for m in range(M):
+        want = v[:, :T - M + m + 1].mean(1).repeat_interleave(group, 0)
+        far = (o[:, m].double() - want).norm(dim=(1, 2)) / want.norm()
+        assert far.max() <= 2.0 ** -21 + 2.0 ** -22 + 2 * n ** 0.5 * 2.0 ** -25
