@@ -13,7 +13,7 @@
 // in 64-bit fixed point: pos times it is exact modulo one turn, an integer
 // product drops the whole turns, and the rest goes to sincospif as a number in
 // [-1, 1], with what its rounding to a float left of it added to first order.
-// Error of an angle: 2^-53 pos of the frequency's own rounding.
+// Error of an angle: 2^-64 pos turns, of the frequency as it is given.
 // hd / 8 lanes take a token and a run of its heads, and keep its cosines and sines
 // in registers.
 //
@@ -296,8 +296,14 @@ __global__ void __launch_bounds__(kThreads, 4)
   float c[8], w[8];  // (pairs side by side: the first four)
   if (half) {
     for (int i = tid; i < half; i += kThreads) {
-      const double turns = P.freq[i] * 0.15915494309189533576888;  // 1 / 2 pi
-      phase[i] = __double2ull_rd((turns - floor(turns)) * 18446744073709551616.0);
+      // of |freq|, negated after it: turning back is the mirror image to the bit
+      constexpr double kTurn = 0.15915494309189533577, kRest = -9.839338337591243e-18;  // 1 / 2 pi
+      const double f = P.freq[i], a = fabs(f), turns = a * kTurn;
+      // (and what the product and the constant's rounding left of it)
+      const double rest = fma(a, kTurn, -turns) + a * kRest;
+      const unsigned long long p = __double2ull_rd((turns - floor(turns)) * 0x1p64) +
+                                   (unsigned long long)__double2ll_rn(rest * 0x1p64);
+      phase[i] = f < 0.0 ? 0ull - p : p;
     }
     __syncthreads();
   }
