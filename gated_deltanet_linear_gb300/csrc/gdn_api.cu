@@ -809,18 +809,21 @@ int gdn_rope_freqs(int rot, double base, int scaling, double factor,
                                    !isfinite(high) || !(low < high)))
     return GDN_EINVAL;
   *amp = 1.0f;
+  bool fine = true;
   for (int i = 0; i < rot / 2; ++i) {
     double f = pow(base, -2.0 * i / rot);
     if (scaling == GDN_ROPE_LINEAR) f /= factor;
     if (scaling == GDN_ROPE_BAND) {
-      double w = (context / 6.283185307179586477 * f - low) / (high - low);
+      // (halves, which no difference leaves the floats by)
+      double w = (context / 6.283185307179586477 * f * 0.5 - low * 0.5) / (high * 0.5 - low * 0.5);
       w = w < 0.0 ? 0.0 : w > 1.0 ? 1.0 : w;
       f *= w + (1.0 - w) / factor;
     }
     freq[i] = f;
+    fine = fine && isfinite(f);
   }
   if (scaling == GDN_ROPE_BAND) *amp = (float)(0.1 * log(factor) + 1.0);
-  return GDN_OK;
+  return fine ? GDN_OK : GDN_EINVAL;
 }
 
 int gdn_rope_m(int rows, int heads, int hd, int dtype, const gdn_rope *rope,

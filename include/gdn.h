@@ -601,7 +601,8 @@ typedef struct gdn_rope {
  * gdn_rope_freqs - frequencies and amplitude on the HOST, in 64 bits (no
  * device work): freq [rot / 2] and *amp, to be copied to the device and kept.
  * rot even, 2 .. 4096 (GDN_ESHAPE; NTK wants rot > 2); base > 0 and factor > 0
- * finite, context > 0 and low < high finite for GDN_ROPE_BAND (GDN_EINVAL).
+ * finite, context > 0 and low < high finite for GDN_ROPE_BAND, and a result that is
+ * finite (GDN_EINVAL).
  */
 int gdn_rope_freqs(int rot, double base, int scaling, double factor,
                    double context, double low, double high, double *freq,
