@@ -35,6 +35,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
+#include <math.h>
 
 #include "gdn_internal.cuh"
 #include "gdn_vec.cuh"
@@ -259,6 +260,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     kv_rows_kernel(const KvRows P) {
   constexpr int kHd = 8 * kLanes, kTokens = 32 / kLanes;
   __shared__ unsigned long long phase[kMaxHalf];
+  __shared__ float amps[kMaxHalf];  // NaN for a frequency that is not finite
   __shared__ float2 angles[4 * kThreads];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -304,6 +306,7 @@ __global__ void __launch_bounds__(kThreads, 4)
       const unsigned long long p = __double2ull_rd((turns - floor(turns)) * 0x1p64) +
                                    (unsigned long long)__double2ll_rn(rest * 0x1p64);
       phase[i] = f < 0.0 ? 0ull - p : p;
+      amps[i] = a < INFINITY ? P.amp : __uint_as_float(0x7fc00000u);
     }
     __syncthreads();
   }
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 4)
       const float rest = __ll2float_rn(a - __float2ll_rn(near)) * 3.4061215800865545e-19f;  // pi 2^-63
       float x, y;
       sincospif(near * 1.0842021724855044e-19f, &y, &x);  // 2^-63
-      cs[i] = make_float2(P.amp * (x - y * rest), P.amp * (y + x * rest));
+      cs[i] = make_float2(amps[i] * (x - y * rest), amps[i] * (y + x * rest));
     }
     __syncwarp();
     const int f0 = !turned ? 0 : pairs ? 4 * gl : 8 * gl - (upper ? half : 0);

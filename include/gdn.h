@@ -591,7 +591,8 @@ enum {
  *     amp (x cos(p f_i) - y sin(p f_i)),  amp (y cos(p f_i) + x sin(p f_i)).
  * Negated frequencies turn back (and, amp aside, give the gradient of x). */
 typedef struct gdn_rope {
-    const double *freq; /* [rot / 2] radians a position, DEVICE memory          */
+    const double *freq; /* [rot / 2] radians a position, DEVICE memory; one that
+                           is not finite makes NaN of its pair                  */
     int rot;            /* a multiple of 16, 16 .. hd                           */
     int layout;         /* GDN_ROPE_HALF or GDN_ROPE_PAIRS                      */
     float amp;          /* finite                                               */

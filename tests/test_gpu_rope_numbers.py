@@ -59,3 +59,19 @@ def test_turning_back_is_the_mirror_image(pairs, dtype):
     gdn.gdn_rope_m(x, ints(FAR), gdn.Rope(-f, layout, 1.25), back)
     on[..., at] = -on[..., at]
     assert torch.equal(on, back)
+
+
+@pytest.mark.parametrize("pairs", [False, True])
+def test_frequencies_that_are_not_finite(pairs):
+    """NaN in their pairs at every position, 0 among them, and nowhere else."""
+    f = torch.tensor([0.5, float("nan"), 0.25, float("inf"), 1e-3, -float("inf"), 0.0, 2.0], dtype=torch.float64, device="cuda")
+    x = torch.ones(4, 2, 64, device="cuda")
+    y, z = torch.empty_like(x), torch.empty_like(x)
+    layout = gdn.GDN_ROPE_PAIRS if pairs else gdn.GDN_ROPE_HALF
+    gdn.gdn_rope_m(x, ints([0, 5, -3, 2 ** 30]), gdn.Rope(f, layout), y)
+    gdn.gdn_rope_m(x, ints([0, 5, -3, 2 ** 30]), gdn.Rope(f.nan_to_num(0.0, 0.0, 0.0), layout), z)
+    bad = torch.zeros(64, dtype=torch.bool, device="cuda")
+    for i in (1, 3, 5):
+        for at in ((2 * i, 2 * i + 1) if pairs else (i, i + 8)):
+            bad[at] = True
+    assert bool(y[..., bad].isnan().all()) and torch.equal(y[..., ~bad], z[..., ~bad])
