@@ -516,9 +516,11 @@ cudaError_t rows_go(KvRows P, cudaStream_t stream, bool read) {
   P.run = (int)(run < heads ? run : heads);
   const long long runs = (heads + P.run - 1) / P.run;
   constexpr int kTokens = 32 / kLanes;
-  // Four tokens a job pay where there are many (37 x 48751 positions of 64, bf16:
-  // 149 us with one, 77 with four; 3 x 16962 of 128, int8: 9.9 and 11.9 us).
-  const bool one = read && heads == 1 && rows > 16 * full;
+  // Four tokens a job pay from 24000 rows on, whatever they hold: with one and
+  // with four, 20000 rows 5.3 and 4.9 us (128 channels, int8 to bf16), 3.5 and 3.8
+  // (64, bf16), 12.2 and 13.2 (256, e4m3 to fp32); 30000 rows 7.0 and 6.5, 4.1 and 4.0,
+  // 17.5 and 17.0; 1.8 million rows 402 and 261, 219 and 136, 905 and 746.
+  const bool one = read && heads == 1 && rows > 24000;
   const long long jobs = one ? (P.tokens + 3) / 4 : P.tokens * runs;
   const long long blocks = read ? (jobs + kGroups - 1) / kGroups
                                 : (P.tokens + 8 * kTokens - 1) / (8 * kTokens) * runs;
