@@ -255,7 +255,9 @@ __device__ __forceinline__ void widen_v(uint32_t w, uint32_t &even, uint32_t &od
 }
 
 // Two numbers as pairs of 16-bit parts: p[0] the nearest, p[i] of what is left.
-template <bool kHalf, int kN>
+// kMost: of any size; the nearest bf16 to the largest floats would be infinite (what is
+// not finite stays so by its second part).
+template <bool kHalf, int kN, bool kMost = false>
 __device__ __forceinline__ void cut(float x, float y, uint32_t (&p)[kN]) {
 #pragma unroll
   for (int i = 0; i < kN; ++i) {
@@ -267,7 +269,11 @@ __device__ __forceinline__ void cut(float x, float y, uint32_t (&p)[kN]) {
         y -= __high2float(h);
       }
     } else {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+      constexpr float kTop16 = 0x1.fep127f;
+      const bool most = kMost && kN > 1 && i == 0;
+      const __nv_bfloat162 h =
+          __floats2bfloat162_rn(most ? fminf(fmaxf(x, -kTop16), kTop16) : x,
+                                most ? fminf(fmaxf(y, -kTop16), kTop16) : y);
       p[i] = *reinterpret_cast<const uint32_t *>(&h);
       if (i + 1 < kN) {
         x -= __uint_as_float(p[i] << 16);
@@ -654,8 +660,8 @@ __global__ void __launch_bounds__(kThreads, Sizes<kHd, kKind, R>::kCtas)
           uint32_t a[kQP], c[kQP];
           // (int8 codes come out as bytes 0 and 2, 1 and 3)
           constexpr int k1 = kKind == kKvInt8 ? 2 : 1, k2 = 3 - k1;
-          cut<kHalf, kQP>(x[e][0], x[e][k1], a);
-          cut<kHalf, kQP>(x[e][k2], x[e][3], c);
+          cut<kHalf, kQP, true>(x[e][0], x[e][k1], a);
+          cut<kHalf, kQP, true>(x[e][k2], x[e][3], c);
 #pragma unroll
           for (int p = 0; p < kQP; ++p)
             reinterpret_cast<uint2 *>(qs)[((ks * kQP + p) * R + i) * 32 + 4 * (r & 7) + tq] =

@@ -199,3 +199,20 @@ def test_sums_do_not_drift(kind, hd, group, M):
         want = v[:, :T - M + m + 1].mean(1).repeat_interleave(group, 0)
         far = (o[:, m].double() - want).norm(dim=(1, 2)) / want.norm()
         assert far.max() <= 2.0 ** -21 + 2.0 ** -22 + 2 * n ** 0.5 * 2.0 ** -25
+
+
+@pytest.mark.parametrize("kind,hd,group,M", [("bf16", 128, 4, 1), ("bf16", 64, 3, 3), ("bf16", 256, 2, 1), ("int8", 128, 4, 1)])
+def test_queries_of_the_largest_floats(kind, hd, group, M):
+    """fp32 queries up to 3.4028e38 over keys as small as that makes the scores
+    ordinary; infinite ones make NaN of their row."""
+    gen = gen_of(hd)
+    T, page, n = 700, 16, 3
+    sc = 20 * torch.rand(n, T, generator=gen, device="cuda", dtype=torch.float64) / 3.4e38
+    c, table = sequences(kind, hd, page, sc, torch.ones_like(sc), gen)
+    q = torch.zeros(n, M, group, hd, device="cuda")
+    q[..., 0] = 3.4028234e38
+    q[:, :, 1, 0] = -3.395e38
+    check_many(c, table, kind, "fp32", q, T, page, copies=20)
+    q[:, :, 0, 0] = float("inf")
+    o, _ = call(c, q, table, ints([T - M] * n), 1.0)
+    assert bool(o[:, :, 0].isnan().all()) and bool(torch.isfinite(o[:, :, 1:]).all())
