@@ -5,8 +5,8 @@ import math
 import pytest
 import torch
 
-from attn_ref import TYPES, attn, attn_bounds, held, make_cache, make_table
-from test_gpu_attn import call, gen_of, ints
+from attn_ref import TYPES, attn, attn_bounds, held, junk_behind, make_cache, make_table
+from test_gpu_attn import call, check, gen_of, ints
 
 pytestmark = pytest.mark.gpu
 
@@ -216,3 +216,39 @@ def test_queries_of_the_largest_floats(kind, hd, group, M):
     q[:, :, 0, 0] = float("inf")
     o, _ = call(c, q, table, ints([T - M] * n), 1.0)
     assert bool(o[:, :, 0].isnan().all()) and bool(torch.isfinite(o[:, :, 1:]).all())
+
+
+@pytest.mark.parametrize("kind,hd,dtype,M,group", [("e4m3", 256, "fp32", 4, 6), ("int8", 256, "bf16", 3, 7), ("int8", 256, "fp32", 2, 8),
+                                                   ("bf16", 128, "bf16", 3, 7), ("int8", 128, "fp32", 4, 6), ("e4m3", 64, "fp32", 4, 4),
+                                                   ("bf16", 256, "fp32", 2, 8), ("bf16", 64, "bf16", 2, 7)])
+def test_drafts_over_long_sequences(kind, hd, dtype, M, group):
+    """9 to 24 rows a head over 60000 positions, joined from many CTAs, and
+    shorter ones beside them."""
+    gen = gen_of(hd + group)
+    page, T = 64, [60000, 33, 20011]
+    cols = -(-max(T) // page)
+    c = make_cache(kind, 3 * cols, 2, page, hd, gen, "cuda")
+    table = make_table(3 * cols, 3, cols, gen, "cuda")
+    junk_behind(c, table, T, page, kind)
+    q = (2 * torch.randn(3, M, 2 * group, hd, generator=gen, device="cuda")).to(TYPES[dtype])
+    check(c, kind, dtype, q, table, [t - M for t in T], None, hd ** -0.5, page)
+
+
+@pytest.mark.parametrize("name", BEHIND)
+@pytest.mark.parametrize("kind,hd,group,M,dtype", [("int8", 128, 4, 1, "bf16"), ("e4m3", 256, 6, 4, "fp32"), ("int8", 64, 5, 2, "fp32")])
+@pytest.mark.parametrize("copies", [1, 9])
+def test_scales_move_no_weights_in_joins(name, kind, hd, group, M, dtype, copies):
+    """The same over sequences that many CTAs share: parts with and without a
+    unit of their own, joined by items and by CTAs."""
+    gen = gen_of(hd + copies)
+    T, page, n = 9000, 64, 4
+    part = torch.arange(T, device="cuda").expand(n, T) * 3 // T
+    part = torch.where(torch.arange(n, device="cuda")[:, None] < 2, part,
+                       torch.randint(0, 3, (n, T), generator=gen, device="cuda"))
+    sc, vs = (torch.tensor([float(p[i]) for p in BEHIND[name]], dtype=torch.float64, device="cuda")[part] for i in (0, 1))
+    sc = (sc + torch.rand(n, T, generator=gen, device="cuda")) * LN2
+    c, table = sequences(kind, hd, page, sc, vs, gen)
+    q = torch.zeros(n, M, group, hd, device="cuda")
+    q[..., 0] = 1.0
+    q[:, :, 1::2, 0] = 0.75
+    check_many(c, table, kind, dtype, q.to(TYPES[dtype]), T, page, copies)
