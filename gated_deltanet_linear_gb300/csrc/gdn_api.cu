@@ -699,9 +699,9 @@ int cache_shape(const gdn_kv_cache *x, gdn::KvCache *c) {
 }
 
 // The buffers of a paged call: what it reads, what it writes, and 4-byte
-// integers of either sort (nullptr: not given).
+// integers that it reads (nullptr: not given).
 struct PagedBufs {
-  Buf in[8], out[8], ints_in[4], ints_out[1];
+  Buf in[8], out[8], ints_in[4];
   int n_in = 0, n_out = 0, n_ints = 0;
   void reads(const void *p, size_t bytes) { in[n_in++] = Buf{p, bytes}; }
   void writes(const void *p, size_t bytes) { out[n_out++] = Buf{p, bytes}; }

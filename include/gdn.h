@@ -632,9 +632,10 @@ int gdn_rope_m(int rows, int heads, int hd, int dtype, const gdn_rope *rope,
  *   rope  NULL: nothing is turned;  q, q_out  NULL, or qh heads likewise:
  *         q_out [B][M][qh][hd] = q turned (q_out may be q if q is contiguous)
  * start: required.  A row whose page number is not one of the cache's is not
- * written and sets *err_dev; its q is turned all the same.  New positions of
- * two sequences must lie in different rows of the cache: of two written to one
- * row either may stay.  M * B < 2^31, M <= GDN_MAX_TOKENS (GDN_ERANGE).
+ * written and sets *err_dev; its q is turned all the same.  New positions must
+ * lie in different rows of the cache, of two sequences and of one: a row that
+ * two of them are written to may hold channels of either and the scale of either.
+ * M * B < 2^31, M <= GDN_MAX_TOKENS (GDN_ERANGE).
  */
 int gdn_kv_write_m(const gdn_kv_cache *cache, int B, int M, int qh, int dtype,
                    const gdn_rope *rope, const void *q, long long q_stride,
@@ -673,10 +674,12 @@ size_t gdn_attn_workspace(const gdn_kv_cache *cache, int M, int qh);
  * A page number that the cache has not sets *err_dev, and the sequence's rows of
  * o and lse are NaN, also those of tokens in front of that page.
  * Numbers: every sum, maximum and weight is fp32.  8-bit codes enter the
- * products as they are; an fp32 q as two fp16 numbers scaled by its row
- * (22 bits), weights times scales as two fp16 numbers (22 bits, down to 2^-37 of
- * the largest).  bf16 caches take bf16 operands: q as it is or (fp32) as three
- * numbers, weights as three (24 bits).  A bf16 o is rounded once.
+ * products as they are; q as an fp16 number scaled by its row (bf16 tokens: exact
+ * from 2^-28 of the row's largest element on) or two (fp32: 22 bits, down to
+ * 2^-38 of the largest), with |scale| times the largest 0 or from 2^-110 to 2^120;
+ * weights times scales as two fp16 numbers (22 bits, down to 2^-37 of the
+ * largest).  bf16 caches take bf16 operands: q as it is or (fp32) as three numbers,
+ * weights as three (24 bits).  A bf16 o is rounded once.
  * Scores are met for |scale q . k| log2 e below 2^100.
  * What is not finite: in q, its own row of o; in a row of k or v, the rows of o
  * that see it (throughout, where it came with the call's own tokens) and no
