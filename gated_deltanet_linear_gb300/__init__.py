@@ -47,7 +47,7 @@ GDN_DECAY_TOKEN, GDN_DECAY_HEAD = 0, 1
 GDN_QUANT_MAX_DIM = 1 << 20
 GDN_KV_BF16, GDN_KV_INT8, GDN_KV_E4M3 = 0, 1, 2
 GDN_KV_MAX_HEADS, GDN_KV_MAX_POSITIONS = 4096, 1 << 30
-GDN_ATTN_MAX_TOKENS = 64
+GDN_ATTN_MAX_TOKENS, GDN_ATTN_MAX_SCALE = 64, 2.3e38
 GDN_ROPE_HALF, GDN_ROPE_PAIRS = 0, 1
 GDN_ROPE_PLAIN, GDN_ROPE_LINEAR, GDN_ROPE_NTK, GDN_ROPE_BAND = 0, 1, 2, 3
 _KINDS = {torch.bfloat16: GDN_KV_BF16, torch.int8: GDN_KV_INT8,

@@ -568,6 +568,8 @@ typedef struct gdn_kv_cache {
 #define GDN_KV_MAX_POSITIONS (1 << 30)
 /* Largest M of gdn_attn_step_m. */
 #define GDN_ATTN_MAX_TOKENS 64
+/* Largest |scale| of gdn_attn_step_m: scale log2 e is a float. */
+#define GDN_ATTN_MAX_SCALE 2.3e38f
 
 /* Which channels make a pair. */
 enum {
@@ -667,7 +669,7 @@ size_t gdn_attn_workspace(const gdn_kv_cache *cache, int M, int qh);
  *     o[b][m][i] = sum_p softmax_p(scale q[b][m][i] . k_p) v_p,
  *     p = 0 .. start[b] + m, key head i / (qh / kvh).
  *   q, o  [B][M][qh][hd], dtype GDN_F32 or GDN_BF16; qh a multiple of kvh
- *   scale finite;  start: required
+ *   |scale| <= GDN_ATTN_MAX_SCALE (GDN_EINVAL);  start: required
  *   lse   NULL, or fp32 [B][M][qh]: log sum_p exp(scale q . k_p)
  *   workspace  at least gdn_attn_workspace() bytes (GDN_ERANGE if smaller);
  *         calls that may overlap on the GPU need one each
