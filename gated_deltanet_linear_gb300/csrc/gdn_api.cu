@@ -545,7 +545,7 @@ int linattn_args(const gdn_shape *s, int M, int dtype, int decay, float scale,
   if (M < 1 || M > GDN_MAX_TOKENS) return GDN_ERANGE;
   const int e = element_size(dtype);
   if (!e || (decay != GDN_DECAY_TOKEN && decay != GDN_DECAY_HEAD)) return GDN_EINVAL;
-  if (!(fabsf(scale) <= GDN_ATTN_MAX_SCALE)) return GDN_EINVAL;
+  if (!(scale >= -3.0e38f && scale <= 3.0e38f)) return GDN_EINVAL;
   if (s->B == 0) return GDN_OK;
   const size_t sb = state_floats(s) * 4;
   const size_t qkb = (size_t)s->B * M * s->kh * s->kd * e;
