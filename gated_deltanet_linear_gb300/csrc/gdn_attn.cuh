@@ -54,10 +54,11 @@
 // 24 rows over bf16, 53 and 58 us).
 //
 // Measured (uniform lengths, copies from HBM at 6.8 TB/s): bf16 caches 91 to 94 %
-// of the copy rate with 4 rows a head, 8 bits 86 to 90 % (64 channels 78), where the
-// widening's integer operations fill 60 % of the issue slots.  16 and 24 rows a head
-// 41 to 61 % (bf16 70): one CTA of 8 warps holds the sums, two warps a scheduler, and
-// waits for its own products.
+// of the copy rate with 4 rows a head, 8 bits 80 to 89 % (64 channels 72), where the
+// widening's integer operations and the weights fill 62 % of the issue slots.  9 to
+// 24 rows a head 30 to 55 % (bf16 caches 53 to 72): one CTA of 8 warps holds the sums,
+// two warps a scheduler, and waits for its own products.  More rows take a pass over
+// keys and values for every 24 (or 16) of them: 64 tokens x 6 heads 4 % over int8.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -84,8 +85,8 @@ constexpr int kSms = 152;
 // Sizes of a variant: R tiles of 8 rows.  kS warps share a tile of positions (a
 // team): each takes its share of them for the scores, and its share of the
 // channels for the sums over v, so that the sums of 24 rows of 256 channels fit its
-// registers (4 tokens x 24 rows of 16 sequences, fp32 tokens: 94 us by single warps
-// with 16 rows, 64 by teams with 24).
+// registers (4 tokens x 24 rows of 16 sequences, fp32 tokens, when they came: 94 us by
+// single warps with 16 rows, 64 by teams with 24).
 template <int kHd, int kKind, int R>
 struct Sizes {
   static constexpr int kBytes = kKind == kKvBf16 ? 2 : 1;
@@ -95,8 +96,8 @@ struct Sizes {
   static constexpr int kCtas = kHd == 64 || (R == 1 && kRow <= 256) ? 2 : 1;
   static constexpr int kTeams = kWarps / kS;
   // positions of a tile: as many as leave a ring of three parts (32 against 16 for
-  // 128 channels of 8 bits: 100 us, 114; 64 against 32 for 64 channels: 107, 118) and
-  // fit the registers (64 channels, 16 rows: 16)
+  // 128 channels of 8 bits: 100 us, 114; 64 against 32 for 64 channels: 107, 118; both
+  // with weights of one part) and fit the registers (64 channels, 16 rows: 16)
   static constexpr int kTile = kRow == 64 && R == 1 ? 64 : kS == 2 || (kCtas == 1 && kRow <= 256)    ? 32
                                : kRow > 128 || (kHd == 64 && R == 2) ? 16
                                                                      : 32;

@@ -26,12 +26,14 @@
 // Layout.  8 channels a lane: 16 bytes of bf16 in and out, hd / 8 lanes a row,
 // several rows a lane asked for at once.
 //
-// Measured: 32768 rows x 32 heads of 128, bf16, whole heads turned: 84 us (537 MB,
-// 94 % of the copy rate).  8 padded prompts of up to 4096 tokens x 32 + 16 heads
-// into e4m3 70 us (369 MB, 5.3 TB/s: the rounding of k and v, 40 % of the
-// instructions, beside the loads) and back 16 us.  65531 positions x 4 heads of 256,
-// int8 to bf16: 62 to 66 us (90 to 96 %).  64 tokens of 24 + 8 heads: 3.1 us a kernel,
-// the chain from lengths to pages and rows to stores.
+// Measured: 32768 rows x 32 heads of 128, bf16, whole heads turned: 88 us (537 MB,
+// 90 % of the copy rate).  8 prompts of 4096 tokens x 32 + 16 heads into bf16 136 us
+// (all of the copy rate), into e4m3 144 us (89 %: the rounding of k and v, 40 % of the
+// instructions, beside the loads); padded ones of up to 4096 tokens 79 and 71 us, and
+// back from e4m3 18 us.  65531 positions x 4 heads of 256, int8 to bf16: 65 us (91 %);
+// 8 x 65531 positions of 128 channels, int8 to bf16: 1 head 76 % of the copy rate, 2
+// heads 69, 3 83, 4 92.  64 tokens of 24 + 8 heads: 4.0 us a kernel, the chain from
+// lengths to pages and rows to stores.
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
